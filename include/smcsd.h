@@ -64,6 +64,7 @@ extern "C" {
 #define SMCSD_ERR_NONFINITE (-5)   /* device: NaN/+inf logit or weight, or an all-masked row */
 #define SMCSD_ERR_RANGE (-6)       /* device: token id, offset, ancestor or page id out of range */
 #define SMCSD_ERR_TIMEOUT (-7)     /* device: a bounded wait inside a kernel ran out (about 2 s) */
+#define SMCSD_ERR_PAGES (-8)       /* device: kv_slot_map found fewer free pages than it needs */
 
 /* logit element types */
 #define SMCSD_F32 0
@@ -81,6 +82,10 @@ extern "C" {
 #define SMCSD_OP_PAGETABLE_REMAP 4
 #define SMCSD_OP_PACER_BLOCK_STOP 5
 #define SMCSD_OP_DRAFT_SAMPLE 6 /* S = number of rows R; K is ignored */
+#define SMCSD_OP_KV_SLOT_MAP 7    /* S sequences, V = number of pages; K is ignored */
+#define SMCSD_OP_KV_APPEND 8      /* any S > 0; K and V are ignored */
+#define SMCSD_OP_TREE_MASK 9      /* any S > 0; K and V are ignored */
+#define SMCSD_OP_LOGITS_PROCESS 10 /* any S > 0; K and V are ignored */
 
 /*
  * Scratch bytes that `op` needs for S sequences (or particles; for the resampling ops S is the
@@ -322,6 +327,130 @@ int smc_step_static(const void* tgt_logits, const void* drf_logits, int dtype,
                     float* ess, int32_t* resampled, const int32_t* table_in, int32_t* table_out,
                     int pages_per_seq, int32_t* refcount, int num_pages, int32_t* status,
                     void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The rest of a speculative step on the device: page tables and slots for the step's tokens, their
+ * keys and values in the paged cache, attention of the drafted tokens over it, and the logits
+ * before sampling or verify. The pages describe these steps ([SMC] sec. 2 step 2: one target pass
+ * scores every particle's drafts; sec. 3: page-based KV with metadata-only resampling; sec. 5:
+ * hard constraints) without formulas; the rules are stated here.
+ *
+ * Shared conventions
+ *   - S sequences; sequence s has n_s new tokens, its NODES: the last committed token and the
+ *     drafts after it, as a chain or a tree. Fixed layout (node_offsets == NULL): n_s = T, node t of
+ *     sequence s is row s*T+t. Ragged: node_offsets int32 [S+1] (ascending from 0), rows
+ *     node_offsets[s] .. node_offsets[s+1]-1, n_s <= T. R is the number of rows (S*T if fixed);
+ *     offsets that do not fit R or T are SMCSD_ERR_RANGE (device side).
+ *   - Paged cache: K and V each [num_pages, Hkv, page_size, D], contiguous, 16-byte aligned;
+ *     page_size a power of two of 8 .. 256. Tables int32 [S, pages_per_seq], -1 = no page. Position x
+ *     of a sequence is in page table[s][x / page_size] at offset x % page_size; its SLOT is
+ *     page * page_size + offset (int64: a cache may have more than 2^31 slots).
+ *   - Node j of sequence s is at position ctx_len[s] + j, ctx_len int32 [S] being the tokens already
+ *     in the cache.
+ *   - A node mask is uint32 [R, (T+31)/32]: bit j of row r says that the row's node sees node j of
+ *     its own sequence (bits past n_s are ignored). NULL is a chain: node t sees nodes 0 .. t.
+ * ------------------------------------------------------------------------------------------- */
+
+/*
+ * Page tables and slots for the new tokens of every sequence, with copy-on-write of shared pages
+ * ([SMC] sec. 3: after a resampling several particles hold the same pages). For s = 0, 1, ... and
+ * every page index j that the sequence writes, ctx_len[s]/page_size <= j <
+ * ceil((ctx_len[s]+n_s)/page_size) (none if n_s = 0), with id = table_in[s][j]:
+ *   id == -1               a free page is taken;
+ *   refcount_in[id] > 1    a free page is taken in its place and refcount_out[id] drops by one; if j
+ *                          is the first of them and ctx_len[s] % page_size > 0, its filled part has
+ *                          to be copied: copy_src[s] = id, copy_dst[s] = the new page;
+ *   otherwise              the page is kept.
+ * Free pages are those with refcount_in == 0, taken in ascending order; a taken page's
+ * refcount_out is 1. Everything else is copied from table_in / refcount_in (the outputs must not
+ * alias them). slots int64 [R]; copy_src, copy_dst int32 [S] (-1: no copy). The result does not
+ * depend on the order of execution.
+ * Device-side errors: SMCSD_ERR_RANGE (a negative length, more positions than the table has, ids or
+ * offsets out of range), SMCSD_ERR_PAGES (too few free pages; the pages that are missing read -1 and
+ * so do their slots).
+ */
+int kv_slot_map(const int32_t* ctx_len, const int32_t* node_offsets, int S, int T, int R,
+                const int32_t* table_in, int32_t* table_out, int pages_per_seq, int page_size,
+                const int32_t* refcount_in, int32_t* refcount_out, int num_pages, int64_t* slots,
+                int32_t* copy_src, int32_t* copy_dst, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Writes the new tokens' keys and values into the paged cache, and the copies that kv_slot_map
+ * asked for. k_new / v_new: R tokens of [Hkv, D] each, token_stride elements from one token to the
+ * next (both may be slices of one projection's output), 16-byte aligned, token_stride * element
+ * size and D * element size multiples of 16. slots int64 [R]; a negative slot writes nothing.
+ * copy_src / copy_dst int32 [S] with ctx_len int32 [S] (all three or none): where copy_src[s] >= 0
+ * the first ctx_len[s] % page_size positions of that page go to copy_dst[s], for every head. Slots
+ * must be distinct, and no slot or destination page lie in a page that is copied from.
+ * Slots or pages outside the cache are SMCSD_ERR_RANGE (device side) and write nothing.
+ */
+int kv_append(const void* k_new, const void* v_new, int dtype, int R, int Hkv, int D,
+              long long token_stride, const int64_t* slots, const int32_t* copy_src,
+              const int32_t* copy_dst, const int32_t* ctx_len, int S, void* k_cache, void* v_cache,
+              int page_size, int num_pages, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Node mask of trees given by parents: parents int32 [R], the index within its own sequence of the
+ * node that a node follows (smaller than its own), -1 for a first node. mask uint32
+ * [R, (T+31)/32]: bit j is set for the node itself and for its ancestors. A parent out of range is
+ * SMCSD_ERR_RANGE (device side).
+ */
+int tree_mask(const int32_t* parents, const int32_t* node_offsets, int S, int T, int R,
+              uint32_t* mask, void* ws, size_t ws_bytes, void* stream);
+
+/* Scratch bytes of tree_attention for these sizes (0 if they are not supported). */
+size_t tree_attention_workspace_size(int S, int N, int T, int Hq, int Hkv, int D);
+
+/*
+ * Attention of every sequence's nodes over its cached tokens and over the nodes that they see
+ * ([SMC] sec. 2 step 2: the target scores all drafted tokens of all particles in one pass). For row
+ * r (node t of sequence s) and query head h, which reads the keys of head h / (Hq/Hkv):
+ *   z_x = scale * q[r,h] . K_x   for x < ctx_len[s] and for x = ctx_len[s]+j with bit j of the mask,
+ *   out[r,h] = sum_x softmax(z)_x V_x,   lse[r,h] = log sum_x exp(z_x).
+ * The nodes' own keys and values are already in the cache (kv_append). A row that sees nothing gives
+ * out = 0 and lse = -inf. What the cache holds at positions that no row sees (unwritten slots,
+ * pages past the end) may be anything, NaN included; a NaN or infinity in a node reaches only the
+ * rows that see that node.
+ * Sequences come in groups of N (S a multiple of N; N = 1: none): pages that all sequences of a group
+ * have in common at the start of their tables (the prompt, common ancestors) are read once for the
+ * group. N changes no result beyond the order of the sums.
+ * q: R rows of [Hq, D], q_stride elements apart (16-byte aligned, q_stride * element size a multiple
+ * of 16); out [R, Hq, D] in the same type; lse float [R, Hq] (NULL to skip). D is 64 or 128, Hq a
+ * multiple of Hkv. dtype is that of q, the caches and out. Products are accumulated in float32;
+ * for bf16 the weights exp(z - max) are rounded to bf16 for the product with V.
+ * Device-side errors: SMCSD_ERR_RANGE (lengths, offsets or page ids out of range).
+ */
+int tree_attention(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
+                   int dtype, int num_pages, int page_size, const int32_t* table, int pages_per_seq,
+                   const int32_t* ctx_len, const int32_t* node_offsets, int S, int N, int T, int R,
+                   const uint32_t* mask, int Hq, int Hkv, int D, float scale, void* out, float* lse,
+                   void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Penalties, biases and grammar masks on logits, before draft_sample or a verify ([SMC] sec. 5:
+ * constraints). Row r (node t of sequence s) predicts the token after that node. count_r(v) is the
+ * number of times that token v stands in the sequence's history, hist_tokens[hist_offsets[s] ..
+ * hist_offsets[s+1]-1], and among the node_tokens of the nodes that the row sees. In float32, rounded
+ * once:
+ *   z = logits[r, v];  if count > 0: z = z > 0 ? z / repetition[s] : z * repetition[s];
+ *   z -= frequency[s] * count;  if count > 0: z -= presence[s];
+ *   z += bias_values[i] for the last i of bias_offsets[s] .. bias_offsets[s+1]-1 with
+ *        bias_tokens[i] == v;
+ *   z = -inf if bit v of allowed[r] is clear.
+ * logits, out [R, V] of dtype; out may be logits itself (nothing but changed values is then written
+ * back). Each of these may be NULL to leave its part out: node_tokens int32 [R], mask (with
+ * node_tokens: chain), hist_tokens int32 [n_hist] with hist_offsets int32 [S+1], repetition (> 0),
+ * presence, frequency float [S] (1, 0, 0), bias_tokens int32 / bias_values float [n_bias] with
+ * bias_offsets int32 [S+1], allowed uint32 [R, (V+31)/32]. A token of -1 in hist_tokens, node_tokens
+ * or bias_tokens counts for nothing; others outside [0, V) are SMCSD_ERR_RANGE (device side), as are
+ * offsets that descend, are negative or pass n_hist or n_bias. S is at most 65535. A row whose mask allows nothing is -inf throughout, which the verify then reports.
+ */
+int logits_process(const void* logits, void* out, int dtype, int R, int V, int S, int T,
+                   const int32_t* node_offsets, const int32_t* node_tokens, const uint32_t* mask,
+                   const int32_t* hist_tokens, const int32_t* hist_offsets, int n_hist,
+                   const float* repetition, const float* presence, const float* frequency,
+                   const int32_t* bias_tokens, const float* bias_values, const int32_t* bias_offsets,
+                   int n_bias, const uint32_t* allowed, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,8 @@ _API = {
     "smc_step", "Workspace", "workspace_size", "check_status", "status_string", "SMCSDError",
     "load", "OP_SD_VERIFY", "OP_SMC_REWEIGHT", "OP_SMC_STEP", "OP_ESS_RESAMPLE",
     "OP_PAGETABLE_REMAP", "OP_PACER_BLOCK_STOP", "LIB_PATH",
+    "kv_slot_map", "kv_append", "tree_mask", "tree_attention", "logits_process",
+    "TreeAttentionWorkspace", "OP_KV_SLOT_MAP", "OP_KV_APPEND", "OP_TREE_MASK", "OP_LOGITS_PROCESS",
 }
 
 __all__ = sorted(_API)

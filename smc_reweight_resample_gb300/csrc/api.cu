@@ -3,6 +3,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "serve_launch.cuh"
 #include "smcsd.h"
 #include "smcsd_launch.cuh"
 
@@ -53,6 +54,13 @@ extern "C" size_t smcsd_workspace_size(int op, int S, int K, int V) {
         case SMCSD_OP_PAGETABLE_REMAP:
         case SMCSD_OP_PACER_BLOCK_STOP:
             return ws_small_bytes(S);
+        case SMCSD_OP_KV_SLOT_MAP:
+            if (V <= 0) return 0;
+            return slot_map_bytes(S, V);
+        case SMCSD_OP_KV_APPEND:
+        case SMCSD_OP_TREE_MASK:
+        case SMCSD_OP_LOGITS_PROCESS:
+            return 256;  // the error flag
         default:
             return 0;
     }
@@ -90,6 +98,7 @@ extern "C" const char* smcsd_status_string(int code) {
         case SMCSD_ERR_NONFINITE: return "non-finite input (NaN/+inf logit or weight, or an all-masked row)";
         case SMCSD_ERR_RANGE: return "index out of range (token id, offsets, ancestor or page id)";
         case SMCSD_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";
+        case SMCSD_ERR_PAGES: return "too few free pages in the cache";
         default: return "unknown status";
     }
 }

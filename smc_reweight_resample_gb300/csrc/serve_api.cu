@@ -1,0 +1,238 @@
+// serve_api.cu -- C ABI of the step around the verify (page tables and slots, cache writes, node
+// masks, attention over the cache, logits): host-side argument checks and launches.
+#include <math.h>
+
+#include "attn_plan.cuh"
+#include "serve_launch.cuh"
+#include "smcsd.h"
+#include "smcsd_launch.cuh"
+
+using namespace smcsd;
+
+namespace {
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+int from_cuda(cudaError_t e) { return e == cudaSuccess ? SMCSD_OK : SMCSD_ERR_CUDA; }
+size_t elem_bytes(int dtype) { return dtype == SMCSD_F32 ? 4 : 2; }
+
+int check_ws(const void* ws, size_t ws_bytes, size_t need) {
+    if (!ws) return SMCSD_ERR_INVALID_ARG;
+    if (((uintptr_t)ws & 255u) != 0 || ws_bytes < need) return SMCSD_ERR_WORKSPACE;
+    return SMCSD_OK;
+}
+
+// log2 of a page size of 8 .. 256, or -1
+int page_shift(int page_size) {
+    for (int b = 3; b <= 8; ++b)
+        if (page_size == 1 << b) return b;
+    return -1;
+}
+
+bool nodes_ok(const int32_t* offsets, int S, int T, int R) {
+    if (S <= 0 || T <= 0 || R <= 0) return false;
+    return offsets || (long long)S * T == R;
+}
+
+// Sizes that tree_attention takes.
+bool attn_sizes_ok(int S, int N, int T, int Hq, int Hkv, int D) {
+    if (S <= 0 || N <= 0 || S % N || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return false;
+    if (D != 64 && D != 128) return false;
+    // rows of a group, and units, are counted in 32 bits
+    const long long rows = (long long)T * (Hq / Hkv);
+    return rows * N < (1ll << 30) && (long long)S * Hkv * (rows / 16 + 1) < (1ll << 30);
+}
+
+constexpr int kSimtBlocksPerSm = 2;
+
+AttnLayout simt_layout(int S, int N, int T, int Hq, int Hkv, int D) {
+    return attn_layout(S, N, T, Hq / Hkv, Hkv, D, 16, kAttnMaxCta);
+}
+
+}  // namespace
+
+extern "C" int kv_slot_map(const int32_t* ctx_len, const int32_t* node_offsets, int S, int T, int R,
+                           const int32_t* table_in, int32_t* table_out, int pages_per_seq,
+                           int page_size, const int32_t* refcount_in, int32_t* refcount_out,
+                           int num_pages, int64_t* slots, int32_t* copy_src, int32_t* copy_dst,
+                           void* ws, size_t ws_bytes, void* stream) {
+    if (!ctx_len || !table_in || !table_out || !refcount_in || !refcount_out || !slots || !copy_src || !copy_dst)
+        return SMCSD_ERR_INVALID_ARG;
+    if (table_in == table_out || refcount_in == refcount_out) return SMCSD_ERR_INVALID_ARG;
+    const int shift = page_shift(page_size);
+    if (!nodes_ok(node_offsets, S, T, R) || pages_per_seq <= 0 || shift < 0 || num_pages <= 0)
+        return SMCSD_ERR_INVALID_ARG;
+    if ((long long)pages_per_seq * page_size > 0x7fffffffLL) return SMCSD_ERR_INVALID_ARG;
+    int rc = check_ws(ws, ws_bytes, slot_map_bytes(S, num_pages));
+    if (rc) return rc;
+    SlotParams p{};
+    p.ctx_len = ctx_len;
+    p.n = Nodes{node_offsets, S, T, R};
+    p.table_in = table_in;
+    p.table_out = table_out;
+    p.pages_per_seq = pages_per_seq;
+    p.page_size = page_size;
+    p.page_shift = shift;
+    p.ref_in = refcount_in;
+    p.ref_out = refcount_out;
+    p.num_pages = num_pages;
+    p.slots = slots;
+    p.copy_src = copy_src;
+    p.copy_dst = copy_dst;
+    p.ws = ws;
+    p.free_list = slot_map_free_list();
+    p.demand = slot_map_demand(num_pages);
+    return from_cuda(launch_slot_map(p, (cudaStream_t)stream));
+}
+
+extern "C" int kv_append(const void* k_new, const void* v_new, int dtype, int R, int Hkv, int D,
+                         long long token_stride, const int64_t* slots, const int32_t* copy_src,
+                         const int32_t* copy_dst, const int32_t* ctx_len, int S, void* k_cache,
+                         void* v_cache, int page_size, int num_pages, void* ws, size_t ws_bytes,
+                         void* stream) {
+    if (dtype != SMCSD_F32 && dtype != SMCSD_BF16) return SMCSD_ERR_DTYPE;
+    if (!k_new || !v_new || !slots || !k_cache || !v_cache) return SMCSD_ERR_INVALID_ARG;
+    if ((copy_src == nullptr) != (copy_dst == nullptr) || (copy_src && (!ctx_len || S <= 0)))
+        return SMCSD_ERR_INVALID_ARG;
+    const int shift = page_shift(page_size);
+    if (R <= 0 || Hkv <= 0 || D <= 0 || shift < 0 || num_pages <= 0) return SMCSD_ERR_INVALID_ARG;
+    const size_t b = elem_bytes(dtype);
+    if ((D * b) % 16 || token_stride < (long long)Hkv * D || (token_stride * b) % 16) return SMCSD_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache))
+        return SMCSD_ERR_INVALID_ARG;
+    if ((long long)Hkv * D > (1 << 24)) return SMCSD_ERR_INVALID_ARG;
+    int rc = check_ws(ws, ws_bytes, 256);
+    if (rc) return rc;
+    AppendParams p{};
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.token_vecs = (long long)(token_stride * b / 16);
+    p.R = R;
+    p.Hkv = Hkv;
+    p.row_vecs = (int)(D * b / 16);
+    p.slots = slots;
+    p.copy_src = copy_src;
+    p.copy_dst = copy_dst;
+    p.ctx_len = ctx_len;
+    p.S = S;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.page_size = page_size;
+    p.page_shift = shift;
+    p.num_pages = num_pages;
+    p.ws = ws;
+    return from_cuda(launch_append(p, (cudaStream_t)stream));
+}
+
+extern "C" int tree_mask(const int32_t* parents, const int32_t* node_offsets, int S, int T, int R,
+                         uint32_t* mask, void* ws, size_t ws_bytes, void* stream) {
+    if (!parents || !mask || !nodes_ok(node_offsets, S, T, R)) return SMCSD_ERR_INVALID_ARG;
+    int rc = check_ws(ws, ws_bytes, 256);
+    if (rc) return rc;
+    MaskParams p{parents, Nodes{node_offsets, S, T, R}, mask, (T + 31) / 32, ws};
+    return from_cuda(launch_tree_mask(p, (cudaStream_t)stream));
+}
+
+extern "C" size_t tree_attention_workspace_size(int S, int N, int T, int Hq, int Hkv, int D) {
+    if (!attn_sizes_ok(S, N, T, Hq, Hkv, D)) return 0;
+    return simt_layout(S, N, T, Hq, Hkv, D).total;
+}
+
+extern "C" int tree_attention(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
+                              int dtype, int num_pages, int page_size, const int32_t* table,
+                              int pages_per_seq, const int32_t* ctx_len, const int32_t* node_offsets,
+                              int S, int N, int T, int R, const uint32_t* mask, int Hq, int Hkv, int D,
+                              float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    if (dtype != SMCSD_F32 && dtype != SMCSD_BF16) return SMCSD_ERR_DTYPE;
+    if (!q || !k_cache || !v_cache || !table || !ctx_len || !out) return SMCSD_ERR_INVALID_ARG;
+    const int shift = page_shift(page_size);
+    if (!nodes_ok(node_offsets, S, T, R) || !attn_sizes_ok(S, N, T, Hq, Hkv, D)) return SMCSD_ERR_INVALID_ARG;
+    if (num_pages <= 0 || shift < 0 || pages_per_seq <= 0 || !isfinite(scale)) return SMCSD_ERR_INVALID_ARG;
+    if ((long long)pages_per_seq * page_size > 0x3fffffffLL || (long long)R * Hq > 0x7fffffffLL)
+        return SMCSD_ERR_INVALID_ARG;
+    const size_t b = elem_bytes(dtype);
+    if (q_stride < (long long)Hq * D || (q_stride * b) % 16) return SMCSD_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return SMCSD_ERR_INVALID_ARG;
+    int rc = check_ws(ws, ws_bytes, tree_attention_workspace_size(S, N, T, Hq, Hkv, D));
+    if (rc) return rc;
+    AttnParams p{};
+    p.q = q;
+    p.q_stride = q_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.page_shift = shift;
+    p.table = table;
+    p.pages_per_seq = pages_per_seq;
+    p.ctx_len = ctx_len;
+    p.node_offsets = node_offsets;
+    p.S = S;
+    p.N = N;
+    p.G = N > 1 ? S / N : 0;
+    p.T = T;
+    p.R = R;
+    p.mask = mask;
+    p.words = (T + 31) / 32;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.gq = Hq / Hkv;
+    p.D = D;
+    p.scale2 = (float)((double)scale * 1.4426950408889634074);
+    p.out = out;
+    p.lse = lse;
+    p.ws = ws;
+    cudaStream_t st = (cudaStream_t)stream;
+    p.L = simt_layout(S, N, T, Hq, Hkv, D);
+    p.tile = 64;
+    p.rb = 16;
+    p.ncta_max = device_sm_count() * kSimtBlocksPerSm;
+    if (p.ncta_max > kAttnMaxCta) p.ncta_max = kAttnMaxCta;
+    p.min_tiles = 1;
+    cudaError_t e = launch_attn_plan(p, st);
+    if (e == cudaSuccess) e = launch_attn_simt(p, dtype, st);
+    if (e == cudaSuccess) e = launch_attn_combine(p, dtype, st);
+    return from_cuda(e);
+}
+
+extern "C" int logits_process(const void* logits, void* out, int dtype, int R, int V, int S, int T,
+                              const int32_t* node_offsets, const int32_t* node_tokens,
+                              const uint32_t* mask, const int32_t* hist_tokens,
+                              const int32_t* hist_offsets, int n_hist, const float* repetition,
+                              const float* presence, const float* frequency,
+                              const int32_t* bias_tokens, const float* bias_values,
+                              const int32_t* bias_offsets, int n_bias, const uint32_t* allowed,
+                              void* ws, size_t ws_bytes, void* stream) {
+    if (dtype != SMCSD_F32 && dtype != SMCSD_BF16) return SMCSD_ERR_DTYPE;
+    if (!logits || !out || V <= 0 || !nodes_ok(node_offsets, S, T, R)) return SMCSD_ERR_INVALID_ARG;
+    if (S > 65535) return SMCSD_ERR_INVALID_ARG;
+    if ((hist_tokens == nullptr) != (hist_offsets == nullptr)) return SMCSD_ERR_INVALID_ARG;
+    if ((bias_tokens == nullptr) != (bias_values == nullptr) || (bias_tokens == nullptr) != (bias_offsets == nullptr))
+        return SMCSD_ERR_INVALID_ARG;
+    if (n_hist < 0 || n_bias < 0) return SMCSD_ERR_INVALID_ARG;
+    if (mask && !node_tokens) return SMCSD_ERR_INVALID_ARG;
+    int rc = check_ws(ws, ws_bytes, 256);
+    if (rc) return rc;
+    LogitsParams p{};
+    p.logits = logits;
+    p.out = out;
+    p.n = Nodes{node_offsets, S, T, R};
+    p.V = V;
+    p.vec = aligned16(logits) && aligned16(out) && ((size_t)V * elem_bytes(dtype)) % 16 == 0;
+    p.node_tokens = node_tokens;
+    p.mask = mask;
+    p.words = (T + 31) / 32;
+    p.hist_tokens = hist_tokens;
+    p.hist_offsets = hist_offsets;
+    p.n_hist = n_hist;
+    p.n_bias = n_bias;
+    p.repetition = repetition;
+    p.presence = presence;
+    p.frequency = frequency;
+    p.bias_tokens = bias_tokens;
+    p.bias_values = bias_values;
+    p.bias_offsets = bias_offsets;
+    p.allowed = allowed;
+    p.allowed_words = (V + 31) / 32;
+    p.ws = ws;
+    return from_cuda(launch_logits(p, dtype, (cudaStream_t)stream));
+}

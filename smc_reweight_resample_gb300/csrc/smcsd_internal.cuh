@@ -34,7 +34,7 @@ constexpr float kPosInf = __builtin_huge_valf();
 
 // status codes (values fixed by the public header)
 constexpr int kOk = 0, kErrInvalid = -1, kErrDtype = -2, kErrWorkspace = -3, kErrCuda = -4,
-              kErrNonfinite = -5, kErrRange = -6, kErrTimeout = -7;
+              kErrNonfinite = -5, kErrRange = -6, kErrTimeout = -7, kErrPages = -8;
 
 // largest |alpha * z / T| the double-float exponential accepts for a sampled row
 constexpr float kMaxScaledLogit = 65536.0f;
