@@ -198,7 +198,8 @@ __device__ __forceinline__ int attn_page(const AttnParams& p, int seq, int j) {
 }
 
 cudaError_t launch_attn_plan(const AttnParams& p, cudaStream_t st);
-cudaError_t launch_attn_simt(const AttnParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_attn_simt(const AttnParams& p, cudaStream_t st);  // float32
+cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t st);  // bf16
 cudaError_t launch_attn_combine(const AttnParams& p, int dtype, cudaStream_t st);
 
 }  // namespace smcsd

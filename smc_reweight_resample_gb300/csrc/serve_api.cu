@@ -42,10 +42,11 @@ bool attn_sizes_ok(int S, int N, int T, int Hq, int Hkv, int D) {
     return rows * N < (1ll << 30) && (long long)S * Hkv * (rows / 16 + 1) < (1ll << 30);
 }
 
+// float32: the FP32 pipes, 64 keys x 16 rows at a time; bf16: the tensor cores, 128 keys x up to 256 rows
 constexpr int kSimtBlocksPerSm = 2;
 
-AttnLayout simt_layout(int S, int N, int T, int Hq, int Hkv, int D) {
-    return attn_layout(S, N, T, Hq / Hkv, Hkv, D, 16, kAttnMaxCta);
+AttnLayout layout_of(int dtype, int S, int N, int T, int Hq, int Hkv, int D) {
+    return attn_layout(S, N, T, Hq / Hkv, Hkv, D, dtype == SMCSD_F32 ? 16 : 256, kAttnMaxCta);
 }
 
 }  // namespace
@@ -134,7 +135,8 @@ extern "C" int tree_mask(const int32_t* parents, const int32_t* node_offsets, in
 
 extern "C" size_t tree_attention_workspace_size(int S, int N, int T, int Hq, int Hkv, int D) {
     if (!attn_sizes_ok(S, N, T, Hq, Hkv, D)) return 0;
-    return simt_layout(S, N, T, Hq, Hkv, D).total;
+    const size_t a = layout_of(SMCSD_F32, S, N, T, Hq, Hkv, D).total, b = layout_of(SMCSD_BF16, S, N, T, Hq, Hkv, D).total;
+    return a > b ? a : b;
 }
 
 extern "C" int tree_attention(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
@@ -182,14 +184,14 @@ extern "C" int tree_attention(const void* q, long long q_stride, const void* k_c
     p.lse = lse;
     p.ws = ws;
     cudaStream_t st = (cudaStream_t)stream;
-    p.L = simt_layout(S, N, T, Hq, Hkv, D);
-    p.tile = 64;
-    p.rb = 16;
-    p.ncta_max = device_sm_count() * kSimtBlocksPerSm;
+    p.L = layout_of(dtype, S, N, T, Hq, Hkv, D);
+    p.tile = dtype == SMCSD_F32 ? 64 : 128;
+    p.rb = dtype == SMCSD_F32 ? 16 : 256;
+    p.ncta_max = device_sm_count() * (dtype == SMCSD_F32 ? kSimtBlocksPerSm : 1);
     if (p.ncta_max > kAttnMaxCta) p.ncta_max = kAttnMaxCta;
     p.min_tiles = 1;
     cudaError_t e = launch_attn_plan(p, st);
-    if (e == cudaSuccess) e = launch_attn_simt(p, dtype, st);
+    if (e == cudaSuccess) e = dtype == SMCSD_F32 ? launch_attn_simt(p, st) : launch_attn_tc(p, st);
     if (e == cudaSuccess) e = launch_attn_combine(p, dtype, st);
     return from_cuda(e);
 }

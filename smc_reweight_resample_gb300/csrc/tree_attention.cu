@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         }
         const int rows = it.nodes * p.gq;
         it.nrb = max(1, attn_blocks(rows, p.rb));
-        it.per = max(1, (rows + it.nrb - 1) / it.nrb);
+        it.per = max(1, min(rows, p.rb));
         if (it.nodes == 0 || it.tiles < 0) it.tiles = 0;
         const int u = it.tiles > 0 ? p.Hkv * it.nrb : 0;
         it.unit0 = u;
@@ -147,27 +147,16 @@ cudaError_t launch_attn_plan(const AttnParams& p, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------------------
-// the kernel on the FP32 pipes
+// float32: the kernel on the FP32 pipes
 // ------------------------------------------------------------------------------------------
 
 constexpr int kSimtThreads = 128;
 constexpr int kSimtKeys = 64;  // keys in a tile
 constexpr int kSimtRows = 16;  // rows in a block
 
-template <int DT>
 __device__ __forceinline__ float4 load4(const void* base, size_t i) {
-    if (DT == 0) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i));
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+    return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
 }
-template <int DT>
-__device__ __forceinline__ void store1(void* base, size_t i, float v) {
-    if (DT == 0)
-        static_cast<float*>(base)[i] = v;
-    else
-        static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
-}
-
 template <int D>
 constexpr int simt_smem() {
     return 4 * (kSimtRows * D + kSimtKeys * (D + 4) + kSimtKeys * D + kSimtKeys * (kSimtRows + 4) + 3 * kSimtRows);
@@ -176,7 +165,7 @@ constexpr int simt_smem() {
 // One block per share of the line; 16 rows x 64 keys at a time. A thread takes one key and 8 rows for
 // the scores, one column (or, for D = 64, one column of half the rows) for the values. The running
 // maximum m (of z / ln 2) and sum l of a row rescale what is there when the maximum grows.
-template <int DT, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_constant__ AttnParams p) {
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;                                // [16][D]
@@ -212,7 +201,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
             float4 v = make_float4(0, 0, 0, 0);
             if (r < c.rows) {
                 const int row = c.row0 + r, node = row / p.gq, hq = c.hkv * p.gq + (row - node * p.gq);
-                v = load4<DT>(p.q, (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + d);
+                v = load4(p.q, (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + d);
             }
             *reinterpret_cast<float4*>(sq + r * D + d) = v;
         }
@@ -230,8 +219,8 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
                 if (pos < keys) {
                     const size_t page = attn_page(p, c.seq, pos >> p.page_shift);
                     const size_t at = ((page * p.Hkv + c.hkv) * p.page_size + (pos & (p.page_size - 1))) * D + d;
-                    a = load4<DT>(p.k_cache, at);
-                    b = load4<DT>(p.v_cache, at);
+                    a = load4(p.k_cache, at);
+                    b = load4(p.v_cache, at);
                 }
                 *reinterpret_cast<float4*>(sk + k * (D + 4) + d) = a;
                 *reinterpret_cast<float4*>(sv + k * D + d) = b;
@@ -316,7 +305,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
             const size_t orow = (size_t)(c.node0 + node) * p.Hq + hq;
             const float l = sm_l[rr], m = sm_m[rr];
             if (c.whole) {
-                store1<DT>(p.out, orow * D + col, l == 0.0f ? 0.0f : acc[r] / l);
+                static_cast<float*>(p.out)[orow * D + col] = l == 0.0f ? 0.0f : acc[r] / l;
                 if (col == 0 && p.lse) p.lse[orow] = l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718056f;
             } else {
                 c.o[(size_t)rr * D + col] = acc[r];
@@ -327,9 +316,9 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
     }
 }
 
-template <int DT, int D>
+template <int D>
 static cudaError_t launch_simt_t(const AttnParams& p, cudaStream_t st) {
-    auto kern = attn_simt_kernel<DT, D>;
+    auto kern = attn_simt_kernel<D>;
     constexpr int smem = simt_smem<D>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -346,9 +335,8 @@ static cudaError_t launch_simt_t(const AttnParams& p, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-cudaError_t launch_attn_simt(const AttnParams& p, int dtype, cudaStream_t st) {
-    if (p.D == 64) return dtype == 0 ? launch_simt_t<0, 64>(p, st) : launch_simt_t<1, 64>(p, st);
-    return dtype == 0 ? launch_simt_t<0, 128>(p, st) : launch_simt_t<1, 128>(p, st);
+cudaError_t launch_attn_simt(const AttnParams& p, cudaStream_t st) {
+    return p.D == 64 ? launch_simt_t<64>(p, st) : launch_simt_t<128>(p, st);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -356,6 +344,14 @@ cudaError_t launch_attn_simt(const AttnParams& p, int dtype, cudaStream_t st) {
 // ------------------------------------------------------------------------------------------
 
 constexpr int kJoinWarps = 8;
+
+template <int DT>
+__device__ __forceinline__ void store1(void* base, size_t i, float v) {
+    if (DT == 0)
+        static_cast<float*>(base)[i] = v;
+    else
+        static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
+}
 
 // Sequence that row r belongs to (ragged offsets: the last one that starts at or before it).
 __device__ __forceinline__ int attn_seq_of(const AttnParams& p, int r) {
