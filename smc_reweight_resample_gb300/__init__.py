@@ -21,5 +21,6 @@ def __getattr__(name):
     if name in _API:
         from . import _binding
 
-        return getattr(_binding, name)
+        value = globals()[name] = getattr(_binding, name)  # found here from now on
+        return value
     raise AttributeError(name)

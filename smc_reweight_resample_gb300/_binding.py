@@ -450,8 +450,9 @@ def _dev_ptr(t, dtype):
     return t.data_ptr()
 
 
-def _stream_ptr(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _stream_ptr(stream, t):
+    """Handle of the given stream, or of the current one of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _token_rows(t, like=None):
@@ -506,7 +507,7 @@ def kv_slot_map(ctx_len, table_in, refcount_in, S, T, page_size, new_offsets=Non
                             _dev_ptr(table_in, i32), _dev_ptr(table_out, i32), table_in.shape[1],
                             page_size, _dev_ptr(refcount_in, i32), _dev_ptr(refcount_out, i32),
                             num_pages, _dev_ptr(slots, torch.int64), _dev_ptr(copy_src, i32),
-                            _dev_ptr(copy_dst, i32), ws.ptr, ws.nbytes, _stream_ptr(stream))
+                            _dev_ptr(copy_dst, i32), ws.ptr, ws.nbytes, _stream_ptr(stream, table_in))
     _check(rc, "kv_slot_map")
     return dict(table_out=table_out, refcount_out=refcount_out, slots=slots, copy_src=copy_src,
                 copy_dst=copy_dst)
@@ -533,7 +534,7 @@ def kv_append(k_new, v_new, slots, k_cache, v_cache, ctx_len=None, copy_src=None
                           _dev_ptr(copy_src, i32), _dev_ptr(copy_dst, i32),
                           _dev_ptr(ctx_len, i32) if S else None, S, _dev_ptr(k_cache, k_new.dtype),
                           _dev_ptr(v_cache, k_new.dtype), page_size, num_pages, ws.ptr, ws.nbytes,
-                          _stream_ptr(stream))
+                          _stream_ptr(stream, k_cache))
     _check(rc, "kv_append")
     return k_cache, v_cache
 
@@ -547,7 +548,7 @@ def tree_mask(parents, S, T, node_offsets=None, mask=None, ws=None, stream=None)
     ws = ws or Workspace(OP_TREE_MASK, 1, device=parents.device)
     i32 = torch.int32
     rc = load().tree_mask(_dev_ptr(parents, i32), _dev_ptr(node_offsets, i32), S, T, R,
-                          _dev_ptr(mask, i32), ws.ptr, ws.nbytes, _stream_ptr(stream))
+                          _dev_ptr(mask, i32), ws.ptr, ws.nbytes, _stream_ptr(stream, parents))
     _check(rc, "tree_mask")
     return mask
 
@@ -580,7 +581,7 @@ def tree_attention(q, k_cache, v_cache, table, ctx_len, S, T, scale, N=1, node_o
                                num_pages, page_size, _dev_ptr(table, i32), table.shape[1],
                                _dev_ptr(ctx_len, i32), _dev_ptr(node_offsets, i32), S, N, T, R,
                                _dev_ptr(mask, i32), Hq, Hkv, D, float(scale), _dev_ptr(out, dt),
-                               _dev_ptr(lse, torch.float32), ws.ptr, ws.nbytes, _stream_ptr(stream))
+                               _dev_ptr(lse, torch.float32), ws.ptr, ws.nbytes, _stream_ptr(stream, q))
     _check(rc, "tree_attention")
     return out, lse
 
@@ -612,6 +613,6 @@ def logits_process(logits, S, T, V, node_offsets=None, node_tokens=None, mask=No
                                _dev_ptr(frequency, f32), _dev_ptr(bias_tokens, i32),
                                _dev_ptr(bias_values, f32), _dev_ptr(bias_offsets, i32),
                                0 if bias_tokens is None else min(bias_tokens.numel(), bias_values.numel()),
-                               _dev_ptr(allowed, i32), ws.ptr, ws.nbytes, _stream_ptr(stream))
+                               _dev_ptr(allowed, i32), ws.ptr, ws.nbytes, _stream_ptr(stream, logits))
     _check(rc, "logits_process")
     return out

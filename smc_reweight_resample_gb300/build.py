@@ -20,7 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsmcsd.so")
 SOURCES = ["api.cu", "verify_stream.cu", "stream_tma.cu", "finish.cu", "sd_sample.cu", "resample_pacer.cu",
            "static_scratch.cu", "serve_api.cu", "kv_cache.cu", "tree_attention.cu",
-           "tree_attention_tc.cu", "logits_process.cu"]
+           "tree_attention_wide.cu",
+           "tree_attention_narrow.cu", "logits_process.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -7,8 +7,8 @@
 // Hkv x nrb units (a key/value head and a block of at most RB rows, a row being a node and one of the
 // Hq/Hkv query heads that share the head), each of `tiles` tiles of keys.
 //
-// Cut. All tiles of all units stand in one line, W of them. Block c of ncta takes tiles [b_c, b_{c+1}),
-// b_c = floor(W c / ncta): equal shares whatever the lengths are. Where a cut falls inside a unit, or a
+// Cut. All tiles of all units stand in one line, W of them (below 2^31). Block c of ncta takes W / ncta of them,
+// the first W % ncta blocks one more: equal shares whatever the lengths are. Where a cut falls inside a unit, or a
 // row has a shared and an own unit, the pieces leave (sum, max, weighted values) in a slot and the
 // combining kernel joins them in a fixed order. A piece of unit u in block c has the number u + c:
 // both rise along the line and one of them rises from piece to piece, so no two pieces share a number.
@@ -18,20 +18,20 @@
 
 namespace smcsd {
 
-struct AttnItem {
+struct __align__(16) AttnItem {
     int node0, nodes;   // rows of q
     int tile0, tiles;   // key tiles of each unit
     int nrb, per;       // row blocks, rows in each of them (the last one may be shorter)
     int seq, unit0;     // page table row; number of the first unit
-    long long cum;      // first tile on the line
+    int cum;            // first tile on the line
+    int pad[3];
 };
 
 struct AttnHead {  // written by the planning kernel
     int flag;      // error flag (first word of every workspace)
     unsigned done; // blocks of the planning kernel that have finished
-    int ncta;
-    int units_shared;  // units of shared items
-    long long W;
+    int ncta, base, rest;  // W = ncta * base + rest
+    int units_shared;      // units of shared items
 };
 
 struct AttnLayout {
@@ -122,13 +122,14 @@ __device__ __forceinline__ int attn_ctx(const AttnParams& p, int s, int n) {
     return c;
 }
 
-__device__ __forceinline__ long long attn_cut(long long W, int ncta, int c) { return W * c / ncta; }
-__device__ __forceinline__ int attn_cta_of(long long W, int ncta, long long x) {
-    return (int)(((x + 1) * ncta - 1) / W);
+__device__ __forceinline__ int attn_cut(const AttnHead* h, int c) { return h->base * c + min(c, h->rest); }
+__device__ __forceinline__ int attn_cta_of(const AttnHead* h, int x) {
+    const int first = h->rest * (h->base + 1);  // tiles of the longer shares
+    return x < first ? x / (h->base + 1) : h->rest + (x - first) / h->base;
 }
 
-// Item that tile x of the line lies in.
-__device__ __forceinline__ int attn_find(const AttnItem* it, int n, long long x) {
+// Item that tile x of the line lies in: among items that begin at the same place the last one, which has tiles.
+__device__ __forceinline__ int attn_find(const AttnItem* it, int n, int x) {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -137,7 +138,7 @@ __device__ __forceinline__ int attn_find(const AttnItem* it, int n, long long x)
         else
             hi = mid - 1;
     }
-    return lo;  // among items of no tiles at the same place the last one, which has some
+    return lo;
 }
 
 // One piece of a unit, as a block walks along its share of the line.
@@ -151,11 +152,10 @@ struct AttnPiece {
     float2* ml;
 };
 
-__device__ __forceinline__ AttnPiece attn_piece(const AttnParams& p, const AttnItem& it, bool own, long long x,
-                                                long long end, int cta, int units_shared, long long& next) {
+__device__ __forceinline__ AttnPiece attn_piece(const AttnParams& p, const AttnItem& it, bool own, int x, int end, int cta,
+                                                int units_shared, int& next) {
     AttnPiece c;
-    const long long in = x - it.cum;
-    const int u = (int)(in / it.tiles), t = (int)(in - (long long)u * it.tiles);
+    const int in = x - it.cum, u = in / it.tiles, t = in - u * it.tiles;
     c.node0 = it.node0;
     c.seq = it.seq;
     c.hkv = u / it.nrb;
@@ -163,13 +163,13 @@ __device__ __forceinline__ AttnPiece attn_piece(const AttnParams& p, const AttnI
     c.row0 = rb * it.per;
     const int left = it.nodes * p.gq - c.row0;
     c.rows = left < it.per ? left : it.per;
-    const long long unit_end = x - t + it.tiles;
+    const int unit_end = x - t + it.tiles;
     next = unit_end < end ? unit_end : end;
     c.t0 = it.tile0 + t;
-    c.t1 = c.t0 + (int)(next - x);
+    c.t1 = c.t0 + (next - x);
     c.own = own;
     c.whole = own && it.tile0 == 0 && t == 0 && next == unit_end;
-    const long long unit = it.unit0 + u;
+    const int unit = it.unit0 + u;
     if (own) {
         const size_t slot = (size_t)(unit - units_shared + cta);
         c.o = ws_ptr<float>(p.ws, p.L.slot_s) + slot * p.L.rows_s * p.D;
@@ -199,7 +199,8 @@ __device__ __forceinline__ int attn_page(const AttnParams& p, int seq, int j) {
 
 cudaError_t launch_attn_plan(const AttnParams& p, cudaStream_t st);
 cudaError_t launch_attn_simt(const AttnParams& p, cudaStream_t st);  // float32
-cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t st);  // bf16
+cudaError_t launch_attn_wide(const AttnParams& p, cudaStream_t st);    // bf16, row blocks of 256
+cudaError_t launch_attn_narrow(const AttnParams& p, cudaStream_t st);  // bf16, row blocks of 128
 cudaError_t launch_attn_combine(const AttnParams& p, int dtype, cudaStream_t st);
 
 }  // namespace smcsd

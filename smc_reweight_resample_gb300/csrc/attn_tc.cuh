@@ -1,0 +1,383 @@
+// attn_tc.cuh -- what the two tensor-core kernels of tree_attention share: tcgen05 / TMA / mbarrier
+// instructions, bounded waits, the walk along a block's share of the line, the warp that brings the pages
+// of keys and values into the ring, the masks of a tile's positions, and the tensor maps.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "attn_plan.cuh"
+
+namespace smcsd {
+
+namespace {
+
+constexpr int kTile = 128;        // keys of a tile
+constexpr int kHalf = 128 * 128;  // bytes of 128 rows of 64 bf16
+
+// ---- instructions ----
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(2000u)  // at most about 2 us
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// One thread of a converged warp, the same each time. Work that is issued by one thread stays in code that the whole
+// warp runs up to the instruction itself, with values that are the same in all lanes (uniform): the instructions
+// of the tensor core and the copy engine take their operands from the warp's uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// both operands in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// the first operand in tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void ld32(uint32_t addr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Shared-memory operand of a product: 128-byte swizzle. Rows along the sum's dimension (K-major): groups of
+// 8 rows 1024 bytes apart. Rows along the output's dimension (the values: a key's 64 columns in a row):
+// groups of 8 keys 1024 bytes apart, blocks of 64 columns kHalf apart.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t block = kHalf) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+// Instruction: float32 sums, bf16 operands, 128 x n outputs; amn / bmn: that operand's rows lie along the output
+__host__ __device__ constexpr uint32_t instruction(int n, int amn, int bmn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)amn << 15) | ((uint32_t)bmn << 16) | ((uint32_t)(n / 8) << 17) |
+           ((128u / 16) << 24);
+}
+
+struct Ctl {
+    void* ws;
+    int* abort;
+};
+// Waits are bounded: each try suspends the thread for a few microseconds at most, and after kTries of them (0.1 to
+// a few seconds) the error is recorded and every later wait of the block returns.
+constexpr int kTries = 1 << 20;
+__device__ __forceinline__ void give_up(const Ctl& c) {
+    raise_error(c.ws, kErrTimeout);
+    *reinterpret_cast<volatile int*>(c.abort) = 1;
+}
+// one thread of a warp
+__device__ __forceinline__ void wait1(const Ctl& c, uint32_t bar, uint32_t parity) {
+    int tries = 0;
+#pragma unroll 1
+    while (!mbar_try(bar, parity)) {
+        if (++tries < kTries && !*reinterpret_cast<volatile int*>(c.abort)) continue;
+        give_up(c);
+        break;
+    }
+}
+// a whole warp
+__device__ __forceinline__ void wait(const Ctl& c, uint32_t bar, uint32_t parity) {
+    wait1(c, bar, parity);
+    __syncwarp();
+}
+
+// The pieces of a block's share, walked alike by all of its warps.
+struct Walk {
+    int x, end, item_end;
+    int ii, units_shared;
+    const AttnItem* items;
+    AttnItem it;
+};
+// One warp: the item that the block's first tile lies in (the last one that begins at or before it), 32 at a time.
+__device__ __forceinline__ int walk_start(const AttnParams& p, int lane) {
+    const AttnHead* h = attn_head(p);
+    const int cta = blockIdx.x, n = p.G + p.S;
+    if (cta >= h->ncta) return 0;
+    const int x = attn_cut(h, cta);
+    const AttnItem* items = ws_ptr<AttnItem>(p.ws, p.L.item);
+    int lo = 0, len = n;  // the answer is one of items [lo, lo + len)
+    while (len > 1) {
+        const int step = (len + 31) / 32, at = lo + lane * step;
+        const bool below = lane * step < len && __ldcg(&items[at].cum) <= x;
+        const int k = max(0, __popc(__ballot_sync(0xffffffffu, below)) - 1);
+        len = min(step, len - k * step);
+        lo += k * step;
+    }
+    return lo;
+}
+__device__ __forceinline__ Walk walk_begin(const AttnParams& p, int start) {
+    const AttnHead* h = attn_head(p);
+    const int cta = blockIdx.x;
+    Walk w;
+    w.units_shared = h->units_shared;
+    w.items = ws_ptr<AttnItem>(p.ws, p.L.item);
+    w.ii = start - 1;
+    w.x = w.end = w.item_end = 0;
+    if (cta < h->ncta) {
+        w.x = w.item_end = attn_cut(h, cta);
+        w.end = attn_cut(h, cta + 1);
+    }
+    return w;
+}
+__device__ __forceinline__ bool walk_next(const AttnParams& p, Walk& w, AttnPiece& c) {
+    if (w.x >= w.end) return false;
+    while (w.x >= w.item_end) {  // x is below W, so an item that holds it follows
+        w.it = w.items[++w.ii];
+        w.item_end = w.it.cum + w.it.tiles * w.it.nrb * p.Hkv;
+    }
+    int next;
+    c = attn_piece(p, w.it, w.ii >= p.G, w.x, w.end, blockIdx.x, w.units_shared, next);
+    w.x = next;
+    return true;
+}
+
+// After a wait that ran out: gives copies and products in flight time to land before the block's shared and
+// tensor memory is handed on.
+__device__ __forceinline__ void settle(int* abort) {
+    if (!*reinterpret_cast<volatile int*>(abort)) return;
+    const unsigned long long t0 = now_ns();
+    while (now_ns() - t0 < 20000000ull) __nanosleep(1000);
+}
+// the warps of the softmax
+template <int kThreads>
+__device__ __forceinline__ void rows_sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
+
+// ---- keys and values ----
+
+// A ring of shared-memory stages that one warp fills, tile after tile.
+template <int kStages>
+struct Ring {
+    uint64_t full[kStages], empty[kStages];
+    __device__ __forceinline__ void init() {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&empty[i]), 1);
+        }
+    }
+};
+
+// One warp for the keys and one for the values: the pages of every tile into its ring of D / 64 * kHalf bytes a
+// stage. A lane holds one page id (a box: up to 128 positions of one page); 32 ids are read at a time, the next 32
+// while these are used. The copies are issued by one thread with the id handed round: lanes issuing a copy each
+// take turns anyway, at four times the cost. Pages past the end are not read.
+template <int D, int kStages>
+__device__ void tc_producer(const AttnParams& p, const CUtensorMap* map, const Ctl& ctl, Ring<kStages>* rg, uint32_t ring, int lane,
+                            int start) {
+    constexpr int kHalves = D / 64, kStage = kHalves * kHalf;
+    const int box = p.page_size < kTile ? p.page_size : kTile;  // rows of one copy
+    const int box_shift = p.page_shift < 7 ? p.page_shift : 7, nbox = kTile >> box_shift;
+    Walk w = walk_begin(p, start);
+    AttnPiece c;
+    uint32_t st = 0, round = 0;
+    while (walk_next(p, w, c)) {
+        const int keys = c.own ? __ldg(p.ctx_len + c.seq) + w.it.nodes : INT_MAX;
+        const int32_t* row = p.table + (long long)c.seq * p.pages_per_seq;
+        const int last = min((long long)c.t1 * kTile, (long long)keys);  // end of the piece's positions
+        auto ids = [&](int batch) {  // of the 32 boxes from 32 * batch on
+            const int pos = c.t0 * kTile + ((32 * batch + lane) << box_shift);
+            return pos < last ? __ldg(row + (pos >> p.page_shift)) : 0;
+        };
+        int id = ids(0), next = ids(1), batch = 1;
+#pragma unroll 1
+        for (int t = c.t0, x = 0; t < c.t1; ++t, x += nbox) {
+            if (x == 32) {
+                x = 0;
+                id = next;
+                next = ids(++batch);
+            }
+            const int boxes = min(nbox, (last - t * kTile + box - 1) >> box_shift);
+            if (round > 0) wait(ctl, smem_u32(&rg->empty[st]), (round - 1) & 1);
+            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(ctl.abort))) return;
+            if (id < 0 || id >= p.num_pages) {
+                raise_error(p.ws, kErrRange);
+                id = 0;
+            }
+            const int ust = uniform(st), uboxes = uniform(boxes);
+            const uint32_t bar = smem_u32(&rg->full[ust]);
+            uint32_t to = ring + ust * kStage;
+            const int at = uniform(c.hkv * p.page_size + ((t * kTile) & (p.page_size - 1)));
+            if (elect_one()) mbar_expect_tx(bar, (uint32_t)(uboxes * box * 128 * kHalves));
+            __syncwarp();
+            for (int b = 0; b < uboxes; ++b, to += box * 128) {
+                const int page = uniform(__shfl_sync(0xffffffffu, id, x + b));
+                if (elect_one()) {
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) tma_tile(to + h * kHalf, map, h * 64, at, page, bar);
+                }
+            }
+            if (++st == kStages) st = 0, ++round;
+        }
+    }
+}
+
+// ---- masks ----
+
+// Zeroes what the product with V must not meet in one key's row of one half: everything past the end,
+// NaN and infinities in nodes (rows of zero weight would turn them into NaN). True if there were some.
+__device__ __forceinline__ bool clean_row(uint32_t half, int k, bool past) {
+    bool found = false;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t at = half + k * 128 + i * 16;
+        uint32_t v[4];
+        if (past) {
+            v[0] = v[1] = v[2] = v[3] = 0;
+        } else {
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u, bad = true;
+                if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0x0000ffffu, bad = true;
+            }
+            if (!bad) continue;
+            found = true;
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+    }
+    return found;
+}
+
+// Which of 32 positions from `base` on a row sees.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+__device__ __forceinline__ uint32_t seen32(const AttnParams& p, const uint32_t* mask_row, int node, int ctx, int keys, int base) {
+    const int j0 = base - ctx;
+    uint32_t nodes;
+    if (mask_row) {
+        const int wd = j0 >> 5, sh = j0 & 31;  // floor
+        const uint32_t lo = wd >= 0 && wd < p.words ? __ldg(mask_row + wd) : 0u;
+        const uint32_t hi = wd + 1 >= 0 && wd + 1 < p.words ? __ldg(mask_row + wd + 1) : 0u;
+        nodes = __funnelshift_r(lo, hi, sh);
+    } else {
+        nodes = low_bits(node + 1 - j0);
+    }
+    return (low_bits(-j0) | nodes) & low_bits(keys - base);
+}
+
+// ---- tensor maps ----
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// A cache as [num_pages][Hkv * page_size][D], in boxes of 64 columns and up to 128 positions of one head.
+bool encode_cache(CUtensorMap* m, const void* base, const AttnParams& p) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dim[3] = {(cuuint64_t)p.D, (cuuint64_t)p.Hkv * p.page_size, (cuuint64_t)p.num_pages};
+    const cuuint64_t stride[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.D * 2 * p.Hkv * p.page_size};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(p.page_size < kTile ? p.page_size : kTile), 1}, one[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Kernel>
+cudaError_t launch_tc(Kernel kern, int threads, int smem, const AttnParams& p, cudaStream_t st) {
+    CUtensorMap mk, mv;
+    if (!encode_cache(&mk, p.k_cache, p) || !encode_cache(&mv, p.v_cache, p)) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.ncta_max);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, mk, mv);
+}
+
+}  // namespace
+
+}  // namespace smcsd

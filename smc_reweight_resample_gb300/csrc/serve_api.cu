@@ -42,11 +42,20 @@ bool attn_sizes_ok(int S, int N, int T, int Hq, int Hkv, int D) {
     return rows * N < (1ll << 30) && (long long)S * Hkv * (rows / 16 + 1) < (1ll << 30);
 }
 
-// float32: the FP32 pipes, 64 keys x 16 rows at a time; bf16: the tensor cores, 128 keys x up to 256 rows
+// float32: the FP32 pipes, 64 keys x 16 rows at a time. bf16: the tensor cores, 128 keys x up to 128 rows of a
+// sequence (narrow) or 256 (wide).
+enum AttnKind { kSimt, kNarrow, kWide };
 constexpr int kSimtBlocksPerSm = 2;
 
-AttnLayout layout_of(int dtype, int S, int N, int T, int Hq, int Hkv, int D) {
-    return attn_layout(S, N, T, Hq / Hkv, Hkv, D, dtype == SMCSD_F32 ? 16 : 256, kAttnMaxCta);
+AttnKind kind_of(int dtype, int T, int Hq, int Hkv) {
+    if (dtype == SMCSD_F32) return kSimt;
+    return (long long)T * (Hq / Hkv) <= 128 ? kNarrow : kWide;
+}
+
+int rows_of(AttnKind k) { return k == kSimt ? 16 : k == kNarrow ? 128 : 256; }
+
+AttnLayout layout_of(AttnKind k, int S, int N, int T, int Hq, int Hkv, int D) {
+    return attn_layout(S, N, T, Hq / Hkv, Hkv, D, rows_of(k), kAttnMaxCta);
 }
 
 }  // namespace
@@ -135,7 +144,8 @@ extern "C" int tree_mask(const int32_t* parents, const int32_t* node_offsets, in
 
 extern "C" size_t tree_attention_workspace_size(int S, int N, int T, int Hq, int Hkv, int D) {
     if (!attn_sizes_ok(S, N, T, Hq, Hkv, D)) return 0;
-    const size_t a = layout_of(SMCSD_F32, S, N, T, Hq, Hkv, D).total, b = layout_of(SMCSD_BF16, S, N, T, Hq, Hkv, D).total;
+    const size_t a = layout_of(kSimt, S, N, T, Hq, Hkv, D).total,
+                 b = layout_of(kind_of(SMCSD_BF16, T, Hq, Hkv), S, N, T, Hq, Hkv, D).total;
     return a > b ? a : b;
 }
 
@@ -184,14 +194,19 @@ extern "C" int tree_attention(const void* q, long long q_stride, const void* k_c
     p.lse = lse;
     p.ws = ws;
     cudaStream_t st = (cudaStream_t)stream;
-    p.L = layout_of(dtype, S, N, T, Hq, Hkv, D);
-    p.tile = dtype == SMCSD_F32 ? 64 : 128;
-    p.rb = dtype == SMCSD_F32 ? 16 : 256;
-    p.ncta_max = device_sm_count() * (dtype == SMCSD_F32 ? kSimtBlocksPerSm : 1);
+    const AttnKind kind = kind_of(dtype, T, Hq, Hkv);
+    // all tiles of all units are numbered in 32 bits
+    const long long units = (long long)S * Hkv * attn_blocks((long long)T * p.gq, rows_of(kind)) +
+                            (long long)p.G * Hkv * attn_blocks((long long)N * T * p.gq, rows_of(kind));
+    if (units * (((long long)pages_per_seq * page_size + 63) / 64) > 0x7fffffffLL) return SMCSD_ERR_INVALID_ARG;
+    p.L = layout_of(kind, S, N, T, Hq, Hkv, D);
+    p.tile = kind == kSimt ? 64 : 128;
+    p.rb = rows_of(kind);
+    p.ncta_max = device_sm_count() * (kind == kSimt ? kSimtBlocksPerSm : 1);
     if (p.ncta_max > kAttnMaxCta) p.ncta_max = kAttnMaxCta;
     p.min_tiles = 1;
     cudaError_t e = launch_attn_plan(p, st);
-    if (e == cudaSuccess) e = dtype == SMCSD_F32 ? launch_attn_simt(p, st) : launch_attn_tc(p, st);
+    if (e == cudaSuccess) e = kind == kSimt ? launch_attn_simt(p, st) : kind == kNarrow ? launch_attn_narrow(p, st) : launch_attn_wide(p, st);
     if (e == cudaSuccess) e = launch_attn_combine(p, dtype, st);
     return from_cuda(e);
 }

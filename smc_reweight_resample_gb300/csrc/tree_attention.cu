@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         if (it.nodes == 0 || it.tiles < 0) it.tiles = 0;
         const int u = it.tiles > 0 ? p.Hkv * it.nrb : 0;
         it.unit0 = u;
-        it.cum = (long long)u * it.tiles;
+        it.cum = u * it.tiles;
         items[i] = it;
         tiles += it.cum;
         units += u;
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     const long long W = sa[32];
     for (int i = i0; i < i1; ++i) {
         const long long ct = items[i].cum, cu = items[i].unit0;
-        items[i].cum = t;
+        items[i].cum = (int)t;
         items[i].unit0 = (int)u;
         t += ct;
         u += cu;
@@ -134,10 +134,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     scan_pair(grp, zero, sa, sb);
     if (tid == 0) {
         AttnHead* h = attn_head(p);
-        h->W = W;
         h->units_shared = (int)sa[32];
         const long long most = (W + p.min_tiles - 1) / p.min_tiles;
-        h->ncta = (int)(most < p.ncta_max ? most : p.ncta_max);
+        const int n = (int)(most < p.ncta_max ? most : p.ncta_max);
+        h->ncta = n;
+        h->base = n > 0 ? (int)(W / n) : 0;
+        h->rest = n > 0 ? (int)(W % n) : 0;
     }
 }
 
@@ -181,17 +183,16 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
     griddep_wait();
     griddep_launch_dependents();
     const AttnHead* h = attn_head(p);
-    const long long W = h->W;
-    const int ncta = h->ncta, cta = blockIdx.x;
-    if (cta >= ncta) return;
+    const int cta = blockIdx.x;
+    if (cta >= h->ncta) return;
     const AttnItem* items = ws_ptr<AttnItem>(p.ws, p.L.item);
-    long long x = attn_cut(W, ncta, cta);
-    const long long end = attn_cut(W, ncta, cta + 1);
+    int x = attn_cut(h, cta);
+    const int end = attn_cut(h, cta + 1);
     const int n_items = p.G + p.S;
     while (x < end) {
         const int ii = attn_find(items, n_items, x);
         const AttnItem it = items[ii];
-        long long next;
+        int next;
         const AttnPiece c = attn_piece(p, it, ii >= p.G, x, end, cta, h->units_shared, next);
         x = next;
         const int ctx = c.own ? __ldg(p.ctx_len + c.seq) : INT_MAX;
@@ -379,8 +380,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(const __g
     const int s = attn_seq_of(p, r);
     const AttnHead* h = attn_head(p);
     const AttnItem* items = ws_ptr<AttnItem>(p.ws, p.L.item);
-    const long long W = h->W;
-    const int ncta = h->ncta;
     float m = kNegInf, l = 0.0f;
     constexpr int kE = D / 32;
     float acc[kE];
@@ -393,8 +392,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(const __g
         if (node < 0 || node >= it.nodes) return;  // bad offsets, already reported
         const int row = node * p.gq + (hq - hkv * p.gq), rb = row / it.per, rr = row - rb * it.per;
         const int u = hkv * it.nrb + rb;
-        const long long x0 = it.cum + (long long)u * it.tiles, x1 = x0 + it.tiles;
-        const int c0 = attn_cta_of(W, ncta, x0), c1 = attn_cta_of(W, ncta, x1 - 1);
+        const int x0 = it.cum + u * it.tiles;
+        const int c0 = attn_cta_of(h, x0), c1 = attn_cta_of(h, x0 + it.tiles - 1);
         if (k == 1 && it.tile0 == 0 && c0 == c1) return;  // written directly
         for (int c = c0; c <= c1; ++c) {
             const size_t slot = k == 0 ? (size_t)(it.unit0 + u + c) : (size_t)(it.unit0 + u - h->units_shared + c);

@@ -1,0 +1,538 @@
+// tree_attention_narrow.cu -- attention of drafted tokens over a paged bf16 cache on the tensor cores, for
+// sequences of up to 128 rows (a row is a node and one of the query heads that share a key/value head).
+//
+// A unit of few rows is bound by the bytes of its keys and values, so the products are turned: the 128 keys of a
+// tile are the rows of the tensor core's output and the query rows its columns,
+//   S^T = K Q^T   (128 keys x N, in tensor memory),   O^T += V^T P^T   (D x N, in tensor memory),
+// which costs N / 128 of the products of padded query rows, and a thread holds one key: 32 exponentials for
+// each of 128 threads in place of 128 for each of 32. Blocks, tiles and cut are those of attn_plan.cuh.
+//   warps 0-15  four groups of four, one thread per key and 32 columns: exponentials, sums, P (bf16) to shared
+//               memory. With up to 32 rows the groups take four tiles at a time, with up to 64 two tiles in
+//               two halves of the rows, above one tile in quarters: group w always has columns 32 w .. 32 w + 31
+//               of the 128 that scores, weights and outputs have.
+//   warps 16 and 18  bring pages of keys and of values into their rings (attn_tc.cuh)
+//   warp 17     issues the products; scores and weights have two buffers, and the scores of the next round of
+//               tiles but one are issued before the weights of this one are there
+//   (warp 19 idle: registers are handed over by fours)
+//
+// Softmax. Per column: a reference m common to the keys of the group's tiles, P = exp2(z - m) with
+// z = scale2 q.k, l the sum of P before it is rounded (each thread adds up its own keys; they meet at the end of
+// the unit) and O. Any reference that keeps exp2 in range serves, so the maximum over the keys is not taken for
+// each tile: a vote of the four warps asks whether some z - m is above 8, and only then (always in a group's first
+// tile) the maximum of that column becomes the new reference and l and O are rescaled. Weights stay below 2^8;
+// sums are in float32; P is rounded to bf16 for the product with V, as in the wide kernel.
+#include "attn_tc.cuh"
+
+namespace smcsd {
+
+namespace {
+
+constexpr int kTcThreads = 640, kSoftThreads = 512;
+constexpr float kNone = -3.402823466e38f;  // reference of a column that has seen nothing: any score is above it
+
+template <int D>
+struct NarrowGeo {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kStage = kHalves * kHalf;
+    static constexpr int kKeys = D == 128 ? 2 : 4, kValues = D == 128 ? 2 : 5;  // stages
+    static constexpr int kWeights = 2 * kHalf;  // one buffer of P: 128 columns x 128 keys
+    static constexpr int kSmem = 1024 + kStage + 2 * kWeights + (kKeys + kValues) * kStage;
+};
+
+template <int D>
+struct __align__(16) NarrowShared {
+    __align__(16) float m[kTile];  // references, read four at a time
+    Ring<NarrowGeo<D>::kKeys> rk;
+    Ring<NarrowGeo<D>::kValues> rv;
+    uint64_t q_full, v_full[2];
+    uint64_t s_full[4][2], o_full[4][2];  // [tile of a round][buffer]
+    uint64_t p_full[4][2];                // [group][buffer]
+    uint32_t tmem;
+    int abort, start;
+    int poison;  // a NaN or infinity among the values of the piece's nodes
+};
+
+// How a unit's rows and tiles are laid over the four groups.
+struct Split {
+    int log_tiles;  // tiles of a round: 4, 2 or 1
+    int log_chunks; // groups side by side on the rows of one tile: 1, 2 or 4
+    int used;       // chunks that have rows
+    __device__ __forceinline__ explicit Split(int rows) {
+        log_chunks = (rows > 32) + (rows > 64);
+        log_tiles = 2 - log_chunks;
+        used = (rows + 31) >> 5;
+    }
+    __device__ __forceinline__ int tiles() const { return 1 << log_tiles; }
+    __device__ __forceinline__ int chunks() const { return 1 << log_chunks; }
+    // tiles of n that are number k of their round
+    __device__ __forceinline__ int rounds(int n, int k) const { return (n - k + tiles() - 1) >> log_tiles; }
+};
+
+// How often the barriers of (tile of a round, buffer) were used by earlier pieces: parities, bit 2 k + b.
+struct Uses {
+    uint32_t bits;
+    __device__ __forceinline__ uint32_t parity(int k, int b, int use) const { return ((bits >> (2 * k + b)) ^ use) & 1u; }
+    __device__ __forceinline__ void add(int n, const Split& sp) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t r = k < sp.tiles() ? sp.rounds(n, k) : 0;
+            bits ^= (((r + 1) >> 1) & 1u) << (2 * k) | ((r >> 1) & 1u) << (2 * k + 1);
+        }
+    }
+};
+
+// ---- products ----
+
+template <int D>
+__device__ void narrow_issue(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, uint32_t sq, uint32_t sp, uint32_t ring_k, uint32_t ring_v,
+                             uint32_t tmem, int start) {
+    using G = NarrowGeo<D>;
+    Walk w = walk_begin(p, start);
+    AttnPiece c;
+    uint32_t f0 = 0, pieces = 0, tails = 0;
+    uint32_t p_uses = 0;  // parity of the next use of p_full[group][buffer], bit 2 * group + buffer
+    while (walk_next(p, w, c)) {
+        const int n = uniform(c.t1 - c.t0);
+        const Split split(uniform(c.rows));
+        const int ahead = 2 * split.tiles(), width = 32 * split.chunks();
+        const uint32_t is = instruction(32 * split.used, 0, 0), io = instruction(32 * split.used, 1, 1);
+        const int first_tail = c.own ? (__ldg(p.ctx_len + c.seq) >> 7) - c.t0 : n;
+        auto scores = [&](int t) {
+            const int k = t & (split.tiles() - 1), b = (t >> split.log_tiles) & 1;
+            const uint32_t f = f0 + t, st = f % G::kKeys;
+            wait(ctl, smem_u32(&sh->rk.full[st]), (f / G::kKeys) & 1);
+            tc_fence_after();
+            const uint64_t ka = operand(ring_k + st * G::kStage), qb = operand(sq);
+            const uint32_t to = tmem + 128 * b + width * k;
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint64_t at = (uint64_t)(((i / 4) * kHalf + (i % 4) * 32) >> 4);
+                    mma_ss(to, ka + at, qb + at, is, i > 0);
+                }
+                tc_commit(smem_u32(&sh->rk.empty[st]));
+                tc_commit(smem_u32(&sh->s_full[k][b]));
+            }
+            __syncwarp();
+        };
+        wait(ctl, smem_u32(&sh->q_full), pieces & 1);
+        ++pieces;
+#pragma unroll 1
+        for (int u = 0; u < n + ahead; ++u) {
+            const int t = u - ahead;
+            if (t >= 0) {
+                const int k = t & (split.tiles() - 1), r = t >> split.log_tiles, b = r & 1;
+                const uint32_t f = f0 + t, st = f % G::kValues;
+                wait(ctl, smem_u32(&sh->rv.full[st]), (f / G::kValues) & 1);
+                if (t >= first_tail) {
+                    if (elect_one()) mbar_arrive(smem_u32(&sh->v_full[tails & 1]));
+                    ++tails;
+                }
+                for (int x = 0; x < split.used; ++x) {
+                    const int bit = 2 * ((k << split.log_chunks) + x) + b;
+                    wait(ctl, smem_u32(&sh->p_full[0][0]) + 8 * bit, (p_uses >> bit) & 1);
+                    p_uses ^= 1u << bit;
+                }
+                tc_fence_after();
+                // 64 columns of V have no second block: the upper half of the outputs repeats the lower one
+                const uint64_t va = operand(ring_v + st * G::kStage, D == 128 ? kHalf : 0);
+                const uint64_t pb = operand(sp + b * G::kWeights + (width * k / 64) * kHalf + (width * k % 64) * 2);
+                const uint32_t to = tmem + 256 + width * k, more = r > 0;
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i) {
+                        const uint64_t at = (uint64_t)((i * 2048) >> 4);
+                        mma_ss(to, va + at, pb + at, io, i > 0 ? 1u : more);
+                    }
+                    tc_commit(smem_u32(&sh->rv.empty[st]));
+                    tc_commit(smem_u32(&sh->o_full[k][b]));
+                }
+                __syncwarp();
+            }
+            if (u < n) scores(u);
+        }
+        f0 += n;
+    }
+}
+
+// ---- softmax ----
+
+// 32 lanes' sums of 32 columns: lane k gets column k's.
+__device__ __forceinline__ float sum_columns(float* v, int lane) {
+#pragma unroll
+    for (int h = 16; h > 0; h >>= 1) {
+        const bool up = lane & h;
+#pragma unroll
+        for (int j = 0; j < h; ++j) {
+            const float send = up ? v[j] : v[j + h], keep = up ? v[j + h] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xffffffffu, send, h);
+        }
+    }
+    return v[0];
+}
+
+__device__ __forceinline__ void ld8(uint32_t addr, float* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void st8(uint32_t addr, const float* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                 "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "r"(addr)
+                 : "memory");
+}
+
+// Whether any thread of a group's four warps says yes.
+__device__ __forceinline__ bool group_any(int g, bool yes) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, 128, q;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)yes), "r"(2 + g)
+                 : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_sync(int g) {
+    __syncwarp();
+    asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory");
+}
+
+// What the row's nodes with a NaN or infinity in column d of their values add to it.
+__device__ __forceinline__ float poison_of(const AttnParams& p, const AttnPiece& c, int nodes, int node, int ctx, int d) {
+    const int j0 = max(0, c.t0 * kTile - ctx), j1 = min(nodes, c.t1 * kTile - ctx);
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+        if (!attn_sees(p, (long long)c.node0 + node, node, j)) continue;
+        const int pos = ctx + j;
+        const size_t page = attn_page(p, c.seq, pos >> p.page_shift);
+        const uint32_t b = __ldg(static_cast<const uint16_t*>(p.v_cache) +
+                                 ((page * p.Hkv + c.hkv) * p.page_size + (pos & (p.page_size - 1))) * p.D + d);
+        if ((b & 0x7f80u) == 0x7f80u) sum += __uint_as_float(b << 16);
+    }
+    return sum;
+}
+
+template <int D>
+__device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, unsigned char* sq, unsigned char* spw,
+                               uint32_t ring_v, uint32_t tmem, int start) {
+    using G = NarrowGeo<D>;
+    const int tid = threadIdx.x, lane = tid & 31, g = tid >> 7, key = tid & 127, quad = (tid >> 5) & 3;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;  // a negative scale goes into q
+    const float scale = fabsf(p.scale2) > 0.0f ? fabsf(p.scale2) : 1e-30f;  // 0: equal weights, and -inf stays -inf
+    float* my_m = &sh->m[32 * g];
+    // This group's 32 columns of the weights' buffer b: 64 bytes of each key's 128-byte line, swizzled. Sixteen
+    // places of the first eight keys' also carry 4 x 32 floats (one of each warp and column) between products.
+    auto place = [&](int group, int b, int wq) {
+        const int x = 8 * wq + (lane >> 2), k = x >> 2;
+        return reinterpret_cast<float*>(spw + b * G::kWeights + (group >> 1) * kHalf + k * 128 +
+                                        ((((group & 1) * 4 + (x & 3)) ^ (k & 7)) << 4)) + (lane & 3);
+    };
+    Walk w = walk_begin(p, start);
+    AttnPiece c;
+    Uses uses{};
+    uint32_t f0 = 0, tails = 0;
+    while (walk_next(p, w, c)) {
+        const int n = c.t1 - c.t0;
+        const Split split(c.rows);
+        const int k = g >> split.log_chunks, chunk = g & (split.chunks() - 1);
+        const int ctx = c.own ? __ldg(p.ctx_len + c.seq) : INT_MAX, keys = c.own ? ctx + w.it.nodes : INT_MAX;
+        const int first_tail = c.own ? (ctx >> 7) - c.t0 : n;
+        for (int i = tid; i < split.used * 32 * (D / 8); i += kSoftThreads) {
+            const int r = i / (D / 8), ch = i - r * (D / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);  // padding columns: scores of zero
+            if (r < c.rows) {
+                const int row = c.row0 + r, node = row / p.gq, hq = c.hkv * p.gq + (row - node * p.gq);
+                v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                         (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + ch * 8));
+                v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+            }
+            *reinterpret_cast<uint4*>(sq + (ch / 8) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+        }
+        if (quad == 0) my_m[lane] = kNone;
+        if (tid == 0) sh->poison = 0;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
+        rows_sync<kSoftThreads>();  // the references and the flag are set
+        float l[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) l[e] = 0.0f;
+        // this lane's row of the group's chunk
+        const int my_row = c.row0 + min(32 * chunk + lane, c.rows - 1), my_node = my_row / p.gq;
+        const int rounds = chunk < split.used ? split.rounds(n, k) : 0;
+#pragma unroll 1
+        for (int i = 0; i < rounds; ++i) {
+            const int tt = (i << split.log_tiles) + k, pos0 = (c.t0 + tt) * kTile, b = i & 1;
+            const bool tail = tt >= first_tail;
+            // the product that read these weights last
+            if (i >= 2) wait(ctl, smem_u32(&sh->o_full[k][b]), uses.parity(k, b, i / 2 - 1));
+            wait(ctl, smem_u32(&sh->s_full[k][b]), uses.parity(k, b, i / 2));
+            tc_fence_after();
+            uint32_t seen = 0xffffffffu;  // rows that see this thread's key
+            if (tail) {
+                // lane e works out which of the warp's 32 keys row e sees; then every lane picks its key's bits
+                const uint32_t* mask_row = p.mask ? p.mask + (long long)(c.node0 + my_node) * p.words : nullptr;
+                const uint32_t row_sees = seen32(p, mask_row, my_node, ctx, keys, pos0 + 32 * quad);
+                seen = 0;
+#pragma unroll 8
+                for (int e = 0; e < 32; ++e) seen |= ((__shfl_sync(0xffffffffu, row_sees, e) >> lane) & 1u) << e;
+                if (chunk == 0 && pos0 + quad * 32 + 31 >= ctx) {
+                    // A piece has at most two such tiles (up to 128 nodes); the issuing warp reports their values.
+                    const uint32_t x = tails + (tt - max(first_tail, 0));
+                    wait(ctl, smem_u32(&sh->v_full[x & 1]), (x >> 1) & 1);
+                    const uint32_t f = f0 + tt, st = f % G::kValues;
+                    wait(ctl, smem_u32(&sh->rv.full[st]), (f / G::kValues) & 1);  // passed by now: the copy's own barrier
+                    bool found = false;
+                    if (pos0 + key >= ctx) {
+#pragma unroll 1
+                        for (int h = 0; h < G::kHalves; ++h)
+                            found |= clean_row(ring_v + st * G::kStage + h * kHalf, key, pos0 + key >= keys);
+                    }
+                    if (found) sh->poison = 1;
+                }
+            }
+            const uint32_t t_s = tmem + lanes + 128 * b + 32 * g;
+            float z[32];  // scores, then arguments of the exponential
+#pragma unroll 1
+            for (int attempt = 0;; ++attempt) {
+                ld32(t_s, z);
+                tc_wait_ld();
+                if (tail) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) z[e] = (seen >> e) & 1u ? z[e] : kNegInf;
+                }
+                float top = kNegInf;
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(my_m + e);
+                    z[e] = fmaf(z[e], scale, -m.x);
+                    z[e + 1] = fmaf(z[e + 1], scale, -m.y);
+                    z[e + 2] = fmaf(z[e + 2], scale, -m.z);
+                    z[e + 3] = fmaf(z[e + 3], scale, -m.w);
+                    asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(z[e]), "f"(z[e + 1]));
+                    asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(z[e + 2]), "f"(z[e + 3]));
+                }
+                if (attempt == 1 || !group_any(g, top > 8.0f)) break;
+                // the columns' maxima: lane e has the warp's of column e, the four meet in the buffer that the
+                // weights are about to fill
+                float mine = kNegInf;
+#pragma unroll 1
+                for (int e = 0; e < 32; e += 8) {
+                    float v[8];
+                    ld8(t_s + e, v);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        float r = (seen >> (e + x)) & 1u ? v[x] : kNegInf;
+                        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(r));
+                        mine = lane == e + x ? r : mine;
+                    }
+                }
+                *place(g, b, quad) = mine;
+                group_sync(g);
+                const float best = fmaxf(fmaxf(*place(g, b, 0), *place(g, b, 1)), fmaxf(*place(g, b, 2), *place(g, b, 3))) * scale;
+                const float old = my_m[lane];
+                const float to = best - old > 8.0f ? best : old;
+                const float fac = to == old ? 1.0f : ex2(old - to);
+                group_sync(g);    // old references and maxima have been read
+                my_m[lane] = to;  // all four warps: each finds it there from now on
+                __syncwarp();
+                if (i > 0) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) l[e] *= __shfl_sync(0xffffffffu, fac, e);
+                    wait(ctl, smem_u32(&sh->o_full[k][b ^ 1]), uses.parity(k, b ^ 1, (i - 1) / 2));
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int e = 0; e < 32; e += 8) {
+                        float o[8];
+                        ld8(tmem + lanes + 256 + 32 * g + e, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) o[x] *= __shfl_sync(0xffffffffu, fac, e + x);
+                        st8(tmem + lanes + 256 + 32 * g + e, o);
+                    }
+                    tc_wait_st();
+                }
+            }
+            // this key's weights of 32 rows: four 16-byte places of its line
+            unsigned char* line = spw + b * G::kWeights + (g >> 1) * kHalf + key * 128;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float a = ex2(z[e + 2 * x]), d = ex2(z[e + 2 * x + 1]);
+                    l[e + 2 * x] += a;
+                    l[e + 2 * x + 1] += d;
+                    pk[x] = pack_bf16(a, d);
+                }
+                *reinterpret_cast<uint4*>(line + ((((g & 1) * 4 + e / 8) ^ (key & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[g][b]));
+        }
+        // the group's last product; then the statistics meet where the weights were
+        if (rounds > 0) {
+            const int i = rounds - 1;
+            wait(ctl, smem_u32(&sh->o_full[k][i & 1]), uses.parity(k, i & 1, i / 2));
+        }
+        *place(g, 0, quad) = sum_columns(l, lane);
+        rows_sync<kSoftThreads>();
+        tc_fence_after();
+        if (chunk < split.used) {
+            // the groups of a chunk join its rows, each a part of them: lane e has row e's factors
+            float m = kNone, sum = 0.0f, f[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (x < split.tiles()) m = fmaxf(m, sh->m[32 * ((x << split.log_chunks) + chunk) + lane]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                f[x] = 0.0f;
+                if (x >= split.tiles()) continue;
+                const int from = (x << split.log_chunks) + chunk;
+                f[x] = ex2(sh->m[32 * from + lane] - m);
+                sum = fmaf((*place(from, 0, 0) + *place(from, 0, 1)) + (*place(from, 0, 2) + *place(from, 0, 3)), f[x], sum);
+            }
+            if (c.whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) f[x] *= inv;
+            }
+            const int orow = (c.node0 + my_node) * p.Hq + c.hkv * p.gq + (my_row - my_node * p.gq);
+            if (k == 0 && quad == 0 && 32 * chunk + lane < c.rows) {
+                if (!c.whole)
+                    c.ml[32 * chunk + lane] = make_float2(m, sum);
+                else if (p.lse)
+                    p.lse[orow] = sum == 0.0f ? kNegInf : (m + log2f(sum)) * 0.69314718056f;
+            }
+            const int part = 32 >> split.log_tiles, d = quad * 32 + lane, rows = min(32, c.rows - 32 * chunk);
+            const bool poison = sh->poison != 0;
+            if (quad * 32 < D) {  // otherwise repeated outputs
+#pragma unroll 1
+                for (int e = k * part; e < (k + 1) * part && e < rows; e += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) v[y] = 0.0f;
+#pragma unroll 1
+                    for (int x = 0; x < split.tiles() && x < n; ++x) {
+                        float o[8];
+                        ld8(tmem + lanes + 256 + 32 * ((x << split.log_chunks) + chunk) + e, o);
+                        tc_wait_ld();
+                        const float fx = x < 2 ? (x == 0 ? f[0] : f[1]) : (x == 2 ? f[2] : f[3]);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) v[y] = fmaf(o[y], __shfl_sync(0xffffffffu, fx, e + y), v[y]);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const int to = __shfl_sync(0xffffffffu, orow, e + y);
+                        if (e + y >= rows) continue;
+                        if (c.whole)
+                            static_cast<__nv_bfloat16*>(p.out)[(size_t)to * D + d] = __float2bfloat16_rn(v[y]);
+                        else
+                            c.o[(size_t)(32 * chunk + e + y) * D + d] = v[y];
+                    }
+                }
+                if (poison) {
+#pragma unroll 1
+                    for (int e = k * part; e < (k + 1) * part && e < rows; ++e) {
+                        const int row = c.row0 + 32 * chunk + e, node = row / p.gq;
+                        const float v = poison_of(p, c, w.it.nodes, node, ctx, d);
+                        if (v == 0.0f) continue;
+                        const size_t to = (size_t)(c.node0 + node) * p.Hq + c.hkv * p.gq + (row - node * p.gq);
+                        if (c.whole) {
+                            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + to * D + d;
+                            *o = __float2bfloat16_rn(__bfloat162float(*o) + v);
+                        } else {
+                            c.o[(size_t)(32 * chunk + e) * D + d] += v;
+                        }
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+        rows_sync<kSoftThreads>();  // everything has been read: the next piece may write over it
+        f0 += n;
+        tails += n > first_tail ? n - max(first_tail, 0) : 0;
+        uses.add(n, split);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using G = NarrowGeo<D>;
+    extern __shared__ unsigned char dyn[];
+    __shared__ NarrowShared<D> shared;
+    NarrowShared<D>* sh = &shared;
+    unsigned char* sq = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+    unsigned char* spw = sq + G::kStage;
+    const uint32_t ring_k = smem_u32(spw + 2 * G::kWeights), ring_v = ring_k + G::kKeys * G::kStage;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        sh->rk.init();
+        sh->rv.init();
+        mbar_init(smem_u32(&sh->q_full), kSoftThreads / 32);
+        mbar_init(smem_u32(&sh->v_full[0]), 1);
+        mbar_init(smem_u32(&sh->v_full[1]), 1);
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(smem_u32(&sh->s_full[i >> 1][i & 1]), 1);
+            mbar_init(smem_u32(&sh->o_full[i >> 1][i & 1]), 1);
+            mbar_init(smem_u32(&sh->p_full[i >> 1][i & 1]), 4);
+        }
+        sh->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+    }
+    if (warp == 17) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+    const Ctl ctl{p.ws, &sh->abort};
+    griddep_wait();
+    griddep_launch_dependents();
+    if (warp == 16) {
+        const int at = walk_start(p, lane);
+        if (lane == 0) sh->start = at;
+    }
+    __syncthreads();
+    const int start = sh->start;
+    // 640 threads start with 96 registers each; the softmax's sixteen warps go on with 104 and the other four with
+    // 64 (4 x 104 + 64 = 5 x 96)
+    if (warp < 16) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        narrow_softmax<D>(p, ctl, sh, sq, spw, ring_v, tmem, start);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 16) {
+            tc_producer<D, G::kKeys>(p, &mk, ctl, &sh->rk, ring_k, lane, start);
+        } else if (warp == 18) {
+            tc_producer<D, G::kValues>(p, &mv, ctl, &sh->rv, ring_v, lane, start);
+        } else if (warp == 17) {
+            narrow_issue<D>(p, ctl, sh, smem_u32(sq), smem_u32(spw), ring_k, ring_v, tmem, start);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    settle(&sh->abort);
+    if (warp == 17) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_narrow(const AttnParams& p, cudaStream_t st) {
+    return p.D == 64 ? launch_tc(attn_narrow_kernel<64>, kTcThreads, NarrowGeo<64>::kSmem, p, st)
+                     : launch_tc(attn_narrow_kernel<128>, kTcThreads, NarrowGeo<128>::kSmem, p, st);
+}
+
+}  // namespace smcsd
