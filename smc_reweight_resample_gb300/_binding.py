@@ -8,6 +8,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -426,7 +427,7 @@ def smc_step_static(tgt_logits, drf_logits, draft_tokens, G, N, K, V, temperatur
 
 # ----------------------------------------------------------------------------------------------
 # the step around the verify: page tables and slots, cache writes, attention of the drafted tokens,
-# logits. Tensor shapes give the sizes that are not named.
+# logits. Tensor shapes give the sizes that are not named; the marshalling is native (_native).
 # ----------------------------------------------------------------------------------------------
 
 class TreeAttentionWorkspace(Workspace):
@@ -437,46 +438,29 @@ class TreeAttentionWorkspace(Workspace):
         self._allocate(n, device)
 
 
-def _dev_ptr(t, dtype):
-    """Address of a contiguous CUDA tensor of one type, or None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise TypeError(f"tensor must be {dtype}, not {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError("tensor must be on the CUDA device")
-    if not t.is_contiguous():
-        raise ValueError("tensor must be contiguous")
-    return t.data_ptr()
+_calls = None
 
 
-def _stream_ptr(stream, t):
-    """Handle of the given stream, or of the current one of t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+def _native():
+    """The call module (csrc/py_calls.cpp), loaded and given the library's entry points on first use."""
+    global _calls
+    if _calls is None:
+        lib = load()
+        path = os.path.join(_HERE, "_calls.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"call module not built: {path} is missing "
+                               "(run smc_reweight_resample_gb300.build.build())")
+        spec = importlib.util.spec_from_file_location("smc_reweight_resample_gb300._calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
+                      ("kv_slot_map", "kv_append", "tree_mask", "tree_attention", "logits_process")), _check)
+        _calls = module
+    return _calls
 
 
-def _token_rows(t, like=None):
-    """Address and token stride of a [R, heads, D] tensor whose rows are contiguous."""
-    if t.dim() != 3 or not t.is_cuda:
-        raise ValueError("tensor must be [rows, heads, D] on the CUDA device")
-    if t.stride(2) != 1 or t.stride(1) != t.shape[2]:
-        raise ValueError("the heads of a row must be contiguous")
-    if like is not None and (t.dtype is not like.dtype or t.shape != like.shape or t.stride(0) != like.stride(0)):
-        raise ValueError("keys and values must be alike")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2])
-
-
-def _cache_shape(k_cache, v_cache, like):
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
-        raise ValueError("caches must be [num_pages, Hkv, page_size, D], both alike")
-    if k_cache.dtype is not like.dtype or v_cache.dtype is not like.dtype:
-        raise TypeError("caches and rows must have one type")
-    return k_cache.shape
-
-
-def _sized(t, n, what):
-    if t is not None and t.numel() < n:
-        raise ValueError(f"{what} is too small")
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def kv_slot_map(ctx_len, table_in, refcount_in, S, T, page_size, new_offsets=None, rows=None, ws=None,
@@ -485,32 +469,11 @@ def kv_slot_map(ctx_len, table_in, refcount_in, S, T, page_size, new_offsets=Non
     """Page tables, slots and copies of the step's new tokens. table_in int32 [S, pages_per_seq],
     refcount_in int32 [num_pages]; T new tokens for each sequence, or given by new_offsets (int32 [S+1],
     `rows` tokens in all). Returns dict(table_out, refcount_out, slots, copy_src, copy_dst)."""
-    dev = table_in.device
-    R = S * T if rows is None else int(rows)
-    if new_offsets is not None and rows is None:
-        raise ValueError("ragged tokens need rows")
-    if table_in.dim() != 2 or table_in.shape[0] != S:
-        raise ValueError("table_in must be [S, pages_per_seq]")
-    num_pages = refcount_in.numel()
-    _sized(ctx_len, S, "ctx_len")
-    _sized(new_offsets, S + 1, "new_offsets")
-    ws = ws or Workspace(OP_KV_SLOT_MAP, S, 0, num_pages, dev)
-    table_out = _out(table_out, table_in.shape, torch.int32, dev)
-    refcount_out = _out(refcount_out, (num_pages,), torch.int32, dev)
-    slots = _out(slots, (R,), torch.int64, dev)
-    copy_src = _out(copy_src, (S,), torch.int32, dev)
-    copy_dst = _out(copy_dst, (S,), torch.int32, dev)
-    for t, n in ((table_out, table_in.numel()), (refcount_out, num_pages), (slots, R), (copy_src, S), (copy_dst, S)):
-        _sized(t, n, "an output")
-    i32 = torch.int32
-    rc = load().kv_slot_map(_dev_ptr(ctx_len, i32), _dev_ptr(new_offsets, i32), S, T, R,
-                            _dev_ptr(table_in, i32), _dev_ptr(table_out, i32), table_in.shape[1],
-                            page_size, _dev_ptr(refcount_in, i32), _dev_ptr(refcount_out, i32),
-                            num_pages, _dev_ptr(slots, torch.int64), _dev_ptr(copy_src, i32),
-                            _dev_ptr(copy_dst, i32), ws.ptr, ws.nbytes, _stream_ptr(stream, table_in))
-    _check(rc, "kv_slot_map")
-    return dict(table_out=table_out, refcount_out=refcount_out, slots=slots, copy_src=copy_src,
-                copy_dst=copy_dst)
+    ws = ws or Workspace(OP_KV_SLOT_MAP, S, 0, refcount_in.numel(), table_in.device)
+    o = (_calls or _native()).kv_slot_map(ctx_len, table_in, refcount_in, S, T, page_size, new_offsets, rows,
+                                          table_out, refcount_out, slots, copy_src, copy_dst, ws.ptr,
+                                          ws.nbytes, _handle(stream))
+    return {"table_out": o[0], "refcount_out": o[1], "slots": o[2], "copy_src": o[3], "copy_dst": o[4]}
 
 
 def kv_append(k_new, v_new, slots, k_cache, v_cache, ctx_len=None, copy_src=None, copy_dst=None, ws=None,
@@ -518,39 +481,16 @@ def kv_append(k_new, v_new, slots, k_cache, v_cache, ctx_len=None, copy_src=None
     """Writes k_new, v_new [R, Hkv, D] (rows may be strided) to their slots (int64 [R]) of the caches
     [num_pages, Hkv, page_size, D], and the page copies that kv_slot_map asked for. Returns the caches,
     which are changed in place."""
-    num_pages, Hkv, page_size, D = _cache_shape(k_cache, v_cache, k_new)
-    kp, stride = _token_rows(k_new)
-    vp, _ = _token_rows(v_new, k_new)
-    R = k_new.shape[0]
-    if k_new.shape[1:] != (Hkv, D):
-        raise ValueError("rows and caches must have the same heads")
-    _sized(slots, R, "slots")
-    S = 0 if copy_src is None else copy_src.numel()
-    for t in (copy_dst, ctx_len):
-        _sized(t, S, "copy_dst and ctx_len")
     ws = ws or Workspace(OP_KV_APPEND, 1, device=k_cache.device)
-    i32 = torch.int32
-    rc = load().kv_append(kp, vp, _dtype_code(k_new), R, Hkv, D, stride, _dev_ptr(slots, torch.int64),
-                          _dev_ptr(copy_src, i32), _dev_ptr(copy_dst, i32),
-                          _dev_ptr(ctx_len, i32) if S else None, S, _dev_ptr(k_cache, k_new.dtype),
-                          _dev_ptr(v_cache, k_new.dtype), page_size, num_pages, ws.ptr, ws.nbytes,
-                          _stream_ptr(stream, k_cache))
-    _check(rc, "kv_append")
+    (_calls or _native()).kv_append(k_new, v_new, slots, k_cache, v_cache, ctx_len, copy_src, copy_dst, ws.ptr,
+                                    ws.nbytes, _handle(stream))
     return k_cache, v_cache
 
 
 def tree_mask(parents, S, T, node_offsets=None, mask=None, ws=None, stream=None):
     """Node mask int32 [R, ceil(T/32)] (bits) of the trees that parents (int32 [R]) describes."""
-    R = parents.numel()
-    _sized(node_offsets, S + 1, "node_offsets")
-    mask = _out(mask, (R, (T + 31) // 32), torch.int32, parents.device)
-    _sized(mask, R * ((T + 31) // 32), "mask")
     ws = ws or Workspace(OP_TREE_MASK, 1, device=parents.device)
-    i32 = torch.int32
-    rc = load().tree_mask(_dev_ptr(parents, i32), _dev_ptr(node_offsets, i32), S, T, R,
-                          _dev_ptr(mask, i32), ws.ptr, ws.nbytes, _stream_ptr(stream, parents))
-    _check(rc, "tree_mask")
-    return mask
+    return (_calls or _native()).tree_mask(parents, S, T, node_offsets, mask, ws.ptr, ws.nbytes, _handle(stream))
 
 
 def tree_attention(q, k_cache, v_cache, table, ctx_len, S, T, scale, N=1, node_offsets=None, mask=None,
@@ -559,31 +499,9 @@ def tree_attention(q, k_cache, v_cache, table, ctx_len, S, T, scale, N=1, node_o
     sequences with tables int32 [S, pages_per_seq] and ctx_len cached tokens, and over the nodes that
     each row sees (mask int32 [R, ceil(T/32)]; None: a chain). Returns (out [R, Hq, D], lse float
     [R, Hq], or None without it)."""
-    num_pages, Hkv, page_size, D = _cache_shape(k_cache, v_cache, q)
-    qp, stride = _token_rows(q)
-    R, Hq = q.shape[0], q.shape[1]
-    dev = q.device
-    if q.shape[2] != D:
-        raise ValueError("rows and caches must have the same head size")
-    if table.dim() != 2 or table.shape[0] != S:
-        raise ValueError("table must be [S, pages_per_seq]")
-    _sized(ctx_len, S, "ctx_len")
-    _sized(node_offsets, S + 1, "node_offsets")
-    _sized(mask, R * ((T + 31) // 32), "mask")
-    ws = ws or TreeAttentionWorkspace(S, N, T, Hq, Hkv, D, dev)
-    out = _out(out, (R, Hq, D), q.dtype, dev)
-    if lse is None and with_lse:
-        lse = torch.empty((R, Hq), dtype=torch.float32, device=dev)
-    _sized(out, R * Hq * D, "out")
-    _sized(lse, R * Hq, "lse")
-    i32, dt = torch.int32, q.dtype
-    rc = load().tree_attention(qp, stride, _dev_ptr(k_cache, dt), _dev_ptr(v_cache, dt), _dtype_code(q),
-                               num_pages, page_size, _dev_ptr(table, i32), table.shape[1],
-                               _dev_ptr(ctx_len, i32), _dev_ptr(node_offsets, i32), S, N, T, R,
-                               _dev_ptr(mask, i32), Hq, Hkv, D, float(scale), _dev_ptr(out, dt),
-                               _dev_ptr(lse, torch.float32), ws.ptr, ws.nbytes, _stream_ptr(stream, q))
-    _check(rc, "tree_attention")
-    return out, lse
+    ws = ws or TreeAttentionWorkspace(S, N, T, q.shape[1], k_cache.shape[1], q.shape[2], q.device)
+    return (_calls or _native()).tree_attention(q, k_cache, v_cache, table, ctx_len, S, T, scale, N, node_offsets,
+                                                mask, out, lse, with_lse, ws.ptr, ws.nbytes, _handle(stream))
 
 
 def logits_process(logits, S, T, V, node_offsets=None, node_tokens=None, mask=None, hist_tokens=None,
@@ -591,28 +509,8 @@ def logits_process(logits, S, T, V, node_offsets=None, node_tokens=None, mask=No
                    bias_values=None, bias_offsets=None, allowed=None, out=None, ws=None, stream=None):
     """Penalties, biases and a grammar mask (bits, int32 [R, ceil(V/32)]) on logits [R, V]; pass
     out=logits to change them in place. Returns out."""
-    R = logits.numel() // V
-    _sized(node_offsets, S + 1, "node_offsets")
-    _sized(node_tokens, R, "node_tokens")
-    _sized(mask, R * ((T + 31) // 32), "mask")
-    _sized(hist_offsets, S + 1, "hist_offsets")
-    _sized(bias_offsets, S + 1, "bias_offsets")
-    _sized(allowed, R * ((V + 31) // 32), "allowed")
-    for t in (repetition, presence, frequency):
-        _sized(t, S, "a penalty")
-    out = _out(out, (R, V), logits.dtype, logits.device)
-    _sized(out, R * V, "out")
     ws = ws or Workspace(OP_LOGITS_PROCESS, 1, device=logits.device)
-    i32, f32 = torch.int32, torch.float32
-    rc = load().logits_process(_dev_ptr(logits, logits.dtype), _dev_ptr(out, logits.dtype),
-                               _dtype_code(logits), R, V, S, T, _dev_ptr(node_offsets, i32),
-                               _dev_ptr(node_tokens, i32), _dev_ptr(mask, i32),
-                               _dev_ptr(hist_tokens, i32), _dev_ptr(hist_offsets, i32),
-                               0 if hist_tokens is None else hist_tokens.numel(),
-                               _dev_ptr(repetition, f32), _dev_ptr(presence, f32),
-                               _dev_ptr(frequency, f32), _dev_ptr(bias_tokens, i32),
-                               _dev_ptr(bias_values, f32), _dev_ptr(bias_offsets, i32),
-                               0 if bias_tokens is None else min(bias_tokens.numel(), bias_values.numel()),
-                               _dev_ptr(allowed, i32), ws.ptr, ws.nbytes, _stream_ptr(stream, logits))
-    _check(rc, "logits_process")
-    return out
+    return (_calls or _native()).logits_process(logits, S, T, V, node_offsets, node_tokens, mask, hist_tokens,
+                                                hist_offsets, repetition, presence, frequency, bias_tokens,
+                                                bias_values, bias_offsets, allowed, out, ws.ptr, ws.nbytes,
+                                                _handle(stream))

@@ -1,7 +1,8 @@
 """Build the CUDA library ``libsmcsd.so`` in-tree for sm_103a (GB300).
 
 Each translation unit is compiled in its own nvcc process, in parallel, then linked into one
-shared library with the CUDA runtime linked statically. Objects go to ``_build/`` beside this
+shared library with the CUDA runtime linked statically; the host-only call module ``_calls.so`` is
+compiled beside them. Objects go to ``_build/`` beside this
 file; the library is written next to this file. Run ``python -m smc_reweight_resample_gb300.build``
 or call ``build()``.
 """
@@ -25,6 +26,10 @@ SOURCES = ["api.cu", "verify_stream.cu", "stream_tma.cu", "finish.cu", "sd_sampl
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
+# CPython module that marshals tensors for the calls around the verify (csrc/py_calls.cpp): host code only
+CALLS = os.path.join(HERE, "_calls.so")
+
+
 def nvcc() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -41,7 +46,7 @@ def _stale(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "smcsd.h")]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")] + [os.path.join(INCLUDE, "smcsd.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -57,9 +62,44 @@ def build_checks(force: bool = False, verbose: bool = False) -> str:
                  objdir=CHECKS_BUILD)
 
 
+def _calls_command(out: str):
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[x for d in inc for x in ("-I", d)],
+            os.path.join(CSRC, "py_calls.cpp"), "-o", out, "-L", os.path.join(root, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def _start_calls():
+    """The module's compiler, running (None if the module is up to date), and its output."""
+    deps = [os.path.join(CSRC, "py_calls.cpp"), os.path.join(INCLUDE, "smcsd.h")]
+    if os.path.exists(CALLS) and all(os.path.getmtime(d) <= os.path.getmtime(CALLS) for d in deps):
+        return None, None
+    tmp = CALLS + f".tmp{os.getpid()}"
+    return subprocess.Popen(_calls_command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp
+
+
+def _finish_calls(proc, tmp):
+    if proc is None:
+        return
+    log, _ = proc.communicate()
+    if proc.returncode != 0:
+        sys.stdout.write(log.decode(errors="replace"))
+        raise RuntimeError("the compiler failed for py_calls.cpp")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str = LIB,
           objdir: str = BUILD) -> str:
+    calls = _start_calls()
     if not force and not _stale(out):
+        _finish_calls(*calls)
         return out
     os.makedirs(objdir, exist_ok=True)
     cc = nvcc()
@@ -84,6 +124,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str =
     tmp = out + f".tmp{os.getpid()}"
     subprocess.check_call([cc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, out)
+    _finish_calls(*calls)
     return out
 
 

@@ -101,3 +101,33 @@ def test_logits_process(lib):
     refused(call, -1, logits=[None], out=[None], R=[0, 7], V=[0], S=[0], T=[0, 3], tokens=[None], ht=[None], ho=[None], nh=[-1],
             bt=[None], bv=[None], bo=[None], nb=[-1], ws=[None])
     assert call(S=70000, R=140000) == -1
+
+
+def test_the_python_calls_refuse_wrong_tensors():
+    import torch
+
+    from smc_reweight_resample_gb300 import _binding as B
+
+    class Ws:
+        ptr, nbytes = 4096, 1 << 20
+
+    i32 = torch.zeros(4, dtype=torch.int32)
+    q, cache = torch.zeros(2, 4, 64), torch.zeros(3, 2, 16, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.tree_mask(i32, 1, 4, ws=Ws)
+    with pytest.raises(TypeError):
+        B._native().tree_mask("parents", 1, 4, None, None, 1, 1, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.tree_attention(q, cache, cache, i32.view(1, 4), i32, 1, 2, 1.0, ws=Ws)
+    with pytest.raises(TypeError, match="one type"):
+        B.tree_attention(q, cache, cache.bfloat16(), i32.view(1, 4), i32, 1, 2, 1.0, ws=Ws)
+    with pytest.raises(ValueError, match="alike"):
+        B.tree_attention(q, cache, cache[:2], i32.view(1, 4), i32, 1, 2, 1.0, ws=Ws)
+    with pytest.raises(ValueError, match="pages_per_seq"):
+        B.kv_slot_map(i32, i32, i32, 4, 1, 16, ws=Ws)
+    with pytest.raises(ValueError, match="rows"):
+        B.kv_slot_map(i32, i32.view(1, 4), i32, 1, 1, 16, new_offsets=i32, ws=Ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.logits_process(q, 1, 2, 128, ws=Ws)
+    with pytest.raises(ValueError, match="node_tokens"):
+        B.logits_process(torch.zeros(8, 10), 8, 1, 10, node_tokens=i32, ws=Ws)
