@@ -186,3 +186,20 @@ def test_errors_on_the_device(smcsd):
     assert status(bias_tokens=i32(1, 100), bias_values=val, bias_offsets=i32(0, 1, 2)) == smcsd.ERR_RANGE
     assert status(bias_tokens=i32(1, 2), bias_values=val, bias_offsets=i32(0, 1, 3)) == smcsd.ERR_RANGE
     assert status(node_tokens=i32(1, 2)) == 0
+
+
+def test_long_bias_lists(smcsd):
+    # more entries than a block has threads, tokens several times over: the last entry of each counts
+    rng = np.random.default_rng(2)
+    V, S = 5000, 2
+    z = torch.from_numpy(rng.normal(0, 3, (S, V)).astype(np.float32)).cuda()
+    tok = rng.integers(0, V, (S, 3000)).astype(np.int32)
+    tok[:, -1] = tok[:, 0]
+    val = rng.normal(0, 2, (S, 3000)).astype(np.float32)
+    want = host(z).astype(np.float64)
+    for s in range(S):
+        for t, v in {int(t): float(v) for t, v in zip(tok[s], val[s])}.items():
+            want[s, t] += v
+    out = smcsd.logits_process(z, S, 1, V, bias_tokens=dev(tok.reshape(-1)), bias_values=dev(val.reshape(-1)),
+                               bias_offsets=dev(np.array([0, 3000, 6000], np.int32)))
+    within(host(out).astype(np.float64), want, 2.0 ** -24 * (np.abs(want) + 16), np.ones_like(want, bool), "f32")
