@@ -13,7 +13,6 @@ namespace smcsd {
 namespace {
 
 constexpr int kTile = 128;        // keys of a tile
-constexpr int kHalf = 128 * 128;  // bytes of 128 rows of 64 bf16
 
 // ---- instructions ----
 
@@ -50,10 +49,10 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int group, int page, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(group), "r"(page), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -112,11 +111,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
-// Shared-memory operand of a product: 128-byte swizzle. Rows along the sum's dimension (K-major): groups of
-// 8 rows 1024 bytes apart. Rows along the output's dimension (the values: a key's 64 columns in a row):
-// groups of 8 keys 1024 bytes apart, blocks of 64 columns kHalf apart.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t block = kHalf) {
-    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+// Tiles in shared memory: 128-byte swizzle, blocks of 8 rows x 64 columns (1 KB) with a row's D / 64 blocks side by
+// side: [row / 8][column / 64][row % 8][column % 64]. One copy brings a page in this order.
+template <int D>
+struct TileGeo {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kGroup = kHalves * 1024;  // bytes of 8 rows
+    static constexpr int kBytes = 16 * kGroup;     // of 128 rows
+    // row r, 16-byte chunk ch (of D / 8) of a row
+    static __host__ __device__ constexpr int at(int r, int ch) {
+        return (r >> 3) * kGroup + (ch >> 3) * 1024 + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+    }
+    // 16 columns of the sum's dimension (rows along the sum): step k
+    static __host__ __device__ constexpr int step(int k) { return (k >> 2) * 1024 + (k & 3) * 32; }
+};
+
+// Shared-memory operand of a product. `next8` bytes from one group of 8 rows to the next; where the rows lie along the
+// sum (values: a key's columns in a row), `block` bytes from one block of 64 columns to the next.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t next8, uint32_t block) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(next8 >> 4) << 32) | (1ull << 46) |
            (2ull << 61);
 }
 // Instruction: float32 sums, bf16 operands, 128 x n outputs; amn / bmn: that operand's rows lie along the output
@@ -230,69 +243,75 @@ struct Ring {
     }
 };
 
-// One warp for the keys and one for the values: the pages of every tile into its ring of D / 64 * kHalf bytes a
-// stage. A lane holds one page id (a box: up to 128 positions of one page); 32 ids are read at a time, the next 32
-// while these are used. The copies are issued by one thread with the id handed round: lanes issuing a copy each
-// take turns anyway, at four times the cost. Pages past the end are not read.
+// Fills a ring with the pages of a run of tiles (one warp; one for the keys and one for the values). A lane holds one
+// page id (a box: up to 128 positions of one page); 32 ids are read at a time, the next 32 while these are used. The
+// copies are issued by one thread with the ids handed round four at a time: lanes issuing a copy each take turns
+// anyway, at four times the cost. Pages past the end are not read.
 template <int D, int kStages>
-__device__ void tc_producer(const AttnParams& p, const CUtensorMap* map, const Ctl& ctl, Ring<kStages>* rg, uint32_t ring, int lane,
-                            int start) {
-    constexpr int kHalves = D / 64, kStage = kHalves * kHalf;
-    const int box = p.page_size < kTile ? p.page_size : kTile;  // rows of one copy
-    const int box_shift = p.page_shift < 7 ? p.page_shift : 7, nbox = kTile >> box_shift;
-    Walk w = walk_begin(p, start);
-    AttnPiece c;
-    uint32_t st = 0, round = 0;
-    while (walk_next(p, w, c)) {
-        const int keys = c.own ? __ldg(p.ctx_len + c.seq) + w.it.nodes : INT_MAX;
-        const int32_t* row = p.table + (long long)c.seq * p.pages_per_seq;
-        const int last = min((long long)c.t1 * kTile, (long long)keys);  // end of the piece's positions
+struct Filler {
+    using T = TileGeo<D>;
+    const CUtensorMap* map;
+    Ring<kStages>* rg;
+    uint32_t ring, st, round;
+    __device__ __forceinline__ Filler(const CUtensorMap* m, Ring<kStages>* r, uint32_t addr) : map(m), rg(r), ring(addr), st(0), round(0) {}
+    // tiles t0 .. t1 - 1 of one head of a sequence with `keys` positions; false after a wait that ran out
+    __device__ __forceinline__ bool fill(const AttnParams& p, const Ctl& ctl, int seq, int hkv, int t0, int t1, int keys, int lane) {
+        const int box_shift = p.page_shift < 7 ? p.page_shift : 7, box = 1 << box_shift, nbox = kTile >> box_shift;
+        const int32_t* row = p.table + (long long)seq * p.pages_per_seq;
+        const int last = (int)min((long long)t1 * kTile, (long long)keys);  // end of the positions
         auto ids = [&](int batch) {  // of the 32 boxes from 32 * batch on
-            const int pos = c.t0 * kTile + ((32 * batch + lane) << box_shift);
-            return pos < last ? __ldg(row + (pos >> p.page_shift)) : 0;
+            const int pos = t0 * kTile + ((32 * batch + lane) << box_shift);
+            int id = pos < last ? __ldg(row + (pos >> p.page_shift)) : 0;
+            if (id < 0 || id >= p.num_pages) {
+                raise_error(p.ws, kErrRange);
+                id = 0;
+            }
+            return id;
         };
+        const int bytes = box * D * 2;
         int id = ids(0), next = ids(1), batch = 1;
 #pragma unroll 1
-        for (int t = c.t0, x = 0; t < c.t1; ++t, x += nbox) {
+        for (int t = t0, x = 0; t < t1; ++t, x += nbox) {
             if (x == 32) {
                 x = 0;
                 id = next;
                 next = ids(++batch);
             }
-            const int boxes = min(nbox, (last - t * kTile + box - 1) >> box_shift);
             if (round > 0) wait(ctl, smem_u32(&rg->empty[st]), (round - 1) & 1);
-            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(ctl.abort))) return;
-            if (id < 0 || id >= p.num_pages) {
-                raise_error(p.ws, kErrRange);
-                id = 0;
-            }
-            const int ust = uniform(st), uboxes = uniform(boxes);
+            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(ctl.abort))) return false;
+            const int ust = uniform(st), boxes = uniform(min(nbox, (last - t * kTile + box - 1) >> box_shift));
             const uint32_t bar = smem_u32(&rg->full[ust]);
-            uint32_t to = ring + ust * kStage;
-            const int at = uniform(c.hkv * p.page_size + ((t * kTile) & (p.page_size - 1)));
-            if (elect_one()) mbar_expect_tx(bar, (uint32_t)(uboxes * box * 128 * kHalves));
+            uint32_t to = ring + ust * T::kBytes;
+            const int at = uniform((hkv * p.page_size + ((t * kTile) & (p.page_size - 1))) >> 3);
+            if (elect_one()) mbar_expect_tx(bar, (uint32_t)(boxes * bytes));
             __syncwarp();
-            for (int b = 0; b < uboxes; ++b, to += box * 128) {
-                const int page = uniform(__shfl_sync(0xffffffffu, id, x + b));
+#pragma unroll 1
+            for (int b = 0; b < boxes; b += 4, to += 4 * bytes) {
+                int page[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) page[y] = __shfl_sync(0xffffffffu, id, (x + b + y) & 31);
                 if (elect_one()) {
 #pragma unroll
-                    for (int h = 0; h < kHalves; ++h) tma_tile(to + h * kHalf, map, h * 64, at, page, bar);
+                    for (int y = 0; y < 4; ++y)
+                        if (b + y < boxes) tma_page(to + y * bytes, map, at, page[y], bar);
                 }
             }
             if (++st == kStages) st = 0, ++round;
         }
+        return true;
     }
-}
+};
 
 // ---- masks ----
 
-// Zeroes what the product with V must not meet in one key's row of one half: everything past the end,
-// NaN and infinities in nodes (rows of zero weight would turn them into NaN). True if there were some.
-__device__ __forceinline__ bool clean_row(uint32_t half, int k, bool past) {
+// Zeroes what the product with V must not meet in `count` blocks of 64 columns of one key's row, from the block at
+// `addr` on: everything past the end, NaN and infinities in nodes (rows of zero weight would turn them into NaN). True
+// if there were some.
+__device__ __forceinline__ bool clean_row(uint32_t addr, int count, bool past) {
     bool found = false;
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t at = half + k * 128 + i * 16;
+    for (int i = 0; i < 8 * count; ++i) {
+        const uint32_t at = addr + (i >> 3) * 1024 + (i & 7) * 16;
         uint32_t v[4];
         if (past) {
             v[0] = v[1] = v[2] = v[3] = 0;
@@ -348,14 +367,17 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// A cache as [num_pages][Hkv * page_size][D], in boxes of 64 columns and up to 128 positions of one head.
+// A cache as [num_pages][Hkv * page_size / 8][8][D / 64][64], taken with the blocks of 64 columns outside the 8 rows: a
+// box is one page of one head (or 128 positions of it) in the order of TileGeo.
 bool encode_cache(CUtensorMap* m, const void* base, const AttnParams& p) {
     EncodeFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dim[3] = {(cuuint64_t)p.D, (cuuint64_t)p.Hkv * p.page_size, (cuuint64_t)p.num_pages};
-    const cuuint64_t stride[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.D * 2 * p.Hkv * p.page_size};
-    const cuuint32_t box[3] = {64, (cuuint32_t)(p.page_size < kTile ? p.page_size : kTile), 1}, one[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint64_t row = (cuuint64_t)p.D * 2, halves = (cuuint64_t)p.D / 64;
+    const cuuint64_t dim[5] = {64, 8, halves, (cuuint64_t)p.Hkv * p.page_size / 8, (cuuint64_t)p.num_pages};
+    const cuuint64_t stride[4] = {row, 128, 8 * row, row * p.Hkv * p.page_size};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)halves, (cuuint32_t)(p.page_size < kTile ? p.page_size : kTile) / 8, 1},
+                     one[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

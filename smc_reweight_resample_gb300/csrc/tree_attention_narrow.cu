@@ -10,10 +10,12 @@
 //               memory. With up to 32 rows the groups take four tiles at a time, with up to 64 two tiles in
 //               two halves of the rows, above one tile in quarters: group w always has columns 32 w .. 32 w + 31
 //               of the 128 that scores, weights and outputs have.
-//   warps 16 and 18  bring pages of keys and of values into their rings (attn_tc.cuh)
-//   warp 17     issues the products; scores and weights have two buffers, and the scores of the next round of
-//               tiles but one are issued before the weights of this one are there
-//   (warp 19 idle: registers are handed over by fours)
+//   warp 16     walks along the block's share, hands the pieces round in shared memory, brings their query rows (two
+//               places of 64 rows, or one of 128) and the pages of keys (attn_tc.cuh)
+//   warp 18     brings the pages of values
+//   warps 17 and 19  issue S^T and O^T: one warp for both has more to issue than a tile's bytes take. Scores and weights
+//               have two buffers, so the scores of the next round of tiles are there when a group comes to them, and
+//               those of the next piece while this one is written out
 //
 // Softmax. Per column: a reference m common to the keys of the group's tiles, P = exp2(z - m) with
 // z = scale2 q.k, l the sum of P before it is rounded (each thread adds up its own keys; they meet at the end of
@@ -32,24 +34,76 @@ constexpr float kNone = -3.402823466e38f;  // reference of a column that has see
 
 template <int D>
 struct NarrowGeo {
-    static constexpr int kHalves = D / 64;
-    static constexpr int kStage = kHalves * kHalf;
+    static constexpr int kStage = TileGeo<D>::kBytes;
     static constexpr int kKeys = D == 128 ? 2 : 4, kValues = D == 128 ? 2 : 5;  // stages
-    static constexpr int kWeights = 2 * kHalf;  // one buffer of P: 128 columns x 128 keys
+    static constexpr int kBlock = 128 * 128;     // 128 keys x 64 columns of P
+    static constexpr int kWeights = 2 * kBlock;  // one buffer of P: 128 columns x 128 keys
+    static constexpr int kSlot = 8 * TileGeo<D>::kGroup;  // 64 query rows
     static constexpr int kSmem = 1024 + kStage + 2 * kWeights + (kKeys + kValues) * kStage;
 };
+
+// A piece (attn_plan.cuh) as it is handed round.
+struct PieceInfo {
+    float* o;
+    float2* ml;
+    int node0, seq, hkv, row0;
+    int rows;  // 0: there are no more
+    int t0, n; // key tiles
+    int ctx;   // tokens in the cache; INT_MAX for keys that a group shares
+    int nodes;
+    bool whole;
+    __device__ __forceinline__ int keys() const { return ctx == INT_MAX ? INT_MAX : ctx + nodes; }
+    // first tile with a node or the end (n or more: none)
+    __device__ __forceinline__ int first_tail() const { return ctx == INT_MAX ? n : (ctx >> 7) - t0; }
+};
+constexpr int kPieces = 4;
 
 template <int D>
 struct __align__(16) NarrowShared {
     __align__(16) float m[kTile];  // references, read four at a time
+    __align__(16) PieceInfo piece[kPieces];
     Ring<NarrowGeo<D>::kKeys> rk;
     Ring<NarrowGeo<D>::kValues> rv;
-    uint64_t q_full, v_full[2];
+    uint64_t piece_full[kPieces];
+    uint64_t q_full[2], q_empty[2], v_full[2];
     uint64_t s_full[4][2], o_full[4][2];  // [tile of a round][buffer]
     uint64_t p_full[4][2];                // [group][buffer]
     uint32_t tmem;
-    int abort, start;
-    int poison;  // a NaN or infinity among the values of the piece's nodes
+    int abort;
+    int poison[2];  // by the piece's parity: a NaN or infinity among the values of its nodes
+};
+
+// The i-th piece, as all warps but the one that walks see it (no rows after a wait that ran out).
+template <int D>
+__device__ __forceinline__ PieceInfo next_piece(const Ctl& ctl, NarrowShared<D>* sh, uint32_t i) {
+    wait(ctl, smem_u32(&sh->piece_full[i % kPieces]), (i / kPieces) & 1);
+    PieceInfo c = sh->piece[i % kPieces];
+    if (*reinterpret_cast<volatile int*>(ctl.abort)) c.rows = 0;
+    c.rows = uniform(c.rows);
+    c.n = uniform(c.n);
+    return c;
+}
+
+// Places of the query rows: a piece of up to 64 rows takes the next of the two, a larger one both.
+struct QuerySlots {
+    uint32_t uses[2] = {0, 0};
+    int next = 0;
+    int slot;
+    bool both;
+    __device__ __forceinline__ void take(int rows) {
+        both = rows > 64;
+        slot = both ? 0 : next;
+        next = both ? 0 : next ^ 1;
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(F f) {  // f(place, how often it was taken before)
+        if (both || slot == 0) f(0, uses[0]);
+        if (both || slot == 1) f(1, uses[1]);
+    }
+    __device__ __forceinline__ void done() {
+        if (both || slot == 0) ++uses[0];
+        if (both || slot == 1) ++uses[1];
+    }
 };
 
 // How a unit's rows and tiles are laid over the four groups.
@@ -81,77 +135,181 @@ struct Uses {
     }
 };
 
-// ---- products ----
+// ---- pieces, query rows and keys ----
 
 template <int D>
-__device__ void narrow_issue(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, uint32_t sq, uint32_t sp, uint32_t ring_k, uint32_t ring_v,
-                             uint32_t tmem, int start) {
+__device__ void narrow_walk(const AttnParams& p, const CUtensorMap* mk, const Ctl& ctl, NarrowShared<D>* sh, uint32_t sq, uint32_t ring_k,
+                            int lane) {
     using G = NarrowGeo<D>;
-    Walk w = walk_begin(p, start);
+    Walk w = walk_begin(p, walk_start(p, lane));
     AttnPiece c;
-    uint32_t f0 = 0, pieces = 0, tails = 0;
-    uint32_t p_uses = 0;  // parity of the next use of p_full[group][buffer], bit 2 * group + buffer
-    while (walk_next(p, w, c)) {
-        const int n = uniform(c.t1 - c.t0);
-        const Split split(uniform(c.rows));
+    QuerySlots qs;
+    Filler<D, G::kKeys> keys(mk, &sh->rk, ring_k);
+    for (uint32_t i = 0;; ++i) {
+        const bool more = walk_next(p, w, c);
+        if (!more) c.rows = 0;
+        qs.take(c.rows);
+        // Once the scores that read this place last are done, everybody is past piece i - 4 (the scores of a piece wait
+        // for all weights of the one before), and its description may be written over.
+        qs.each([&](int x, uint32_t uses) {
+            if (uses > 0) wait(ctl, smem_u32(&sh->q_empty[x]), (uses - 1) & 1);
+        });
+        const int ctx = more && c.own ? __ldg(p.ctx_len + c.seq) : INT_MAX;
+        if (lane == 0) {
+            PieceInfo* to = &sh->piece[i % kPieces];
+            to->o = c.o;
+            to->ml = c.ml;
+            to->node0 = c.node0;
+            to->seq = c.seq;
+            to->hkv = c.hkv;
+            to->row0 = c.row0;
+            to->rows = c.rows;
+            to->t0 = c.t0;
+            to->n = c.t1 - c.t0;
+            to->ctx = ctx;
+            to->nodes = w.it.nodes;
+            to->whole = c.whole;
+            mbar_arrive(smem_u32(&sh->piece_full[i % kPieces]));
+        }
+        __syncwarp();
+        if (!more) {
+            // the last scores' reports land before the block ends
+            for (int x = 0; x < 2; ++x)
+                if (qs.uses[x] > 0) wait(ctl, smem_u32(&sh->q_empty[x]), (qs.uses[x] - 1) & 1);
+            return;
+        }
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(ctl.abort))) return;
+        // rows of zeros up to a multiple of 32: scores of zero
+        const int padded = (c.rows + 31) & ~31;
+        const uint32_t to = sq + qs.slot * G::kSlot;
+#pragma unroll 4
+        for (int x = lane; x < padded * (D / 8); x += 32) {
+            const int r = x / (D / 8), ch = x - r * (D / 8);
+            const int row = c.row0 + min(r, c.rows - 1), node = row / p.gq, hq = c.hkv * p.gq + (row - node * p.gq);
+            const void* from = static_cast<const __nv_bfloat16*>(p.q) + (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + ch * 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + TileGeo<D>::at(r, ch)),
+                         "l"(from), "r"(r < c.rows ? 16 : 0)
+                         : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) qs.each([&](int x, uint32_t) { mbar_arrive(smem_u32(&sh->q_full[x])); });
+        __syncwarp();
+        qs.done();
+        if (!keys.fill(p, ctl, c.seq, c.hkv, c.t0, c.t1, c.own ? ctx + w.it.nodes : INT_MAX, lane)) return;
+    }
+}
+
+template <int D>
+__device__ void narrow_values(const AttnParams& p, const CUtensorMap* mv, const Ctl& ctl, NarrowShared<D>* sh, uint32_t ring_v, int lane) {
+    Filler<D, NarrowGeo<D>::kValues> values(mv, &sh->rv, ring_v);
+    for (uint32_t i = 0;; ++i) {
+        const PieceInfo c = next_piece(ctl, sh, i);
+        if (c.rows == 0 || !values.fill(p, ctl, c.seq, c.hkv, c.t0, c.t0 + c.n, c.keys(), lane)) return;
+    }
+}
+
+// ---- products ----
+
+// Parities of the groups' weights, as one issuing warp waits for them: bit 2 * group + buffer.
+struct Weights {
+    uint32_t bits = 0;
+    template <int D>
+    __device__ __forceinline__ void wait_for(const Ctl& ctl, NarrowShared<D>* sh, const Split& split, int t) {
+        const int k = t & (split.tiles() - 1), b = (t >> split.log_tiles) & 1;
+        for (int x = 0; x < split.used; ++x) {
+            const int bit = 2 * ((k << split.log_chunks) + x) + b;
+            wait(ctl, smem_u32(&sh->p_full[0][0]) + 8 * bit, (bits >> bit) & 1);
+            bits ^= 1u << bit;
+        }
+    }
+};
+
+template <int D>
+__device__ void narrow_scores(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, uint32_t sq, uint32_t ring_k, uint32_t tmem) {
+    using G = NarrowGeo<D>;
+    Weights weights;
+    QuerySlots qs;
+    uint32_t st = 0, round = 0;
+    int left = 0;  // tiles of the piece before whose weights are still to be waited for
+    Split before(1);
+    int n_before = 0;
+    for (uint32_t i = 0;; ++i) {
+        const PieceInfo c = next_piece(ctl, sh, i);
+        if (c.rows == 0) return;
+        const Split split(c.rows);
         const int ahead = 2 * split.tiles(), width = 32 * split.chunks();
-        const uint32_t is = instruction(32 * split.used, 0, 0), io = instruction(32 * split.used, 1, 1);
-        const int first_tail = c.own ? (__ldg(p.ctx_len + c.seq) >> 7) - c.t0 : n;
-        auto scores = [&](int t) {
+        qs.take(c.rows);
+        qs.each([&](int x, uint32_t uses) { wait(ctl, smem_u32(&sh->q_full[x]), uses & 1); });
+        for (; left > 0; --left) weights.wait_for(ctl, sh, before, n_before - left);
+        const uint32_t is = instruction(32 * split.used, 0, 0);
+        const uint64_t qb = operand(sq + qs.slot * G::kSlot, TileGeo<D>::kGroup, 0);
+#pragma unroll 1
+        for (int t = 0; t < c.n; ++t) {
             const int k = t & (split.tiles() - 1), b = (t >> split.log_tiles) & 1;
-            const uint32_t f = f0 + t, st = f % G::kKeys;
-            wait(ctl, smem_u32(&sh->rk.full[st]), (f / G::kKeys) & 1);
+            wait(ctl, smem_u32(&sh->rk.full[st]), round & 1);
+            if (t >= ahead) weights.wait_for(ctl, sh, split, t - ahead);  // the buffer's last scores have been read
             tc_fence_after();
-            const uint64_t ka = operand(ring_k + st * G::kStage), qb = operand(sq);
+            const uint64_t ka = operand(ring_k + st * G::kStage, TileGeo<D>::kGroup, 0);
             const uint32_t to = tmem + 128 * b + width * k;
             if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint64_t at = (uint64_t)(((i / 4) * kHalf + (i % 4) * 32) >> 4);
-                    mma_ss(to, ka + at, qb + at, is, i > 0);
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint64_t at = (uint64_t)(TileGeo<D>::step(x) >> 4);
+                    mma_ss(to, ka + at, qb + at, is, x > 0);
                 }
                 tc_commit(smem_u32(&sh->rk.empty[st]));
                 tc_commit(smem_u32(&sh->s_full[k][b]));
             }
             __syncwarp();
-        };
-        wait(ctl, smem_u32(&sh->q_full), pieces & 1);
-        ++pieces;
-#pragma unroll 1
-        for (int u = 0; u < n + ahead; ++u) {
-            const int t = u - ahead;
-            if (t >= 0) {
-                const int k = t & (split.tiles() - 1), r = t >> split.log_tiles, b = r & 1;
-                const uint32_t f = f0 + t, st = f % G::kValues;
-                wait(ctl, smem_u32(&sh->rv.full[st]), (f / G::kValues) & 1);
-                if (t >= first_tail) {
-                    if (elect_one()) mbar_arrive(smem_u32(&sh->v_full[tails & 1]));
-                    ++tails;
-                }
-                for (int x = 0; x < split.used; ++x) {
-                    const int bit = 2 * ((k << split.log_chunks) + x) + b;
-                    wait(ctl, smem_u32(&sh->p_full[0][0]) + 8 * bit, (p_uses >> bit) & 1);
-                    p_uses ^= 1u << bit;
-                }
-                tc_fence_after();
-                // 64 columns of V have no second block: the upper half of the outputs repeats the lower one
-                const uint64_t va = operand(ring_v + st * G::kStage, D == 128 ? kHalf : 0);
-                const uint64_t pb = operand(sp + b * G::kWeights + (width * k / 64) * kHalf + (width * k % 64) * 2);
-                const uint32_t to = tmem + 256 + width * k, more = r > 0;
-                if (elect_one()) {
-#pragma unroll
-                    for (int i = 0; i < kTile / 16; ++i) {
-                        const uint64_t at = (uint64_t)((i * 2048) >> 4);
-                        mma_ss(to, va + at, pb + at, io, i > 0 ? 1u : more);
-                    }
-                    tc_commit(smem_u32(&sh->rv.empty[st]));
-                    tc_commit(smem_u32(&sh->o_full[k][b]));
-                }
-                __syncwarp();
-            }
-            if (u < n) scores(u);
+            if (++st == G::kKeys) st = 0, ++round;
         }
-        f0 += n;
+        if (elect_one()) qs.each([&](int x, uint32_t) { tc_commit(smem_u32(&sh->q_empty[x])); });
+        __syncwarp();
+        qs.done();
+        left = min(c.n, ahead);
+        n_before = c.n;
+        before = split;
+    }
+}
+
+template <int D>
+__device__ void narrow_outputs(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, uint32_t sp, uint32_t ring_v, uint32_t tmem) {
+    using G = NarrowGeo<D>;
+    Weights weights;
+    uint32_t st = 0, round = 0, tails = 0;
+    for (uint32_t i = 0;; ++i) {
+        const PieceInfo c = next_piece(ctl, sh, i);
+        if (c.rows == 0) return;
+        const Split split(c.rows);
+        const int width = 32 * split.chunks(), first_tail = c.first_tail();
+        const uint32_t io = instruction(32 * split.used, 1, 1);
+#pragma unroll 1
+        for (int t = 0; t < c.n; ++t) {
+            const int k = t & (split.tiles() - 1), r = t >> split.log_tiles, b = r & 1;
+            wait(ctl, smem_u32(&sh->rv.full[st]), round & 1);
+            if (t >= first_tail) {
+                if (elect_one()) mbar_arrive(smem_u32(&sh->v_full[tails & 1]));
+                ++tails;
+            }
+            weights.wait_for(ctl, sh, split, t);
+            tc_fence_after();
+            // 64 columns of V have no second block: the upper half of the outputs repeats the lower one
+            const uint64_t va = operand(ring_v + st * G::kStage, TileGeo<D>::kGroup, D == 128 ? 1024 : 0);
+            const uint64_t pb = operand(sp + b * G::kWeights + (width * k / 64) * G::kBlock + (width * k % 64) * 2, 1024, G::kBlock);
+            const uint32_t to = tmem + 256 + width * k, more = r > 0;
+            if (elect_one()) {
+#pragma unroll
+                for (int x = 0; x < kTile / 16; ++x) {
+                    mma_ss(to, va + (uint64_t)((x * 2 * TileGeo<D>::kGroup) >> 4), pb + (uint64_t)((x * 2048) >> 4), io, x > 0 ? 1u : more);
+                }
+                tc_commit(smem_u32(&sh->rv.empty[st]));
+                tc_commit(smem_u32(&sh->o_full[k][b]));
+            }
+            __syncwarp();
+            if (++st == G::kValues) st = 0, ++round;
+        }
     }
 }
 
@@ -192,19 +350,28 @@ __device__ __forceinline__ bool group_any(int g, bool yes) {
                  : "memory");
     return r != 0;
 }
+// Whether any thread of the sixteen warps says yes.
+__device__ __forceinline__ bool soft_any(bool yes) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, 1, %2, q;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)yes), "n"(kSoftThreads)
+                 : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ void group_sync(int g) {
     __syncwarp();
     asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory");
 }
 
 // What the row's nodes with a NaN or infinity in column d of their values add to it.
-__device__ __forceinline__ float poison_of(const AttnParams& p, const AttnPiece& c, int nodes, int node, int ctx, int d) {
-    const int j0 = max(0, c.t0 * kTile - ctx), j1 = min(nodes, c.t1 * kTile - ctx);
+__device__ __forceinline__ float poison_of(const AttnParams& p, const PieceInfo& c, int node, int d) {
+    const int j0 = max(0, c.t0 * kTile - c.ctx), j1 = min(c.nodes, (c.t0 + c.n) * kTile - c.ctx);
     float sum = 0.0f;
 #pragma unroll 1
     for (int j = j0; j < j1; ++j) {
         if (!attn_sees(p, (long long)c.node0 + node, node, j)) continue;
-        const int pos = ctx + j;
+        const int pos = c.ctx + j;
         const size_t page = attn_page(p, c.seq, pos >> p.page_shift);
         const uint32_t b = __ldg(static_cast<const uint16_t*>(p.v_cache) +
                                  ((page * p.Hkv + c.hkv) * p.page_size + (pos & (p.page_size - 1))) * p.D + d);
@@ -214,48 +381,30 @@ __device__ __forceinline__ float poison_of(const AttnParams& p, const AttnPiece&
 }
 
 template <int D>
-__device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, unsigned char* sq, unsigned char* spw,
-                               uint32_t ring_v, uint32_t tmem, int start) {
+__device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, unsigned char* spw, uint32_t ring_v,
+                               uint32_t tmem) {
     using G = NarrowGeo<D>;
     const int tid = threadIdx.x, lane = tid & 31, g = tid >> 7, key = tid & 127, quad = (tid >> 5) & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;  // a negative scale goes into q
-    const float scale = fabsf(p.scale2) > 0.0f ? fabsf(p.scale2) : 1e-30f;  // 0: equal weights, and -inf stays -inf
+    const float scale = p.scale2 != 0.0f ? p.scale2 : 1e-30f;  // 0: equal weights, and what is not seen stays so
     float* my_m = &sh->m[32 * g];
     // This group's 32 columns of the weights' buffer b: 64 bytes of each key's 128-byte line, swizzled. Sixteen
     // places of the first eight keys' also carry 4 x 32 floats (one of each warp and column) between products.
     auto place = [&](int group, int b, int wq) {
         const int x = 8 * wq + (lane >> 2), k = x >> 2;
-        return reinterpret_cast<float*>(spw + b * G::kWeights + (group >> 1) * kHalf + k * 128 +
+        return reinterpret_cast<float*>(spw + b * G::kWeights + (group >> 1) * G::kBlock + k * 128 +
                                         ((((group & 1) * 4 + (x & 3)) ^ (k & 7)) << 4)) + (lane & 3);
     };
-    Walk w = walk_begin(p, start);
-    AttnPiece c;
     Uses uses{};
     uint32_t f0 = 0, tails = 0;
-    while (walk_next(p, w, c)) {
-        const int n = c.t1 - c.t0;
+    for (uint32_t piece = 0;; ++piece) {
+        const PieceInfo c = next_piece(ctl, sh, piece);
+        if (soft_any(c.rows == 0)) return;  // all sixteen warps or none: they meet at barriers below
+        const int n = c.n, ctx = c.ctx, keys = c.keys(), first_tail = c.first_tail();
         const Split split(c.rows);
         const int k = g >> split.log_chunks, chunk = g & (split.chunks() - 1);
-        const int ctx = c.own ? __ldg(p.ctx_len + c.seq) : INT_MAX, keys = c.own ? ctx + w.it.nodes : INT_MAX;
-        const int first_tail = c.own ? (ctx >> 7) - c.t0 : n;
-        for (int i = tid; i < split.used * 32 * (D / 8); i += kSoftThreads) {
-            const int r = i / (D / 8), ch = i - r * (D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);  // padding columns: scores of zero
-            if (r < c.rows) {
-                const int row = c.row0 + r, node = row / p.gq, hq = c.hkv * p.gq + (row - node * p.gq);
-                v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                         (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + ch * 8));
-                v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-            }
-            *reinterpret_cast<uint4*>(sq + (ch / 8) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
-        }
-        if (quad == 0) my_m[lane] = kNone;
-        if (tid == 0) sh->poison = 0;
-        fence_async_smem();
+        my_m[lane] = kNone;  // all four warps: each finds it there
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
-        rows_sync<kSoftThreads>();  // the references and the flag are set
         float l[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) l[e] = 0.0f;
@@ -285,12 +434,9 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                     const uint32_t f = f0 + tt, st = f % G::kValues;
                     wait(ctl, smem_u32(&sh->rv.full[st]), (f / G::kValues) & 1);  // passed by now: the copy's own barrier
                     bool found = false;
-                    if (pos0 + key >= ctx) {
-#pragma unroll 1
-                        for (int h = 0; h < G::kHalves; ++h)
-                            found |= clean_row(ring_v + st * G::kStage + h * kHalf, key, pos0 + key >= keys);
-                    }
-                    if (found) sh->poison = 1;
+                    if (pos0 + key >= ctx)
+                        found = clean_row(ring_v + st * G::kStage + (key >> 3) * TileGeo<D>::kGroup + (key & 7) * 128, D / 64, pos0 + key >= keys);
+                    if (found) sh->poison[piece & 1] = 1;
                 }
             }
             const uint32_t t_s = tmem + lanes + 128 * b + 32 * g;
@@ -299,10 +445,6 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
             for (int attempt = 0;; ++attempt) {
                 ld32(t_s, z);
                 tc_wait_ld();
-                if (tail) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) z[e] = (seen >> e) & 1u ? z[e] : kNegInf;
-                }
                 float top = kNegInf;
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
@@ -311,6 +453,10 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                     z[e + 1] = fmaf(z[e + 1], scale, -m.y);
                     z[e + 2] = fmaf(z[e + 2], scale, -m.z);
                     z[e + 3] = fmaf(z[e + 3], scale, -m.w);
+                    if (tail) {
+#pragma unroll
+                        for (int x = e; x < e + 4; ++x) z[x] = (seen >> x) & 1u ? z[x] : kNegInf;
+                    }
                     asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(z[e]), "f"(z[e + 1]));
                     asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(z[e + 2]), "f"(z[e + 3]));
                 }
@@ -325,14 +471,14 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                     tc_wait_ld();
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        float r = (seen >> (e + x)) & 1u ? v[x] : kNegInf;
+                        float r = (seen >> (e + x)) & 1u ? v[x] * scale : kNegInf;
                         asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(r));
                         mine = lane == e + x ? r : mine;
                     }
                 }
                 *place(g, b, quad) = mine;
                 group_sync(g);
-                const float best = fmaxf(fmaxf(*place(g, b, 0), *place(g, b, 1)), fmaxf(*place(g, b, 2), *place(g, b, 3))) * scale;
+                const float best = fmaxf(fmaxf(*place(g, b, 0), *place(g, b, 1)), fmaxf(*place(g, b, 2), *place(g, b, 3)));
                 const float old = my_m[lane];
                 const float to = best - old > 8.0f ? best : old;
                 const float fac = to == old ? 1.0f : ex2(old - to);
@@ -357,7 +503,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                 }
             }
             // this key's weights of 32 rows: four 16-byte places of its line
-            unsigned char* line = spw + b * G::kWeights + (g >> 1) * kHalf + key * 128;
+            unsigned char* line = spw + b * G::kWeights + (g >> 1) * G::kBlock + key * 128;
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
                 uint32_t pk[4];
@@ -383,6 +529,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
         *place(g, 0, quad) = sum_columns(l, lane);
         rows_sync<kSoftThreads>();
         tc_fence_after();
+        if (tid == 0) sh->poison[(piece & 1) ^ 1] = 0;  // read for the last time before the barrier before this one
         if (chunk < split.used) {
             // the groups of a chunk join its rows, each a part of them: lane e has row e's factors
             float m = kNone, sum = 0.0f, f[4];
@@ -410,7 +557,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                     p.lse[orow] = sum == 0.0f ? kNegInf : (m + log2f(sum)) * 0.69314718056f;
             }
             const int part = 32 >> split.log_tiles, d = quad * 32 + lane, rows = min(32, c.rows - 32 * chunk);
-            const bool poison = sh->poison != 0;
+            const bool poison = sh->poison[piece & 1] != 0;
             if (quad * 32 < D) {  // otherwise repeated outputs
 #pragma unroll 1
                 for (int e = k * part; e < (k + 1) * part && e < rows; e += 8) {
@@ -440,7 +587,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
 #pragma unroll 1
                     for (int e = k * part; e < (k + 1) * part && e < rows; ++e) {
                         const int row = c.row0 + 32 * chunk + e, node = row / p.gq;
-                        const float v = poison_of(p, c, w.it.nodes, node, ctx, d);
+                        const float v = poison_of(p, c, node, d);
                         if (v == 0.0f) continue;
                         const size_t to = (size_t)(c.node0 + node) * p.Hq + c.hkv * p.gq + (row - node * p.gq);
                         if (c.whole) {
@@ -475,9 +622,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (threadIdx.x == 0) {
         sh->rk.init();
         sh->rv.init();
-        mbar_init(smem_u32(&sh->q_full), kSoftThreads / 32);
-        mbar_init(smem_u32(&sh->v_full[0]), 1);
-        mbar_init(smem_u32(&sh->v_full[1]), 1);
+        for (int i = 0; i < kPieces; ++i) mbar_init(smem_u32(&sh->piece_full[i]), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh->q_full[i]), 1);
+            mbar_init(smem_u32(&sh->q_empty[i]), 1);
+            mbar_init(smem_u32(&sh->v_full[i]), 1);
+            sh->poison[i] = 0;
+        }
         for (int i = 0; i < 8; ++i) {
             mbar_init(smem_u32(&sh->s_full[i >> 1][i & 1]), 1);
             mbar_init(smem_u32(&sh->o_full[i >> 1][i & 1]), 1);
@@ -498,26 +649,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const Ctl ctl{p.ws, &sh->abort};
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 16) {
-        const int at = walk_start(p, lane);
-        if (lane == 0) sh->start = at;
-    }
-    __syncthreads();
-    const int start = sh->start;
     // 640 threads start with 96 registers each; the softmax's sixteen warps go on with 104 and the other four with
     // 64 (4 x 104 + 64 = 5 x 96)
     if (warp < 16) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        narrow_softmax<D>(p, ctl, sh, sq, spw, ring_v, tmem, start);
+        narrow_softmax<D>(p, ctl, sh, spw, ring_v, tmem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == 16) {
-            tc_producer<D, G::kKeys>(p, &mk, ctl, &sh->rk, ring_k, lane, start);
-        } else if (warp == 18) {
-            tc_producer<D, G::kValues>(p, &mv, ctl, &sh->rv, ring_v, lane, start);
-        } else if (warp == 17) {
-            narrow_issue<D>(p, ctl, sh, smem_u32(sq), smem_u32(spw), ring_k, ring_v, tmem, start);
-        }
+        if (warp == 16)
+            narrow_walk<D>(p, &mk, ctl, sh, smem_u32(sq), ring_k, lane);
+        else if (warp == 17)
+            narrow_scores<D>(p, ctl, sh, smem_u32(sq), ring_k, tmem);
+        else if (warp == 18)
+            narrow_values<D>(p, &mv, ctl, sh, ring_v, lane);
+        else
+            narrow_outputs<D>(p, ctl, sh, smem_u32(spw), ring_v, tmem);
     }
     tc_fence_before();
     __syncthreads();

@@ -31,8 +31,7 @@ constexpr int kTcThreads = 384;
 
 template <int D>
 struct TcGeo {
-    static constexpr int kHalves = D / 64;
-    static constexpr int kStage = kHalves * kHalf;         // one tile of keys or of values
+    static constexpr int kStage = TileGeo<D>::kBytes;  // one tile of keys or of values
     static constexpr int kKeys = D == 128 ? 2 : 5, kValues = D == 128 ? 3 : 5;  // stages
     static constexpr int kSmem = 1024 + 2 * kStage + (kKeys + kValues) * kStage;  // alignment, two blocks of q, the rings
 };
@@ -47,6 +46,15 @@ struct __align__(8) TcShared {
     int abort, start;
     int poison;  // a NaN or infinity among the values of the piece's nodes
 };
+
+template <int D, int kStages>
+__device__ void wide_fill(const AttnParams& p, const CUtensorMap* map, const Ctl& ctl, Ring<kStages>* rg, uint32_t ring, int lane, int start) {
+    Filler<D, kStages> filler(map, rg, ring);
+    Walk w = walk_begin(p, start);
+    AttnPiece c;
+    while (walk_next(p, w, c))
+        if (!filler.fill(p, ctl, c.seq, c.hkv, c.t0, c.t1, c.own ? __ldg(p.ctx_len + c.seq) + w.it.nodes : INT_MAX, lane)) return;
+}
 
 // ---- products ----
 
@@ -76,12 +84,12 @@ __device__ void tc_issue(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, u
                     wait(ctl, smem_u32(&sh->p_full[s]), np[s] & 1);
                     ++np[s];
                     tc_fence_after();
-                    const uint64_t vb = operand(ring_v + st * G::kStage);
+                    const uint64_t vb = operand(ring_v + st * G::kStage, TileGeo<D>::kGroup, 1024);
                     const uint32_t more = i > 1;
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k, vb + (uint64_t)((k * 2048) >> 4), io, k > 0 ? 1u : more);
+                            mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k, vb + (uint64_t)((k * 2 * TileGeo<D>::kGroup) >> 4), io, k > 0 ? 1u : more);
                         if (!two || s == 1) tc_commit(smem_u32(&sh->rv.empty[st]));
                         tc_commit(smem_u32(&sh->o_full[s]));
                     }
@@ -91,11 +99,12 @@ __device__ void tc_issue(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, u
                     const uint32_t f = f0 + tn, st = f % G::kKeys;
                     wait(ctl, smem_u32(&sh->rk.full[st]), (f / G::kKeys) & 1);
                     tc_fence_after();
-                    const uint64_t qa = operand(sq + (two ? s * G::kStage : 0)), kb = operand(ring_k + st * G::kStage);
+                    const uint64_t qa = operand(sq + (two ? s * G::kStage : 0), TileGeo<D>::kGroup, 0),
+                                   kb = operand(ring_k + st * G::kStage, TileGeo<D>::kGroup, 0);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
-                            const uint64_t at = (uint64_t)(((k / 4) * kHalf + (k % 4) * 32) >> 4);
+                            const uint64_t at = (uint64_t)(TileGeo<D>::step(k) >> 4);
                             mma_ss(tmem + 128 * s, qa + at, kb + at, is, k > 0);
                         }
                         if (!two || s == 1) tc_commit(smem_u32(&sh->rk.empty[st]));
@@ -180,7 +189,7 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
                                                            (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + ch * 8));
             v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
             const int k = rr & (kTile - 1);
-            *reinterpret_cast<uint4*>(sq + (rr / kTile) * G::kStage + (ch / 8) * kHalf + k * 128 + (((ch & 7) ^ (k & 7)) << 4)) = v;
+            *reinterpret_cast<uint4*>(sq + (rr / kTile) * G::kStage + TileGeo<D>::at(k, ch)) = v;
         }
         if (tid == 0) sh->poison = 0;
         fence_async_smem();
@@ -208,11 +217,9 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
                 const uint32_t v = ring_v + st * G::kStage;
                 bool found = false;
                 const int k = two ? tid >> 1 : r;
-                if (pos0 + k >= ctx) {
-#pragma unroll 1
-                    for (int h = 0; h < G::kHalves; ++h)
-                        if (!two || G::kHalves == 1 || h == (tid & 1)) found |= clean_row(v + h * kHalf, k, pos0 + k >= keys);
-                }
+                // two threads for a row of two blocks where both groups have the tile
+                const int h = two ? (tid & 1) * (D / 64 - 1) : 0, count = two ? 1 : D / 64;
+                if (pos0 + k >= ctx) found = clean_row(v + (k >> 3) * TileGeo<D>::kGroup + h * 1024 + (k & 7) * 128, count, pos0 + k >= keys);
                 if (found) sh->poison = 1;
                 fence_async_smem();
                 if (two) rows_sync<256>();  // the other stream's product reads the same values
@@ -385,9 +392,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
-            tc_producer<D, G::kKeys>(p, &mk, ctl, &sh->rk, ring_k, lane, start);
+            wide_fill<D, G::kKeys>(p, &mk, ctl, &sh->rk, ring_k, lane, start);
         } else if (warp == 10) {
-            tc_producer<D, G::kValues>(p, &mv, ctl, &sh->rv, ring_v, lane, start);
+            wide_fill<D, G::kValues>(p, &mv, ctl, &sh->rv, ring_v, lane, start);
         } else if (warp == 9) {
             tc_issue<D>(p, ctl, sh, smem_u32(sq), ring_k, ring_v, tmem, start);
         }
