@@ -31,7 +31,7 @@ struct AttnHead {  // written by the planning kernel
     int flag;      // error flag (first word of every workspace)
     unsigned done; // blocks of the planning kernel that have finished
     int ncta, base, rest;  // W = ncta * base + rest
-    int units_shared;      // units of shared items
+    int units, units_shared;  // units, those of shared items among them (the first ones)
 };
 
 struct AttnLayout {
@@ -128,17 +128,18 @@ __device__ __forceinline__ int attn_cta_of(const AttnHead* h, int x) {
     return x < first ? x / (h->base + 1) : h->rest + (x - first) / h->base;
 }
 
-// Item that tile x of the line lies in: among items that begin at the same place the last one, which has tiles.
-__device__ __forceinline__ int attn_find(const AttnItem* it, int n, int x) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldcg(&it[mid].cum) <= x)
-            lo = mid;
-        else
-            hi = mid - 1;
+// A warp's search: the last of items [first, first + n) whose key is at most x (the first one's is), 32 at a time. With
+// keys that rise along the line it is the one that x lies in, as items without tiles come before it.
+template <typename Key>
+__device__ __forceinline__ int attn_search(const AttnItem* items, int first, int n, int x, int lane, Key key) {
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const bool below = lane * step < n && key(items[first + lane * step]) <= x;
+        const int k = max(0, __popc(__ballot_sync(0xffffffffu, below)) - 1);
+        n = min(step, n - k * step);
+        first += k * step;
     }
-    return lo;
+    return first;
 }
 
 // One piece of a unit, as a block walks along its share of the line.

@@ -172,22 +172,12 @@ struct Walk {
     const AttnItem* items;
     AttnItem it;
 };
-// One warp: the item that the block's first tile lies in (the last one that begins at or before it), 32 at a time.
+// One warp: the item that the block's first tile lies in.
 __device__ __forceinline__ int walk_start(const AttnParams& p, int lane) {
     const AttnHead* h = attn_head(p);
-    const int cta = blockIdx.x, n = p.G + p.S;
-    if (cta >= h->ncta) return 0;
-    const int x = attn_cut(h, cta);
-    const AttnItem* items = ws_ptr<AttnItem>(p.ws, p.L.item);
-    int lo = 0, len = n;  // the answer is one of items [lo, lo + len)
-    while (len > 1) {
-        const int step = (len + 31) / 32, at = lo + lane * step;
-        const bool below = lane * step < len && __ldcg(&items[at].cum) <= x;
-        const int k = max(0, __popc(__ballot_sync(0xffffffffu, below)) - 1);
-        len = min(step, len - k * step);
-        lo += k * step;
-    }
-    return lo;
+    if ((int)blockIdx.x >= h->ncta) return 0;
+    return attn_search(ws_ptr<AttnItem>(p.ws, p.L.item), 0, p.G + p.S, attn_cut(h, blockIdx.x), lane,
+                       [](const AttnItem& a) { return __ldcg(&a.cum); });
 }
 __device__ __forceinline__ Walk walk_begin(const AttnParams& p, int start) {
     const AttnHead* h = attn_head(p);

@@ -195,6 +195,7 @@ extern "C" int tree_attention(const void* q, long long q_stride, const void* k_c
     p.ws = ws;
     cudaStream_t st = (cudaStream_t)stream;
     const AttnKind kind = kind_of(dtype, T, Hq, Hkv);
+    if (p.G > 0 && (long long)Hkv * attn_blocks((long long)T * p.gq, rows_of(kind)) > 65535) return SMCSD_ERR_INVALID_ARG;
     // all tiles of all units are numbered in 32 bits
     const long long units = (long long)S * Hkv * attn_blocks((long long)T * p.gq, rows_of(kind)) +
                             (long long)p.G * Hkv * attn_blocks((long long)N * T * p.gq, rows_of(kind));

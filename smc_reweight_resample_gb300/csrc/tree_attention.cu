@@ -13,59 +13,84 @@ namespace smcsd {
 
 constexpr int kPlanThreads = 512;
 
-__device__ __forceinline__ void scan_pair(long long& a, long long& b, long long* sa, long long* sb) {
-    // exclusive prefix over the block's threads
+// Exclusive prefix of v over the block's threads, and the total.
+__device__ __forceinline__ long long plan_prefix(long long v, long long* sums, long long& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long ia = a, ib = b;
+    long long in = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long va = __shfl_up_sync(0xffffffffu, ia, o), vb = __shfl_up_sync(0xffffffffu, ib, o);
-        if (lane >= o) ia += va, ib += vb;
+        const long long t = __shfl_up_sync(0xffffffffu, in, o);
+        if (lane >= o) in += t;
     }
-    if (lane == 31) sa[warp] = ia, sb[warp] = ib;
+    if (lane == 31) sums[warp] = in;
     __syncthreads();
-    if (warp == 0) {
-        const int nw = blockDim.x >> 5;
-        long long wa = lane < nw ? sa[lane] : 0, wb = lane < nw ? sb[lane] : 0;
-        const long long oa = wa, ob = wb;
+    long long w = lane < kPlanThreads / 32 ? sums[lane] : 0, before = w;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long va = __shfl_up_sync(0xffffffffu, wa, o), vb = __shfl_up_sync(0xffffffffu, wb, o);
-            if (lane >= o) wa += va, wb += vb;
-        }
-        if (lane < nw) sa[lane] = wa - oa, sb[lane] = wb - ob;
-        if (lane == 31) sa[32] = wa, sb[32] = wb;
+    for (int o = 1; o < kPlanThreads / 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += t;
     }
-    __syncthreads();
-    a = ia - a + sa[warp];
-    b = ib - b + sb[warp];
+    total = __shfl_sync(0xffffffffu, before, kPlanThreads / 32 - 1);
+    return __shfl_sync(0xffffffffu, before - w, warp) + in - v;
+}
+
+// Item i without its places on the line.
+__device__ __forceinline__ AttnItem plan_item(const AttnParams& p, const int* shared, int i) {
+    AttnItem it;
+    if (i < p.G) {
+        it.seq = i * p.N;
+        it.tiles = __ldcg(shared + i);
+        it.tile0 = 0;
+        int first, a;
+        it.nodes = attn_nodes(p, it.seq, first);
+        for (int k = 1; k < p.N; ++k) {
+            const int m = attn_nodes(p, it.seq + k, a);
+            if (m > 0 && a != first + it.nodes) {  // offsets that do not fit, already reported
+                it.nodes = 0;
+                break;
+            }
+            it.nodes += m;
+        }
+        it.node0 = first;
+    } else {
+        it.seq = i - p.G;
+        it.nodes = attn_nodes(p, it.seq, it.node0);
+        const int c = attn_ctx(p, it.seq, it.nodes);
+        if (c < 0) it.nodes = 0;
+        it.tile0 = p.G > 0 ? __ldcg(shared + it.seq / p.N) : 0;
+        it.tiles = it.nodes > 0 ? (c + it.nodes + p.tile - 1) / p.tile - it.tile0 : 0;
+    }
+    const int rows = it.nodes * p.gq;
+    it.nrb = max(1, attn_blocks(rows, p.rb));
+    it.per = max(1, min(rows, p.rb));
+    if (it.nodes == 0 || it.tiles < 0) it.tiles = 0;
+    it.pad[0] = it.pad[1] = it.pad[2] = 0;
+    return it;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnParams p) {
     __shared__ int best;
     __shared__ unsigned last;
-    __shared__ long long sa[33], sb[33];
+    __shared__ long long sums[kPlanThreads / 32];
     griddep_launch_dependents();
     const int tid = threadIdx.x;
     int* shared = ws_ptr<int>(p.ws, p.L.shared);
     if (p.G > 0) {
-        // pages that every sequence of the group has at the same place, all of them full context
+        // pages that every sequence of the group has at the same place, all of them full context; a thread has a column
         const int s0 = blockIdx.x * p.N;
-        if (tid == 0) best = INT_MAX;
+        if (tid == 0) best = p.pages_per_seq;
         __syncthreads();
-        int c = INT_MAX;
-        for (int i = tid; i < p.N; i += kPlanThreads) c = min(c, max(0, __ldg(p.ctx_len + s0 + i)));
-        if (c != INT_MAX) atomicMin(&best, c);
+        for (int i = tid; i < p.N; i += kPlanThreads) atomicMin(&best, max(0, __ldg(p.ctx_len + s0 + i)) >> p.page_shift);
         __syncthreads();
-        const int lim = min(best >> p.page_shift, p.pages_per_seq);
-        __syncthreads();
-        if (tid == 0) best = lim;
+        const int lim = best;
         __syncthreads();
         const int32_t* row = p.table + (long long)s0 * p.pages_per_seq;
-        for (long long i = tid; i < (long long)(p.N - 1) * lim; i += kPlanThreads) {
-            const int s = (int)(i / lim), j = (int)(i - (long long)s * lim);
+        for (int j = tid; j < lim && j < *reinterpret_cast<volatile int*>(&best); j += kPlanThreads) {
             const int id = __ldg(row + j);
-            if (id < 0 || id != __ldg(row + (long long)(s + 1) * p.pages_per_seq + j)) atomicMin(&best, j);
+            bool same = id >= 0;
+#pragma unroll 8
+            for (int k = 1; k < p.N; ++k) same &= __ldg(row + (long long)k * p.pages_per_seq + j) == id;
+            if (!same) atomicMin(&best, j);
         }
         __syncthreads();
         if (tid == 0) {
@@ -80,66 +105,38 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         __syncthreads();
         if (!last) return;
     }
+    // tiles (high word) and units (low word) before each item: a thread has a run of them
     AttnItem* items = ws_ptr<AttnItem>(p.ws, p.L.item);
     const int n = p.G + p.S, per = (n + kPlanThreads - 1) / kPlanThreads;
     const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    long long tiles = 0, units = 0, grp = 0;
+    auto size_of = [&](const AttnItem& it) {
+        const long long u = it.tiles > 0 ? (long long)p.Hkv * it.nrb : 0;
+        return ((u * it.tiles) << 32) + u;
+    };
+    AttnItem it;
+    long long mine = 0, total;
     for (int i = i0; i < i1; ++i) {
-        AttnItem it;
-        if (i < p.G) {
-            it.seq = i * p.N;
-            it.tiles = __ldcg(shared + i);
-            it.tile0 = 0;
-            it.nodes = 0;
-            int a, first = 0;
-            for (int k = 0; k < p.N; ++k) {
-                const int m = attn_nodes(p, it.seq + k, a);
-                if (k == 0) first = a;
-                if (m > 0 && a != first + it.nodes) raise_error(p.ws, kErrRange), it.nodes = 0, k = p.N;
-                else it.nodes += m;
-            }
-            it.node0 = first;
-        } else {
-            it.seq = i - p.G;
-            it.nodes = attn_nodes(p, it.seq, it.node0);
-            const int c = attn_ctx(p, it.seq, it.nodes);
-            if (c < 0) it.nodes = 0;
-            it.tile0 = p.G > 0 ? __ldcg(shared + it.seq / p.N) : 0;
-            it.tiles = it.nodes > 0 ? (c + it.nodes + p.tile - 1) / p.tile - it.tile0 : 0;
-        }
-        const int rows = it.nodes * p.gq;
-        it.nrb = max(1, attn_blocks(rows, p.rb));
-        it.per = max(1, min(rows, p.rb));
-        if (it.nodes == 0 || it.tiles < 0) it.tiles = 0;
-        const int u = it.tiles > 0 ? p.Hkv * it.nrb : 0;
-        it.unit0 = u;
-        it.cum = u * it.tiles;
+        it = plan_item(p, shared, i);
+        mine += size_of(it);
+    }
+    long long at = plan_prefix(mine, sums, total);
+    for (int i = i0; i < i1; ++i) {
+        if (per > 1) it = plan_item(p, shared, i);
+        it.cum = (int)(at >> 32);
+        it.unit0 = (int)(at & 0xffffffffll);
         items[i] = it;
-        tiles += it.cum;
-        units += u;
-        if (i < p.G) grp += u;
+        at += size_of(it);
+        if (i == p.G - 1) attn_head(p)->units_shared = (int)(at & 0xffffffffll);
     }
-    long long t = tiles, u = units;
-    scan_pair(t, u, sa, sb);
-    const long long W = sa[32];
-    for (int i = i0; i < i1; ++i) {
-        const long long ct = items[i].cum, cu = items[i].unit0;
-        items[i].cum = (int)t;
-        items[i].unit0 = (int)u;
-        t += ct;
-        u += cu;
-    }
-    __syncthreads();
-    long long zero = 0;
-    scan_pair(grp, zero, sa, sb);
     if (tid == 0) {
         AttnHead* h = attn_head(p);
-        h->units_shared = (int)sa[32];
-        const long long most = (W + p.min_tiles - 1) / p.min_tiles;
-        const int n = (int)(most < p.ncta_max ? most : p.ncta_max);
-        h->ncta = n;
-        h->base = n > 0 ? (int)(W / n) : 0;
-        h->rest = n > 0 ? (int)(W % n) : 0;
+        const int W = (int)(total >> 32);
+        const int cta = min(p.ncta_max, (W + p.min_tiles - 1) / p.min_tiles);
+        if (p.G == 0) h->units_shared = 0;
+        h->units = (int)(total & 0xffffffffll);
+        h->ncta = cta;
+        h->base = cta > 0 ? W / cta : 0;
+        h->rest = cta > 0 ? W % cta : 0;
     }
 }
 
@@ -190,7 +187,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
     const int end = attn_cut(h, cta + 1);
     const int n_items = p.G + p.S;
     while (x < end) {
-        const int ii = attn_find(items, n_items, x);
+        const int ii = attn_search(items, 0, n_items, x, lane, [](const AttnItem& a) { return __ldcg(&a.cum); });
         const AttnItem it = items[ii];
         int next;
         const AttnPiece c = attn_piece(p, it, ii >= p.G, x, end, cta, h->units_shared, next);
@@ -344,87 +341,119 @@ cudaError_t launch_attn_simt(const AttnParams& p, cudaStream_t st) {
 // joining the pieces
 // ------------------------------------------------------------------------------------------
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = 256;  // a unit's rows are dealt to gridDim.z blocks
 
 template <int DT>
-__device__ __forceinline__ void store1(void* base, size_t i, float v) {
-    if (DT == 0)
-        static_cast<float*>(base)[i] = v;
-    else
-        static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
-}
-
-// Sequence that row r belongs to (ragged offsets: the last one that starts at or before it).
-__device__ __forceinline__ int attn_seq_of(const AttnParams& p, int r) {
-    if (!p.node_offsets) return r / p.T;
-    int lo = 0, hi = p.S - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(p.node_offsets + mid) <= r)
-            lo = mid;
-        else
-            hi = mid - 1;
+__device__ __forceinline__ void store4(void* base, size_t i, float4 v) {
+    if (DT == 0) {
+        *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = v;
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
-    return lo;
 }
 
-// One warp for each row and query head: the shared unit's pieces, then the own unit's, in the order of
-// the line.
+// The pieces of one row: slots c0 .. c1 of a unit, row r of each.
+struct JoinRun {
+    const float* o;
+    const float2* ml;
+    size_t step_o, step_ml;  // from one piece to the next
+    int count;
+};
+
+// A few blocks for each unit that was cut (found from the cuts: the first one inside a unit answers for it) or, where
+// groups share keys, for each own unit. A row's pieces are joined in the order of the line, the shared unit's
+// first: 4 columns a thread.
 template <int DT, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid_constant__ AttnParams p) {
     griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-    if (w >= (long long)p.R * p.Hq) return;
-    const int r = (int)(w / p.Hq), hq = (int)(w - (long long)r * p.Hq), hkv = hq / p.gq;
-    const int s = attn_seq_of(p, r);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const AttnHead* h = attn_head(p);
     const AttnItem* items = ws_ptr<AttnItem>(p.ws, p.L.item);
-    float m = kNegInf, l = 0.0f;
-    constexpr int kE = D / 32;
-    float acc[kE];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
-    for (int k = p.G > 0 ? 0 : 1; k < 2; ++k) {
-        const AttnItem it = items[k == 0 ? s / p.N : p.G + s];
-        if (it.tiles == 0) continue;
-        const int node = r - it.node0;
-        if (node < 0 || node >= it.nodes) return;  // bad offsets, already reported
-        const int row = node * p.gq + (hq - hkv * p.gq), rb = row / it.per, rr = row - rb * it.per;
-        const int u = hkv * it.nrb + rb;
+    const int n = p.G + p.S;
+    // the unit: item `it`, number u of its units
+    AttnItem it;
+    int u;
+    if (p.G == 0) {
+        const int cut = blockIdx.x + 1;  // the last block has none
+        if (cut >= h->ncta) return;
+        const int x = attn_cut(h, cut);
+        it = items[attn_search(items, 0, n, x, lane, [](const AttnItem& a) { return __ldcg(&a.cum); })];
+        u = (x - it.cum) / it.tiles;
         const int x0 = it.cum + u * it.tiles;
-        const int c0 = attn_cta_of(h, x0), c1 = attn_cta_of(h, x0 + it.tiles - 1);
-        if (k == 1 && it.tile0 == 0 && c0 == c1) return;  // written directly
-        for (int c = c0; c <= c1; ++c) {
-            const size_t slot = k == 0 ? (size_t)(it.unit0 + u + c) : (size_t)(it.unit0 + u - h->units_shared + c);
-            const size_t at = slot * (k == 0 ? p.L.rows_g : p.L.rows_s) + rr;
-            const float2 ml = __ldcg(ws_ptr<float2>(p.ws, k == 0 ? p.L.ml_g : p.L.ml_s) + at);
-            const float* o = ws_ptr<float>(p.ws, k == 0 ? p.L.slot_g : p.L.slot_s) + at * D;
-            float v[kE];
-#pragma unroll
-            for (int e = 0; e < kE; ++e) v[e] = __ldcg(o + e * 32 + lane);
-            if (ml.y == 0.0f) continue;  // saw nothing
-            const float mx = fmaxf(m, ml.x);
-            const float base = mx == kNegInf ? 0.0f : mx;
-            const float fa = l == 0.0f ? 0.0f : exp2f(m - base), fb = exp2f(ml.x - base);
-            l = l * fa + ml.y * fb;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) acc[e] = fmaf(acc[e], fa, v[e] * fb);
-            m = mx;
-        }
+        if (x == x0 || attn_cut(h, cut - 1) > x0) return;  // between units, or not the first cut inside
+    } else {
+        it = items[p.G + blockIdx.x];
+        u = blockIdx.y;
+        if (it.tiles == 0 || u >= p.Hkv * it.nrb) return;
     }
-    const size_t orow = (size_t)r * p.Hq + hq;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) store1<DT>(p.out, orow * D + e * 32 + lane, acc[e] * inv);
-    if (lane == 0 && p.lse) p.lse[orow] = l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718056f;
+    const int hkv = u / it.nrb, row0 = (u - hkv * it.nrb) * it.per, rows = min(it.per, it.nodes * p.gq - row0);
+    JoinRun own, sh{};
+    {
+        const int x0 = it.cum + u * it.tiles, c0 = attn_cta_of(h, x0);
+        const size_t slot = (size_t)(it.unit0 + u - h->units_shared + c0);
+        own.count = attn_cta_of(h, x0 + it.tiles - 1) - c0 + 1;
+        own.step_o = (size_t)p.L.rows_s * D;
+        own.step_ml = p.L.rows_s;
+        own.o = ws_ptr<float>(p.ws, p.L.slot_s) + slot * own.step_o;
+        own.ml = ws_ptr<float2>(p.ws, p.L.ml_s) + slot * own.step_ml;
+    }
+    AttnItem grp;
+    if (p.G > 0) grp = items[it.seq / p.N];
+    const bool shared = p.G > 0 && grp.tiles > 0;
+    if (!shared && own.count == 1) return;  // written directly
+    constexpr int kLanes = D / 4, kRows = 32 / kLanes;  // lanes of a row, rows of a warp at a time
+    const int col = (lane % kLanes) * 4;
+    const int step = gridDim.z * (kJoinThreads / 32) * kRows;
+    for (int r = (blockIdx.z * (kJoinThreads / 32) + warp) * kRows + lane / kLanes; r < rows; r += step) {
+        const int row = row0 + r, node = it.node0 + row / p.gq, hq = hkv * p.gq + row % p.gq;
+        if (shared) {
+            const int gr = row + (it.node0 - grp.node0) * p.gq, rb = gr / grp.per, gu = hkv * grp.nrb + rb;
+            const int x0 = grp.cum + gu * grp.tiles, c0 = attn_cta_of(h, x0);
+            const size_t slot = (size_t)(grp.unit0 + gu + c0);
+            sh.count = attn_cta_of(h, x0 + grp.tiles - 1) - c0 + 1;
+            sh.step_o = (size_t)p.L.rows_g * D;
+            sh.step_ml = p.L.rows_g;
+            sh.o = ws_ptr<float>(p.ws, p.L.slot_g) + slot * sh.step_o + (size_t)(gr - rb * grp.per) * D;
+            sh.ml = ws_ptr<float2>(p.ws, p.L.ml_g) + slot * sh.step_ml + (gr - rb * grp.per);
+        }
+        float m = kNegInf, l = 0.0f;
+        float4 acc = make_float4(0, 0, 0, 0);
+        auto join = [&](const JoinRun& j, int r) {
+#pragma unroll 4
+            for (int i = 0; i < j.count; ++i) {
+                const float2 ml = __ldcg(j.ml + i * j.step_ml + r);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(j.o + i * j.step_o + (size_t)r * D + col));
+                if (ml.y == 0.0f) continue;  // saw nothing
+                const float mx = fmaxf(m, ml.x);
+                const float base = mx == kNegInf ? 0.0f : mx;
+                const float fa = l == 0.0f ? 0.0f : exp2f(m - base), fb = exp2f(ml.x - base);
+                l = l * fa + ml.y * fb;
+                acc.x = fmaf(acc.x, fa, v.x * fb);
+                acc.y = fmaf(acc.y, fa, v.y * fb);
+                acc.z = fmaf(acc.z, fa, v.z * fb);
+                acc.w = fmaf(acc.w, fa, v.w * fb);
+                m = mx;
+            }
+        };
+        if (shared) join(sh, 0);
+        join(own, r);
+        const size_t orow = (size_t)node * p.Hq + hq;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        store4<DT>(p.out, orow * D + col, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        if (col == 0 && p.lse) p.lse[orow] = l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718056f;
+    }
 }
 
 template <int DT, int D>
 static cudaError_t launch_combine_t(const AttnParams& p, cudaStream_t st) {
+    // a block's eight warps take up to four rows each
+    const long long rows = (long long)p.T * p.gq;
+    const unsigned parts = (unsigned)((rows < p.rb ? rows : p.rb) + 31) / 32;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(((long long)p.R * p.Hq + kJoinWarps - 1) / kJoinWarps));
-    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.gridDim = p.G > 0 ? dim3((unsigned)p.S, (unsigned)(p.Hkv * attn_blocks(rows, p.rb)), parts) : dim3((unsigned)p.ncta_max, 1, parts);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
