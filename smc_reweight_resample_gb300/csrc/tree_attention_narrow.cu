@@ -13,9 +13,9 @@
 //   warp 16     walks along the block's share, hands the pieces round in shared memory, brings their query rows (two
 //               places of 64 rows, or one of 128) and the pages of keys (attn_tc.cuh)
 //   warp 18     brings the pages of values
-//   warps 17 and 19  issue S^T and O^T: one warp for both has more to issue than a tile's bytes take. Scores and weights
-//               have two buffers, so the scores of the next round of tiles are there when a group comes to them, and
-//               those of the next piece while this one is written out
+//   warps 17 and 19  issue S^T and O^T: one warp for both has more to issue than a tile's bytes take. Scores have two
+//               buffers, so those of the next round of tiles are there when a group comes to them, and those of the next
+//               piece while this one is written out
 //
 // Softmax. Per column: a reference m common to the keys of the group's tiles, P = exp2(z - m) with
 // z = scale2 q.k, l the sum of P before it is rounded (each thread adds up its own keys; they meet at the end of
@@ -35,11 +35,11 @@ constexpr float kNone = -3.402823466e38f;  // reference of a column that has see
 template <int D>
 struct NarrowGeo {
     static constexpr int kStage = TileGeo<D>::kBytes;
-    static constexpr int kKeys = D == 128 ? 2 : 4, kValues = D == 128 ? 2 : 5;  // stages
+    static constexpr int kKeys = D == 128 ? 2 : 5, kValues = D == 128 ? 3 : 6;  // stages
     static constexpr int kBlock = 128 * 128;     // 128 keys x 64 columns of P
-    static constexpr int kWeights = 2 * kBlock;  // one buffer of P: 128 columns x 128 keys
+    static constexpr int kWeights = 2 * kBlock;  // P: 128 columns x 128 keys
     static constexpr int kSlot = 8 * TileGeo<D>::kGroup;  // 64 query rows
-    static constexpr int kSmem = 1024 + kStage + 2 * kWeights + (kKeys + kValues) * kStage;
+    static constexpr int kSmem = 1024 + kStage + kWeights + (kKeys + kValues) * kStage;
 };
 
 // A piece (attn_plan.cuh) as it is handed round.
@@ -297,7 +297,7 @@ __device__ void narrow_outputs(const AttnParams& p, const Ctl& ctl, NarrowShared
             tc_fence_after();
             // 64 columns of V have no second block: the upper half of the outputs repeats the lower one
             const uint64_t va = operand(ring_v + st * G::kStage, TileGeo<D>::kGroup, D == 128 ? 1024 : 0);
-            const uint64_t pb = operand(sp + b * G::kWeights + (width * k / 64) * G::kBlock + (width * k % 64) * 2, 1024, G::kBlock);
+            const uint64_t pb = operand(sp + (width * k / 64) * G::kBlock + (width * k % 64) * 2, 1024, G::kBlock);
             const uint32_t to = tmem + 256 + width * k, more = r > 0;
             if (elect_one()) {
 #pragma unroll
@@ -388,12 +388,12 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const float scale = p.scale2 != 0.0f ? p.scale2 : 1e-30f;  // 0: equal weights, and what is not seen stays so
     float* my_m = &sh->m[32 * g];
-    // This group's 32 columns of the weights' buffer b: 64 bytes of each key's 128-byte line, swizzled. Sixteen
-    // places of the first eight keys' also carry 4 x 32 floats (one of each warp and column) between products.
-    auto place = [&](int group, int b, int wq) {
+    // A group's 32 columns of the weights: 64 bytes of each key's 128-byte line, swizzled. Sixteen places of the first
+    // eight keys' also carry 4 x 32 floats (one of each warp and column) between products.
+    auto place = [&](int group, int wq) {
         const int x = 8 * wq + (lane >> 2), k = x >> 2;
-        return reinterpret_cast<float*>(spw + b * G::kWeights + (group >> 1) * G::kBlock + k * 128 +
-                                        ((((group & 1) * 4 + (x & 3)) ^ (k & 7)) << 4)) + (lane & 3);
+        return reinterpret_cast<float*>(spw + (group >> 1) * G::kBlock + k * 128 + ((((group & 1) * 4 + (x & 3)) ^ (k & 7)) << 4)) +
+               (lane & 3);
     };
     Uses uses{};
     uint32_t f0 = 0, tails = 0;
@@ -415,8 +415,10 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
         for (int i = 0; i < rounds; ++i) {
             const int tt = (i << split.log_tiles) + k, pos0 = (c.t0 + tt) * kTile, b = i & 1;
             const bool tail = tt >= first_tail;
-            // the product that read these weights last
-            if (i >= 2) wait(ctl, smem_u32(&sh->o_full[k][b]), uses.parity(k, b, i / 2 - 1));
+            // the product that read the group's weights last
+            auto weights_free = [&] {
+                if (i > 0) wait(ctl, smem_u32(&sh->o_full[k][b ^ 1]), uses.parity(k, b ^ 1, (i - 1) / 2));
+            };
             wait(ctl, smem_u32(&sh->s_full[k][b]), uses.parity(k, b, i / 2));
             tc_fence_after();
             uint32_t seen = 0xffffffffu;  // rows that see this thread's key
@@ -476,9 +478,10 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                         mine = lane == e + x ? r : mine;
                     }
                 }
-                *place(g, b, quad) = mine;
+                weights_free();
+                *place(g, quad) = mine;
                 group_sync(g);
-                const float best = fmaxf(fmaxf(*place(g, b, 0), *place(g, b, 1)), fmaxf(*place(g, b, 2), *place(g, b, 3)));
+                const float best = fmaxf(fmaxf(*place(g, 0), *place(g, 1)), fmaxf(*place(g, 2), *place(g, 3)));
                 const float old = my_m[lane];
                 const float to = best - old > 8.0f ? best : old;
                 const float fac = to == old ? 1.0f : ex2(old - to);
@@ -488,7 +491,6 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                 if (i > 0) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) l[e] *= __shfl_sync(0xffffffffu, fac, e);
-                    wait(ctl, smem_u32(&sh->o_full[k][b ^ 1]), uses.parity(k, b ^ 1, (i - 1) / 2));
                     tc_fence_after();
 #pragma unroll 1
                     for (int e = 0; e < 32; e += 8) {
@@ -503,7 +505,8 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                 }
             }
             // this key's weights of 32 rows: four 16-byte places of its line
-            unsigned char* line = spw + b * G::kWeights + (g >> 1) * G::kBlock + key * 128;
+            weights_free();
+            unsigned char* line = spw + (g >> 1) * G::kBlock + key * 128;
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
                 uint32_t pk[4];
@@ -526,7 +529,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
             const int i = rounds - 1;
             wait(ctl, smem_u32(&sh->o_full[k][i & 1]), uses.parity(k, i & 1, i / 2));
         }
-        *place(g, 0, quad) = sum_columns(l, lane);
+        *place(g, quad) = sum_columns(l, lane);
         rows_sync<kSoftThreads>();
         tc_fence_after();
         if (tid == 0) sh->poison[(piece & 1) ^ 1] = 0;  // read for the last time before the barrier before this one
@@ -542,7 +545,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                 if (x >= split.tiles()) continue;
                 const int from = (x << split.log_chunks) + chunk;
                 f[x] = ex2(sh->m[32 * from + lane] - m);
-                sum = fmaf((*place(from, 0, 0) + *place(from, 0, 1)) + (*place(from, 0, 2) + *place(from, 0, 3)), f[x], sum);
+                sum = fmaf((*place(from, 0) + *place(from, 1)) + (*place(from, 2) + *place(from, 3)), f[x], sum);
             }
             if (c.whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     NarrowShared<D>* sh = &shared;
     unsigned char* sq = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
     unsigned char* spw = sq + G::kStage;
-    const uint32_t ring_k = smem_u32(spw + 2 * G::kWeights), ring_v = ring_k + G::kKeys * G::kStage;
+    const uint32_t ring_k = smem_u32(spw + G::kWeights), ring_v = ring_k + G::kKeys * G::kStage;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         sh->rk.init();
