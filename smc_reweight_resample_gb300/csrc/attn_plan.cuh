@@ -9,10 +9,18 @@
 //
 // Cut. All tiles of all units stand in one line, W of them (below 2^31). Block c of ncta takes W / ncta of them,
 // the first W % ncta blocks one more: equal shares whatever the lengths are. Where a cut falls inside a unit, or a
-// row has a shared and an own unit, the pieces leave (sum, max, weighted values) in a slot and the
-// combining kernel joins them in a fixed order. A piece of unit u in block c has the number u + c:
-// both rise along the line and one of them rises from piece to piece, so no two pieces share a number.
+// row has a shared and an own unit, the pieces leave (sum, max, weighted values) in a slot. Without groups only a block's
+// first and last piece can be part of a unit: block c has slots 2 c (a unit that began before it) and 2 c + 1 (one
+// that ends behind it), and the last block to finish a unit's pieces joins them, in the order of the line. With groups a
+// piece of unit u in block c has slot u + c (both rise along the line and one of them rises from piece to piece, so no
+// two pieces share a slot), and a kernel of its own joins a row's pieces.
+//
+// Who works the line out. Without groups and for up to 1024 sequences a warp of each block does, from the lengths
+// alone (a few loads, all in flight together; a planning kernel before it and the loads of its results took 5 us of a
+// call's 17). Otherwise the planning kernel writes the items down.
 #pragma once
+
+#include <cuda_bf16.h>
 
 #include "smcsd_internal.cuh"
 
@@ -31,10 +39,15 @@ struct AttnHead {  // written by the planning kernel
     int flag;      // error flag (first word of every workspace)
     unsigned done; // blocks of the planning kernel that have finished
     int ncta, base, rest;  // W = ncta * base + rest
-    int units, units_shared;  // units, those of shared items among them (the first ones)
+    int units_shared;      // units of shared items, which are the first ones
 };
 
+// Every kernel that takes part has at most kAttnMaxCta blocks on the line.
+constexpr int kAttnMaxCta = 1024;
+constexpr int kAttnWarpPlan = 1024;  // sequences whose places on the line a warp works out
+
 struct AttnLayout {
+    size_t count;    // unsigned [kAttnMaxCta]: pieces that have arrived, of the unit that is cut first at a block's end
     size_t item;     // AttnItem [G + S]
     size_t shared;   // int [G] tiles shared by a group
     size_t slot_g;   // pieces of shared units: float [slots][rows_g][D], then float2 [slots][rows_g]
@@ -44,15 +57,14 @@ struct AttnLayout {
     size_t total;
 };
 
-// Every kernel that takes part has at most kAttnMaxCta blocks on the line.
-constexpr int kAttnMaxCta = 1024;
-
-__host__ __device__ inline int attn_blocks(long long rows, int rb) { return (int)((rows + rb - 1) / rb); }
+inline int attn_blocks(long long rows, int rb) { return (int)((rows + rb - 1) / rb); }
 
 inline AttnLayout attn_layout(int S, int N, int T, int gq, int Hkv, int D, int RB, int ncta) {
     AttnLayout L{};
     const size_t G = N > 1 ? (size_t)S / N : 0;
     size_t o = 256;
+    L.count = o;
+    o = align256(o + 4 * kAttnMaxCta);
     L.item = o;
     o = align256(o + sizeof(AttnItem) * (G + S));
     L.shared = o;
@@ -60,7 +72,7 @@ inline AttnLayout attn_layout(int S, int N, int T, int gq, int Hkv, int D, int R
     const long long rs = (long long)T * gq, rg = rs * N;
     L.rows_s = (int)(rs < RB ? rs : RB);
     L.rows_g = (int)(rg < RB ? rg : RB);
-    const size_t us = (size_t)S * Hkv * attn_blocks(rs, RB) + ncta;
+    const size_t us = G ? (size_t)S * Hkv * attn_blocks(rs, RB) + ncta : 2 * (size_t)ncta;
     const size_t ug = G ? G * Hkv * attn_blocks(rg, RB) + ncta : 0;
     L.slot_s = o;
     o = align256(o + us * L.rows_s * D * 4);
@@ -93,7 +105,10 @@ struct AttnParams {
     float* lse;
     void* ws;
     AttnLayout L;
-    int tile, rb, ncta_max, min_tiles;
+    int log_tile, log_rb;  // keys of a tile, rows of a block
+    int ncta_max;
+    FastDiv div_gq, div_cta;
+    bool planned;  // by the planning kernel
 };
 
 __device__ __forceinline__ AttnHead* attn_head(const AttnParams& p) { return static_cast<AttnHead*>(p.ws); }
@@ -122,19 +137,36 @@ __device__ __forceinline__ int attn_ctx(const AttnParams& p, int s, int n) {
     return c;
 }
 
-__device__ __forceinline__ int attn_cut(const AttnHead* h, int c) { return h->base * c + min(c, h->rest); }
-__device__ __forceinline__ int attn_cta_of(const AttnHead* h, int x) {
-    const int first = h->rest * (h->base + 1);  // tiles of the longer shares
-    return x < first ? x / (h->base + 1) : h->rest + (x - first) / h->base;
+struct AttnCut {  // W = ncta * base + rest
+    int base, rest, ncta;
+    __device__ __forceinline__ AttnCut() {}
+    __device__ __forceinline__ AttnCut(const AttnParams& p, int W) {
+        ncta = min(p.ncta_max, W);
+        base = W < p.ncta_max ? 1 : (int)fast_div((uint32_t)W, p.div_cta);
+        rest = W - base * ncta;
+    }
+    __device__ __forceinline__ int of(int c) const { return base * c + min(c, rest); }  // first tile of block c
+    __device__ __forceinline__ int block(int x) const {                                 // of tile x
+        const int first = rest * (base + 1);  // tiles of the longer shares
+        return x < first ? x / (base + 1) : rest + (x - first) / base;
+    }
+};
+
+// Row blocks of an item, and its units.
+__device__ __forceinline__ int attn_units(const AttnParams& p, AttnItem& it) {
+    const int rows = it.nodes * p.gq, rb = 1 << p.log_rb;
+    it.nrb = max(1, (rows + rb - 1) >> p.log_rb);
+    it.per = max(1, min(rows, rb));
+    if (it.nodes == 0 || it.tiles < 0) it.tiles = 0;
+    return it.tiles > 0 ? p.Hkv * it.nrb : 0;
 }
 
-// A warp's search: the last of items [first, first + n) whose key is at most x (the first one's is), 32 at a time. With
-// keys that rise along the line it is the one that x lies in, as items without tiles come before it.
-template <typename Key>
-__device__ __forceinline__ int attn_search(const AttnItem* items, int first, int n, int x, int lane, Key key) {
+// A warp's search: the item that tile x of the line lies in, 32 at a time (the last one that begins at or before it: items
+// without tiles come before the one that has them).
+__device__ __forceinline__ int attn_search(const AttnItem* items, int first, int n, int x, int lane) {
     while (n > 1) {
         const int step = (n + 31) / 32;
-        const bool below = lane * step < n && key(items[first + lane * step]) <= x;
+        const bool below = lane * step < n && __ldcg(&items[first + lane * step].cum) <= x;
         const int k = max(0, __popc(__ballot_sync(0xffffffffu, below)) - 1);
         n = min(step, n - k * step);
         first += k * step;
@@ -142,45 +174,251 @@ __device__ __forceinline__ int attn_search(const AttnItem* items, int first, int
     return first;
 }
 
-// One piece of a unit, as a block walks along its share of the line.
-struct AttnPiece {
-    int node0, seq;        // first row of the item, page table row
-    int hkv, row0, rows;   // key/value head; rows of the item in this block of rows
-    int t0, t1;            // key tiles
-    bool own;              // holds the sequence's own keys (and nodes), not a group's shared ones
-    bool whole;            // all that its rows have to see: the result is written directly
-    float* o;              // its slot otherwise
+// One piece of a unit, as a block comes to it on its share of the line and hands it round in shared memory.
+struct PieceInfo {
+    float* o;  // its slot
     float2* ml;
+    int join, counter;       // pieces of the unit, joined by the last to arrive (0: none are); its first block, its counter
+    int node0, seq, hkv;     // first row of the item, page table row, key/value head
+    int row0, rows;          // rows of the item in this block of rows (none: there are no more pieces)
+    int t0, n;               // key tiles
+    int ctx;                 // tokens in the cache; INT_MAX for keys that a group shares
+    int nodes;
+    bool whole;              // all that its rows have to see: the result is written directly
+    __device__ __forceinline__ int keys() const { return ctx == INT_MAX ? INT_MAX : ctx + nodes; }
+    // first tile of `size` keys with a node or the end (n or more: none)
+    __device__ __forceinline__ int first_tail(int log_size) const { return ctx == INT_MAX ? n : (ctx >> log_size) - t0; }
 };
 
-__device__ __forceinline__ AttnPiece attn_piece(const AttnParams& p, const AttnItem& it, bool own, int x, int end, int cta,
-                                                int units_shared, int& next) {
-    AttnPiece c;
-    const int in = x - it.cum, u = in / it.tiles, t = in - u * it.tiles;
-    c.node0 = it.node0;
-    c.seq = it.seq;
-    c.hkv = u / it.nrb;
-    const int rb = u - c.hkv * it.nrb;
-    c.row0 = rb * it.per;
-    const int left = it.nodes * p.gq - c.row0;
-    c.rows = left < it.per ? left : it.per;
-    const int unit_end = x - t + it.tiles;
-    next = unit_end < end ? unit_end : end;
-    c.t0 = it.tile0 + t;
-    c.t1 = c.t0 + (next - x);
-    c.own = own;
-    c.whole = own && it.tile0 == 0 && t == 0 && next == unit_end;
-    const int unit = it.unit0 + u;
-    if (own) {
-        const size_t slot = (size_t)(unit - units_shared + cta);
-        c.o = ws_ptr<float>(p.ws, p.L.slot_s) + slot * p.L.rows_s * p.D;
-        c.ml = ws_ptr<float2>(p.ws, p.L.ml_s) + slot * p.L.rows_s;
-    } else {
-        const size_t slot = (size_t)(unit + cta);
-        c.o = ws_ptr<float>(p.ws, p.L.slot_g) + slot * p.L.rows_g * p.D;
-        c.ml = ws_ptr<float2>(p.ws, p.L.ml_g) + slot * p.L.rows_g;
+// A warp's walk along its block's share.
+struct Walker {
+    AttnCut cut;
+    int x, end, item_end;
+    int units_shared, ii;  // ii: number of the present item
+    AttnItem it;
+    // where the warp works the line out itself: 32 sequences at a time, one a lane
+    AttnItem mine;
+    int first, mine_end;  // the 32's first sequence, line after this lane's item
+
+    // this lane's item of the 32; its tiles on the line
+    __device__ __forceinline__ int load(const AttnParams& p, int lane) {
+        const int s = first + lane;
+        mine.nodes = mine.tiles = mine.node0 = 0;
+        if (s < p.S) {
+            mine.nodes = attn_nodes(p, s, mine.node0);
+            const int c = attn_ctx(p, s, mine.nodes);
+            if (c < 0) mine.nodes = 0;
+            mine.tiles = mine.nodes > 0 ? (c + mine.nodes + (1 << p.log_tile) - 1) >> p.log_tile : 0;
+        }
+        return attn_units(p, mine) * mine.tiles;
     }
-    return c;
+    __device__ __forceinline__ void place(int at, int size, int lane) {
+        int in = size;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, in, o);
+            if (lane >= o) in += t;
+        }
+        mine_end = at + in;
+        mine.cum = mine_end - size;
+    }
+
+    __device__ __forceinline__ void begin(const AttnParams& p, int lane) {
+        const int cta = blockIdx.x;
+        x = end = item_end = 0;
+        units_shared = 0;
+        if (p.planned) {
+            const AttnHead* h = attn_head(p);
+            cut.base = h->base;
+            cut.rest = h->rest;
+            units_shared = h->units_shared;
+            if (cta >= h->ncta) return;
+            x = item_end = cut.of(cta);
+            end = cut.of(cta + 1);
+            ii = attn_search(ws_ptr<AttnItem>(p.ws, p.L.item), 0, p.G + p.S, x, lane) - 1;
+            return;
+        }
+        int W = 0, size = 0;
+#pragma unroll 1
+        for (first = 0; first < p.S; first += 32) {
+            size = load(p, lane);
+            W += __reduce_add_sync(0xffffffffu, size);
+        }
+        first -= 32;
+        if (first == 0) {
+            place(0, size, lane);
+        } else {
+            first = -32;  // next_item begins with the first 32
+            mine_end = 0;
+        }
+        cut = AttnCut(p, W);
+        if (cta >= cut.ncta) return;
+        x = item_end = cut.of(cta);
+        end = cut.of(cta + 1);
+    }
+    __device__ __forceinline__ void next_item(const AttnParams& p, int lane) {
+        if (p.planned) {
+            it = ws_ptr<AttnItem>(p.ws, p.L.item)[++ii];
+        } else {
+            unsigned after;  // lanes whose items end behind x
+            while ((after = __ballot_sync(0xffffffffu, mine_end > x)) == 0) {
+                const int at = __shfl_sync(0xffffffffu, mine_end, 31);
+                first += 32;
+                const int size = load(p, lane);
+                place(at, size, lane);
+            }
+            const int l = __ffs(after) - 1;
+            it.node0 = __shfl_sync(0xffffffffu, mine.node0, l);
+            it.nodes = __shfl_sync(0xffffffffu, mine.nodes, l);
+            it.tiles = __shfl_sync(0xffffffffu, mine.tiles, l);
+            it.cum = __shfl_sync(0xffffffffu, mine.cum, l);
+            attn_units(p, it);
+            it.unit0 = 0;
+            it.tile0 = 0;
+            it.seq = ii = first + l;
+        }
+        item_end = it.cum + it.tiles * it.nrb * p.Hkv;
+    }
+    // The next piece; false (and no rows) after the last one.
+    __device__ __forceinline__ bool next(const AttnParams& p, PieceInfo& c, int lane) {
+        c.rows = 0;
+        if (x >= end) return false;
+        while (x >= item_end) next_item(p, lane);  // x is below W, so an item that holds it follows
+        const bool own = ii >= p.G;
+        const int in = x - it.cum, u = in / it.tiles, t = in - u * it.tiles, cta = blockIdx.x, units = it.nrb;
+        c.node0 = it.node0;
+        c.nodes = it.nodes;
+        c.seq = it.seq;
+        c.hkv = units == 1 ? u : u / units;
+        c.row0 = (u - c.hkv * units) * it.per;
+        c.rows = min(it.nodes * p.gq - c.row0, it.per);
+        const int unit_end = x - t + it.tiles, to = min(unit_end, end);
+        c.t0 = it.tile0 + t;
+        c.n = to - x;
+        c.whole = own && it.tile0 == 0 && c.n == it.tiles;
+        c.ctx = own ? __ldg(p.ctx_len + it.seq) : INT_MAX;
+        c.join = 0;
+        const int rows = own ? p.L.rows_s : p.L.rows_g;
+        float* o = ws_ptr<float>(p.ws, own ? p.L.slot_s : p.L.slot_g);
+        float2* ml = ws_ptr<float2>(p.ws, own ? p.L.ml_s : p.L.ml_g);
+        size_t slot = (size_t)(it.unit0 + u - (own ? units_shared : 0)) + cta;
+        if (p.G == 0) {
+            slot = 2 * cta + (t == 0);
+            if (!c.whole) {
+                c.counter = t == 0 ? cta : cut.block(x - t);
+                c.join = (to == unit_end ? cta : cut.block(unit_end - 1)) - c.counter + 1;
+            }
+        }
+        c.o = o + slot * rows * p.D;
+        c.ml = ml + slot * rows;
+        x = to;
+        return true;
+    }
+};
+
+__device__ __forceinline__ float attn_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float attn_lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Node and query head of row `row` of an item whose rows are those of key/value head hkv.
+__device__ __forceinline__ int attn_node(const AttnParams& p, int row) { return (int)fast_div((uint32_t)row, p.div_gq); }
+// log of a sum l of exp2(z - m)
+__device__ __forceinline__ float attn_lse(float m, float l) { return l == 0.0f ? kNegInf : (m + attn_lg2(l)) * 0.69314718056f; }
+template <int DT>
+__device__ __forceinline__ void attn_store4(void* base, size_t i, float4 v) {
+    if (DT == 0) {
+        *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = v;
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+}
+
+// Pieces of one row, joined one after the other.
+struct AttnJoin {
+    float m = kNegInf, l = 0.0f;
+    float4 acc = make_float4(0, 0, 0, 0);
+    __device__ __forceinline__ void add(float2 ml, float4 v) {
+        if (ml.y == 0.0f) return;  // saw nothing
+        const float mx = fmaxf(m, ml.x);
+        const float base = mx == kNegInf ? 0.0f : mx;
+        const float fa = l == 0.0f ? 0.0f : attn_ex2(m - base), fb = attn_ex2(ml.x - base);
+        l = l * fa + ml.y * fb;
+        acc.x = fmaf(acc.x, fa, v.x * fb);
+        acc.y = fmaf(acc.y, fa, v.y * fb);
+        acc.z = fmaf(acc.z, fa, v.z * fb);
+        acc.w = fmaf(acc.w, fa, v.w * fb);
+        m = mx;
+    }
+    template <int DT, int D>
+    __device__ __forceinline__ void store(const AttnParams& p, size_t orow, int col) const {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        attn_store4<DT>(p.out, orow * D + col, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        if (col == 0 && p.lse) p.lse[orow] = attn_lse(m, l);
+    }
+};
+
+// The block's threads, all of whose stores to the pieces' slots lie before a barrier: reports up to two pieces (a block's
+// first and last) and joins the units that they complete. `s_last` is shared; sync() a barrier of these threads.
+template <int DT, int D, int kRows, int kPieces, typename Sync>
+__device__ __forceinline__ void attn_join_last(const AttnParams& p, const PieceInfo* piece, int count, int tid, int threads,
+                                               volatile int* s_last, Sync sync) {
+    if (tid < count) {
+        unsigned* counter = ws_ptr<unsigned>(p.ws, p.L.count) + piece[tid].counter;
+        const bool last = atom_add_release(counter, 1u) == (unsigned)piece[tid].join - 1;
+        if (last) {
+            fence_acquire();
+            atomicExch(counter, 0u);
+        }
+        s_last[tid] = last;
+    }
+    sync();
+#pragma unroll 1
+    for (int k = 0; k < count; ++k) {
+        if (!s_last[k]) continue;
+        const PieceInfo c = piece[k];
+        const float* o = ws_ptr<float>(p.ws, p.L.slot_s);
+        const float2* ml = ws_ptr<float2>(p.ws, p.L.ml_s);
+        // kRows rows and kPieces pieces a thread at a time, to have enough loads in flight
+        const int step = threads / (D / 4), col = (tid % (D / 4)) * 4;
+#pragma unroll 1
+        for (int r0 = tid / (D / 4); r0 < c.rows; r0 += kRows * step) {
+            AttnJoin j[kRows];
+#pragma unroll 1
+            for (int x0 = 0; x0 < c.join; x0 += kPieces) {
+                float2 s[kPieces][kRows];
+                float4 v[kPieces][kRows];
+#pragma unroll
+                for (int x = 0; x < kPieces; ++x) {
+                    const int k = min(x0 + x, c.join - 1);
+                    const size_t slot = 2 * (size_t)(c.counter + k) + (k == 0);
+#pragma unroll
+                    for (int y = 0; y < kRows; ++y) {
+                        const size_t at = slot * p.L.rows_s + min(r0 + y * step, c.rows - 1);
+                        s[x][y] = __ldcg(ml + at);
+                        v[x][y] = __ldcg(reinterpret_cast<const float4*>(o + at * D + col));
+                        if (x0 + x >= c.join) s[x][y].y = 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < kPieces; ++x)
+#pragma unroll
+                    for (int y = 0; y < kRows; ++y) j[y].add(s[x][y], v[x][y]);
+            }
+#pragma unroll
+            for (int y = 0; y < kRows; ++y) {
+                const int r = r0 + y * step, row = c.row0 + r, node = attn_node(p, row);
+                if (r < c.rows) j[y].store<DT, D>(p, (size_t)(c.node0 + node) * p.Hq + c.hkv * p.gq + (row - node * p.gq), col);
+            }
+        }
+    }
 }
 
 // Whether node t (of the sequence whose first row is row0) sees node j.

@@ -1,6 +1,6 @@
 // attn_tc.cuh -- what the two tensor-core kernels of tree_attention share: tcgen05 / TMA / mbarrier
-// instructions, bounded waits, the walk along a block's share of the line, the warp that brings the pages
-// of keys and values into the ring, the masks of a tile's positions, and the tensor maps.
+// instructions, bounded waits, the pieces of a block's share handed round, the warps that bring the pages of keys
+// and values into their rings, the masks of a tile's positions, and the tensor maps.
 #pragma once
 
 #include <cuda.h>
@@ -100,11 +100,7 @@ __device__ __forceinline__ void st32(uint32_t addr, const uint32_t* r) {
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+__device__ __forceinline__ float ex2(float x) { return attn_ex2(x); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -165,45 +161,35 @@ __device__ __forceinline__ void wait(const Ctl& c, uint32_t bar, uint32_t parity
     __syncwarp();
 }
 
-// The pieces of a block's share, walked alike by all of its warps.
-struct Walk {
-    int x, end, item_end;
-    int ii, units_shared;
-    const AttnItem* items;
-    AttnItem it;
+// The pieces of a block's share as one warp hands them to the others. The walker is at most three pieces ahead of the
+// slowest reader (both kernels say why), so a place is free when it comes round again.
+constexpr int kPieces = 4;
+struct PieceRing {
+    PieceInfo piece[kPieces];
+    PieceInfo pending[2];  // cut units' pieces, to be reported at the end
+    uint64_t full[kPieces];
+    int last[2];
+    __device__ __forceinline__ void init() {
+        for (int i = 0; i < kPieces; ++i) mbar_init(smem_u32(&full[i]), 1);
+    }
+    // one warp
+    __device__ __forceinline__ void put(uint32_t i, const PieceInfo& c, int lane) {
+        if (lane == 0) {
+            piece[i % kPieces] = c;
+            mbar_arrive(smem_u32(&full[i % kPieces]));
+        }
+        __syncwarp();
+    }
+    // The i-th piece, as the other warps see it (no rows after a wait that ran out).
+    __device__ __forceinline__ PieceInfo get(const Ctl& ctl, uint32_t i) {
+        wait(ctl, smem_u32(&full[i % kPieces]), (i / kPieces) & 1);
+        PieceInfo c = piece[i % kPieces];
+        if (*reinterpret_cast<volatile int*>(ctl.abort)) c.rows = 0;
+        c.rows = uniform(c.rows);
+        c.n = uniform(c.n);
+        return c;
+    }
 };
-// One warp: the item that the block's first tile lies in.
-__device__ __forceinline__ int walk_start(const AttnParams& p, int lane) {
-    const AttnHead* h = attn_head(p);
-    if ((int)blockIdx.x >= h->ncta) return 0;
-    return attn_search(ws_ptr<AttnItem>(p.ws, p.L.item), 0, p.G + p.S, attn_cut(h, blockIdx.x), lane,
-                       [](const AttnItem& a) { return __ldcg(&a.cum); });
-}
-__device__ __forceinline__ Walk walk_begin(const AttnParams& p, int start) {
-    const AttnHead* h = attn_head(p);
-    const int cta = blockIdx.x;
-    Walk w;
-    w.units_shared = h->units_shared;
-    w.items = ws_ptr<AttnItem>(p.ws, p.L.item);
-    w.ii = start - 1;
-    w.x = w.end = w.item_end = 0;
-    if (cta < h->ncta) {
-        w.x = w.item_end = attn_cut(h, cta);
-        w.end = attn_cut(h, cta + 1);
-    }
-    return w;
-}
-__device__ __forceinline__ bool walk_next(const AttnParams& p, Walk& w, AttnPiece& c) {
-    if (w.x >= w.end) return false;
-    while (w.x >= w.item_end) {  // x is below W, so an item that holds it follows
-        w.it = w.items[++w.ii];
-        w.item_end = w.it.cum + w.it.tiles * w.it.nrb * p.Hkv;
-    }
-    int next;
-    c = attn_piece(p, w.it, w.ii >= p.G, w.x, w.end, blockIdx.x, w.units_shared, next);
-    w.x = next;
-    return true;
-}
 
 // After a wait that ran out: gives copies and products in flight time to land before the block's shared and
 // tensor memory is handed on.
@@ -217,6 +203,16 @@ template <int kThreads>
 __device__ __forceinline__ void rows_sync() {
     __syncwarp();
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
+// Whether any thread of them says yes.
+template <int kThreads>
+__device__ __forceinline__ bool rows_any(bool yes) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, 1, %2, q;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)yes), "n"(kThreads)
+                 : "memory");
+    return r != 0;
 }
 
 // ---- keys and values ----
@@ -237,17 +233,19 @@ struct Ring {
 // page id (a box: up to 128 positions of one page); 32 ids are read at a time, the next 32 while these are used. The
 // copies are issued by one thread with the ids handed round four at a time: lanes issuing a copy each take turns
 // anyway, at four times the cost. Pages past the end are not read.
-template <int D, int kStages>
+template <int D>
 struct Filler {
     using T = TileGeo<D>;
     const CUtensorMap* map;
-    Ring<kStages>* rg;
-    uint32_t ring, st, round;
-    __device__ __forceinline__ Filler(const CUtensorMap* m, Ring<kStages>* r, uint32_t addr) : map(m), rg(r), ring(addr), st(0), round(0) {}
-    // tiles t0 .. t1 - 1 of one head of a sequence with `keys` positions; false after a wait that ran out
-    __device__ __forceinline__ bool fill(const AttnParams& p, const Ctl& ctl, int seq, int hkv, int t0, int t1, int keys, int lane) {
+    uint64_t *full, *empty;
+    uint32_t stages, ring, st, round;
+    __device__ __forceinline__ Filler(const CUtensorMap* m, uint64_t* f, uint64_t* e, int n, uint32_t addr)
+        : map(m), full(f), empty(e), stages(n), ring(addr), st(0), round(0) {}
+    // the tiles of a piece; false after a wait that ran out
+    __device__ __forceinline__ bool fill(const AttnParams& p, const Ctl& ctl, const PieceInfo& c, int lane) {
+        const int hkv = c.hkv, t0 = c.t0, t1 = c.t0 + c.n, keys = c.keys();
         const int box_shift = p.page_shift < 7 ? p.page_shift : 7, box = 1 << box_shift, nbox = kTile >> box_shift;
-        const int32_t* row = p.table + (long long)seq * p.pages_per_seq;
+        const int32_t* row = p.table + (long long)c.seq * p.pages_per_seq;
         const int last = (int)min((long long)t1 * kTile, (long long)keys);  // end of the positions
         auto ids = [&](int batch) {  // of the 32 boxes from 32 * batch on
             const int pos = t0 * kTile + ((32 * batch + lane) << box_shift);
@@ -267,10 +265,10 @@ struct Filler {
                 id = next;
                 next = ids(++batch);
             }
-            if (round > 0) wait(ctl, smem_u32(&rg->empty[st]), (round - 1) & 1);
+            if (round > 0) wait(ctl, smem_u32(&empty[st]), (round - 1) & 1);
             if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(ctl.abort))) return false;
             const int ust = uniform(st), boxes = uniform(min(nbox, (last - t * kTile + box - 1) >> box_shift));
-            const uint32_t bar = smem_u32(&rg->full[ust]);
+            const uint32_t bar = smem_u32(&full[ust]);
             uint32_t to = ring + ust * T::kBytes;
             const int at = uniform((hkv * p.page_size + ((t * kTile) & (p.page_size - 1))) >> 3);
             if (elect_one()) mbar_expect_tx(bar, (uint32_t)(boxes * bytes));
@@ -286,7 +284,7 @@ struct Filler {
                         if (b + y < boxes) tma_page(to + y * bytes, map, at, page[y], bar);
                 }
             }
-            if (++st == kStages) st = 0, ++round;
+            if (++st == stages) st = 0, ++round;
         }
         return true;
     }
@@ -386,7 +384,7 @@ cudaError_t launch_tc(Kernel kern, int threads, int smem, const AttnParams& p, c
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.planned ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, p, mk, mv);
 }
 

@@ -201,14 +201,17 @@ extern "C" int tree_attention(const void* q, long long q_stride, const void* k_c
                             (long long)p.G * Hkv * attn_blocks((long long)N * T * p.gq, rows_of(kind));
     if (units * (((long long)pages_per_seq * page_size + 63) / 64) > 0x7fffffffLL) return SMCSD_ERR_INVALID_ARG;
     p.L = layout_of(kind, S, N, T, Hq, Hkv, D);
-    p.tile = kind == kSimt ? 64 : 128;
-    p.rb = rows_of(kind);
+    p.log_tile = kind == kSimt ? 6 : 7;
+    p.log_rb = kind == kSimt ? 4 : kind == kNarrow ? 7 : 8;
+    p.div_gq = make_fastdiv((uint32_t)p.gq);
     p.ncta_max = device_sm_count() * (kind == kSimt ? kSimtBlocksPerSm : 1);
     if (p.ncta_max > kAttnMaxCta) p.ncta_max = kAttnMaxCta;
-    p.min_tiles = 1;
-    cudaError_t e = launch_attn_plan(p, st);
-    if (e == cudaSuccess) e = kind == kSimt ? launch_attn_simt(p, st) : kind == kNarrow ? launch_attn_narrow(p, st) : launch_attn_wide(p, st);
-    if (e == cudaSuccess) e = launch_attn_combine(p, dtype, st);
+    p.div_cta = make_fastdiv((uint32_t)p.ncta_max);
+    p.planned = p.G > 0 || S > kAttnWarpPlan;
+    cudaError_t e = p.planned ? launch_attn_plan(p, st) : cudaSuccess;
+    if (e == cudaSuccess)
+        e = kind == kSimt ? launch_attn_simt(p, st) : kind == kNarrow ? launch_attn_narrow(p, st) : launch_attn_wide(p, st);
+    if (e == cudaSuccess && p.G > 0) e = launch_attn_combine(p, dtype, st);
     return from_cuda(e);
 }
 

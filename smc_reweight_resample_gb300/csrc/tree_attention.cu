@@ -58,12 +58,8 @@ __device__ __forceinline__ AttnItem plan_item(const AttnParams& p, const int* sh
         const int c = attn_ctx(p, it.seq, it.nodes);
         if (c < 0) it.nodes = 0;
         it.tile0 = p.G > 0 ? __ldcg(shared + it.seq / p.N) : 0;
-        it.tiles = it.nodes > 0 ? (c + it.nodes + p.tile - 1) / p.tile - it.tile0 : 0;
+        it.tiles = it.nodes > 0 ? ((c + it.nodes + (1 << p.log_tile) - 1) >> p.log_tile) - it.tile0 : 0;
     }
-    const int rows = it.nodes * p.gq;
-    it.nrb = max(1, attn_blocks(rows, p.rb));
-    it.per = max(1, min(rows, p.rb));
-    if (it.nodes == 0 || it.tiles < 0) it.tiles = 0;
     it.pad[0] = it.pad[1] = it.pad[2] = 0;
     return it;
 }
@@ -94,7 +90,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         }
         __syncthreads();
         if (tid == 0) {
-            shared[blockIdx.x] = (int)(((long long)best << p.page_shift) / p.tile);
+            shared[blockIdx.x] = (int)(((long long)best << p.page_shift) >> p.log_tile);
             const unsigned old = atom_add_release(&attn_head(p)->done, 1u);
             last = old == gridDim.x - 1;
             if (last) {
@@ -109,34 +105,31 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     AttnItem* items = ws_ptr<AttnItem>(p.ws, p.L.item);
     const int n = p.G + p.S, per = (n + kPlanThreads - 1) / kPlanThreads;
     const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    auto size_of = [&](const AttnItem& it) {
-        const long long u = it.tiles > 0 ? (long long)p.Hkv * it.nrb : 0;
-        return ((u * it.tiles) << 32) + u;
-    };
     AttnItem it;
     long long mine = 0, total;
     for (int i = i0; i < i1; ++i) {
         it = plan_item(p, shared, i);
-        mine += size_of(it);
+        const long long u = attn_units(p, it);
+        mine += ((u * it.tiles) << 32) + u;
     }
     long long at = plan_prefix(mine, sums, total);
     for (int i = i0; i < i1; ++i) {
         if (per > 1) it = plan_item(p, shared, i);
+        const long long u = attn_units(p, it);
         it.cum = (int)(at >> 32);
         it.unit0 = (int)(at & 0xffffffffll);
         items[i] = it;
-        at += size_of(it);
+        at += ((u * it.tiles) << 32) + u;
         if (i == p.G - 1) attn_head(p)->units_shared = (int)(at & 0xffffffffll);
     }
     if (tid == 0) {
         AttnHead* h = attn_head(p);
         const int W = (int)(total >> 32);
-        const int cta = min(p.ncta_max, (W + p.min_tiles - 1) / p.min_tiles);
+        const AttnCut cut(p, W);
         if (p.G == 0) h->units_shared = 0;
-        h->units = (int)(total & 0xffffffffll);
-        h->ncta = cta;
-        h->base = cta > 0 ? W / cta : 0;
-        h->rest = cta > 0 ? W % cta : 0;
+        h->ncta = cut.ncta;
+        h->base = cut.base;
+        h->rest = cut.rest;
     }
 }
 
@@ -179,26 +172,26 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_wait();
     griddep_launch_dependents();
-    const AttnHead* h = attn_head(p);
-    const int cta = blockIdx.x;
-    if (cta >= h->ncta) return;
-    const AttnItem* items = ws_ptr<AttnItem>(p.ws, p.L.item);
-    int x = attn_cut(h, cta);
-    const int end = attn_cut(h, cta + 1);
-    const int n_items = p.G + p.S;
-    while (x < end) {
-        const int ii = attn_search(items, 0, n_items, x, lane, [](const AttnItem& a) { return __ldcg(&a.cum); });
-        const AttnItem it = items[ii];
-        int next;
-        const AttnPiece c = attn_piece(p, it, ii >= p.G, x, end, cta, h->units_shared, next);
-        x = next;
-        const int ctx = c.own ? __ldg(p.ctx_len + c.seq) : INT_MAX;
-        const int keys = c.own ? ctx + it.nodes : INT_MAX;  // positions that exist
+    __shared__ PieceInfo s_piece, s_pending[2];
+    __shared__ int s_last[2];
+    int pending = 0;
+    Walker walk;
+    if (warp == 0) walk.begin(p, lane);
+    for (;;) {
+        if (warp == 0) {
+            PieceInfo c;
+            walk.next(p, c, lane);
+            if (lane == 0) s_piece = c;
+        }
+        __syncthreads();
+        const PieceInfo c = s_piece;
+        if (c.rows == 0) break;
+        const int ctx = c.ctx, keys = c.keys();  // positions that exist
         for (int i = tid; i < kSimtRows * kV4; i += kSimtThreads) {
             const int r = i / kV4, d = (i - r * kV4) * 4;
             float4 v = make_float4(0, 0, 0, 0);
             if (r < c.rows) {
-                const int row = c.row0 + r, node = row / p.gq, hq = c.hkv * p.gq + (row - node * p.gq);
+                const int row = c.row0 + r, node = attn_node(p, row), hq = c.hkv * p.gq + (row - node * p.gq);
                 v = load4(p.q, (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + d);
             }
             *reinterpret_cast<float4*>(sq + r * D + d) = v;
@@ -208,7 +201,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
 #pragma unroll
         for (int r = 0; r < kHold; ++r) acc[r] = 0.0f;
         const int col = tid % D, vr0 = (tid / D) * kHold;
-        for (int t = c.t0; t < c.t1; ++t) {
+        for (int t = c.t0; t < c.t0 + c.n; ++t) {
             const int pos0 = t * kSimtKeys;
             __syncthreads();
             for (int i = tid; i < kSimtKeys * kV4; i += kSimtThreads) {
@@ -244,7 +237,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
                 const int row = c.row0 + r0 + r;
                 bool sees = r0 + r < c.rows && pos < keys;
                 if (sees && pos >= ctx) {
-                    const int node = row / p.gq;
+                    const int node = attn_node(p, row);
                     sees = attn_sees(p, c.node0 + node, node, pos - ctx);
                 }
                 sp[key * kP + r0 + r] = sees ? z[r] * p.scale2 : kNegInf;
@@ -299,19 +292,24 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
         for (int r = 0; r < kHold; ++r) {
             const int rr = vr0 + r;
             if (rr >= c.rows) break;
-            const int row = c.row0 + rr, node = row / p.gq, hq = c.hkv * p.gq + (row - node * p.gq);
+            const int row = c.row0 + rr, node = attn_node(p, row), hq = c.hkv * p.gq + (row - node * p.gq);
             const size_t orow = (size_t)(c.node0 + node) * p.Hq + hq;
             const float l = sm_l[rr], m = sm_m[rr];
             if (c.whole) {
                 static_cast<float*>(p.out)[orow * D + col] = l == 0.0f ? 0.0f : acc[r] / l;
-                if (col == 0 && p.lse) p.lse[orow] = l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718056f;
+                if (col == 0 && p.lse) p.lse[orow] = attn_lse(m, l);
             } else {
                 c.o[(size_t)rr * D + col] = acc[r];
                 if (col == 0) c.ml[rr] = make_float2(m, l);
             }
         }
+        if (c.join > 0) {
+            if (tid == 0) s_pending[pending] = c;
+            ++pending;
+        }
         __syncthreads();
     }
+    if (pending > 0) attn_join_last<0, D, 2, 4>(p, s_pending, pending, tid, kSimtThreads, s_last, [] { __syncthreads(); });
 }
 
 template <int D>
@@ -329,7 +327,7 @@ static cudaError_t launch_simt_t(const AttnParams& p, cudaStream_t st) {
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.planned ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -338,111 +336,63 @@ cudaError_t launch_attn_simt(const AttnParams& p, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------------------
-// joining the pieces
+// joining the pieces of groups
 // ------------------------------------------------------------------------------------------
 
-constexpr int kJoinThreads = 256;  // a unit's rows are dealt to gridDim.z blocks
+constexpr int kJoinThreads = 256;
 
-template <int DT>
-__device__ __forceinline__ void store4(void* base, size_t i, float4 v) {
-    if (DT == 0) {
-        *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = v;
-    } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + i) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    }
-}
-
-// The pieces of one row: slots c0 .. c1 of a unit, row r of each.
+// The slots of one row's pieces of a unit.
 struct JoinRun {
     const float* o;
     const float2* ml;
-    size_t step_o, step_ml;  // from one piece to the next
+    size_t rows;  // of a slot
     int count;
+    template <int D>
+    __device__ __forceinline__ void add_to(AttnJoin& j, int col) const {
+#pragma unroll 4
+        for (int i = 0; i < count; ++i)
+            j.add(__ldcg(ml + i * rows), __ldcg(reinterpret_cast<const float4*>(o + i * rows * D + col)));
+    }
 };
 
-// A few blocks for each unit that was cut (found from the cuts: the first one inside a unit answers for it) or, where
-// groups share keys, for each own unit. A row's pieces are joined in the order of the line, the shared unit's
-// first: 4 columns a thread.
+// Where groups share keys: a few blocks (z) for each sequence (x) and unit of it (y). A row's pieces are joined in the
+// order of the line, the shared unit's first: 4 columns a thread.
 template <int DT, int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid_constant__ AttnParams p) {
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const AttnHead* h = attn_head(p);
     const AttnItem* items = ws_ptr<AttnItem>(p.ws, p.L.item);
-    const int n = p.G + p.S;
-    // the unit: item `it`, number u of its units
-    AttnItem it;
-    int u;
-    if (p.G == 0) {
-        const int cut = blockIdx.x + 1;  // the last block has none
-        if (cut >= h->ncta) return;
-        const int x = attn_cut(h, cut);
-        it = items[attn_search(items, 0, n, x, lane, [](const AttnItem& a) { return __ldcg(&a.cum); })];
-        u = (x - it.cum) / it.tiles;
-        const int x0 = it.cum + u * it.tiles;
-        if (x == x0 || attn_cut(h, cut - 1) > x0) return;  // between units, or not the first cut inside
-    } else {
-        it = items[p.G + blockIdx.x];
-        u = blockIdx.y;
-        if (it.tiles == 0 || u >= p.Hkv * it.nrb) return;
-    }
+    AttnCut cut;
+    cut.base = h->base;
+    cut.rest = h->rest;
+    const AttnItem it = items[p.G + blockIdx.x], grp = items[blockIdx.x / p.N];
+    const int u = blockIdx.y;
+    if (it.tiles == 0 || u >= p.Hkv * it.nrb) return;
     const int hkv = u / it.nrb, row0 = (u - hkv * it.nrb) * it.per, rows = min(it.per, it.nodes * p.gq - row0);
-    JoinRun own, sh{};
-    {
-        const int x0 = it.cum + u * it.tiles, c0 = attn_cta_of(h, x0);
-        const size_t slot = (size_t)(it.unit0 + u - h->units_shared + c0);
-        own.count = attn_cta_of(h, x0 + it.tiles - 1) - c0 + 1;
-        own.step_o = (size_t)p.L.rows_s * D;
-        own.step_ml = p.L.rows_s;
-        own.o = ws_ptr<float>(p.ws, p.L.slot_s) + slot * own.step_o;
-        own.ml = ws_ptr<float2>(p.ws, p.L.ml_s) + slot * own.step_ml;
-    }
-    AttnItem grp;
-    if (p.G > 0) grp = items[it.seq / p.N];
-    const bool shared = p.G > 0 && grp.tiles > 0;
-    if (!shared && own.count == 1) return;  // written directly
+    const int x0 = it.cum + u * it.tiles, c0 = cut.block(x0), own_count = cut.block(x0 + it.tiles - 1) - c0 + 1;
+    const size_t own_slot = (size_t)(it.unit0 + u - h->units_shared + c0);
+    const bool shared = grp.tiles > 0;
+    if (!shared && own_count == 1) return;  // written directly
     constexpr int kLanes = D / 4, kRows = 32 / kLanes;  // lanes of a row, rows of a warp at a time
     const int col = (lane % kLanes) * 4;
     const int step = gridDim.z * (kJoinThreads / 32) * kRows;
     for (int r = (blockIdx.z * (kJoinThreads / 32) + warp) * kRows + lane / kLanes; r < rows; r += step) {
-        const int row = row0 + r, node = it.node0 + row / p.gq, hq = hkv * p.gq + row % p.gq;
+        const int row = row0 + r, n = attn_node(p, row);
+        AttnJoin j;
+        JoinRun run;
         if (shared) {
             const int gr = row + (it.node0 - grp.node0) * p.gq, rb = gr / grp.per, gu = hkv * grp.nrb + rb;
-            const int x0 = grp.cum + gu * grp.tiles, c0 = attn_cta_of(h, x0);
-            const size_t slot = (size_t)(grp.unit0 + gu + c0);
-            sh.count = attn_cta_of(h, x0 + grp.tiles - 1) - c0 + 1;
-            sh.step_o = (size_t)p.L.rows_g * D;
-            sh.step_ml = p.L.rows_g;
-            sh.o = ws_ptr<float>(p.ws, p.L.slot_g) + slot * sh.step_o + (size_t)(gr - rb * grp.per) * D;
-            sh.ml = ws_ptr<float2>(p.ws, p.L.ml_g) + slot * sh.step_ml + (gr - rb * grp.per);
+            const int g0 = grp.cum + gu * grp.tiles, b0 = cut.block(g0);
+            const size_t at = (size_t)(grp.unit0 + gu + b0) * p.L.rows_g + (gr - rb * grp.per);
+            run = JoinRun{ws_ptr<float>(p.ws, p.L.slot_g) + at * D, ws_ptr<float2>(p.ws, p.L.ml_g) + at, (size_t)p.L.rows_g,
+                          cut.block(g0 + grp.tiles - 1) - b0 + 1};
+            run.add_to<D>(j, col);
         }
-        float m = kNegInf, l = 0.0f;
-        float4 acc = make_float4(0, 0, 0, 0);
-        auto join = [&](const JoinRun& j, int r) {
-#pragma unroll 4
-            for (int i = 0; i < j.count; ++i) {
-                const float2 ml = __ldcg(j.ml + i * j.step_ml + r);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(j.o + i * j.step_o + (size_t)r * D + col));
-                if (ml.y == 0.0f) continue;  // saw nothing
-                const float mx = fmaxf(m, ml.x);
-                const float base = mx == kNegInf ? 0.0f : mx;
-                const float fa = l == 0.0f ? 0.0f : exp2f(m - base), fb = exp2f(ml.x - base);
-                l = l * fa + ml.y * fb;
-                acc.x = fmaf(acc.x, fa, v.x * fb);
-                acc.y = fmaf(acc.y, fa, v.y * fb);
-                acc.z = fmaf(acc.z, fa, v.z * fb);
-                acc.w = fmaf(acc.w, fa, v.w * fb);
-                m = mx;
-            }
-        };
-        if (shared) join(sh, 0);
-        join(own, r);
-        const size_t orow = (size_t)node * p.Hq + hq;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        store4<DT>(p.out, orow * D + col, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-        if (col == 0 && p.lse) p.lse[orow] = l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718056f;
+        const size_t at = own_slot * p.L.rows_s + r;
+        run = JoinRun{ws_ptr<float>(p.ws, p.L.slot_s) + at * D, ws_ptr<float2>(p.ws, p.L.ml_s) + at, (size_t)p.L.rows_s, own_count};
+        run.add_to<D>(j, col);
+        j.store<DT, D>(p, (size_t)(it.node0 + n) * p.Hq + hkv * p.gq + (row - n * p.gq), col);
     }
 }
 
@@ -450,9 +400,9 @@ template <int DT, int D>
 static cudaError_t launch_combine_t(const AttnParams& p, cudaStream_t st) {
     // a block's eight warps take up to four rows each
     const long long rows = (long long)p.T * p.gq;
-    const unsigned parts = (unsigned)((rows < p.rb ? rows : p.rb) + 31) / 32;
+    const unsigned parts = (unsigned)((rows < (1 << p.log_rb) ? rows : (1 << p.log_rb)) + 31) / 32;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = p.G > 0 ? dim3((unsigned)p.S, (unsigned)(p.Hkv * attn_blocks(rows, p.rb)), parts) : dim3((unsigned)p.ncta_max, 1, parts);
+    cfg.gridDim = dim3((unsigned)p.S, (unsigned)(p.Hkv * attn_blocks(rows, 1 << p.log_rb)), parts);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at{};

@@ -10,9 +10,9 @@
 //               memory. With up to 32 rows the groups take four tiles at a time, with up to 64 two tiles in
 //               two halves of the rows, above one tile in quarters: group w always has columns 32 w .. 32 w + 31
 //               of the 128 that scores, weights and outputs have.
-//   warp 16     walks along the block's share, hands the pieces round in shared memory, brings their query rows (two
-//               places of 64 rows, or one of 128) and the pages of keys (attn_tc.cuh)
-//   warp 18     brings the pages of values
+//   warp 16     walks along the block's share, hands the pieces round in shared memory and brings the pages of keys
+//               (attn_tc.cuh)
+//   warp 18     brings the query rows (two places of 64 rows, or one of 128) and the pages of values
 //   warps 17 and 19  issue S^T and O^T: one warp for both has more to issue than a tile's bytes take. Scores have two
 //               buffers, so those of the next round of tiles are there when a group comes to them, and those of the next
 //               piece while this one is written out
@@ -42,29 +42,12 @@ struct NarrowGeo {
     static constexpr int kSmem = 1024 + kStage + kWeights + (kKeys + kValues) * kStage;
 };
 
-// A piece (attn_plan.cuh) as it is handed round.
-struct PieceInfo {
-    float* o;
-    float2* ml;
-    int node0, seq, hkv, row0;
-    int rows;  // 0: there are no more
-    int t0, n; // key tiles
-    int ctx;   // tokens in the cache; INT_MAX for keys that a group shares
-    int nodes;
-    bool whole;
-    __device__ __forceinline__ int keys() const { return ctx == INT_MAX ? INT_MAX : ctx + nodes; }
-    // first tile with a node or the end (n or more: none)
-    __device__ __forceinline__ int first_tail() const { return ctx == INT_MAX ? n : (ctx >> 7) - t0; }
-};
-constexpr int kPieces = 4;
-
 template <int D>
 struct __align__(16) NarrowShared {
     __align__(16) float m[kTile];  // references, read four at a time
-    __align__(16) PieceInfo piece[kPieces];
+    PieceRing pieces;
     Ring<NarrowGeo<D>::kKeys> rk;
     Ring<NarrowGeo<D>::kValues> rv;
-    uint64_t piece_full[kPieces];
     uint64_t q_full[2], q_empty[2], v_full[2];
     uint64_t s_full[4][2], o_full[4][2];  // [tile of a round][buffer]
     uint64_t p_full[4][2];                // [group][buffer]
@@ -72,17 +55,6 @@ struct __align__(16) NarrowShared {
     int abort;
     int poison[2];  // by the piece's parity: a NaN or infinity among the values of its nodes
 };
-
-// The i-th piece, as all warps but the one that walks see it (no rows after a wait that ran out).
-template <int D>
-__device__ __forceinline__ PieceInfo next_piece(const Ctl& ctl, NarrowShared<D>* sh, uint32_t i) {
-    wait(ctl, smem_u32(&sh->piece_full[i % kPieces]), (i / kPieces) & 1);
-    PieceInfo c = sh->piece[i % kPieces];
-    if (*reinterpret_cast<volatile int*>(ctl.abort)) c.rows = 0;
-    c.rows = uniform(c.rows);
-    c.n = uniform(c.n);
-    return c;
-}
 
 // Places of the query rows: a piece of up to 64 rows takes the next of the two, a larger one both.
 struct QuerySlots {
@@ -135,79 +107,61 @@ struct Uses {
     }
 };
 
-// ---- pieces, query rows and keys ----
+// ---- pieces, keys, query rows and values ----
 
+// Two warps in one piece of code (it is long): the one with `keys` walks and brings the pages of keys, the other the query
+// rows and the pages of values.
 template <int D>
-__device__ void narrow_walk(const AttnParams& p, const CUtensorMap* mk, const Ctl& ctl, NarrowShared<D>* sh, uint32_t sq, uint32_t ring_k,
-                            int lane) {
+__device__ void narrow_fill(const AttnParams& p, bool keys, const CUtensorMap* map, const Ctl& ctl, NarrowShared<D>* sh, uint32_t sq,
+                            uint32_t ring, int lane) {
     using G = NarrowGeo<D>;
-    Walk w = walk_begin(p, walk_start(p, lane));
-    AttnPiece c;
+    Filler<D> filler(map, keys ? sh->rk.full : sh->rv.full, keys ? sh->rk.empty : sh->rv.empty, keys ? G::kKeys : G::kValues, ring);
     QuerySlots qs;
-    Filler<D, G::kKeys> keys(mk, &sh->rk, ring_k);
+    Walker walk;
+    if (keys) walk.begin(p, lane);
+#pragma unroll 1
     for (uint32_t i = 0;; ++i) {
-        const bool more = walk_next(p, w, c);
-        if (!more) c.rows = 0;
-        qs.take(c.rows);
-        // Once the scores that read this place last are done, everybody is past piece i - 4 (the scores of a piece wait
-        // for all weights of the one before), and its description may be written over.
-        qs.each([&](int x, uint32_t uses) {
-            if (uses > 0) wait(ctl, smem_u32(&sh->q_empty[x]), (uses - 1) & 1);
-        });
-        const int ctx = more && c.own ? __ldg(p.ctx_len + c.seq) : INT_MAX;
-        if (lane == 0) {
-            PieceInfo* to = &sh->piece[i % kPieces];
-            to->o = c.o;
-            to->ml = c.ml;
-            to->node0 = c.node0;
-            to->seq = c.seq;
-            to->hkv = c.hkv;
-            to->row0 = c.row0;
-            to->rows = c.rows;
-            to->t0 = c.t0;
-            to->n = c.t1 - c.t0;
-            to->ctx = ctx;
-            to->nodes = w.it.nodes;
-            to->whole = c.whole;
-            mbar_arrive(smem_u32(&sh->piece_full[i % kPieces]));
+        PieceInfo c;
+        if (keys) {
+            walk.next(p, c, lane);
+            qs.take(c.rows);
+            // Once the scores that read this place last are done, everybody is past piece i - 4 (the scores of a piece
+            // wait for all weights of the one before), and its description may be written over.
+            qs.each([&](int x, uint32_t uses) {
+                if (uses > 0) wait(ctl, smem_u32(&sh->q_empty[x]), (uses - 1) & 1);
+            });
+            sh->pieces.put(i, c, lane);
+        } else {
+            c = sh->pieces.get(ctl, i);  // the place of its query rows is free
+            qs.take(c.rows);
         }
-        __syncwarp();
-        if (!more) {
-            // the last scores' reports land before the block ends
-            for (int x = 0; x < 2; ++x)
-                if (qs.uses[x] > 0) wait(ctl, smem_u32(&sh->q_empty[x]), (qs.uses[x] - 1) & 1);
-            return;
+        if (c.rows == 0) break;
+        if (!keys) {
+            // rows of zeros up to a multiple of 32: scores of zero
+            const int padded = (c.rows + 31) & ~31;
+            const uint32_t to = sq + qs.slot * G::kSlot;
+#pragma unroll 2
+            for (int x = lane; x < padded * (D / 8); x += 32) {
+                const int r = x / (D / 8), ch = x - r * (D / 8);
+                const int row = c.row0 + min(r, c.rows - 1), node = attn_node(p, row), hq = c.hkv * p.gq + (row - node * p.gq);
+                const void* from = static_cast<const __nv_bfloat16*>(p.q) + (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + ch * 8;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + TileGeo<D>::at(r, ch)), "l"(from),
+                             "r"(r < c.rows ? 16 : 0)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) qs.each([&](int x, uint32_t) { mbar_arrive(smem_u32(&sh->q_full[x])); });
+            __syncwarp();
         }
-        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(ctl.abort))) return;
-        // rows of zeros up to a multiple of 32: scores of zero
-        const int padded = (c.rows + 31) & ~31;
-        const uint32_t to = sq + qs.slot * G::kSlot;
-#pragma unroll 4
-        for (int x = lane; x < padded * (D / 8); x += 32) {
-            const int r = x / (D / 8), ch = x - r * (D / 8);
-            const int row = c.row0 + min(r, c.rows - 1), node = row / p.gq, hq = c.hkv * p.gq + (row - node * p.gq);
-            const void* from = static_cast<const __nv_bfloat16*>(p.q) + (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + ch * 8;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + TileGeo<D>::at(r, ch)),
-                         "l"(from), "r"(r < c.rows ? 16 : 0)
-                         : "memory");
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) qs.each([&](int x, uint32_t) { mbar_arrive(smem_u32(&sh->q_full[x])); });
-        __syncwarp();
         qs.done();
-        if (!keys.fill(p, ctl, c.seq, c.hkv, c.t0, c.t1, c.own ? ctx + w.it.nodes : INT_MAX, lane)) return;
+        if (!filler.fill(p, ctl, c, lane)) return;
     }
-}
-
-template <int D>
-__device__ void narrow_values(const AttnParams& p, const CUtensorMap* mv, const Ctl& ctl, NarrowShared<D>* sh, uint32_t ring_v, int lane) {
-    Filler<D, NarrowGeo<D>::kValues> values(mv, &sh->rv, ring_v);
-    for (uint32_t i = 0;; ++i) {
-        const PieceInfo c = next_piece(ctl, sh, i);
-        if (c.rows == 0 || !values.fill(p, ctl, c.seq, c.hkv, c.t0, c.t0 + c.n, c.keys(), lane)) return;
-    }
+    // the last scores' reports land before the block ends
+    if (keys)
+        for (int x = 0; x < 2; ++x)
+            if (qs.uses[x] > 0) wait(ctl, smem_u32(&sh->q_empty[x]), (qs.uses[x] - 1) & 1);
 }
 
 // ---- products ----
@@ -236,7 +190,7 @@ __device__ void narrow_scores(const AttnParams& p, const Ctl& ctl, NarrowShared<
     Split before(1);
     int n_before = 0;
     for (uint32_t i = 0;; ++i) {
-        const PieceInfo c = next_piece(ctl, sh, i);
+        const PieceInfo c = sh->pieces.get(ctl, i);
         if (c.rows == 0) return;
         const Split split(c.rows);
         const int ahead = 2 * split.tiles(), width = 32 * split.chunks();
@@ -280,10 +234,10 @@ __device__ void narrow_outputs(const AttnParams& p, const Ctl& ctl, NarrowShared
     Weights weights;
     uint32_t st = 0, round = 0, tails = 0;
     for (uint32_t i = 0;; ++i) {
-        const PieceInfo c = next_piece(ctl, sh, i);
+        const PieceInfo c = sh->pieces.get(ctl, i);
         if (c.rows == 0) return;
         const Split split(c.rows);
-        const int width = 32 * split.chunks(), first_tail = c.first_tail();
+        const int width = 32 * split.chunks(), first_tail = c.first_tail(7);
         const uint32_t io = instruction(32 * split.used, 1, 1);
 #pragma unroll 1
         for (int t = 0; t < c.n; ++t) {
@@ -350,15 +304,6 @@ __device__ __forceinline__ bool group_any(int g, bool yes) {
                  : "memory");
     return r != 0;
 }
-// Whether any thread of the sixteen warps says yes.
-__device__ __forceinline__ bool soft_any(bool yes) {
-    uint32_t r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, 1, %2, q;\n selp.u32 %0, 1, 0, p;\n}"
-                 : "=r"(r)
-                 : "r"((uint32_t)yes), "n"(kSoftThreads)
-                 : "memory");
-    return r != 0;
-}
 __device__ __forceinline__ void group_sync(int g) {
     __syncwarp();
     asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory");
@@ -397,10 +342,11 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
     };
     Uses uses{};
     uint32_t f0 = 0, tails = 0;
+    int pending = 0;
     for (uint32_t piece = 0;; ++piece) {
-        const PieceInfo c = next_piece(ctl, sh, piece);
-        if (soft_any(c.rows == 0)) return;  // all sixteen warps or none: they meet at barriers below
-        const int n = c.n, ctx = c.ctx, keys = c.keys(), first_tail = c.first_tail();
+        const PieceInfo c = sh->pieces.get(ctl, piece);
+        if (rows_any<kSoftThreads>(c.rows == 0)) break;  // all sixteen warps or none: they meet at barriers below
+        const int n = c.n, ctx = c.ctx, keys = c.keys(), first_tail = c.first_tail(7);
         const Split split(c.rows);
         const int k = g >> split.log_chunks, chunk = g & (split.chunks() - 1);
         my_m[lane] = kNone;  // all four warps: each finds it there
@@ -409,7 +355,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
 #pragma unroll
         for (int e = 0; e < 32; ++e) l[e] = 0.0f;
         // this lane's row of the group's chunk
-        const int my_row = c.row0 + min(32 * chunk + lane, c.rows - 1), my_node = my_row / p.gq;
+        const int my_row = c.row0 + min(32 * chunk + lane, c.rows - 1), my_node = attn_node(p, my_row);
         const int rounds = chunk < split.used ? split.rounds(n, k) : 0;
 #pragma unroll 1
         for (int i = 0; i < rounds; ++i) {
@@ -443,8 +389,52 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
             }
             const uint32_t t_s = tmem + lanes + 128 * b + 32 * g;
             float z[32];  // scores, then arguments of the exponential
+            bool move = i == 0;  // whether references have to move: always in the first tile
 #pragma unroll 1
-            for (int attempt = 0;; ++attempt) {
+            for (bool moved = false;;) {
+                if (move) {
+                    // the columns' maxima: lane e has the warp's of column e, the four meet in the buffer that the
+                    // weights are about to fill
+                    float mine = kNegInf;
+#pragma unroll 1
+                    for (int e = 0; e < 32; e += 8) {
+                        float v[8];
+                        ld8(t_s + e, v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            float r = (seen >> (e + x)) & 1u ? v[x] * scale : kNegInf;
+                            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(r));
+                            mine = lane == e + x ? r : mine;
+                        }
+                    }
+                    weights_free();
+                    *place(g, quad) = mine;
+                    group_sync(g);
+                    const float best = fmaxf(fmaxf(*place(g, 0), *place(g, 1)), fmaxf(*place(g, 2), *place(g, 3)));
+                    const float old = my_m[lane];
+                    const float to = best - old > 8.0f ? best : old;
+                    const float fac = to == old ? 1.0f : ex2(old - to);
+                    group_sync(g);    // old references and maxima have been read
+                    my_m[lane] = to;  // all four warps: each finds it there from now on
+                    __syncwarp();
+                    if (i > 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) l[e] *= __shfl_sync(0xffffffffu, fac, e);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int e = 0; e < 32; e += 8) {
+                            float o[8];
+                            ld8(tmem + lanes + 256 + 32 * g + e, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) o[x] *= __shfl_sync(0xffffffffu, fac, e + x);
+                            st8(tmem + lanes + 256 + 32 * g + e, o);
+                        }
+                        tc_wait_st();
+                    }
+                    moved = true;
+                }
                 ld32(t_s, z);
                 tc_wait_ld();
                 float top = kNegInf;
@@ -462,47 +452,9 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                     asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(z[e]), "f"(z[e + 1]));
                     asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(z[e + 2]), "f"(z[e + 3]));
                 }
-                if (attempt == 1 || !group_any(g, top > 8.0f)) break;
-                // the columns' maxima: lane e has the warp's of column e, the four meet in the buffer that the
-                // weights are about to fill
-                float mine = kNegInf;
-#pragma unroll 1
-                for (int e = 0; e < 32; e += 8) {
-                    float v[8];
-                    ld8(t_s + e, v);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        float r = (seen >> (e + x)) & 1u ? v[x] * scale : kNegInf;
-                        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(r));
-                        mine = lane == e + x ? r : mine;
-                    }
-                }
-                weights_free();
-                *place(g, quad) = mine;
-                group_sync(g);
-                const float best = fmaxf(fmaxf(*place(g, 0), *place(g, 1)), fmaxf(*place(g, 2), *place(g, 3)));
-                const float old = my_m[lane];
-                const float to = best - old > 8.0f ? best : old;
-                const float fac = to == old ? 1.0f : ex2(old - to);
-                group_sync(g);    // old references and maxima have been read
-                my_m[lane] = to;  // all four warps: each finds it there from now on
-                __syncwarp();
-                if (i > 0) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) l[e] *= __shfl_sync(0xffffffffu, fac, e);
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int e = 0; e < 32; e += 8) {
-                        float o[8];
-                        ld8(tmem + lanes + 256 + 32 * g + e, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) o[x] *= __shfl_sync(0xffffffffu, fac, e + x);
-                        st8(tmem + lanes + 256 + 32 * g + e, o);
-                    }
-                    tc_wait_st();
-                }
+                if (moved) break;
+                move = group_any(g, top > 8.0f);
+                if (!move) break;
             }
             // this key's weights of 32 rows: four 16-byte places of its line
             weights_free();
@@ -557,7 +509,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                 if (!c.whole)
                     c.ml[32 * chunk + lane] = make_float2(m, sum);
                 else if (p.lse)
-                    p.lse[orow] = sum == 0.0f ? kNegInf : (m + log2f(sum)) * 0.69314718056f;
+                    p.lse[orow] = attn_lse(m, sum);
             }
             const int part = 32 >> split.log_tiles, d = quad * 32 + lane, rows = min(32, c.rows - 32 * chunk);
             const bool poison = sh->poison[piece & 1] != 0;
@@ -589,7 +541,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                 if (poison) {
 #pragma unroll 1
                     for (int e = k * part; e < (k + 1) * part && e < rows; ++e) {
-                        const int row = c.row0 + 32 * chunk + e, node = row / p.gq;
+                        const int row = c.row0 + 32 * chunk + e, node = attn_node(p, row);
                         const float v = poison_of(p, c, node, d);
                         if (v == 0.0f) continue;
                         const size_t to = (size_t)(c.node0 + node) * p.Hq + c.hkv * p.gq + (row - node * p.gq);
@@ -608,7 +560,13 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
         f0 += n;
         tails += n > first_tail ? n - max(first_tail, 0) : 0;
         uses.add(n, split);
+        if (c.join > 0) {
+            if (tid == 0) sh->pieces.pending[pending] = c;
+            ++pending;
+        }
     }
+    if (pending > 0)  // behind the barrier of the loop's end
+        attn_join_last<1, D, 2, 4>(p, sh->pieces.pending, pending, tid, kSoftThreads, sh->pieces.last, [] { rows_sync<kSoftThreads>(); });
 }
 
 template <int D>
@@ -625,7 +583,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (threadIdx.x == 0) {
         sh->rk.init();
         sh->rv.init();
-        for (int i = 0; i < kPieces; ++i) mbar_init(smem_u32(&sh->piece_full[i]), 1);
+        sh->pieces.init();
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh->q_full[i]), 1);
             mbar_init(smem_u32(&sh->q_empty[i]), 1);
@@ -659,14 +617,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         narrow_softmax<D>(p, ctl, sh, spw, ring_v, tmem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == 16)
-            narrow_walk<D>(p, &mk, ctl, sh, smem_u32(sq), ring_k, lane);
-        else if (warp == 17)
+        if (warp == 17)
             narrow_scores<D>(p, ctl, sh, smem_u32(sq), ring_k, tmem);
-        else if (warp == 18)
-            narrow_values<D>(p, &mv, ctl, sh, ring_v, lane);
-        else
+        else if (warp == 19)
             narrow_outputs<D>(p, ctl, sh, smem_u32(spw), ring_v, tmem);
+        else
+            narrow_fill<D>(p, warp == 16, warp == 16 ? &mk : &mv, ctl, sh, smem_u32(sq), warp == 16 ? ring_k : ring_v, lane);
     }
     tc_fence_before();
     __syncthreads();

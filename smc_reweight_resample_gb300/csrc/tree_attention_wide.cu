@@ -3,7 +3,8 @@
 //
 // A row is a node and one of the query heads that share a key/value head. One block per SM walks its
 // share of the line of key tiles (attn_plan.cuh); a tile is 128 keys.
-//   warps 8 and 10  bring the pages of keys and of values into their rings (attn_tc.cuh)
+//   warp 8     walks along the block's share, hands the pieces round and brings the pages of keys (attn_tc.cuh)
+//   warp 10    brings the pages of values
 //   warp 9     issues the products: S = Q K^T (128 rows x 128 keys, sums in tensor memory) and
 //              O += P V with P read from tensor memory
 //   (warp 11 idle: registers are handed over by fours)
@@ -40,36 +41,52 @@ template <int D>
 struct __align__(8) TcShared {
     Ring<TcGeo<D>::kKeys> rk;
     Ring<TcGeo<D>::kValues> rv;
-    uint64_t q_full;
+    PieceRing pieces;
+    uint64_t q_full[2];  // by the piece's parity
     uint64_t s_full[2], p_full[2], o_full[2];
     uint32_t tmem;
-    int abort, start;
+    int abort;
     int poison;  // a NaN or infinity among the values of the piece's nodes
 };
 
-template <int D, int kStages>
-__device__ void wide_fill(const AttnParams& p, const CUtensorMap* map, const Ctl& ctl, Ring<kStages>* rg, uint32_t ring, int lane, int start) {
-    Filler<D, kStages> filler(map, rg, ring);
-    Walk w = walk_begin(p, start);
-    AttnPiece c;
-    while (walk_next(p, w, c))
-        if (!filler.fill(p, ctl, c.seq, c.hkv, c.t0, c.t1, c.own ? __ldg(p.ctx_len + c.seq) + w.it.nodes : INT_MAX, lane)) return;
+// ---- pieces, keys and values ----
+
+// Two warps in one piece of code: the one with `keys` walks and brings the pages of keys, the other the pages of values.
+// Piece i is handed round once the query rows of piece i - 2 are there, which the softmax brings when it is done with
+// piece i - 3: the place of piece i - 4 is free.
+template <int D>
+__device__ void wide_fill(const AttnParams& p, bool keys, const CUtensorMap* map, const Ctl& ctl, TcShared<D>* sh, uint32_t ring, int lane) {
+    using G = TcGeo<D>;
+    Filler<D> filler(map, keys ? sh->rk.full : sh->rv.full, keys ? sh->rk.empty : sh->rv.empty, keys ? G::kKeys : G::kValues, ring);
+    Walker walk;
+    if (keys) walk.begin(p, lane);
+#pragma unroll 1
+    for (uint32_t i = 0;; ++i) {
+        PieceInfo c;
+        if (keys) {
+            walk.next(p, c, lane);
+            if (i >= 2) wait(ctl, smem_u32(&sh->q_full[i & 1]), ((i - 2) >> 1) & 1);
+            sh->pieces.put(i, c, lane);
+        } else {
+            c = sh->pieces.get(ctl, i);
+        }
+        if (c.rows == 0 || !filler.fill(p, ctl, c, lane)) return;
+    }
 }
 
 // ---- products ----
 
 template <int D>
-__device__ void tc_issue(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, uint32_t sq, uint32_t ring_k, uint32_t ring_v, uint32_t tmem, int start) {
+__device__ void tc_issue(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, uint32_t sq, uint32_t ring_k, uint32_t ring_v, uint32_t tmem) {
     using G = TcGeo<D>;
     constexpr uint32_t is = instruction(kTile, 0, 0), io = instruction(D, 0, 1);
-    Walk w = walk_begin(p, start);
-    AttnPiece c;
-    uint32_t f0 = 0, pieces = 0, np[2] = {0, 0};
-    while (walk_next(p, w, c)) {
-        const int n = uniform(c.t1 - c.t0);
-        const bool two = uniform(c.rows) > kTile;
-        wait(ctl, smem_u32(&sh->q_full), pieces & 1);
-        ++pieces;
+    uint32_t f0 = 0, np[2] = {0, 0};
+    for (uint32_t piece = 0;; ++piece) {
+        const PieceInfo c = sh->pieces.get(ctl, piece);
+        if (c.rows == 0) return;
+        const int n = c.n;
+        const bool two = c.rows > kTile;
+        wait(ctl, smem_u32(&sh->q_full[piece & 1]), (piece >> 1) & 1);
         tc_fence_after();
         const int steps = two ? n : (n + 1) / 2;
 #pragma unroll 1
@@ -121,7 +138,7 @@ __device__ void tc_issue(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, u
 // ---- rows ----
 
 template <int D>
-__device__ __forceinline__ void store_row(const AttnParams& p, const AttnPiece& c, size_t orow, int rr, int col, const float* v, float inv) {
+__device__ __forceinline__ void store_row(const AttnParams& p, const PieceInfo& c, size_t orow, int rr, int col, const float* v, float inv) {
     if (c.whole) {
         uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + col);
 #pragma unroll
@@ -138,14 +155,13 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const AttnPiece& 
 // NaN and infinities that were kept out of the product: added to the columns just stored where the row
 // sees their node (an infinity over the sum, or times a later factor, is the same infinity).
 template <int D>
-__device__ __forceinline__ void add_poison(const AttnParams& p, const AttnPiece& c, int nodes, const uint32_t* mask_row, int node, int ctx,
-                                        size_t orow, int rr, int c0, int c1) {
-    const int j0 = max(0, c.t0 * kTile - ctx), j1 = min(nodes, c.t1 * kTile - ctx);
+__device__ __forceinline__ void add_poison(const AttnParams& p, const PieceInfo& c, const uint32_t* mask_row, int node, size_t orow, int rr, int c0, int c1) {
+    const int j0 = max(0, c.t0 * kTile - c.ctx), j1 = min(c.nodes, (c.t0 + c.n) * kTile - c.ctx);
 #pragma unroll 1
     for (int j = j0; j < j1; ++j) {
         const bool sees = mask_row ? (__ldg(mask_row + (j >> 5)) >> (j & 31)) & 1u : j <= node;
         if (!sees) continue;
-        const int pos = ctx + j;
+        const int pos = c.ctx + j;
         const size_t page = attn_page(p, c.seq, pos >> p.page_shift);
         const uint16_t* from =
             static_cast<const uint16_t*>(p.v_cache) + ((page * p.Hkv + c.hkv) * p.page_size + (pos & (p.page_size - 1))) * D;
@@ -165,26 +181,26 @@ __device__ __forceinline__ void add_poison(const AttnParams& p, const AttnPiece&
 }
 
 template <int D>
-__device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, unsigned char* sq, uint32_t ring_v, uint32_t tmem, int start) {
+__device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, unsigned char* sq, uint32_t ring_v, uint32_t tmem) {
     using G = TcGeo<D>;
     const int tid = threadIdx.x, lane = tid & 31, s = tid >> 7, r = tid & 127, quad = (tid >> 5) & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t t_s = tmem + lanes + 128 * s;
     const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;  // a negative scale goes into q
     const float scale = fabsf(p.scale2) > 0.0f ? fabsf(p.scale2) : 1e-30f;  // 0: equal weights, and -inf stays -inf
-    Walk w = walk_begin(p, start);
-    AttnPiece c;
     uint32_t f0 = 0, steps0[2] = {0, 0};  // fills and steps of earlier pieces
-    while (walk_next(p, w, c)) {
-        const int n = c.t1 - c.t0;
+    int pending = 0;
+    for (uint32_t piece = 0;; ++piece) {
+        const PieceInfo c = sh->pieces.get(ctl, piece);
+        if (rows_any<256>(c.rows == 0)) break;  // all eight warps or none: they meet at barriers below
+        const int n = c.n, ctx = c.ctx, keys = c.keys(), first_tail = c.first_tail(7);
         const bool two = c.rows > kTile;
-        const int ctx = c.own ? __ldg(p.ctx_len + c.seq) : INT_MAX, keys = c.own ? ctx + w.it.nodes : INT_MAX;
         // q: a block of 128 rows for each stream, or one for both
         const int rows_q = min(c.rows, 2 * kTile);
 #pragma unroll 2
         for (int i = tid; i < rows_q * (D / 8); i += 256) {
             const int rr = i / (D / 8), ch = i - rr * (D / 8);
-            const int row = c.row0 + rr, node = row / p.gq, hq = c.hkv * p.gq + (row - node * p.gq);
+            const int row = c.row0 + rr, node = attn_node(p, row), hq = c.hkv * p.gq + (row - node * p.gq);
             uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                                            (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + ch * 8));
             v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
@@ -194,12 +210,12 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         if (tid == 0) sh->poison = 0;
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
+        if (lane == 0) mbar_arrive(smem_u32(&sh->q_full[piece & 1]));
         rows_sync<256>();  // poison is clear
         const int rr = two ? s * kTile + r : r;  // row of the unit's block
         const bool active = quad * 32 + (two ? s * kTile : 0) < c.rows;
         const bool mine = rr < c.rows;
-        const int row = c.row0 + (mine ? rr : 0), node = row / p.gq, hq = c.hkv * p.gq + (row - node * p.gq);
+        const int row = c.row0 + (mine ? rr : 0), node = attn_node(p, row), hq = c.hkv * p.gq + (row - node * p.gq);
         const uint32_t* mask_row = p.mask ? p.mask + (long long)(c.node0 + node) * p.words : nullptr;
         const int steps = two ? n : (n + 1 - s) / 2;  // tiles of this stream
         float m = kNegInf, l = 0.0f;                  // reference (times scale), sum
@@ -207,7 +223,7 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         for (int i = 0; i < steps; ++i) {
             const int tt = two ? i : 2 * i + s, pos0 = (c.t0 + tt) * kTile;
             const uint32_t step = steps0[s] + i;
-            const bool tail = c.own && pos0 + kTile > ctx;
+            const bool tail = tt >= first_tail;
             wait(ctl, smem_u32(&sh->s_full[s]), step & 1);
             if (tail) {
                 // The scores are there, and with them the products with the values of two tiles before: the
@@ -326,10 +342,10 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
                 }
                 if (mine) store_row<D>(p, c, orow, rr, col, a, inv);
             }
-            if (mine && poison) add_poison<D>(p, c, w.it.nodes, mask_row, node, ctx, orow, rr, c0, c1);
+            if (mine && poison) add_poison<D>(p, c, mask_row, node, orow, rr, c0, c1);
             if (mine && (two || s == 0)) {
                 if (c.whole) {
-                    if (p.lse) p.lse[orow] = l == 0.0f ? kNegInf : (m + log2f(l)) * 0.69314718056f;
+                    if (p.lse) p.lse[orow] = attn_lse(m, l);
                 } else {
                     c.ml[rr] = make_float2(m, l);
                 }
@@ -340,7 +356,13 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         f0 += n;
         steps0[0] += steps_a;
         steps0[1] += steps_b;
+        if (c.join > 0) {
+            if (tid == 0) sh->pieces.pending[pending] = c;
+            ++pending;
+        }
     }
+    if (pending > 0)  // behind the barrier of the loop's end
+        attn_join_last<1, D, 8, 2>(p, sh->pieces.pending, pending, tid, 256, sh->pieces.last, [] { rows_sync<256>(); });
 }
 
 template <int D>
@@ -357,7 +379,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (threadIdx.x == 0) {
         sh->rk.init();
         sh->rv.init();
-        mbar_init(smem_u32(&sh->q_full), 8);
+        sh->pieces.init();
+        mbar_init(smem_u32(&sh->q_full[0]), 8);
+        mbar_init(smem_u32(&sh->q_full[1]), 8);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sh->s_full[s]), 1);
             mbar_init(smem_u32(&sh->p_full[s]), 4);
@@ -378,26 +402,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const Ctl ctl{p.ws, &sh->abort};
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 8) {
-        const int at = walk_start(p, lane);
-        if (lane == 0) sh->start = at;
-    }
-    __syncthreads();
-    const int start = sh->start;
     // 384 threads start with 168 registers each; the rows' eight warps go on with 216 and the other four
     // with 72 (2 x 216 + 72 = 3 x 168)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        tc_rows<D>(p, ctl, sh, sq, ring_v, tmem, start);
+        tc_rows<D>(p, ctl, sh, sq, ring_v, tmem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8) {
-            wide_fill<D, G::kKeys>(p, &mk, ctl, &sh->rk, ring_k, lane, start);
-        } else if (warp == 10) {
-            wide_fill<D, G::kValues>(p, &mv, ctl, &sh->rv, ring_v, lane, start);
-        } else if (warp == 9) {
-            tc_issue<D>(p, ctl, sh, smem_u32(sq), ring_k, ring_v, tmem, start);
-        }
+        if (warp == 9)
+            tc_issue<D>(p, ctl, sh, smem_u32(sq), ring_k, ring_v, tmem);
+        else if (warp != 11)
+            wide_fill<D>(p, warp == 8, warp == 8 ? &mk : &mv, ctl, sh, warp == 8 ? ring_k : ring_v, lane);
     }
     tc_fence_before();
     __syncthreads();
