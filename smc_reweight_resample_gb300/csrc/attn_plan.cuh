@@ -28,11 +28,12 @@ namespace smcsd {
 
 struct __align__(16) AttnItem {
     int node0, nodes;   // rows of q
-    int tile0, tiles;   // key tiles of each unit
+    int key0, tiles;    // first key, key tiles of each unit
     int nrb, per;       // row blocks, rows in each of them (the last one may be shorter)
     int seq, unit0;     // page table row; number of the first unit
     int cum;            // first tile on the line
-    int pad[3];
+    int keys;           // keys that a group shares (key0 of its sequences)
+    int pad[2];
 };
 
 struct AttnHead {  // written by the planning kernel
@@ -49,7 +50,7 @@ constexpr int kAttnWarpPlan = 1024;  // sequences whose places on the line a war
 struct AttnLayout {
     size_t count;    // unsigned [kAttnMaxCta]: pieces that have arrived, of the unit that is cut first at a block's end
     size_t item;     // AttnItem [G + S]
-    size_t shared;   // int [G] tiles shared by a group
+    size_t shared;   // int [G] keys shared by a group
     size_t slot_g;   // pieces of shared units: float [slots][rows_g][D], then float2 [slots][rows_g]
     size_t slot_s;   // pieces of own units
     size_t ml_g, ml_s;
@@ -181,13 +182,11 @@ struct PieceInfo {
     int join, counter;       // pieces of the unit, joined by the last to arrive (0: none are); its first block, its counter
     int node0, seq, hkv;     // first row of the item, page table row, key/value head
     int row0, rows;          // rows of the item in this block of rows (none: there are no more pieces)
-    int t0, n;               // key tiles
-    int ctx;                 // tokens in the cache; INT_MAX for keys that a group shares
-    int nodes;
+    int key0, n;             // first key, key tiles
+    int ctx, end;            // tokens in the cache and behind them the nodes; for keys that a group shares both are their end
     bool whole;              // all that its rows have to see: the result is written directly
-    __device__ __forceinline__ int keys() const { return ctx == INT_MAX ? INT_MAX : ctx + nodes; }
-    // first tile of `size` keys with a node or the end (n or more: none)
-    __device__ __forceinline__ int first_tail(int log_size) const { return ctx == INT_MAX ? n : (ctx >> log_size) - t0; }
+    // first tile with a node or the end inside it (n or more: none; rounded down, below zero where nodes are all there is)
+    __device__ __forceinline__ int first_tail(int log_size) const { return (ctx - key0) >> log_size; }
 };
 
 // A warp's walk along its block's share.
@@ -274,7 +273,7 @@ struct Walker {
             it.cum = __shfl_sync(0xffffffffu, mine.cum, l);
             attn_units(p, it);
             it.unit0 = 0;
-            it.tile0 = 0;
+            it.key0 = 0;
             it.seq = ii = first + l;
         }
         item_end = it.cum + it.tiles * it.nrb * p.Hkv;
@@ -287,16 +286,16 @@ struct Walker {
         const bool own = ii >= p.G;
         const int in = x - it.cum, u = in / it.tiles, t = in - u * it.tiles, cta = blockIdx.x, units = it.nrb;
         c.node0 = it.node0;
-        c.nodes = it.nodes;
         c.seq = it.seq;
         c.hkv = units == 1 ? u : u / units;
         c.row0 = (u - c.hkv * units) * it.per;
         c.rows = min(it.nodes * p.gq - c.row0, it.per);
         const int unit_end = x - t + it.tiles, to = min(unit_end, end);
-        c.t0 = it.tile0 + t;
+        c.key0 = it.key0 + (t << p.log_tile);
         c.n = to - x;
-        c.whole = own && it.tile0 == 0 && c.n == it.tiles;
-        c.ctx = own ? __ldg(p.ctx_len + it.seq) : INT_MAX;
+        c.whole = own && it.key0 == 0 && c.n == it.tiles;
+        c.ctx = own ? __ldg(p.ctx_len + it.seq) : it.keys;
+        c.end = own ? c.ctx + it.nodes : it.keys;
         c.join = 0;
         const int rows = own ? p.L.rows_s : p.L.rows_g;
         float* o = ws_ptr<float>(p.ws, own ? p.L.slot_s : p.L.slot_g);

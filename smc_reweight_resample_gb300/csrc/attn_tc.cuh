@@ -243,13 +243,13 @@ struct Filler {
         : map(m), full(f), empty(e), stages(n), ring(addr), st(0), round(0) {}
     // the tiles of a piece; false after a wait that ran out
     __device__ __forceinline__ bool fill(const AttnParams& p, const Ctl& ctl, const PieceInfo& c, int lane) {
-        const int hkv = c.hkv, t0 = c.t0, t1 = c.t0 + c.n, keys = c.keys();
+        const int hkv = c.hkv, n = c.n, key0 = c.key0;
         const int box_shift = p.page_shift < 7 ? p.page_shift : 7, box = 1 << box_shift, nbox = kTile >> box_shift;
         const int32_t* row = p.table + (long long)c.seq * p.pages_per_seq;
-        const int last = (int)min((long long)t1 * kTile, (long long)keys);  // end of the positions
+        const int last = min(n * kTile, c.end - key0);  // end of the positions
         auto ids = [&](int batch) {  // of the 32 boxes from 32 * batch on
-            const int pos = t0 * kTile + ((32 * batch + lane) << box_shift);
-            int id = pos < last ? __ldg(row + (pos >> p.page_shift)) : 0;
+            const int at = (32 * batch + lane) << box_shift;
+            int id = at < last ? __ldg(row + ((key0 + at) >> p.page_shift)) : 0;
             if (id < 0 || id >= p.num_pages) {
                 raise_error(p.ws, kErrRange);
                 id = 0;
@@ -259,7 +259,7 @@ struct Filler {
         const int bytes = box * D * 2;
         int id = ids(0), next = ids(1), batch = 1;
 #pragma unroll 1
-        for (int t = t0, x = 0; t < t1; ++t, x += nbox) {
+        for (int t = 0, x = 0; t < n; ++t, x += nbox) {
             if (x == 32) {
                 x = 0;
                 id = next;
@@ -270,7 +270,7 @@ struct Filler {
             const int ust = uniform(st), boxes = uniform(min(nbox, (last - t * kTile + box - 1) >> box_shift));
             const uint32_t bar = smem_u32(&full[ust]);
             uint32_t to = ring + ust * T::kBytes;
-            const int at = uniform((hkv * p.page_size + ((t * kTile) & (p.page_size - 1))) >> 3);
+            const int at = uniform((hkv * p.page_size + ((key0 + t * kTile) & (p.page_size - 1))) >> 3);
             if (elect_one()) mbar_expect_tx(bar, (uint32_t)(boxes * bytes));
             __syncwarp();
 #pragma unroll 1
@@ -292,16 +292,21 @@ struct Filler {
 
 // ---- masks ----
 
-// Zeroes what the product with V must not meet in `count` blocks of 64 columns of one key's row, from the block at
-// `addr` on: everything past the end, NaN and infinities in nodes (rows of zero weight would turn them into NaN). True
-// if there were some.
-__device__ __forceinline__ bool clean_row(uint32_t addr, int count, bool past) {
+// Keys of a tile that the product with V takes, of `keys` that it has: up to the next 16 (one step of it).
+__device__ __forceinline__ int tile_steps(int keys) { return (min(keys, kTile) + 15) >> 4; }
+
+// Zeroes what the product with V must not meet in a tile of `keys` keys: in what it takes of the rows past the end everything,
+// in those of the nodes (from `first` on) NaN and infinities, which rows of zero weight would turn into NaN. Thread i of n takes
+// every n-th 16 bytes; true if it found some.
+template <int D>
+__device__ __forceinline__ bool clean_values(uint32_t tile, int first, int keys, int i, int n) {
     bool found = false;
 #pragma unroll 1
-    for (int i = 0; i < 8 * count; ++i) {
-        const uint32_t at = addr + (i >> 3) * 1024 + (i & 7) * 16;
+    for (int x = first * (D / 8) + i; x < 16 * tile_steps(keys) * (D / 8); x += n) {
+        const int r = x / (D / 8), ch = x % (D / 8);
+        const uint32_t at = tile + (r >> 3) * TileGeo<D>::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 + (ch & 7) * 16;
         uint32_t v[4];
-        if (past) {
+        if (r >= keys) {
             v[0] = v[1] = v[2] = v[3] = 0;
         } else {
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");

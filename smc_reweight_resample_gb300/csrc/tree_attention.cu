@@ -39,8 +39,9 @@ __device__ __forceinline__ AttnItem plan_item(const AttnParams& p, const int* sh
     AttnItem it;
     if (i < p.G) {
         it.seq = i * p.N;
-        it.tiles = __ldcg(shared + i);
-        it.tile0 = 0;
+        it.keys = __ldcg(shared + i);
+        it.tiles = (it.keys + (1 << p.log_tile) - 1) >> p.log_tile;
+        it.key0 = 0;
         int first, a;
         it.nodes = attn_nodes(p, it.seq, first);
         for (int k = 1; k < p.N; ++k) {
@@ -57,10 +58,11 @@ __device__ __forceinline__ AttnItem plan_item(const AttnParams& p, const int* sh
         it.nodes = attn_nodes(p, it.seq, it.node0);
         const int c = attn_ctx(p, it.seq, it.nodes);
         if (c < 0) it.nodes = 0;
-        it.tile0 = p.G > 0 ? __ldcg(shared + it.seq / p.N) : 0;
-        it.tiles = it.nodes > 0 ? ((c + it.nodes + (1 << p.log_tile) - 1) >> p.log_tile) - it.tile0 : 0;
+        it.key0 = p.G > 0 ? __ldcg(shared + it.seq / p.N) : 0;
+        it.tiles = it.nodes > 0 ? (c + it.nodes - it.key0 + (1 << p.log_tile) - 1) >> p.log_tile : 0;
+        it.keys = 0;
     }
-    it.pad[0] = it.pad[1] = it.pad[2] = 0;
+    it.pad[0] = it.pad[1] = 0;
     return it;
 }
 
@@ -90,7 +92,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         }
         __syncthreads();
         if (tid == 0) {
-            shared[blockIdx.x] = (int)(((long long)best << p.page_shift) >> p.log_tile);
+            // less than a tile is not worth a unit of its own
+            const int keys = best << p.page_shift;
+            shared[blockIdx.x] = keys >> p.log_tile ? keys : 0;
             const unsigned old = atom_add_release(&attn_head(p)->done, 1u);
             last = old == gridDim.x - 1;
             if (last) {
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
         __syncthreads();
         const PieceInfo c = s_piece;
         if (c.rows == 0) break;
-        const int ctx = c.ctx, keys = c.keys();  // positions that exist
+        const int ctx = c.ctx, keys = c.end;  // positions that exist
         for (int i = tid; i < kSimtRows * kV4; i += kSimtThreads) {
             const int r = i / kV4, d = (i - r * kV4) * 4;
             float4 v = make_float4(0, 0, 0, 0);
@@ -201,8 +205,8 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
 #pragma unroll
         for (int r = 0; r < kHold; ++r) acc[r] = 0.0f;
         const int col = tid % D, vr0 = (tid / D) * kHold;
-        for (int t = c.t0; t < c.t0 + c.n; ++t) {
-            const int pos0 = t * kSimtKeys;
+        for (int t = 0; t < c.n; ++t) {
+            const int pos0 = c.key0 + t * kSimtKeys;
             __syncthreads();
             for (int i = tid; i < kSimtKeys * kV4; i += kSimtThreads) {
                 const int k = i / kV4, d = (i - k * kV4) * 4, pos = pos0 + k;

@@ -253,10 +253,12 @@ __device__ void narrow_outputs(const AttnParams& p, const Ctl& ctl, NarrowShared
             const uint64_t va = operand(ring_v + st * G::kStage, TileGeo<D>::kGroup, D == 128 ? 1024 : 0);
             const uint64_t pb = operand(sp + (width * k / 64) * G::kBlock + (width * k % 64) * 2, 1024, G::kBlock);
             const uint32_t to = tmem + 256 + width * k, more = r > 0;
+            const int steps = uniform(tile_steps(c.end - c.key0 - t * kTile));
             if (elect_one()) {
 #pragma unroll
                 for (int x = 0; x < kTile / 16; ++x) {
-                    mma_ss(to, va + (uint64_t)((x * 2 * TileGeo<D>::kGroup) >> 4), pb + (uint64_t)((x * 2048) >> 4), io, x > 0 ? 1u : more);
+                    if (x < steps)
+                        mma_ss(to, va + (uint64_t)((x * 2 * TileGeo<D>::kGroup) >> 4), pb + (uint64_t)((x * 2048) >> 4), io, x > 0 ? 1u : more);
                 }
                 tc_commit(smem_u32(&sh->rv.empty[st]));
                 tc_commit(smem_u32(&sh->o_full[k][b]));
@@ -311,7 +313,7 @@ __device__ __forceinline__ void group_sync(int g) {
 
 // What the row's nodes with a NaN or infinity in column d of their values add to it.
 __device__ __forceinline__ float poison_of(const AttnParams& p, const PieceInfo& c, int node, int d) {
-    const int j0 = max(0, c.t0 * kTile - c.ctx), j1 = min(c.nodes, (c.t0 + c.n) * kTile - c.ctx);
+    const int j0 = max(0, c.key0 - c.ctx), j1 = min(c.end, c.key0 + c.n * kTile) - c.ctx;
     float sum = 0.0f;
 #pragma unroll 1
     for (int j = j0; j < j1; ++j) {
@@ -346,7 +348,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
     for (uint32_t piece = 0;; ++piece) {
         const PieceInfo c = sh->pieces.get(ctl, piece);
         if (rows_any<kSoftThreads>(c.rows == 0)) break;  // all sixteen warps or none: they meet at barriers below
-        const int n = c.n, ctx = c.ctx, keys = c.keys(), first_tail = c.first_tail(7);
+        const int n = c.n, ctx = c.ctx, keys = c.end, first_tail = c.first_tail(7);
         const Split split(c.rows);
         const int k = g >> split.log_chunks, chunk = g & (split.chunks() - 1);
         my_m[lane] = kNone;  // all four warps: each finds it there
@@ -359,7 +361,7 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
         const int rounds = chunk < split.used ? split.rounds(n, k) : 0;
 #pragma unroll 1
         for (int i = 0; i < rounds; ++i) {
-            const int tt = (i << split.log_tiles) + k, pos0 = (c.t0 + tt) * kTile, b = i & 1;
+            const int tt = (i << split.log_tiles) + k, pos0 = c.key0 + tt * kTile, b = i & 1;
             const bool tail = tt >= first_tail;
             // the product that read the group's weights last
             auto weights_free = [&] {
@@ -369,22 +371,24 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
             tc_fence_after();
             uint32_t seen = 0xffffffffu;  // rows that see this thread's key
             if (tail) {
-                // lane e works out which of the warp's 32 keys row e sees; then every lane picks its key's bits
-                const uint32_t* mask_row = p.mask ? p.mask + (long long)(c.node0 + my_node) * p.words : nullptr;
-                const uint32_t row_sees = seen32(p, mask_row, my_node, ctx, keys, pos0 + 32 * quad);
-                seen = 0;
+                const int pos = pos0 + key;
+                if (!p.mask) {
+                    // a chain: node j is seen by the rows from j * gq on
+                    seen = pos < ctx ? 0xffffffffu : (pos < keys ? ~low_bits((pos - ctx) * p.gq - c.row0 - 32 * chunk) : 0u);
+                } else {
+                    // lane e works out which of the warp's 32 keys row e sees; then every lane picks its key's bits
+                    const uint32_t row_sees = seen32(p, p.mask + (long long)(c.node0 + my_node) * p.words, my_node, ctx, keys, pos0 + 32 * quad);
+                    seen = 0;
 #pragma unroll 8
-                for (int e = 0; e < 32; ++e) seen |= ((__shfl_sync(0xffffffffu, row_sees, e) >> lane) & 1u) << e;
-                if (chunk == 0 && pos0 + quad * 32 + 31 >= ctx) {
+                    for (int e = 0; e < 32; ++e) seen |= ((__shfl_sync(0xffffffffu, row_sees, e) >> lane) & 1u) << e;
+                }
+                if (chunk == 0) {
                     // A piece has at most two such tiles (up to 128 nodes); the issuing warp reports their values.
                     const uint32_t x = tails + (tt - max(first_tail, 0));
                     wait(ctl, smem_u32(&sh->v_full[x & 1]), (x >> 1) & 1);
                     const uint32_t f = f0 + tt, st = f % G::kValues;
                     wait(ctl, smem_u32(&sh->rv.full[st]), (f / G::kValues) & 1);  // passed by now: the copy's own barrier
-                    bool found = false;
-                    if (pos0 + key >= ctx)
-                        found = clean_row(ring_v + st * G::kStage + (key >> 3) * TileGeo<D>::kGroup + (key & 7) * 128, D / 64, pos0 + key >= keys);
-                    if (found) sh->poison[piece & 1] = 1;
+                    if (clean_values<D>(ring_v + st * G::kStage, max(ctx - pos0, 0), keys - pos0, key, 128)) sh->poison[piece & 1] = 1;
                 }
             }
             const uint32_t t_s = tmem + lanes + 128 * b + 32 * g;

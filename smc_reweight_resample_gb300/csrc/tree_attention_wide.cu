@@ -103,10 +103,11 @@ __device__ void tc_issue(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, u
                     tc_fence_after();
                     const uint64_t vb = operand(ring_v + st * G::kStage, TileGeo<D>::kGroup, 1024);
                     const uint32_t more = i > 1;
+                    const int steps_v = uniform(tile_steps(c.end - c.key0 - tp * kTile));
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k, vb + (uint64_t)((k * 2 * TileGeo<D>::kGroup) >> 4), io, k > 0 ? 1u : more);
+                            if (k < steps_v) mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k, vb + (uint64_t)((k * 2 * TileGeo<D>::kGroup) >> 4), io, k > 0 ? 1u : more);
                         if (!two || s == 1) tc_commit(smem_u32(&sh->rv.empty[st]));
                         tc_commit(smem_u32(&sh->o_full[s]));
                     }
@@ -156,7 +157,7 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const PieceInfo& 
 // sees their node (an infinity over the sum, or times a later factor, is the same infinity).
 template <int D>
 __device__ __forceinline__ void add_poison(const AttnParams& p, const PieceInfo& c, const uint32_t* mask_row, int node, size_t orow, int rr, int c0, int c1) {
-    const int j0 = max(0, c.t0 * kTile - c.ctx), j1 = min(c.nodes, (c.t0 + c.n) * kTile - c.ctx);
+    const int j0 = max(0, c.key0 - c.ctx), j1 = min(c.end, c.key0 + c.n * kTile) - c.ctx;
 #pragma unroll 1
     for (int j = j0; j < j1; ++j) {
         const bool sees = mask_row ? (__ldg(mask_row + (j >> 5)) >> (j & 31)) & 1u : j <= node;
@@ -193,7 +194,7 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
     for (uint32_t piece = 0;; ++piece) {
         const PieceInfo c = sh->pieces.get(ctl, piece);
         if (rows_any<256>(c.rows == 0)) break;  // all eight warps or none: they meet at barriers below
-        const int n = c.n, ctx = c.ctx, keys = c.keys(), first_tail = c.first_tail(7);
+        const int n = c.n, ctx = c.ctx, keys = c.end, first_tail = c.first_tail(7);
         const bool two = c.rows > kTile;
         // q: a block of 128 rows for each stream, or one for both
         const int rows_q = min(c.rows, 2 * kTile);
@@ -221,7 +222,7 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         float m = kNegInf, l = 0.0f;                  // reference (times scale), sum
 #pragma unroll 1
         for (int i = 0; i < steps; ++i) {
-            const int tt = two ? i : 2 * i + s, pos0 = (c.t0 + tt) * kTile;
+            const int tt = two ? i : 2 * i + s, pos0 = c.key0 + tt * kTile;
             const uint32_t step = steps0[s] + i;
             const bool tail = tt >= first_tail;
             wait(ctl, smem_u32(&sh->s_full[s]), step & 1);
@@ -230,13 +231,8 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
                 // stage's earlier fill has landed, so this one may be waited for.
                 const uint32_t f = f0 + tt, st = f % G::kValues;
                 wait(ctl, smem_u32(&sh->rv.full[st]), (f / G::kValues) & 1);
-                const uint32_t v = ring_v + st * G::kStage;
-                bool found = false;
-                const int k = two ? tid >> 1 : r;
-                // two threads for a row of two blocks where both groups have the tile
-                const int h = two ? (tid & 1) * (D / 64 - 1) : 0, count = two ? 1 : D / 64;
-                if (pos0 + k >= ctx) found = clean_row(v + (k >> 3) * TileGeo<D>::kGroup + h * 1024 + (k & 7) * 128, count, pos0 + k >= keys);
-                if (found) sh->poison = 1;
+                // by both groups where both have the tile
+                if (clean_values<D>(ring_v + st * G::kStage, max(ctx - pos0, 0), keys - pos0, two ? tid : r, two ? 256 : 128)) sh->poison = 1;
                 fence_async_smem();
                 if (two) rows_sync<256>();  // the other stream's product reads the same values
             }
