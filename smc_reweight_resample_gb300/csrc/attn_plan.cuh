@@ -7,13 +7,15 @@
 // Hkv x nrb units (a key/value head and a block of at most RB rows, a row being a node and one of the
 // Hq/Hkv query heads that share the head), each of `tiles` tiles of keys.
 //
-// Cut. All tiles of all units stand in one line, W of them (below 2^31). Block c of ncta takes W / ncta of them,
+// Cut. All tiles of all units stand in one line, and before each unit's tiles as many empty places as beginning and ending a
+// unit costs tiles: W places (below 2^31). Block c of ncta takes W / ncta of them,
 // the first W % ncta blocks one more: equal shares whatever the lengths are. Where a cut falls inside a unit, or a
-// row has a shared and an own unit, the pieces leave (sum, max, weighted values) in a slot. Without groups only a block's
-// first and last piece can be part of a unit: block c has slots 2 c (a unit that began before it) and 2 c + 1 (one
-// that ends behind it), and the last block to finish a unit's pieces joins them, in the order of the line. With groups a
-// piece of unit u in block c has slot u + c (both rise along the line and one of them rises from piece to piece, so no
-// two pieces share a slot), and a kernel of its own joins a row's pieces.
+// row has a shared and an own unit, the pieces leave (sum, max, weighted values) in a slot. Without the planning kernel (and so
+// without groups) only a block's first and last piece can be part of a unit: block c has slots 2 c (a unit that began before
+// it) and 2 c + 1 (one that ends behind it), and the last block to finish a unit's pieces joins them, in the order of the
+// line. With it a piece of unit u in block c has slot u + c (both rise along the line and one of them rises from piece to
+// piece, so no two pieces share a slot), and a kernel of its own joins a row's pieces. The kernels exist once for each of the
+// two: what a call does not come to costs it all the same, since their code is longer than what an SM holds of it at a time.
 //
 // Who works the line out. Without groups and for up to 1024 sequences a warp of each block does, from the lengths
 // alone (a few loads, all in flight together; a planning kernel before it and the loads of its results took 5 us of a
@@ -31,7 +33,7 @@ struct __align__(16) AttnItem {
     int key0, tiles;    // first key, key tiles of each unit
     int nrb, per;       // row blocks, rows in each of them (the last one may be shorter)
     int seq, unit0;     // page table row; number of the first unit
-    int cum;            // first tile on the line
+    int cum;            // first place on the line
     int keys;           // keys that a group shares (key0 of its sequences)
     int pad[2];
 };
@@ -46,6 +48,7 @@ struct AttnHead {  // written by the planning kernel
 // Every kernel that takes part has at most kAttnMaxCta blocks on the line.
 constexpr int kAttnMaxCta = 1024;
 constexpr int kAttnWarpPlan = 1024;  // sequences whose places on the line a warp works out
+inline bool attn_planned(int S, int N) { return N > 1 || S > kAttnWarpPlan; }
 
 struct AttnLayout {
     size_t count;    // unsigned [kAttnMaxCta]: pieces that have arrived, of the unit that is cut first at a block's end
@@ -73,7 +76,7 @@ inline AttnLayout attn_layout(int S, int N, int T, int gq, int Hkv, int D, int R
     const long long rs = (long long)T * gq, rg = rs * N;
     L.rows_s = (int)(rs < RB ? rs : RB);
     L.rows_g = (int)(rg < RB ? rg : RB);
-    const size_t us = G ? (size_t)S * Hkv * attn_blocks(rs, RB) + ncta : 2 * (size_t)ncta;
+    const size_t us = attn_planned(S, N) ? (size_t)S * Hkv * attn_blocks(rs, RB) + ncta : 2 * (size_t)ncta;
     const size_t ug = G ? G * Hkv * attn_blocks(rg, RB) + ncta : 0;
     L.slot_s = o;
     o = align256(o + us * L.rows_s * D * 4);
@@ -107,6 +110,7 @@ struct AttnParams {
     void* ws;
     AttnLayout L;
     int log_tile, log_rb;  // keys of a tile, rows of a block
+    int empty;             // places before a unit's tiles
     int ncta_max;
     FastDiv div_gq, div_cta;
     bool planned;  // by the planning kernel
@@ -146,10 +150,11 @@ struct AttnCut {  // W = ncta * base + rest
         base = W < p.ncta_max ? 1 : (int)fast_div((uint32_t)W, p.div_cta);
         rest = W - base * ncta;
     }
-    __device__ __forceinline__ int of(int c) const { return base * c + min(c, rest); }  // first tile of block c
-    __device__ __forceinline__ int block(int x) const {                                 // of tile x
-        const int first = rest * (base + 1);  // tiles of the longer shares
-        return x < first ? x / (base + 1) : rest + (x - first) / base;
+    __device__ __forceinline__ int of(int c) const { return base * c + min(c, rest); }  // first place of block c
+    __device__ __forceinline__ int block(int x) const {                                 // of place x
+        const int first = rest * (base + 1);  // places of the longer shares
+        const bool longer = x < first;
+        return (longer ? 0 : rest) + (int)((unsigned)(longer ? x : x - first) / (unsigned)(longer ? base + 1 : base));
     }
 };
 
@@ -162,7 +167,7 @@ __device__ __forceinline__ int attn_units(const AttnParams& p, AttnItem& it) {
     return it.tiles > 0 ? p.Hkv * it.nrb : 0;
 }
 
-// A warp's search: the item that tile x of the line lies in, 32 at a time (the last one that begins at or before it: items
+// A warp's search: the item that place x of the line lies in, 32 at a time (the last one that begins at or before it: items
 // without tiles come before the one that has them).
 __device__ __forceinline__ int attn_search(const AttnItem* items, int first, int n, int x, int lane) {
     while (n > 1) {
@@ -189,17 +194,19 @@ struct PieceInfo {
     __device__ __forceinline__ int first_tail(int log_size) const { return (ctx - key0) >> log_size; }
 };
 
-// A warp's walk along its block's share.
+// A warp's walk along its block's share, with the items of the planning kernel or from the lengths alone.
+template <bool kPlanned>
 struct Walker {
     AttnCut cut;
     int x, end, item_end;
     int units_shared, ii;  // ii: number of the present item
     AttnItem it;
+    int unit, hkv, rb, at, ctx;  // next unit of it, its head and block of rows, first place of what is left; its tokens in the cache
     // where the warp works the line out itself: 32 sequences at a time, one a lane
     AttnItem mine;
     int first, mine_end;  // the 32's first sequence, line after this lane's item
 
-    // this lane's item of the 32; its tiles on the line
+    // this lane's item of the 32; its places on the line
     __device__ __forceinline__ int load(const AttnParams& p, int lane) {
         const int s = first + lane;
         mine.nodes = mine.tiles = mine.node0 = 0;
@@ -209,7 +216,7 @@ struct Walker {
             if (c < 0) mine.nodes = 0;
             mine.tiles = mine.nodes > 0 ? (c + mine.nodes + (1 << p.log_tile) - 1) >> p.log_tile : 0;
         }
-        return attn_units(p, mine) * mine.tiles;
+        return attn_units(p, mine) * (mine.tiles + p.empty);
     }
     __device__ __forceinline__ void place(int at, int size, int lane) {
         int in = size;
@@ -226,7 +233,7 @@ struct Walker {
         const int cta = blockIdx.x;
         x = end = item_end = 0;
         units_shared = 0;
-        if (p.planned) {
+        if (kPlanned) {
             const AttnHead* h = attn_head(p);
             cut.base = h->base;
             cut.rest = h->rest;
@@ -256,7 +263,7 @@ struct Walker {
         end = cut.of(cta + 1);
     }
     __device__ __forceinline__ void next_item(const AttnParams& p, int lane) {
-        if (p.planned) {
+        if (kPlanned) {
             it = ws_ptr<AttnItem>(p.ws, p.L.item)[++ii];
         } else {
             unsigned after;  // lanes whose items end behind x
@@ -276,41 +283,57 @@ struct Walker {
             it.key0 = 0;
             it.seq = ii = first + l;
         }
-        item_end = it.cum + it.tiles * it.nrb * p.Hkv;
+        item_end = it.cum + (it.tiles + p.empty) * it.nrb * p.Hkv;
+        ctx = ii >= p.G ? __ldg(p.ctx_len + it.seq) : 0;
     }
     // The next piece; false (and no rows) after the last one.
     __device__ __forceinline__ bool next(const AttnParams& p, PieceInfo& c, int lane) {
         c.rows = 0;
         if (x >= end) return false;
-        while (x >= item_end) next_item(p, lane);  // x is below W, so an item that holds it follows
+        if (x >= item_end) {
+            while (x >= item_end) next_item(p, lane);  // x is below W, so an item that holds it follows
+            const int in = x - it.cum;
+            unit = (int)((unsigned)in / (unsigned)(it.tiles + p.empty));
+            at = in - unit * (it.tiles + p.empty);
+            hkv = it.nrb == 1 ? unit : (int)((unsigned)unit / (unsigned)it.nrb);
+            rb = unit - hkv * it.nrb;
+        }
         const bool own = ii >= p.G;
-        const int in = x - it.cum, u = in / it.tiles, t = in - u * it.tiles, cta = blockIdx.x, units = it.nrb;
+        const int cta = blockIdx.x, first = x - at + p.empty;  // first tile's place
         c.node0 = it.node0;
         c.seq = it.seq;
-        c.hkv = units == 1 ? u : u / units;
-        c.row0 = (u - c.hkv * units) * it.per;
+        c.hkv = hkv;
+        c.row0 = rb * it.per;
         c.rows = min(it.nodes * p.gq - c.row0, it.per);
-        const int unit_end = x - t + it.tiles, to = min(unit_end, end);
+        const int unit_end = first + it.tiles, to = min(unit_end, end), t = max(x - first, 0);
         c.key0 = it.key0 + (t << p.log_tile);
-        c.n = to - x;
+        c.n = to - first - t;
+        if (c.n <= 0) {  // the share ends before the unit's tiles
+            x = end;
+            c.rows = 0;
+            return false;
+        }
         c.whole = own && it.key0 == 0 && c.n == it.tiles;
-        c.ctx = own ? __ldg(p.ctx_len + it.seq) : it.keys;
-        c.end = own ? c.ctx + it.nodes : it.keys;
+        c.ctx = own ? ctx : it.keys;
+        c.end = own ? ctx + it.nodes : it.keys;
         c.join = 0;
         const int rows = own ? p.L.rows_s : p.L.rows_g;
         float* o = ws_ptr<float>(p.ws, own ? p.L.slot_s : p.L.slot_g);
         float2* ml = ws_ptr<float2>(p.ws, own ? p.L.ml_s : p.L.ml_g);
-        size_t slot = (size_t)(it.unit0 + u - (own ? units_shared : 0)) + cta;
-        if (p.G == 0) {
+        size_t slot = (size_t)(it.unit0 + unit - (own ? units_shared : 0)) + cta;
+        if (!kPlanned) {
             slot = 2 * cta + (t == 0);
             if (!c.whole) {
-                c.counter = t == 0 ? cta : cut.block(x - t);
+                c.counter = t == 0 ? cta : cut.block(first);
                 c.join = (to == unit_end ? cta : cut.block(unit_end - 1)) - c.counter + 1;
             }
         }
         c.o = o + slot * rows * p.D;
         c.ml = ml + slot * rows;
-        x = to;
+        x = to;  // the end, or the next unit
+        at = 0;
+        ++unit;
+        if (++rb == it.nrb) rb = 0, ++hkv;
         return true;
     }
 };

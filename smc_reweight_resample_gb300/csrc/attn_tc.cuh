@@ -139,19 +139,15 @@ struct Ctl {
     int* abort;
 };
 // Waits are bounded: each try suspends the thread for a few microseconds at most, and after kTries of them (0.1 to
-// a few seconds) the error is recorded and every later wait of the block returns.
-constexpr int kTries = 1 << 20;
-__device__ __forceinline__ void give_up(const Ctl& c) {
-    raise_error(c.ws, kErrTimeout);
-    *reinterpret_cast<volatile int*>(c.abort) = 1;
-}
+// a few seconds) every later wait of the block returns; the error is recorded at the block's end.
+constexpr int kTries = 1 << 19;
 // one thread of a warp
 __device__ __forceinline__ void wait1(const Ctl& c, uint32_t bar, uint32_t parity) {
     int tries = 0;
 #pragma unroll 1
     while (!mbar_try(bar, parity)) {
         if (++tries < kTries && !*reinterpret_cast<volatile int*>(c.abort)) continue;
-        give_up(c);
+        *reinterpret_cast<volatile int*>(c.abort) = 1;
         break;
     }
 }
@@ -161,40 +157,48 @@ __device__ __forceinline__ void wait(const Ctl& c, uint32_t bar, uint32_t parity
     __syncwarp();
 }
 
-// The pieces of a block's share as one warp hands them to the others. The walker is at most three pieces ahead of the
-// slowest reader (both kernels say why), so a place is free when it comes round again.
-constexpr int kPieces = 4;
+// The pieces of a block's share as one warp hands them to the others. They stay in shared memory, where each reader takes from
+// them what it needs when it needs it (copies of its own were spilled, and with nearly all of the SM's memory in use as shared
+// memory a spilled value comes from the second-level cache), and reports when it is through with one.
+constexpr int kPieces = 8;
 struct PieceRing {
     PieceInfo piece[kPieces];
     PieceInfo pending[2];  // cut units' pieces, to be reported at the end
-    uint64_t full[kPieces];
+    uint64_t full[kPieces], empty[kPieces];
     int last[2];
-    __device__ __forceinline__ void init() {
-        for (int i = 0; i < kPieces; ++i) mbar_init(smem_u32(&full[i]), 1);
+    __device__ __forceinline__ void init(int readers) {
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&empty[i]), readers);
+        }
     }
     // one warp
-    __device__ __forceinline__ void put(uint32_t i, const PieceInfo& c, int lane) {
+    __device__ __forceinline__ void put(const Ctl& ctl, uint32_t i, const PieceInfo& c, int lane) {
+        if (i >= kPieces) wait(ctl, smem_u32(&empty[i % kPieces]), (i / kPieces - 1) & 1);
         if (lane == 0) {
             piece[i % kPieces] = c;
             mbar_arrive(smem_u32(&full[i % kPieces]));
         }
         __syncwarp();
     }
-    // The i-th piece, as the other warps see it (no rows after a wait that ran out).
-    __device__ __forceinline__ PieceInfo get(const Ctl& ctl, uint32_t i) {
+    // Waits for the i-th piece; its rows (none after a wait that ran out).
+    __device__ __forceinline__ int get(const Ctl& ctl, uint32_t i) const {
         wait(ctl, smem_u32(&full[i % kPieces]), (i / kPieces) & 1);
-        PieceInfo c = piece[i % kPieces];
-        if (*reinterpret_cast<volatile int*>(ctl.abort)) c.rows = 0;
-        c.rows = uniform(c.rows);
-        c.n = uniform(c.n);
-        return c;
+        return uniform(*reinterpret_cast<volatile int*>(ctl.abort) ? 0 : piece[i % kPieces].rows);
+    }
+    __device__ __forceinline__ const PieceInfo& at(uint32_t i) const { return piece[i % kPieces]; }
+    __device__ __forceinline__ void done(uint32_t i) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&empty[i % kPieces]));
+        __syncwarp();
     }
 };
 
-// After a wait that ran out: gives copies and products in flight time to land before the block's shared and
-// tensor memory is handed on.
-__device__ __forceinline__ void settle(int* abort) {
-    if (!*reinterpret_cast<volatile int*>(abort)) return;
+// After a wait that ran out: records the error, and gives copies and products in flight time to land before the block's
+// shared and tensor memory is handed on.
+__device__ __forceinline__ void settle(const Ctl& c) {
+    if (!*reinterpret_cast<volatile int*>(c.abort)) return;
+    raise_error(c.ws, kErrTimeout);
     const unsigned long long t0 = now_ns();
     while (now_ns() - t0 < 20000000ull) __nanosleep(1000);
 }
@@ -241,31 +245,34 @@ struct Filler {
     uint32_t stages, ring, st, round;
     __device__ __forceinline__ Filler(const CUtensorMap* m, uint64_t* f, uint64_t* e, int n, uint32_t addr)
         : map(m), full(f), empty(e), stages(n), ring(addr), st(0), round(0) {}
-    // the tiles of a piece; false after a wait that ran out
-    __device__ __forceinline__ bool fill(const AttnParams& p, const Ctl& ctl, const PieceInfo& c, int lane) {
+    // A lane's page id among the 32 boxes of a piece from 32 * batch on.
+    __device__ __forceinline__ int page_id(const AttnParams& p, const PieceInfo& c, int batch, int lane) {
+        const int at = (32 * batch + lane) << min(p.page_shift, 7);
+        return at < min(c.n * kTile, c.end - c.key0) ? __ldg(p.table + (long long)c.seq * p.pages_per_seq + ((c.key0 + at) >> p.page_shift)) : 0;
+    }
+    __device__ __forceinline__ int checked(const AttnParams& p, int id) {
+        if (id < 0 || id >= p.num_pages) {
+            raise_error(p.ws, kErrRange);
+            id = 0;
+        }
+        return id;
+    }
+    // the tiles of a piece, whose first 32 ids were read before; false after a wait that ran out
+    __device__ __forceinline__ bool fill(const AttnParams& p, const Ctl& ctl, const PieceInfo& c, int id, int lane) {
         const int hkv = c.hkv, n = c.n, key0 = c.key0;
-        const int box_shift = p.page_shift < 7 ? p.page_shift : 7, box = 1 << box_shift, nbox = kTile >> box_shift;
-        const int32_t* row = p.table + (long long)c.seq * p.pages_per_seq;
+        const int box_shift = min(p.page_shift, 7), box = 1 << box_shift, nbox = kTile >> box_shift;
         const int last = min(n * kTile, c.end - key0);  // end of the positions
-        auto ids = [&](int batch) {  // of the 32 boxes from 32 * batch on
-            const int at = (32 * batch + lane) << box_shift;
-            int id = at < last ? __ldg(row + ((key0 + at) >> p.page_shift)) : 0;
-            if (id < 0 || id >= p.num_pages) {
-                raise_error(p.ws, kErrRange);
-                id = 0;
-            }
-            return id;
-        };
         const int bytes = box * D * 2;
-        int id = ids(0), next = ids(1), batch = 1;
+        int next = page_id(p, c, 1, lane), batch = 1;
+        id = checked(p, id);
 #pragma unroll 1
         for (int t = 0, x = 0; t < n; ++t, x += nbox) {
             if (x == 32) {
                 x = 0;
-                id = next;
-                next = ids(++batch);
+                id = checked(p, next);
+                next = page_id(p, c, ++batch, lane);
             }
-            if (round > 0) wait(ctl, smem_u32(&empty[st]), (round - 1) & 1);
+            wait(ctl, smem_u32(&empty[st]), (round & 1) ^ 1);  // at once the first time round
             if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(ctl.abort))) return false;
             const int ust = uniform(st), boxes = uniform(min(nbox, (last - t * kTile + box - 1) >> box_shift));
             const uint32_t bar = smem_u32(&full[ust]);
@@ -300,27 +307,38 @@ __device__ __forceinline__ int tile_steps(int keys) { return (min(keys, kTile) +
 // every n-th 16 bytes; true if it found some.
 template <int D>
 __device__ __forceinline__ bool clean_values(uint32_t tile, int first, int keys, int i, int n) {
+    auto at = [&](int x) {
+        const int r = x / (D / 8), ch = x % (D / 8);
+        return tile + (r >> 3) * TileGeo<D>::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 + (ch & 7) * 16;
+    };
+    const int nodes = min(keys, kTile) * (D / 8), end = 16 * tile_steps(keys) * (D / 8);
     bool found = false;
 #pragma unroll 1
-    for (int x = first * (D / 8) + i; x < 16 * tile_steps(keys) * (D / 8); x += n) {
-        const int r = x / (D / 8), ch = x % (D / 8);
-        const uint32_t at = tile + (r >> 3) * TileGeo<D>::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 + (ch & 7) * 16;
-        uint32_t v[4];
-        if (r >= keys) {
-            v[0] = v[1] = v[2] = v[3] = 0;
-        } else {
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+    for (int x = first * (D / 8) + i; x < nodes; x += 2 * n) {
+        uint32_t v[2][4];
+#pragma unroll
+        for (int y = 0; y < 2; ++y)  // the last one twice rather than none
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v[y][0]), "=r"(v[y][1]), "=r"(v[y][2]), "=r"(v[y][3])
+                         : "r"(at(x + y * n < nodes ? x + y * n : x))
+                         : "memory");
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
             bool bad = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u, bad = true;
-                if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0x0000ffffu, bad = true;
+                if ((v[y][e] & 0x7f80u) == 0x7f80u) v[y][e] &= 0xffff0000u, bad = true;
+                if ((v[y][e] & 0x7f800000u) == 0x7f800000u) v[y][e] &= 0x0000ffffu, bad = true;
             }
             if (!bad) continue;
             found = true;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at(x + y * n < nodes ? x + y * n : x)), "r"(v[y][0]), "r"(v[y][1]),
+                         "r"(v[y][2]), "r"(v[y][3])
+                         : "memory");
         }
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
     }
+#pragma unroll 1
+    for (int x = nodes + i; x < end; x += n) asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at(x)), "r"(0) : "memory");
     return found;
 }
 

@@ -46,6 +46,10 @@ bool attn_sizes_ok(int S, int N, int T, int Hq, int Hkv, int D) {
 // sequence (narrow) or 256 (wide).
 enum AttnKind { kSimt, kNarrow, kWide };
 constexpr int kSimtBlocksPerSm = 2;
+// What a unit of the tensor-core kernels costs besides its tiles, in tiles: 0, 1, 2, 3, 4 took 123, 104, 111, 118 and 124 us for 8
+// groups of 16 sequences, whose shared units have dearer tiles than the short units of the sequences, and 170, 168, 167, 165 and
+// 165 us for 64 sequences of 21 nodes over 4096 tokens.
+constexpr int kEmptyGroups = 1, kEmptyPlaces = 3;
 
 AttnKind kind_of(int dtype, int T, int Hq, int Hkv) {
     if (dtype == SMCSD_F32) return kSimt;
@@ -195,23 +199,23 @@ extern "C" int tree_attention(const void* q, long long q_stride, const void* k_c
     p.ws = ws;
     cudaStream_t st = (cudaStream_t)stream;
     const AttnKind kind = kind_of(dtype, T, Hq, Hkv);
-    if (p.G > 0 && (long long)Hkv * attn_blocks((long long)T * p.gq, rows_of(kind)) > 65535) return SMCSD_ERR_INVALID_ARG;
-    // all tiles of all units are numbered in 32 bits
+    // all places of all units are numbered in 32 bits
     const long long units = (long long)S * Hkv * attn_blocks((long long)T * p.gq, rows_of(kind)) +
                             (long long)p.G * Hkv * attn_blocks((long long)N * T * p.gq, rows_of(kind));
-    if (units * (((long long)pages_per_seq * page_size + 63) / 64) > 0x7fffffffLL) return SMCSD_ERR_INVALID_ARG;
+    if (units * (((long long)pages_per_seq * page_size + 63) / 64 + kEmptyPlaces) > 0x7fffffffLL) return SMCSD_ERR_INVALID_ARG;
     p.L = layout_of(kind, S, N, T, Hq, Hkv, D);
     p.log_tile = kind == kSimt ? 6 : 7;
     p.log_rb = kind == kSimt ? 4 : kind == kNarrow ? 7 : 8;
+    p.empty = kind == kSimt ? 0 : p.G > 0 ? kEmptyGroups : kEmptyPlaces;
     p.div_gq = make_fastdiv((uint32_t)p.gq);
     p.ncta_max = device_sm_count() * (kind == kSimt ? kSimtBlocksPerSm : 1);
     if (p.ncta_max > kAttnMaxCta) p.ncta_max = kAttnMaxCta;
     p.div_cta = make_fastdiv((uint32_t)p.ncta_max);
-    p.planned = p.G > 0 || S > kAttnWarpPlan;
+    p.planned = attn_planned(S, N);
     cudaError_t e = p.planned ? launch_attn_plan(p, st) : cudaSuccess;
     if (e == cudaSuccess)
         e = kind == kSimt ? launch_attn_simt(p, st) : kind == kNarrow ? launch_attn_narrow(p, st) : launch_attn_wide(p, st);
-    if (e == cudaSuccess && p.G > 0) e = launch_attn_combine(p, dtype, st);
+    if (e == cudaSuccess && p.planned) e = launch_attn_combine(p, dtype, st);
     return from_cuda(e);
 }
 

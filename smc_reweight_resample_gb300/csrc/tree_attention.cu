@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         __syncthreads();
         if (!last) return;
     }
-    // tiles (high word) and units (low word) before each item: a thread has a run of them
+    // places (high word) and units (low word) before each item: a thread has a run of them
     AttnItem* items = ws_ptr<AttnItem>(p.ws, p.L.item);
     const int n = p.G + p.S, per = (n + kPlanThreads - 1) / kPlanThreads;
     const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     for (int i = i0; i < i1; ++i) {
         it = plan_item(p, shared, i);
         const long long u = attn_units(p, it);
-        mine += ((u * it.tiles) << 32) + u;
+        mine += ((u * (it.tiles + p.empty)) << 32) + u;
     }
     long long at = plan_prefix(mine, sums, total);
     for (int i = i0; i < i1; ++i) {
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         it.cum = (int)(at >> 32);
         it.unit0 = (int)(at & 0xffffffffll);
         items[i] = it;
-        at += ((u * it.tiles) << 32) + u;
+        at += ((u * (it.tiles + p.empty)) << 32) + u;
         if (i == p.G - 1) attn_head(p)->units_shared = (int)(at & 0xffffffffll);
     }
     if (tid == 0) {
@@ -161,7 +161,7 @@ constexpr int simt_smem() {
 // One block per share of the line; 16 rows x 64 keys at a time. A thread takes one key and 8 rows for
 // the scores, one column (or, for D = 64, one column of half the rows) for the values. The running
 // maximum m (of z / ln 2) and sum l of a row rescale what is there when the maximum grows.
-template <int D>
+template <int D, bool kPlanned>
 __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_constant__ AttnParams p) {
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;                                // [16][D]
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
     __shared__ PieceInfo s_piece, s_pending[2];
     __shared__ int s_last[2];
     int pending = 0;
-    Walker walk;
+    Walker<kPlanned> walk;
     if (warp == 0) walk.begin(p, lane);
     for (;;) {
         if (warp == 0) {
@@ -313,12 +313,12 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(const __grid_co
         }
         __syncthreads();
     }
-    if (pending > 0) attn_join_last<0, D, 2, 4>(p, s_pending, pending, tid, kSimtThreads, s_last, [] { __syncthreads(); });
+    if (!kPlanned && pending > 0) attn_join_last<0, D, 1, 4>(p, s_pending, pending, tid, kSimtThreads, s_last, [] { __syncthreads(); });
 }
 
 template <int D>
 static cudaError_t launch_simt_t(const AttnParams& p, cudaStream_t st) {
-    auto kern = attn_simt_kernel<D>;
+    auto kern = p.planned ? attn_simt_kernel<D, true> : attn_simt_kernel<D, false>;
     constexpr int smem = simt_smem<D>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -340,7 +340,7 @@ cudaError_t launch_attn_simt(const AttnParams& p, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------------------
-// joining the pieces of groups
+// joining the pieces after the planning kernel
 // ------------------------------------------------------------------------------------------
 
 constexpr int kJoinThreads = 256;
@@ -351,16 +351,11 @@ struct JoinRun {
     const float2* ml;
     size_t rows;  // of a slot
     int count;
-    template <int D>
-    __device__ __forceinline__ void add_to(AttnJoin& j, int col) const {
-#pragma unroll 4
-        for (int i = 0; i < count; ++i)
-            j.add(__ldcg(ml + i * rows), __ldcg(reinterpret_cast<const float4*>(o + i * rows * D + col)));
-    }
 };
 
-// Where groups share keys: a few blocks (z) for each sequence (x) and unit of it (y). A row's pieces are joined in the
-// order of the line, the shared unit's first: 4 columns a thread.
+// After the planning kernel: a few blocks (z) for each sequence (x) and unit of it (y). A row's pieces are joined in the
+// order of the line, the shared unit's first: a warp has a row (of 64 columns: two), four columns a thread, and the first two
+// pieces of both units are loaded together.
 template <int DT, int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid_constant__ AttnParams p) {
     griddep_wait();
@@ -370,43 +365,66 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
     AttnCut cut;
     cut.base = h->base;
     cut.rest = h->rest;
-    const AttnItem it = items[p.G + blockIdx.x], grp = items[blockIdx.x / p.N];
-    const int u = blockIdx.y;
-    if (it.tiles == 0 || u >= p.Hkv * it.nrb) return;
-    const int hkv = u / it.nrb, row0 = (u - hkv * it.nrb) * it.per, rows = min(it.per, it.nodes * p.gq - row0);
-    const int x0 = it.cum + u * it.tiles, c0 = cut.block(x0), own_count = cut.block(x0 + it.tiles - 1) - c0 + 1;
-    const size_t own_slot = (size_t)(it.unit0 + u - h->units_shared + c0);
-    const bool shared = grp.tiles > 0;
-    if (!shared && own_count == 1) return;  // written directly
+    const AttnItem it = items[p.G + blockIdx.x], grp = items[p.G > 0 ? blockIdx.x / p.N : 0];
+    if (it.tiles == 0) return;
+    const bool shared = p.G > 0 && grp.tiles > 0;
     constexpr int kLanes = D / 4, kRows = 32 / kLanes;  // lanes of a row, rows of a warp at a time
     const int col = (lane % kLanes) * 4;
     const int step = gridDim.z * (kJoinThreads / 32) * kRows;
-    for (int r = (blockIdx.z * (kJoinThreads / 32) + warp) * kRows + lane / kLanes; r < rows; r += step) {
-        const int row = row0 + r, n = attn_node(p, row);
-        AttnJoin j;
-        JoinRun run;
-        if (shared) {
-            const int gr = row + (it.node0 - grp.node0) * p.gq, rb = gr / grp.per, gu = hkv * grp.nrb + rb;
-            const int g0 = grp.cum + gu * grp.tiles, b0 = cut.block(g0);
-            const size_t at = (size_t)(grp.unit0 + gu + b0) * p.L.rows_g + (gr - rb * grp.per);
-            run = JoinRun{ws_ptr<float>(p.ws, p.L.slot_g) + at * D, ws_ptr<float2>(p.ws, p.L.ml_g) + at, (size_t)p.L.rows_g,
-                          cut.block(g0 + grp.tiles - 1) - b0 + 1};
-            run.add_to<D>(j, col);
+#pragma unroll 1
+    for (int u = blockIdx.y; u < p.Hkv * it.nrb; u += gridDim.y) {
+        const int hkv = u / it.nrb, row0 = (u - hkv * it.nrb) * it.per, rows = min(it.per, it.nodes * p.gq - row0);
+        const int x0 = it.cum + u * (it.tiles + p.empty) + p.empty, c0 = cut.block(x0), own_count = cut.block(x0 + it.tiles - 1) - c0 + 1;
+        if (!shared && own_count == 1) continue;  // written directly
+#pragma unroll 1
+        for (int r = (blockIdx.z * (kJoinThreads / 32) + warp) * kRows + lane / kLanes; r < rows; r += step) {
+            const int row = row0 + r, n = attn_node(p, row);
+            JoinRun run[2];
+            run[0].count = 0;
+            if (shared) {
+                const int gr = row + (it.node0 - grp.node0) * p.gq, rb = gr / grp.per, gu = hkv * grp.nrb + rb;
+                const int g0 = grp.cum + gu * (grp.tiles + p.empty) + p.empty, b0 = cut.block(g0);
+                const size_t at = (size_t)(grp.unit0 + gu + b0) * p.L.rows_g + (gr - rb * grp.per);
+                run[0] = JoinRun{ws_ptr<float>(p.ws, p.L.slot_g) + at * D, ws_ptr<float2>(p.ws, p.L.ml_g) + at, (size_t)p.L.rows_g,
+                                 cut.block(g0 + grp.tiles - 1) - b0 + 1};
+            }
+            const size_t at = (size_t)(it.unit0 + u - h->units_shared + c0) * p.L.rows_s + r;
+            run[1] = JoinRun{ws_ptr<float>(p.ws, p.L.slot_s) + at * D, ws_ptr<float2>(p.ws, p.L.ml_s) + at, (size_t)p.L.rows_s, own_count};
+            float2 s[4];
+            float4 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const JoinRun& of = run[x >> 1];
+                s[x] = make_float2(0, 0);
+                v[x] = make_float4(0, 0, 0, 0);
+                if ((x & 1) < of.count) {
+                    s[x] = __ldcg(of.ml + (x & 1) * of.rows);
+                    v[x] = __ldcg(reinterpret_cast<const float4*>(of.o + (x & 1) * of.rows * D + col));
+                }
+            }
+            AttnJoin j;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                j.add(s[x], v[x]);
+                if (x & 1) {
+#pragma unroll 2
+                    for (int i = 2; i < run[x >> 1].count; ++i)
+                        j.add(__ldcg(run[x >> 1].ml + i * run[x >> 1].rows),
+                              __ldcg(reinterpret_cast<const float4*>(run[x >> 1].o + i * run[x >> 1].rows * D + col)));
+                }
+            }
+            j.store<DT, D>(p, (size_t)(it.node0 + n) * p.Hq + hkv * p.gq + (row - n * p.gq), col);
         }
-        const size_t at = own_slot * p.L.rows_s + r;
-        run = JoinRun{ws_ptr<float>(p.ws, p.L.slot_s) + at * D, ws_ptr<float2>(p.ws, p.L.ml_s) + at, (size_t)p.L.rows_s, own_count};
-        run.add_to<D>(j, col);
-        j.store<DT, D>(p, (size_t)(it.node0 + n) * p.Hq + hkv * p.gq + (row - n * p.gq), col);
     }
 }
 
 template <int DT, int D>
 static cudaError_t launch_combine_t(const AttnParams& p, cudaStream_t st) {
-    // a block's eight warps take up to four rows each
-    const long long rows = (long long)p.T * p.gq;
-    const unsigned parts = (unsigned)((rows < (1 << p.log_rb) ? rows : (1 << p.log_rb)) + 31) / 32;
+    // a warp takes one row (four rows each, loads of its pieces one after the other: 21 us in place of 17 for 1024 units of 20 rows)
+    const long long rows = (long long)p.T * p.gq, units = (long long)p.Hkv * attn_blocks(rows, 1 << p.log_rb);
+    const unsigned parts = (unsigned)((rows < (1 << p.log_rb) ? rows : (1 << p.log_rb)) + 7) / 8;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)p.S, (unsigned)(p.Hkv * attn_blocks(rows, 1 << p.log_rb)), parts);
+    cfg.gridDim = dim3((unsigned)p.S, (unsigned)(units < 65535 ? units : 65535), parts);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at{};

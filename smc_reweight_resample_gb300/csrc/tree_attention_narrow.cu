@@ -48,60 +48,68 @@ struct __align__(16) NarrowShared {
     PieceRing pieces;
     Ring<NarrowGeo<D>::kKeys> rk;
     Ring<NarrowGeo<D>::kValues> rv;
-    uint64_t q_full[2], q_empty[2], v_full[2];
-    uint64_t s_full[4][2], o_full[4][2];  // [tile of a round][buffer]
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[4][2], o_full[4][2];  // [tile of a round, or a single group][buffer]
     uint64_t p_full[4][2];                // [group][buffer]
     uint32_t tmem;
     int abort;
-    int poison[2];  // by the piece's parity: a NaN or infinity among the values of its nodes
+    uint32_t poison[kPieces];  // i + 1: a NaN or infinity among the values of the i-th piece's nodes
 };
 
 // Places of the query rows: a piece of up to 64 rows takes the next of the two, a larger one both.
 struct QuerySlots {
-    uint32_t uses[2] = {0, 0};
-    int next = 0;
-    int slot;
-    bool both;
+    uint32_t uses = 0;  // parities
+    int next = 0, first, last;
     __device__ __forceinline__ void take(int rows) {
-        both = rows > 64;
-        slot = both ? 0 : next;
+        const bool both = rows > 64;
+        first = both ? 0 : next;
+        last = both ? 2 : next + 1;
         next = both ? 0 : next ^ 1;
     }
     template <typename F>
-    __device__ __forceinline__ void each(F f) {  // f(place, how often it was taken before)
-        if (both || slot == 0) f(0, uses[0]);
-        if (both || slot == 1) f(1, uses[1]);
+    __device__ __forceinline__ void each(F f) {  // f(place, parity of how often it was taken before)
+#pragma unroll 1
+        for (int x = first; x < last; ++x) f(x, (uses >> x) & 1u);
     }
-    __device__ __forceinline__ void done() {
-        if (both || slot == 0) ++uses[0];
-        if (both || slot == 1) ++uses[1];
-    }
+    __device__ __forceinline__ void done() { uses ^= (1u << last) - (1u << first); }
 };
 
-// How a unit's rows and tiles are laid over the four groups.
+// How a piece's rows and tiles are laid over the four groups: all of them on one piece, or (a short piece of few rows) the next
+// group alone, so that up to four such pieces are under way and the waits of one are filled by the others.
+constexpr int kSoloTiles = 4;
 struct Split {
     int log_tiles;  // tiles of a round: 4, 2 or 1
     int log_chunks; // groups side by side on the rows of one tile: 1, 2 or 4
     int used;       // chunks that have rows
-    __device__ __forceinline__ explicit Split(int rows) {
+    bool solo;      // one group has it
+    int first;      // that group, or the first one
+    // `turn`: the group that takes the next such piece
+    __device__ __forceinline__ Split(int rows, int n, int& turn) {
+        solo = rows <= 32 && n <= kSoloTiles;
         log_chunks = (rows > 32) + (rows > 64);
-        log_tiles = 2 - log_chunks;
+        log_tiles = solo ? 0 : 2 - log_chunks;
         used = (rows + 31) >> 5;
+        first = solo ? turn : 0;
+        turn = (turn + solo) & 3;
     }
+    // barriers and first group of tile k of a round
+    __device__ __forceinline__ int bar(int k) const { return first + k; }
+    __device__ __forceinline__ int group(int k) const { return first + (k << log_chunks); }
     __device__ __forceinline__ int tiles() const { return 1 << log_tiles; }
     __device__ __forceinline__ int chunks() const { return 1 << log_chunks; }
     // tiles of n that are number k of their round
     __device__ __forceinline__ int rounds(int n, int k) const { return (n - k + tiles() - 1) >> log_tiles; }
 };
 
-// How often the barriers of (tile of a round, buffer) were used by earlier pieces: parities, bit 2 k + b.
+// How often the barriers of [k][buffer b] were used by earlier pieces: parities, bit 2 k + b.
 struct Uses {
     uint32_t bits;
     __device__ __forceinline__ uint32_t parity(int k, int b, int use) const { return ((bits >> (2 * k + b)) ^ use) & 1u; }
     __device__ __forceinline__ void add(int n, const Split& sp) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const uint32_t r = k < sp.tiles() ? sp.rounds(n, k) : 0;
+            const int x = k - sp.first;
+            const uint32_t r = x >= 0 && x < sp.tiles() ? sp.rounds(n, x) : 0;
             bits ^= (((r + 1) >> 1) & 1u) << (2 * k) | ((r >> 1) & 1u) << (2 * k + 1);
         }
     }
@@ -109,59 +117,86 @@ struct Uses {
 
 // ---- pieces, keys, query rows and values ----
 
-// Two warps in one piece of code (it is long): the one with `keys` walks and brings the pages of keys, the other the query
-// rows and the pages of values.
+// A piece's query rows, and rows of zeros (scores of zero) up to a multiple of 32. A lane has one 16-byte column and every
+// second or fourth row: eight rows a turn, with a few additions each (a division for each row and a long address took 3000
+// clocks for 32 rows, and this warp's turn for a piece was what bound short ones).
 template <int D>
+__device__ __forceinline__ void narrow_queries(const AttnParams& p, const PieceInfo& c, uint32_t to, int lane) {
+    constexpr int kCols = D / 8, kStep = 32 / kCols;
+    const int ch = lane % kCols, r0 = lane / kCols, node = attn_node(p, c.row0 + r0);
+    int h = c.row0 + r0 - node * p.gq;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+    const __nv_bfloat16* from = q + (size_t)(c.node0 + node) * p.q_stride + (size_t)(c.hkv * p.gq + h) * D + ch * 8;
+    const int nodes = attn_node(p, kStep), heads = kStep - nodes * p.gq;  // from one row of this lane to the next
+    const long long step = nodes * p.q_stride + heads * D, wrap = p.q_stride - (long long)p.gq * D;
+    const uint32_t at = (uint32_t)((ch & 7) ^ r0) << 4;
+    to += (ch >> 3) * 1024 + r0 * 128;
+#pragma unroll 1
+    for (int r = r0; r < ((c.rows + 31) & ~31); r += 8, to += TileGeo<D>::kGroup) {
+#pragma unroll
+        for (int y = 0; y < 8; y += kStep) {
+            const bool there = r + y < c.rows;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + y * 128 + (at ^ (y << 4))), "l"(there ? from : q),
+                         "r"(there ? 16 : 0)
+                         : "memory");
+            from += step;
+            h += heads;
+            if (h >= p.gq) h -= p.gq, from += wrap;
+        }
+    }
+}
+
+// Two warps in one piece of code (it is long): the one with `keys` walks and brings the pages of keys, the other the query rows
+// and the pages of values. The next piece, its query rows and its first page ids are fetched before the present one's tiles have
+// to wait for places.
+template <int D, bool kPlanned>
 __device__ void narrow_fill(const AttnParams& p, bool keys, const CUtensorMap* map, const Ctl& ctl, NarrowShared<D>* sh, uint32_t sq,
                             uint32_t ring, int lane) {
     using G = NarrowGeo<D>;
     Filler<D> filler(map, keys ? sh->rk.full : sh->rv.full, keys ? sh->rk.empty : sh->rv.empty, keys ? G::kKeys : G::kValues, ring);
     QuerySlots qs;
-    Walker walk;
+    Walker<kPlanned> walk;
     if (keys) walk.begin(p, lane);
+    int id = 0, rows = 0;  // of the piece before
 #pragma unroll 1
     for (uint32_t i = 0;; ++i) {
-        PieceInfo c;
+        int rows_ahead;
         if (keys) {
-            walk.next(p, c, lane);
-            qs.take(c.rows);
-            // Once the scores that read this place last are done, everybody is past piece i - 4 (the scores of a piece
-            // wait for all weights of the one before), and its description may be written over.
-            qs.each([&](int x, uint32_t uses) {
-                if (uses > 0) wait(ctl, smem_u32(&sh->q_empty[x]), (uses - 1) & 1);
-            });
-            sh->pieces.put(i, c, lane);
+            PieceInfo next;
+            walk.next(p, next, lane);
+            sh->pieces.put(ctl, i, next, lane);
+            rows_ahead = next.rows;
         } else {
-            c = sh->pieces.get(ctl, i);  // the place of its query rows is free
-            qs.take(c.rows);
+            rows_ahead = sh->pieces.get(ctl, i);
         }
-        if (c.rows == 0) break;
-        if (!keys) {
-            // rows of zeros up to a multiple of 32: scores of zero
-            const int padded = (c.rows + 31) & ~31;
-            const uint32_t to = sq + qs.slot * G::kSlot;
-#pragma unroll 2
-            for (int x = lane; x < padded * (D / 8); x += 32) {
-                const int r = x / (D / 8), ch = x - r * (D / 8);
-                const int row = c.row0 + min(r, c.rows - 1), node = attn_node(p, row), hq = c.hkv * p.gq + (row - node * p.gq);
-                const void* from = static_cast<const __nv_bfloat16*>(p.q) + (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + ch * 8;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + TileGeo<D>::at(r, ch)), "l"(from),
-                             "r"(r < c.rows ? 16 : 0)
-                             : "memory");
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_async_smem();
+        const PieceInfo &c = sh->pieces.at(i - 1), &ahead = sh->pieces.at(i);
+        const bool more = rows_ahead > 0;
+        const int id_ahead = more ? filler.page_id(p, ahead, 0, lane) : 0;
+        // Query rows ahead of this piece's values only where they do not take its own places: those are free when its scores are
+        // done, for which its values are needed.
+        const bool early = max(rows, rows_ahead) <= 64;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            if (pass == 1 && i > 0 && !filler.fill(p, ctl, c, id, lane)) return;
+            if (keys || !more || early != (pass == 0)) continue;
+            qs.take(rows_ahead);
+            qs.each([&](int x, uint32_t uses) { wait(ctl, smem_u32(&sh->q_empty[x]), uses ^ 1); });  // at once the first time
+            narrow_queries<D>(p, ahead, sq + qs.first * G::kSlot, lane);
+            // reported by the copies themselves; the warp that issues the scores has the fence
+            qs.each([&](int x, uint32_t) {
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh->q_full[x])) : "memory");
+            });
             __syncwarp();
-            if (lane == 0) qs.each([&](int x, uint32_t) { mbar_arrive(smem_u32(&sh->q_full[x])); });
-            __syncwarp();
+            qs.done();
         }
-        qs.done();
-        if (!filler.fill(p, ctl, c, lane)) return;
+        if (!keys && i > 0) sh->pieces.done(i - 1);
+        if (!more) break;
+        rows = rows_ahead;
+        id = id_ahead;
     }
     // the last scores' reports land before the block ends
-    if (keys)
-        for (int x = 0; x < 2; ++x)
-            if (qs.uses[x] > 0) wait(ctl, smem_u32(&sh->q_empty[x]), (qs.uses[x] - 1) & 1);
+    if (!keys)
+        for (int x = 0; x < 2; ++x) wait(ctl, smem_u32(&sh->q_empty[x]), ((qs.uses >> x) & 1) ^ 1);
 }
 
 // ---- products ----
@@ -170,43 +205,52 @@ __device__ void narrow_fill(const AttnParams& p, bool keys, const CUtensorMap* m
 struct Weights {
     uint32_t bits = 0;
     template <int D>
-    __device__ __forceinline__ void wait_for(const Ctl& ctl, NarrowShared<D>* sh, const Split& split, int t) {
-        const int k = t & (split.tiles() - 1), b = (t >> split.log_tiles) & 1;
-        for (int x = 0; x < split.used; ++x) {
-            const int bit = 2 * ((k << split.log_chunks) + x) + b;
-            wait(ctl, smem_u32(&sh->p_full[0][0]) + 8 * bit, (bits >> bit) & 1);
-            bits ^= 1u << bit;
-        }
+    __device__ __forceinline__ void wait_for(const Ctl& ctl, NarrowShared<D>* sh, int bit) {
+        wait(ctl, smem_u32(&sh->p_full[0][0]) + 8 * bit, (bits >> bit) & 1);
+        bits ^= 1u << bit;
     }
 };
 
+// A buffer of scores is free when its group's weights are there (`out`: those not yet waited for). Where all groups take part in
+// this piece or the one before, everybody has to be through with that one, since they wait for each other's barriers; pieces of
+// single groups have barriers of their own.
 template <int D>
 __device__ void narrow_scores(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, uint32_t sq, uint32_t ring_k, uint32_t tmem) {
     using G = NarrowGeo<D>;
     Weights weights;
     QuerySlots qs;
-    uint32_t st = 0, round = 0;
-    int left = 0;  // tiles of the piece before whose weights are still to be waited for
-    Split before(1);
-    int n_before = 0;
+    uint32_t st = 0, round = 0, out = 0;
+    int turn = 0;
+    bool solo = false;
+    auto drain = [&](uint32_t some) {
+        some &= out;
+        out ^= some;
+        for (; some; some &= some - 1) weights.wait_for(ctl, sh, __ffs(some) - 1);
+    };
     for (uint32_t i = 0;; ++i) {
-        const PieceInfo c = sh->pieces.get(ctl, i);
-        if (c.rows == 0) return;
-        const Split split(c.rows);
-        const int ahead = 2 * split.tiles(), width = 32 * split.chunks();
-        qs.take(c.rows);
-        qs.each([&](int x, uint32_t uses) { wait(ctl, smem_u32(&sh->q_full[x]), uses & 1); });
-        for (; left > 0; --left) weights.wait_for(ctl, sh, before, n_before - left);
+        const int rows = sh->pieces.get(ctl, i);
+        if (rows == 0) return;
+        const int n = uniform(sh->pieces.at(i).n);
+        sh->pieces.done(i);
+        const Split split(rows, n, turn);
+        qs.take(rows);
+        qs.each([&](int x, uint32_t uses) { wait(ctl, smem_u32(&sh->q_full[x]), uses); });
+        fence_async_smem();
+        if (!split.solo || !solo) drain(~0u);
+        solo = split.solo;
         const uint32_t is = instruction(32 * split.used, 0, 0);
-        const uint64_t qb = operand(sq + qs.slot * G::kSlot, TileGeo<D>::kGroup, 0);
+        const uint64_t qb = operand(sq + qs.first * G::kSlot, TileGeo<D>::kGroup, 0);
 #pragma unroll 1
-        for (int t = 0; t < c.n; ++t) {
+        for (int t = 0; t < n; ++t) {
             const int k = t & (split.tiles() - 1), b = (t >> split.log_tiles) & 1;
+            // bits 2 * group + b of the tile's groups
+            const uint32_t groups = ((1u << 2 * split.used) - 1) / 3 << (2 * split.group(k) + b);
             wait(ctl, smem_u32(&sh->rk.full[st]), round & 1);
-            if (t >= ahead) weights.wait_for(ctl, sh, split, t - ahead);  // the buffer's last scores have been read
+            drain(groups);
+            out |= groups;
             tc_fence_after();
             const uint64_t ka = operand(ring_k + st * G::kStage, TileGeo<D>::kGroup, 0);
-            const uint32_t to = tmem + 128 * b + width * k;
+            const uint32_t to = tmem + 128 * b + 32 * split.group(k);
             if (elect_one()) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
@@ -214,7 +258,7 @@ __device__ void narrow_scores(const AttnParams& p, const Ctl& ctl, NarrowShared<
                     mma_ss(to, ka + at, qb + at, is, x > 0);
                 }
                 tc_commit(smem_u32(&sh->rk.empty[st]));
-                tc_commit(smem_u32(&sh->s_full[k][b]));
+                tc_commit(smem_u32(&sh->s_full[split.bar(k)][b]));
             }
             __syncwarp();
             if (++st == G::kKeys) st = 0, ++round;
@@ -222,9 +266,6 @@ __device__ void narrow_scores(const AttnParams& p, const Ctl& ctl, NarrowShared<
         if (elect_one()) qs.each([&](int x, uint32_t) { tc_commit(smem_u32(&sh->q_empty[x])); });
         __syncwarp();
         qs.done();
-        left = min(c.n, ahead);
-        n_before = c.n;
-        before = split;
     }
 }
 
@@ -232,28 +273,32 @@ template <int D>
 __device__ void narrow_outputs(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, uint32_t sp, uint32_t ring_v, uint32_t tmem) {
     using G = NarrowGeo<D>;
     Weights weights;
-    uint32_t st = 0, round = 0, tails = 0;
+    uint32_t st = 0, round = 0;
+    int turn = 0;
     for (uint32_t i = 0;; ++i) {
-        const PieceInfo c = sh->pieces.get(ctl, i);
-        if (c.rows == 0) return;
-        const Split split(c.rows);
-        const int width = 32 * split.chunks(), first_tail = c.first_tail(7);
+        const int rows = sh->pieces.get(ctl, i);
+        if (rows == 0) return;
+        const PieceInfo& c = sh->pieces.at(i);
+        const int n = uniform(c.n), first_tail = c.first_tail(7), keys = uniform(c.end - c.key0);
+        const Split split(rows, n, turn);
         const uint32_t io = instruction(32 * split.used, 1, 1);
 #pragma unroll 1
-        for (int t = 0; t < c.n; ++t) {
-            const int k = t & (split.tiles() - 1), r = t >> split.log_tiles, b = r & 1;
+        for (int t = 0; t < n; ++t) {
+            const int k = t & (split.tiles() - 1), r = t >> split.log_tiles, b = r & 1, g = split.group(k);
             wait(ctl, smem_u32(&sh->rv.full[st]), round & 1);
-            if (t >= first_tail) {
-                if (elect_one()) mbar_arrive(smem_u32(&sh->v_full[tails & 1]));
-                ++tails;
+            if (t >= first_tail) {  // while the weights are worked out
+                if (clean_values<D>(ring_v + st * G::kStage, max(c.ctx - c.key0 - t * kTile, 0), keys - t * kTile, threadIdx.x & 31, 32))
+                    *reinterpret_cast<volatile uint32_t*>(&sh->poison[i % kPieces]) = i + 1;
+                fence_async_smem();
+                __syncwarp();
             }
-            weights.wait_for(ctl, sh, split, t);
+            for (int x = 0; x < split.used; ++x) weights.wait_for(ctl, sh, 2 * (g + x) + b);
             tc_fence_after();
             // 64 columns of V have no second block: the upper half of the outputs repeats the lower one
             const uint64_t va = operand(ring_v + st * G::kStage, TileGeo<D>::kGroup, D == 128 ? 1024 : 0);
-            const uint64_t pb = operand(sp + (width * k / 64) * G::kBlock + (width * k % 64) * 2, 1024, G::kBlock);
-            const uint32_t to = tmem + 256 + width * k, more = r > 0;
-            const int steps = uniform(tile_steps(c.end - c.key0 - t * kTile));
+            const uint64_t pb = operand(sp + (g >> 1) * G::kBlock + (g & 1) * 64, 1024, G::kBlock);
+            const uint32_t to = tmem + 256 + 32 * g, more = r > 0;
+            const int steps = tile_steps(keys - t * kTile);
             if (elect_one()) {
 #pragma unroll
                 for (int x = 0; x < kTile / 16; ++x) {
@@ -261,11 +306,13 @@ __device__ void narrow_outputs(const AttnParams& p, const Ctl& ctl, NarrowShared
                         mma_ss(to, va + (uint64_t)((x * 2 * TileGeo<D>::kGroup) >> 4), pb + (uint64_t)((x * 2048) >> 4), io, x > 0 ? 1u : more);
                 }
                 tc_commit(smem_u32(&sh->rv.empty[st]));
-                tc_commit(smem_u32(&sh->o_full[k][b]));
+                tc_commit(smem_u32(&sh->o_full[split.bar(k)][b]));
+                mbar_arrive(smem_u32(&sh->o_full[split.bar(k)][b]));  // orders the piece's poison before it
             }
             __syncwarp();
             if (++st == G::kValues) st = 0, ++round;
         }
+        sh->pieces.done(i);
     }
 }
 
@@ -327,9 +374,8 @@ __device__ __forceinline__ float poison_of(const AttnParams& p, const PieceInfo&
     return sum;
 }
 
-template <int D>
-__device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, unsigned char* spw, uint32_t ring_v,
-                               uint32_t tmem) {
+template <int D, bool kPlanned>
+__device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared<D>* sh, unsigned char* spw, uint32_t tmem) {
     using G = NarrowGeo<D>;
     const int tid = threadIdx.x, lane = tid & 31, g = tid >> 7, key = tid & 127, quad = (tid >> 5) & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
@@ -342,36 +388,50 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
         return reinterpret_cast<float*>(spw + (group >> 1) * G::kBlock + k * 128 + ((((group & 1) * 4 + (x & 3)) ^ (k & 7)) << 4)) +
                (lane & 3);
     };
-    Uses uses{};
-    uint32_t f0 = 0, tails = 0;
-    int pending = 0;
+    Uses all_uses{};
+    int pending = 0, turn = 0;
     for (uint32_t piece = 0;; ++piece) {
-        const PieceInfo c = sh->pieces.get(ctl, piece);
-        if (rows_any<kSoftThreads>(c.rows == 0)) break;  // all sixteen warps or none: they meet at barriers below
-        const int n = c.n, ctx = c.ctx, keys = c.end, first_tail = c.first_tail(7);
-        const Split split(c.rows);
-        const int k = g >> split.log_chunks, chunk = g & (split.chunks() - 1);
+        const int rows = sh->pieces.get(ctl, piece);
+        const PieceInfo& c = sh->pieces.at(piece);
+        const int n = c.n;
+        // All warps of a group take the piece or none, and all groups where it is theirs together: they meet at barriers below.
+        // Every group leaves through the barrier of all.
+        const bool stop = group_any(g, rows == 0);
+        const Split split(rows, n, turn);
+        if ((stop || !split.solo) && rows_any<kSoftThreads>(stop)) break;
+        const Uses uses = all_uses;
+        all_uses.add(n, split);
+        if (!kPlanned && c.join > 0) {
+            if (tid == 0) sh->pieces.pending[pending] = c;
+            ++pending;
+        }
+        if (split.solo && g != split.first) {
+            sh->pieces.done(piece);
+            continue;
+        }
+        const int first_tail = c.first_tail(7);
+        const int k = split.solo ? 0 : g >> split.log_chunks, chunk = split.solo ? 0 : g & (split.chunks() - 1), bar = split.bar(k);
         my_m[lane] = kNone;  // all four warps: each finds it there
         __syncwarp();
         float l[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) l[e] = 0.0f;
         // this lane's row of the group's chunk
-        const int my_row = c.row0 + min(32 * chunk + lane, c.rows - 1), my_node = attn_node(p, my_row);
+        const int my_row = c.row0 + min(32 * chunk + lane, rows - 1), my_node = attn_node(p, my_row);
         const int rounds = chunk < split.used ? split.rounds(n, k) : 0;
 #pragma unroll 1
         for (int i = 0; i < rounds; ++i) {
-            const int tt = (i << split.log_tiles) + k, pos0 = c.key0 + tt * kTile, b = i & 1;
+            const int tt = (i << split.log_tiles) + k, b = i & 1;
             const bool tail = tt >= first_tail;
             // the product that read the group's weights last
             auto weights_free = [&] {
-                if (i > 0) wait(ctl, smem_u32(&sh->o_full[k][b ^ 1]), uses.parity(k, b ^ 1, (i - 1) / 2));
+                if (i > 0) wait(ctl, smem_u32(&sh->o_full[bar][b ^ 1]), uses.parity(bar, b ^ 1, (i - 1) / 2));
             };
-            wait(ctl, smem_u32(&sh->s_full[k][b]), uses.parity(k, b, i / 2));
+            wait(ctl, smem_u32(&sh->s_full[bar][b]), uses.parity(bar, b, i / 2));
             tc_fence_after();
             uint32_t seen = 0xffffffffu;  // rows that see this thread's key
             if (tail) {
-                const int pos = pos0 + key;
+                const int ctx = c.ctx, keys = c.end, pos0 = c.key0 + tt * kTile, pos = pos0 + key;
                 if (!p.mask) {
                     // a chain: node j is seen by the rows from j * gq on
                     seen = pos < ctx ? 0xffffffffu : (pos < keys ? ~low_bits((pos - ctx) * p.gq - c.row0 - 32 * chunk) : 0u);
@@ -381,14 +441,6 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                     seen = 0;
 #pragma unroll 8
                     for (int e = 0; e < 32; ++e) seen |= ((__shfl_sync(0xffffffffu, row_sees, e) >> lane) & 1u) << e;
-                }
-                if (chunk == 0) {
-                    // A piece has at most two such tiles (up to 128 nodes); the issuing warp reports their values.
-                    const uint32_t x = tails + (tt - max(first_tail, 0));
-                    wait(ctl, smem_u32(&sh->v_full[x & 1]), (x >> 1) & 1);
-                    const uint32_t f = f0 + tt, st = f % G::kValues;
-                    wait(ctl, smem_u32(&sh->rv.full[st]), (f / G::kValues) & 1);  // passed by now: the copy's own barrier
-                    if (clean_values<D>(ring_v + st * G::kStage, max(ctx - pos0, 0), keys - pos0, key, 128)) sh->poison[piece & 1] = 1;
                 }
             }
             const uint32_t t_s = tmem + lanes + 128 * b + 32 * g;
@@ -483,23 +535,24 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
         // the group's last product; then the statistics meet where the weights were
         if (rounds > 0) {
             const int i = rounds - 1;
-            wait(ctl, smem_u32(&sh->o_full[k][i & 1]), uses.parity(k, i & 1, i / 2));
+            wait(ctl, smem_u32(&sh->o_full[bar][i & 1]), uses.parity(bar, i & 1, i / 2));
         }
         *place(g, quad) = sum_columns(l, lane);
-        rows_sync<kSoftThreads>();
+        __syncwarp();
+        const bool poisoned = *reinterpret_cast<volatile uint32_t*>(&sh->poison[piece % kPieces]) == piece + 1;
+        const bool poison = split.solo ? group_any(g, poisoned) : rows_any<kSoftThreads>(poisoned);
         tc_fence_after();
-        if (tid == 0) sh->poison[(piece & 1) ^ 1] = 0;  // read for the last time before the barrier before this one
         if (chunk < split.used) {
             // the groups of a chunk join its rows, each a part of them: lane e has row e's factors
             float m = kNone, sum = 0.0f, f[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                if (x < split.tiles()) m = fmaxf(m, sh->m[32 * ((x << split.log_chunks) + chunk) + lane]);
+                if (x < split.tiles()) m = fmaxf(m, sh->m[32 * (split.group(x) + chunk) + lane]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 f[x] = 0.0f;
                 if (x >= split.tiles()) continue;
-                const int from = (x << split.log_chunks) + chunk;
+                const int from = split.group(x) + chunk;
                 f[x] = ex2(sh->m[32 * from + lane] - m);
                 sum = fmaf((*place(from, 0) + *place(from, 1)) + (*place(from, 2) + *place(from, 3)), f[x], sum);
             }
@@ -509,24 +562,27 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                 for (int x = 0; x < 4; ++x) f[x] *= inv;
             }
             const int orow = (c.node0 + my_node) * p.Hq + c.hkv * p.gq + (my_row - my_node * p.gq);
-            if (k == 0 && quad == 0 && 32 * chunk + lane < c.rows) {
+            if (k == 0 && quad == 0 && 32 * chunk + lane < rows) {
                 if (!c.whole)
                     c.ml[32 * chunk + lane] = make_float2(m, sum);
                 else if (p.lse)
                     p.lse[orow] = attn_lse(m, sum);
             }
-            const int part = 32 >> split.log_tiles, d = quad * 32 + lane, rows = min(32, c.rows - 32 * chunk);
-            const bool poison = sh->poison[piece & 1] != 0;
+            const int part = 32 >> split.log_tiles, d = quad * 32 + lane, count = min(32, rows - 32 * chunk);
             if (quad * 32 < D) {  // otherwise repeated outputs
+                // rows of the result, or of the slot
+                const bool whole = c.whole;
+                const int row_to = whole ? orow : 32 * chunk + lane, size = whole ? 2 : 4;
+                char* base = (whole ? static_cast<char*>(p.out) : reinterpret_cast<char*>(c.o)) + d * size;
 #pragma unroll 1
-                for (int e = k * part; e < (k + 1) * part && e < rows; e += 8) {
+                for (int e = k * part; e < (k + 1) * part && e < count; e += 8) {
                     float v[8];
 #pragma unroll
                     for (int y = 0; y < 8; ++y) v[y] = 0.0f;
 #pragma unroll 1
                     for (int x = 0; x < split.tiles() && x < n; ++x) {
                         float o[8];
-                        ld8(tmem + lanes + 256 + 32 * ((x << split.log_chunks) + chunk) + e, o);
+                        ld8(tmem + lanes + 256 + 32 * (split.group(x) + chunk) + e, o);
                         tc_wait_ld();
                         const float fx = x < 2 ? (x == 0 ? f[0] : f[1]) : (x == 2 ? f[2] : f[3]);
 #pragma unroll
@@ -534,17 +590,17 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
                     }
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
-                        const int to = __shfl_sync(0xffffffffu, orow, e + y);
-                        if (e + y >= rows) continue;
-                        if (c.whole)
-                            static_cast<__nv_bfloat16*>(p.out)[(size_t)to * D + d] = __float2bfloat16_rn(v[y]);
+                        char* to = base + (long long)__shfl_sync(0xffffffffu, row_to, e + y) * (D * size);
+                        if (e + y >= count) continue;
+                        if (whole)
+                            *reinterpret_cast<__nv_bfloat16*>(to) = __float2bfloat16_rn(v[y]);
                         else
-                            c.o[(size_t)(32 * chunk + e + y) * D + d] = v[y];
+                            *reinterpret_cast<float*>(to) = v[y];
                     }
                 }
                 if (poison) {
 #pragma unroll 1
-                    for (int e = k * part; e < (k + 1) * part && e < rows; ++e) {
+                    for (int e = k * part; e < (k + 1) * part && e < count; ++e) {
                         const int row = c.row0 + 32 * chunk + e, node = attn_node(p, row);
                         const float v = poison_of(p, c, node, d);
                         if (v == 0.0f) continue;
@@ -560,20 +616,18 @@ __device__ void narrow_softmax(const AttnParams& p, const Ctl& ctl, NarrowShared
             }
         }
         tc_fence_before();
-        rows_sync<kSoftThreads>();  // everything has been read: the next piece may write over it
-        f0 += n;
-        tails += n > first_tail ? n - max(first_tail, 0) : 0;
-        uses.add(n, split);
-        if (c.join > 0) {
-            if (tid == 0) sh->pieces.pending[pending] = c;
-            ++pending;
-        }
+        sh->pieces.done(piece);
+        // everything has been read: the next piece may write over it
+        if (split.solo)
+            group_sync(g);
+        else
+            rows_sync<kSoftThreads>();
     }
-    if (pending > 0)  // behind the barrier of the loop's end
-        attn_join_last<1, D, 2, 4>(p, sh->pieces.pending, pending, tid, kSoftThreads, sh->pieces.last, [] { rows_sync<kSoftThreads>(); });
+    if (!kPlanned && pending > 0)  // behind the barrier of the loop's end
+        attn_join_last<1, D, 1, 4>(p, sh->pieces.pending, pending, tid, kSoftThreads, sh->pieces.last, [] { rows_sync<kSoftThreads>(); });
 }
 
-template <int D>
+template <int D, bool kPlanned>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
     using G = NarrowGeo<D>;
@@ -587,16 +641,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (threadIdx.x == 0) {
         sh->rk.init();
         sh->rv.init();
-        sh->pieces.init();
+        sh->pieces.init(19);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh->q_full[i]), 1);
+            mbar_init(smem_u32(&sh->q_full[i]), 32);
             mbar_init(smem_u32(&sh->q_empty[i]), 1);
-            mbar_init(smem_u32(&sh->v_full[i]), 1);
-            sh->poison[i] = 0;
         }
+        for (int i = 0; i < kPieces; ++i) sh->poison[i] = 0;
         for (int i = 0; i < 8; ++i) {
             mbar_init(smem_u32(&sh->s_full[i >> 1][i & 1]), 1);
-            mbar_init(smem_u32(&sh->o_full[i >> 1][i & 1]), 1);
+            mbar_init(smem_u32(&sh->o_full[i >> 1][i & 1]), 2);
             mbar_init(smem_u32(&sh->p_full[i >> 1][i & 1]), 4);
         }
         sh->abort = 0;
@@ -618,7 +671,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // 64 (4 x 104 + 64 = 5 x 96)
     if (warp < 16) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        narrow_softmax<D>(p, ctl, sh, spw, ring_v, tmem);
+        narrow_softmax<D, kPlanned>(p, ctl, sh, spw, tmem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 17)
@@ -626,11 +679,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         else if (warp == 19)
             narrow_outputs<D>(p, ctl, sh, smem_u32(spw), ring_v, tmem);
         else
-            narrow_fill<D>(p, warp == 16, warp == 16 ? &mk : &mv, ctl, sh, smem_u32(sq), warp == 16 ? ring_k : ring_v, lane);
+            narrow_fill<D, kPlanned>(p, warp == 16, warp == 16 ? &mk : &mv, ctl, sh, smem_u32(sq), warp == 16 ? ring_k : ring_v, lane);
     }
     tc_fence_before();
     __syncthreads();
-    settle(&sh->abort);
+    settle(ctl);
     if (warp == 17) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -639,9 +692,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 }  // namespace
 
+template <int D>
+static cudaError_t launch_narrow_t(const AttnParams& p, cudaStream_t st) {
+    return launch_tc(p.planned ? attn_narrow_kernel<D, true> : attn_narrow_kernel<D, false>, kTcThreads, NarrowGeo<D>::kSmem, p, st);
+}
+
 cudaError_t launch_attn_narrow(const AttnParams& p, cudaStream_t st) {
-    return p.D == 64 ? launch_tc(attn_narrow_kernel<64>, kTcThreads, NarrowGeo<64>::kSmem, p, st)
-                     : launch_tc(attn_narrow_kernel<128>, kTcThreads, NarrowGeo<128>::kSmem, p, st);
+    return p.D == 64 ? launch_narrow_t<64>(p, st) : launch_narrow_t<128>(p, st);
 }
 
 }  // namespace smcsd

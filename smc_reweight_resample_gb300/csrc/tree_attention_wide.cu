@@ -52,25 +52,32 @@ struct __align__(8) TcShared {
 // ---- pieces, keys and values ----
 
 // Two warps in one piece of code: the one with `keys` walks and brings the pages of keys, the other the pages of values.
-// Piece i is handed round once the query rows of piece i - 2 are there, which the softmax brings when it is done with
-// piece i - 3: the place of piece i - 4 is free.
-template <int D>
+template <int D, bool kPlanned>
 __device__ void wide_fill(const AttnParams& p, bool keys, const CUtensorMap* map, const Ctl& ctl, TcShared<D>* sh, uint32_t ring, int lane) {
     using G = TcGeo<D>;
     Filler<D> filler(map, keys ? sh->rk.full : sh->rv.full, keys ? sh->rk.empty : sh->rv.empty, keys ? G::kKeys : G::kValues, ring);
-    Walker walk;
+    Walker<kPlanned> walk;
     if (keys) walk.begin(p, lane);
+    int id = 0;
 #pragma unroll 1
     for (uint32_t i = 0;; ++i) {
-        PieceInfo c;
+        // the next piece, and its first ids, are fetched before this one's tiles have to wait for places
+        int rows;
         if (keys) {
-            walk.next(p, c, lane);
-            if (i >= 2) wait(ctl, smem_u32(&sh->q_full[i & 1]), ((i - 2) >> 1) & 1);
-            sh->pieces.put(i, c, lane);
+            PieceInfo next;
+            walk.next(p, next, lane);
+            sh->pieces.put(ctl, i, next, lane);
+            rows = next.rows;
         } else {
-            c = sh->pieces.get(ctl, i);
+            rows = sh->pieces.get(ctl, i);
         }
-        if (c.rows == 0 || !filler.fill(p, ctl, c, lane)) return;
+        const int id_ahead = rows > 0 ? filler.page_id(p, sh->pieces.at(i), 0, lane) : 0;
+        if (i > 0) {
+            if (!filler.fill(p, ctl, sh->pieces.at(i - 1), id, lane)) return;
+            if (!keys) sh->pieces.done(i - 1);
+        }
+        if (rows == 0) return;
+        id = id_ahead;
     }
 }
 
@@ -82,10 +89,11 @@ __device__ void tc_issue(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, u
     constexpr uint32_t is = instruction(kTile, 0, 0), io = instruction(D, 0, 1);
     uint32_t f0 = 0, np[2] = {0, 0};
     for (uint32_t piece = 0;; ++piece) {
-        const PieceInfo c = sh->pieces.get(ctl, piece);
-        if (c.rows == 0) return;
-        const int n = c.n;
-        const bool two = c.rows > kTile;
+        const int rows = sh->pieces.get(ctl, piece);
+        if (rows == 0) return;
+        const int n = uniform(sh->pieces.at(piece).n), keys = uniform(sh->pieces.at(piece).end - sh->pieces.at(piece).key0);
+        sh->pieces.done(piece);
+        const bool two = rows > kTile;
         wait(ctl, smem_u32(&sh->q_full[piece & 1]), (piece >> 1) & 1);
         tc_fence_after();
         const int steps = two ? n : (n + 1) / 2;
@@ -103,7 +111,7 @@ __device__ void tc_issue(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, u
                     tc_fence_after();
                     const uint64_t vb = operand(ring_v + st * G::kStage, TileGeo<D>::kGroup, 1024);
                     const uint32_t more = i > 1;
-                    const int steps_v = uniform(tile_steps(c.end - c.key0 - tp * kTile));
+                    const int steps_v = tile_steps(keys - tp * kTile);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)
@@ -181,7 +189,7 @@ __device__ __forceinline__ void add_poison(const AttnParams& p, const PieceInfo&
     }
 }
 
-template <int D>
+template <int D, bool kPlanned>
 __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, unsigned char* sq, uint32_t ring_v, uint32_t tmem) {
     using G = TcGeo<D>;
     const int tid = threadIdx.x, lane = tid & 31, s = tid >> 7, r = tid & 127, quad = (tid >> 5) & 3;
@@ -192,12 +200,13 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
     uint32_t f0 = 0, steps0[2] = {0, 0};  // fills and steps of earlier pieces
     int pending = 0;
     for (uint32_t piece = 0;; ++piece) {
-        const PieceInfo c = sh->pieces.get(ctl, piece);
-        if (rows_any<256>(c.rows == 0)) break;  // all eight warps or none: they meet at barriers below
-        const int n = c.n, ctx = c.ctx, keys = c.end, first_tail = c.first_tail(7);
-        const bool two = c.rows > kTile;
+        const int rows = sh->pieces.get(ctl, piece);
+        if (rows_any<256>(rows == 0)) break;  // all eight warps or none: they meet at barriers below
+        const PieceInfo& c = sh->pieces.at(piece);
+        const int n = c.n, first_tail = c.first_tail(7);
+        const bool two = rows > kTile;
         // q: a block of 128 rows for each stream, or one for both
-        const int rows_q = min(c.rows, 2 * kTile);
+        const int rows_q = min(rows, 2 * kTile);
 #pragma unroll 2
         for (int i = tid; i < rows_q * (D / 8); i += 256) {
             const int rr = i / (D / 8), ch = i - rr * (D / 8);
@@ -214,15 +223,15 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         if (lane == 0) mbar_arrive(smem_u32(&sh->q_full[piece & 1]));
         rows_sync<256>();  // poison is clear
         const int rr = two ? s * kTile + r : r;  // row of the unit's block
-        const bool active = quad * 32 + (two ? s * kTile : 0) < c.rows;
-        const bool mine = rr < c.rows;
+        const bool active = quad * 32 + (two ? s * kTile : 0) < rows;
+        const bool mine = rr < rows;
         const int row = c.row0 + (mine ? rr : 0), node = attn_node(p, row), hq = c.hkv * p.gq + (row - node * p.gq);
         const uint32_t* mask_row = p.mask ? p.mask + (long long)(c.node0 + node) * p.words : nullptr;
         const int steps = two ? n : (n + 1 - s) / 2;  // tiles of this stream
         float m = kNegInf, l = 0.0f;                  // reference (times scale), sum
 #pragma unroll 1
         for (int i = 0; i < steps; ++i) {
-            const int tt = two ? i : 2 * i + s, pos0 = c.key0 + tt * kTile;
+            const int tt = two ? i : 2 * i + s;
             const uint32_t step = steps0[s] + i;
             const bool tail = tt >= first_tail;
             wait(ctl, smem_u32(&sh->s_full[s]), step & 1);
@@ -231,8 +240,9 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
                 // stage's earlier fill has landed, so this one may be waited for.
                 const uint32_t f = f0 + tt, st = f % G::kValues;
                 wait(ctl, smem_u32(&sh->rv.full[st]), (f / G::kValues) & 1);
+                const int pos0 = c.key0 + tt * kTile;
                 // by both groups where both have the tile
-                if (clean_values<D>(ring_v + st * G::kStage, max(ctx - pos0, 0), keys - pos0, two ? tid : r, two ? 256 : 128)) sh->poison = 1;
+                if (clean_values<D>(ring_v + st * G::kStage, max(c.ctx - pos0, 0), c.end - pos0, two ? tid : r, two ? 256 : 128)) sh->poison = 1;
                 fence_async_smem();
                 if (two) rows_sync<256>();  // the other stream's product reads the same values
             }
@@ -245,7 +255,7 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
                 if (tail) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t seen = seen32(p, mask_row, node, ctx, keys, pos0 + 32 * q);
+                        const uint32_t seen = seen32(p, mask_row, node, c.ctx, c.end, c.key0 + tt * kTile + 32 * q);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) z[32 * q + e] = (seen >> e) & 1u ? z[32 * q + e] : kNegInf;
                     }
@@ -311,7 +321,7 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         rows_sync<256>();
         tc_fence_after();
         const bool poison = sh->poison != 0;
-        if (quad * 32 + (two ? s * kTile : 0) < c.rows) {
+        if (quad * 32 + (two ? s * kTile : 0) < rows) {
             const size_t orow = (size_t)(c.node0 + node) * p.Hq + hq;
             float fa = 1.0f, fb = 0.0f;
             const bool join = !two && steps_b > 0;
@@ -352,16 +362,17 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         f0 += n;
         steps0[0] += steps_a;
         steps0[1] += steps_b;
-        if (c.join > 0) {
+        if (!kPlanned && c.join > 0) {
             if (tid == 0) sh->pieces.pending[pending] = c;
             ++pending;
         }
+        sh->pieces.done(piece);
     }
-    if (pending > 0)  // behind the barrier of the loop's end
+    if (!kPlanned && pending > 0)  // behind the barrier of the loop's end
         attn_join_last<1, D, 8, 2>(p, sh->pieces.pending, pending, tid, 256, sh->pieces.last, [] { rows_sync<256>(); });
 }
 
-template <int D>
+template <int D, bool kPlanned>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
     using G = TcGeo<D>;
@@ -375,7 +386,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (threadIdx.x == 0) {
         sh->rk.init();
         sh->rv.init();
-        sh->pieces.init();
+        sh->pieces.init(10);
         mbar_init(smem_u32(&sh->q_full[0]), 8);
         mbar_init(smem_u32(&sh->q_full[1]), 8);
         for (int s = 0; s < 2; ++s) {
@@ -402,17 +413,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // with 72 (2 x 216 + 72 = 3 x 168)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        tc_rows<D>(p, ctl, sh, sq, ring_v, tmem);
+        tc_rows<D, kPlanned>(p, ctl, sh, sq, ring_v, tmem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 9)
             tc_issue<D>(p, ctl, sh, smem_u32(sq), ring_k, ring_v, tmem);
         else if (warp != 11)
-            wide_fill<D>(p, warp == 8, warp == 8 ? &mk : &mv, ctl, sh, warp == 8 ? ring_k : ring_v, lane);
+            wide_fill<D, kPlanned>(p, warp == 8, warp == 8 ? &mk : &mv, ctl, sh, warp == 8 ? ring_k : ring_v, lane);
     }
     tc_fence_before();
     __syncthreads();
-    settle(&sh->abort);
+    settle(ctl);
     if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -421,9 +432,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 }  // namespace
 
+template <int D>
+static cudaError_t launch_wide_t(const AttnParams& p, cudaStream_t st) {
+    return launch_tc(p.planned ? attn_wide_kernel<D, true> : attn_wide_kernel<D, false>, kTcThreads, TcGeo<D>::kSmem, p, st);
+}
+
 cudaError_t launch_attn_wide(const AttnParams& p, cudaStream_t st) {
-    return p.D == 64 ? launch_tc(attn_wide_kernel<64>, kTcThreads, TcGeo<64>::kSmem, p, st)
-                     : launch_tc(attn_wide_kernel<128>, kTcThreads, TcGeo<128>::kSmem, p, st);
+    return p.D == 64 ? launch_wide_t<64>(p, st) : launch_wide_t<128>(p, st);
 }
 
 }  // namespace smcsd
