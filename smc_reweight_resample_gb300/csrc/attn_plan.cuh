@@ -7,9 +7,10 @@
 // Hkv x nrb units (a key/value head and a block of at most RB rows, a row being a node and one of the
 // Hq/Hkv query heads that share the head), each of `tiles` tiles of keys.
 //
-// Cut. All tiles of all units stand in one line, and before each unit's tiles as many empty places as beginning and ending a
-// unit costs tiles: W places (below 2^31). Block c of ncta takes W / ncta of them,
-// the first W % ncta blocks one more: equal shares whatever the lengths are. Where a cut falls inside a unit, or a
+// Cut. All tiles of all units stand in one line, each of them on as many places as its unit's rows make it cost, and before each
+// unit's tiles as many empty places as beginning and ending a unit costs: W places (below 2^31). Block c of ncta has W / ncta
+// of them, the first W % ncta blocks one more, and takes the tiles that begin there: shares of equal cost whatever the lengths
+// and the rows are. Where a block would not get a tile's places, all tiles count one (AttnCost). Where a cut falls inside a unit, or a
 // row has a shared and an own unit, the pieces leave (sum, max, weighted values) in a slot. Without the planning kernel (and so
 // without groups) only a block's first and last piece can be part of a unit: block c has slots 2 c (a unit that began before
 // it) and 2 c + 1 (one that ends behind it), and the last block to finish a unit's pieces joins them, in the order of the
@@ -43,6 +44,7 @@ struct AttnHead {  // written by the planning kernel
     unsigned done; // blocks of the planning kernel that have finished
     int ncta, base, rest;  // W = ncta * base + rest
     int units_shared;      // units of shared items, which are the first ones
+    int weighted;          // AttnCost
 };
 
 // Every kernel that takes part has at most kAttnMaxCta blocks on the line.
@@ -110,7 +112,8 @@ struct AttnParams {
     void* ws;
     AttnLayout L;
     int log_tile, log_rb;  // keys of a tile, rows of a block
-    int empty;             // places before a unit's tiles
+    int heavy, w_light, w_heavy, empty;  // places of a tile of up to `heavy` rows, of more, before a unit's tiles
+    int empty_one;                       // the last where a tile has one place
     int ncta_max;
     FastDiv div_gq, div_cta;
     bool planned;  // by the planning kernel
@@ -158,6 +161,23 @@ struct AttnCut {  // W = ncta * base + rest
     }
 };
 
+// What tiles and units cost in places. `weighted` only where every block has at least a tile's places, so that each of the
+// blocks between a unit's first and last tile has a tile of it.
+struct AttnCost {
+    int heavy, light_tile, heavy_tile, empty;
+    __device__ __forceinline__ AttnCost() {}
+    __device__ __forceinline__ AttnCost(const AttnParams& p, bool weighted)
+        : heavy(p.heavy), light_tile(weighted ? p.w_light : 1), heavy_tile(weighted ? p.w_heavy : 1), empty(weighted ? p.empty : p.empty_one) {}
+    __device__ __forceinline__ static bool fits(const AttnParams& p, long long W) { return W >= (long long)p.w_heavy * p.ncta_max; }
+    __device__ __forceinline__ int tile(int rows) const { return rows > heavy ? heavy_tile : light_tile; }
+    __device__ __forceinline__ int unit(int rows, int tiles) const { return tile(rows) * tiles + empty; }
+    // the row blocks of one head
+    __device__ __forceinline__ int head(const AttnParams& p, const AttnItem& it) const {
+        return (it.nrb - 1) * unit(it.per, it.tiles) + unit(it.nodes * p.gq - (it.nrb - 1) * it.per, it.tiles);
+    }
+    __device__ __forceinline__ int item(const AttnParams& p, const AttnItem& it) const { return it.tiles > 0 ? p.Hkv * head(p, it) : 0; }
+};
+
 // Row blocks of an item, and its units.
 __device__ __forceinline__ int attn_units(const AttnParams& p, AttnItem& it) {
     const int rows = it.nodes * p.gq, rb = 1 << p.log_rb;
@@ -198,6 +218,7 @@ struct PieceInfo {
 template <bool kPlanned>
 struct Walker {
     AttnCut cut;
+    AttnCost cost;
     int x, end, item_end;
     int units_shared, ii;  // ii: number of the present item
     AttnItem it;
@@ -206,8 +227,8 @@ struct Walker {
     AttnItem mine;
     int first, mine_end;  // the 32's first sequence, line after this lane's item
 
-    // this lane's item of the 32; its places on the line
-    __device__ __forceinline__ int load(const AttnParams& p, int lane) {
+    // this lane's item of the 32
+    __device__ __forceinline__ void load(const AttnParams& p, int lane) {
         const int s = first + lane;
         mine.nodes = mine.tiles = mine.node0 = 0;
         if (s < p.S) {
@@ -216,7 +237,7 @@ struct Walker {
             if (c < 0) mine.nodes = 0;
             mine.tiles = mine.nodes > 0 ? (c + mine.nodes + (1 << p.log_tile) - 1) >> p.log_tile : 0;
         }
-        return attn_units(p, mine) * (mine.tiles + p.empty);
+        attn_units(p, mine);
     }
     __device__ __forceinline__ void place(int at, int size, int lane) {
         int in = size;
@@ -238,21 +259,26 @@ struct Walker {
             cut.base = h->base;
             cut.rest = h->rest;
             units_shared = h->units_shared;
+            cost = AttnCost(p, h->weighted);
             if (cta >= h->ncta) return;
             x = item_end = cut.of(cta);
             end = cut.of(cta + 1);
             ii = attn_search(ws_ptr<AttnItem>(p.ws, p.L.item), 0, p.G + p.S, x, lane) - 1;
             return;
         }
-        int W = 0, size = 0;
+        int W = 0, one = 0;
 #pragma unroll 1
         for (first = 0; first < p.S; first += 32) {
-            size = load(p, lane);
-            W += __reduce_add_sync(0xffffffffu, size);
+            load(p, lane);
+            W += __reduce_add_sync(0xffffffffu, AttnCost(p, true).item(p, mine));
+            one += __reduce_add_sync(0xffffffffu, AttnCost(p, false).item(p, mine));
         }
+        const bool weighted = AttnCost::fits(p, W);
+        cost = AttnCost(p, weighted);
+        W = weighted ? W : one;
         first -= 32;
         if (first == 0) {
-            place(0, size, lane);
+            place(0, cost.item(p, mine), lane);
         } else {
             first = -32;  // next_item begins with the first 32
             mine_end = 0;
@@ -270,8 +296,8 @@ struct Walker {
             while ((after = __ballot_sync(0xffffffffu, mine_end > x)) == 0) {
                 const int at = __shfl_sync(0xffffffffu, mine_end, 31);
                 first += 32;
-                const int size = load(p, lane);
-                place(at, size, lane);
+                load(p, lane);
+                place(at, cost.item(p, mine), lane);
             }
             const int l = __ffs(after) - 1;
             it.node0 = __shfl_sync(0xffffffffu, mine.node0, l);
@@ -283,36 +309,49 @@ struct Walker {
             it.key0 = 0;
             it.seq = ii = first + l;
         }
-        item_end = it.cum + (it.tiles + p.empty) * it.nrb * p.Hkv;
+        item_end = it.cum + cost.item(p, it);
         ctx = ii >= p.G ? __ldg(p.ctx_len + it.seq) : 0;
+    }
+    // To the end, or the next unit.
+    __device__ __forceinline__ void go_on(int to) {
+        x = to;
+        at = 0;
+        ++unit;
+        if (++rb == it.nrb) rb = 0, ++hkv;
     }
     // The next piece; false (and no rows) after the last one.
     __device__ __forceinline__ bool next(const AttnParams& p, PieceInfo& c, int lane) {
         c.rows = 0;
-        if (x >= end) return false;
-        if (x >= item_end) {
-            while (x >= item_end) next_item(p, lane);  // x is below W, so an item that holds it follows
-            const int in = x - it.cum;
-            unit = (int)((unsigned)in / (unsigned)(it.tiles + p.empty));
-            at = in - unit * (it.tiles + p.empty);
-            hkv = it.nrb == 1 ? unit : (int)((unsigned)unit / (unsigned)it.nrb);
-            rb = unit - hkv * it.nrb;
+        int first, w, a, b, to;  // the unit's first tile's place, places of a tile, tiles from a to b, place behind them
+#pragma unroll 1
+        for (;; go_on(to)) {
+            if (x >= end) return false;
+            if (x >= item_end) {
+                while (x >= item_end) next_item(p, lane);  // x is below W, so an item that holds it follows
+                const int per_head = cost.head(p, it), per_unit = cost.unit(it.per, it.tiles);
+                hkv = (int)((unsigned)(x - it.cum) / (unsigned)per_head);
+                at = x - it.cum - hkv * per_head;
+                rb = it.nrb == 1 ? 0 : min((int)((unsigned)at / (unsigned)per_unit), it.nrb - 1);
+                at -= rb * per_unit;
+                unit = hkv * it.nrb + rb;
+            }
+            c.row0 = rb * it.per;
+            c.rows = min(it.nodes * p.gq - c.row0, it.per);
+            w = cost.tile(c.rows);
+            first = x - at + cost.empty;
+            to = min(first + w * it.tiles, end);
+            a = (int)((unsigned)(max(x - first, 0) + w - 1) / (unsigned)w);
+            b = (int)((unsigned)(max(to - first, 0) + w - 1) / (unsigned)w);
+            if (b > a) break;
+            c.rows = 0;  // no tile of the unit begins on this share
         }
         const bool own = ii >= p.G;
-        const int cta = blockIdx.x, first = x - at + p.empty;  // first tile's place
+        const int cta = blockIdx.x;
         c.node0 = it.node0;
         c.seq = it.seq;
         c.hkv = hkv;
-        c.row0 = rb * it.per;
-        c.rows = min(it.nodes * p.gq - c.row0, it.per);
-        const int unit_end = first + it.tiles, to = min(unit_end, end), t = max(x - first, 0);
-        c.key0 = it.key0 + (t << p.log_tile);
-        c.n = to - first - t;
-        if (c.n <= 0) {  // the share ends before the unit's tiles
-            x = end;
-            c.rows = 0;
-            return false;
-        }
+        c.key0 = it.key0 + (a << p.log_tile);
+        c.n = b - a;
         c.whole = own && it.key0 == 0 && c.n == it.tiles;
         c.ctx = own ? ctx : it.keys;
         c.end = own ? ctx + it.nodes : it.keys;
@@ -322,18 +361,15 @@ struct Walker {
         float2* ml = ws_ptr<float2>(p.ws, own ? p.L.ml_s : p.L.ml_g);
         size_t slot = (size_t)(it.unit0 + unit - (own ? units_shared : 0)) + cta;
         if (!kPlanned) {
-            slot = 2 * cta + (t == 0);
+            slot = 2 * cta + (a == 0);
             if (!c.whole) {
-                c.counter = t == 0 ? cta : cut.block(first);
-                c.join = (to == unit_end ? cta : cut.block(unit_end - 1)) - c.counter + 1;
+                c.counter = cut.block(first);
+                c.join = cut.block(first + (it.tiles - 1) * w) - c.counter + 1;
             }
         }
         c.o = o + slot * rows * p.D;
         c.ml = ml + slot * rows;
-        x = to;  // the end, or the next unit
-        at = 0;
-        ++unit;
-        if (++rb == it.nrb) rb = 0, ++hkv;
+        go_on(to);
         return true;
     }
 };

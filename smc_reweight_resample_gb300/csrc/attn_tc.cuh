@@ -225,10 +225,10 @@ __device__ __forceinline__ bool rows_any(bool yes) {
 template <int kStages>
 struct Ring {
     uint64_t full[kStages], empty[kStages];
-    __device__ __forceinline__ void init() {
+    __device__ __forceinline__ void init(int readers) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&full[i]), 1);
-            mbar_init(smem_u32(&empty[i]), 1);
+            mbar_init(smem_u32(&empty[i]), readers);
         }
     }
 };

@@ -46,10 +46,9 @@ bool attn_sizes_ok(int S, int N, int T, int Hq, int Hkv, int D) {
 // sequence (narrow) or 256 (wide).
 enum AttnKind { kSimt, kNarrow, kWide };
 constexpr int kSimtBlocksPerSm = 2;
-// What a unit of the tensor-core kernels costs besides its tiles, in tiles: 0, 1, 2, 3, 4 took 123, 104, 111, 118 and 124 us for 8
-// groups of 16 sequences, whose shared units have dearer tiles than the short units of the sequences, and 170, 168, 167, 165 and
-// 165 us for 64 sequences of 21 nodes over 4096 tokens.
-constexpr int kEmptyGroups = 1, kEmptyPlaces = 3;
+// Places on the line (attn_plan.cuh): {rows from which a tile is heavy, of a light tile, of a heavy one, before a unit's tiles}.
+struct LineCost { int heavy, light_tile, heavy_tile, empty; };
+constexpr LineCost kNarrowGroups{64, 2, 3, 3}, kNarrowCost{64, 2, 3, 6}, kWideCost{128, 2, 3, 6};
 
 AttnKind kind_of(int dtype, int T, int Hq, int Hkv) {
     if (dtype == SMCSD_F32) return kSimt;
@@ -202,11 +201,17 @@ extern "C" int tree_attention(const void* q, long long q_stride, const void* k_c
     // all places of all units are numbered in 32 bits
     const long long units = (long long)S * Hkv * attn_blocks((long long)T * p.gq, rows_of(kind)) +
                             (long long)p.G * Hkv * attn_blocks((long long)N * T * p.gq, rows_of(kind));
-    if (units * (((long long)pages_per_seq * page_size + 63) / 64 + kEmptyPlaces) > 0x7fffffffLL) return SMCSD_ERR_INVALID_ARG;
+    const long long keys = (long long)pages_per_seq * page_size, places = kind == kSimt ? (keys + 63) / 64 : 3 * ((keys + 127) / 128) + 6;
+    if (units * places > 0x7fffffffLL) return SMCSD_ERR_INVALID_ARG;
     p.L = layout_of(kind, S, N, T, Hq, Hkv, D);
     p.log_tile = kind == kSimt ? 6 : 7;
     p.log_rb = kind == kSimt ? 4 : kind == kNarrow ? 7 : 8;
-    p.empty = kind == kSimt ? 0 : p.G > 0 ? kEmptyGroups : kEmptyPlaces;
+    const LineCost cost = kind == kSimt ? LineCost{0, 1, 1, 0} : kind == kWide ? kWideCost : p.G > 0 ? kNarrowGroups : kNarrowCost;
+    p.heavy = cost.heavy;
+    p.w_light = cost.light_tile;
+    p.w_heavy = cost.heavy_tile;
+    p.empty = cost.empty;
+    p.empty_one = kind == kSimt ? 0 : 1;
     p.div_gq = make_fastdiv((uint32_t)p.gq);
     p.ncta_max = device_sm_count() * (kind == kSimt ? kSimtBlocksPerSm : 1);
     if (p.ncta_max > kAttnMaxCta) p.ncta_max = kAttnMaxCta;

@@ -110,20 +110,30 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     const int n = p.G + p.S, per = (n + kPlanThreads - 1) / kPlanThreads;
     const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
     AttnItem it;
-    long long mine = 0, total;
-    for (int i = i0; i < i1; ++i) {
-        it = plan_item(p, shared, i);
-        const long long u = attn_units(p, it);
-        mine += ((u * (it.tiles + p.empty)) << 32) + u;
+    // by cost; where that leaves blocks less than a tile's places, with a place for each tile
+    AttnCost cost(p, true);
+    long long at, total;
+    bool weighted = true;
+    for (;;) {
+        long long mine = 0;
+        for (int i = i0; i < i1; ++i) {
+            it = plan_item(p, shared, i);
+            const long long u = attn_units(p, it);
+            mine += ((long long)cost.item(p, it) << 32) + u;
+        }
+        at = plan_prefix(mine, sums, total);
+        if (!weighted || AttnCost::fits(p, total >> 32)) break;
+        weighted = false;
+        cost = AttnCost(p, false);
+        __syncthreads();  // the sums have been read
     }
-    long long at = plan_prefix(mine, sums, total);
     for (int i = i0; i < i1; ++i) {
         if (per > 1) it = plan_item(p, shared, i);
         const long long u = attn_units(p, it);
         it.cum = (int)(at >> 32);
         it.unit0 = (int)(at & 0xffffffffll);
         items[i] = it;
-        at += ((u * (it.tiles + p.empty)) << 32) + u;
+        at += ((long long)cost.item(p, it) << 32) + u;
         if (i == p.G - 1) attn_head(p)->units_shared = (int)(at & 0xffffffffll);
     }
     if (tid == 0) {
@@ -131,6 +141,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         const int W = (int)(total >> 32);
         const AttnCut cut(p, W);
         if (p.G == 0) h->units_shared = 0;
+        h->weighted = weighted;
         h->ncta = cut.ncta;
         h->base = cut.base;
         h->rest = cut.rest;
@@ -365,6 +376,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
     AttnCut cut;
     cut.base = h->base;
     cut.rest = h->rest;
+    const AttnCost cost(p, h->weighted);
     const AttnItem it = items[p.G + blockIdx.x], grp = items[p.G > 0 ? blockIdx.x / p.N : 0];
     if (it.tiles == 0) return;
     const bool shared = p.G > 0 && grp.tiles > 0;
@@ -374,7 +386,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
 #pragma unroll 1
     for (int u = blockIdx.y; u < p.Hkv * it.nrb; u += gridDim.y) {
         const int hkv = u / it.nrb, row0 = (u - hkv * it.nrb) * it.per, rows = min(it.per, it.nodes * p.gq - row0);
-        const int x0 = it.cum + u * (it.tiles + p.empty) + p.empty, c0 = cut.block(x0), own_count = cut.block(x0 + it.tiles - 1) - c0 + 1;
+        const int rb = u - hkv * it.nrb, x0 = it.cum + hkv * cost.head(p, it) + rb * cost.unit(it.per, it.tiles) + cost.empty;  // its first tile's place
+        const int c0 = cut.block(x0), own_count = cut.block(x0 + (it.tiles - 1) * cost.tile(rows)) - c0 + 1;
         if (!shared && own_count == 1) continue;  // written directly
 #pragma unroll 1
         for (int r = (blockIdx.z * (kJoinThreads / 32) + warp) * kRows + lane / kLanes; r < rows; r += step) {
@@ -382,11 +395,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
             JoinRun run[2];
             run[0].count = 0;
             if (shared) {
-                const int gr = row + (it.node0 - grp.node0) * p.gq, rb = gr / grp.per, gu = hkv * grp.nrb + rb;
-                const int g0 = grp.cum + gu * (grp.tiles + p.empty) + p.empty, b0 = cut.block(g0);
-                const size_t at = (size_t)(grp.unit0 + gu + b0) * p.L.rows_g + (gr - rb * grp.per);
+                const int gr = row + (it.node0 - grp.node0) * p.gq, grb = gr / grp.per, grows = min(grp.per, grp.nodes * p.gq - grb * grp.per);
+                const int g0 = grp.cum + hkv * cost.head(p, grp) + grb * cost.unit(grp.per, grp.tiles) + cost.empty, b0 = cut.block(g0);
+                const size_t at = (size_t)(grp.unit0 + hkv * grp.nrb + grb + b0) * p.L.rows_g + (gr - grb * grp.per);
                 run[0] = JoinRun{ws_ptr<float>(p.ws, p.L.slot_g) + at * D, ws_ptr<float2>(p.ws, p.L.ml_g) + at, (size_t)p.L.rows_g,
-                                 cut.block(g0 + grp.tiles - 1) - b0 + 1};
+                                 cut.block(g0 + (grp.tiles - 1) * cost.tile(grows)) - b0 + 1};
             }
             const size_t at = (size_t)(it.unit0 + u - h->units_shared + c0) * p.L.rows_s + r;
             run[1] = JoinRun{ws_ptr<float>(p.ws, p.L.slot_s) + at * D, ws_ptr<float2>(p.ws, p.L.ml_s) + at, (size_t)p.L.rows_s, own_count};

@@ -639,8 +639,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t ring_k = smem_u32(spw + G::kWeights), ring_v = ring_k + G::kKeys * G::kStage;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        sh->rk.init();
-        sh->rv.init();
+        sh->rk.init(1);
+        sh->rv.init(1);
         sh->pieces.init(19);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh->q_full[i]), 32);

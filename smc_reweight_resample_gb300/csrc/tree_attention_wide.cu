@@ -43,10 +43,11 @@ struct __align__(8) TcShared {
     Ring<TcGeo<D>::kValues> rv;
     PieceRing pieces;
     uint64_t q_full[2];  // by the piece's parity
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2][2];  // [stream][half of the tile]
+    uint64_t v_clean[TcGeo<D>::kValues];  // [stage] the first stream's warp has cleaned the values for both
     uint32_t tmem;
     int abort;
-    int poison;  // a NaN or infinity among the values of the piece's nodes
+    uint32_t poison[kPieces];  // i + 1: a NaN or infinity among the values of the i-th piece's nodes
 };
 
 // ---- pieces, keys and values ----
@@ -83,64 +84,115 @@ __device__ void wide_fill(const AttnParams& p, bool keys, const CUtensorMap* map
 
 // ---- products ----
 
+// One warp for each stream. Its products follow one another: a tile's scores are written over the weights of its tile before,
+// behind the product that reads them. Both warps watch all tiles land and report all of them as read, so that neither falls
+// a round of the rings behind where the streams take turns on the tiles.
 template <int D>
-__device__ void tc_issue(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, uint32_t sq, uint32_t ring_k, uint32_t ring_v, uint32_t tmem) {
+__device__ void wide_products(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, int s, uint32_t sq, uint32_t ring_k, uint32_t ring_v,
+                              uint32_t tmem) {
     using G = TcGeo<D>;
     constexpr uint32_t is = instruction(kTile, 0, 0), io = instruction(D, 0, 1);
-    uint32_t f0 = 0, np[2] = {0, 0};
+    const uint32_t t_s = tmem + 128 * s, t_o = tmem + 256 + 128 * s;
+    uint32_t used = 0, tails = 0;  // parities of the weights and of the stages' cleaned values
+    uint32_t kst = 0, kround = 0, vst = 0, vround = 0;
     for (uint32_t piece = 0;; ++piece) {
         const int rows = sh->pieces.get(ctl, piece);
         if (rows == 0) return;
-        const int n = uniform(sh->pieces.at(piece).n), keys = uniform(sh->pieces.at(piece).end - sh->pieces.at(piece).key0);
-        sh->pieces.done(piece);
+        const PieceInfo& c = sh->pieces.at(piece);
+        const int n = uniform(c.n), keys = uniform(c.end - c.key0), first_tail = c.first_tail(7);
         const bool two = rows > kTile;
         wait(ctl, smem_u32(&sh->q_full[piece & 1]), (piece >> 1) & 1);
-        tc_fence_after();
-        const int steps = two ? n : (n + 1) / 2;
+        const uint64_t qa = operand(sq + (two ? s * G::kStage : 0), TileGeo<D>::kGroup, 0);
+        int ts = 0, to = 0;  // tiles whose keys, whose values have landed
+        // own: this stream's next tile whose scores are issued (n or more: none is left)
 #pragma unroll 1
-        for (int i = 0; i <= steps; ++i) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                // tile of this stream's previous and present step
-                const int tp = two ? i - 1 : 2 * (i - 1) + s, tn = two ? i : 2 * i + s;
-                if (i > 0 && tp < n) {
-                    const uint32_t f = f0 + tp, st = f % G::kValues;
-                    wait(ctl, smem_u32(&sh->rv.full[st]), (f / G::kValues) & 1);
-                    wait(ctl, smem_u32(&sh->p_full[s]), np[s] & 1);
-                    ++np[s];
-                    tc_fence_after();
-                    const uint64_t vb = operand(ring_v + st * G::kStage, TileGeo<D>::kGroup, 1024);
-                    const uint32_t more = i > 1;
-                    const int steps_v = tile_steps(keys - tp * kTile);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            if (k < steps_v) mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * k, vb + (uint64_t)((k * 2 * TileGeo<D>::kGroup) >> 4), io, k > 0 ? 1u : more);
-                        if (!two || s == 1) tc_commit(smem_u32(&sh->rv.empty[st]));
-                        tc_commit(smem_u32(&sh->o_full[s]));
-                    }
-                    __syncwarp();
-                }
-                if (i < steps && tn < n) {
-                    const uint32_t f = f0 + tn, st = f % G::kKeys;
-                    wait(ctl, smem_u32(&sh->rk.full[st]), (f / G::kKeys) & 1);
-                    tc_fence_after();
-                    const uint64_t qa = operand(sq + (two ? s * G::kStage : 0), TileGeo<D>::kGroup, 0),
-                                   kb = operand(ring_k + st * G::kStage, TileGeo<D>::kGroup, 0);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint64_t at = (uint64_t)(TileGeo<D>::step(k) >> 4);
-                            mma_ss(tmem + 128 * s, qa + at, kb + at, is, k > 0);
+        for (int own = two ? 0 : s, before = -1;; before = own, own += two ? 1 : 2) {
+            uint32_t v = 0, vbar = 0;
+            int steps = 0;
+            if (before >= 0) {
+#pragma unroll 1
+                for (; to <= before; ++to) {
+                    wait(ctl, smem_u32(&sh->rv.full[vst]), vround & 1);
+                    vbar = smem_u32(&sh->rv.empty[vst]);
+                    v = ring_v + vst * G::kStage;
+                    if (to < before) {
+                        if (elect_one()) mbar_arrive(vbar);
+                    } else if (to >= first_tail) {  // while the weights are worked out
+                        if (!two || s == 0) {
+                            if (clean_values<D>(v, max(c.ctx - c.key0 - to * kTile, 0), keys - to * kTile, threadIdx.x & 31, 32))
+                                *reinterpret_cast<volatile uint32_t*>(&sh->poison[piece % kPieces]) = piece + 1;
+                            fence_async_smem();
+                            __syncwarp();
+                            if (two && elect_one()) mbar_arrive(smem_u32(&sh->v_clean[vst]));
+                        } else {
+                            wait(ctl, smem_u32(&sh->v_clean[vst]), (tails >> vst) & 1);
+                            tails ^= 1u << vst;
+                            fence_async_smem();
                         }
-                        if (!two || s == 1) tc_commit(smem_u32(&sh->rk.empty[st]));
-                        tc_commit(smem_u32(&sh->s_full[s]));
                     }
                     __syncwarp();
+                    if (++vst == G::kValues) vst = 0, ++vround;
+                }
+                steps = tile_steps(keys - before * kTile);
+                const uint32_t more = before > (two ? 0 : s);
+                const uint64_t vb = operand(v, TileGeo<D>::kGroup, 1024);
+                wait(ctl, smem_u32(&sh->p_full[s][0]), used & 1);
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < steps) mma_ts(t_o, t_s + 8 * k, vb + (uint64_t)((k * 2 * TileGeo<D>::kGroup) >> 4), io, k > 0 ? 1u : more);
+                    tc_commit(smem_u32(&sh->o_full[s][0]));
+                    mbar_arrive(smem_u32(&sh->o_full[s][0]));  // orders the piece's poison before it
+                }
+                __syncwarp();
+            }
+            // keys for the next scores, before the weights that they wait for
+            uint32_t k0 = 0, kbar = 0;
+#pragma unroll 1
+            for (; ts < n && ts <= own; ++ts) {
+                wait(ctl, smem_u32(&sh->rk.full[kst]), kround & 1);
+                kbar = smem_u32(&sh->rk.empty[kst]);
+                k0 = ring_k + kst * G::kStage;
+                if (ts < own && elect_one()) mbar_arrive(kbar);
+                __syncwarp();
+                if (++kst == G::kKeys) kst = 0, ++kround;
+            }
+            const uint64_t kb = operand(k0, TileGeo<D>::kGroup, 0), vb = operand(v + 8 * TileGeo<D>::kGroup, TileGeo<D>::kGroup, 1024);
+            if (before >= 0) wait(ctl, smem_u32(&sh->p_full[s][1]), used & 1);
+            tc_fence_after();
+            if (elect_one()) {
+                if (before >= 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (4 + k < steps) mma_ts(t_o, t_s + 64 + 8 * k, vb + (uint64_t)((k * 2 * TileGeo<D>::kGroup) >> 4), io, 1u);
+                    tc_commit(vbar);
+                    tc_commit(smem_u32(&sh->o_full[s][1]));
+                    mbar_arrive(smem_u32(&sh->o_full[s][1]));
+                }
+                if (own < n) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t at = (uint64_t)(TileGeo<D>::step(k) >> 4);
+                        mma_ss(t_s, qa + at, kb + at, is, k > 0);
+                    }
+                    tc_commit(kbar);
+                    tc_commit(smem_u32(&sh->s_full[s]));
                 }
             }
+            __syncwarp();
+            if (before >= 0) ++used;
+            if (own >= n) break;
         }
-        f0 += n;
+        // the other stream's last tile
+#pragma unroll 1
+        for (; to < n; ++to) {
+            wait(ctl, smem_u32(&sh->rv.full[vst]), vround & 1);
+            if (elect_one()) mbar_arrive(smem_u32(&sh->rv.empty[vst]));
+            __syncwarp();
+            if (++vst == G::kValues) vst = 0, ++vround;
+        }
+        sh->pieces.done(piece);
     }
 }
 
@@ -190,14 +242,14 @@ __device__ __forceinline__ void add_poison(const AttnParams& p, const PieceInfo&
 }
 
 template <int D, bool kPlanned>
-__device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, unsigned char* sq, uint32_t ring_v, uint32_t tmem) {
+__device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, unsigned char* sq, uint32_t tmem) {
     using G = TcGeo<D>;
     const int tid = threadIdx.x, lane = tid & 31, s = tid >> 7, r = tid & 127, quad = (tid >> 5) & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t t_s = tmem + lanes + 128 * s;
     const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;  // a negative scale goes into q
     const float scale = fabsf(p.scale2) > 0.0f ? fabsf(p.scale2) : 1e-30f;  // 0: equal weights, and -inf stays -inf
-    uint32_t f0 = 0, steps0[2] = {0, 0};  // fills and steps of earlier pieces
+    uint32_t steps0[2] = {0, 0};  // steps of earlier pieces
     int pending = 0;
     for (uint32_t piece = 0;; ++piece) {
         const int rows = sh->pieces.get(ctl, piece);
@@ -217,11 +269,9 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
             const int k = rr & (kTile - 1);
             *reinterpret_cast<uint4*>(sq + (rr / kTile) * G::kStage + TileGeo<D>::at(k, ch)) = v;
         }
-        if (tid == 0) sh->poison = 0;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh->q_full[piece & 1]));
-        rows_sync<256>();  // poison is clear
         const int rr = two ? s * kTile + r : r;  // row of the unit's block
         const bool active = quad * 32 + (two ? s * kTile : 0) < rows;
         const bool mine = rr < rows;
@@ -230,39 +280,29 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         const int steps = two ? n : (n + 1 - s) / 2;  // tiles of this stream
         float m = kNegInf, l = 0.0f;                  // reference (times scale), sum
 #pragma unroll 1
-        for (int i = 0; i < steps; ++i) {
-            const int tt = two ? i : 2 * i + s;
+        for (int x = 0; x < 2 * steps; ++x) {
+            const int i = x >> 1, h = x & 1, tt = two ? i : 2 * i + s;
             const uint32_t step = steps0[s] + i;
             const bool tail = tt >= first_tail;
-            wait(ctl, smem_u32(&sh->s_full[s]), step & 1);
-            if (tail) {
-                // The scores are there, and with them the products with the values of two tiles before: the
-                // stage's earlier fill has landed, so this one may be waited for.
-                const uint32_t f = f0 + tt, st = f % G::kValues;
-                wait(ctl, smem_u32(&sh->rv.full[st]), (f / G::kValues) & 1);
-                const int pos0 = c.key0 + tt * kTile;
-                // by both groups where both have the tile
-                if (clean_values<D>(ring_v + st * G::kStage, max(c.ctx - pos0, 0), c.end - pos0, two ? tid : r, two ? 256 : 128)) sh->poison = 1;
-                fence_async_smem();
-                if (two) rows_sync<256>();  // the other stream's product reads the same values
-            }
+            if (h == 0) wait(ctl, smem_u32(&sh->s_full[s]), step & 1);
             if (active) {
+                const uint32_t at_s = t_s + 64 * h;
                 tc_fence_after();
-                float z[kTile];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) ld32(t_s + 32 * q, z + 32 * q);
+                float z[64];
+                ld32(at_s, z);
+                ld32(at_s + 32, z + 32);
                 tc_wait_ld();
                 if (tail) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t seen = seen32(p, mask_row, node, c.ctx, c.end, c.key0 + tt * kTile + 32 * q);
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t seen = seen32(p, mask_row, node, c.ctx, c.end, c.key0 + tt * kTile + 64 * h + 32 * q);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) z[32 * q + e] = (seen >> e) & 1u ? z[32 * q + e] : kNegInf;
                     }
                 }
                 float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                for (int e = 0; e < kTile; e += 8)
+                for (int e = 0; e < 64; e += 8)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[q]) : "f"(z[e + 2 * q]), "f"(z[e + 2 * q + 1]));
@@ -271,8 +311,8 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
                 if (__any_sync(0xffffffffu, grow)) {
                     const float to = grow ? fmaxf(top, m) : m;
                     const float fac = m == kNegInf ? 0.0f : (grow ? ex2(m - to) : 1.0f);
-                    if (i > 0) {
-                        wait(ctl, smem_u32(&sh->o_full[s]), (step - 1) & 1);
+                    if (x > 0) {
+                        wait(ctl, smem_u32(&sh->o_full[s][h ^ 1]), (step - (h ^ 1)) & 1);  // the half before
                         tc_fence_after();
 #pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
@@ -290,37 +330,31 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
                 }
                 const float base = m == kNegInf ? 0.0f : -m;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                uint32_t pk[32];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float a = ex2(fmaf(z[64 * q + 2 * e], scale, base)), b = ex2(fmaf(z[64 * q + 2 * e + 1], scale, base));
-                        sum[(2 * e) & 3] += a;
-                        sum[(2 * e + 1) & 3] += b;
-                        pk[e] = pack_bf16(a, b);
-                    }
-                    st32(t_s + 32 * q, pk);
+                for (int e = 0; e < 32; ++e) {
+                    const float a = ex2(fmaf(z[2 * e], scale, base)), b = ex2(fmaf(z[2 * e + 1], scale, base));
+                    sum[(2 * e) & 3] += a;
+                    sum[(2 * e + 1) & 3] += b;
+                    pk[e] = pack_bf16(a, b);
                 }
+                st32(at_s, pk);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tc_wait_st();
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[s]));
-            } else {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[s]));
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[s][h]));
         }
         // the stream's last product; the other's is known to be done behind the next barrier
         const int steps_a = two ? n : (n + 1) / 2, steps_b = two ? n : n / 2;
-        if (steps > 0) wait(ctl, smem_u32(&sh->o_full[s]), (steps0[s] + steps - 1) & 1);
+        if (steps > 0) wait(ctl, smem_u32(&sh->o_full[s][1]), (steps0[s] + steps - 1) & 1);
         // with one block of rows the streams exchange their statistics where a second block of q would be
         float2* ml = reinterpret_cast<float2*>(sq + G::kStage);
         if (!two) ml[s * kTile + r] = make_float2(m, l);
         rows_sync<256>();
         tc_fence_after();
-        const bool poison = sh->poison != 0;
+        const bool poison = *reinterpret_cast<volatile uint32_t*>(&sh->poison[piece % kPieces]) == piece + 1;
         if (quad * 32 + (two ? s * kTile : 0) < rows) {
             const size_t orow = (size_t)(c.node0 + node) * p.Hq + hq;
             float fa = 1.0f, fb = 0.0f;
@@ -359,7 +393,6 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         }
         tc_fence_before();
         rows_sync<256>();  // sums and statistics have been read: the next piece may write over them
-        f0 += n;
         steps0[0] += steps_a;
         steps0[1] += steps_b;
         if (!kPlanned && c.join > 0) {
@@ -384,16 +417,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t ring_k = smem_u32(base + 2 * G::kStage), ring_v = ring_k + G::kKeys * G::kStage;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        sh->rk.init();
-        sh->rv.init();
-        sh->pieces.init(10);
+        sh->rk.init(2);
+        sh->rv.init(2);
+        sh->pieces.init(11);
         mbar_init(smem_u32(&sh->q_full[0]), 8);
         mbar_init(smem_u32(&sh->q_full[1]), 8);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&sh->s_full[s]), 1);
-            mbar_init(smem_u32(&sh->p_full[s]), 4);
-            mbar_init(smem_u32(&sh->o_full[s]), 1);
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(smem_u32(&sh->p_full[s >> 1][s & 1]), 4);
+            mbar_init(smem_u32(&sh->o_full[s >> 1][s & 1]), 2);
         }
+        mbar_init(smem_u32(&sh->s_full[0]), 1);
+        mbar_init(smem_u32(&sh->s_full[1]), 1);
+        for (int i = 0; i < G::kValues; ++i) mbar_init(smem_u32(&sh->v_clean[i]), 1);
+        for (int i = 0; i < kPieces; ++i) sh->poison[i] = 0;
         sh->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
@@ -413,12 +449,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // with 72 (2 x 216 + 72 = 3 x 168)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        tc_rows<D, kPlanned>(p, ctl, sh, sq, ring_v, tmem);
+        tc_rows<D, kPlanned>(p, ctl, sh, sq, tmem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 9)
-            tc_issue<D>(p, ctl, sh, smem_u32(sq), ring_k, ring_v, tmem);
-        else if (warp != 11)
+        if (warp == 9 || warp == 11)
+            wide_products<D>(p, ctl, sh, warp == 11, smem_u32(sq), ring_k, ring_v, tmem);
+        else
             wide_fill<D, kPlanned>(p, warp == 8, warp == 8 ? &mk : &mv, ctl, sh, warp == 8 ? ring_k : ring_v, lane);
     }
     tc_fence_before();
