@@ -34,7 +34,10 @@ template <int D>
 struct TcGeo {
     static constexpr int kStage = TileGeo<D>::kBytes;  // one tile of keys or of values
     static constexpr int kKeys = D == 128 ? 2 : 5, kValues = D == 128 ? 3 : 5;  // stages
-    static constexpr int kSmem = 1024 + 2 * kStage + (kKeys + kValues) * kStage;  // alignment, two blocks of q, the rings
+    // 2 KB of statistics: where a second block of q would be, or (the eight warps' 4 KB for outputs take two blocks of 64 columns)
+    // behind the rings
+    static constexpr int kStats = D == 128 ? kStage : (2 + kKeys + kValues) * kStage;
+    static constexpr int kSmem = 1024 + (2 + kKeys + kValues) * kStage + (D == 128 ? 0 : 2048);  // alignment, two blocks of q, the rings
 };
 
 template <int D>
@@ -198,19 +201,30 @@ __device__ void wide_products(const AttnParams& p, const Ctl& ctl, TcShared<D>* 
 
 // ---- rows ----
 
+// 32 columns of a warp's 32 rows, a lane's row in v, to the result or the slot (`to`: the lane's row of the result). They pass
+// through 4 KB of shared memory, after which eight lanes have a row's 128 bytes: stores by rows touched 32 lines each, and
+// those of a piece of 256 rows took 8000 clocks.
 template <int D>
-__device__ __forceinline__ void store_row(const AttnParams& p, const PieceInfo& c, size_t orow, int rr, int col, const float* v, float inv) {
-    if (c.whole) {
-        uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + col);
+__device__ __forceinline__ void store_rows(const AttnParams& p, const PieceInfo& c, unsigned char* stage, int row0, int count, int to, int col,
+                                           const float* v, int lane) {
+    float4* st = reinterpret_cast<float4*>(stage);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            to[i] = make_uint4(pack_bf16(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                               pack_bf16(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
-    } else {
-        float4* to = reinterpret_cast<float4*>(c.o + (size_t)rr * D + col);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) to[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int x = 0; x < 8; ++x) st[lane * 8 + (x ^ (lane & 7))] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+    __syncwarp();
+    const bool whole = c.whole;
+    float* o = c.o + (size_t)row0 * D + col;
+#pragma unroll 4
+    for (int x = 0; x < 8; ++x) {
+        const int r = 4 * x + (lane >> 3), part = lane & 7;
+        const float4 f = st[r * 8 + (part ^ (r & 7))];
+        const int at = __shfl_sync(0xffffffffu, to, r);
+        if (r >= count) continue;
+        if (whole)
+            attn_store4<1>(p.out, (size_t)at * D + col + 4 * part, f);
+        else
+            *reinterpret_cast<float4*>(o + r * D + 4 * part) = f;
     }
+    __syncwarp();
 }
 
 // NaN and infinities that were kept out of the product: added to the columns just stored where the row
@@ -259,15 +273,23 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         const bool two = rows > kTile;
         // q: a block of 128 rows for each stream, or one for both
         const int rows_q = min(rows, 2 * kTile);
-#pragma unroll 2
-        for (int i = tid; i < rows_q * (D / 8); i += 256) {
-            const int rr = i / (D / 8), ch = i - rr * (D / 8);
-            const int row = c.row0 + rr, node = attn_node(p, row), hq = c.hkv * p.gq + (row - node * p.gq);
-            uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                           (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + ch * 8));
-            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-            const int k = rr & (kTile - 1);
-            *reinterpret_cast<uint4*>(sq + (rr / kTile) * G::kStage + TileGeo<D>::at(k, ch)) = v;
+#pragma unroll 1
+        for (int i0 = tid; i0 < rows_q * (D / 8); i0 += 8 * 256) {  // eight loads in flight
+            uint4 v[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const int i = min(i0 + 256 * y, rows_q * (D / 8) - 1), rr = i / (D / 8), ch = i - rr * (D / 8);
+                const int row = c.row0 + rr, node = attn_node(p, row), hq = c.hkv * p.gq + (row - node * p.gq);
+                v[y] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                            (size_t)(c.node0 + node) * p.q_stride + (size_t)hq * D + ch * 8));
+            }
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const int i = i0 + 256 * y, rr = i / (D / 8), ch = i - rr * (D / 8);
+                if (rr >= rows_q) continue;
+                v[y].x ^= flip, v[y].y ^= flip, v[y].z ^= flip, v[y].w ^= flip;
+                *reinterpret_cast<uint4*>(sq + (rr / kTile) * G::kStage + TileGeo<D>::at(rr & (kTile - 1), ch)) = v[y];
+            }
         }
         fence_async_smem();
         __syncwarp();
@@ -349,8 +371,8 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         // the stream's last product; the other's is known to be done behind the next barrier
         const int steps_a = two ? n : (n + 1) / 2, steps_b = two ? n : n / 2;
         if (steps > 0) wait(ctl, smem_u32(&sh->o_full[s][1]), (steps0[s] + steps - 1) & 1);
-        // with one block of rows the streams exchange their statistics where a second block of q would be
-        float2* ml = reinterpret_cast<float2*>(sq + G::kStage);
+        // with one block of rows the streams exchange their statistics; the outputs pass through the place of the first block of q
+        float2* ml = reinterpret_cast<float2*>(sq + G::kStats);
         if (!two) ml[s * kTile + r] = make_float2(m, l);
         rows_sync<256>();
         tc_fence_after();
@@ -380,7 +402,12 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
 #pragma unroll
                     for (int e = 0; e < 32; ++e) a[e] = fmaf(a[e], fa, b[e] * fb);
                 }
-                if (mine) store_row<D>(p, c, orow, rr, col, a, inv);
+                if (c.whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) a[e] *= inv;
+                }
+                const int row_w = quad * 32 + (two ? s * kTile : 0);  // this warp's first
+                store_rows<D>(p, c, sq + (tid >> 5) * 4096, row_w, rows - row_w, (int)orow, col, a, lane);
             }
             if (mine && poison) add_poison<D>(p, c, mask_row, node, orow, rr, c0, c1);
             if (mine && (two || s == 0)) {
@@ -402,7 +429,7 @@ __device__ void tc_rows(const AttnParams& p, const Ctl& ctl, TcShared<D>* sh, un
         sh->pieces.done(piece);
     }
     if (!kPlanned && pending > 0)  // behind the barrier of the loop's end
-        attn_join_last<1, D, 8, 2>(p, sh->pieces.pending, pending, tid, 256, sh->pieces.last, [] { rows_sync<256>(); });
+        attn_join_last<1, D, 8, 3>(p, sh->pieces.pending, pending, tid, 256, sh->pieces.last, [] { rows_sync<256>(); });
 }
 
 template <int D, bool kPlanned>
