@@ -76,7 +76,7 @@ struct QuerySlots {
 
 // How a piece's rows and tiles are laid over the four groups: all of them on one piece, or (a short piece of few rows) the next
 // group alone, so that up to four such pieces are under way and the waits of one are filled by the others.
-constexpr int kSoloTiles = 4;
+constexpr int kSoloTiles = 8;
 struct Split {
     int log_tiles;  // tiles of a round: 4, 2 or 1
     int log_chunks; // groups side by side on the rows of one tile: 1, 2 or 4
