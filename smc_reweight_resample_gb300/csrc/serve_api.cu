@@ -42,17 +42,26 @@ bool attn_sizes_ok(int S, int N, int T, int Hq, int Hkv, int D) {
     return rows * N < (1ll << 30) && (long long)S * Hkv * (rows / 16 + 1) < (1ll << 30);
 }
 
-// float32: the FP32 pipes, 64 keys x 16 rows at a time. bf16: the tensor cores, 128 keys x up to 128 rows of a
-// sequence (narrow) or 256 (wide).
+// float32: the FP32 pipes, 64 keys x 16 rows at a time. bf16: the tensor cores, 128 keys x up to 128 rows (narrow) or 256 (wide)
+// at a time. The narrow kernel's time grows with a sequence's rows, the wide one's hardly does; with groups the
+// shared units are large in any case, and the wide kernel is the better one for them. Measured in us, narrow / wide:
+//   64 sequences over 4096 tokens, D = 128: 32 rows 140 / 152, 64 rows 151 / 159, 96 rows 166 / 171, 112 rows 194 / 176, 128 rows 198 / 178
+//   16 over 4096, D = 64: 64 rows 66.5 / 67.8, 100 rows 104 / 73
+//   8 groups of 16 over 2048, nine tenths shared: D = 128, 20 rows 98 / 102, 36 rows 157 / 132; D = 64, 5 rows 110 / 113, 21 rows 161 / 144
 enum AttnKind { kSimt, kNarrow, kWide };
 constexpr int kSimtBlocksPerSm = 2;
 // Places on the line (attn_plan.cuh): {rows from which a tile is heavy, of a light tile, of a heavy one, before a unit's tiles}.
+// A narrow tile takes 142 us' worth with 32 rows, 158 with 64, 183 with 96, 224 with 128 (64 sequences over 4096 tokens); a wide one of one
+// block of rows is shared out between the two streams. Measured: 64 chains of up to 21 nodes 165 us with equal tiles, 161 so, 177
+// with 2 : 4; 8 groups of 16 particles, whose own units are short and run four at a time, 118 / 110 / 99.5 / 102 us with 1 / 2 / 3 / 4
+// before a unit; 8 trees of up to 64 nodes 349 us with 1 : 2, 329 with 2 : 3, 341 with 3 : 4.
 struct LineCost { int heavy, light_tile, heavy_tile, empty; };
 constexpr LineCost kNarrowGroups{64, 2, 3, 3}, kNarrowCost{64, 2, 3, 6}, kWideCost{128, 2, 3, 6};
 
-AttnKind kind_of(int dtype, int T, int Hq, int Hkv) {
+AttnKind kind_of(int dtype, int N, int T, int Hq, int Hkv, int D) {
     if (dtype == SMCSD_F32) return kSimt;
-    return (long long)T * (Hq / Hkv) <= 128 ? kNarrow : kWide;
+    const int most = N > 1 ? D / 4 : D == 128 ? 96 : 64;
+    return (long long)T * (Hq / Hkv) <= most ? kNarrow : kWide;
 }
 
 int rows_of(AttnKind k) { return k == kSimt ? 16 : k == kNarrow ? 128 : 256; }
@@ -148,7 +157,7 @@ extern "C" int tree_mask(const int32_t* parents, const int32_t* node_offsets, in
 extern "C" size_t tree_attention_workspace_size(int S, int N, int T, int Hq, int Hkv, int D) {
     if (!attn_sizes_ok(S, N, T, Hq, Hkv, D)) return 0;
     const size_t a = layout_of(kSimt, S, N, T, Hq, Hkv, D).total,
-                 b = layout_of(kind_of(SMCSD_BF16, T, Hq, Hkv), S, N, T, Hq, Hkv, D).total;
+                 b = layout_of(kind_of(SMCSD_BF16, N, T, Hq, Hkv, D), S, N, T, Hq, Hkv, D).total;
     return a > b ? a : b;
 }
 
@@ -197,7 +206,7 @@ extern "C" int tree_attention(const void* q, long long q_stride, const void* k_c
     p.lse = lse;
     p.ws = ws;
     cudaStream_t st = (cudaStream_t)stream;
-    const AttnKind kind = kind_of(dtype, T, Hq, Hkv);
+    const AttnKind kind = kind_of(dtype, N, T, Hq, Hkv, D);
     // all places of all units are numbered in 32 bits
     const long long units = (long long)S * Hkv * attn_blocks((long long)T * p.gq, rows_of(kind)) +
                             (long long)p.G * Hkv * attn_blocks((long long)N * T * p.gq, rows_of(kind));
