@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     const int tid = threadIdx.x;
     int* shared = ws_ptr<int>(p.ws, p.L.shared);
     if (p.G > 0) {
-        // pages that every sequence of the group has at the same place, all of them full context; a thread has a column
+        // pages that every sequence of the group has at the same place, all of them full context; four threads have a
+        // column, a quarter of the sequences each
         const int s0 = blockIdx.x * p.N;
         if (tid == 0) best = p.pages_per_seq;
         __syncthreads();
@@ -83,11 +84,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         const int lim = best;
         __syncthreads();
         const int32_t* row = p.table + (long long)s0 * p.pages_per_seq;
-        for (int j = tid; j < lim && j < *reinterpret_cast<volatile int*>(&best); j += kPlanThreads) {
+        for (int j = tid & 127; j < lim && j < *reinterpret_cast<volatile int*>(&best); j += 128) {
             const int id = __ldg(row + j);
             bool same = id >= 0;
-#pragma unroll 8
-            for (int k = 1; k < p.N; ++k) same &= __ldg(row + (long long)k * p.pages_per_seq + j) == id;
+#pragma unroll 4
+            for (int k = 1 + (tid >> 7); k < p.N; k += kPlanThreads / 128) same &= __ldg(row + (long long)k * p.pages_per_seq + j) == id;
             if (!same) atomicMin(&best, j);
         }
         __syncthreads();
@@ -383,26 +384,48 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
     constexpr int kLanes = D / 4, kRows = 32 / kLanes;  // lanes of a row, rows of a warp at a time
     const int col = (lane % kLanes) * 4;
     const int step = gridDim.z * (kJoinThreads / 32) * kRows;
+    // Where the unit's pieces are is worked out once a block: its own, and those of the one or two row blocks of the shared
+    // unit that its rows lie in (with each thread's own divisions the kernel's instructions bound it).
+    __shared__ JoinRun s_run[3];
 #pragma unroll 1
     for (int u = blockIdx.y; u < p.Hkv * it.nrb; u += gridDim.y) {
-        const int hkv = u / it.nrb, row0 = (u - hkv * it.nrb) * it.per, rows = min(it.per, it.nodes * p.gq - row0);
-        const int rb = u - hkv * it.nrb, x0 = it.cum + hkv * cost.head(p, it) + rb * cost.unit(it.per, it.tiles) + cost.empty;  // its first tile's place
-        const int c0 = cut.block(x0), own_count = cut.block(x0 + (it.tiles - 1) * cost.tile(rows)) - c0 + 1;
-        if (!shared && own_count == 1) continue;  // written directly
+        const int hkv = it.nrb == 1 ? u : u / it.nrb, row0 = (u - hkv * it.nrb) * it.per, rows = min(it.per, it.nodes * p.gq - row0);
+        const int gr0 = row0 + (it.node0 - grp.node0) * p.gq, grb0 = shared ? gr0 / grp.per : 0;
+        if (threadIdx.x < 3) {
+            const bool own = threadIdx.x == 0;
+            const AttnItem& of = own ? it : grp;
+            const int rb = own ? u - hkv * it.nrb : grb0 + (int)threadIdx.x - 1;
+            JoinRun r{nullptr, nullptr, 0, 0};
+            if (own || (shared && rb < grp.nrb)) {
+                const int its = min(of.per, of.nodes * p.gq - rb * of.per);
+                const int x0 = of.cum + hkv * cost.head(p, of) + rb * cost.unit(of.per, of.tiles) + cost.empty;  // its first tile's place
+                const int c0 = cut.block(x0);
+                r.rows = own ? p.L.rows_s : p.L.rows_g;
+                const size_t at = (size_t)(of.unit0 + hkv * of.nrb + rb - (own ? h->units_shared : 0) + c0) * r.rows;
+                r.o = ws_ptr<float>(p.ws, own ? p.L.slot_s : p.L.slot_g) + at * D;
+                r.ml = ws_ptr<float2>(p.ws, own ? p.L.ml_s : p.L.ml_g) + at;
+                r.count = cut.block(x0 + (of.tiles - 1) * cost.tile(its)) - c0 + 1;
+            }
+            s_run[threadIdx.x] = r;
+        }
+        __syncthreads();
+        const bool direct = !shared && s_run[0].count == 1;  // written by the pass itself
 #pragma unroll 1
-        for (int r = (blockIdx.z * (kJoinThreads / 32) + warp) * kRows + lane / kLanes; r < rows; r += step) {
+        for (int r = (blockIdx.z * (kJoinThreads / 32) + warp) * kRows + lane / kLanes; r < rows && !direct; r += step) {
             const int row = row0 + r, n = attn_node(p, row);
             JoinRun run[2];
             run[0].count = 0;
             if (shared) {
-                const int gr = row + (it.node0 - grp.node0) * p.gq, grb = gr / grp.per, grows = min(grp.per, grp.nodes * p.gq - grb * grp.per);
-                const int g0 = grp.cum + hkv * cost.head(p, grp) + grb * cost.unit(grp.per, grp.tiles) + cost.empty, b0 = cut.block(g0);
-                const size_t at = (size_t)(grp.unit0 + hkv * grp.nrb + grb + b0) * p.L.rows_g + (gr - grb * grp.per);
-                run[0] = JoinRun{ws_ptr<float>(p.ws, p.L.slot_g) + at * D, ws_ptr<float2>(p.ws, p.L.ml_g) + at, (size_t)p.L.rows_g,
-                                 cut.block(g0 + (grp.tiles - 1) * cost.tile(grows)) - b0 + 1};
+                int at = gr0 + r - grb0 * grp.per;
+                const bool next = at >= grp.per;
+                at -= next ? grp.per : 0;
+                run[0] = s_run[1 + next];
+                run[0].o += (size_t)at * D;
+                run[0].ml += at;
             }
-            const size_t at = (size_t)(it.unit0 + u - h->units_shared + c0) * p.L.rows_s + r;
-            run[1] = JoinRun{ws_ptr<float>(p.ws, p.L.slot_s) + at * D, ws_ptr<float2>(p.ws, p.L.ml_s) + at, (size_t)p.L.rows_s, own_count};
+            run[1] = s_run[0];
+            run[1].o += (size_t)r * D;
+            run[1].ml += r;
             float2 s[4];
             float4 v[4];
 #pragma unroll
@@ -428,12 +451,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
             }
             j.store<DT, D>(p, (size_t)(it.node0 + n) * p.Hq + hkv * p.gq + (row - n * p.gq), col);
         }
+        __syncthreads();  // the unit's pieces have been read
     }
 }
 
 template <int DT, int D>
 static cudaError_t launch_combine_t(const AttnParams& p, cudaStream_t st) {
-    // a warp takes one row (four rows each, loads of its pieces one after the other: 21 us in place of 17 for 1024 units of 20 rows)
+    // a warp takes one row (four rows each, loads of its pieces one after the other: 21 us in place of 17, with cold caches, for
+    // 1024 units of 20 rows)
     const long long rows = (long long)p.T * p.gq, units = (long long)p.Hkv * attn_blocks(rows, 1 << p.log_rb);
     const unsigned parts = (unsigned)((rows < (1 << p.log_rb) ? rows : (1 << p.log_rb)) + 7) / 8;
     cudaLaunchConfig_t cfg{};
