@@ -16,7 +16,7 @@
 // last product with V. The softmax goes through a tile in two halves of 64 keys: half the registers (none of the loop's
 // values is spilled), and the first half's product runs during the second one's exponentials.
 //
-// 8 trees of up to 64 nodes over up to 32768 tokens, 64 query heads on 8, D = 128: 312 us, 0.87 PFLOP/s (45 % of the
+// 8 trees of up to 64 nodes over up to 32768 tokens, 64 query heads on 8, D = 128: 310 us, 0.88 PFLOP/s (45 % of the
 // measured bf16 rate; 140 us). What bounds it is a stream's chain: of 4200 clocks for a tile a group computes 1700, waits 1600 for
 // its next scores (last weights -> product -> scores -> commit) and spends the rest between; the products of both streams
 // take 2200. Measured otherwise: one warp issuing for both streams 356 us, scores by halves of 64 keys in two buffers 408 us
