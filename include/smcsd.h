@@ -34,9 +34,9 @@
  *     run is reproducible and its randomness can be shared with a checker.
  *   - `ws` is a scratch buffer of at least smcsd_workspace_size(op, ...) bytes, 256-byte aligned,
  *     which must be zero-filled once before its first use (smcsd_workspace_init). Every call that
- *     returns SMCSD_OK leaves the buffer's counters at zero again, so a buffer can be reused by
- *     calls in stream order without clearing. Calls that may overlap on the GPU need separate
- *     buffers.
+ *     returns SMCSD_OK leaves the buffer's counters at zero again, at one place for all operators
+ *     and sizes, so a buffer of the largest size needed can be reused by calls of any of them in
+ *     stream order without clearing. Calls that may overlap on the GPU need separate buffers.
  *   - Return value: SMCSD_OK, or a negative status for errors found on the host before anything
  *     is enqueued (bad argument, dtype, workspace size) or at launch (CUDA error). Errors that
  *     depend on device data (non-finite logits, token ids or offsets out of range) are recorded
@@ -305,7 +305,7 @@ int smc_step_tilted(const void* tgt_logits, const void* drf_logits, int dtype,
  * interface variant of smc_step (same step, same arguments and results, minus ws / ws_bytes)
  * for callers that cannot allocate device memory for a workspace, such as a host program with no
  * device allocator or a plugin that must not use its host's allocator. The call allocates
- * nothing: its scratch is a 32 MiB device area owned by this library (SMCSD_STATIC_SCRATCH_BYTES),
+ * nothing: its scratch is a device area of a little over 32 MiB owned by this library (SMCSD_STATIC_SCRATCH_BYTES),
  * set aside when the library's device code is loaded.
  *   status: optional int32 device pointer; receives this call's device-side status (SMCSD_OK or
  *     a negative SMCSD_* code, as smcsd_check_status would report), written in stream order.
@@ -319,7 +319,7 @@ int smc_step_tilted(const void* tgt_logits, const void* drf_logits, int dtype,
  * order them, for instance on one stream. The first call on a device looks the area's address up
  * with that device current; make that first call before any stream capture begins.
  */
-#define SMCSD_STATIC_SCRATCH_BYTES (32u << 20)
+#define SMCSD_STATIC_SCRATCH_BYTES ((32u << 20) + (32u << 10))
 int smc_step_static(const void* tgt_logits, const void* drf_logits, int dtype,
                     const int32_t* draft_tokens, int G, int N, int K, int V, float temperature,
                     float alpha, const float* bonus_uniforms, float* logw, int32_t* bonus_token,

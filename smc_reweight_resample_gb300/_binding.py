@@ -390,7 +390,7 @@ def smc_step_logq(tgt_logits, draft_tokens, drf_logq, G, N, K, V, temperature, a
                 table_out=table_out, refcount=refcount)
 
 
-STATIC_SCRATCH_BYTES = 32 << 20
+STATIC_SCRATCH_BYTES = (32 << 20) + (32 << 10)
 
 
 def smc_step_static(tgt_logits, drf_logits, draft_tokens, G, N, K, V, temperature, alpha,

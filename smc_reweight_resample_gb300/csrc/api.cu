@@ -37,6 +37,11 @@ int check_ws(const void* ws, size_t ws_bytes, size_t need) {
 
 int elem_bytes(int dtype) { return dtype == SMCSD_F32 ? 4 : 2; }
 
+// Counters that do not stand in the workspace's front.
+cudaError_t clear_counters(const WsLayout& L, void* ws, cudaStream_t st) {
+    return L.clear_bytes ? cudaMemsetAsync(static_cast<char*>(ws) + L.clear, 0, L.clear_bytes, st) : cudaSuccess;
+}
+
 }  // namespace
 
 extern "C" size_t smcsd_workspace_size(int op, int S, int K, int V) {
@@ -53,7 +58,7 @@ extern "C" size_t smcsd_workspace_size(int op, int S, int K, int V) {
         case SMCSD_OP_ESS_RESAMPLE:
         case SMCSD_OP_PAGETABLE_REMAP:
         case SMCSD_OP_PACER_BLOCK_STOP:
-            return ws_small_bytes(S);
+            return ws_small_bytes();
         case SMCSD_OP_KV_SLOT_MAP:
             if (V <= 0) return 0;
             return slot_map_bytes(S, V);
@@ -141,7 +146,8 @@ extern "C" int sd_verify(const void* tgt_logits, const void* drf_logits, int dty
     if (p.items >= (1ll << 31)) return SMCSD_ERR_INVALID_ARG;
     p.div_seq = make_fastdiv((uint32_t)(p.slots * p.cpr));
     p.div_cpr = make_fastdiv((uint32_t)p.cpr);
-    cudaError_t e = launch_stream(p, st);
+    cudaError_t e = clear_counters(L, ws, st);
+    if (e == cudaSuccess) e = launch_stream(p, st);
     if (e != cudaSuccess) return SMCSD_ERR_CUDA;
 
     SampleParams q{};
@@ -274,7 +280,8 @@ static int smc_step_impl(const void* tgt_logits, const void* drf_logits, const f
     p.pages_per_seq = pages_per_seq;
     p.refcount = remap ? refcount : nullptr;  // zeroed by the streaming pass
     p.num_pages = num_pages;
-    return from_cuda(launch_stream(p, st));
+    const cudaError_t e = clear_counters(p.L, ws, st);
+    return from_cuda(e == cudaSuccess ? launch_stream(p, st) : e);
 }
 
 extern "C" int smc_step_tilted(const void* tgt_logits, const void* drf_logits, int dtype,
@@ -345,7 +352,7 @@ extern "C" int smc_ess_resample(float* logw, int G, int N, float ess_threshold,
                                 int32_t* resampled, void* ws, size_t ws_bytes, void* stream) {
     if (!logw || !uniforms || !ancestors || G <= 0 || N <= 0 || isnan(ess_threshold))
         return SMCSD_ERR_INVALID_ARG;
-    int rc = check_ws(ws, ws_bytes, ws_small_bytes(G));
+    int rc = check_ws(ws, ws_bytes, ws_small_bytes());
     if (rc) return rc;
     ResampleParams p{logw, G, N, ess_threshold, uniforms, ancestors, ess, resampled, ws, exp2_table()};
     return from_cuda(launch_resample(p, (cudaStream_t)stream));
@@ -358,7 +365,7 @@ extern "C" int kv_pagetable_remap(const int32_t* ancestors, const int32_t* resam
     if (!ancestors || !table_in || !table_out || table_in == table_out) return SMCSD_ERR_INVALID_ARG;
     if (G <= 0 || N <= 0 || pages_per_seq <= 0) return SMCSD_ERR_INVALID_ARG;
     if (refcount && num_pages <= 0) return SMCSD_ERR_INVALID_ARG;
-    int rc = check_ws(ws, ws_bytes, ws_small_bytes(G));
+    int rc = check_ws(ws, ws_bytes, ws_small_bytes());
     if (rc) return rc;
     cudaStream_t st = (cudaStream_t)stream;
     if (refcount && cudaMemsetAsync(refcount, 0, (size_t)num_pages * sizeof(int32_t), st) != cudaSuccess)
@@ -376,7 +383,7 @@ extern "C" int pacer_block_stop_pos(const void* hidden, const void* w, const voi
     if (S <= 0 || b <= 0 || b > 64 || max_blocks <= 0 || d <= 0) return SMCSD_ERR_INVALID_ARG;
     if (!isfinite(c) || !isfinite(t0) || !finite_pos(rho)) return SMCSD_ERR_INVALID_ARG;
     if ((tgt_offsets == nullptr) != (drf_offsets == nullptr)) return SMCSD_ERR_INVALID_ARG;
-    int rc = check_ws(ws, ws_bytes, ws_small_bytes(S));
+    int rc = check_ws(ws, ws_bytes, ws_small_bytes());
     if (rc) return rc;
     PacerParams p{};
     p.hidden = static_cast<const uint16_t*>(hidden);

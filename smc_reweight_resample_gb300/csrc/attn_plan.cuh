@@ -40,8 +40,6 @@ struct __align__(16) AttnItem {
 };
 
 struct AttnHead {  // written by the planning kernel
-    int flag;      // error flag (first word of every workspace)
-    unsigned done; // blocks of the planning kernel that have finished
     int ncta, base, rest;  // W = ncta * base + rest
     int units_shared;      // units of shared items, which are the first ones
     int weighted;          // AttnCost
@@ -49,11 +47,12 @@ struct AttnHead {  // written by the planning kernel
 
 // Every kernel that takes part has at most kAttnMaxCta blocks on the line.
 constexpr int kAttnMaxCta = 1024;
+static_assert(kAttnMaxCta <= kFrontArrivals, "a block's counter in the workspace's front");
 constexpr int kAttnWarpPlan = 1024;  // sequences whose places on the line a warp works out
 inline bool attn_planned(int S, int N) { return N > 1 || S > kAttnWarpPlan; }
 
 struct AttnLayout {
-    size_t count;    // unsigned [kAttnMaxCta]: pieces that have arrived, of the unit that is cut first at a block's end
+    size_t head;     // AttnHead
     size_t item;     // AttnItem [G + S]
     size_t shared;   // int [G] keys shared by a group
     size_t slot_g;   // pieces of shared units: float [slots][rows_g][D], then float2 [slots][rows_g]
@@ -68,9 +67,9 @@ inline int attn_blocks(long long rows, int rb) { return (int)((rows + rb - 1) / 
 inline AttnLayout attn_layout(int S, int N, int T, int gq, int Hkv, int D, int RB, int ncta) {
     AttnLayout L{};
     const size_t G = N > 1 ? (size_t)S / N : 0;
-    size_t o = 256;
-    L.count = o;
-    o = align256(o + 4 * kAttnMaxCta);
+    size_t o = kFrontBytes;
+    L.head = o;
+    o = align256(o + sizeof(AttnHead));
     L.item = o;
     o = align256(o + sizeof(AttnItem) * (G + S));
     L.shared = o;
@@ -119,7 +118,7 @@ struct AttnParams {
     bool planned;  // by the planning kernel
 };
 
-__device__ __forceinline__ AttnHead* attn_head(const AttnParams& p) { return static_cast<AttnHead*>(p.ws); }
+__device__ __forceinline__ AttnHead* attn_head(const AttnParams& p) { return ws_ptr<AttnHead>(p.ws, p.L.head); }
 
 // First row and number of nodes of sequence s; none (and an error) if the offsets do not fit.
 __device__ __forceinline__ int attn_nodes(const AttnParams& p, int s, int& node0) {
@@ -423,13 +422,14 @@ struct AttnJoin {
     }
 };
 
+// The counter of a unit is that of the block in which it is cut first (kFrontArrive).
 // The block's threads, all of whose stores to the pieces' slots lie before a barrier: reports up to two pieces (a block's
 // first and last) and joins the units that they complete. `s_last` is shared; sync() a barrier of these threads.
 template <int DT, int D, int kRows, int kPieces, typename Sync>
 __device__ __forceinline__ void attn_join_last(const AttnParams& p, const PieceInfo* piece, int count, int tid, int threads,
                                                volatile int* s_last, Sync sync) {
     if (tid < count) {
-        unsigned* counter = ws_ptr<unsigned>(p.ws, p.L.count) + piece[tid].counter;
+        unsigned* counter = ws_ptr<unsigned>(p.ws, kFrontArrive) + piece[tid].counter;
         const bool last = atom_add_release(counter, 1u) == (unsigned)piece[tid].join - 1;
         if (last) {
             fence_acquire();

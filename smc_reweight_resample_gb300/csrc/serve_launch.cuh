@@ -90,8 +90,8 @@ struct LogitsParams {
     void* ws;
 };
 
-inline size_t slot_map_free_list() { return 256; }
-inline size_t slot_map_demand(int num_pages) { return align256(256 + 4 * (size_t)num_pages); }
+inline size_t slot_map_free_list() { return kFrontBytes; }
+inline size_t slot_map_demand(int num_pages) { return align256(slot_map_free_list() + 4 * (size_t)num_pages); }
 inline size_t slot_map_bytes(int S, int num_pages) { return align256(slot_map_demand(num_pages) + 4 * (size_t)S); }
 
 cudaError_t launch_slot_map(const SlotParams& p, cudaStream_t st);

@@ -88,20 +88,37 @@ struct SeqState {  // per-sequence hand-off between the SD kernels
     int pad;
 };
 
+// The front of every workspace, at the same place for every operator and shape: what has to be zero when a call begins
+// (and is zero again when it has ended), and the exp table with the scale that it was built for. Everything else that a
+// call writes lies behind it (kFrontBytes), so that one buffer serves calls of any operators and sizes in turn. Operators
+// that keep neither (kv_append, tree_mask, logits_process) have the first 256 bytes alone.
+constexpr int kFrontSeqs = 1024;  // sequences whose counters stand here; those of larger calls are cleared by each call
+constexpr int kFrontArrivals = 1024;
+constexpr size_t kFrontSeq2 = 256;                                  // uint32 [kFrontSeqs]  second pass (SD)
+constexpr size_t kFrontSeq3 = kFrontSeq2 + 4 * kFrontSeqs;          // uint32 [kFrontSeqs]  third pass (SD)
+constexpr size_t kFrontGroup = kFrontSeq3 + 4 * kFrontSeqs;         // uint32 [kFrontSeqs]
+constexpr size_t kFrontMisc = kFrontGroup + 4 * kFrontSeqs;         // uint32 [16]
+constexpr size_t kFrontClaim = kFrontMisc + 256;                    // uint32 [64]  chunk claim counters (one per stripe) and a blocks-done count
+constexpr size_t kFrontArrive = kFrontClaim + 256;                  // uint32 [kFrontArrivals]  attention: pieces of cut units
+constexpr size_t kFrontPlanned = kFrontArrive + 4 * kFrontArrivals; // uint32  attention: blocks of the planning kernel
+constexpr size_t kFrontTab = kFrontPlanned + 256;                   // 4 tag words + kTabSize float2 (see setup_exp_table)
+constexpr size_t kFrontBytes = (kFrontTab + 16 + 8 * (size_t)kTabSize + 255) & ~(size_t)255;
+
 struct WsLayout {
     size_t flag;       // int32 error flag
-    size_t cnt_seq2;   // uint32 [S]  second pass (SD)
-    size_t cnt_seq3;   // uint32 [S]  third pass (SD)
-    size_t cnt_group;  // uint32 [S]
-    size_t cnt_misc;   // uint32 [16]
-    size_t claim;      // uint32 [64]  chunk claim counters (one per stripe) and a blocks-done count
+    size_t cnt_seq2;   // uint32 [S]  counters, in the front or (more than kFrontSeqs sequences) from `clear` on
+    size_t cnt_seq3;
+    size_t cnt_group;
+    size_t cnt_misc;
+    size_t claim;
+    size_t clear, clear_bytes;  // what a call has to clear first
     size_t fast;       // float2 [S * (2K+1) * cpr]
     size_t ddtot;      // float4 [S * 2 * cpr]          chunk totals of sampled rows
     size_t ddsub;      // float4 [S * 2 * cpr * kSubs]  lane-block partials of sampled rows
     size_t rtot;       // float4 [S * cpr]              residual chunk totals (SD)
     size_t rsub;       // float4 [S * cpr * kSubs]      residual lane-block partials (SD)
     size_t seq;        // SeqState [S]
-    size_t tab;        // cached exp table: 4 tag words + kTabSize float2 (see setup_exp_table)
+    size_t tab;        // cached exp table
     size_t total;
 };
 
@@ -112,19 +129,24 @@ inline WsLayout ws_layout(int S, int K, int V) {
     WsLayout L{};
     const size_t s = (size_t)(S > 0 ? S : 1), k = (size_t)(K > 0 ? K : 0);
     const size_t cpr = (size_t)chunks_per_row(V > 0 ? V : 1, 0);
-    size_t o = 0;
-    L.flag = o;
-    o = align256(o + 16);
-    L.cnt_seq2 = o;
-    o = align256(o + 4 * s);
-    L.cnt_seq3 = o;
-    o = align256(o + 4 * s);
-    L.cnt_group = o;
-    o = align256(o + 4 * s);
-    L.cnt_misc = o;
-    o = align256(o + 4 * 16);
-    L.claim = o;
-    o = align256(o + 4 * 64);
+    L.flag = 0;
+    L.cnt_seq2 = kFrontSeq2;
+    L.cnt_seq3 = kFrontSeq3;
+    L.cnt_group = kFrontGroup;
+    L.cnt_misc = kFrontMisc;
+    L.claim = kFrontClaim;
+    L.tab = kFrontTab;
+    size_t o = kFrontBytes;
+    L.clear = o;
+    if (s > kFrontSeqs) {
+        L.cnt_seq2 = o;
+        o = align256(o + 4 * s);
+        L.cnt_seq3 = o;
+        o = align256(o + 4 * s);
+        L.cnt_group = o;
+        o = align256(o + 4 * s);
+    }
+    L.clear_bytes = o - L.clear;
     L.fast = o;
     o = align256(o + 8 * s * (2 * k + 1) * cpr);
     L.ddtot = o;
@@ -137,14 +159,12 @@ inline WsLayout ws_layout(int S, int K, int V) {
     o = align256(o + 16 * s * cpr * kSubs);
     L.seq = o;
     o = align256(o + sizeof(SeqState) * s);
-    L.tab = o;
-    o = align256(o + 16 + 8 * (size_t)kTabSize);
     L.total = o;
     return L;
 }
 
-// Only the header and the counters are used by the resampling-only ops.
-inline size_t ws_small_bytes(int S) { return ws_layout(S, 0, 1).cnt_misc + 256; }
+// The resampling-only ops use the flag and the sixteen counters.
+inline size_t ws_small_bytes() { return kFrontMisc + 256; }
 
 template <typename T>
 __device__ __forceinline__ T* ws_ptr(void* ws, size_t off) {

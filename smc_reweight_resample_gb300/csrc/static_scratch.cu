@@ -5,16 +5,16 @@
 // program without a device allocator, a plugin that may not touch its host's allocator or memory
 // pools, a serving step whose device memory was planned once up front. This entry point gives
 // them the same step as smc_step with nothing allocated by the call: the scratch lives in a
-// file-scope device array of kStaticScratchBytes (32 MiB), set aside when the library's device
+// file-scope device array of kStaticScratchBytes (32 MiB and its front), set aside when the library's device
 // code is loaded.
 //
-// Placement. The workspace of a call is the last ws_layout(G*N, K, V).total bytes of the area.
-// The cached exp table is the last section of every layout and has the same size for every
-// shape, so it sits at one address for all shapes, and no section of any other shape ever
-// overlaps it: a table published by one call stays intact whatever shapes run in between, and
-// its tag (the scale it was built for) decides alone whether a later call may copy it.
+// Placement. The workspace of a call is the first ws_layout(G*N, K, V).total bytes of the area. The
+// counters and the cached exp table stand in its front (kFrontBytes), at one address for every
+// shape, and no section of any other shape ever overlaps them: a table published by one call stays
+// intact whatever shapes run in between, and its tag (the scale it was built for) decides alone
+// whether a later call may copy it.
 //
-// Per call: the part of the workspace that must start at zero (error flag, completion and claim
+// Per call: the part of the front that must start at zero (error flag, completion and claim
 // counters) is cleared on the stream first. The call then runs smc_step on that workspace and,
 // if `status` is given, copies the call's device-side status (0 or a negative SMCSD_* code)
 // there. No host-side state depends on the shape.
@@ -70,10 +70,8 @@ extern "C" int smc_step_static(const void* tgt_logits, const void* drf_logits, i
     void* ws = nullptr;
     int rc = scratch_address(dev, &ws);
     if (rc) return rc;
-    // the workspace ends where the area ends (L.total is a multiple of 256, so it stays aligned)
-    ws = static_cast<char*>(ws) + (kStaticScratchBytes - L.total);
     cudaStream_t st = (cudaStream_t)stream;
-    if (cudaMemsetAsync(ws, 0, L.fast, st) != cudaSuccess) return SMCSD_ERR_CUDA;
+    if (cudaMemsetAsync(ws, 0, kFrontTab, st) != cudaSuccess) return SMCSD_ERR_CUDA;
     rc = smc_step(tgt_logits, drf_logits, dtype, draft_tokens, G, N, K, V, temperature, alpha,
                   bonus_uniforms, logw, bonus_token, ess_threshold, resample_uniforms, ancestors,
                   ess, resampled, table_in, table_out, pages_per_seq, refcount, num_pages, ws,

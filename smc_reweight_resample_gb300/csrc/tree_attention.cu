@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
             // less than a tile is not worth a unit of its own
             const int keys = best << p.page_shift;
             shared[blockIdx.x] = keys >> p.log_tile ? keys : 0;
-            const unsigned old = atom_add_release(&attn_head(p)->done, 1u);
-            last = old == gridDim.x - 1;
+            unsigned* done = ws_ptr<unsigned>(p.ws, kFrontPlanned);
+            last = atom_add_release(done, 1u) == gridDim.x - 1;
             if (last) {
                 fence_acquire();
-                atomicExch(&attn_head(p)->done, 0u);
+                atomicExch(done, 0u);
             }
         }
         __syncthreads();
