@@ -42,7 +42,8 @@
  *     depend on device data (non-finite logits, token ids or offsets out of range) are recorded
  *     in `ws` and read with smcsd_check_status(). The kernels never trap and never wait on
  *     another block; the waits inside a block (the copy pipeline of the streaming pass) give
- *     up after about 2 s and record SMCSD_ERR_TIMEOUT. So a bad input cannot fault or hang the
+ *     up after about 2 s and record SMCSD_ERR_TIMEOUT. The counters that such a call leaves behind are
+ *     cleared by smcsd_check_status; calls that use the buffer before that are unspecified. So a bad input cannot fault or hang the
  *     GPU; outputs are unspecified after such an error.
  */
 #ifndef SMCSD_H
@@ -110,7 +111,7 @@ const char* smcsd_status_string(int code);
  * runs the streaming pass's two pipeline waits against a barrier and a slot tag that nothing
  * completes, each giving up after limit_us microseconds (1 .. 2000000) and recording
  * SMCSD_ERR_TIMEOUT in `ws` as a stalled pipeline would. Read it with smcsd_check_status; the
- * context stays usable. ws: any workspace of at least 4 bytes (zero-filled once, as always).
+ * context stays usable. ws: any workspace of at least 8 bytes (zero-filled once, as always).
  */
 int smcsd_selftest_wait(unsigned int limit_us, void* ws, size_t ws_bytes, void* stream);
 

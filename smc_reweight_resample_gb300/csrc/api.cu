@@ -79,18 +79,20 @@ extern "C" int smcsd_workspace_init(void* ws, size_t ws_bytes, void* stream) {
 extern "C" int smcsd_check_status(void* ws, void* stream) {
     if (!ws) return SMCSD_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
+    int flag[2] = {0, 0};  // the first error, and what a wait that ran out left to be cleared (raise_timeout)
     if (cudaStreamSynchronize(st) != cudaSuccess) return SMCSD_ERR_CUDA;
-    int flag = 0;
-    if (cudaMemcpy(&flag, ws, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return SMCSD_ERR_CUDA;
-    if (flag != 0 && cudaMemset(ws, 0, sizeof(int)) != cudaSuccess) return SMCSD_ERR_CUDA;
-    return flag;
+    if (cudaMemcpy(flag, ws, sizeof flag, cudaMemcpyDeviceToHost) != cudaSuccess) return SMCSD_ERR_CUDA;
+    // on the stream, whose next call may begin as soon as this returns
+    const size_t clear = flag[1] == (int)kFrontTab ? kFrontTab : flag[0] ? sizeof flag : 0;
+    if (clear && cudaMemsetAsync(ws, 0, clear, st) != cudaSuccess) return SMCSD_ERR_CUDA;
+    return flag[0];
 }
 
 extern "C" int smcsd_selftest_wait(unsigned int limit_us, void* ws, size_t ws_bytes, void* stream) {
     if (limit_us == 0 || limit_us > 2000000u) return SMCSD_ERR_INVALID_ARG;
-    int rc = check_ws(ws, ws_bytes, sizeof(int));
+    int rc = check_ws(ws, ws_bytes, 2 * sizeof(int));
     if (rc) return rc;
-    return from_cuda(launch_wait_selftest(ws, 1000ull * limit_us, (cudaStream_t)stream));
+    return from_cuda(launch_wait_selftest(ws, ws_bytes >= kFrontTab, 1000ull * limit_us, (cudaStream_t)stream));
 }
 
 extern "C" const char* smcsd_status_string(int code) {

@@ -198,7 +198,7 @@ struct PieceRing {
 // shared and tensor memory is handed on.
 __device__ __forceinline__ void settle(const Ctl& c) {
     if (!*reinterpret_cast<volatile int*>(c.abort)) return;
-    raise_error(c.ws, kErrTimeout);
+    raise_timeout(c.ws);
     const unsigned long long t0 = now_ns();
     while (now_ns() - t0 < 20000000ull) __nanosleep(1000);
 }

@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kFinishMaxWarps * kWarp)
             const bool ok = __all_sync(0xffffffffu, cluster_wait(smem_addr(&sBar), 0u));
             if (lane == 0) {
                 sLast = ok ? 1 : 0;
-                if (!ok) raise_error(p.ws, kErrTimeout);
+                if (!ok) raise_timeout(p.ws);
             }
         }
     }

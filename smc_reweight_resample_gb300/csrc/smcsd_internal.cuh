@@ -175,6 +175,13 @@ __device__ __forceinline__ void raise_error(void* ws, int code) {
     atomicCAS(reinterpret_cast<int*>(ws), 0, code);
 }
 
+// A wait ran out: what the call leaves of its counters is unknown. The workspace's second word says how much of the front
+// smcsd_check_status has to clear, whatever error the first word holds.
+__device__ __forceinline__ void raise_timeout(void* ws) {
+    atomicExch(reinterpret_cast<unsigned*>(ws) + 1, (unsigned)kFrontTab);
+    raise_error(ws, kErrTimeout);
+}
+
 // Opt-in self-checks (build with -DSMCSD_CHECKS): a failed check records a site code (-100 and
 // below) in the error flag and the offending value in the next word, and the caller skips the
 // access.

@@ -141,9 +141,9 @@ __device__ __forceinline__ bool tag_wait(uint32_t addr, uint32_t k, unsigned lon
 
 // Diagnostic: the pipeline's two waits, run by one warp against a full barrier and a slot tag
 // that nothing completes, each giving up after limit_ns and recording kErrTimeout, as the
-// streaming pass does when its pipeline stalls. No copy is issued, so none is in flight when the
+// streaming pass does when its pipeline stalls (`front`: in a workspace that has counters). No copy is issued, so none is in flight when the
 // kernel returns.
-__global__ void __launch_bounds__(32) wait_selftest_kernel(void* ws, unsigned long long limit_ns) {
+__global__ void __launch_bounds__(32) wait_selftest_kernel(void* ws, bool front, unsigned long long limit_ns) {
     __shared__ __align__(8) uint64_t bar;
     __shared__ __align__(8) unsigned long long tag;
     if (threadIdx.x == 0) {
@@ -155,7 +155,11 @@ __global__ void __launch_bounds__(32) wait_selftest_kernel(void* ws, unsigned lo
     const bool got_bar = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), 0u, limit_ns));
     unsigned long long seen = 0;
     const bool got_tag = __all_sync(0xffffffffu, tag_wait(smem_u32(&tag), 0u, seen, limit_ns));
-    if (threadIdx.x == 0 && (!got_bar || !got_tag)) raise_error(ws, kErrTimeout);
+    if (threadIdx.x != 0 || (got_bar && got_tag)) return;
+    if (front)
+        raise_timeout(ws);
+    else
+        raise_error(ws, kErrTimeout);
 }
 
 // Makes every word of `raw` an input of an (empty) instruction: what follows in program order
@@ -227,7 +231,7 @@ __device__ __noinline__ void tma_producer(const StreamParams& p, unsigned char* 
                 continue;
             }
             if ((streak & 1023u) != 0 || global_ns() - t_streak <= kWaitLimitNs) continue;
-            raise_error(p.ws, kErrTimeout);
+            raise_timeout(p.ws);
             it = -1;  // give the slot up below so that its consumers stop
         } else {
             streak = 0;
@@ -442,7 +446,7 @@ __device__ __forceinline__ void final_consumer(const StreamParams& p, const Prec
         const int slot0 = (int)(k % kRing), slot1 = slot0 + 1;
         unsigned long long seen0, seen1;
         if (!__all_sync(0xffffffffu, tag_wait(smem_u32(&tag[slot0]), k, seen0))) {
-            if (lane == 0) raise_error(p.ws, kErrTimeout);
+            if (lane == 0) raise_timeout(p.ws);
             break;
         }
         seen0 = __shfl_sync(0xffffffffu, seen0, 0);
@@ -453,7 +457,7 @@ __device__ __forceinline__ void final_consumer(const StreamParams& p, const Prec
             continue;
         }
         if (!__all_sync(0xffffffffu, tag_wait(smem_u32(&tag[slot1]), k + 1, seen1))) {
-            if (lane == 0) raise_error(p.ws, kErrTimeout);
+            if (lane == 0) raise_timeout(p.ws);
             break;
         }
         seen1 = __shfl_sync(0xffffffffu, seen1, 0);
@@ -470,7 +474,7 @@ __device__ __forceinline__ void final_consumer(const StreamParams& p, const Prec
         const bool pair = c.valid && mode == 1 && item1 != 0xffffffffu;
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[slot0]), (k / kRing) & 1u) &&
                                          mbar_wait(smem_u32(&full[slot1]), (k / kRing) & 1u))) {
-            if (lane == 0) raise_error(p.ws, kErrTimeout);
+            if (lane == 0) raise_timeout(p.ws);
             break;
         }
         bool wrote = false;
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
         const int slot = (int)(k % kRing);
         unsigned long long seen;
         if (!__all_sync(0xffffffffu, tag_wait(smem_u32(&tag[slot]), k, seen))) {
-            if (lane == 0) raise_error(p.ws, kErrTimeout);
+            if (lane == 0) raise_timeout(p.ws);
             break;
         }
         seen = __shfl_sync(0xffffffffu, seen, 0);
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
             continue;
         }
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[slot]), (k / kRing) & 1u))) {
-            if (lane == 0) raise_error(p.ws, kErrTimeout);
+            if (lane == 0) raise_timeout(p.ws);
             break;
         }
         const uint32_t item = (uint32_t)seen;  // 0xffffffff: a chunk with nothing to load
@@ -739,8 +743,8 @@ static cudaError_t launch_tma_t(const StreamParams& p0, cudaStream_t st) {
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kern), args);
 }
 
-cudaError_t launch_wait_selftest(void* ws, unsigned long long limit_ns, cudaStream_t st) {
-    wait_selftest_kernel<<<1, 32, 0, st>>>(ws, limit_ns);
+cudaError_t launch_wait_selftest(void* ws, bool front, unsigned long long limit_ns, cudaStream_t st) {
+    wait_selftest_kernel<<<1, 32, 0, st>>>(ws, front, limit_ns);
     return cudaGetLastError();
 }
 

@@ -157,3 +157,36 @@ def test_node_masks_and_lists_need_no_more_than_a_flag(smcsd):
     def logits(ws):
         return (smcsd.logits_process(z, 2, 2, 1000, ws=ws),)
     check_in_turn(smcsd, [(256, mask), attention(smcsd, 1, 1, 1, 2, 4, 1, 64, 2500, 0, torch.bfloat16), (256, logits)])
+
+
+@pytest.mark.parametrize("other", [False, True])
+def test_counters_after_a_wait_that_ran_out(smcsd, other):
+    # an aborted call leaves its counters anywhere; reading its status makes the buffer whole again, also where another error
+    # was recorded first
+    for need, call in (attention(smcsd, 2, 1, 1, 1, 4, 1, 128, 3000, 0, torch.bfloat16),
+                       attention(smcsd, 5, 8, 4, 3, 4, 2, 128, 700, 640, torch.bfloat16),
+                       verify(smcsd, 3, 7, 3, 5003), step(smcsd, 6, 90, 2, 2, 2048)):
+        ws = Buffer(smcsd, need).ws
+        want = [t.clone() for t in call(ws)]
+        words = ws.buf[ws.ptr - ws.buf.data_ptr():][:COUNTERS.stop].view(torch.int32)
+        words[64:] = 1
+        if other:
+            words[0] = smcsd.ERR_RANGE
+        smcsd.selftest_wait(ws, 1000)
+        assert smcsd.check_status(ws) == (smcsd.ERR_RANGE if other else smcsd.ERR_TIMEOUT)
+        assert int(words.count_nonzero()) == 0
+        for a, b in zip(call(ws), want):
+            assert torch.equal(a, b)
+        assert smcsd.check_status(ws) == 0
+
+
+def test_a_status_is_cleared_on_its_stream(smcsd):
+    # the next call on the stream records an error at once: the clearing of the one before may not come after it
+    need, call = verify(smcsd, 3, 7, 3, 5003)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        ws = Buffer(smcsd, need).ws
+        for _ in range(20):
+            smcsd.selftest_wait(ws, 10)
+            assert smcsd.check_status(ws, stream) == smcsd.ERR_TIMEOUT
+        assert smcsd.check_status(ws, stream) == 0
