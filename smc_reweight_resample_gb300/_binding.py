@@ -98,7 +98,7 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -150,6 +150,26 @@ def check_status(ws: Workspace, stream=None) -> int:
     return int(load().smcsd_check_status(ctypes.c_void_p(ws.ptr), _stream(stream)))
 
 
+def _on(stream, call, given):
+    """call(**given) with `stream` as the current one, so that what it allocates (workspace, outputs) is that stream's memory
+    and is filled in its order. The caching allocator hands memory out again in the order of the stream that it belongs to:
+    what crosses between `stream` and the caller's own is marked as in use on both."""
+    del given["stream"]
+    current = torch.cuda.current_stream(stream.device)
+    if stream == current:
+        return call(**given)
+    with torch.cuda.stream(stream):
+        got = call(**given)
+    for t in given.values():
+        t = getattr(t, "buf", t)  # of a workspace
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    for t in got.values() if isinstance(got, dict) else got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            t.record_stream(current)
+    return got
+
+
 def _out(t, shape, dtype, device):
     return torch.empty(shape, dtype=dtype, device=device) if t is None else t
 
@@ -158,6 +178,8 @@ def sd_verify(tgt_logits, drf_logits, draft_tokens, S, K, V, temperature, unifor
               tgt_offsets=None, drf_offsets=None, ws=None, accept_len=None, out_token=None,
               lse_tgt=None, lse_drf=None, stream=None):
     """Returns (accept_len, out_token) int32 tensors [S]."""
+    if stream is not None:
+        return _on(stream, sd_verify, locals())
     dev = tgt_logits.device
     ws = ws or Workspace(OP_SD_VERIFY, S, K, V, dev)
     accept_len = _out(accept_len, (S,), torch.int32, dev)
@@ -166,7 +188,7 @@ def sd_verify(tgt_logits, drf_logits, draft_tokens, S, K, V, temperature, unifor
     rc = load().sd_verify(_ptr(tgt_logits), _ptr(drf_logits), _dtype_code(tgt_logits),
                           _ptr(draft_tokens), _ptr(tgt_offsets), _ptr(drf_offsets), S, K, V,
                           float(temperature), _ptr(uniforms), _ptr(accept_len), _ptr(out_token),
-                          _ptr(lse_tgt), _ptr(lse_drf), w, n, _stream(stream))
+                          _ptr(lse_tgt), _ptr(lse_drf), w, n, _stream())
     _check(rc, "sd_verify")
     return accept_len, out_token
 
@@ -174,6 +196,8 @@ def sd_verify(tgt_logits, drf_logits, draft_tokens, S, K, V, temperature, unifor
 def smc_reweight(tgt_logits, drf_logits, draft_tokens, S, K, V, temperature, alpha, uniforms,
                  logw, ws=None, bonus_token=None, lse_tgt=None, lse_drf=None, stream=None):
     """Updates logw in place; returns bonus_token int32 [S]."""
+    if stream is not None:
+        return _on(stream, smc_reweight, locals())
     dev = tgt_logits.device
     ws = ws or Workspace(OP_SMC_REWEIGHT, S, K, V, dev)
     bonus_token = _out(bonus_token, (S,), torch.int32, dev)
@@ -181,7 +205,7 @@ def smc_reweight(tgt_logits, drf_logits, draft_tokens, S, K, V, temperature, alp
     rc = load().smc_reweight(_ptr(tgt_logits), _ptr(drf_logits), _dtype_code(tgt_logits),
                              _ptr(draft_tokens), S, K, V, float(temperature), float(alpha),
                              _ptr(uniforms), _ptr(logw), _ptr(bonus_token), _ptr(lse_tgt),
-                             _ptr(lse_drf), w, n, _stream(stream))
+                             _ptr(lse_drf), w, n, _stream())
     _check(rc, "smc_reweight")
     return bonus_token
 
@@ -193,6 +217,8 @@ def smc_reweight_tilted(tgt_logits, drf_logits, draft_tokens, S, K, V, temperatu
     """smc_reweight toward the per-position (TARGET_TOKEN) or whole-sequence (TARGET_SEQUENCE)
     power target, with an optional additive log-reward float32 [S]. Updates logw in place;
     returns bonus_token int32 [S]."""
+    if stream is not None:
+        return _on(stream, smc_reweight_tilted, locals())
     dev = tgt_logits.device
     ws = ws or Workspace(OP_SMC_REWEIGHT, S, K, V, dev)
     bonus_token = _out(bonus_token, (S,), torch.int32, dev)
@@ -201,7 +227,7 @@ def smc_reweight_tilted(tgt_logits, drf_logits, draft_tokens, S, K, V, temperatu
                                     _ptr(draft_tokens), S, K, V, float(temperature), float(alpha),
                                     int(target), _ptr(log_reward), float(reward_scale),
                                     _ptr(uniforms), _ptr(logw), _ptr(bonus_token), _ptr(lse_tgt),
-                                    _ptr(lse_drf), w, n, _stream(stream))
+                                    _ptr(lse_drf), w, n, _stream())
     _check(rc, "smc_reweight_tilted")
     return bonus_token
 
@@ -210,6 +236,8 @@ def draft_sample(logits, R, V, temperature, uniforms, ws=None, tokens=None, logq
                  stream=None):
     """One token per row of logits [R, V] from softmax(z/T). Returns (tokens int32 [R], logq
     float [R] or None); pass logq=False to skip it, lse (float [R]) to get the normalisers."""
+    if stream is not None:
+        return _on(stream, draft_sample, locals())
     dev = logits.device
     ws = ws or Workspace(OP_DRAFT_SAMPLE, R, 0, V, dev)
     tokens = _out(tokens, (R,), torch.int32, dev)
@@ -220,7 +248,7 @@ def draft_sample(logits, R, V, temperature, uniforms, ws=None, tokens=None, logq
     w, n = ws.args
     rc = load().draft_sample(_ptr(logits), _dtype_code(logits), R, V, float(temperature),
                              _ptr(uniforms), _ptr(tokens), _ptr(logq), _ptr(lse), w, n,
-                             _stream(stream))
+                             _stream())
     _check(rc, "draft_sample")
     return tokens, logq
 
@@ -228,6 +256,8 @@ def draft_sample(logits, R, V, temperature, uniforms, ws=None, tokens=None, logq
 def smc_ess_resample(logw, G, N, ess_threshold, uniforms, ws=None, ancestors=None, ess=None,
                      resampled=None, stream=None):
     """Updates logw in place; returns (ancestors [G*N], ess [G], resampled [G])."""
+    if stream is not None:
+        return _on(stream, smc_ess_resample, locals())
     dev = logw.device
     ws = ws or Workspace(OP_ESS_RESAMPLE, G, 0, 1, dev)
     ancestors = _out(ancestors, (G * N,), torch.int32, dev)
@@ -235,7 +265,7 @@ def smc_ess_resample(logw, G, N, ess_threshold, uniforms, ws=None, ancestors=Non
     resampled = _out(resampled, (G,), torch.int32, dev)
     w, n = ws.args
     rc = load().smc_ess_resample(_ptr(logw), G, N, float(ess_threshold), _ptr(uniforms),
-                                 _ptr(ancestors), _ptr(ess), _ptr(resampled), w, n, _stream(stream))
+                                 _ptr(ancestors), _ptr(ess), _ptr(resampled), w, n, _stream())
     _check(rc, "smc_ess_resample")
     return ancestors, ess, resampled
 
@@ -243,6 +273,8 @@ def smc_ess_resample(logw, G, N, ess_threshold, uniforms, ws=None, ancestors=Non
 def kv_pagetable_remap(ancestors, resampled, G, N, table_in, pages_per_seq, num_pages=0,
                        table_out=None, refcount=None, with_refcount=True, ws=None, stream=None):
     """Returns (table_out, refcount or None)."""
+    if stream is not None:
+        return _on(stream, kv_pagetable_remap, locals())
     dev = table_in.device
     ws = ws or Workspace(OP_PAGETABLE_REMAP, G, 0, 1, dev)
     table_out = _out(table_out, table_in.shape, torch.int32, dev)
@@ -251,7 +283,7 @@ def kv_pagetable_remap(ancestors, resampled, G, N, table_in, pages_per_seq, num_
     w, n = ws.args
     rc = load().kv_pagetable_remap(_ptr(ancestors), _ptr(resampled), G, N, _ptr(table_in),
                                    _ptr(table_out), pages_per_seq, _ptr(refcount), num_pages, w, n,
-                                   _stream(stream))
+                                   _stream())
     _check(rc, "kv_pagetable_remap")
     return table_out, refcount
 
@@ -260,6 +292,8 @@ def pacer_block_stop(hidden, w, c, S, b, max_blocks, d, t0, rho, ws=None, length
                      block_scores=None, offsets=True, stream=None):
     """hidden bf16 [S, max_blocks*b, d], w bf16 [d]. Returns (lengths, block_scores,
     tgt_offsets, drf_offsets); the offsets are None when offsets=False."""
+    if stream is not None:
+        return _on(stream, pacer_block_stop, locals())
     return pacer_block_stop_pos(hidden, w, None, c, S, b, max_blocks, d, t0, rho, ws, lengths,
                                 block_scores, offsets, stream)
 
@@ -267,6 +301,8 @@ def pacer_block_stop(hidden, w, c, S, b, max_blocks, d, t0, rho, ws=None, length
 def pacer_block_stop_pos(hidden, w, pos_emb, c, S, b, max_blocks, d, t0, rho, ws=None,
                          lengths=None, block_scores=None, offsets=True, stream=None):
     """pacer_block_stop with position embeddings pos_emb bf16 [max_blocks*b, d] (None: none)."""
+    if stream is not None:
+        return _on(stream, pacer_block_stop_pos, locals())
     dev = hidden.device
     ws = ws or Workspace(OP_PACER_BLOCK_STOP, S, 0, 1, dev)
     lengths = _out(lengths, (S,), torch.int32, dev)
@@ -277,12 +313,12 @@ def pacer_block_stop_pos(hidden, w, pos_emb, c, S, b, max_blocks, d, t0, rho, ws
     if pos_emb is None:
         rc = load().pacer_block_stop(_ptr(hidden), _ptr(w), float(c), S, b, max_blocks, d,
                                      float(t0), float(rho), _ptr(lengths), _ptr(block_scores),
-                                     _ptr(to), _ptr(do), wp, n, _stream(stream))
+                                     _ptr(to), _ptr(do), wp, n, _stream())
     else:
         rc = load().pacer_block_stop_pos(_ptr(hidden), _ptr(w), _ptr(pos_emb), float(c), S, b,
                                          max_blocks, d, float(t0), float(rho), _ptr(lengths),
                                          _ptr(block_scores), _ptr(to), _ptr(do), wp, n,
-                                         _stream(stream))
+                                         _stream())
     _check(rc, "pacer_block_stop")
     return lengths, block_scores, to, do
 
@@ -312,6 +348,8 @@ def smc_step_tilted(tgt_logits, drf_logits, draft_tokens, G, N, K, V, temperatur
                     stream=None):
     """smc_step toward a tilted target (see smc_reweight_tilted). Updates logw in place.
     Returns a dict of output tensors."""
+    if stream is not None:
+        return _on(stream, smc_step_tilted, locals())
     dev = tgt_logits.device
     ws = ws or Workspace(OP_SMC_STEP, G * N, K, V, dev)
     o = _step_outputs(dev, G, N, table_in, num_pages, bonus_token, ancestors, ess, resampled,
@@ -324,7 +362,7 @@ def smc_step_tilted(tgt_logits, drf_logits, draft_tokens, G, N, K, V, temperatur
                                 float(ess_threshold), _ptr(resample_uniforms),
                                 _ptr(o["ancestors"]), _ptr(o["ess"]), _ptr(o["resampled"]),
                                 _ptr(table_in), _ptr(o["table_out"]), pages_per_seq,
-                                _ptr(o["refcount"]), num_pages, w, n, _stream(stream))
+                                _ptr(o["refcount"]), num_pages, w, n, _stream())
     _check(rc, "smc_step_tilted")
     return o
 
@@ -334,6 +372,8 @@ def smc_step(tgt_logits, drf_logits, draft_tokens, G, N, K, V, temperature, alph
              pages_per_seq=0, num_pages=0, ws=None, bonus_token=None, ancestors=None, ess=None,
              resampled=None, table_out=None, refcount=None, with_refcount=True, stream=None):
     """Fused SMC-SD step. Updates logw in place. Returns a dict of output tensors."""
+    if stream is not None:
+        return _on(stream, smc_step, locals())
     dev = tgt_logits.device
     S = G * N
     ws = ws or Workspace(OP_SMC_STEP, S, K, V, dev)
@@ -353,7 +393,7 @@ def smc_step(tgt_logits, drf_logits, draft_tokens, G, N, K, V, temperature, alph
                          _ptr(bonus_uniforms), _ptr(logw), _ptr(bonus_token), float(ess_threshold),
                          _ptr(resample_uniforms), _ptr(ancestors), _ptr(ess), _ptr(resampled),
                          _ptr(table_in), _ptr(table_out), pages_per_seq, _ptr(refcount), num_pages,
-                         w, n, _stream(stream))
+                         w, n, _stream())
     _check(rc, "smc_step")
     return dict(bonus_token=bonus_token, ancestors=ancestors, ess=ess, resampled=resampled,
                 table_out=table_out, refcount=refcount)
@@ -365,6 +405,8 @@ def smc_step_logq(tgt_logits, draft_tokens, drf_logq, G, N, K, V, temperature, a
                   ess=None, resampled=None, table_out=None, refcount=None, with_refcount=True,
                   stream=None):
     """smc_step with the draft's log q(x_k) (float32 [G*N*K]) in place of the draft logits."""
+    if stream is not None:
+        return _on(stream, smc_step_logq, locals())
     dev = tgt_logits.device
     S = G * N
     ws = ws or Workspace(OP_SMC_STEP, S, K, V, dev)
@@ -384,7 +426,7 @@ def smc_step_logq(tgt_logits, draft_tokens, drf_logq, G, N, K, V, temperature, a
                               _ptr(bonus_uniforms), _ptr(logw), _ptr(bonus_token),
                               float(ess_threshold), _ptr(resample_uniforms), _ptr(ancestors),
                               _ptr(ess), _ptr(resampled), _ptr(table_in), _ptr(table_out),
-                              pages_per_seq, _ptr(refcount), num_pages, w, n, _stream(stream))
+                              pages_per_seq, _ptr(refcount), num_pages, w, n, _stream())
     _check(rc, "smc_step_logq")
     return dict(bonus_token=bonus_token, ancestors=ancestors, ess=ess, resampled=resampled,
                 table_out=table_out, refcount=refcount)
@@ -401,6 +443,8 @@ def smc_step_static(tgt_logits, drf_logits, draft_tokens, G, N, K, V, temperatur
     """smc_step on the library's own scratch area (no workspace argument). Output tensors must
     be passed in by a caller that cannot allocate; missing ones are allocated here for
     convenience. `status` (int32 [1] on the device) receives the call's device-side status."""
+    if stream is not None:
+        return _on(stream, smc_step_static, locals())
     dev = tgt_logits.device
     S = G * N
     bonus_token = _out(bonus_token, (S,), torch.int32, dev)
@@ -419,7 +463,7 @@ def smc_step_static(tgt_logits, drf_logits, draft_tokens, G, N, K, V, temperatur
                                 float(ess_threshold), _ptr(resample_uniforms), _ptr(ancestors),
                                 _ptr(ess), _ptr(resampled), _ptr(table_in), _ptr(table_out),
                                 pages_per_seq, _ptr(refcount), num_pages, _ptr(status),
-                                _stream(stream))
+                                _stream())
     _check(rc, "smc_step_static")
     return dict(bonus_token=bonus_token, ancestors=ancestors, ess=ess, resampled=resampled,
                 table_out=table_out, refcount=refcount)
@@ -459,20 +503,18 @@ def _native():
     return _calls
 
 
-def _handle(stream):
-    return None if stream is None else stream.cuda_stream
-
-
 def kv_slot_map(ctx_len, table_in, refcount_in, S, T, page_size, new_offsets=None, rows=None, ws=None,
                 table_out=None, refcount_out=None, slots=None, copy_src=None, copy_dst=None,
                 stream=None):
     """Page tables, slots and copies of the step's new tokens. table_in int32 [S, pages_per_seq],
     refcount_in int32 [num_pages]; T new tokens for each sequence, or given by new_offsets (int32 [S+1],
     `rows` tokens in all). Returns dict(table_out, refcount_out, slots, copy_src, copy_dst)."""
+    if stream is not None:
+        return _on(stream, kv_slot_map, locals())
     ws = ws or Workspace(OP_KV_SLOT_MAP, S, 0, refcount_in.numel(), table_in.device)
     o = (_calls or _native()).kv_slot_map(ctx_len, table_in, refcount_in, S, T, page_size, new_offsets, rows,
                                           table_out, refcount_out, slots, copy_src, copy_dst, ws.ptr,
-                                          ws.nbytes, _handle(stream))
+                                          ws.nbytes)
     return {"table_out": o[0], "refcount_out": o[1], "slots": o[2], "copy_src": o[3], "copy_dst": o[4]}
 
 
@@ -481,16 +523,20 @@ def kv_append(k_new, v_new, slots, k_cache, v_cache, ctx_len=None, copy_src=None
     """Writes k_new, v_new [R, Hkv, D] (rows may be strided) to their slots (int64 [R]) of the caches
     [num_pages, Hkv, page_size, D], and the page copies that kv_slot_map asked for. Returns the caches,
     which are changed in place."""
+    if stream is not None:
+        return _on(stream, kv_append, locals())
     ws = ws or Workspace(OP_KV_APPEND, 1, device=k_cache.device)
     (_calls or _native()).kv_append(k_new, v_new, slots, k_cache, v_cache, ctx_len, copy_src, copy_dst, ws.ptr,
-                                    ws.nbytes, _handle(stream))
+                                    ws.nbytes)
     return k_cache, v_cache
 
 
 def tree_mask(parents, S, T, node_offsets=None, mask=None, ws=None, stream=None):
     """Node mask int32 [R, ceil(T/32)] (bits) of the trees that parents (int32 [R]) describes."""
+    if stream is not None:
+        return _on(stream, tree_mask, locals())
     ws = ws or Workspace(OP_TREE_MASK, 1, device=parents.device)
-    return (_calls or _native()).tree_mask(parents, S, T, node_offsets, mask, ws.ptr, ws.nbytes, _handle(stream))
+    return (_calls or _native()).tree_mask(parents, S, T, node_offsets, mask, ws.ptr, ws.nbytes)
 
 
 def tree_attention(q, k_cache, v_cache, table, ctx_len, S, T, scale, N=1, node_offsets=None, mask=None,
@@ -499,9 +545,11 @@ def tree_attention(q, k_cache, v_cache, table, ctx_len, S, T, scale, N=1, node_o
     sequences with tables int32 [S, pages_per_seq] and ctx_len cached tokens, and over the nodes that
     each row sees (mask int32 [R, ceil(T/32)]; None: a chain). Returns (out [R, Hq, D], lse float
     [R, Hq], or None without it)."""
+    if stream is not None:
+        return _on(stream, tree_attention, locals())
     ws = ws or TreeAttentionWorkspace(S, N, T, q.shape[1], k_cache.shape[1], q.shape[2], q.device)
     return (_calls or _native()).tree_attention(q, k_cache, v_cache, table, ctx_len, S, T, scale, N, node_offsets,
-                                                mask, out, lse, with_lse, ws.ptr, ws.nbytes, _handle(stream))
+                                                mask, out, lse, with_lse, ws.ptr, ws.nbytes)
 
 
 def logits_process(logits, S, T, V, node_offsets=None, node_tokens=None, mask=None, hist_tokens=None,
@@ -509,8 +557,9 @@ def logits_process(logits, S, T, V, node_offsets=None, node_tokens=None, mask=No
                    bias_values=None, bias_offsets=None, allowed=None, out=None, ws=None, stream=None):
     """Penalties, biases and a grammar mask (bits, int32 [R, ceil(V/32)]) on logits [R, V]; pass
     out=logits to change them in place. Returns out."""
+    if stream is not None:
+        return _on(stream, logits_process, locals())
     ws = ws or Workspace(OP_LOGITS_PROCESS, 1, device=logits.device)
     return (_calls or _native()).logits_process(logits, S, T, V, node_offsets, node_tokens, mask, hist_tokens,
                                                 hist_offsets, repetition, presence, frequency, bias_tokens,
-                                                bias_values, bias_offsets, allowed, out, ws.ptr, ws.nbytes,
-                                                _handle(stream))
+                                                bias_values, bias_offsets, allowed, out, ws.ptr, ws.nbytes)

@@ -125,7 +125,7 @@ int dim(int64_t n) {
     return (int)n;
 }
 
-// The last three arguments of every call: workspace address and size, stream (None: the current one).
+// The last two arguments of every call, workspace address and size, and the current stream.
 struct Tail {
     void* ws;
     size_t bytes;
@@ -134,8 +134,7 @@ struct Tail {
         ws = reinterpret_cast<void*>((uintptr_t)a.integer());
         bytes = (size_t)a.integer();
         if (!like.is_cuda()) value_error("tensor must be on the CUDA device");
-        stream = a.none() ? (void*)c10::cuda::getCurrentCUDAStream(like.get_device()).stream()
-                          : reinterpret_cast<void*>((uintptr_t)a.integer());
+        stream = (void*)c10::cuda::getCurrentCUDAStream(like.get_device()).stream();
     }
 };
 
@@ -190,10 +189,10 @@ PyObject* py_bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 // kv_slot_map(ctx_len, table_in, refcount_in, S, T, page_size, new_offsets, rows, table_out, refcount_out, slots,
-//             copy_src, copy_dst, ws, bytes, stream)
+//             copy_src, copy_dst, ws, bytes)
 PyObject* py_slot_map(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        Args a(args, n, 16);
+        Args a(args, n, 15);
         const at::Tensor &ctx = a.some(), &table = a.some(), &ref = a.some();
         const int S = a.size(), T = a.size(), page = a.size();
         const at::Tensor* off = a.tensor();
@@ -219,10 +218,10 @@ PyObject* py_slot_map(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// kv_append(k_new, v_new, slots, k_cache, v_cache, ctx_len, copy_src, copy_dst, ws, bytes, stream)
+// kv_append(k_new, v_new, slots, k_cache, v_cache, ctx_len, copy_src, copy_dst, ws, bytes)
 PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        Args a(args, n, 11);
+        Args a(args, n, 10);
         const at::Tensor &k = a.some(), &v = a.some(), &slots = a.some(), &kc = a.some(), &vc = a.some();
         const at::Tensor *ctx = a.tensor(), *src = a.tensor(), *dst = a.tensor();
         check_caches(kc, vc, k);
@@ -246,10 +245,10 @@ PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// tree_mask(parents, S, T, node_offsets, mask, ws, bytes, stream)
+// tree_mask(parents, S, T, node_offsets, mask, ws, bytes)
 PyObject* py_tree_mask(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        Args a(args, n, 8);
+        Args a(args, n, 7);
         const at::Tensor& parents = a.some();
         const int S = a.size(), T = a.size(), R = dim(parents.numel());
         const at::Tensor* off = a.tensor();
@@ -264,10 +263,10 @@ PyObject* py_tree_mask(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 // tree_attention(q, k_cache, v_cache, table, ctx_len, S, T, scale, N, node_offsets, mask, out, lse, with_lse, ws,
-//                bytes, stream)
+//                bytes)
 PyObject* py_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        Args a(args, n, 17);
+        Args a(args, n, 16);
         const at::Tensor &q = a.some(), &kc = a.some(), &vc = a.some(), &table = a.some(), &ctx = a.some();
         const int S = a.size(), T = a.size();
         const double scale = a.real();
@@ -298,10 +297,10 @@ PyObject* py_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 // logits_process(logits, S, T, V, node_offsets, node_tokens, mask, hist_tokens, hist_offsets, repetition, presence,
-//                frequency, bias_tokens, bias_values, bias_offsets, allowed, out, ws, bytes, stream)
+//                frequency, bias_tokens, bias_values, bias_offsets, allowed, out, ws, bytes)
 PyObject* py_logits(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        Args a(args, n, 20);
+        Args a(args, n, 19);
         const at::Tensor& z = a.some();
         const int S = a.size(), T = a.size(), V = a.size();
         if (V <= 0) value_error("V must be positive");
