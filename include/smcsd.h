@@ -341,7 +341,9 @@ int smc_step_static(const void* tgt_logits, const void* drf_logits, int dtype,
  *     drafts after it, as a chain or a tree. Fixed layout (node_offsets == NULL): n_s = T, node t of
  *     sequence s is row s*T+t. Ragged: node_offsets int32 [S+1] (ascending from 0), rows
  *     node_offsets[s] .. node_offsets[s+1]-1, n_s <= T. R is the number of rows (S*T if fixed);
- *     offsets that do not fit R or T are SMCSD_ERR_RANGE (device side).
+ *     offsets that do not fit R or T are SMCSD_ERR_RANGE (device side). Rows that no sequence has (before
+ *     node_offsets[0] or from node_offsets[S] on, as where R is padded for a captured graph) get the
+ *     slot -1 from kv_slot_map; the other operators leave their outputs as they are.
  *   - Paged cache: K and V each [num_pages, Hkv, page_size, D], contiguous, 16-byte aligned;
  *     page_size a power of two of 8 .. 256. Tables int32 [S, pages_per_seq], -1 = no page. Position x
  *     of a sequence is in page table[s][x / page_size] at offset x % page_size; its SLOT is
@@ -364,7 +366,7 @@ int smc_step_static(const void* tgt_logits, const void* drf_logits, int dtype,
  *   otherwise              the page is kept.
  * Free pages are those with refcount_in == 0, taken in ascending order; a taken page's
  * refcount_out is 1. Everything else is copied from table_in / refcount_in (the outputs must not
- * alias them). slots int64 [R]; copy_src, copy_dst int32 [S] (-1: no copy). The result does not
+ * alias them). slots int64 [R], -1 for every row of a sequence that is refused; copy_src, copy_dst int32 [S] (-1: no copy). The result does not
  * depend on the order of execution.
  * Device-side errors: SMCSD_ERR_RANGE (a negative length, more positions than the table has, ids or
  * offsets out of range), SMCSD_ERR_PAGES (too few free pages; the pages that are missing read -1 and

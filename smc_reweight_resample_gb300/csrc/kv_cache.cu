@@ -93,6 +93,9 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
         if (lane == 0) demand[s] = d;
         want += d;
     }
+    // ragged rows that no sequence has, or whose sequence is refused, keep this; the others are written behind the barriers
+    if (p.n.offsets)
+        for (long long i = (long long)rank * kSlotThreads + threadIdx.x; i < p.n.R; i += (long long)C * kSlotThreads) p.slots[i] = -1;
     // pages of this warp, in runs of 32 that a ballot counts
     const int runs = (p.num_pages + 31) / 32, rper = (runs + nw - 1) / nw;
     const int r0 = min(runs, gw * rper), r1 = min(runs, r0 + rper);
