@@ -92,12 +92,27 @@ void at_least(const at::Tensor* t, int64_t n, const char* what) {
     if (t && t->numel() < n) value_error(std::string(what) + " is too small");
 }
 
+// n rows of `row` elements, one behind the other: a flat tensor, or one whose inner dimensions make up a row (of rows longer
+// than the call takes them for, all but the first would be met at the wrong place).
+void rows_of(const at::Tensor* t, int64_t n, int64_t row, const char* what) {
+    if (!t) return;
+    at_least(t, n * row, what);
+    if (t->dim() < 2 || t->numel() == row) return;
+    int64_t inner = 1;
+    for (int64_t k = t->dim() - 1; k > 0; --k)
+        if ((inner *= t->size(k)) == row) return;
+    value_error(std::string(what) + " has rows of another size");
+}
+
 // An output: the given tensor, or a new one.
 at::Tensor output(const at::Tensor* t, at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
     if (!t) return at::empty(shape, like.options().dtype(type));
-    int64_t n = 1;
-    for (const int64_t s : shape) n *= s;
-    at_least(t, n, "an output");
+    int64_t row = 1;
+    for (size_t i = 1; i < shape.size(); ++i) row *= shape[i];
+    if (shape.size() > 1)
+        rows_of(t, shape[0], row, "an output");
+    else
+        at_least(t, shape[0], "an output");
     return *t;
 }
 
@@ -279,7 +294,7 @@ PyObject* py_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
         if (table.dim() != 2 || table.size(0) != S) value_error("table must be [S, pages_per_seq]");
         at_least(&ctx, S, "ctx_len");
         at_least(off, (int64_t)S + 1, "node_offsets");
-        at_least(mask, R * (((int64_t)T + 31) / 32), "mask");
+        rows_of(mask, R, ((int64_t)T + 31) / 32, "mask");
         const c10::cuda::CUDAGuard guard(q.device());
         const at::Tensor out = output(a.tensor(), {R, Hq, D}, q.scalar_type(), q);
         const at::Tensor* lse_in = a.tensor();
@@ -310,13 +325,15 @@ PyObject* py_logits(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor *bt = a.tensor(), *bv = a.tensor(), *bo = a.tensor(), *allowed = a.tensor();
         at_least(off, (int64_t)S + 1, "node_offsets");
         at_least(tokens, R, "node_tokens");
-        at_least(mask, R * (((int64_t)T + 31) / 32), "mask");
+        rows_of(mask, R, ((int64_t)T + 31) / 32, "mask");
         at_least(ho, (int64_t)S + 1, "hist_offsets");
         at_least(bo, (int64_t)S + 1, "bias_offsets");
-        at_least(allowed, R * (((int64_t)V + 31) / 32), "allowed");
+        rows_of(allowed, R, ((int64_t)V + 31) / 32, "allowed");
         for (const at::Tensor* t : {rep, pres, freq}) at_least(t, S, "a penalty");
         if (bt) at_least(bv, bt->numel(), "bias_values");
         if (!z.is_cuda()) value_error("tensor must be on the CUDA device");
+        rows_of(&z, R, V, "logits");
+        if (z.numel() != (int64_t)R * V) value_error("logits must be rows of V");
         const c10::cuda::CUDAGuard guard(z.device());
         const at::Tensor out = output(a.tensor(), {R, V}, z.scalar_type(), z);
         const Tail t(a, z);
