@@ -125,7 +125,9 @@ int dtype_code(const at::Tensor& t) {
 // A [rows, heads, D] tensor whose rows are contiguous: elements from one row to the next.
 int64_t row_stride(const at::Tensor& t) {
     if (t.dim() != 3 || !t.is_cuda()) value_error("tensor must be [rows, heads, D] on the CUDA device");
-    if (t.stride(2) != 1 || t.stride(1) != t.size(2)) value_error("the heads of a row must be contiguous");
+    // the stride of a dimension of one is never used and may be anything
+    if ((t.size(2) > 1 && t.stride(2) != 1) || (t.size(1) > 1 && t.stride(1) != t.size(2)))
+        value_error("the heads of a row must be contiguous");
     return t.size(0) > 1 ? t.stride(0) : t.size(1) * t.size(2);
 }
 
@@ -241,8 +243,7 @@ PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor *ctx = a.tensor(), *src = a.tensor(), *dst = a.tensor();
         check_caches(kc, vc, k);
         const int64_t stride = row_stride(k);
-        row_stride(v);
-        if (v.scalar_type() != k.scalar_type() || !v.sizes().equals(k.sizes()) || v.stride(0) != k.stride(0))
+        if (v.scalar_type() != k.scalar_type() || !v.sizes().equals(k.sizes()) || row_stride(v) != stride)
             value_error("keys and values must be alike");
         if (k.size(1) != kc.size(1) || k.size(2) != kc.size(3)) value_error("rows and caches must have the same heads");
         at_least(&slots, k.size(0), "slots");

@@ -72,3 +72,29 @@ def test_layouts_that_hold_the_same_rows_are_taken(smcsd):
     flat, l2 = torch.empty(4, 128, device="cuda"), torch.empty(6, device="cuda")
     smcsd.tree_attention(*args, out=flat, lse=l2)
     assert torch.equal(flat[:3].view(3, 2, 64), out) and torch.equal(l2.view(3, 2), lse)
+
+
+def test_strides_of_dimensions_of_one_do_not_matter(smcsd):
+    torch.manual_seed(1)
+    cache = torch.randn(4, 1, 16, 64, device="cuda")
+    args = (i32(0, 1)[None], i32(9), 1, 3, 1.0)
+    q = torch.randn(3, 1, 64, device="cuda")
+    want = smcsd.tree_attention(q, cache, cache, *args)[0]
+    one_head = torch.randn(3, 5, 64, device="cuda").transpose(0, 1)[:1].transpose(0, 1)  # [3, 1, 64] of a wider row
+    one_head.copy_(q)
+    assert one_head.stride(1) == 64 and torch.equal(smcsd.tree_attention(one_head, cache, cache, *args)[0], want)
+    odd = q.as_strided((3, 1, 64), (64, 7, 1))
+    assert torch.equal(smcsd.tree_attention(odd, cache, cache, *args)[0], want)
+    # one new token: keys and values as slices of differently wide rows, whose row strides differ
+    k, v = torch.randn(1, 2, 64, device="cuda"), torch.randn(1, 6, 64, device="cuda")[:, 3:5]
+    assert k.stride(0) != v.stride(0)
+    kc, vc = zeros(3, 2, 16, 64, dtype=torch.float32), zeros(3, 2, 16, 64, dtype=torch.float32)
+    smcsd.kv_append(k, v, torch.tensor([21], device="cuda"), kc, vc)
+    assert torch.equal(kc[1, :, 5], k[0]) and torch.equal(vc[1, :, 5], v[0])
+    # of several rows they have to be alike, and a row's heads side by side
+    k, v = torch.randn(2, 2, 64, device="cuda"), torch.randn(2, 6, 64, device="cuda")[:, 3:5]
+    with pytest.raises(ValueError, match="alike"):
+        smcsd.kv_append(k, v, torch.tensor([21, 22], device="cuda"), kc, vc)
+    with pytest.raises(ValueError, match="heads of a row"):
+        smcsd.tree_attention(torch.randn(4, 3, 64, device="cuda")[:, ::2], cache.expand(4, 2, 16, 64).contiguous(),
+                             cache.expand(4, 2, 16, 64).contiguous(), i32(0, 1)[None], i32(9), 1, 4, 1.0)
