@@ -116,6 +116,12 @@ at::Tensor output(const at::Tensor* t, at::IntArrayRef shape, at::ScalarType typ
     return *t;
 }
 
+// Whatever is given of these is where `like` is.
+void one_device(const at::Tensor& like, std::initializer_list<const at::Tensor*> list) {
+    for (const at::Tensor* t : list)
+        if (t && t->device() != like.device()) value_error("tensors must be on one device");
+}
+
 int dtype_code(const at::Tensor& t) {
     if (t.scalar_type() == at::kFloat) return SMCSD_F32;
     if (t.scalar_type() == at::kBFloat16) return SMCSD_BF16;
@@ -227,6 +233,7 @@ PyObject* py_slot_map(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor slots = output(a.tensor(), {R}, at::kLong, table);
         const at::Tensor src = output(a.tensor(), {S}, at::kInt, table);
         const at::Tensor dst = output(a.tensor(), {S}, at::kInt, table);
+        one_device(table, {&ctx, &ref, off, &table_out, &ref_out, &slots, &src, &dst});
         const Tail t(a, table);
         check(f_slot_map(i32(&ctx), i32(off), S, T, R, i32(&table), i32(&table_out), dim(table.size(1)), page, i32(&ref), i32(&ref_out),
                          pages, static_cast<int64_t*>(address(&slots, at::kLong)), i32(&src), i32(&dst), t.ws, t.bytes, t.stream),
@@ -250,6 +257,7 @@ PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const int S = src ? dim(src->numel()) : 0;
         at_least(dst, S, "copy_dst");
         at_least(ctx, S, "ctx_len");
+        one_device(kc, {&k, &v, &slots, &vc, ctx, src, dst});
         const Tail t(a, kc);
         const c10::cuda::CUDAGuard guard(kc.device());
         check(f_append(k.data_ptr(), v.data_ptr(), dtype_code(k), dim(k.size(0)), dim(kc.size(1)), dim(kc.size(3)), stride,
@@ -272,6 +280,7 @@ PyObject* py_tree_mask(PyObject*, PyObject* const* args, Py_ssize_t n) {
         if (!parents.is_cuda()) value_error("tensor must be on the CUDA device");
         const c10::cuda::CUDAGuard guard(parents.device());
         const at::Tensor mask = output(a.tensor(), {R, ((int64_t)T + 31) / 32}, at::kInt, parents);
+        one_device(parents, {off, &mask});
         const Tail t(a, parents);
         check(f_tree_mask(i32(&parents), i32(off), S, T, R, reinterpret_cast<uint32_t*>(i32(&mask)), t.ws, t.bytes, t.stream), "tree_mask");
         return THPVariable_Wrap(mask);
@@ -301,6 +310,7 @@ PyObject* py_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor* lse_in = a.tensor();
         at::Tensor lse;
         if (a.integer() || lse_in) lse = output(lse_in, {R, Hq}, at::kFloat, q);
+        one_device(q, {&kc, &vc, &table, &ctx, off, mask, &out, lse_in});
         const Tail t(a, q);
         const at::ScalarType type = q.scalar_type();
         check(f_attention(q.data_ptr(), stride, address(&kc, type), address(&vc, type), dtype_code(q), dim(kc.size(0)), dim(kc.size(2)),
@@ -337,6 +347,7 @@ PyObject* py_logits(PyObject*, PyObject* const* args, Py_ssize_t n) {
         if (z.numel() != (int64_t)R * V) value_error("logits must be rows of V");
         const c10::cuda::CUDAGuard guard(z.device());
         const at::Tensor out = output(a.tensor(), {R, V}, z.scalar_type(), z);
+        one_device(z, {off, tokens, mask, ht, ho, rep, pres, freq, bt, bv, bo, allowed, &out});
         const Tail t(a, z);
         const at::ScalarType type = z.scalar_type();
         check(f_logits(address(&z, type), address(&out, type), dtype_code(z), R, V, S, T, i32(off), i32(tokens),

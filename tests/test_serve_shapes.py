@@ -98,3 +98,26 @@ def test_strides_of_dimensions_of_one_do_not_matter(smcsd):
     with pytest.raises(ValueError, match="heads of a row"):
         smcsd.tree_attention(torch.randn(4, 3, 64, device="cuda")[:, ::2], cache.expand(4, 2, 16, 64).contiguous(),
                              cache.expand(4, 2, 16, 64).contiguous(), i32(0, 1)[None], i32(9), 1, 4, 1.0)
+
+
+def test_tensors_of_one_call_are_on_one_device(smcsd):
+    # any other device than the first tensor's, here the host, is named as what is wrong
+    cpu = torch.zeros(9, dtype=torch.int32)
+    q, cache = torch.randn(3, 2, 64, device="cuda"), torch.randn(4, 2, 16, 64, device="cuda")
+    table, ctx = i32(0, 1)[None], i32(9)
+    z = torch.randn(2, 100, device="cuda")
+    one = dict(match="one device")
+    with pytest.raises(ValueError, **one):
+        smcsd.tree_attention(q, cache, cache, table.cpu(), ctx, 1, 3, 1.0)
+    with pytest.raises(ValueError, **one):
+        smcsd.tree_attention(q, cache, cache, table, ctx, 1, 3, 1.0, out=torch.empty(3, 2, 64))
+    with pytest.raises(ValueError, **one):
+        smcsd.tree_attention(q, cache, cache.cpu(), table, ctx, 1, 3, 1.0)
+    with pytest.raises(ValueError, **one):
+        smcsd.kv_slot_map(ctx, table, cpu, 1, 1, 16, ws=smcsd.Workspace(smcsd.OP_KV_SLOT_MAP, 1, 0, 9))
+    with pytest.raises(ValueError, **one):
+        smcsd.kv_append(q, q, torch.zeros(3, dtype=torch.int64), cache, cache)
+    with pytest.raises(ValueError, **one):
+        smcsd.tree_mask(i32(-1, 0), 1, 2, mask=torch.zeros(2, 1, dtype=torch.int32))
+    with pytest.raises(ValueError, **one):
+        smcsd.logits_process(z, 2, 1, 100, node_tokens=cpu)
