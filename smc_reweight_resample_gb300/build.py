@@ -28,6 +28,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 # CPython module that marshals tensors for the calls around the verify (csrc/py_calls.cpp): host code only
 CALLS = os.path.join(HERE, "_calls.so")
+CALLS_KEY = os.path.join(BUILD, "calls.key")
 
 
 def nvcc() -> str:
@@ -76,31 +77,65 @@ def _calls_command(out: str):
             "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
+def _calls_key() -> str:
+    """What the module is good for: one Python, one torch with its C++ ABI, one compiler line."""
+    import torch
+
+    return "\n".join([sys.version, torch.__version__, *_calls_command(CALLS)])
+
+
 def _start_calls():
-    """The module's compiler, running (None if the module is up to date), and its output."""
+    """The module's compiler, running, with its output and key; None if the module is up to date, or if there is no torch that
+    it could be called from; or the error that kept the compiler from running."""
     deps = [os.path.join(CSRC, "py_calls.cpp"), os.path.join(INCLUDE, "smcsd.h")]
+    try:
+        key = _calls_key()
+    except ImportError:
+        return None
     if os.path.exists(CALLS) and all(os.path.getmtime(d) <= os.path.getmtime(CALLS) for d in deps):
-        return None, None
+        try:
+            with open(CALLS_KEY) as f:
+                if f.read() == key:
+                    return None
+        except OSError:
+            pass
     tmp = CALLS + f".tmp{os.getpid()}"
-    return subprocess.Popen(_calls_command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp
+    try:
+        return subprocess.Popen(_calls_command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp, key
+    except OSError as e:
+        return e
 
 
-def _finish_calls(proc, tmp):
-    if proc is None:
+def _finish_calls(started):
+    if started is None:
         return
+    if isinstance(started, OSError):
+        raise RuntimeError(f"no compiler for py_calls.cpp: {started}") from started
+    proc, tmp, key = started
     log, _ = proc.communicate()
     if proc.returncode != 0:
         sys.stdout.write(log.decode(errors="replace"))
         raise RuntimeError("the compiler failed for py_calls.cpp")
+    if os.path.exists(CALLS_KEY):
+        os.remove(CALLS_KEY)
     os.replace(tmp, CALLS)
+    os.makedirs(os.path.dirname(CALLS_KEY), exist_ok=True)
+    with open(CALLS_KEY, "w") as f:
+        f.write(key)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str = LIB,
           objdir: str = BUILD) -> str:
+    """The library, and the call module beside it, where they are not up to date. The library is there even if the module
+    cannot be built, which raises all the same."""
     calls = _start_calls()
-    if not force and not _stale(out):
-        _finish_calls(*calls)
-        return out
+    if force or _stale(out):
+        _build_library(verbose, extra_flags, out, objdir)
+    _finish_calls(calls)
+    return out
+
+
+def _build_library(verbose, extra_flags, out, objdir):
     os.makedirs(objdir, exist_ok=True)
     cc = nvcc()
     procs = []
@@ -124,8 +159,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str =
     tmp = out + f".tmp{os.getpid()}"
     subprocess.check_call([cc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, out)
-    _finish_calls(*calls)
-    return out
 
 
 if __name__ == "__main__":
