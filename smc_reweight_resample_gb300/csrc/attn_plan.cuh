@@ -11,11 +11,11 @@
 // unit's tiles as many empty places as beginning and ending a unit costs: W places (below 2^31). Block c of ncta has W / ncta
 // of them, the first W % ncta blocks one more, and takes the tiles that begin there: shares of equal cost whatever the lengths
 // and the rows are. Where a block would not get a tile's places, all tiles count one (AttnCost). Where a cut falls inside a unit, or a
-// row has a shared and an own unit, the pieces leave (sum, max, weighted values) in a slot. Without the planning kernel (and so
-// without groups) only a block's first and last piece can be part of a unit: block c has slots 2 c (a unit that began before
-// it) and 2 c + 1 (one that ends behind it), and the last block to finish a unit's pieces joins them, in the order of the
-// line. With it a piece of unit u in block c has slot u + c (both rise along the line and one of them rises from piece to
-// piece, so no two pieces share a slot), and a kernel of its own joins a row's pieces. The kernels exist once for each of the
+// row has a shared and an own unit, the pieces leave (sum, max, weighted values) in a slot. Without groups only a block's first
+// and last piece can be part of a unit: block c has slots 2 c (a unit that began before it) and 2 c + 1 (one that ends behind
+// it). With groups a piece of unit u in block c has slot u + c (both rise along the line and one of them rises from piece to
+// piece, so no two pieces share a slot). Without the planning kernel the last block to finish a unit's pieces joins them, in
+// the order of the line; with it a kernel of its own joins a row's pieces. The kernels exist once for each of the
 // two: what a call does not come to costs it all the same, since their code is longer than what an SM holds of it at a time.
 //
 // Who works the line out. Without groups and for up to 1024 sequences a warp of each block does, from the lengths
@@ -45,8 +45,9 @@ struct AttnHead {  // written by the planning kernel
     int weighted;          // AttnCost
 };
 
-// Every kernel that takes part has at most kAttnMaxCta blocks on the line.
-constexpr int kAttnMaxCta = 1024;
+// Blocks on the line: one or two for each SM, of which the GPU has 152 and a kernel uses no more than kAttnMaxSm. The scratch is
+// sized for them.
+constexpr int kAttnMaxSm = 160, kAttnMaxCta = 2 * kAttnMaxSm;
 static_assert(kAttnMaxCta <= kFrontArrivals, "a block's counter in the workspace's front");
 constexpr int kAttnWarpPlan = 1024;  // sequences whose places on the line a warp works out
 inline bool attn_planned(int S, int N) { return N > 1 || S > kAttnWarpPlan; }
@@ -77,7 +78,7 @@ inline AttnLayout attn_layout(int S, int N, int T, int gq, int Hkv, int D, int R
     const long long rs = (long long)T * gq, rg = rs * N;
     L.rows_s = (int)(rs < RB ? rs : RB);
     L.rows_g = (int)(rg < RB ? rg : RB);
-    const size_t us = attn_planned(S, N) ? (size_t)S * Hkv * attn_blocks(rs, RB) + ncta : 2 * (size_t)ncta;
+    const size_t us = G ? (size_t)S * Hkv * attn_blocks(rs, RB) + ncta : 2 * (size_t)ncta;
     const size_t ug = G ? G * Hkv * attn_blocks(rg, RB) + ncta : 0;
     L.slot_s = o;
     o = align256(o + us * L.rows_s * D * 4);
@@ -359,12 +360,10 @@ struct Walker {
         float* o = ws_ptr<float>(p.ws, own ? p.L.slot_s : p.L.slot_g);
         float2* ml = ws_ptr<float2>(p.ws, own ? p.L.ml_s : p.L.ml_g);
         size_t slot = (size_t)(it.unit0 + unit - (own ? units_shared : 0)) + cta;
-        if (!kPlanned) {
-            slot = 2 * cta + (a == 0);
-            if (!c.whole) {
-                c.counter = cut.block(first);
-                c.join = cut.block(first + (it.tiles - 1) * w) - c.counter + 1;
-            }
+        if (!kPlanned || p.G == 0) slot = 2 * cta + (a == 0);
+        if (!kPlanned && !c.whole) {
+            c.counter = cut.block(first);
+            c.join = cut.block(first + (it.tiles - 1) * w) - c.counter + 1;
         }
         c.o = o + slot * rows * p.D;
         c.ml = ml + slot * rows;

@@ -65,9 +65,10 @@ AttnKind kind_of(int dtype, int N, int T, int Hq, int Hkv, int D) {
 }
 
 int rows_of(AttnKind k) { return k == kSimt ? 16 : k == kNarrow ? 128 : 256; }
+int blocks_of(AttnKind k, int sms) { return (sms < kAttnMaxSm ? sms : kAttnMaxSm) * (k == kSimt ? kSimtBlocksPerSm : 1); }
 
 AttnLayout layout_of(AttnKind k, int S, int N, int T, int Hq, int Hkv, int D) {
-    return attn_layout(S, N, T, Hq / Hkv, Hkv, D, rows_of(k), kAttnMaxCta);
+    return attn_layout(S, N, T, Hq / Hkv, Hkv, D, rows_of(k), blocks_of(k, kAttnMaxSm));
 }
 
 }  // namespace
@@ -222,8 +223,7 @@ extern "C" int tree_attention(const void* q, long long q_stride, const void* k_c
     p.empty = cost.empty;
     p.empty_one = kind == kSimt ? 0 : 1;
     p.div_gq = make_fastdiv((uint32_t)p.gq);
-    p.ncta_max = device_sm_count() * (kind == kSimt ? kSimtBlocksPerSm : 1);
-    if (p.ncta_max > kAttnMaxCta) p.ncta_max = kAttnMaxCta;
+    p.ncta_max = blocks_of(kind, device_sm_count());
     p.div_cta = make_fastdiv((uint32_t)p.ncta_max);
     p.planned = attn_planned(S, N);
     cudaError_t e = p.planned ? launch_attn_plan(p, st) : cudaSuccess;

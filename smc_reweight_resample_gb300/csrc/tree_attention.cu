@@ -359,18 +359,23 @@ cudaError_t launch_attn_simt(const AttnParams& p, cudaStream_t st) {
 
 constexpr int kJoinThreads = 256;
 
-// The slots of one row's pieces of a unit.
+// The slots of one row's pieces of a unit, from the i-th on: one after the other with groups, otherwise every second one from
+// the second piece on.
 struct JoinRun {
     const float* o;
     const float2* ml;
     size_t rows;  // of a slot
     int count;
+    template <bool kGroups>
+    __device__ __forceinline__ size_t at(int i) const {
+        return (kGroups || i == 0 ? i : 2 * i - 1) * rows;
+    }
 };
 
 // After the planning kernel: a few blocks (z) for each sequence (x) and unit of it (y). A row's pieces are joined in the
 // order of the line, the shared unit's first: a warp has a row (of 64 columns: two), four columns a thread, and the first two
 // pieces of both units are loaded together.
-template <int DT, int D>
+template <int DT, int D, bool kGroups>
 __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid_constant__ AttnParams p) {
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -380,9 +385,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
     cut.base = h->base;
     cut.rest = h->rest;
     const AttnCost cost(p, h->weighted);
-    const AttnItem it = items[p.G + blockIdx.x], grp = items[p.G > 0 ? blockIdx.x / p.N : 0];
+    const AttnItem it = items[p.G + blockIdx.x], grp = items[kGroups ? blockIdx.x / p.N : 0];
     if (it.tiles == 0) return;
-    const bool shared = p.G > 0 && grp.tiles > 0;
+    const bool shared = kGroups && grp.tiles > 0;
     constexpr int kLanes = D / 4, kRows = 32 / kLanes;  // lanes of a row, rows of a warp at a time
     const int col = (lane % kLanes) * 4;
     const int step = gridDim.z * (kJoinThreads / 32) * kRows;
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
                 const int x0 = of.cum + hkv * cost.head(p, of) + rb * cost.unit(of.per, of.tiles) + cost.empty;  // its first tile's place
                 const int c0 = cut.block(x0);
                 r.rows = own ? p.L.rows_s : p.L.rows_g;
-                const size_t at = (size_t)(of.unit0 + hkv * of.nrb + rb - (own ? h->units_shared : 0) + c0) * r.rows;
+                const size_t at = (size_t)(kGroups ? of.unit0 + hkv * of.nrb + rb - (own ? h->units_shared : 0) + c0 : 2 * c0 + 1) * r.rows;
                 r.o = ws_ptr<float>(p.ws, own ? p.L.slot_s : p.L.slot_g) + at * D;
                 r.ml = ws_ptr<float2>(p.ws, own ? p.L.ml_s : p.L.ml_g) + at;
                 r.count = cut.block(x0 + (of.tiles - 1) * cost.tile(its)) - c0 + 1;
@@ -436,8 +441,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
                 s[x] = make_float2(0, 0);
                 v[x] = make_float4(0, 0, 0, 0);
                 if ((x & 1) < of.count) {
-                    s[x] = __ldcg(of.ml + (x & 1) * of.rows);
-                    v[x] = __ldcg(reinterpret_cast<const float4*>(of.o + (x & 1) * of.rows * D + col));
+                    s[x] = __ldcg(of.ml + of.at<kGroups>(x & 1));
+                    v[x] = __ldcg(reinterpret_cast<const float4*>(of.o + of.at<kGroups>(x & 1) * D + col));
                 }
             }
             AttnJoin j;
@@ -447,8 +452,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
                 if (x & 1) {
 #pragma unroll 2
                     for (int i = 2; i < run[x >> 1].count; ++i)
-                        j.add(__ldcg(run[x >> 1].ml + i * run[x >> 1].rows),
-                              __ldcg(reinterpret_cast<const float4*>(run[x >> 1].o + i * run[x >> 1].rows * D + col)));
+                        j.add(__ldcg(run[x >> 1].ml + run[x >> 1].at<kGroups>(i)),
+                              __ldcg(reinterpret_cast<const float4*>(run[x >> 1].o + run[x >> 1].at<kGroups>(i) * D + col)));
                 }
             }
             j.store<DT, D>(p, (size_t)(it.node0 + n) * p.Hq + hkv * p.gq + (row - n * p.gq), col);
@@ -472,7 +477,7 @@ static cudaError_t launch_combine_t(const AttnParams& p, cudaStream_t st) {
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<DT, D>, p);
+    return cudaLaunchKernelEx(&cfg, p.G > 0 ? attn_combine_kernel<DT, D, true> : attn_combine_kernel<DT, D, false>, p);
 }
 
 cudaError_t launch_attn_combine(const AttnParams& p, int dtype, cudaStream_t st) {
