@@ -28,8 +28,11 @@ int page_shift(int page_size) {
     return -1;
 }
 
+// words of a row of n bits, and blocks of n tokens, are counted in 32 bits with their last one filled up
+constexpr int kMostBits = 0x7fffffff - 4095;
+
 bool nodes_ok(const int32_t* offsets, int S, int T, int R) {
-    if (S <= 0 || T <= 0 || R <= 0) return false;
+    if (S <= 0 || T <= 0 || T > kMostBits || R <= 0) return false;
     return offsets || (long long)S * T == R;
 }
 
@@ -242,7 +245,7 @@ extern "C" int logits_process(const void* logits, void* out, int dtype, int R, i
                               const int32_t* bias_offsets, int n_bias, const uint32_t* allowed,
                               void* ws, size_t ws_bytes, void* stream) {
     if (dtype != SMCSD_F32 && dtype != SMCSD_BF16) return SMCSD_ERR_DTYPE;
-    if (!logits || !out || V <= 0 || !nodes_ok(node_offsets, S, T, R)) return SMCSD_ERR_INVALID_ARG;
+    if (!logits || !out || V <= 0 || V > kMostBits || !nodes_ok(node_offsets, S, T, R)) return SMCSD_ERR_INVALID_ARG;
     if (S > 65535) return SMCSD_ERR_INVALID_ARG;
     if ((hist_tokens == nullptr) != (hist_offsets == nullptr)) return SMCSD_ERR_INVALID_ARG;
     if ((bias_tokens == nullptr) != (bias_values == nullptr) || (bias_tokens == nullptr) != (bias_offsets == nullptr))
