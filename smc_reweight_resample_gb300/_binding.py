@@ -130,6 +130,7 @@ class Workspace:
         if n == 0:
             raise ValueError("invalid workspace request")
         self.buf = torch.zeros(n + 256, dtype=torch.uint8, device=device or "cuda")
+        self.filled_on = torch.cuda.current_stream(self.buf.device)  # until a call on another stream has waited for it
         off = (-self.buf.data_ptr()) % 256
         self.ptr = self.buf.data_ptr() + off
         self.nbytes = n
@@ -158,7 +159,12 @@ def _on(stream, call, given):
     current = torch.cuda.current_stream(stream.device)
     if stream == current:
         return call(**given)
+    ws = given.get("ws")
     with torch.cuda.stream(stream):
+        # a new workspace may not be zero yet (a captured stream cannot wait for what lies outside the capture)
+        if getattr(ws, "filled_on", stream) not in (None, stream) and not torch.cuda.is_current_stream_capturing():
+            stream.wait_stream(ws.filled_on)
+            ws.filled_on = None
         got = call(**given)
     for t in given.values():
         t = getattr(t, "buf", t)  # of a workspace

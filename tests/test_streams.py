@@ -162,3 +162,31 @@ def test_a_captured_call_on_a_side_stream(smcsd):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("name", ["tree_attention", "sd_verify", "smc_step"])
+def test_a_workspace_that_is_not_zero_yet(smcsd, name):
+    # made on the caller's stream behind other work, used on another stream at once
+    call, inputs = operators(smcsd)[name]
+    give = lambda: tuple(t.clone() for t in inputs)  # noqa: E731
+    want = [t.clone() for t in tensors(call(give()))]
+    given, side = give(), torch.cuda.Stream()
+    litter()
+    torch.cuda._sleep(SPIN)
+    if name == "tree_attention":
+        ws = smcsd.TreeAttentionWorkspace(1, 1, 3, 4, 1, 64)
+    elif name == "sd_verify":
+        ws = smcsd.Workspace(smcsd.OP_SD_VERIFY, 6, 2, 4096)
+    else:
+        ws = smcsd.Workspace(smcsd.OP_SMC_STEP, 16, 2, 4096)
+    got = tensors(call(given, stream=side, ws=ws))
+    torch.cuda.synchronize()
+    assert smcsd.check_status(ws, side) == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    again = give()
+    torch.cuda.synchronize()
+    got = tensors(call(again, stream=side, ws=ws))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
