@@ -39,7 +39,7 @@ int elem_bytes(int dtype) { return dtype == SMCSD_F32 ? 4 : 2; }
 
 // Counters that do not stand in the workspace's front.
 cudaError_t clear_counters(const WsLayout& L, void* ws, cudaStream_t st) {
-    return L.clear_bytes ? cudaMemsetAsync(static_cast<char*>(ws) + L.clear, 0, L.clear_bytes, st) : cudaSuccess;
+    return L.fast > kFrontBytes ? cudaMemsetAsync(static_cast<char*>(ws) + kFrontBytes, 0, L.fast - kFrontBytes, st) : cudaSuccess;
 }
 
 }  // namespace

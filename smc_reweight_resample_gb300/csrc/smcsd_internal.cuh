@@ -104,14 +104,14 @@ constexpr size_t kFrontPlanned = kFrontArrive + 4 * kFrontArrivals; // uint32  a
 constexpr size_t kFrontTab = kFrontPlanned + 256;                   // 4 tag words + kTabSize float2 (see setup_exp_table)
 constexpr size_t kFrontBytes = (kFrontTab + 16 + 8 * (size_t)kTabSize + 255) & ~(size_t)255;
 
+// (A part of the kernels' launch parameters, whose size counts: 16 bytes more took 0.9 us of an SD verify's 104.4, four kernels.)
 struct WsLayout {
     size_t flag;       // int32 error flag
-    size_t cnt_seq2;   // uint32 [S]  counters, in the front or (more than kFrontSeqs sequences) from `clear` on
+    size_t cnt_seq2;   // uint32 [S]  counters, in the front or (more than kFrontSeqs sequences) between it and `fast`
     size_t cnt_seq3;
     size_t cnt_group;
     size_t cnt_misc;
     size_t claim;
-    size_t clear, clear_bytes;  // what a call has to clear first
     size_t fast;       // float2 [S * (2K+1) * cpr]
     size_t ddtot;      // float4 [S * 2 * cpr]          chunk totals of sampled rows
     size_t ddsub;      // float4 [S * 2 * cpr * kSubs]  lane-block partials of sampled rows
@@ -137,7 +137,6 @@ inline WsLayout ws_layout(int S, int K, int V) {
     L.claim = kFrontClaim;
     L.tab = kFrontTab;
     size_t o = kFrontBytes;
-    L.clear = o;
     if (s > kFrontSeqs) {
         L.cnt_seq2 = o;
         o = align256(o + 4 * s);
@@ -146,7 +145,6 @@ inline WsLayout ws_layout(int S, int K, int V) {
         L.cnt_group = o;
         o = align256(o + 4 * s);
     }
-    L.clear_bytes = o - L.clear;
     L.fast = o;
     o = align256(o + 8 * s * (2 * k + 1) * cpr);
     L.ddtot = o;
