@@ -40,11 +40,15 @@
  *   - Return value: SMCSD_OK, or a negative status for errors found on the host before anything
  *     is enqueued (bad argument, dtype, workspace size) or at launch (CUDA error). Errors that
  *     depend on device data (non-finite logits, token ids or offsets out of range) are recorded
- *     in `ws` and read with smcsd_check_status(). The kernels never trap and never wait on
- *     another block; the waits inside a block (the copy pipeline of the streaming pass) give
- *     up after about 2 s and record SMCSD_ERR_TIMEOUT. The counters that such a call leaves behind are
- *     cleared by smcsd_check_status; calls that use the buffer before that are unspecified. So a bad input cannot fault or hang the
- *     GPU; outputs are unspecified after such an error.
+ *     in `ws` and read with smcsd_check_status(). The kernels never trap. The waits inside a block
+ *     (the copy pipelines of the streaming pass and of the attention) and those of the steps for
+ *     another block of their cluster give up after a few seconds at most and record
+ *     SMCSD_ERR_TIMEOUT. The counters that such a call leaves behind are cleared by
+ *     smcsd_check_status; calls that use the buffer before that are unspecified. Two waits have no
+ *     limit of their own: the cluster barriers of kv_slot_map (a cluster's blocks run at the same
+ *     time), and those of tree_attention in bf16 for its SM's tensor memory, as long as another
+ *     kernel holds some of it. So a bad input cannot fault or hang the GPU; outputs are unspecified
+ *     after such an error.
  */
 #ifndef SMCSD_H
 #define SMCSD_H
@@ -64,7 +68,7 @@ extern "C" {
 #define SMCSD_ERR_CUDA (-4)        /* a CUDA call or kernel launch failed */
 #define SMCSD_ERR_NONFINITE (-5)   /* device: NaN/+inf logit or weight, or an all-masked row */
 #define SMCSD_ERR_RANGE (-6)       /* device: token id, offset, ancestor or page id out of range */
-#define SMCSD_ERR_TIMEOUT (-7)     /* device: a bounded wait inside a kernel ran out (about 2 s) */
+#define SMCSD_ERR_TIMEOUT (-7)     /* device: a bounded wait inside a kernel ran out (a few seconds) */
 #define SMCSD_ERR_PAGES (-8)       /* device: kv_slot_map found fewer free pages than it needs */
 
 /* logit element types */
@@ -442,11 +446,13 @@ int tree_attention(const void* q, long long q_stride, const void* k_cache, const
  *   z = -inf if bit v of allowed[r] is clear.
  * logits, out [R, V] of dtype; out may be logits itself (nothing but changed values is then written
  * back). Each of these may be NULL to leave its part out: node_tokens int32 [R], mask (with
- * node_tokens: chain), hist_tokens int32 [n_hist] with hist_offsets int32 [S+1], repetition (> 0),
- * presence, frequency float [S] (1, 0, 0), bias_tokens int32 / bias_values float [n_bias] with
- * bias_offsets int32 [S+1], allowed uint32 [R, (V+31)/32]. A token of -1 in hist_tokens, node_tokens
- * or bias_tokens counts for nothing; others outside [0, V) are SMCSD_ERR_RANGE (device side), as are
- * offsets that descend, are negative or pass n_hist or n_bias. S is at most 65535. A row whose mask allows nothing is -inf throughout, which the verify then reports.
+ * node_tokens: chain), hist_tokens int32 [n_hist] with hist_offsets int32 [S+1] (one history for
+ * all three penalties), repetition (> 0), presence, frequency float [S] (1, 0, 0), bias_tokens int32 /
+ * bias_values float [n_bias] with bias_offsets int32 [S+1], allowed uint32 [R, (V+31)/32]. A token
+ * of -1 in hist_tokens, node_tokens or bias_tokens counts for nothing; others outside [0, V) are
+ * SMCSD_ERR_RANGE (device side), as are offsets that descend, are negative or pass n_hist or n_bias.
+ * S is at most 65535. A row whose mask allows nothing is -inf throughout, which the verify then
+ * reports.
  */
 int logits_process(const void* logits, void* out, int dtype, int R, int V, int S, int T,
                    const int32_t* node_offsets, const int32_t* node_tokens, const uint32_t* mask,

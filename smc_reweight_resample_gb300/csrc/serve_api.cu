@@ -46,11 +46,16 @@ bool attn_sizes_ok(int S, int N, int T, int Hq, int Hkv, int D) {
 }
 
 // float32: the FP32 pipes, 64 keys x 16 rows at a time. bf16: the tensor cores, 128 keys x up to 128 rows (narrow) or 256 (wide)
-// at a time. The narrow kernel's time grows with a sequence's rows, the wide one's hardly does; with groups the
-// shared units are large in any case, and the wide kernel is the better one for them. Measured in us, narrow / wide:
+// at a time. The narrow kernel's time grows with a sequence's rows, the wide one's hardly does. With groups the shared units
+// have N times the rows; how much is shared is not known here, and from D / 4 rows on the wide kernel gains more where much is
+// than it loses where nothing is. Measured in us, narrow / wide:
 //   64 sequences over 4096 tokens, D = 128: 32 rows 140 / 152, 64 rows 151 / 159, 96 rows 166 / 171, 112 rows 194 / 176, 128 rows 198 / 178
 //   16 over 4096, D = 64: 64 rows 66.5 / 67.8, 100 rows 104 / 73
-//   8 groups of 16 over 2048, nine tenths shared: D = 128, 20 rows 98 / 102, 36 rows 157 / 132; D = 64, 5 rows 110 / 113, 21 rows 161 / 144
+//   8 groups of 16 over 2048, D = 128, a share of 0, 0.5 and 0.9 of the context alike:
+//     20 rows 141 / 154, 138 / 140, 96 / 100; 36 rows 156 / 163, 159 / 164, 154 / 127; 64 rows 168 / 173, 198 / 203, 223 / 165
+//   16 groups of 4 over 4096, D = 128: 20 rows 145 / 150, 108 / 114, 86 / 82; 36 rows 154 / 155, 138 / 137, 159 / 108
+//   8 groups of 16 over 2048, D = 64: 8 rows 185 / 201, 182 / 157, 109 / 113; 17 rows 199 / 211, 206 / 199, 148 / 138;
+//     32 rows 206 / 214, 239 / 229, 182 / 166
 enum AttnKind { kSimt, kNarrow, kWide };
 constexpr int kSimtBlocksPerSm = 2;
 // Places on the line (attn_plan.cuh): {rows from which a tile is heavy, of a light tile, of a heavy one, before a unit's tiles}.

@@ -22,7 +22,7 @@
 // (76 % of a copy's rate; 142 us with 8 nodes, where the wait for the four groups' barriers is shorter). 8 groups of
 // 16 particles with 5 nodes over 2048 tokens, 90 % of them shared: 97 us with the planning and the joining kernel (8 and
 // about 10): 1024 units of two tiles each, bound by the warps that fetch and issue, a few thousand clocks for each unit; the
-// kernel's code (80 KB) does not stay in an SM's instruction cache, and what made it shorter, or took steps out of
+// kernel's code (83 KB; 95 KB without a plan) does not stay in an SM's instruction cache, and what made it shorter, or took steps out of
 // those warps' loops, made these units faster. 16 sequences with 5 nodes over 2048 tokens, 16 heads of 64: 34 us; one token
 // over 517: 11.4 us, nearly all of it the first pass through the code and the chain of waits of one tile.
 //
