@@ -66,8 +66,8 @@ __device__ __forceinline__ int warp_prefix(int v, int* s, int& total) {
 // One cluster. Its warps share out the sequences and the pages, both in order: a warp takes a run of
 // sequences (their demand) and a run of pages (how many are free). The counts meet in the cluster's
 // shared memories; then every free page knows its place in the list of free pages and every sequence
-// the place where its pages begin, so the k-th page needed gets the k-th free page whatever runs first. Latency bounds it: 7.0 us
-// for 16 sequences of one token (one block: its launch and three dependent loads on either side of a barrier), 10.7 us for 256 of
+// the place where its pages begin, so the k-th page needed gets the k-th free page whatever runs first. Latency bounds it: 7.2 us
+// for 16 sequences of one token (one block: its launch and three dependent loads on either side of a barrier), 10.8 us for 256 of
 // nine after a resampling (eight blocks: two barriers of the cluster, and a sequence and some runs of pages for each warp in turn),
 // whose bytes would take 0.2 us.
 __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_constant__ SlotParams p) {
