@@ -20,10 +20,6 @@ LEVELS = {2: 7.0, 4: 14.0}
 FACTORS = (1.0, 0.5, 0.0, -0.7)
 
 
-def sms():
-    return torch.cuda.get_device_properties(0).multi_processor_count
-
-
 class Long:
     def __init__(self, seed, ctx, counts, T, Hq, Hkv, D, dtype, N=1, shared=0, tree=False, scale=None, moving=True):
         rng, gen = np.random.default_rng(seed), torch.Generator("cuda").manual_seed(seed)

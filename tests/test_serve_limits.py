@@ -2,7 +2,7 @@
 refused before anything runs. A GPU is not needed."""
 import pytest
 
-from test_serve_args import F, FAKE, I, LL, P, SZ, caller, lib  # noqa: F401
+from test_serve_args import FAKE, I, P, SZ, caller, lib  # noqa: F401
 
 END = 0x7fffffff
 
