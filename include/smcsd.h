@@ -91,6 +91,11 @@ extern "C" {
 #define SMCSD_OP_KV_APPEND 8      /* any S > 0; K and V are ignored */
 #define SMCSD_OP_TREE_MASK 9      /* any S > 0; K and V are ignored */
 #define SMCSD_OP_LOGITS_PROCESS 10 /* any S > 0; K and V are ignored */
+#define SMCSD_OP_BEAM_SELECT 11    /* S = rows of logits (G*N), V; K is ignored */
+#define SMCSD_OP_STATE_REORDER 12  /* any S > 0; K and V are ignored */
+#define SMCSD_OP_KV_FORK 13        /* kv_fork, kv_free and kv_copy_pages: any S > 0; K and V are ignored */
+#define SMCSD_OP_KV_COMPACT 14     /* any S > 0, V = number of pages; K is ignored (serves kv_fork's calls too) */
+#define SMCSD_OP_DISTILL_LOSS 15   /* any S > 0; K and V are ignored */
 
 /*
  * Scratch bytes that `op` needs for S sequences (or particles; for the resampling ops S is the
@@ -460,6 +465,127 @@ int logits_process(const void* logits, void* out, int dtype, int R, int V, int S
                    const float* repetition, const float* presence, const float* frequency,
                    const int32_t* bias_tokens, const float* bias_values, const int32_t* bias_offsets,
                    int n_bias, const uint32_t* allowed, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Beam search, the pages' housekeeping, and what a draft learns from. None of the pages has these steps; they
+ * stand beside the ones above: a beam search (or the growing of a draft tree) over the same logits, with
+ * its sequences' pages and states following their ancestors as after a resampling; requests that come, fork and
+ * end in the same cache; and the loss that draws the draft's distribution to the target's, on which the
+ * acceptance rate rests.
+ *
+ * Shared conventions
+ *   - G groups of N sequences (beams); sequence i of group g is row g*N+i. Ancestors are group-local, as
+ *     smc_ess_resample's, and go to kv_pagetable_remap (with resampled == NULL) as they are.
+ *   - Tables int32 [S, pages_per_seq] and refcounts int32 [num_pages] as above; -1 = no page. Tables and refcounts are
+ *     written anew: outputs must not overlap inputs.
+ * ------------------------------------------------------------------------------------------- */
+
+/*
+ * The M best continuations of each group's beams. With L_i = log sum_v exp(z_iv / T) of row i of `logits`,
+ * candidate (i, v) has the score scores[i] + z_iv / T - L_i. A beam with finished[i] != 0 has one
+ * candidate in place of V: the token pad_token, with the score scores[i] as it is; its logits are not
+ * read. A beam with a score of -inf has none, and its logits are not read. For m = 0 .. M-1, the m-th
+ * best candidate of group g in the order of score (falling), beam, token:
+ *   tokens[g*M+m] = v;  ancestors[g*M+m] = i (group-local);  out_scores[g*M+m] = its score;
+ *   out_finished[g*M+m] = 1 if the beam was finished or v == eos_token, else 0.
+ * Where there are fewer than M candidates (masked tokens of -inf are none), the remaining places get pad_token, 0,
+ * -inf and 1. A row with nothing but -inf has no candidate; that is not an error here.
+ * The order is that of the scores' real values, up to 1e-11 or so: candidates of one beam are ordered by their logits
+ * exactly, those of two beams by sums that are computed again in double-floats where hardware exponentials
+ * could not tell them apart (a slower path: some 10 us for each row of 128256).
+ * N = 1 and scores == NULL gives the M largest log-probabilities of each row: a teacher's top logits, or the children
+ * of a draft tree's node.
+ * logits [G*N rows, row_stride elements apart, V used], aligned to their type; scores float [G*N] (NULL: 0);
+ * finished int32 [G*N] (NULL: none); eos_token < 0: none; tokens, ancestors int32, out_scores float,
+ * out_finished int32 (NULL to skip) [G*M]; out_scores and out_finished must not be scores and finished. N and
+ * M are at most 256. ws: smcsd_workspace_size(SMCSD_OP_BEAM_SELECT, G*N, 0, V).
+ * Device-side errors: SMCSD_ERR_NONFINITE (NaN or +inf in logits that are read, or in scores; such a beam has no candidate).
+ */
+int beam_select(const void* logits, long long row_stride, int dtype, int G, int N, int V, int M,
+                float temperature, const float* scores, const int32_t* finished, int pad_token,
+                int eos_token, int32_t* tokens, int32_t* ancestors, float* out_scores,
+                int32_t* out_finished, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Rows of per-sequence states by ancestors: for each of `count` tensors, row g*M+m of dst = row
+ * g*N + ancestors[g*M+m] of src (M = N after a resampling or a step of beam search; N = 1: copies for M beams).
+ * src, dst and row_bytes are HOST arrays of `count` (at most 64) device pointers and sizes; a source of G*N and a
+ * destination of G*M rows of row_bytes each, contiguous, of any type, which must not overlap. An ancestor
+ * outside [0, N) is SMCSD_ERR_RANGE (device side) and leaves its rows as they are.
+ */
+int state_reorder(const void* const* src, void* const* dst, const long long* row_bytes, int count,
+                  const int32_t* ancestors, int G, int N, int M, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Forks: every sequence s becomes a copy of sequence parents[s] as table_in holds it, of its first
+ * ceil(lengths[s] / page_size) pages (lengths == NULL, or a length of INT32_MAX: all of them; pages past the
+ * end of the table: none); parents[s] == s keeps it (cut to its length), -1 frees it. Pages are shared, not copied:
+ *   refcount_out[id] = refcount_in[id] + (entries of table_out == id) - (entries of table_in == id),
+ * so holders other than the table (a prefix cache) keep their share. A partly filled last page is shared too:
+ * kv_slot_map copies it when one of its holders writes. parents, lengths int32 [S].
+ * Device-side errors: SMCSD_ERR_RANGE for a parent outside [-1, S) or a negative length (the sequence is kept as it is), for page
+ * ids outside [-1, num_pages) (copied, not counted), and for a page that is let go though nothing counted it.
+ */
+int kv_fork(const int32_t* parents, const int32_t* lengths, int S, const int32_t* table_in,
+            int32_t* table_out, int pages_per_seq, int page_size, const int32_t* refcount_in,
+            int32_t* refcount_out, int num_pages, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Lets go of every sequence's pages past its length: kv_fork with every sequence its own parent (0: all of
+ * them, as for a sequence that has ended; the accepted length: those of rejected drafts).
+ */
+int kv_free(const int32_t* lengths, int S, const int32_t* table_in, int32_t* table_out,
+            int pages_per_seq, int page_size, const int32_t* refcount_in, int32_t* refcount_out,
+            int num_pages, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Moves the pages in use (refcount_in > 0) to the front of the cache with as few moves as there can be: with U pages in
+ * use, the k-th (ascending) page in use from page U on takes the k-th free page below U.
+ *   src[k], dst[k], k < counts[0]: the moves, for kv_copy_pages (-1 behind them); counts[1] = U;
+ *   table_out, refcount_out: table_in and refcount_in with the pages' new ids; pages from U on are free.
+ * src, dst int32 [num_pages / 2] (NULL for one page), counts int32 [2]. Nothing but counts and tables is touched: the caller
+ * copies the pages of every layer. ws: smcsd_workspace_size(SMCSD_OP_KV_COMPACT, 1, 0, num_pages).
+ * Device-side errors: SMCSD_ERR_RANGE (a negative refcount, taken as free; table entries outside [-1, num_pages) or of free pages,
+ * left as they are).
+ */
+int kv_compact(int S, const int32_t* table_in, int32_t* table_out, int pages_per_seq,
+               const int32_t* refcount_in, int32_t* refcount_out, int num_pages, int32_t* src,
+               int32_t* dst, int32_t* counts, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Copies whole pages within each of n_caches caches: page src[i] to page dst[i] for i < n, or i < *count (int32, device,
+ * NULL: n). caches: HOST array of at most 256 device pointers (every layer's keys and values), 16-byte aligned, each
+ * num_pages pages of page_bytes (a multiple of 16). An entry with src and dst both negative is passed over. Destinations must be distinct,
+ * and none of them a source of the same call. Pages out of range are SMCSD_ERR_RANGE (device side) and copy
+ * nothing, as does a count outside [0, n].
+ */
+int kv_copy_pages(void* const* caches, int n_caches, long long page_bytes, int num_pages,
+                  const int32_t* src, const int32_t* dst, int n, const int32_t* count, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top logits: for each of R rows, q = softmax(z / T) of the draft's logits, and the
+ * teacher's probabilities p_k of the row's listed tokens top_tokens[r*K+k] (-1: none), from top_values:
+ *   rest == 0: p = softmax of the row's values (log-probabilities or logits): the list stands for everything, p_r = 0;
+ *   rest == 1: p_k = exp(value), log-probabilities over the whole vocabulary; p_r = max(0, 1 - sum_k p_k) is
+ *              the share of all tokens that are not listed, as one event of probability q_r = 1 - sum of the listed q.
+ *   loss[r] = sum_k p_k (log p_k - log q_k) + p_r (log p_r - log q_r)             (terms with p = 0 are 0)
+ *   dlogits[r, v] = weight[r] * dloss[r] / dz_v
+ *                 = weight[r] / T * (P q_v - p_v) for a listed v, weight[r] / T * q_v (P - p_r / q_r) for others,
+ * P = sum_k p_k + p_r. weight is the gradient that comes to loss[r] (NULL: 1); it does not scale the loss. A token that is listed
+ * several times has the sum of its entries' p in the gradient. A row whose list is empty, or holds nothing but values of -inf, has
+ * a loss and a gradient of 0, whatever its logits are (padding). q_v = 0 for a masked token; a loss is +inf where p > 0 meets q = 0.
+ * Either output may be NULL, loss for the backward pass alone and dlogits for the forward one; both together read the logits once,
+ * as each alone does. logits, dlogits: rows row_stride and dlogits_stride elements apart, V used, of dtype, aligned to
+ * it; dlogits may be logits (with one stride), else they must not overlap. top_tokens int32, top_values float [R, K], K at most 256;
+ * weight, loss float [R]. V times the element size is at most 1638368 bytes. Sums are float32, the gradient is rounded once.
+ * Device-side errors: SMCSD_ERR_NONFINITE (NaN or +inf in logits or values, a row of -inf), SMCSD_ERR_RANGE (a token outside
+ * [-1, V), taken as none).
+ */
+int distill_loss(const void* logits, long long row_stride, int dtype, int R, int V,
+                 const int32_t* top_tokens, const float* top_values, int K, float temperature,
+                 int rest, const float* weight, float* loss, void* dlogits, long long dlogits_stride,
+                 void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -12,6 +12,8 @@ _API = {
     "OP_PAGETABLE_REMAP", "OP_PACER_BLOCK_STOP", "LIB_PATH",
     "kv_slot_map", "kv_append", "tree_mask", "tree_attention", "logits_process",
     "TreeAttentionWorkspace", "OP_KV_SLOT_MAP", "OP_KV_APPEND", "OP_TREE_MASK", "OP_LOGITS_PROCESS",
+    "beam_select", "state_reorder", "kv_fork", "kv_free", "kv_compact", "kv_copy_pages", "distill_loss",
+    "OP_BEAM_SELECT", "OP_STATE_REORDER", "OP_KV_FORK", "OP_KV_COMPACT", "OP_DISTILL_LOSS",
 }
 
 __all__ = sorted(_API)

@@ -21,7 +21,8 @@ ERR_PAGES = -8
 F32, BF16 = 0, 1
 TARGET_TOKEN, TARGET_SEQUENCE = 0, 1
 (OP_SD_VERIFY, OP_SMC_REWEIGHT, OP_SMC_STEP, OP_ESS_RESAMPLE, OP_PAGETABLE_REMAP, OP_PACER_BLOCK_STOP,
- OP_DRAFT_SAMPLE, OP_KV_SLOT_MAP, OP_KV_APPEND, OP_TREE_MASK, OP_LOGITS_PROCESS) = range(11)
+ OP_DRAFT_SAMPLE, OP_KV_SLOT_MAP, OP_KV_APPEND, OP_TREE_MASK, OP_LOGITS_PROCESS, OP_BEAM_SELECT, OP_STATE_REORDER,
+ OP_KV_FORK, OP_KV_COMPACT, OP_DISTILL_LOSS) = range(16)
 
 _lib = None
 
@@ -73,12 +74,21 @@ def load(path: str = LIB_PATH):
     lib.tree_attention_workspace_size.restype = sz
     lib.tree_attention.argtypes = [P, ll, P, P, i, i, i, P, i, P, P, i, i, i, i, P, i, i, i, f, P, P,
                                    P, sz, P]
+    pp, llp = ctypes.POINTER(P), ctypes.POINTER(ll)
+    lib.beam_select.argtypes = [P, ll, i, i, i, i, i, f, P, P, i, i, P, P, P, P, P, sz, P]
+    lib.state_reorder.argtypes = [pp, pp, llp, i, P, i, i, i, P, sz, P]
+    lib.kv_fork.argtypes = [P, P, i, P, P, i, i, P, P, i, P, sz, P]
+    lib.kv_free.argtypes = [P, i, P, P, i, i, P, P, i, P, sz, P]
+    lib.kv_compact.argtypes = [i, P, P, i, P, P, i, P, P, P, P, sz, P]
+    lib.kv_copy_pages.argtypes = [pp, i, ll, i, P, P, i, P, P, sz, P]
+    lib.distill_loss.argtypes = [P, ll, i, i, i, P, P, i, f, i, P, P, P, ll, P, sz, P]
     lib.logits_process.argtypes = [P, P, i, i, i, i, i, P, P, P, P, P, i, P, P, P, P, P, P, i, P, P, sz, P]
     for fn in ("smcsd_workspace_init", "smcsd_check_status", "sd_verify", "smc_reweight",
                "smc_ess_resample", "kv_pagetable_remap", "pacer_block_stop", "smc_step",
                "smc_step_static", "smc_step_logq", "smc_reweight_tilted", "smc_step_tilted",
                "pacer_block_stop_pos", "draft_sample", "smcsd_selftest_wait", "kv_slot_map",
-               "kv_append", "tree_mask", "tree_attention", "logits_process"):
+               "kv_append", "tree_mask", "tree_attention", "logits_process", "beam_select",
+               "state_reorder", "kv_fork", "kv_free", "kv_compact", "kv_copy_pages", "distill_loss"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -166,14 +176,22 @@ def _on(stream, call, given):
             stream.wait_stream(ws.filled_on)
             ws.filled_on = None
         got = call(**given)
-    for t in given.values():
-        t = getattr(t, "buf", t)  # of a workspace
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            t.record_stream(stream)
-    for t in got.values() if isinstance(got, dict) else got if isinstance(got, tuple) else (got,):
-        if t is not None:
-            t.record_stream(current)
+    for t in _tensors(given.values()):
+        t.record_stream(stream)
+    for t in _tensors(got.values() if isinstance(got, dict) else got if isinstance(got, tuple) else (got,)):
+        t.record_stream(current)
     return got
+
+
+def _tensors(values):
+    """The CUDA tensors among arguments or results: themselves, a workspace's buffer, those of a list or tuple."""
+    for t in values:
+        if isinstance(t, (list, tuple)):
+            yield from _tensors(t)
+            continue
+        t = getattr(t, "buf", t)
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            yield t
 
 
 def _out(t, shape, dtype, device):
@@ -504,7 +522,8 @@ def _native():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
-                      ("kv_slot_map", "kv_append", "tree_mask", "tree_attention", "logits_process")), _check)
+                      ("kv_slot_map", "kv_append", "tree_mask", "tree_attention", "logits_process", "beam_select",
+                       "state_reorder", "kv_fork", "kv_free", "kv_compact", "kv_copy_pages", "distill_loss")), _check)
         _calls = module
     return _calls
 
@@ -569,3 +588,79 @@ def logits_process(logits, S, T, V, node_offsets=None, node_tokens=None, mask=No
     return (_calls or _native()).logits_process(logits, S, T, V, node_offsets, node_tokens, mask, hist_tokens,
                                                 hist_offsets, repetition, presence, frequency, bias_tokens,
                                                 bias_values, bias_offsets, allowed, out, ws.ptr, ws.nbytes)
+
+
+# ----------------------------------------------------------------------------------------------
+# beam search, the pages' housekeeping, distillation
+# ----------------------------------------------------------------------------------------------
+
+def beam_select(logits, G, N, V, M, temperature=1.0, scores=None, finished=None, pad_token=0, eos_token=-1, ws=None, tokens=None,
+                ancestors=None, out_scores=None, out_finished=None, stream=None):
+    """The M best continuations of each of G groups of N beams: logits [G*N, >= V] (rows may be strided), scores float [G*N] of the
+    beams so far, finished int32 [G*N] (such a beam stays as it is, with pad_token). Returns dict(tokens, ancestors (group-local),
+    scores, finished), each [G*M], in falling order of score. N=1 without scores: the M largest log-probabilities of each row."""
+    if stream is not None:
+        return _on(stream, beam_select, locals())
+    ws = ws or Workspace(OP_BEAM_SELECT, G * N, 0, V, logits.device)
+    o = (_calls or _native()).beam_select(logits, G, N, V, M, temperature, scores, finished, pad_token, eos_token, tokens, ancestors,
+                                          out_scores, out_finished, ws.ptr, ws.nbytes)
+    return {"tokens": o[0], "ancestors": o[1], "scores": o[2], "finished": o[3]}
+
+
+def state_reorder(states, ancestors, G, N, M=None, out=None, ws=None, stream=None):
+    """Rows of each of the tensors `states` [G*N, ...] by ancestors (int32 [G*M], group-local; M=None: N). Returns the list of
+    tensors [G*M, ...] (`out`, if given; not the states themselves)."""
+    if stream is not None:
+        return _on(stream, state_reorder, locals())
+    ws = ws or Workspace(OP_STATE_REORDER, 1, device=ancestors.device)
+    return (_calls or _native()).state_reorder(states, ancestors, G, N, N if M is None else M, out, ws.ptr, ws.nbytes)
+
+
+def kv_fork(table_in, refcount_in, parents, page_size, lengths=None, table_out=None, refcount_out=None, ws=None, stream=None):
+    """Every sequence becomes a copy of its parent's first ceil(length / page_size) pages (parents int32 [S]: itself to stay, -1 for
+    none; lengths int32 [S], None: all pages), shared by reference counts. Returns (table_out, refcount_out)."""
+    if stream is not None:
+        return _on(stream, kv_fork, locals())
+    ws = ws or Workspace(OP_KV_FORK, 1, device=table_in.device)
+    return (_calls or _native()).kv_fork(table_in, refcount_in, parents, page_size, lengths, table_out, refcount_out, ws.ptr, ws.nbytes)
+
+
+def kv_free(table_in, refcount_in, lengths, page_size, table_out=None, refcount_out=None, ws=None, stream=None):
+    """Lets go of every sequence's pages past its length (int32 [S]; 0: all of them). Returns (table_out, refcount_out)."""
+    if stream is not None:
+        return _on(stream, kv_free, locals())
+    ws = ws or Workspace(OP_KV_FORK, 1, device=table_in.device)
+    return (_calls or _native()).kv_free(table_in, refcount_in, lengths, page_size, table_out, refcount_out, ws.ptr, ws.nbytes)
+
+
+def kv_compact(table_in, refcount_in, table_out=None, refcount_out=None, src=None, dst=None, counts=None, ws=None, stream=None):
+    """New ids for the pages in use, so that they fill the front of the cache: dict(table_out, refcount_out, src, dst (int32
+    [num_pages // 2], -1 behind the moves), counts (int32 [2]: moves, pages in use)); kv_copy_pages then moves the pages."""
+    if stream is not None:
+        return _on(stream, kv_compact, locals())
+    ws = ws or Workspace(OP_KV_COMPACT, 1, 0, refcount_in.numel(), table_in.device)
+    o = (_calls or _native()).kv_compact(table_in, refcount_in, table_out, refcount_out, src, dst, counts, ws.ptr, ws.nbytes)
+    return {"table_out": o[0], "refcount_out": o[1], "src": o[2], "dst": o[3], "counts": o[4]}
+
+
+def kv_copy_pages(caches, src, dst, count=None, ws=None, stream=None):
+    """Copies page src[i] to page dst[i] (int32) in each of the tensors `caches` [num_pages, ...], for all i or the first count[0]
+    (int32). Returns the caches, which are changed in place."""
+    if stream is not None:
+        return _on(stream, kv_copy_pages, locals())
+    ws = ws or Workspace(OP_KV_FORK, 1, device=src.device)
+    (_calls or _native()).kv_copy_pages(caches, src, dst, count, ws.ptr, ws.nbytes)
+    return caches
+
+
+def distill_loss(logits, top_tokens, top_values, V, temperature=1.0, rest=False, weight=None, loss=None, dlogits=None, grad=True,
+                 with_loss=True, ws=None, stream=None):
+    """Loss of the draft's logits [R, >= V] (rows may be strided) against a teacher's top tokens (int32 [R, K], -1: none) with their
+    values (float [R, K]), and the gradient weight[r] * dloss[r]/dlogits (pass dlogits=logits for it to take their place). rest: the
+    values are log-probabilities over the whole vocabulary, and what they leave goes to all other tokens. Returns (loss float [R] or
+    None, dlogits [R, V] or None)."""
+    if stream is not None:
+        return _on(stream, distill_loss, locals())
+    ws = ws or Workspace(OP_DISTILL_LOSS, 1, device=logits.device)
+    return (_calls or _native()).distill_loss(logits, top_tokens, top_values, V, temperature, bool(rest), weight, loss, dlogits, bool(grad),
+                                              bool(with_loss), ws.ptr, ws.nbytes)

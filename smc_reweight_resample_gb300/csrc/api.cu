@@ -3,6 +3,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "ops_launch.cuh"
 #include "serve_launch.cuh"
 #include "smcsd.h"
 #include "smcsd_launch.cuh"
@@ -65,7 +66,16 @@ extern "C" size_t smcsd_workspace_size(int op, int S, int K, int V) {
         case SMCSD_OP_KV_APPEND:
         case SMCSD_OP_TREE_MASK:
         case SMCSD_OP_LOGITS_PROCESS:
+        case SMCSD_OP_STATE_REORDER:
+        case SMCSD_OP_KV_FORK:
+        case SMCSD_OP_DISTILL_LOSS:
             return 256;  // the error flag
+        case SMCSD_OP_BEAM_SELECT:
+            if (V <= 0 || V > 0x7fffffff - 65535) return 0;
+            return beam_layout(S, V).total;
+        case SMCSD_OP_KV_COMPACT:
+            if (V <= 0) return 0;
+            return compact_bytes(V);
         default:
             return 0;
     }

@@ -1,0 +1,329 @@
+// kv_pages.cu -- sequences' states and pages: rows of states by ancestors, tables forked and freed, pages in use moved to the
+// front of the cache, pages copied.
+#include <cooperative_groups.h>
+
+#include "ops_launch.cuh"
+#include "smcsd_launch.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace smcsd {
+
+// ------------------------------------------------------------------------------------------
+// state_reorder
+// ------------------------------------------------------------------------------------------
+
+constexpr int kReorderThreads = 256;
+constexpr int kReorderUnits = 4;  // units of a thread and turn
+constexpr long long kReorderTurn = kReorderThreads * kReorderUnits;
+
+template <typename U>
+__device__ __forceinline__ void reorder_units(const ReorderParams& p, int t, int block, int blocks) {
+    const U* src = static_cast<const U*>(p.src[t]);
+    U* dst = static_cast<U*>(p.dst[t]);
+    const long long w = p.row_units[t], n = w * p.G * p.M;
+    for (long long i0 = block * kReorderTurn + threadIdx.x; i0 < n; i0 += blocks * kReorderTurn) {
+        U x[kReorderUnits];
+        bool there[kReorderUnits];
+#pragma unroll
+        for (int k = 0; k < kReorderUnits; ++k) {
+            const long long i = i0 + k * kReorderThreads;
+            there[k] = i < n;
+            if (there[k]) {
+                const int row = (int)(i / w), g = row / p.M, a = __ldg(p.ancestors + row);
+                there[k] = a >= 0 && a < p.N;
+                if (there[k])
+                    x[k] = src[((long long)g * p.N + a) * w + (i - row * w)];
+                else
+                    raise_error(p.ws, kErrRange);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kReorderUnits; ++k)
+            if (there[k]) dst[i0 + k * kReorderThreads] = x[k];
+    }
+}
+
+// All tensors in one launch: each has a run of blocks.
+__global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_constant__ ReorderParams p) {
+    int t = 0;
+    while (blockIdx.x >= p.first[t + 1]) ++t;
+    const int block = (int)(blockIdx.x - p.first[t]), blocks = (int)(p.first[t + 1] - p.first[t]);
+    if (p.unit[t] == 4)
+        reorder_units<uint4>(p, t, block, blocks);
+    else if (p.unit[t] == 2)
+        reorder_units<uint32_t>(p, t, block, blocks);
+    else
+        reorder_units<unsigned char>(p, t, block, blocks);
+}
+
+cudaError_t launch_reorder(const ReorderParams& p0, cudaStream_t st) {
+    ReorderParams p = p0;
+    const long long cap = 16ll * device_sm_count();  // two waves of eight blocks an SM
+    for (int t = 0; t < p.count; ++t) {
+        const long long n = p.row_units[t] * p.G * p.M;
+        long long blocks = (n + kReorderTurn - 1) / kReorderTurn;
+        if (blocks > cap) blocks = cap;
+        p.first[t + 1] = p.first[t] + (unsigned)blocks;
+    }
+    reorder_kernel<<<p.first[p.count], kReorderThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------------------
+// kv_fork, kv_free
+// ------------------------------------------------------------------------------------------
+
+constexpr int kForkThreads = 256;
+
+__global__ void __launch_bounds__(kForkThreads) fork_counts_kernel(const __grid_constant__ ForkParams p) {
+    griddep_launch_dependents();
+    for (long long i = (long long)blockIdx.x * kForkThreads + threadIdx.x; i < p.num_pages; i += (long long)gridDim.x * kForkThreads)
+        p.ref_out[i] = __ldg(p.ref_in + i);
+}
+
+// A page id of a table: whether it is counted. -1 is no page.
+__device__ __forceinline__ bool fork_counts(const ForkParams& p, int id) {
+    if (id >= 0 && id < p.num_pages) return true;
+    if (id != -1) raise_error(p.ws, kErrRange);
+    return false;
+}
+
+// One thread an entry of the new table. Counts change where an entry does: what a sequence keeps costs no atomic.
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constant__ ForkParams p) {
+    const int P = p.pages_per_seq;
+    const long long n = (long long)p.S * P;
+    bool waited = false;
+    for (long long i = (long long)blockIdx.x * kForkThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kForkThreads) {
+        const int s = (int)(i / P), j = (int)(i - (long long)s * P);
+        int parent = p.parents ? __ldg(p.parents + s) : s;
+        const int length = p.lengths ? __ldg(p.lengths + s) : INT_MAX;
+        bool all = length == INT_MAX;
+        if (parent < -1 || parent >= p.S || length < 0) {
+            raise_error(p.ws, kErrRange);
+            parent = s;
+            all = true;
+        }
+        const int old = __ldg(p.table_in + i);
+        int id = -1;
+        if (parent >= 0 && (all || j < (int)(((long long)length + (1 << p.page_shift) - 1) >> p.page_shift)))
+            id = parent == s ? old : __ldg(p.table_in + (long long)parent * P + j);
+        p.table_out[i] = id;
+        if (id == old) {
+            fork_counts(p, id);
+            continue;
+        }
+        if (!waited) {
+            griddep_wait();  // the counts have been copied
+            waited = true;
+        }
+        if (fork_counts(p, id)) atomicAdd(p.ref_out + id, 1);
+        if (fork_counts(p, old) && atomicSub(p.ref_out + old, 1) <= 0) raise_error(p.ws, kErrRange);  // held, but not counted
+    }
+    if (!waited) griddep_wait();
+}
+
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t st) {
+    const long long cap = 16ll * device_sm_count();
+    long long b = ((long long)p.num_pages + kForkThreads - 1) / kForkThreads;
+    fork_counts_kernel<<<(unsigned)(b < cap ? b : cap), kForkThreads, 0, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    b = ((long long)p.S * p.pages_per_seq + kForkThreads - 1) / kForkThreads;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(b < cap ? b : cap));
+    cfg.blockDim = dim3(kForkThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fork_kernel, p);
+}
+
+// ------------------------------------------------------------------------------------------
+// kv_compact
+// ------------------------------------------------------------------------------------------
+
+constexpr int kCompactThreads = 1024;
+constexpr int kCompactWarps = kCompactThreads / 32;
+
+// Which page goes where: one cluster. Its warps share out the pages in order, in runs of 32 that a ballot counts. The number
+// of pages in use, U, is the border: a hole's place is the number of free pages before it, that of a page from behind the
+// number of pages in use between the border and it, so that the k-th page from behind meets the k-th hole whatever runs first.
+__global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(const __grid_constant__ CompactParams p) {
+    __shared__ int s_warp[kCompactWarps];
+    __shared__ int s_tot, s_before;
+    cg::cluster_group cl = cg::this_cluster();
+    const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int gw = rank * kCompactWarps + warp, nw = C * kCompactWarps;
+    int32_t* place = ws_ptr<int32_t>(p.ws, p.place);
+    griddep_launch_dependents();
+    const int runs = (p.num_pages + 31) / 32, per = (runs + nw - 1) / nw;
+    const int r0 = min(runs, gw * per), r1 = min(runs, r0 + per);
+    int have = 0;
+    for (int r = r0; r < r1; ++r) {
+        const int id = r * 32 + lane;
+        have += __popc(__ballot_sync(0xffffffffu, id < p.num_pages && __ldg(p.ref_in + id) > 0));
+    }
+    if (lane == 0) s_warp[warp] = have;
+    if (threadIdx.x == 0) s_before = -1;
+    __syncthreads();
+    int x = s_warp[lane], in = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, in, o);
+        if (lane >= o) in += t;
+    }
+    int before = __shfl_sync(0xffffffffu, in - x, warp);
+    if (threadIdx.x == 31) s_tot = in;
+    cl.sync();
+    int used = 0;
+    for (int c = 0; c < C; ++c) {
+        const int t = *cl.map_shared_rank(&s_tot, c);
+        if (c < rank) before += t;
+        used += t;
+    }
+    // pages in use before the border, by the warp that the border is in (none's if every page is in use)
+    if (used < p.num_pages && used >= r0 * 32 && used < r1 * 32) {
+        int n = before;
+        for (int r = r0; r <= used / 32; ++r) {
+            const int id = r * 32 + lane;
+            n += __popc(__ballot_sync(0xffffffffu, id < used && __ldg(p.ref_in + id) > 0));
+        }
+        if (lane == 0) s_before = n;
+    }
+    cl.sync();
+    int low = used;
+    for (int c = 0; c < C; ++c) {
+        const int t = *cl.map_shared_rank(&s_before, c);
+        if (t >= 0) low = t;
+    }
+    if (gw == 0 && lane == 0) {
+        p.counts[0] = used - low;
+        p.counts[1] = used;
+    }
+    const int moves = used - low, half = p.num_pages / 2;
+    for (int i = moves + rank * kCompactThreads + threadIdx.x; i < half; i += C * kCompactThreads) p.src[i] = p.dst[i] = -1;
+    for (int r = r0; r < r1; ++r) {
+        const int id = r * 32 + lane;
+        const int ref = id < p.num_pages ? __ldg(p.ref_in + id) : 0;
+        const unsigned b = __ballot_sync(0xffffffffu, ref > 0);
+        const int held = before + __popc(b & ((1u << lane) - 1u));  // pages in use before this one
+        before += __popc(b);
+        if (id >= p.num_pages) continue;
+        if (ref < 0) raise_error(p.ws, kErrRange);
+        if (id < used) {
+            if (ref > 0)
+                p.ref_out[id] = ref;
+            else
+                p.dst[id - held] = id;  // its count comes with its page
+        } else {
+            p.ref_out[id] = 0;
+            if (ref > 0) {
+                p.src[held - low] = id;
+                place[id] = held - low;
+            }
+        }
+    }
+    cl.sync();  // no block's shared memory is read any more
+}
+
+constexpr int kApplyThreads = 256;
+
+// Table entries and counts of the pages that move.
+__global__ void __launch_bounds__(kApplyThreads) compact_apply_kernel(const __grid_constant__ CompactParams p) {
+    const int32_t* place = ws_ptr<const int32_t>(p.ws, p.place);
+    const long long first = (long long)blockIdx.x * kApplyThreads + threadIdx.x, step = (long long)gridDim.x * kApplyThreads;
+    griddep_wait();
+    const int moves = __ldcg(p.counts), used = __ldcg(p.counts + 1);
+    for (long long i = first; i < moves; i += step) p.ref_out[__ldcg(p.dst + i)] = __ldg(p.ref_in + __ldcg(p.src + i));
+    for (long long i = first; i < p.entries; i += step) {
+        int id = __ldg(p.table_in + i);
+        if (id != -1) {
+            if (id < 0 || id >= p.num_pages || __ldg(p.ref_in + id) <= 0)
+                raise_error(p.ws, kErrRange);  // left as it is
+            else if (id >= used)
+                id = __ldcg(p.dst + __ldcg(place + id));
+        }
+        p.table_out[i] = id;
+    }
+}
+
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t st) {
+    // as many blocks as leave every warp about 128 pages, at most a portable cluster of 8
+    int C = 1;
+    while (C < 8 && p.num_pages > C * kCompactWarps * 128) C *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kCompactThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = C;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, compact_plan_kernel, p);
+    if (e != cudaSuccess) return e;
+    const long long cap = 16ll * device_sm_count(), most = p.entries > p.num_pages / 2 ? p.entries : p.num_pages / 2;
+    long long b = (most + kApplyThreads - 1) / kApplyThreads;
+    cfg.gridDim = dim3((unsigned)(b < cap ? b : cap));
+    cfg.blockDim = dim3(kApplyThreads);
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, compact_apply_kernel, p);
+}
+
+// ------------------------------------------------------------------------------------------
+// kv_copy_pages
+// ------------------------------------------------------------------------------------------
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyLoads = 8;  // 16-byte vectors of a thread and turn: 32 KB a block
+
+// An item is one page of one cache; blocks take them in turn.
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyParams p) {
+    int n = p.n;
+    if (p.count) {
+        const int c = __ldg(p.count);
+        if (c < 0 || c > n) {
+            if (threadIdx.x == 0) raise_error(p.ws, kErrRange);
+            return;
+        }
+        n = c;
+    }
+    const long long w = p.page_vecs, pieces = (w + kCopyThreads * kCopyLoads - 1) / (kCopyThreads * kCopyLoads);
+    const long long items = (long long)n * p.caches * pieces;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const long long move = it / pieces, piece = it - move * pieces;
+        const int i = (int)(move / p.caches), c = (int)(move - (long long)i * p.caches);
+        const int src = __ldg(p.src + i), dst = __ldg(p.dst + i);
+        if (src < 0 && dst < 0) continue;
+        if (src < 0 || dst < 0 || src >= p.num_pages || dst >= p.num_pages) {
+            if (threadIdx.x == 0) raise_error(p.ws, kErrRange);
+            continue;
+        }
+        const uint4* from = static_cast<const uint4*>(p.cache[c]) + src * w;
+        uint4* to = static_cast<uint4*>(p.cache[c]) + dst * w;
+        const long long v0 = piece * kCopyThreads * kCopyLoads + threadIdx.x;
+        uint4 x[kCopyLoads];
+#pragma unroll
+        for (int k = 0; k < kCopyLoads; ++k)
+            if (v0 + k * kCopyThreads < w) x[k] = from[v0 + k * kCopyThreads];
+#pragma unroll
+        for (int k = 0; k < kCopyLoads; ++k)
+            if (v0 + k * kCopyThreads < w) to[v0 + k * kCopyThreads] = x[k];
+    }
+}
+
+cudaError_t launch_copy_pages(const CopyParams& p, cudaStream_t st) {
+    const long long pieces = (p.page_vecs + kCopyThreads * kCopyLoads - 1) / (kCopyThreads * kCopyLoads);
+    const long long items = (long long)p.n * p.caches * pieces, cap = 8ll * device_sm_count();
+    copy_pages_kernel<<<(unsigned)(items < cap ? items : cap), kCopyThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace smcsd

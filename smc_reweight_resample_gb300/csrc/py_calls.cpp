@@ -13,6 +13,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
+#include <vector>
 
 #include "smcsd.h"
 
@@ -31,6 +32,13 @@ decltype(&kv_append) f_append;
 decltype(&tree_mask) f_tree_mask;
 decltype(&tree_attention) f_attention;
 decltype(&logits_process) f_logits;
+decltype(&beam_select) f_beam;
+decltype(&state_reorder) f_reorder;
+decltype(&kv_fork) f_fork;
+decltype(&kv_free) f_free;
+decltype(&kv_compact) f_compact;
+decltype(&kv_copy_pages) f_copy;
+decltype(&distill_loss) f_distill;
 PyObject* f_error;  // error(status, where) raises
 
 // One call's positional arguments.
@@ -65,6 +73,7 @@ class Args {
         if (v == -1.0 && PyErr_Occurred()) throw Raised{};
         return v;
     }
+    void skip() { ++i_; }
     bool none() {
         if (a_[i_] != Py_None) return false;
         ++i_;
@@ -199,14 +208,21 @@ PyObject* tuple(std::initializer_list<at::Tensor> list) {
 
 PyObject* py_bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        Args a(args, n, 6);
+        Args a(args, n, 13);
         f_slot_map = reinterpret_cast<decltype(f_slot_map)>((uintptr_t)a.integer());
         f_append = reinterpret_cast<decltype(f_append)>((uintptr_t)a.integer());
         f_tree_mask = reinterpret_cast<decltype(f_tree_mask)>((uintptr_t)a.integer());
         f_attention = reinterpret_cast<decltype(f_attention)>((uintptr_t)a.integer());
         f_logits = reinterpret_cast<decltype(f_logits)>((uintptr_t)a.integer());
+        f_beam = reinterpret_cast<decltype(f_beam)>((uintptr_t)a.integer());
+        f_reorder = reinterpret_cast<decltype(f_reorder)>((uintptr_t)a.integer());
+        f_fork = reinterpret_cast<decltype(f_fork)>((uintptr_t)a.integer());
+        f_free = reinterpret_cast<decltype(f_free)>((uintptr_t)a.integer());
+        f_compact = reinterpret_cast<decltype(f_compact)>((uintptr_t)a.integer());
+        f_copy = reinterpret_cast<decltype(f_copy)>((uintptr_t)a.integer());
+        f_distill = reinterpret_cast<decltype(f_distill)>((uintptr_t)a.integer());
         Py_XDECREF(f_error);
-        f_error = Py_NewRef(args[5]);
+        f_error = Py_NewRef(args[12]);
         Py_RETURN_NONE;
     });
 }
@@ -359,6 +375,256 @@ PyObject* py_logits(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// Rows of at least V elements, each contiguous: elements from one row to the next.
+int64_t matrix_stride(const at::Tensor& t, int64_t V, const char* what) {
+    if (t.dim() != 2 || t.size(1) < V || (t.size(1) > 1 && t.stride(1) != 1)) value_error(std::string(what) + " must be rows of V");
+    // rows that share memory, or a step that is never taken
+    if (t.size(0) > 1 && t.stride(0) < V) value_error(std::string(what) + " must be rows of V");
+    return t.size(0) > 1 ? t.stride(0) : V;
+}
+
+// The tensors of a list or tuple.
+std::vector<const at::Tensor*> tensors_of(PyObject* o, size_t most, const char* what) {
+    if (!PyList_Check(o) && !PyTuple_Check(o)) type_error(std::string(what) + " must be a list of tensors");
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+    if (n < 1 || (size_t)n > most) value_error(std::string(what) + " must be 1 to " + std::to_string(most) + " tensors");
+    std::vector<const at::Tensor*> got;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        PyObject* t = PySequence_Fast_GET_ITEM(o, i);
+        if (!THPVariable_Check(t)) type_error("expected a tensor");
+        got.push_back(&THPVariable_Unpack(t));
+    }
+    return got;
+}
+constexpr size_t kMostStates = 64, kMostCaches = 256;
+
+// beam_select(logits, G, N, V, M, temperature, scores, finished, pad, eos, tokens, ancestors, out_scores, out_finished, ws, bytes)
+PyObject* py_beam(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 16);
+        const at::Tensor& z = a.some();
+        const int G = a.size(), N = a.size(), V = a.size(), M = a.size();
+        const double temperature = a.real();
+        const at::Tensor *scores = a.tensor(), *finished = a.tensor();
+        const int pad = a.size(), eos = a.size();
+        if (G <= 0 || N <= 0 || V <= 0 || M <= 0) value_error("sizes must be positive");
+        const int64_t stride = matrix_stride(z, V, "logits"), rows = (int64_t)G * N;
+        if (z.size(0) != rows) value_error("logits must have G * N rows");
+        at_least(scores, rows, "scores");
+        at_least(finished, rows, "finished");
+        const int dtype = dtype_code(z);
+        if (!z.is_cuda()) value_error("tensor must be on the CUDA device");
+        const c10::cuda::CUDAGuard guard(z.device());
+        const int64_t out = (int64_t)G * M;
+        const at::Tensor tokens = output(a.tensor(), {out}, at::kInt, z), ancestors = output(a.tensor(), {out}, at::kInt, z);
+        const at::Tensor out_scores = output(a.tensor(), {out}, at::kFloat, z), over = output(a.tensor(), {out}, at::kInt, z);
+        one_device(z, {scores, finished, &tokens, &ancestors, &out_scores, &over});
+        const Tail t(a, z);
+        check(f_beam(z.data_ptr(), stride, dtype, G, N, V, M, (float)temperature, f32(scores), i32(finished), pad, eos, i32(&tokens),
+                     i32(&ancestors), f32(&out_scores), i32(&over), t.ws, t.bytes, t.stream),
+              "beam_select");
+        return tuple({tokens, ancestors, out_scores, over});
+    });
+}
+
+// state_reorder(states, ancestors, G, N, M, out, ws, bytes)
+PyObject* py_reorder(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n < 1) type_error("wrong number of arguments");
+        Args a(args + 1, n - 1, 7);
+        const std::vector<const at::Tensor*> src = tensors_of(args[0], kMostStates, "states");
+        const at::Tensor& ancestors = a.some();
+        const int G = a.size(), N = a.size(), M = a.size();
+        if (G <= 0 || N <= 0 || M <= 0) value_error("sizes must be positive");
+        const int64_t rows = (int64_t)G * N, rows_out = (int64_t)G * M;
+        at_least(&ancestors, rows_out, "ancestors");
+        if (!ancestors.is_cuda()) value_error("tensor must be on the CUDA device");
+        const c10::cuda::CUDAGuard guard(ancestors.device());
+        std::vector<const at::Tensor*> given;
+        if (!a.none()) given = tensors_of(args[5], kMostStates, "out"), a.skip();
+        if (!given.empty() && given.size() != src.size()) value_error("out must have a tensor for each state");
+        std::vector<at::Tensor> dst;
+        const void* from[kMostStates];
+        void* to[kMostStates];
+        long long bytes[kMostStates];
+        for (size_t i = 0; i < src.size(); ++i) {
+            const at::Tensor& t = *src[i];
+            if (!t.is_cuda() || t.device() != ancestors.device()) value_error("tensors must be on one device");
+            if (t.dim() < 1 || t.size(0) != rows || t.numel() == 0) value_error("states must have G * N rows");
+            if (!t.is_contiguous()) value_error("tensor must be contiguous");
+            std::vector<int64_t> shape = t.sizes().vec();
+            shape[0] = rows_out;
+            if (given.empty()) {
+                dst.push_back(at::empty(shape, t.options()));
+            } else {
+                const at::Tensor& o = *given[i];
+                if (o.device() != t.device()) value_error("tensors must be on one device");
+                if (o.scalar_type() != t.scalar_type()) type_error("out must have the states' types");
+                if (!o.sizes().equals(shape)) value_error("out must have the states' shapes, with G * M rows");
+                if (!o.is_contiguous()) value_error("tensor must be contiguous");
+                dst.push_back(o);
+            }
+            from[i] = t.data_ptr();
+            to[i] = dst.back().data_ptr();
+            bytes[i] = (long long)(t.numel() / rows) * t.element_size();
+        }
+        const Tail t(a, ancestors);
+        check(f_reorder(from, to, bytes, (int)src.size(), i32(&ancestors), G, N, M, t.ws, t.bytes, t.stream), "state_reorder");
+        PyObject* list = PyList_New((Py_ssize_t)dst.size());
+        if (!list) throw Raised{};
+        for (size_t i = 0; i < dst.size(); ++i) {
+            PyObject* o = THPVariable_Wrap(dst[i]);
+            if (!o) {
+                Py_DECREF(list);
+                throw Raised{};
+            }
+            PyList_SET_ITEM(list, (Py_ssize_t)i, o);
+        }
+        return list;
+    });
+}
+
+// kv_fork(table_in, refcount_in, parents, page_size, lengths, table_out, refcount_out, ws, bytes)
+PyObject* py_fork(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 9);
+        const at::Tensor &table = a.some(), &ref = a.some(), &parents = a.some();
+        const int page = a.size();
+        const at::Tensor* lengths = a.tensor();
+        if (table.dim() != 2) value_error("table_in must be [S, pages_per_seq]");
+        const int S = dim(table.size(0)), pages = dim(ref.numel());
+        at_least(&parents, S, "parents");
+        at_least(lengths, S, "lengths");
+        if (!table.is_cuda()) value_error("tensor must be on the CUDA device");
+        const c10::cuda::CUDAGuard guard(table.device());
+        const at::Tensor table_out = output(a.tensor(), table.sizes(), at::kInt, table);
+        const at::Tensor ref_out = output(a.tensor(), {pages}, at::kInt, table);
+        one_device(table, {&ref, &parents, lengths, &table_out, &ref_out});
+        const Tail t(a, table);
+        check(f_fork(i32(&parents), i32(lengths), S, i32(&table), i32(&table_out), dim(table.size(1)), page, i32(&ref), i32(&ref_out), pages,
+                     t.ws, t.bytes, t.stream),
+              "kv_fork");
+        return tuple({table_out, ref_out});
+    });
+}
+
+// kv_free(table_in, refcount_in, lengths, page_size, table_out, refcount_out, ws, bytes)
+PyObject* py_free(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 8);
+        const at::Tensor &table = a.some(), &ref = a.some(), &lengths = a.some();
+        const int page = a.size();
+        if (table.dim() != 2) value_error("table_in must be [S, pages_per_seq]");
+        const int S = dim(table.size(0)), pages = dim(ref.numel());
+        at_least(&lengths, S, "lengths");
+        if (!table.is_cuda()) value_error("tensor must be on the CUDA device");
+        const c10::cuda::CUDAGuard guard(table.device());
+        const at::Tensor table_out = output(a.tensor(), table.sizes(), at::kInt, table);
+        const at::Tensor ref_out = output(a.tensor(), {pages}, at::kInt, table);
+        one_device(table, {&ref, &lengths, &table_out, &ref_out});
+        const Tail t(a, table);
+        check(f_free(i32(&lengths), S, i32(&table), i32(&table_out), dim(table.size(1)), page, i32(&ref), i32(&ref_out), pages, t.ws, t.bytes,
+                     t.stream),
+              "kv_free");
+        return tuple({table_out, ref_out});
+    });
+}
+
+// kv_compact(table_in, refcount_in, table_out, refcount_out, src, dst, counts, ws, bytes)
+PyObject* py_compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 9);
+        const at::Tensor &table = a.some(), &ref = a.some();
+        if (table.dim() != 2) value_error("table_in must be [S, pages_per_seq]");
+        const int S = dim(table.size(0)), pages = dim(ref.numel());
+        if (!table.is_cuda()) value_error("tensor must be on the CUDA device");
+        const c10::cuda::CUDAGuard guard(table.device());
+        const at::Tensor table_out = output(a.tensor(), table.sizes(), at::kInt, table);
+        const at::Tensor ref_out = output(a.tensor(), {pages}, at::kInt, table);
+        const at::Tensor src = output(a.tensor(), {pages / 2}, at::kInt, table), dst = output(a.tensor(), {pages / 2}, at::kInt, table);
+        const at::Tensor counts = output(a.tensor(), {2}, at::kInt, table);
+        one_device(table, {&ref, &table_out, &ref_out, &src, &dst, &counts});
+        const Tail t(a, table);
+        check(f_compact(S, i32(&table), i32(&table_out), dim(table.size(1)), i32(&ref), i32(&ref_out), pages, i32(&src), i32(&dst),
+                        i32(&counts), t.ws, t.bytes, t.stream),
+              "kv_compact");
+        return tuple({table_out, ref_out, src, dst, counts});
+    });
+}
+
+// kv_copy_pages(caches, src, dst, count, ws, bytes)
+PyObject* py_copy(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n < 1) type_error("wrong number of arguments");
+        Args a(args + 1, n - 1, 5);
+        const std::vector<const at::Tensor*> caches = tensors_of(args[0], kMostCaches, "caches");
+        const at::Tensor &src = a.some(), &dst = a.some();
+        const at::Tensor* count = a.tensor();
+        const int moves = dim(src.numel());
+        if (dst.numel() != moves) value_error("src and dst must be alike");
+        at_least(count, 1, "count");
+        const at::Tensor& like = *caches[0];
+        if (!like.is_cuda()) value_error("tensor must be on the CUDA device");
+        if (like.dim() < 1 || like.numel() == 0) value_error("caches must be [num_pages, ...]");
+        const c10::cuda::CUDAGuard guard(like.device());
+        void* at_[kMostCaches];
+        for (size_t i = 0; i < caches.size(); ++i) {
+            const at::Tensor& c = *caches[i];
+            if (c.scalar_type() != like.scalar_type()) type_error("caches must have one type");
+            if (!c.sizes().equals(like.sizes())) value_error("caches must be alike");
+            if (!c.is_contiguous()) value_error("tensor must be contiguous");
+            one_device(like, {&c});
+            at_[i] = c.data_ptr();
+        }
+        one_device(like, {&src, &dst, count});
+        const Tail t(a, like);
+        if (moves == 0) Py_RETURN_NONE;
+        check(f_copy(at_, (int)caches.size(), (long long)(like.numel() / like.size(0)) * like.element_size(), dim(like.size(0)), i32(&src),
+                     i32(&dst), moves, i32(count), t.ws, t.bytes, t.stream),
+              "kv_copy_pages");
+        Py_RETURN_NONE;
+    });
+}
+
+// distill_loss(logits, top_tokens, top_values, V, temperature, rest, weight, loss, dlogits, grad, with_loss, ws, bytes)
+PyObject* py_distill(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 13);
+        const at::Tensor &z = a.some(), &tokens = a.some(), &values = a.some();
+        const int V = a.size();
+        const double temperature = a.real();
+        const bool rest = a.integer() != 0;
+        const at::Tensor* weight = a.tensor();
+        if (V <= 0) value_error("V must be positive");
+        const int64_t stride = matrix_stride(z, V, "logits");
+        const int R = dim(z.size(0)), dtype = dtype_code(z);
+        if (tokens.dim() != 2 || tokens.size(0) != R || !tokens.sizes().equals(values.sizes()))
+            value_error("top_tokens and top_values must be [R, K]");
+        at_least(weight, R, "weight");
+        if (!z.is_cuda()) value_error("tensor must be on the CUDA device");
+        const c10::cuda::CUDAGuard guard(z.device());
+        const at::Tensor *loss_in = a.tensor(), *grad_in = a.tensor();
+        at::Tensor loss, grad;
+        const bool want_grad = a.integer() || grad_in;
+        if (a.integer() || loss_in) loss = output(loss_in, {R}, at::kFloat, z);
+        int64_t grad_stride = 0;
+        if (want_grad) {
+            grad = grad_in ? *grad_in : at::empty({R, V}, z.options());
+            grad_stride = matrix_stride(grad, V, "dlogits");
+            if (grad.size(0) != R) value_error("dlogits must have the logits' rows");
+            if (grad.scalar_type() != z.scalar_type()) type_error("dlogits must have the logits' type");
+            if (R == 1 && grad.data_ptr() == z.data_ptr()) grad_stride = stride;
+        }
+        one_device(z, {&tokens, &values, weight, loss.defined() ? &loss : nullptr, grad.defined() ? &grad : nullptr});
+        const Tail t(a, z);
+        check(f_distill(z.data_ptr(), stride, dtype, R, V, i32(&tokens), f32(&values), dim(tokens.size(1)), (float)temperature, rest,
+                        f32(weight), loss.defined() ? f32(&loss) : nullptr, grad.defined() ? grad.data_ptr() : nullptr, grad_stride, t.ws,
+                        t.bytes, t.stream),
+              "distill_loss");
+        return tuple({loss, grad});
+    });
+}
+
 PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))py_bind, METH_FASTCALL, nullptr},
     {"kv_slot_map", (PyCFunction)(void (*)(void))py_slot_map, METH_FASTCALL, nullptr},
@@ -366,6 +632,13 @@ PyMethodDef methods[] = {
     {"tree_mask", (PyCFunction)(void (*)(void))py_tree_mask, METH_FASTCALL, nullptr},
     {"tree_attention", (PyCFunction)(void (*)(void))py_attention, METH_FASTCALL, nullptr},
     {"logits_process", (PyCFunction)(void (*)(void))py_logits, METH_FASTCALL, nullptr},
+    {"beam_select", (PyCFunction)(void (*)(void))py_beam, METH_FASTCALL, nullptr},
+    {"state_reorder", (PyCFunction)(void (*)(void))py_reorder, METH_FASTCALL, nullptr},
+    {"kv_fork", (PyCFunction)(void (*)(void))py_fork, METH_FASTCALL, nullptr},
+    {"kv_free", (PyCFunction)(void (*)(void))py_free, METH_FASTCALL, nullptr},
+    {"kv_compact", (PyCFunction)(void (*)(void))py_compact, METH_FASTCALL, nullptr},
+    {"kv_copy_pages", (PyCFunction)(void (*)(void))py_copy, METH_FASTCALL, nullptr},
+    {"distill_loss", (PyCFunction)(void (*)(void))py_distill, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "The calls around the verify over the C ABI.", -1, methods,
