@@ -16,8 +16,7 @@ namespace cg = cooperative_groups;
 
 namespace smcsd {
 
-constexpr int kDistillThreads = 256;
-constexpr int kDistillWarps = kDistillThreads / 32;
+constexpr int kDistillThreads = 256, kDistillMostThreads = 512;
 static_assert(kDistillThreads >= kDistillMostTokens, "a thread for each listed token");
 
 __device__ __forceinline__ void copy16_async(uint32_t to, const void* from) {
@@ -28,6 +27,32 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// Two floats in one register pair, for the instructions that work on both.
+struct f32x2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void halves(f32x2 a, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ f32x2 exp2_2(f32x2 a) {
+    float lo, hi;
+    halves(a, lo, hi);
+    return pair(exp2_fast(lo), exp2_fast(hi));
 }
 
 template <int DT>
@@ -47,118 +72,196 @@ __device__ __forceinline__ uint32_t round_to(float f) {
     asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(f));
     return r;
 }
+// A 16-byte vector as pairs of floats: 2 of float32, 4 of bf16.
 template <int DT>
-__device__ __forceinline__ uint4 pack(const float* f) {
-    uint32_t w[4];
+struct Vec {
+    static constexpr int kPairs = Geo<DT>::kPerVec / 2;
+    f32x2 x[kPairs];
+    __device__ __forceinline__ explicit Vec(const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (DT == 0)
-            w[i] = __float_as_uint(f[i]);
-        else
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+        for (int i = 0; i < kPairs; ++i)
+            x[i] = DT == 0 ? pair(__uint_as_float(w[(2 * i) & 3]), __uint_as_float(w[(2 * i + 1) & 3])) : pair(bf16_lo(w[i & 3]), bf16_hi(w[i & 3]));
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    __device__ __forceinline__ uint4 packed() const {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            float lo, hi;
+            halves(x[i], lo, hi);
+            if (DT == 0)
+                w[(2 * i) & 3] = __float_as_uint(lo), w[(2 * i + 1) & 3] = __float_as_uint(hi);
+            else
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i & 3]) : "f"(hi), "f"(lo));
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+// Maxima that pass over NaN: of words of the type, and of a word's halves.
+template <int DT>
+__device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (DT == 0)
+        r = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    else
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 template <int DT>
-__device__ __forceinline__ void unpack_vec(const uint4& x, float* f) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ float word_value(uint32_t a) {
+    return DT == 0 ? __uint_as_float(a) : fmaxf(bf16_lo(a), bf16_hi(a));
+}
+
+// A sum of exp(c (z - m)) and its reference m. A reference of -inf goes with a sum of 0, or of NaN.
+struct Mass {
+    float m, s;
+};
+__device__ __forceinline__ float rescale(float from, float to, float c2) { return from > kNegInf ? exp2_fast((from - to) * c2) : 1.0f; }
+__device__ __forceinline__ Mass warp_mass(Mass a, float c2) {
+    const float m = warp_max(a.m);
+    return Mass{m, warp_sum(a.s * rescale(a.m, m, c2))};
+}
+__device__ __forceinline__ Mass join(Mass a, Mass b, float c2) {
+    const float m = fmaxf(a.m, b.m);
+    return Mass{m, a.s * rescale(a.m, m, c2) + b.s * rescale(b.m, m, c2)};
+}
+// Two masses each of up to 16 entries, on every lane of the calling warp.
+struct Masses {
+    Mass a, b;
+};
+__device__ __forceinline__ Masses join_lanes(const float4* q, int n, float c2) {
+    const int lane = threadIdx.x & 31;
+    const float4 x = lane < n ? q[lane] : make_float4(kNegInf, 0.0f, kNegInf, 0.0f);
+    const float a = warp_max(x.x), b = warp_max(x.z);
+    float sa = x.y * rescale(x.x, a, c2), sb = x.w * rescale(x.z, b, c2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (DT == 0) {
-            f[i] = __uint_as_float(w[i]);
-        } else {
-            f[2 * i] = bf16_lo(w[i]);
-            f[2 * i + 1] = bf16_hi(w[i]);
-        }
+    for (int o = 8; o > 0; o >>= 1) {
+        sa += __shfl_xor_sync(0xffffffffu, sa, o);
+        sb += __shfl_xor_sync(0xffffffffu, sb, o);
     }
+    return Masses{Mass{a, __shfl_sync(0xffffffffu, sa, 0)}, Mass{b, __shfl_sync(0xffffffffu, sb, 0)}};
 }
 
 struct DistillShared {
-    int token[kDistillMostTokens];
+    alignas(16) int token[kDistillMostTokens];
     float p[kDistillMostTokens];
-    float z[kDistillMostTokens];       // in the first block: the listed tokens' logits
-    float4 part[kDistillMostCtas];     // of each block: maximum and sum of the rest, of the listed tokens
-    float a[kDistillWarps], b[kDistillWarps];
-    dd d[kDistillWarps];
+    float z[kDistillMostTokens];    // in the first block: the listed tokens' logits
+    float4 part[kDistillMostCtas];       // of each block: the rest's mass, the listed tokens' mass
+    float4 q[kDistillMostThreads / 32];  // of each warp: the same
+    float4 row;                          // the row's mass, the factor of the gradient and the reference that it goes with
+    float a[kDistillMostTokens / 32], b[kDistillMostTokens / 32];
+    dd d[kDistillMostTokens / 32];
+    int repeats;       // whether a token is listed several times
 };
 
-// Maxima, or sums, of two values over the block.
-__device__ __forceinline__ float2 block_max2(DistillShared& s, float a, float b) {
+// Maximum, or sum, over the list's entries, one of each thread of the block's first `warps` warps, which alone call these.
+__device__ __forceinline__ void list_sync(int warps) { asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory"); }
+__device__ __forceinline__ float list_max(DistillShared& s, float a, int warps) {
     a = warp_max(a);
-    b = warp_max(b);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s.a[threadIdx.x >> 5] = a, s.b[threadIdx.x >> 5] = b;
-    __syncthreads();
-    a = s.a[0], b = s.b[0];
-#pragma unroll
-    for (int w = 1; w < kDistillWarps; ++w) a = fmaxf(a, s.a[w]), b = fmaxf(b, s.b[w]);
-    return make_float2(a, b);
+    if (warps == 1) return a;
+    if ((threadIdx.x & 31) == 0) s.a[threadIdx.x >> 5] = a;
+    list_sync(warps);
+    for (int w = 0; w < warps; ++w) a = fmaxf(a, s.a[w]);
+    return a;
 }
-__device__ __forceinline__ float2 block_sum2(DistillShared& s, float a, float b) {
+__device__ __forceinline__ float list_sum(DistillShared& s, float a, int warps) {
     a = warp_sum(a);
-    b = warp_sum(b);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s.a[threadIdx.x >> 5] = a, s.b[threadIdx.x >> 5] = b;
-    __syncthreads();
-    a = s.a[0], b = s.b[0];
-#pragma unroll
-    for (int w = 1; w < kDistillWarps; ++w) a += s.a[w], b += s.b[w];
-    return make_float2(a, b);
+    if (warps == 1) return a;
+    if ((threadIdx.x & 31) == 0) s.b[threadIdx.x >> 5] = a;
+    list_sync(warps);
+    a = s.b[0];
+    for (int w = 1; w < warps; ++w) a += s.b[w];
+    return a;
 }
-__device__ __forceinline__ dd block_sum_dd(DistillShared& s, dd a) {
-    a = warp_sum_dd(a);
-    __syncthreads();
+__device__ __forceinline__ dd list_sum_dd(DistillShared& s, float v, int warps) {
+    dd a = warp_sum_dd(dd{v, 0.0f});
+    if (warps == 1) return a;
     if ((threadIdx.x & 31) == 0) s.d[threadIdx.x >> 5] = a;
-    __syncthreads();
+    list_sync(warps);
     a = s.d[0];
-#pragma unroll
-    for (int w = 1; w < kDistillWarps; ++w) a = dd_add(a, s.d[w]);
+    for (int w = 1; w < warps; ++w) a = dd_add(a, s.d[w]);
     return a;
 }
 
-// This block's share of a row: vectors first .. first + n - 1 of the row's aligned vectors, the first of which begins `shift`
-// elements before the row.
+// Whether this thread's token stands in the list more than once.
+__device__ __forceinline__ bool list_repeats(int token, const DistillShared& s, int warps, int K) {
+    if (token < 0) token = -2 - (int)threadIdx.x;  // alike with nobody's
+    if (warps == 1) return __popc(__match_any_sync(0xffffffffu, token)) > 1;
+    int n = 0;
+    for (int k = 0; k < K; k += 4) {  // behind K there are -1
+        const int4 t = *reinterpret_cast<const int4*>(s.token + k);
+        n += (t.x == token) + (t.y == token) + (t.z == token) + (t.w == token);
+    }
+    return n > 1;
+}
+
+// This block's share of a row: n of the row's aligned vectors, the first of which begins at the row's element `e0`. It may begin
+// before the row (the row's first vector) and end behind it (its last).
 template <int DT>
 struct Share {
-    const char* row;
-    int shift, V;
-    long long first;
-    int n;
-    // the elements of vector i of the share that lie in the row: from lo to hi - 1
-    __device__ void within(int i, int& lo, int& hi) const {
-        constexpr int PV = Geo<DT>::kPerVec;
-        const long long e = (first + i) * PV - shift;
-        lo = e < 0 ? (int)-e : 0;
-        hi = e + PV > V ? (int)(V - e) : PV;
+    const char* at;  // first vector
+    int n, e0, V;
+    __device__ Share(const DistillParams& p, int r, int rank) {
+        constexpr int PV = Geo<DT>::kPerVec, B = Geo<DT>::kBytes;
+        const char* row = static_cast<const char*>(p.logits) + (long long)r * p.row_stride * B;
+        const int shift = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / B;
+        const int first = rank * p.vecs, all = (p.V + shift + PV - 1) / PV - first;
+        V = p.V;
+        n = all < 0 ? 0 : all < p.vecs ? all : p.vecs;
+        e0 = first * PV - shift;
+        at = row + (long long)e0 * B;
     }
-    __device__ long long element(int i) const { return (first + i) * (long long)Geo<DT>::kPerVec - shift; }
+    // vectors that lie in the row whole: from whole_from() to whole_to() - 1; the first and the last one may not
+    __device__ int whole_from() const { return e0 < 0 && n > 0 ? 1 : 0; }
+    __device__ int whole_to() const { return n > 0 && e0 + n * Geo<DT>::kPerVec > V ? n - 1 : n; }
 };
 
-// Writes f(i) (a vector of elements) for every vector i of the share to the row of the gradient.
+// Elements of a vector one by one: f(e, bits) for those from `lo` to `hi` - 1.
 template <int DT, typename F>
-__device__ __forceinline__ void write_share(const Share<DT>& h, char* out, F&& f) {
-    constexpr int PV = Geo<DT>::kPerVec, B = Geo<DT>::kBytes;
-    using T = typename Elem<DT>::T;
-    const bool alike = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(h.row)) & 15u) == 0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < h.n; i += kDistillThreads) {
-        int lo, hi;
-        h.within(i, lo, hi);
-        const uint4 x = f(i);
-        char* to = out + h.element(i) * B;
-        if (alike && lo == 0 && hi == PV) {
-            *reinterpret_cast<uint4*>(to) = x;
-        } else {
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ void each_element(const uint4& x, int lo, int hi, F&& f) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int e = 0; e < PV; ++e)
-                if (e >= lo && e < hi) reinterpret_cast<T*>(to)[e] = (T)(DT == 0 ? w[e & 3] : w[(e >> 1) & 3] >> (16 * (e & 1)));
-        }
+    for (int e = 0; e < Geo<DT>::kPerVec; ++e)
+        if (e >= lo && e < hi) f(e, DT == 0 ? w[e & 3] : (w[(e >> 1) & 3] >> (16 * (e & 1))) & 0xffffu);
+}
+
+// The share on its way to shared memory, its whole vectors as they are, of the others the elements that lie in the row.
+template <int DT, int TH>
+__device__ __forceinline__ void fetch(const Share<DT>& h, uint4* to) {
+    constexpr int PV = Geo<DT>::kPerVec;
+    using T = typename Elem<DT>::T;
+    const int from = h.whole_from(), upto = h.whole_to();
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    for (int i = from + threadIdx.x; i < upto; i += TH) copy16_async(at + 16u * i, h.at + 16ll * i);
+    if (threadIdx.x < 2 * PV) {  // a thread for each element of the first and the last vector
+        const int i = threadIdx.x < PV ? 0 : h.n - 1, e = threadIdx.x & (PV - 1), v = h.e0 + i * PV + e;
+        if (i < h.n && i >= 0 && (i < from || i >= upto))
+            reinterpret_cast<T*>(to + i)[e] = (T)(v >= 0 && v < h.V ? logit_bits<DT>(h.at, (long long)i * PV + e) : neg_inf_bits<DT>());
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kDistillThreads) distill_kernel(const __grid_constant__ DistillParams p) {
+// Writes f(i), a vector, for every vector i of the share to the row `out` of the gradient.
+template <int DT, int TH, typename F>
+__device__ __forceinline__ void write_share(const Share<DT>& h, char* out, F&& f) {
+    constexpr int PV = Geo<DT>::kPerVec, B = Geo<DT>::kBytes;
+    using T = typename Elem<DT>::T;
+    char* to = out + (long long)h.e0 * B;
+    const bool alike = (reinterpret_cast<uintptr_t>(to) & 15u) == 0;
+    const int from = alike ? h.whole_from() : h.n, upto = alike ? h.whole_to() : h.n;
+#pragma unroll 1
+    for (int i = from + threadIdx.x; i < upto; i += TH) *reinterpret_cast<uint4*>(to + 16ll * i) = f(i);
+    if (from == 0 && upto == h.n) return;
+    // the first and the last vector, or all of a row that lies otherwise than the logits'
+    for (int i = threadIdx.x; i < h.n; i += TH) {
+        if (i >= from && i < upto) continue;
+        const int v = h.e0 + i * PV;
+        each_element<DT>(f(i), v < 0 ? -v : 0, v + PV > h.V ? h.V - v : PV, [&](int e, uint32_t bits) { reinterpret_cast<T*>(to)[(long long)i * PV + e] = (T)bits; });
+    }
+}
+
+// Shares of 32 KB: six blocks of 256 threads in an SM, each at another point of its row, so that loads, sums and stores overlap.
+template <int DT, int TH>
+__global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 2) distill_kernel(const __grid_constant__ DistillParams p) {
     constexpr int PV = Geo<DT>::kPerVec, B = Geo<DT>::kBytes;
     using T = typename Elem<DT>::T;
     extern __shared__ uint4 s_row[];
@@ -168,6 +271,7 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const __grid_c
     const int r = blockIdx.x / C;
     auto started = cl.barrier_arrive();  // the other blocks' shared memory may be written once all have come here
 
+    const Share<DT> h(p, r, rank);
     // the row's list
     int token = -1;
     float value = kNegInf;
@@ -183,178 +287,169 @@ __global__ void __launch_bounds__(kDistillThreads) distill_kernel(const __grid_c
         }
     }
     if (tid < kDistillMostTokens) s.token[tid] = token;
+    if (tid == 0) s.repeats = 0;
     const float weight = p.weight ? __ldg(p.weight + r) : 1.0f;
-
-    Share<DT> h;
-    h.row = static_cast<const char*>(p.logits) + (long long)r * p.row_stride * B;
-    h.shift = (int)(reinterpret_cast<uintptr_t>(h.row) & 15u) / B;
-    h.V = p.V;
-    h.first = (long long)rank * p.vecs;
-    const long long all = ((long long)p.V + h.shift + PV - 1) / PV;
-    h.n = (int)(all - h.first < 0 ? 0 : all - h.first < p.vecs ? all - h.first : p.vecs);
     char* out = p.grad ? static_cast<char*>(p.grad) + (long long)r * p.grad_stride * B : nullptr;
 
     const bool some = __syncthreads_or(value > kNegInf);
     if (!some || (weight == 0.0f && !p.loss)) {
         cl.barrier_wait(std::move(started));
-        if (out) write_share<DT>(h, out, [](int) { return make_uint4(0, 0, 0, 0); });
+        if (out) write_share<DT, TH>(h, out, [](int) { return make_uint4(0, 0, 0, 0); });
         if (rank == 0 && tid == 0 && p.loss) p.loss[r] = 0.0f;
         return;
     }
-
-    // the share's whole vectors on their way; the row's first and last vector may lie in it in part
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(s_row);
-    for (int i = tid; i < h.n; i += kDistillThreads) {
-        int lo, hi;
-        h.within(i, lo, hi);
-        if (lo == 0 && hi == PV) {
-            copy16_async(to + 16u * i, h.row + h.element(i) * B);
-        } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = DT == 0 ? neg_inf_bits<0>() : neg_inf_bits<1>() * 0x10001u;
-#pragma unroll
-            for (int e = 0; e < PV; ++e)
-                if (e >= lo && e < hi) {
-                    const uint32_t bits = logit_bits<DT>(h.row, h.element(i) + e);
-                    if (DT == 0)
-                        w[e & 3] = bits;
-                    else
-                        w[(e >> 1) & 3] = e & 1 ? (w[(e >> 1) & 3] & 0xffffu) | bits << 16 : (w[(e >> 1) & 3] & 0xffff0000u) | bits;
-                }
-            s_row[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
-
+    fetch<DT, TH>(h, s_row);
     // meanwhile the teacher's probabilities
-    float logp, prob, rest = 0.0f, mass = 1.0f;
-    if (p.rest) {
-        logp = value;
-        prob = value > kNegInf ? expf(value) : 0.0f;
-        const dd sum = block_sum_dd(s, dd{prob, 0.0f});
-        rest = fmaxf(dd_add(dd{1.0f, 0.0f}, dd_neg(sum)).hi, 0.0f);
-        mass = fmaxf(sum.hi, 1.0f);
-    } else {
-        const float top = block_max2(s, value, kNegInf).x;
-        const float e = value > kNegInf ? expf(value - top) : 0.0f;
-        const dd sum = block_sum_dd(s, dd{e, 0.0f});
-        logp = value - top - logf(sum.hi);
-        prob = e / sum.hi;
-    }
-    if (tid < kDistillMostTokens) s.p[tid] = prob;
-    __syncthreads();
-    // a token that is listed several times: its first place stands for all of them
+    const int lists = (p.K + 31) / 32;  // warps with entries
+    const bool lister = tid < 32 * lists;
+    float logp = kNegInf, prob = 0.0f, rest = 0.0f, mass = 1.0f, listed = 0.0f;
     bool first = token >= 0;
-    float listed = 0.0f;
-    if (token >= 0)
-        for (int k = 0; k < p.K; ++k)
-            if (s.token[k] == token) {
-                listed += s.p[k];
-                first = first && k >= tid;
-            }
-
+    if (lister) {
+        if (p.rest) {
+            logp = value;
+            prob = value > kNegInf ? expf(value) : 0.0f;
+            const dd sum = list_sum_dd(s, prob, lists);
+            rest = fmaxf(dd_add(dd{1.0f, 0.0f}, dd_neg(sum)).hi, 0.0f);
+            mass = fmaxf(sum.hi, 1.0f);
+        } else {
+            const float top = list_max(s, value, lists);
+            const float e = value > kNegInf ? expf(value - top) : 0.0f;
+            const dd sum = list_sum_dd(s, e, lists);
+            logp = value - top - logf(sum.hi);
+            prob = e / sum.hi;
+        }
+        s.p[tid] = prob;
+        if (list_repeats(token, s, lists, p.K)) s.repeats = 1;
+    }
     copies_done();
     __syncthreads();
-    // the listed tokens are taken out of the share
+    // the listed tokens' logits. Where there is a rest, they are taken out of the share, so that its mass is a sum and no difference
     T* elems = reinterpret_cast<T*>(s_row);
-    const long long at = token + (long long)h.shift - h.first * PV;
-    const bool mine = token >= 0 && at >= 0 && at < (long long)h.n * PV;
+    const int at = token - h.e0;
+    const bool mine = token >= 0 && at >= 0 && at < h.n * PV;
     float z = kNegInf;
     if (mine) z = bits_to_float<DT>((uint32_t)elems[at]);
-    __syncthreads();
-    if (mine) elems[at] = (T)neg_inf_bits<DT>();
-    __syncthreads();
-
-    // the share's maximum and sum
-    float m = kNegInf;
-    for (int i = tid; i < h.n; i += kDistillThreads) {
-        float f[PV];
-        unpack_vec<DT>(s_row[i], f);
-#pragma unroll
-        for (int e = 0; e < PV; ++e) m = fmaxf(m, f[e]);
-    }
-    const float2 top = block_max2(s, m, first ? z : kNegInf);
-    float sum = 0.0f;
-    const float m0 = top.x > kNegInf ? top.x : 0.0f;  // a share of -inf alone adds up to 0, one with NaN to NaN
-    for (int i = tid; i < h.n; i += kDistillThreads) {
-        float f[PV];
-        unpack_vec<DT>(s_row[i], f);
-#pragma unroll
-        for (int e = 0; e < PV; ++e) f[e] = exp2_fast((f[e] - m0) * p.c2);
-#pragma unroll
-        for (int o = PV / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int e = 0; e < o; ++e) f[e] += f[e + o];
-        sum += f[0];
-    }
-    const float ez = first && mine ? (top.y > kNegInf ? exp2f((z - top.y) * p.c2) : z != z ? z : 0.0f) : 0.0f;
-    const float2 total = block_sum2(s, sum, ez);
-
-    cl.barrier_wait(std::move(started));
-    if (mine) *cl.map_shared_rank(&s.z[tid], 0) = z;
-    if (tid < C) *cl.map_shared_rank(&s.part[rank], tid) = make_float4(top.x, total.x, top.y, total.y);
-    cl.sync();
-
-    // the row's
-    float mr = kNegInf, mt = kNegInf;
-    for (int k = 0; k < C; ++k) mr = fmaxf(mr, s.part[k].x), mt = fmaxf(mt, s.part[k].z);
-    float sr = 0.0f, st = 0.0f;
-    for (int k = 0; k < C; ++k) {
-        const float4 x = s.part[k];
-        sr += x.x > kNegInf ? x.y * exp2f((x.x - mr) * p.c2) : x.y;
-        st += x.z > kNegInf ? x.w * exp2f((x.z - mt) * p.c2) : x.w;
-    }
-    const float mm = fmaxf(mr, mt);
-    const float kr = mr > kNegInf ? exp2f((mr - mm) * p.c2) : 0.0f, kt = mt > kNegInf ? exp2f((mt - mm) * p.c2) : 0.0f;
-    const float S = sr * kr + st * kt;
-    if (rank == 0) {
-        if (tid == 0 && !(S > 0.0f && S < kPosInf)) raise_error(p.ws, kErrNonfinite);
-        if (p.loss) {
-            const float ls = logf(S);
-            float term = 0.0f;
-            if (prob > 0.0f) term = prob * (logp - ((s.z[tid] - mm) * p.c - ls));
-            if (tid == 0 && rest > 0.0f) term += rest * (logf(rest) - (logf(sr) + (mr - mm) * p.c - ls));
-            const float loss = block_sum2(s, term, 0.0f).x;
-            if (tid == 0) p.loss[r] = loss;
+    if (lister) {
+        // a token that is listed several times: its first place stands for all of them
+        listed = prob;
+        if (s.repeats && token >= 0) {
+            listed = 0.0f;
+            for (int k = p.K - 1; k >= 0; --k)
+                if (s.token[k] == token) {
+                    listed += s.p[k];
+                    first = k == tid;
+                }
         }
     }
-    if (!out) return;
-    const float wc = weight * p.c;
-    // a rest without mass (all -inf) gets no gradient
-    const float scale = mr > kNegInf ? wc * (mass * (kr / S) - rest / sr) : 0.0f;
-    const float m1 = mr > kNegInf ? mr : 0.0f;
-    write_share<DT>(h, out, [&](int i) {
-        float f[PV];
-        unpack_vec<DT>(s_row[i], f);
+    if (p.rest) {
+        if (lister) list_sync(lists);
+        if (mine) elems[at] = (T)neg_inf_bits<DT>();
+        __syncthreads();
+    }
+
+    // the share's mass: each thread relative to its first vector's maximum, unless a later one is so much larger (or the first
+    // one is masked) that the sum says little; then to its own maximum
+    const f32x2 c2 = pair(p.c2, p.c2);
+    const auto mass_of = [&](float m) {
+        const float m0 = m > kNegInf ? -m : 0.0f;  // -inf alone adds up to 0, NaN to NaN
+        const f32x2 m2 = pair(m0, m0);
+        f32x2 sum[Vec<DT>::kPairs];
 #pragma unroll
-        for (int e = 0; e < PV; ++e) f[e] = exp2_fast((f[e] - m1) * p.c2) * scale;
-        return pack<DT>(f);
+        for (int k = 0; k < Vec<DT>::kPairs; ++k) sum[k] = pair(0.0f, 0.0f);
+#pragma unroll 2
+        for (int i = tid; i < h.n; i += TH) {
+            const Vec<DT> v(s_row[i]);
+#pragma unroll
+            for (int k = 0; k < Vec<DT>::kPairs; ++k) sum[k] = add2(sum[k], exp2_2(mul2(add2(v.x[k], m2), c2)));
+        }
+#pragma unroll
+        for (int k = 1; k < Vec<DT>::kPairs; ++k) sum[0] = add2(sum[0], sum[k]);
+        float lo, hi;
+        halves(sum[0], lo, hi);
+        return Mass{m, lo + hi};
+    };
+    Mass a{kNegInf, 0.0f};
+    if (tid < h.n) {
+        const uint4 x = s_row[tid];
+        uint32_t top = word_max<DT>(word_max<DT>(x.x, x.y), word_max<DT>(x.z, x.w));
+        for (bool whole = false;; whole = true) {
+            a = mass_of(word_value<DT>(top));
+            if (whole || (a.m > kNegInf && a.s < 1.2676506e30f)) break;  // 2^100
+            for (int i = tid; i < h.n; i += TH) {
+                const uint4 y = s_row[i];
+                top = word_max<DT>(top, word_max<DT>(word_max<DT>(y.x, y.y), word_max<DT>(y.z, y.w)));
+            }
+        }
+    }
+    a = warp_mass(a, p.c2);
+    Mass b{kNegInf, 0.0f};
+    if (lister && p.rest) {
+        if (first && mine) b = Mass{z, z > kNegInf ? 1.0f : z != z ? z : 0.0f};
+        b = warp_mass(b, p.c2);
+    }
+    if ((tid & 31) == 0) s.q[tid >> 5] = make_float4(a.m, a.s, b.m, b.s);
+    cl.barrier_wait(std::move(started));
+    __syncthreads();
+    if (mine) *cl.map_shared_rank(&s.z[tid], 0) = z;
+    if (tid < 32) {
+        const Masses q = join_lanes(s.q, TH / 32, p.c2);
+        if (tid < C) *cl.map_shared_rank(&s.part[rank], tid) = make_float4(q.a.m, q.a.s, q.b.m, q.b.s);
+    }
+    cl.sync();
+
+    // the row's mass, by one warp; without a rest all of it is in R
+    const float wc = weight * p.c;
+    if (tid < 32) {
+        const Masses row = join_lanes(s.part, C, p.c2);
+        const Mass R = row.a, all = p.rest ? join(R, row.b, p.c2) : R;
+        if (tid == 0) {
+            // the rest relative to its own maximum; one without mass (all -inf) gets no gradient
+            float scale = 0.0f;
+            if (R.m > kNegInf) scale = p.rest ? wc * (mass * exp2f((R.m - all.m) * p.c2) / all.s - rest / R.s) : wc / all.s;
+            s.row = make_float4(all.m, all.s, scale, R.m > kNegInf ? R.m : 0.0f);
+            s.q[0].x = R.m, s.q[0].y = R.s;
+            if (rank == 0 && !(all.s > 0.0f && all.s < kPosInf && all.m < kPosInf)) raise_error(p.ws, kErrNonfinite);
+        }
+    }
+    __syncthreads();
+    const float4 row = s.row;
+    const Mass all{row.x, row.y};
+    if (rank == 0 && lister && p.loss) {
+        const float ls = logf(all.s);
+        float term = 0.0f;
+        if (prob > 0.0f) term = prob * (logp - ((s.z[tid] - all.m) * p.c - ls));
+        if (tid == 0 && rest > 0.0f) term += rest * (logf(rest) - (logf(s.q[0].y) + (s.q[0].x - all.m) * p.c - ls));
+        const float loss = list_sum(s, term, lists);
+        if (tid == 0) p.loss[r] = loss;
+    }
+    if (!out) return;
+    const f32x2 m2 = pair(-row.w, -row.w), scale2 = pair(row.z, row.z);
+    write_share<DT, TH>(h, out, [&](int i) {
+        Vec<DT> v(s_row[i]);
+#pragma unroll
+        for (int k = 0; k < Vec<DT>::kPairs; ++k) v.x[k] = mul2(exp2_2(mul2(add2(v.x[k], m2), c2)), scale2);
+        return v.packed();
     });
     __syncthreads();  // the listed tokens' places have been written as part of the rest
     if (mine && first) {
-        const float q = exp2f((z - mm) * p.c2) / S;
+        const float q = exp2f((z - all.m) * p.c2) / all.s;
         reinterpret_cast<T*>(out)[token] = (T)round_to<DT>(wc * (mass * q - listed));
     }
 }
 
-cudaError_t launch_distill(const DistillParams& p0, int dtype, cudaStream_t st) {
-    DistillParams p = p0;
-    // shares of at most 32 KB, so that several rows' blocks are in an SM at a time
-    const long long bytes = (long long)p.V * (dtype == 0 ? 4 : 2), vecs = (bytes + 30) / 16;
-    p.ctas = 1;
-    while (p.ctas < kDistillMostCtas && vecs > p.ctas * 2048ll) p.ctas *= 2;
-    p.vecs = (int)((vecs + p.ctas - 1) / p.ctas);
+template <int DT, int TH>
+static cudaError_t launch_distill_as(const DistillParams& p, cudaStream_t st) {
     const size_t shared = 16 * (size_t)p.vecs;
-    const auto kernel = dtype == 0 ? distill_kernel<0> : distill_kernel<1>;
     cudaError_t e = cudaSuccess;
-    if (shared > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+    if (shared > 40 * 1024) e = cudaFuncSetAttribute(distill_kernel<DT, TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+    if (e == cudaSuccess && p.ctas > 8) e = cudaFuncSetAttribute(distill_kernel<DT, TH>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return e;
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((long long)p.R * p.ctas));
-    cfg.blockDim = dim3(kDistillThreads);
+    cfg.blockDim = dim3(TH);
     cfg.dynamicSmemBytes = shared;
     cfg.stream = st;
     cudaLaunchAttribute at{};
@@ -363,7 +458,19 @@ cudaError_t launch_distill(const DistillParams& p0, int dtype, cudaStream_t st) 
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, distill_kernel<DT, TH>, p);
+}
+
+cudaError_t launch_distill(const DistillParams& p0, int dtype, cudaStream_t st) {
+    DistillParams p = p0;
+    // shares of at most 40 KB, as long as sixteen blocks are enough for that
+    const long long bytes = (long long)p.V * (dtype == 0 ? 4 : 2), vecs = (bytes + 30) / 16;
+    p.ctas = 1;
+    while (p.ctas < kDistillMostCtas && vecs > p.ctas * 2560ll) p.ctas *= 2;
+    p.vecs = (int)((vecs + p.ctas - 1) / p.ctas);
+    const bool large = p.vecs > 2560;
+    if (dtype == 0) return large ? launch_distill_as<0, kDistillMostThreads>(p, st) : launch_distill_as<0, kDistillThreads>(p, st);
+    return large ? launch_distill_as<1, kDistillMostThreads>(p, st) : launch_distill_as<1, kDistillThreads>(p, st);
 }
 
 }  // namespace smcsd

@@ -189,7 +189,7 @@ extern "C" int distill_loss(const void* logits, long long row_stride, int dtype,
                             long long dlogits_stride, void* ws, size_t ws_bytes, void* stream) {
     if (dtype != SMCSD_F32 && dtype != SMCSD_BF16) return SMCSD_ERR_DTYPE;
     if (!logits || !top_tokens || !top_values || (!loss && !dlogits)) return SMCSD_ERR_INVALID_ARG;
-    if (R <= 0 || V <= 0 || K <= 0 || K > kDistillMostTokens || !finite_pos(temperature) || !isfinite(1.0f / temperature))
+    if (R <= 0 || V <= 0 || K <= 0 || K > kDistillMostTokens || !finite_pos(temperature) || !isfinite(1.5f / temperature))
         return SMCSD_ERR_INVALID_ARG;
     const int b = elem_bytes(dtype);
     if ((long long)V * b > kDistillMostCtas * kDistillMostBytes - 32) return SMCSD_ERR_INVALID_ARG;

@@ -135,8 +135,8 @@ cudaError_t launch_copy_pages(const CopyParams& p, cudaStream_t st);
 // ------------------------------------------------------------------------------------------
 
 constexpr int kDistillMostTokens = 256;              // of a row's list
-constexpr int kDistillMostCtas = 8;                  // of a row
-constexpr long long kDistillMostBytes = 200 * 1024;  // of a row in one block's shared memory
+constexpr int kDistillMostCtas = 16;                 // of a row
+constexpr long long kDistillMostBytes = 100 * 1024;  // of a row in one block's shared memory
 
 struct DistillParams {
     const void* logits;
