@@ -498,7 +498,7 @@ int logits_process(const void* logits, void* out, int dtype, int R, int V, int S
  * logits [G*N rows, row_stride elements apart, V used], aligned to their type; scores float [G*N] (NULL: 0);
  * finished int32 [G*N] (NULL: none); eos_token < 0: none; tokens, ancestors int32, out_scores float,
  * out_finished int32 (NULL to skip) [G*M]; out_scores and out_finished must not be scores and finished. N and
- * M are at most 256. ws: smcsd_workspace_size(SMCSD_OP_BEAM_SELECT, G*N, 0, V).
+ * M are at most 256, and a group's N rows of V logits at most 160 MB. ws: smcsd_workspace_size(SMCSD_OP_BEAM_SELECT, G*N, 0, V).
  * Device-side errors: SMCSD_ERR_NONFINITE (NaN or +inf in logits that are read, or in scores; such a beam has no candidate).
  */
 int beam_select(const void* logits, long long row_stride, int dtype, int G, int N, int V, int M,

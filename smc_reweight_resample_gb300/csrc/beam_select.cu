@@ -1,8 +1,8 @@
 // beam_select.cu -- the best continuations of every group's beams over the vocabulary.
 //
 // Candidate (beam i, token v) of a group has the score s_i + c z_iv - L_i with L_i = log sum_v exp(c z_iv), c = 1 / temperature; with
-// the row's maximum m_i that is s_i + c (z_iv - m_i) - log S_i, S_i = sum_v exp(c (z_iv - m_i)).
-// The M best of a group's N * V candidates are wanted, in the order of score, beam, token.
+// the row's maximum m_i that is s_i + c (z_iv - m_i) - log S_i, S_i = sum_v exp(c (z_iv - m_i)). The M best of a group's N * V
+// candidates are wanted, in the order of score, beam, token.
 //
 // One pass over the logits: a warp takes a chunk of 4 KB (eight 16-byte vectors a lane, loads back to back) and leaves its
 // maximum, its sum of exp(c (z - maximum)) and the maxima of its eight sets (a set: the 32 lanes' vectors of one load, 512
@@ -10,27 +10,29 @@
 // hold the M best tokens: each of these M ranges has a token that comes before any token of a range behind them. So the last
 // block of a group to finish
 //   - adds up the beams' sums, which gives every score up to the beam's own constant,
-//   - finds M (to 2 M) of the group's chunks, then M of those chunks' sets, by bisection on their maxima's scores,
+//   - finds the M (to 5/4 M + 8) best of the group's sets, where there are many of its chunks first and then of their sets, by
+//     bisection on their maxima's scores,
 //   - reads these sets again and keeps what is not below the last of them: a little more than M candidates,
 //   - ranks them by counting.
-// Scores are compared as double-floats (FP64 runs at two lanes a clock here), relative to the group's best one, in 64-bit keys
-// whose order is theirs. Of one beam this order is exact, whatever its sum; between beams it is as good as the sums: hardware
-// exponentials and float sums of 64 terms are off by at most 1.3e-6 (see kTol). Where two scores of different beams that decide
+// Scores are compared as double-floats (FP64 runs at two lanes a clock here), relative to the group's best one. Of one beam this
+// order is exact, whatever its sum; between beams it is as good as the sums (kTol). Where two scores of different beams that decide
 // anything are nearer than that, the block computes the beams' sums again in double-floats (1e-12) and selects anew.
+#include "f32x2.cuh"
 #include "ops_launch.cuh"
 #include "smcsd_launch.cuh"
 
 namespace smcsd {
 
-constexpr int kBeamThreads = 512;
-constexpr int kBeamWarps = kBeamThreads / 32;
-constexpr int kBeamKeys = 4096;  // keys of a level in shared memory
-constexpr int kBeamCands = 1024; // candidates that are ranked
+// Blocks of 512 threads for few groups, whose rows several blocks share; of 128 for many groups (a block each), so that one
+// group's selection, which is latency, goes on beside the reading of others.
+constexpr int kBeamWide = 512, kBeamNarrow = 128;
+constexpr int kBeamMostCands = 1024;  // candidates that are ranked
 
-// Bound on how far the scores of two beams may be off from one another with hardware exponentials. Of one sum, relative: the
-// exponential 2^-22, its argument's two roundings at most 2^-23 (x 2^-x has its maximum 0.53 / ln 2 there), at most 7 + 8 + 5
-// additions one after another 20 * 2^-24, the chunks' scale 2^-22 and their sum in 64 bits: 1.9e-6; two sums: 3.8e-6.
-constexpr float kTol = 4.0e-6f;
+// How far the scores of two beams may be off from one another with hardware exponentials. A sum, relative: the exponential 2^-22; its
+// argument's roundings (of z - m, of c log2 e and of their product: 2.5 * 2^-24 of it, and it is 31 on the average at most, the
+// distribution's entropy over up to 2^31 tokens), times ln 2: 3.2e-6; 8 + 3 + 1 + 5 additions one after another and 8 + 5 of
+// chunks, 2^-24 each; the chunks' scale 2^-22: 6.1e-6. Two of them: 1.2e-5.
+constexpr float kTol = 1.25e-5f;
 
 // A score as an unsigned integer of the same order: the high float first, then the low one (of a normalised double-float). 0 is
 // no score (minus infinity, NaN).
@@ -117,15 +119,10 @@ __device__ __forceinline__ float vec_max(const uint4& x) {
     const uint32_t m = max_bf16x2(max_bf16x2(x.x, x.y), max_bf16x2(x.z, x.w));
     return fmaxf(bf16_lo(m), bf16_hi(m));
 }
-__device__ __forceinline__ float ex2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // One chunk of a row: its maximum, sum and set maxima. NaN and +inf show in the sum.
 template <int DT>
-__device__ __forceinline__ void beam_chunk(const BeamParams& p, const BeamRow<DT>& b, int chunk, float2* part, float* sets, int lane) {
+__device__ __forceinline__ void beam_chunk(const BeamParams& p, const BeamRow<DT>& b, int chunk, float* maximum, float* total, float* sets, int lane) {
     constexpr int PV = Geo<DT>::kPerVec;
     uint4 x[kBeamSets];
     const int v0 = chunk * kBeamSets * 32;
@@ -146,19 +143,21 @@ __device__ __forceinline__ void beam_chunk(const BeamParams& p, const BeamRow<DT
     }
     float sum = 0.0f;
     if (m > kNegInf) {
+        const f32x2 m2 = pair(-m, -m), c2 = pair(p.c2, p.c2);
+        f32x2 sums[Vec<DT>::kPairs];
+#pragma unroll
+        for (int k = 0; k < Vec<DT>::kPairs; ++k) sums[k] = pair(0.0f, 0.0f);
 #pragma unroll
         for (int s = 0; s < kBeamSets; ++s) {
-            float f[PV];
-            unpack<DT>(x[s], f);
+            const Vec<DT> v(x[s]);
 #pragma unroll
-            for (int i = 0; i < PV; ++i) f[i] = ex2_fast((f[i] - m) * p.c2);
-#pragma unroll
-            for (int o = PV / 2; o > 0; o >>= 1)
-#pragma unroll
-                for (int i = 0; i < o; ++i) f[i] += f[i + o];
-            sum += f[0];
+            for (int k = 0; k < Vec<DT>::kPairs; ++k) sums[k] = add2(sums[k], exp2_2(mul2(add2(v.x[k], m2), c2)));
         }
-        sum = warp_sum(sum);
+#pragma unroll
+        for (int k = 1; k < Vec<DT>::kPairs; ++k) sums[0] = add2(sums[0], sums[k]);
+        float lo, hi;
+        halves(sums[0], lo, hi);
+        sum = warp_sum(lo + hi);
     } else {
         // nothing but -inf, unless there are NaN, which the maxima pass over
         bool nan = false;
@@ -172,49 +171,77 @@ __device__ __forceinline__ void beam_chunk(const BeamParams& p, const BeamRow<DT
         if (__any_sync(0xffffffffu, nan)) sum = __int_as_float(0x7fffffff);
     }
     if (lane < kBeamSets) sets[lane] = mine;
-    if (lane == 0) *part = make_float2(m, sum);
+    if (lane == 0) *maximum = m, *total = sum;
 }
 
+// A block's shared memory, sized by the call, by offsets (which keep its accesses in 32 bits).
+extern __shared__ __align__(16) char s_beam[];
 struct BeamShared {
-    double based[kBeamMostBeams];  // S_i, then s_i - log S_i: the beam's best score (of a finished beam s_i)
-    float2 base[kBeamMostBeams];   // the same, relative to the group's best score
-    float zmin[kBeamMostBeams];    // no candidate below this logit
-    float zmax[kBeamMostBeams];    // the row's maximum
-    int live[kBeamMostBeams];      // beams whose rows are read
-    int over[kBeamMostBeams];      // finished beams
-    int nlive, nover;
-    int list1[2 * kBeamMost], list2[2 * kBeamMost], order[kBeamMost + 1];
-    int count, last;
-    double ref;
-    unsigned long long reduce, fixed[2];
-    union {
-        uint64_t keys[kBeamKeys];
-        struct {
-            uint64_t key[kBeamCands];
-            uint64_t at[kBeamCands];  // beam, token
-        } cand;
-    };
+    int N, most, M, cands;
+    template <typename T>
+    __device__ __forceinline__ T* at_offset(int bytes) const {
+        return reinterpret_cast<T*>(s_beam + bytes);
+    }
+    __device__ __forceinline__ float2& sum(int i) const { return at_offset<float2>(0)[i]; }       // [N] S_i, a double-float
+    __device__ __forceinline__ float2& base(int i) const { return at_offset<float2>(8 * N)[i]; }  // [N] s_i - log S_i, the beam's best score,
+                                                                                                 // relative to the group's (of a finished beam s_i)
+    __device__ __forceinline__ float& zmax(int i) const { return at_offset<float>(16 * N)[i]; }   // [N] the row's maximum
+    __device__ __forceinline__ float& zmin(int i) const { return at_offset<float>(20 * N)[i]; }   // [N] no candidate below this logit
+    __device__ __forceinline__ int& live(int i) const { return at_offset<int>(24 * N)[i]; }       // [N] beams whose rows are read
+    __device__ __forceinline__ int& over(int i) const { return at_offset<int>(28 * N)[i]; }       // [N] finished beams
+    __device__ __forceinline__ int* list1() const { return at_offset<int>(32 * N); }              // [most] chunks
+    __device__ __forceinline__ int* list2() const { return at_offset<int>(32 * N + 4 * most); }   // [most] sets
+    __device__ __forceinline__ int& order(int i) const { return at_offset<int>(32 * N + 8 * most)[i]; }  // [M + 1]
+    __host__ __device__ __forceinline__ int tail() const { return (32 * N + 8 * most + 4 * (M + 1) + 15) & ~15; }
+    __device__ __forceinline__ float& score(int i) const { return at_offset<float>(tail())[i]; }  // [keys] maxima, then their scores; shares its
+                                                                                                 // memory with the candidates
+    __device__ __forceinline__ uint64_t& key(int i) const { return at_offset<uint64_t>(tail())[i]; }             // [cands + N]
+    __device__ __forceinline__ uint64_t& at(int i) const { return at_offset<uint64_t>(tail())[cands + N + i]; }  // [cands + N] beam, token
 };
-static_assert(sizeof(BeamShared) <= 48 * 1024, "static shared memory");
-
-__device__ __forceinline__ int count_from(const uint64_t* keys, int n, uint64_t from) {
-    int c = 0;
-    for (int i = threadIdx.x; i - (int)threadIdx.x < n; i += kBeamThreads) c += __syncthreads_count(i < n && keys[i] >= from);
-    return c;
+struct BeamCounts {
+    int nlive, nover, count, last;
+    int votes[4];
+    dd ref;  // the best score of the group
+    unsigned long long reduce, fixed[2];
+};
+__host__ __device__ inline BeamShared beam_shared(int N, int M) {
+    return BeamShared{N, M + M / 4 + 8, M, 4 * M + 64 < kBeamMostCands ? 4 * M + 64 : kBeamMostCands};
 }
-// What is kept of n keys: those above K, and those equal to K before place I; between M and `most` of them, the first in the
-// order of keys and places (all that are not 0 if they are no more than `most`).
+// Scores of a level: of the sets of all chunks kept, and of all chunks; of all sets where those are not many more.
+__host__ __device__ inline int beam_keys(const BeamShared& s, int chunks, int threads) {
+    int n = kBeamSets * s.most;
+    const int some = threads == kBeamWide ? 4096 : 1024;
+    if (n < some) n = some;
+    return n < chunks ? chunks : n;
+}
+inline size_t beam_shared_bytes(int N, int M, int chunks, int threads) {
+    const BeamShared s = beam_shared(N, M);
+    const size_t keys = 4 * (size_t)beam_keys(s, chunks, threads), cands = 16 * (size_t)(s.cands + N);
+    return (size_t)s.tail() + (keys > cands ? keys : cands);
+}
+
+constexpr float kLowest = -3.402823466e38f;
+
+// What is kept of a level's n items: those whose key is above K, and those with K before place I.
 struct Cut {
     uint64_t K;
     int I;
 };
 __device__ __forceinline__ bool kept(const Cut& c, uint64_t key, int i) { return key > c.K || (key == c.K && i < c.I); }
-__device__ Cut find_cut(const uint64_t* keys, int n, int M, int most) {
-    if (count_from(keys, n, 1) <= most) return Cut{0, 0};
+
+// Keys by bisection of their bits and then of their places, for levels whose scores differ too little for find_cut: between M and
+// `most` of them, the first in the order of keys and places. There are more than `most`.
+template <int TH, typename F>
+__device__ __noinline__ Cut find_cut_exact(int n, int M, int most, F key_of) {
+    const auto count = [&](uint64_t K, int I) {
+        int c = 0;
+        for (int i = threadIdx.x; i - (int)threadIdx.x < n; i += TH) c += __syncthreads_count(i < n && kept(Cut{K, I}, key_of(i), i));
+        return c;
+    };
     uint64_t lo = 1, hi = ~0ull;  // more than `most` from lo on, fewer than M from hi on
     while (hi - lo > 1) {
         const uint64_t mid = lo + (hi - lo) / 2;
-        const int c = count_from(keys, n, mid);
+        const int c = count(mid, n);
         if (c > most)
             lo = mid;
         else if (c < M)
@@ -222,12 +249,9 @@ __device__ Cut find_cut(const uint64_t* keys, int n, int M, int most) {
         else
             return Cut{mid, n};
     }
-    // many are equal to lo: the first places of them
-    int a = 0, b = n;
+    int a = 0, b = n;  // many are equal to lo: the first places of them
     while (b - a > 1) {
-        const int mid = a + (b - a) / 2;
-        int c = 0;
-        for (int i = threadIdx.x; i - (int)threadIdx.x < n; i += kBeamThreads) c += __syncthreads_count(i < n && kept(Cut{lo, mid}, keys[i], i));
+        const int mid = a + (b - a) / 2, c = count(lo, mid);
         if (c < M)
             a = mid;
         else if (c > most)
@@ -238,46 +262,162 @@ __device__ Cut find_cut(const uint64_t* keys, int n, int M, int most) {
     return Cut{lo, b};
 }
 
-// The places of what is kept, ascending, in `list`; returns how many.
-__device__ int gather_kept(BeamShared& s, const uint64_t* keys, int n, const Cut& cut, int* list) {
+// A score from which on there are between M and `most` of the n scores (relative to the best, so at most 0): a bisection of values,
+// since the M best are mostly within a few units of the best. Fails where ties, or scores next to the best, leave none.
+template <int TH>
+__device__ __forceinline__ bool find_cut(const BeamShared& s, BeamCounts& c, int n, int M, int most, float& from) {
+    float above = 1.0f, below = kNegInf;  // fewer than M from `above` on; more than `most` from `below` on
+    from = -1.0f;
+    for (int turn = 0; turn < 28; ++turn) {
+        int mine = 0;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += TH) mine += s.score(i) >= from;
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if ((threadIdx.x & 31) == 0 && mine) atomicAdd(&c.votes[turn & 3], mine);
+        __syncthreads();
+        const int got = c.votes[turn & 3];
+        if (threadIdx.x == 0) c.votes[(turn + 2) & 3] = 0;  // all have read it by the last barrier
+        if (got > most)
+            below = from;
+        else if (got < M)
+            above = from;
+        else
+            return true;
+        const float next = below == kNegInf ? (turn < 8 ? from * 2.0f : from * 65536.0f) : 0.5f * (fminf(above, 0.0f) + below);
+        if (!(next > kNegInf) || next == from) break;
+        from = next;
+    }
+    return false;
+}
+template <int TH>
+__device__ __forceinline__ void clear_votes(BeamCounts& c) {
     __syncthreads();
-    if (threadIdx.x == 0) s.count = 0;
+    if (threadIdx.x < 4) c.votes[threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kBeamThreads)
-        if (kept(cut, keys[i], i)) {
-            const int k = atomicAdd(&s.count, 1);
-            if (k < 2 * kBeamMost) list[k] = i;
-        }
-    __syncthreads();
-    const int got = min(s.count, 2 * kBeamMost);
-    // by counting: the list is short
-    int mine[2 * kBeamMost / kBeamThreads], rank[2 * kBeamMost / kBeamThreads];
+}
+
+// Puts a short list of distinct places in ascending order.
+template <int TH>
+__device__ void sort_list(int* list, int n) {
+    constexpr int kEach = (kBeamMost + kBeamMost / 4 + 8 + TH - 1) / TH;
+    int mine[kEach], rank[kEach];
 #pragma unroll
-    for (int t = 0; t < 2 * kBeamMost / kBeamThreads; ++t) {
-        const int i = threadIdx.x + t * kBeamThreads;
+    for (int t = 0; t < kEach; ++t) {
+        const int i = threadIdx.x + t * TH;
         rank[t] = 0;
-        if (i < got) {
+        if (i < n) {
             mine[t] = list[i];
-            for (int j = 0; j < got; ++j) rank[t] += list[j] < mine[t];
+            for (int j = 0; j < n; ++j) rank[t] += list[j] < mine[t];
         }
     }
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < 2 * kBeamMost / kBeamThreads; ++t)
-        if ((int)threadIdx.x + t * kBeamThreads < got) list[rank[t]] = mine[t];
+    for (int t = 0; t < kEach; ++t)
+        if ((int)threadIdx.x + t * TH < n) list[rank[t]] = mine[t];
     __syncthreads();
-    return got;
+}
+
+// The level that is looked at first: all sets of the group's live beams where they are few, else all their chunks.
+struct FirstLevel {
+    const float* z_;  // maxima of the group's rows
+    int per, n, log;  // items of a row, of the live rows; log2 of the items of a chunk
+    FastDiv chunks;   // by the chunks of a row
+    __device__ __forceinline__ int beam(const BeamShared& s, int i) const { return s.live((int)fast_div((uint32_t)i >> log, chunks)); }
+    __device__ __forceinline__ float z(const BeamShared& s, int i) const {
+        const int l = (int)fast_div((uint32_t)i >> log, chunks);
+        return __ldcg(z_ + (long long)s.live(l) * per + (i - l * per));
+    }
+};
+template <int TH>
+__device__ __forceinline__ FirstLevel first_level(const BeamParams& p, const BeamShared& s, int g, int nlive) {
+    FirstLevel v;
+    v.log = nlive * p.cpr <= beam_keys(s, p.N * p.cpr, TH) / kBeamSets ? 3 : 0;
+    static_assert(kBeamSets == 8, "shifts by 3");
+    v.chunks = p.div_cpr;
+    v.per = p.cpr << v.log;
+    v.n = nlive * v.per;
+    v.z_ = ws_ptr<const float>(p.ws, v.log ? p.sets : p.maxima) + (long long)g * p.N * v.per;
+    return v;
+}
+// The sets of the chunks in list1.
+struct SecondLevel {
+    const float* z_;
+    int cpr;
+    FastDiv chunks;
+    __device__ __forceinline__ int beam(const BeamShared& s, int i) const { return s.live((int)fast_div((uint32_t)s.list1()[i / kBeamSets], chunks)); }
+    __device__ __forceinline__ float z(const BeamShared& s, int i) const {
+        const int chunk = s.list1()[i / kBeamSets], l = (int)fast_div((uint32_t)chunk, chunks);
+        return __ldcg(z_ + ((long long)s.live(l) * cpr + (chunk - l * cpr)) * kBeamSets + i % kBeamSets);
+    }
+};
+// Keys of a level's items, for what is not done as a rule.
+template <typename L>
+struct LevelKey {
+    const BeamParams* p;
+    BeamShared s;
+    L level;
+    __device__ __forceinline__ uint64_t operator()(int i) const {
+        const int beam = level.beam(s, i);
+        return score_key(*p, level.z(s, i), s.zmax(beam), s.base(beam));
+    }
+};
+// An item's score: in float32, off by at most three roundings, 1.8e-7 of it (both terms are negative), and for one beam in the order of
+// the logits; or as the high half of its key.
+constexpr float kScoreError = 3e-7f;
+template <typename L>
+__device__ __forceinline__ float level_score(const BeamParams& p, const BeamShared& s, const L& level, int i, float z, bool exact) {
+    const int beam = level.beam(s, i);
+    if (!exact) return z > kNegInf ? fmaf(p.c_hi, z - s.zmax(beam), s.base(beam).x) : kNegInf;
+    const uint64_t key = score_key(p, z, s.zmax(beam), s.base(beam));
+    return key ? float_of_order((uint32_t)(key >> 32)) : kNegInf;
+}
+
+// The places of a level's n items that hold the group's M best tokens, in `list`; returns how many. All that are there, if they are
+// no more than `most`. `floor`: a score, up to kScoreError; no item below it has been kept.
+template <int TH, typename L>
+__device__ __forceinline__ int choose(const BeamParams& p, const BeamShared& s, BeamCounts& c, int n, const L& level, int* list,
+                                      float& floor, bool& by_place) {
+    const int most = s.most;
+    float from = kLowest;
+    Cut cut{0, n};
+    by_place = false;
+    clear_votes<TH>(c);
+    bool ok = n <= most;
+    if (!ok) {
+        ok = find_cut<TH>(s, c, n, p.M, most, from);
+        if (!ok) {
+            int some = 0;
+            for (int i = threadIdx.x; i - (int)threadIdx.x < n; i += TH) some += __syncthreads_count(i < n && s.score(i) > kNegInf);
+            ok = some <= most;  // fewer than M perhaps: all of them
+            from = kLowest;
+            if (!ok) {
+                cut = find_cut_exact<TH>(n, p.M, most, LevelKey<L>{&p, s, level});
+                by_place = cut.I < n;
+            }
+        }
+    }
+    floor = fmaxf(floor, ok ? from : key_value(cut.K).hi);
+    __syncthreads();
+    if (threadIdx.x == 0) c.count = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += TH)
+        if (ok ? s.score(i) >= from : kept(cut, LevelKey<L>{&p, s, level}(i), i)) {
+            const int k = atomicAdd(&c.count, 1);
+            if (k < most) list[k] = i;
+        }
+    __syncthreads();
+    return min(c.count, most);
 }
 
 // Sum of exp(c (z - m)) over row b by the whole block: every term from double-floats, rounded to a multiple of 2^-56 and added up
 // in integers, so that rows with the same logits have the same sum however they lie in memory. Off by at most 2^-57 a term and
 // 1e-13 of it.
-template <int DT>
-__device__ double precise_sum(const BeamParams& p, BeamShared& s, const BeamRow<DT>& b, float m) {
+template <int DT, int TH>
+__device__ __noinline__ dd precise_sum(const BeamParams& p, BeamCounts& c, BeamRow<DT> b, float m) {
     constexpr int PV = Geo<DT>::kPerVec;
     const int vecs = (int)(((long long)b.V + b.shift + PV - 1) / PV);
     unsigned __int128 acc = 0;
-    for (int v = threadIdx.x; v < vecs; v += kBeamThreads) {
+    for (int v = threadIdx.x; v < vecs; v += TH) {
         float f[PV];
         unpack<DT>(beam_vec<DT>(b, v), f);
 #pragma unroll 1
@@ -290,45 +430,24 @@ __device__ double precise_sum(const BeamParams& p, BeamShared& s, const BeamRow<
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) s.fixed[0] = s.fixed[1] = 0;
+    if (threadIdx.x == 0) c.fixed[0] = c.fixed[1] = 0;
     __syncthreads();
     // in units of 2^-56 and 2^-24: both stay below 2^63 with 2^31 terms
-    atomicAdd(&s.fixed[0], (unsigned long long)acc & 0xffffffffull);
-    atomicAdd(&s.fixed[1], (unsigned long long)(acc >> 32));
+    atomicAdd(&c.fixed[0], (unsigned long long)acc & 0xffffffffull);
+    atomicAdd(&c.fixed[1], (unsigned long long)(acc >> 32));
     __syncthreads();
-    return ldexp((double)s.fixed[1], -24) + ldexp((double)s.fixed[0], -56);
+    const double sum = ldexp((double)c.fixed[1], -24) + ldexp((double)c.fixed[0], -56);
+    const float hi = (float)sum;
+    return dd{hi, (float)(sum - (double)hi)};
 }
 
-// Calls f(key, beam, token) for every token of the sets in list2 whose logit is not below its beam's zmin.
-template <int DT, typename F>
-__device__ __forceinline__ void scan_sets(const BeamParams& p, BeamShared& s, int g, int n2, F&& f) {
-    constexpr int PV = Geo<DT>::kPerVec;
-    const int lane = threadIdx.x & 31, per = p.cpr * kBeamSets;
-    for (int i = threadIdx.x >> 5; i < n2; i += kBeamWarps) {
-        const int set = s.list2[i], l = set / per, beam = s.live[l], v = (set - l * per) * 32 + lane;
-        const BeamRow<DT> b = beam_row<DT>(p, (long long)g * p.N + beam);
-        float z[PV];
-        unpack<DT>(beam_vec<DT>(b, v), z);
-        const float zmin = s.zmin[beam], m = s.zmax[beam];
-        const float2 base = s.base[beam];
-#pragma unroll
-        for (int e = 0; e < PV; ++e)
-            if (z[e] >= zmin) {
-                const uint64_t key = score_key(p, z[e], m, base);
-                if (key) f(key, beam, (int)((long long)v * PV + e - b.shift));
-            }
-    }
-}
-
-// Adds up one count a thread.
-__device__ __forceinline__ unsigned long long block_total(BeamShared& s, unsigned mine) {
-    __syncthreads();
-    if (threadIdx.x == 0) s.reduce = 0;
-    __syncthreads();
-    const unsigned w = __reduce_add_sync(0xffffffffu, mine);
-    if ((threadIdx.x & 31) == 0 && w) atomicAdd(&s.reduce, (unsigned long long)w);
-    __syncthreads();
-    return s.reduce;
+// log of a positive double-float: one step of Newton's method from the float logarithm, in double-floats.
+__device__ __forceinline__ dd dd_log(dd v, const Exp2Table& T) {
+    const float y = logf(v.hi);
+    const ddx e = exp_split(dd{-y, 0.0f}, T);
+    const float u = pow2i(e.n);  // v is at most 2^31
+    const dd r = dd_add(dd_mul(v, dd{e.hi * u, e.lo * u}), dd{-1.0f, 0.0f});
+    return dd_add(dd{y, 0.0f}, dd_add(r, dd{-0.5f * r.hi * r.hi, 0.0f}));
 }
 
 // Candidates by beam and token; kEnded stands for the token of a finished beam.
@@ -338,163 +457,236 @@ __device__ __forceinline__ float start_score(const BeamParams& p, int g, int bea
     return p.scores ? __ldg(p.scores + (long long)g * p.N + beam) : 0.0f;
 }
 
-// Fills s.cand with the candidates that can be among the first M; returns how many, and in `floor` the key below which
-// candidates were left out (0: none were).
-template <int DT>
-__device__ int collect(const BeamParams& p, BeamShared& s, int g, uint64_t& floor) {
-    const int M = p.M, most = min(2 * M, M + 64), nlive = s.nlive;
-    const float2* part = ws_ptr<const float2>(p.ws, p.part) + (long long)g * p.N * p.cpr;
-    const float* sets = ws_ptr<const float>(p.ws, p.sets) + (long long)g * p.N * p.cpr * kBeamSets;
-    const int n = nlive * p.cpr;
-    uint64_t* keys = n <= kBeamKeys ? s.keys : ws_ptr<uint64_t>(p.ws, p.keys) + (long long)g * p.N * p.cpr;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kBeamThreads) {
-        const int l = i / p.cpr, beam = s.live[l];
-        keys[i] = score_key(p, __ldcg(part + beam * p.cpr + (i - l * p.cpr)).x, s.zmax[beam], s.base[beam]);
-    }
-    __syncthreads();
-    const Cut c1 = find_cut(keys, n, M, most);
-    const int n1 = gather_kept(s, keys, n, c1, s.list1);
-    for (int i = threadIdx.x; i < n1 * kBeamSets; i += kBeamThreads) {
-        const int chunk = s.list1[i / kBeamSets], l = chunk / p.cpr, beam = s.live[l];
-        s.keys[i] = score_key(p, __ldcg(sets + ((long long)beam * p.cpr + (chunk - l * p.cpr)) * kBeamSets + i % kBeamSets),
-                              s.zmax[beam], s.base[beam]);
-    }
-    __syncthreads();
-    const Cut c2 = find_cut(s.keys, n1 * kBeamSets, M, most);
-    const int n2 = gather_kept(s, s.keys, n1 * kBeamSets, c2, s.list2);
-    // places in list1 to sets of the group's live beams
-    for (int i = threadIdx.x; i < n2; i += kBeamThreads) s.list2[i] = s.list1[s.list2[i] / kBeamSets] * kBeamSets + s.list2[i] % kBeamSets;
-    floor = c1.K > c2.K ? c1.K : c2.K;
-    // the floor as a logit of each live beam, lowered by more than its rounding
-    const float at = floor ? key_value(floor).hi : kNegInf;
-    for (int l = threadIdx.x; l < nlive; l += kBeamThreads) {
-        const int beam = s.live[l];
-        const float b = s.base[beam].x, m = s.zmax[beam], z = m + (at - b) / p.c_hi;
-        s.zmin[beam] = floor ? z - (fabsf(m) + (fabsf(at) + fabsf(b)) / p.c_hi) * 1e-6f - 1e-35f : -3.402823466e38f;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) s.count = 0;
-    __syncthreads();
-    const int room = kBeamCands - s.nover;
-    uint64_t K = floor, I = ~0ull;  // kept: keys above K, and those equal to K up to place I
-    scan_sets<DT>(p, s, g, n2, [&](uint64_t key, int beam, int token) {
-        if (key >= K) {
-            const int k = atomicAdd(&s.count, 1);
-            if (k < room) s.cand.key[k] = key, s.cand.at[k] = place_of(beam, token);
+// Calls f(logit, beam, token) for every token of the sets in list2 whose logit is not below its beam's zmin. A warp takes four sets
+// at a time, so that their loads are on the way together.
+template <int DT, int TH, typename F>
+__device__ __forceinline__ void scan_sets(const BeamParams& p, const BeamShared& s, int g, int n2, F&& f) {
+    constexpr int PV = Geo<DT>::kPerVec, kEach = 4, kWarps = TH / 32;
+    const int lane = threadIdx.x & 31, per = p.cpr * kBeamSets;
+    for (int i0 = threadIdx.x >> 5; i0 < n2; i0 += kEach * kWarps) {
+        uint4 x[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = i0 + k * kWarps;
+            if (i >= n2) break;
+            const int set = s.list2()[i], l = (int)fast_div((uint32_t)set / kBeamSets, p.div_cpr);
+            x[k] = beam_vec<DT>(beam_row<DT>(p, (long long)g * p.N + s.live(l)), (set - l * per) * 32 + lane);
         }
-    });
-    __syncthreads();
-    if (s.count > room) {
-        // many tokens next to one another in the order: bisection over the tokens themselves
-        uint64_t lo = K, hi = ~0ull;
-        bool found = false;
-        auto total = [&](uint64_t k, uint64_t i) {
-            unsigned mine = 0;
-            scan_sets<DT>(p, s, g, n2, [&](uint64_t key, int beam, int token) { mine += key > k || (key == k && place_of(beam, token) <= i); });
-            return block_total(s, mine);
-        };
-        while (hi - lo > 1 && !found) {
-            const uint64_t mid = lo + (hi - lo) / 2;
-            const unsigned long long c = total(mid, ~0ull);
-            if (c > (unsigned)room)
-                lo = mid;
-            else if (c < (unsigned)M)
-                hi = mid;
-            else
-                K = mid, found = true;
-        }
-        if (!found) {
-            K = lo;
-            uint64_t a = 0, b = place_of(p.N, 0);
-            I = b;
-            while (b - a > 1) {
-                const uint64_t mid = a + (b - a) / 2;
-                const unsigned long long c = total(K, mid);
-                if (c < (unsigned)M) {
-                    a = mid;
-                } else {
-                    b = I = mid;
-                    if (c <= (unsigned)room) break;
-                }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = i0 + k * kWarps;
+            if (i >= n2) break;
+            const int set = s.list2()[i], l = (int)fast_div((uint32_t)set / kBeamSets, p.div_cpr), beam = s.live(l);
+            const float zmin = s.zmin(beam);
+            float z[PV];
+            unpack<DT>(x[k], z);
+            unsigned hits = 0;
+#pragma unroll
+            for (int e = 0; e < PV; ++e) hits |= z[e] >= zmin ? 1u << e : 0u;
+            if (hits) {
+                const int v = (set - l * per) * 32 + lane, shift = beam_row<DT>(p, (long long)g * p.N + beam).shift;
+                do {
+                    const int e = __ffs(hits) - 1, w = DT == 0 ? e : e >> 1;
+                    hits &= hits - 1;
+                    const uint32_t word = w & 2 ? (w & 1 ? x[k].w : x[k].z) : (w & 1 ? x[k].y : x[k].x);
+                    f(bits_to_float<DT>(DT == 0 ? word : (word >> (16 * (e & 1))) & 0xffffu), beam, (int)((long long)v * PV + e - shift));
+                } while (hits);
             }
         }
-        floor = K;
+    }
+}
+
+// Adds up one count a thread.
+__device__ __forceinline__ unsigned long long block_total(BeamCounts& c, unsigned mine) {
+    __syncthreads();
+    if (threadIdx.x == 0) c.reduce = 0;
+    __syncthreads();
+    const unsigned w = __reduce_add_sync(0xffffffffu, mine);
+    if ((threadIdx.x & 31) == 0 && w) atomicAdd(&c.reduce, (unsigned long long)w);
+    __syncthreads();
+    return c.reduce;
+}
+
+// More candidates than can be ranked, as where many tokens lie next to one another in the order: K and I so that those with a key
+// above K, or with K and a place up to I, are at least M and no more than s.cands.
+template <int DT, int TH>
+__device__ __noinline__ void narrow_tokens(const BeamParams& p, BeamShared s, BeamCounts& c, int g, int n2, uint64_t* K, uint64_t* I) {
+    const unsigned room = s.cands, M = p.M;
+    uint64_t lo = *K, hi = ~0ull;
+    const auto total = [&](uint64_t k, uint64_t i) {
+        unsigned mine = 0;
+        scan_sets<DT, TH>(p, s, g, n2, [&](float z, int beam, int token) {
+            const uint64_t key = score_key(p, z, s.zmax(beam), s.base(beam));
+            mine += key > k || (key == k && place_of(beam, token) <= i);
+        });
+        return block_total(c, mine);
+    };
+    while (hi - lo > 1) {
+        const uint64_t mid = lo + (hi - lo) / 2;
+        const unsigned long long n = total(mid, ~0ull);
+        if (n > room) {
+            lo = mid;
+        } else if (n < M) {
+            hi = mid;
+        } else {
+            *K = mid;
+            return;
+        }
+    }
+    *K = lo;
+    uint64_t a = 0, b = place_of(p.N, 0);
+    while (b - a > 1) {
+        const uint64_t mid = a + (b - a) / 2;
+        const unsigned long long n = total(lo, mid);
+        if (n < M) {
+            a = mid;
+        } else {
+            b = mid;
+            if (n <= room) break;
+        }
+    }
+    *I = b;
+}
+
+// Fills s.key, s.at with the candidates that can be among the first M; returns how many, and in `floor` the score below which
+// candidates were left out (kLowest: none were). In a first turn the first level's maxima have been fetched to its scores, and
+// scores are float32; in a second one they are exact.
+template <int DT, int TH>
+__device__ __forceinline__ int collect(const BeamParams& p, const BeamShared& s, BeamCounts& c, int g, bool exact, float& floor) {
+    const int nlive = c.nlive;
+    const FirstLevel v = first_level<TH>(p, s, g, nlive);
+    for (int i = threadIdx.x; i < v.n; i += TH)  // each by the thread that fetched it
+        s.score(i) = level_score(p, s, v, i, exact ? v.z(s, i) : s.score(i), exact);
+    floor = kLowest;
+    bool by_place;
+    int n1 = choose<TH>(p, s, c, v.n, v, v.log ? s.list2() : s.list1(), floor, by_place), n2 = n1;
+    if (!v.log) {
+        const SecondLevel w{ws_ptr<const float>(p.ws, p.sets) + (long long)g * p.N * p.cpr * kBeamSets, p.cpr, p.div_cpr};
+        const float floor1 = floor;
+        for (int turn = 0; turn < 2; ++turn) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < n1 * kBeamSets; i += TH) s.score(i) = level_score(p, s, w, i, w.z(s, i), exact);
+            floor = floor1;
+            n2 = choose<TH>(p, s, c, n1 * kBeamSets, w, s.list2(), floor, by_place);
+            if (!by_place || turn == 1) break;
+            // sets are chosen by their places, which follow the chunks'
+            __syncthreads();
+            sort_list<TH>(s.list1(), n1);
+        }
+        // places in list1 to sets of the group's live beams
         __syncthreads();
-        if (threadIdx.x == 0) s.count = 0;
+        for (int i = threadIdx.x; i < n2; i += TH) s.list2()[i] = s.list1()[s.list2()[i] / kBeamSets] * kBeamSets + s.list2()[i] % kBeamSets;
+    }
+    // the floor as a logit of each live beam, lowered by more than its roundings
+    for (int l = threadIdx.x; l < nlive; l += TH) {
+        const int beam = s.live(l);
+        const float b = s.base(beam).x, m = s.zmax(beam), z = m + (floor - b) / p.c_hi;
+        s.zmin(beam) = floor > kLowest ? fmaxf(z - (fabsf(m) + (fabsf(floor) + fabsf(b)) / p.c_hi) * 1e-6f - 1e-35f, kLowest) : kLowest;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) c.count = 0;
+    __syncthreads();
+    const int room = s.cands;
+    scan_sets<DT, TH>(p, s, g, n2, [&](float z, int beam, int token) {
+        const int k = atomicAdd(&c.count, 1);
+        if (k < room) s.key(k) = __float_as_uint(z), s.at(k) = place_of(beam, token);
+    });
+    __syncthreads();
+    if (c.count <= room) {
+        for (int i = threadIdx.x; i < c.count; i += TH) {
+            const int beam = (int)(s.at(i) >> 32);
+            s.key(i) = score_key(p, __uint_as_float((uint32_t)s.key(i)), s.zmax(beam), s.base(beam));
+        }
+    } else {
+        uint64_t K = 1, I = ~0ull;  // kept: keys above K, and those equal to K up to place I
+        narrow_tokens<DT, TH>(p, s, c, g, n2, &K, &I);
+        floor = key_value(K).hi;
         __syncthreads();
-        scan_sets<DT>(p, s, g, n2, [&](uint64_t key, int beam, int token) {
+        if (threadIdx.x == 0) c.count = 0;
+        __syncthreads();
+        scan_sets<DT, TH>(p, s, g, n2, [&](float z, int beam, int token) {
+            const uint64_t key = score_key(p, z, s.zmax(beam), s.base(beam));
             if (key > K || (key == K && place_of(beam, token) <= I)) {
-                const int k = atomicAdd(&s.count, 1);
-                if (k < room) s.cand.key[k] = key, s.cand.at[k] = place_of(beam, token);
+                const int k = atomicAdd(&c.count, 1);
+                if (k < room) s.key(k) = key, s.at(k) = place_of(beam, token);
             }
         });
         __syncthreads();
     }
-    const int got = min(s.count, room);
-    for (int i = threadIdx.x; i < s.nover; i += kBeamThreads) {
-        const int beam = s.over[i];
-        s.cand.key[got + i] = key_of(dd{s.base[beam].x, s.base[beam].y});
-        s.cand.at[got + i] = place_of(beam, kEnded);
+    const int got = min(c.count, room);
+    for (int i = threadIdx.x; i < c.nover; i += TH) {
+        const int beam = s.over(i);
+        s.key(got + i) = key_of(dd{s.base(beam).x, s.base(beam).y});
+        s.at(got + i) = place_of(beam, kEnded);
     }
     __syncthreads();
-    return got + s.nover;
+    return got + c.nover;
 }
 
 // Ranks the candidates: s.order holds the first M (and one more, if there is one). Whether scores of different beams that
 // decide about this order are nearer than the sums are good for.
-__device__ bool rank_and_doubt(const BeamParams& p, BeamShared& s, int n, uint64_t floor) {
-    for (int i = threadIdx.x; i < n; i += kBeamThreads) {
-        const uint64_t key = s.cand.key[i], at = s.cand.at[i];
+template <int TH>
+__device__ __forceinline__ bool rank_and_doubt(const BeamParams& p, const BeamShared& s, const BeamCounts& c, int n, float floor) {
+    for (int i = threadIdx.x; i < n; i += TH) {
+        const uint64_t key = s.key(i), at = s.at(i);
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += s.cand.key[j] > key || (s.cand.key[j] == key && s.cand.at[j] < at);
-        if (rank <= p.M) s.order[rank] = i;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) rank += s.key(j) > key || (s.key(j) == key && s.at(j) < at);
+        if (rank <= p.M) s.order(rank) = i;
     }
     __syncthreads();
+    if (c.nlive + c.nover <= 1) return false;
     bool doubt = false;
-    auto near = [&](int i, int j) {
-        const uint64_t a = s.cand.at[i], b = s.cand.at[j];
+    const auto near = [&](int i, int j) {
+        const uint64_t a = s.at(i), b = s.at(j);
         if (a >> 32 == b >> 32 || ((int)(uint32_t)a == kEnded && (int)(uint32_t)b == kEnded)) return false;  // of one beam; exact
-        const dd d = dd_sub(key_value(s.cand.key[i]), key_value(s.cand.key[j]));
+        const dd d = dd_sub(key_value(s.key(i)), key_value(s.key(j)));
         return fabsf(d.hi) <= kTol;
     };
     const int m = min(p.M, n);
-    for (int r = threadIdx.x; r < m && r + 1 < n; r += kBeamThreads) doubt |= near(s.order[r], s.order[r + 1]);
+    for (int r = threadIdx.x; r < m && r + 1 < n; r += TH) doubt |= near(s.order(r), s.order(r + 1));
     if (n > p.M) {  // what is next to the last one, on either side, in any beam
-        const int last = s.order[p.M - 1];
-        for (int i = threadIdx.x; i < n; i += kBeamThreads) doubt |= near(i, last);
+        const int last = s.order(p.M - 1);
+        for (int i = threadIdx.x; i < n; i += TH) doubt |= near(i, last);
     }
-    if (floor && n >= p.M && s.nlive + s.nover > 1) {  // and what was left out
-        // (a bisection's key need not be one of a double-float: its high half is as near as that half's last place)
-        const float f = key_value(floor).hi;
-        doubt |= key_value(s.cand.key[s.order[p.M - 1]]).hi - f <= kTol + 2.4e-7f * fabsf(f);
-    }
+    if (floor > kLowest && n >= p.M)  // and what was left out
+        doubt |= key_value(s.key(s.order(p.M - 1))).hi - floor <= kTol + 2.0f * kScoreError * fabsf(floor);
     return __syncthreads_or(doubt);
 }
 
 // The group's selection, by the last block of the group.
-template <int DT>
-__device__ void beam_finish(const BeamParams& p, BeamShared& s, int g) {
+template <int DT, int TH>
+__device__ __forceinline__ void beam_finish(const BeamParams& p, const BeamShared& s, BeamCounts& c, int g) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float2* part = ws_ptr<const float2>(p.ws, p.part) + (long long)g * p.N * p.cpr;
+    const long long rows = (long long)g * p.N;
+    {   // the first level's maxima, for which nothing has to be known yet
+        const FirstLevel v = first_level<TH>(p, s, g, c.nlive);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < v.n; i += TH) s.score(i) = v.z(s, i);
+    }
     // a warp a beam: maximum and sum of its chunks
-    for (int l = warp; l < s.nlive; l += kBeamWarps) {
-        const float2* q = part + (long long)s.live[l] * p.cpr;
-        float m = kNegInf;
-        for (int k = lane; k < p.cpr; k += 32) m = fmaxf(m, __ldcg(q + k).x);
-        m = warp_max(m);
-        double sum = 0.0;
-        for (int k = lane; k < p.cpr; k += 32) {
-            const float2 x = __ldcg(q + k);
-            if (x.x > kNegInf)
-                sum += (double)(x.y * exp2f((x.x - m) * p.c2));
-            else if (x.y != x.y)
-                sum += (double)x.y;
+    for (int l = warp; l < c.nlive; l += TH / 32) {
+        const int beam = s.live(l);
+        const float* qm = ws_ptr<const float>(p.ws, p.maxima) + (rows + beam) * p.cpr;
+        const float* qs = ws_ptr<const float>(p.ws, p.sums) + (rows + beam) * p.cpr;
+        float m = kNegInf, sum = 0.0f, first[3][2];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const bool in = k * 32 + lane < p.cpr;
+            first[k][0] = in ? __ldcg(qm + k * 32 + lane) : kNegInf;
+            first[k][1] = in ? __ldcg(qs + k * 32 + lane) : 0.0f;
+            m = fmaxf(m, first[k][0]);
         }
-        sum = warp_sum_d(sum);
+        for (int k = 96 + lane; k < p.cpr; k += 32) m = fmaxf(m, __ldcg(qm + k));
+        m = warp_max(m);
+        const auto part = [&](float km, float ks) { return km > kNegInf ? ks * exp2f((km - m) * p.c2) : ks; };  // of -inf: 0, or NaN
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sum += part(first[k][0], first[k][1]);
+        for (int k = 96 + lane; k < p.cpr; k += 32) sum += part(__ldcg(qm + k), __ldcg(qs + k));
+        sum = warp_sum(sum);
         if (lane == 0) {
-            s.zmax[s.live[l]] = m;
-            s.based[s.live[l]] = sum;
+            s.zmax(beam) = m;
+            s.sum(beam) = make_float2(sum, 0.0f);
         }
     }
     __syncthreads();
@@ -502,62 +694,66 @@ __device__ void beam_finish(const BeamParams& p, BeamShared& s, int g) {
     int n;
     for (;;) {
         // the beams' constants: scores are c (z - m) + base
-        for (int l = threadIdx.x; l < s.nlive; l += kBeamThreads) {
-            const int beam = s.live[l];
-            const double sum = s.based[beam];
-            const float m = s.zmax[beam];
-            double base = (double)kNegInf;
-            if (!(sum < (double)kPosInf) || m == kPosInf)
+        for (int l = threadIdx.x; l < c.nlive; l += TH) {
+            const int beam = s.live(l);
+            const dd sum{s.sum(beam).x, s.sum(beam).y};
+            dd base{kNegInf, 0.0f};
+            if (!(sum.hi < kPosInf) || s.zmax(beam) == kPosInf)
                 raise_error(p.ws, kErrNonfinite);
-            else if (sum > 0.0)
-                base = (double)start_score(p, g, beam) - log(sum);
-            s.based[beam] = base;
+            else if (sum.hi > 0.0f)
+                base = dd_sub(dd{start_score(p, g, beam), 0.0f}, dd_log(sum, p.T));
+            s.base(beam) = make_float2(base.hi, base.lo);
         }
-        for (int i = threadIdx.x; i < s.nover; i += kBeamThreads) s.based[s.over[i]] = (double)start_score(p, g, s.over[i]);
+        for (int i = threadIdx.x; i < c.nover; i += TH) s.base(s.over(i)) = make_float2(start_score(p, g, s.over(i)), 0.0f);
         __syncthreads();
         if (warp == 0) {  // the best score, which all others are taken relative to
-            double best = (double)kNegInf;
-            for (int l = lane; l < s.nlive; l += 32) best = fmax(best, s.based[s.live[l]]);
-            for (int i = lane; i < s.nover; i += 32) best = fmax(best, s.based[s.over[i]]);
-            best = warp_max_d(best);
-            if (lane == 0) s.ref = best;
+            uint64_t best = 0;
+            for (int i = lane; i < c.nlive + c.nover; i += 32) {
+                const float2 b = s.base(i < c.nlive ? s.live(i) : s.over(i - c.nlive));
+                const uint64_t k = key_of(dd{b.x, b.y});
+                best = k > best ? k : best;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const uint64_t k = __shfl_xor_sync(0xffffffffu, best, o);
+                best = k > best ? k : best;
+            }
+            const dd ref = best ? key_value(best) : dd{0.0f, 0.0f};
+            if (lane == 0) c.ref = ref;
+            for (int i = lane; i < c.nlive + c.nover; i += 32) {
+                const int beam = i < c.nlive ? s.live(i) : s.over(i - c.nlive);
+                if (s.base(beam).x > kNegInf) {
+                    const dd b = dd_sub(dd{s.base(beam).x, s.base(beam).y}, ref);
+                    s.base(beam) = make_float2(b.hi, b.lo);
+                }
+            }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < s.nlive + s.nover; i += kBeamThreads) {
-            const int beam = i < s.nlive ? s.live[i] : s.over[i - s.nlive];
-            const double b = s.based[beam] - s.ref;
-            const float hi = (float)b;
-            s.base[beam] = b > (double)kNegInf ? make_float2(hi, (float)(b - (double)hi)) : make_float2(kNegInf, 0.0f);
-        }
-        __syncthreads();
-        uint64_t floor;
-        n = collect<DT>(p, s, g, floor);
-        const bool doubt = rank_and_doubt(p, s, n, floor);
+        float floor;
+        n = collect<DT, TH>(p, s, c, g, precise, floor);
+        const bool doubt = rank_and_doubt<TH>(p, s, c, n, floor);
         if (!doubt || precise) break;
         precise = true;
-        for (int l = 0; l < s.nlive; ++l) {
-            const int beam = s.live[l];
-            const float m = s.zmax[beam];
-            const bool whole = s.based[beam] > (double)kNegInf;
-            const double sum = whole ? precise_sum<DT>(p, s, beam_row<DT>(p, (long long)g * p.N + beam), m) : 0.0;
+        for (int l = 0; l < c.nlive; ++l) {
+            const int beam = s.live(l);
+            if (!(s.base(beam).x > kNegInf)) continue;  // the same for all threads
+            const dd sum = precise_sum<DT, TH>(p, c, beam_row<DT>(p, rows + beam), s.zmax(beam));
             __syncthreads();
-            if (threadIdx.x == 0) s.based[beam] = sum;
+            if (threadIdx.x == 0) s.sum(beam) = make_float2(sum.hi, sum.lo);
         }
         __syncthreads();
     }
-    for (int r = threadIdx.x; r < p.M; r += kBeamThreads) {
+    for (int r = threadIdx.x; r < p.M; r += TH) {
         int token = p.pad, beam = 0, over = 1;
         float score = kNegInf;
-        if (r < n && s.cand.key[s.order[r]]) {
-            const uint64_t at = s.cand.at[s.order[r]];
+        if (r < n && s.key(s.order(r))) {
+            const uint64_t at = s.at(s.order(r));
             beam = (int)(at >> 32);
-            const long long row = (long long)g * p.N + beam;
             if ((int)(uint32_t)at == kEnded) {
                 score = start_score(p, g, beam);
             } else {
                 token = (int)(uint32_t)at;
-                const float z = logit_at<DT>(beam_row<DT>(p, row).row, token);
-                score = (float)(s.based[beam] + p.c * ((double)z - (double)s.zmax[beam]));
+                score = dd_add(key_value(s.key(s.order(r))), c.ref).hi;
                 over = p.eos >= 0 && token == p.eos;
             }
         }
@@ -569,67 +765,79 @@ __device__ void beam_finish(const BeamParams& p, BeamShared& s, int g) {
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kBeamThreads, 2) beam_kernel(const __grid_constant__ BeamParams p) {
-    __shared__ BeamShared s;
+template <int DT, int TH>
+__global__ void __launch_bounds__(TH, TH == kBeamWide ? 2 : 8) beam_kernel(const __grid_constant__ BeamParams p) {
+    __shared__ BeamCounts c;
+    const BeamShared s = beam_shared(p.N, p.M);
+    constexpr int kWarps = TH / 32;
     const int g = blockIdx.x / p.blocks, b = blockIdx.x - g * p.blocks;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (warp == 0) {  // beams in order: those whose rows are read, and the finished ones
         int live = 0, over = 0;
         for (int i0 = 0; i0 < p.N; i0 += 32) {
             const int i = i0 + lane;
-            const long long row = (long long)g * p.N + i;
             const float score = i < p.N ? start_score(p, g, i) : kNegInf;
             if (!(score < kPosInf) && b == 0) raise_error(p.ws, kErrNonfinite);
             const bool some = score > kNegInf && score < kPosInf;
-            const bool ended = some && p.finished && __ldg(p.finished + row);
+            const bool ended = some && p.finished && __ldg(p.finished + (long long)g * p.N + i);
             const unsigned l = __ballot_sync(0xffffffffu, some && !ended), o = __ballot_sync(0xffffffffu, ended);
-            const unsigned below = (1u << lane) - 1u;
-            if (some && !ended) s.live[live + __popc(l & below)] = i;
-            if (ended) s.over[over + __popc(o & below)] = i;
+            const unsigned before = (1u << lane) - 1u;
+            if (some && !ended) s.live(live + __popc(l & before)) = i;
+            if (ended) s.over(over + __popc(o & before)) = i;
             live += __popc(l);
             over += __popc(o);
         }
-        if (lane == 0) s.nlive = live, s.nover = over;
+        if (lane == 0) c.nlive = live, c.nover = over;
     }
     __syncthreads();
-    float2* part = ws_ptr<float2>(p.ws, p.part);
-    float* sets = ws_ptr<float>(p.ws, p.sets);
-    const int items = s.nlive * p.cpr;
-    for (int i = b * kBeamWarps + warp; i < items; i += p.blocks * kBeamWarps) {
+    const int items = c.nlive * p.cpr;
+    for (int i = b * kWarps + warp; i < items; i += p.blocks * kWarps) {
         const int l = i / p.cpr, chunk = i - l * p.cpr;
-        const long long row = (long long)g * p.N + s.live[l], at = row * p.cpr + chunk;
-        beam_chunk<DT>(p, beam_row<DT>(p, row), chunk, part + at, sets + at * kBeamSets, lane);
+        const long long row = (long long)g * p.N + s.live(l), at = row * p.cpr + chunk;
+        beam_chunk<DT>(p, beam_row<DT>(p, row), chunk, ws_ptr<float>(p.ws, p.maxima) + at, ws_ptr<float>(p.ws, p.sums) + at,
+                       ws_ptr<float>(p.ws, p.sets) + at * kBeamSets, lane);
     }
     __syncthreads();
     if (p.blocks > 1) {
         if (threadIdx.x == 0) {
             unsigned* count = ws_ptr<unsigned>(p.ws, p.count) + g;
-            s.last = atom_add_release(count, 1u) == (unsigned)p.blocks - 1u;
-            if (s.last) {
+            c.last = atom_add_release(count, 1u) == (unsigned)p.blocks - 1u;
+            if (c.last) {
                 fence_acquire();
                 atomicExch(count, 0u);
             }
         }
         __syncthreads();
-        if (!s.last) return;
+        if (!c.last) return;
     }
-    beam_finish<DT>(p, s, g);
+    beam_finish<DT, TH>(p, s, c, g);
+}
+
+template <int DT, int TH>
+static cudaError_t launch_beam_as(const BeamParams& p, cudaStream_t st) {
+    const size_t shared = beam_shared_bytes(p.N, p.M, p.N * p.cpr, TH);
+    if (shared > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(beam_kernel<DT, TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return e;
+        }
+    }
+    beam_kernel<DT, TH><<<(unsigned)p.G * (unsigned)p.blocks, TH, shared, st>>>(p);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_beam(const BeamParams& p0, int dtype, cudaStream_t st) {
     BeamParams p = p0;
-    // a chunk for each warp, as long as all blocks run at the same time
-    const long long chunks = (long long)p.N * p.cpr, want = (chunks + kBeamWarps - 1) / kBeamWarps;
-    const long long fit = 2ll * device_sm_count() / p.G;
+    const int sms = device_sm_count();
+    const bool many = p.G >= 2 * sms;
+    // few groups: a chunk for each warp, as long as all blocks run at the same time
+    const long long chunks = (long long)p.N * p.cpr, want = (chunks + kBeamWide / 32 - 1) / (kBeamWide / 32);
+    const long long fit = many ? 1 : 2ll * sms / p.G;
     p.blocks = (int)(want < fit ? want : fit);
     if (p.blocks < 1) p.blocks = 1;
-    const unsigned grid = (unsigned)p.G * (unsigned)p.blocks;
-    if (dtype == 0)
-        beam_kernel<0><<<grid, kBeamThreads, 0, st>>>(p);
-    else
-        beam_kernel<1><<<grid, kBeamThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    if (dtype == 0) return many ? launch_beam_as<0, kBeamNarrow>(p, st) : launch_beam_as<0, kBeamWide>(p, st);
+    return many ? launch_beam_as<1, kBeamNarrow>(p, st) : launch_beam_as<1, kBeamWide>(p, st);
 }
 
 }  // namespace smcsd

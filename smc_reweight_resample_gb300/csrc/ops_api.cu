@@ -43,8 +43,7 @@ extern "C" int beam_select(const void* logits, long long row_stride, int dtype, 
     if (row_stride < V || (uintptr_t)logits % elem_bytes(dtype)) return SMCSD_ERR_INVALID_ARG;
     // outputs that are read while others are written
     if (out_scores == scores || (finished && out_finished == finished)) return SMCSD_ERR_INVALID_ARG;
-    // a group's chunks are numbered in 32 bits
-    if ((long long)N * beam_chunks(V, 4) * kBeamSets > 0x3fffffffLL) return SMCSD_ERR_INVALID_ARG;
+    if ((long long)N * beam_chunks(V, elem_bytes(dtype)) > kBeamMostChunks) return SMCSD_ERR_INVALID_ARG;
     const BeamLayout L = beam_layout(G * N, V);
     int rc = check_ws(ws, ws_bytes, L.total);
     if (rc) return rc;
@@ -69,10 +68,11 @@ extern "C" int beam_select(const void* logits, long long row_stride, int dtype, 
     p.out_finished = out_finished;
     p.ws = ws;
     p.count = L.count;
-    p.part = L.part;
+    p.maxima = L.maxima;
+    p.sums = L.sums;
     p.sets = L.sets;
-    p.keys = L.keys;
     p.cpr = beam_chunks(V, elem_bytes(dtype));
+    p.div_cpr = make_fastdiv((uint32_t)p.cpr);
     p.T = make_exp2_table();
     cudaStream_t st = (cudaStream_t)stream;
     if (L.zeroed && cudaMemsetAsync(static_cast<char*>(ws) + L.count, 0, L.zeroed, st) != cudaSuccess) return SMCSD_ERR_CUDA;

@@ -12,6 +12,7 @@ namespace smcsd {
 constexpr int kBeamMostBeams = 256;  // of a group
 constexpr int kBeamMost = 256;       // selected of a group
 constexpr int kBeamSets = 8;         // sets of 32 16-byte vectors in a chunk of 4 KB
+constexpr int kBeamMostChunks = 40960;  // of a group: their scores stand in shared memory
 
 struct BeamParams {
     const void* logits;
@@ -28,10 +29,11 @@ struct BeamParams {
     int32_t* out_finished;
     void* ws;
     size_t count;  // uint32 [G]                     blocks of a group that are done
-    size_t part;   // float2 [G * N, cpr]            maximum and sum of a chunk
-    size_t sets;   // float  [G * N, cpr, kBeamSets] maximum of a set
-    size_t keys;   // uint64 [G * N, cpr]            chunk keys of groups with many chunks
+    size_t maxima; // float [G * N, cpr]             of a chunk
+    size_t sums;   // float [G * N, cpr]             relative to it
+    size_t sets;   // float [G * N, cpr, kBeamSets]  maximum of a set
     int cpr, blocks;  // chunks of a row, blocks of a group
+    FastDiv div_cpr;
     Exp2Table T;
 };
 
@@ -39,7 +41,7 @@ struct BeamParams {
 inline int beam_chunks(int V, int bytes) { return (int)(((long long)V * bytes + 15 + kChunkBytes - 1) / kChunkBytes); }
 
 struct BeamLayout {
-    size_t count, part, sets, keys, total, zeroed;
+    size_t count, maxima, sums, sets, total, zeroed;
 };
 // Counters of more groups than the front has places for stand behind it (`zeroed` bytes) and are cleared by the call.
 inline BeamLayout beam_layout(int rows, int V) {
@@ -52,12 +54,12 @@ inline BeamLayout beam_layout(int rows, int V) {
         L.zeroed = 4 * (size_t)rows;
         o = align256(o + L.zeroed);
     }
-    L.part = o;
-    o = align256(o + 8 * n);
+    L.maxima = o;
+    o = align256(o + 4 * n);
+    L.sums = o;
+    o = align256(o + 4 * n);
     L.sets = o;
     o = align256(o + 4 * kBeamSets * n);
-    L.keys = o;
-    o = align256(o + 8 * n);
     L.total = o;
     return L;
 }
