@@ -490,9 +490,10 @@ int logits_process(const void* logits, void* out, int dtype, int R, int V, int S
  *   out_finished[g*M+m] = 1 if the beam was finished or v == eos_token, else 0.
  * Where there are fewer than M candidates (masked tokens of -inf are none), the remaining places get pad_token, 0,
  * -inf and 1. A row with nothing but -inf has no candidate; that is not an error here.
- * The order is that of the scores' real values, up to 1e-11 or so: candidates of one beam are ordered by their logits
- * exactly, those of two beams by sums that are computed again in double-floats where hardware exponentials
- * could not tell them apart (a slower path: some 10 us for each row of 128256).
+ * The order is that of the scores' real values, up to 1e-9 or so: candidates of one beam are ordered by their logits
+ * exactly, those of two beams by sums that are computed again, to 2e-10, where hardware exponentials could
+ * not tell them apart (a slower path: some 20 us for each such row of 128256). Beams with equal scores and
+ * equal rows are exactly equal.
  * N = 1 and scores == NULL gives the M largest log-probabilities of each row: a teacher's top logits, or the children
  * of a draft tree's node.
  * logits [G*N rows, row_stride elements apart, V used], aligned to their type; scores float [G*N] (NULL: 0);

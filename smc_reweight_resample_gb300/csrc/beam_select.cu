@@ -5,8 +5,8 @@
 // candidates are wanted, in the order of score, beam, token.
 //
 // One pass over the logits: a warp takes a chunk of 4 KB (eight 16-byte vectors a lane, loads back to back) and leaves its
-// maximum, its sum of exp(c (z - maximum)) and the maxima of its eight sets (a set: the 32 lanes' vectors of one load, 512
-// contiguous bytes). Nothing is selected on the way. Of ranges of tokens ordered by their maxima, ties by place, the first M
+// maximum, its sum of exp(c (z - maximum)) and the maxima of its sixteen sets (a set: the vectors of half the lanes of one load,
+// 256 contiguous bytes). Nothing is selected on the way. Of ranges of tokens ordered by their maxima, ties by place, the first M
 // hold the M best tokens: each of these M ranges has a token that comes before any token of a range behind them. So the last
 // block of a group to finish
 //   - adds up the beams' sums, which gives every score up to the beam's own constant,
@@ -14,9 +14,9 @@
 //     bisection on their maxima's scores,
 //   - reads these sets again and keeps what is not below the last of them: a little more than M candidates,
 //   - ranks them by counting.
-// Scores are compared as double-floats (FP64 runs at two lanes a clock here), relative to the group's best one. Of one beam this
+// Scores are compared as double-floats (FP64 runs at two lanes a clock here). Of one beam this
 // order is exact, whatever its sum; between beams it is as good as the sums (kTol). Where two scores of different beams that decide
-// anything are nearer than that, the block computes the beams' sums again in double-floats (1e-12) and selects anew.
+// anything are nearer than that, the block computes these beams' sums again to 2e-10 and selects anew.
 #include "f32x2.cuh"
 #include "ops_launch.cuh"
 #include "smcsd_launch.cuh"
@@ -120,27 +120,37 @@ __device__ __forceinline__ float vec_max(const uint4& x) {
     return fmaxf(bf16_lo(m), bf16_hi(m));
 }
 
+// Maximum over the lanes of a mask, which all of them give.
+__device__ __forceinline__ float part_max(float v, unsigned mask) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "r"(mask));
+    return r;
+}
+
 // One chunk of a row: its maximum, sum and set maxima. NaN and +inf show in the sum.
 template <int DT>
 __device__ __forceinline__ void beam_chunk(const BeamParams& p, const BeamRow<DT>& b, int chunk, float* maximum, float* total, float* sets, int lane) {
     constexpr int PV = Geo<DT>::kPerVec;
-    uint4 x[kBeamSets];
-    const int v0 = chunk * kBeamSets * 32;
+    constexpr int kLoads = kBeamSets / 2;
+    uint4 x[kLoads];
+    const int v0 = chunk * kLoads * 32;
     const long long e0 = (long long)v0 * PV - b.shift;
-    if (e0 >= 0 && e0 + kBeamSets * 32 * PV <= b.V) {
+    if (e0 >= 0 && e0 + kLoads * 32 * PV <= b.V) {
 #pragma unroll
-        for (int s = 0; s < kBeamSets; ++s) x[s] = ld_vec(b.at + 16ll * (v0 + s * 32 + lane));
+        for (int s = 0; s < kLoads; ++s) x[s] = ld_vec(b.at + 16ll * (v0 + s * 32 + lane));
     } else {
 #pragma unroll
-        for (int s = 0; s < kBeamSets; ++s) x[s] = beam_vec<DT>(b, v0 + s * 32 + lane);
+        for (int s = 0; s < kLoads; ++s) x[s] = beam_vec<DT>(b, v0 + s * 32 + lane);
     }
     float m = kNegInf, mine = kNegInf;
+    const unsigned half = lane < 16 ? 0xffffu : 0xffff0000u;
 #pragma unroll
-    for (int s = 0; s < kBeamSets; ++s) {
-        const float a = warp_max(vec_max<DT>(x[s]));
-        if (lane == s) mine = a;
+    for (int s = 0; s < kLoads; ++s) {
+        const float a = part_max(vec_max<DT>(x[s]), half);
+        if ((lane & 15) == s) mine = a;
         m = fmaxf(m, a);
     }
+    m = warp_max(m);
     float sum = 0.0f;
     if (m > kNegInf) {
         const f32x2 m2 = pair(-m, -m), c2 = pair(p.c2, p.c2);
@@ -148,7 +158,7 @@ __device__ __forceinline__ void beam_chunk(const BeamParams& p, const BeamRow<DT
 #pragma unroll
         for (int k = 0; k < Vec<DT>::kPairs; ++k) sums[k] = pair(0.0f, 0.0f);
 #pragma unroll
-        for (int s = 0; s < kBeamSets; ++s) {
+        for (int s = 0; s < kLoads; ++s) {
             const Vec<DT> v(x[s]);
 #pragma unroll
             for (int k = 0; k < Vec<DT>::kPairs; ++k) sums[k] = add2(sums[k], exp2_2(mul2(add2(v.x[k], m2), c2)));
@@ -162,7 +172,7 @@ __device__ __forceinline__ void beam_chunk(const BeamParams& p, const BeamRow<DT
         // nothing but -inf, unless there are NaN, which the maxima pass over
         bool nan = false;
 #pragma unroll
-        for (int s = 0; s < kBeamSets; ++s) {
+        for (int s = 0; s < kLoads; ++s) {
             float f[PV];
             unpack<DT>(x[s], f);
 #pragma unroll
@@ -170,7 +180,7 @@ __device__ __forceinline__ void beam_chunk(const BeamParams& p, const BeamRow<DT
         }
         if (__any_sync(0xffffffffu, nan)) sum = __int_as_float(0x7fffffff);
     }
-    if (lane < kBeamSets) sets[lane] = mine;
+    if ((lane & 15) < kLoads) sets[2 * (lane & 15) + (lane >> 4)] = mine;
     if (lane == 0) *maximum = m, *total = sum;
 }
 
@@ -182,17 +192,16 @@ struct BeamShared {
     __device__ __forceinline__ T* at_offset(int bytes) const {
         return reinterpret_cast<T*>(s_beam + bytes);
     }
-    __device__ __forceinline__ float2& sum(int i) const { return at_offset<float2>(0)[i]; }       // [N] S_i, a double-float
-    __device__ __forceinline__ float2& base(int i) const { return at_offset<float2>(8 * N)[i]; }  // [N] s_i - log S_i, the beam's best score,
-                                                                                                 // relative to the group's (of a finished beam s_i)
-    __device__ __forceinline__ float& zmax(int i) const { return at_offset<float>(16 * N)[i]; }   // [N] the row's maximum
-    __device__ __forceinline__ float& zmin(int i) const { return at_offset<float>(20 * N)[i]; }   // [N] no candidate below this logit
-    __device__ __forceinline__ int& live(int i) const { return at_offset<int>(24 * N)[i]; }       // [N] beams whose rows are read
-    __device__ __forceinline__ int& over(int i) const { return at_offset<int>(28 * N)[i]; }       // [N] finished beams
-    __device__ __forceinline__ int* list1() const { return at_offset<int>(32 * N); }              // [most] chunks
-    __device__ __forceinline__ int* list2() const { return at_offset<int>(32 * N + 4 * most); }   // [most] sets
-    __device__ __forceinline__ int& order(int i) const { return at_offset<int>(32 * N + 8 * most)[i]; }  // [M + 1]
-    __host__ __device__ __forceinline__ int tail() const { return (32 * N + 8 * most + 4 * (M + 1) + 15) & ~15; }
+    __device__ __forceinline__ float2& base(int i) const { return at_offset<float2>(0)[i]; }  // [N] s_i - log S_i, the beam's best score (of a finished beam s_i)
+    __device__ __forceinline__ float& zmax(int i) const { return at_offset<float>(8 * N)[i]; }   // [N] the row's maximum
+    __device__ __forceinline__ float& zmin(int i) const { return at_offset<float>(12 * N)[i]; }   // [N] no candidate below this logit
+    __device__ __forceinline__ int& live(int i) const { return at_offset<int>(16 * N)[i]; }       // [N] beams whose rows are read
+    __device__ __forceinline__ int& over(int i) const { return at_offset<int>(20 * N)[i]; }       // [N] finished beams
+    __device__ __forceinline__ int* list1() const { return at_offset<int>(24 * N); }              // [most] chunks
+    __device__ __forceinline__ int* list2() const { return at_offset<int>(24 * N + 4 * most); }   // [most] sets
+    __device__ __forceinline__ int& order(int i) const { return at_offset<int>(24 * N + 8 * most)[i]; }  // [M + 1]
+    __device__ __forceinline__ int& unsure(int i) const { return at_offset<int>(24 * N + 8 * most + 4 * (M + 1))[i]; }  // [N] beams in doubt
+    __host__ __device__ __forceinline__ int tail() const { return (28 * N + 8 * most + 4 * (M + 1) + 15) & ~15; }
     __device__ __forceinline__ float& score(int i) const { return at_offset<float>(tail())[i]; }  // [keys] maxima, then their scores; shares its
                                                                                                  // memory with the candidates
     __device__ __forceinline__ uint64_t& key(int i) const { return at_offset<uint64_t>(tail())[i]; }             // [cands + N]
@@ -200,9 +209,11 @@ struct BeamShared {
 };
 struct BeamCounts {
     int nlive, nover, count, last;
-    int votes[4];
-    dd ref;  // the best score of the group
-    unsigned long long reduce, fixed[2];
+    int chunks, narrowed;  // chunks in list1; whether candidates were left out
+    unsigned votes[3][2];
+    unsigned best;  // the best beam's score, by float_order (0: there is none)
+    unsigned long long reduce;
+    dd part[kBeamWide / 32];
 };
 __host__ __device__ inline BeamShared beam_shared(int N, int M) {
     return BeamShared{N, M + M / 4 + 8, M, 4 * M + 64 < kBeamMostCands ? 4 * M + 64 : kBeamMostCands};
@@ -210,7 +221,7 @@ __host__ __device__ inline BeamShared beam_shared(int N, int M) {
 // Scores of a level: of the sets of all chunks kept, and of all chunks; of all sets where those are not many more.
 __host__ __device__ inline int beam_keys(const BeamShared& s, int chunks, int threads) {
     int n = kBeamSets * s.most;
-    const int some = threads == kBeamWide ? 4096 : 1024;
+    const int some = threads == kBeamWide ? 8192 : 2048;
     if (n < some) n = some;
     return n < chunks ? chunks : n;
 }
@@ -262,37 +273,59 @@ __device__ __noinline__ Cut find_cut_exact(int n, int M, int most, F key_of) {
     return Cut{lo, b};
 }
 
-// A score from which on there are between M and `most` of the n scores (relative to the best, so at most 0): a bisection of values,
-// since the M best are mostly within a few units of the best. Fails where ties, or scores next to the best, leave none.
+// A score from which on there are between M and `most` of the n scores: a bisection of values, four at a time, since the M best are
+// mostly within a few nats (`unit`) of the best. Fails where ties, or scores next to the best, leave none.
 template <int TH>
-__device__ __forceinline__ bool find_cut(const BeamShared& s, BeamCounts& c, int n, int M, int most, float& from) {
-    float above = 1.0f, below = kNegInf;  // fewer than M from `above` on; more than `most` from `below` on
-    from = -1.0f;
-    for (int turn = 0; turn < 28; ++turn) {
-        int mine = 0;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < n; i += TH) mine += s.score(i) >= from;
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        if ((threadIdx.x & 31) == 0 && mine) atomicAdd(&c.votes[turn & 3], mine);
+__device__ __forceinline__ bool find_cut(const BeamShared& s, BeamCounts& c, int n, int M, int most, float best, float unit, float& from) {
+    float above = best, below = kNegInf, step = 0.5f * unit;  // the border lies between them: more than `most` from `below` on
+    for (int turn = 0; turn < 16; ++turn) {
+        float t[4];
+        if (below == kNegInf) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] = best - step * (float)(1 << k);
+            step *= turn < 2 ? 16.0f : 65536.0f;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] = above + (below - above) * (0.2f * (float)(k + 1));
+        }
+        unsigned lo = 0, hi = 0;  // counts of 16 bits: n is less than 65536
+        for (int i = threadIdx.x; i < n; i += TH) {
+            const float x = s.score(i);
+            lo += (x >= t[0] ? 1u : 0u) + (x >= t[1] ? 0x10000u : 0u);
+            hi += (x >= t[2] ? 1u : 0u) + (x >= t[3] ? 0x10000u : 0u);
+        }
+        lo = __reduce_add_sync(0xffffffffu, lo);
+        hi = __reduce_add_sync(0xffffffffu, hi);
+        const int slot = turn % 3;
+        if ((threadIdx.x & 31) == 0 && hi) {
+            atomicAdd(&c.votes[slot][0], lo);
+            atomicAdd(&c.votes[slot][1], hi);
+        }
         __syncthreads();
-        const int got = c.votes[turn & 3];
-        if (threadIdx.x == 0) c.votes[(turn + 2) & 3] = 0;  // all have read it by the last barrier
-        if (got > most)
-            below = from;
-        else if (got < M)
-            above = from;
-        else
-            return true;
-        const float next = below == kNegInf ? (turn < 8 ? from * 2.0f : from * 65536.0f) : 0.5f * (fminf(above, 0.0f) + below);
-        if (!(next > kNegInf) || next == from) break;
-        from = next;
+        lo = c.votes[slot][0], hi = c.votes[slot][1];
+        if (threadIdx.x < 2) c.votes[(turn + 2) % 3][threadIdx.x] = 0;  // all have read that one by the last barrier
+        const int got[4] = {(int)(lo & 0xffffu), (int)(lo >> 16), (int)(hi & 0xffffu), (int)(hi >> 16)};
+        const float was_above = above, was_below = below;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (got[k] >= M && got[k] <= most) {
+                from = t[k];
+                return true;
+            }
+            if (got[k] < M) above = t[k];
+        }
+#pragma unroll
+        for (int k = 3; k >= 0; --k)
+            if (got[k] > most) below = t[k];
+        if (!(t[3] > kNegInf) || (was_above == above && was_below == below && below != kNegInf)) break;
     }
     return false;
 }
 template <int TH>
 __device__ __forceinline__ void clear_votes(BeamCounts& c) {
     __syncthreads();
-    if (threadIdx.x < 4) c.votes[threadIdx.x] = 0;
+    if (threadIdx.x < 6) c.votes[threadIdx.x >> 1][threadIdx.x & 1] = 0;
+    if (threadIdx.x == 0) c.count = 0;
     __syncthreads();
 }
 
@@ -331,8 +364,8 @@ struct FirstLevel {
 template <int TH>
 __device__ __forceinline__ FirstLevel first_level(const BeamParams& p, const BeamShared& s, int g, int nlive) {
     FirstLevel v;
-    v.log = nlive * p.cpr <= beam_keys(s, p.N * p.cpr, TH) / kBeamSets ? 3 : 0;
-    static_assert(kBeamSets == 8, "shifts by 3");
+    v.log = nlive * p.cpr <= beam_keys(s, p.N * p.cpr, TH) / kBeamSets ? 4 : 0;
+    static_assert(kBeamSets == 16, "shifts by 4");
     v.chunks = p.div_cpr;
     v.per = p.cpr << v.log;
     v.n = nlive * v.per;
@@ -361,7 +394,7 @@ struct LevelKey {
         return score_key(*p, level.z(s, i), s.zmax(beam), s.base(beam));
     }
 };
-// An item's score: in float32, off by at most three roundings, 1.8e-7 of it (both terms are negative), and for one beam in the order of
+// An item's score: in float32, off by at most three roundings (of the difference, of the factor, of the sum) of its terms, and for one beam in the order of
 // the logits; or as the high half of its key.
 constexpr float kScoreError = 3e-7f;
 template <typename L>
@@ -374,9 +407,9 @@ __device__ __forceinline__ float level_score(const BeamParams& p, const BeamShar
 
 // The places of a level's n items that hold the group's M best tokens, in `list`; returns how many. All that are there, if they are
 // no more than `most`. `floor`: a score, up to kScoreError; no item below it has been kept.
-template <int TH, typename L>
-__device__ __forceinline__ int choose(const BeamParams& p, const BeamShared& s, BeamCounts& c, int n, const L& level, int* list,
-                                      float& floor, bool& by_place) {
+template <int TH, typename F>
+__device__ __forceinline__ int choose(const BeamShared& s, BeamCounts& c, int n, float best, float unit, const F& key_of, int* list, float& floor,
+                                      bool& by_place) {
     const int most = s.most;
     float from = kLowest;
     Cut cut{0, n};
@@ -384,24 +417,21 @@ __device__ __forceinline__ int choose(const BeamParams& p, const BeamShared& s, 
     clear_votes<TH>(c);
     bool ok = n <= most;
     if (!ok) {
-        ok = find_cut<TH>(s, c, n, p.M, most, from);
+        ok = find_cut<TH>(s, c, n, s.M, most, best, unit, from);
         if (!ok) {
             int some = 0;
             for (int i = threadIdx.x; i - (int)threadIdx.x < n; i += TH) some += __syncthreads_count(i < n && s.score(i) > kNegInf);
             ok = some <= most;  // fewer than M perhaps: all of them
             from = kLowest;
             if (!ok) {
-                cut = find_cut_exact<TH>(n, p.M, most, LevelKey<L>{&p, s, level});
+                cut = find_cut_exact<TH>(n, s.M, most, key_of);
                 by_place = cut.I < n;
             }
         }
     }
     floor = fmaxf(floor, ok ? from : key_value(cut.K).hi);
-    __syncthreads();
-    if (threadIdx.x == 0) c.count = 0;
-    __syncthreads();
     for (int i = threadIdx.x; i < n; i += TH)
-        if (ok ? s.score(i) >= from : kept(cut, LevelKey<L>{&p, s, level}(i), i)) {
+        if (ok ? s.score(i) >= from : kept(cut, key_of(i), i)) {
             const int k = atomicAdd(&c.count, 1);
             if (k < most) list[k] = i;
         }
@@ -409,36 +439,56 @@ __device__ __forceinline__ int choose(const BeamParams& p, const BeamShared& s, 
     return min(c.count, most);
 }
 
-// Sum of exp(c (z - m)) over row b by the whole block: every term from double-floats, rounded to a multiple of 2^-56 and added up
-// in integers, so that rows with the same logits have the same sum however they lie in memory. Off by at most 2^-57 a term and
-// 1e-13 of it.
+// Sum of exp(c (z - m)) over a row by the whole block, for the beams whose order is in doubt. 2^t for t = c log2(e) (z - m) as a
+// double-float: t = n + j / 256 + g with |g| <= 1 / 512, 2^(j / 256) from a table and 2^g - 1 (at most 0.0014) by three terms of
+// its series in float32, 1.2e-10 off. Which thread adds which tokens in which order depends on their places in the row alone, so
+// that rows with the same logits have the same sum however they lie in memory.
+constexpr int kTable = 256;
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: a sum with it is rounded to a whole number
+__device__ __forceinline__ float2* exp_table(const BeamShared& s) { return s.at_offset<float2>(s.tail()); }
+template <int TH>
+__device__ __forceinline__ void fill_exp_table(const BeamParams& p, const BeamShared& s) {
+    for (int j = threadIdx.x; j < kTable; j += TH) {
+        const ddx e = exp_split(dd_mul_f(dd{SMCSD_LN2_HI, SMCSD_LN2_LO}, (float)j / 256.0f), p.T);
+        const float u = pow2i(e.n);
+        exp_table(s)[j] = make_float2(e.hi * u, e.lo * u);
+    }
+}
 template <int DT, int TH>
-__device__ __noinline__ dd precise_sum(const BeamParams& p, BeamCounts& c, BeamRow<DT> b, float m) {
-    constexpr int PV = Geo<DT>::kPerVec;
-    const int vecs = (int)(((long long)b.V + b.shift + PV - 1) / PV);
-    unsigned __int128 acc = 0;
-    for (int v = threadIdx.x; v < vecs; v += TH) {
-        float f[PV];
-        unpack<DT>(beam_vec<DT>(b, v), f);
-#pragma unroll 1
-        for (int i = 0; i < PV; ++i) {
-            const dd x = dd_mul(two_sum(f[i], -m), dd{p.c_hi, p.c_lo});
-            if (!(x.hi > -42.0f)) continue;  // below 2^-60
-            const ddx e = exp_split(x, p.T);
-            const float u = pow2i(e.n + 56);
-            acc += (unsigned long long)(__float2ll_rn(e.hi * u) + __float2ll_rn(e.lo * u));
+__device__ __noinline__ dd precise_sum(const BeamParams& p, BeamShared s, BeamCounts& c, const void* row, float m) {
+    constexpr int kEach = 8;
+    const float2* table = exp_table(s);
+    const dd c2 = dd_mul(dd{p.c_hi, p.c_lo}, dd{SMCSD_LOG2E_HI, SMCSD_LOG2E_LO});
+    const int V = p.V;
+    dd acc{0.0f, 0.0f};
+    for (long long v0 = threadIdx.x; v0 < V; v0 += kEach * TH) {
+        float z[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) z[k] = v0 + k * TH < V ? logit_at<DT>(row, v0 + k * TH) : kNegInf;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const dd d = two_sum(z[k], -m);
+            const float th = fmaxf(f_mul(d.hi, c2.hi), -100.0f);  // what is smaller adds nothing, whatever the rest is
+            const float tl = f_add(f_add(f_fma(d.hi, c2.hi, -th), f_mul(d.hi, c2.lo)), f_mul(d.lo, c2.hi));
+            const float r = f_fma(th, 256.0f, kRound);  // 256 n + j in its last bits
+            const int i = __float_as_int(r) - __float_as_int(kRound);
+            const float g = f_add(f_fma(f_sub(r, kRound), -0.00390625f, th), th > -100.0f ? tl : 0.0f);
+            const float e = f_mul(g, f_fma(g, f_fma(g, 0.0555041087f, 0.240226507f), 0.693147181f));
+            const float2 t = table[i & 255];
+            const float u = __int_as_float(((i >> 8) + 127) << 23);
+            const dd a = two_sum(acc.hi, f_mul(t.x, u));
+            acc.hi = a.hi;
+            acc.lo = f_add(acc.lo, f_add(a.lo, f_mul(f_fma(t.x, e, t.y), u)));
         }
     }
+    acc = warp_sum_dd(fast_two_sum(acc.hi, acc.lo));
     __syncthreads();
-    if (threadIdx.x == 0) c.fixed[0] = c.fixed[1] = 0;
+    if ((threadIdx.x & 31) == 0) c.part[threadIdx.x >> 5] = acc;
     __syncthreads();
-    // in units of 2^-56 and 2^-24: both stay below 2^63 with 2^31 terms
-    atomicAdd(&c.fixed[0], (unsigned long long)acc & 0xffffffffull);
-    atomicAdd(&c.fixed[1], (unsigned long long)(acc >> 32));
+    acc = c.part[0];
+    for (int w = 1; w < TH / 32; ++w) acc = dd_add(acc, c.part[w]);
     __syncthreads();
-    const double sum = ldexp((double)c.fixed[1], -24) + ldexp((double)c.fixed[0], -56);
-    const float hi = (float)sum;
-    return dd{hi, (float)(sum - (double)hi)};
+    return acc;
 }
 
 // log of a positive double-float: one step of Newton's method from the float logarithm, in double-floats.
@@ -457,24 +507,24 @@ __device__ __forceinline__ float start_score(const BeamParams& p, int g, int bea
     return p.scores ? __ldg(p.scores + (long long)g * p.N + beam) : 0.0f;
 }
 
-// Calls f(logit, beam, token) for every token of the sets in list2 whose logit is not below its beam's zmin. A warp takes four sets
-// at a time, so that their loads are on the way together.
+// Calls f(logit, beam, token) for every token of the sets in list2 whose logit is not below its beam's zmin. Half a warp takes a set,
+// and four of them at a time, so that their loads are on the way together.
 template <int DT, int TH, typename F>
 __device__ __forceinline__ void scan_sets(const BeamParams& p, const BeamShared& s, int g, int n2, F&& f) {
-    constexpr int PV = Geo<DT>::kPerVec, kEach = 4, kWarps = TH / 32;
-    const int lane = threadIdx.x & 31, per = p.cpr * kBeamSets;
-    for (int i0 = threadIdx.x >> 5; i0 < n2; i0 += kEach * kWarps) {
+    constexpr int PV = Geo<DT>::kPerVec, kEach = 4, kHalves = TH / 16;
+    const int lane = threadIdx.x & 15, per = p.cpr * kBeamSets;
+    for (int i0 = threadIdx.x >> 4; i0 < n2; i0 += kEach * kHalves) {
         uint4 x[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int i = i0 + k * kWarps;
+            const int i = i0 + k * kHalves;
             if (i >= n2) break;
             const int set = s.list2()[i], l = (int)fast_div((uint32_t)set / kBeamSets, p.div_cpr);
-            x[k] = beam_vec<DT>(beam_row<DT>(p, (long long)g * p.N + s.live(l)), (set - l * per) * 32 + lane);
+            x[k] = beam_vec<DT>(beam_row<DT>(p, (long long)g * p.N + s.live(l)), (set - l * per) * 16 + lane);
         }
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int i = i0 + k * kWarps;
+            const int i = i0 + k * kHalves;
             if (i >= n2) break;
             const int set = s.list2()[i], l = (int)fast_div((uint32_t)set / kBeamSets, p.div_cpr), beam = s.live(l);
             const float zmin = s.zmin(beam);
@@ -484,7 +534,7 @@ __device__ __forceinline__ void scan_sets(const BeamParams& p, const BeamShared&
 #pragma unroll
             for (int e = 0; e < PV; ++e) hits |= z[e] >= zmin ? 1u << e : 0u;
             if (hits) {
-                const int v = (set - l * per) * 32 + lane, shift = beam_row<DT>(p, (long long)g * p.N + beam).shift;
+                const int v = (set - l * per) * 16 + lane, shift = beam_row<DT>(p, (long long)g * p.N + beam).shift;
                 do {
                     const int e = __ffs(hits) - 1, w = DT == 0 ? e : e >> 1;
                     hits &= hits - 1;
@@ -559,7 +609,7 @@ __device__ __forceinline__ int collect(const BeamParams& p, const BeamShared& s,
         s.score(i) = level_score(p, s, v, i, exact ? v.z(s, i) : s.score(i), exact);
     floor = kLowest;
     bool by_place;
-    int n1 = choose<TH>(p, s, c, v.n, v, v.log ? s.list2() : s.list1(), floor, by_place), n2 = n1;
+    int n1 = choose<TH>(s, c, v.n, float_of_order(c.best), 1.0f, LevelKey<FirstLevel>{&p, s, v}, v.log ? s.list2() : s.list1(), floor, by_place), n2 = n1;
     if (!v.log) {
         const SecondLevel w{ws_ptr<const float>(p.ws, p.sets) + (long long)g * p.N * p.cpr * kBeamSets, p.cpr, p.div_cpr};
         const float floor1 = floor;
@@ -567,7 +617,7 @@ __device__ __forceinline__ int collect(const BeamParams& p, const BeamShared& s,
             __syncthreads();
             for (int i = threadIdx.x; i < n1 * kBeamSets; i += TH) s.score(i) = level_score(p, s, w, i, w.z(s, i), exact);
             floor = floor1;
-            n2 = choose<TH>(p, s, c, n1 * kBeamSets, w, s.list2(), floor, by_place);
+            n2 = choose<TH>(s, c, n1 * kBeamSets, float_of_order(c.best), 1.0f, LevelKey<SecondLevel>{&p, s, w}, s.list2(), floor, by_place);
             if (!by_place || turn == 1) break;
             // sets are chosen by their places, which follow the chunks'
             __syncthreads();
@@ -575,6 +625,7 @@ __device__ __forceinline__ int collect(const BeamParams& p, const BeamShared& s,
         }
         // places in list1 to sets of the group's live beams
         __syncthreads();
+        if (threadIdx.x == 0) c.chunks = n1;
         for (int i = threadIdx.x; i < n2; i += TH) s.list2()[i] = s.list1()[s.list2()[i] / kBeamSets] * kBeamSets + s.list2()[i] % kBeamSets;
     }
     // the floor as a logit of each live beam, lowered by more than its roundings
@@ -592,6 +643,7 @@ __device__ __forceinline__ int collect(const BeamParams& p, const BeamShared& s,
         if (k < room) s.key(k) = __float_as_uint(z), s.at(k) = place_of(beam, token);
     });
     __syncthreads();
+    if (threadIdx.x == 0) c.narrowed = c.count > room;
     if (c.count <= room) {
         for (int i = threadIdx.x; i < c.count; i += TH) {
             const int beam = (int)(s.at(i) >> 32);
@@ -623,10 +675,31 @@ __device__ __forceinline__ int collect(const BeamParams& p, const BeamShared& s,
     return got + c.nover;
 }
 
-// Ranks the candidates: s.order holds the first M (and one more, if there is one). Whether scores of different beams that
-// decide about this order are nearer than the sums are good for.
+// Marks the beams of ranges that may have been left out though they come next to the last of the M best, whose beam and score are
+// given; whether there are any of other beams. (Ranges that were kept are looked at token by token.)
 template <int TH>
-__device__ __forceinline__ bool rank_and_doubt(const BeamParams& p, const BeamShared& s, const BeamCounts& c, int n, float floor) {
+__device__ __noinline__ bool mark_near(const BeamParams& p, BeamShared s, BeamCounts& c, int g, int of, float last) {
+    bool found = false;
+    const auto mark = [&](int beam, float x) {
+        if (beam == of || !(fabsf(x - last) <= kTol + 2.0f * kScoreError * fabsf(last))) return;
+        s.unsure(beam) = s.unsure(of) = 1;
+        found = true;
+    };
+    const FirstLevel v = first_level<TH>(p, s, g, c.nlive);
+    for (int i = threadIdx.x; i < v.n; i += TH) mark(v.beam(s, i), level_score(p, s, v, i, v.z(s, i), false));
+    if (!v.log) {
+        const SecondLevel w{ws_ptr<const float>(p.ws, p.sets) + (long long)g * p.N * p.cpr * kBeamSets, p.cpr, p.div_cpr};
+        for (int i = threadIdx.x; i < c.chunks * kBeamSets; i += TH) mark(w.beam(s, i), level_score(p, s, w, i, w.z(s, i), false));
+    }
+    if (c.narrowed)
+        for (int l = threadIdx.x; l < c.nlive; l += TH) mark(s.live(l), last);
+    return found;
+}
+
+// Ranks the candidates: s.order holds the first M (and one more, if there is one). Whether scores of different beams that
+// decide about this order are nearer than the sums are good for; s.unsure marks those beams.
+template <int TH>
+__device__ __forceinline__ bool rank_and_doubt(const BeamParams& p, const BeamShared& s, BeamCounts& c, int g, int n, float floor) {
     for (int i = threadIdx.x; i < n; i += TH) {
         const uint64_t key = s.key(i), at = s.at(i);
         int rank = 0;
@@ -636,12 +709,16 @@ __device__ __forceinline__ bool rank_and_doubt(const BeamParams& p, const BeamSh
     }
     __syncthreads();
     if (c.nlive + c.nover <= 1) return false;
+    for (int i = threadIdx.x; i < p.N; i += TH) s.unsure(i) = 0;
+    __syncthreads();
     bool doubt = false;
     const auto near = [&](int i, int j) {
         const uint64_t a = s.at(i), b = s.at(j);
         if (a >> 32 == b >> 32 || ((int)(uint32_t)a == kEnded && (int)(uint32_t)b == kEnded)) return false;  // of one beam; exact
         const dd d = dd_sub(key_value(s.key(i)), key_value(s.key(j)));
-        return fabsf(d.hi) <= kTol;
+        if (!(fabsf(d.hi) <= kTol)) return false;
+        s.unsure((int)(a >> 32)) = s.unsure((int)(b >> 32)) = 1;
+        return true;
     };
     const int m = min(p.M, n);
     for (int r = threadIdx.x; r < m && r + 1 < n; r += TH) doubt |= near(s.order(r), s.order(r + 1));
@@ -649,9 +726,47 @@ __device__ __forceinline__ bool rank_and_doubt(const BeamParams& p, const BeamSh
         const int last = s.order(p.M - 1);
         for (int i = threadIdx.x; i < n; i += TH) doubt |= near(i, last);
     }
-    if (floor > kLowest && n >= p.M)  // and what was left out
-        doubt |= key_value(s.key(s.order(p.M - 1))).hi - floor <= kTol + 2.0f * kScoreError * fabsf(floor);
+    if (floor > kLowest && n >= p.M) {  // and what was left out
+        const float last = key_value(s.key(s.order(p.M - 1))).hi;
+        if (last - floor <= kTol + 2.0f * kScoreError * fabsf(floor)) doubt |= mark_near<TH>(p, s, c, g, (int)(s.at(s.order(p.M - 1)) >> 32), last);
+    }
     return __syncthreads_or(doubt);
+}
+
+struct Mass {
+    float m, s;
+};
+// Maximum and sum of a row's chunks, by one warp; NaN and +inf show in the sum.
+__device__ __forceinline__ Mass row_mass(const BeamParams& p, long long row) {
+    const int lane = threadIdx.x & 31;
+    const float* qm = ws_ptr<const float>(p.ws, p.maxima) + row * p.cpr;
+    const float* qs = ws_ptr<const float>(p.ws, p.sums) + row * p.cpr;
+    float m = kNegInf, sum = 0.0f, first[3][2];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const bool in = k * 32 + lane < p.cpr;
+        first[k][0] = in ? __ldcg(qm + k * 32 + lane) : kNegInf;
+        first[k][1] = in ? __ldcg(qs + k * 32 + lane) : 0.0f;
+        m = fmaxf(m, first[k][0]);
+    }
+    for (int k = 96 + lane; k < p.cpr; k += 32) m = fmaxf(m, __ldcg(qm + k));
+    m = warp_max(m);
+    const auto part = [&](float km, float ks) { return km > kNegInf ? ks * exp2f((km - m) * p.c2) : ks; };  // of -inf: 0, or NaN
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sum += part(first[k][0], first[k][1]);
+    for (int k = 96 + lane; k < p.cpr; k += 32) sum += part(__ldcg(qm + k), __ldcg(qs + k));
+    return Mass{m, warp_sum(sum)};
+}
+
+// A beam's constant from its sum, by whole warps: s_i - log S_i, or none if there is no mass.
+__device__ __forceinline__ void set_base(const BeamParams& p, const BeamShared& s, BeamCounts& c, int g, int beam, float m, dd sum) {
+    dd base{kNegInf, 0.0f};
+    if (sum.hi > 0.0f) base = dd_sub(dd{start_score(p, g, beam), 0.0f}, dd_log(sum, p.T));
+    if ((threadIdx.x & 31) == 0) {
+        s.zmax(beam) = m;
+        s.base(beam) = make_float2(base.hi, base.lo);
+        if (sum.hi > 0.0f) atomicMax(&c.best, float_order(base.hi));
+    }
 }
 
 // The group's selection, by the last block of the group.
@@ -667,81 +782,37 @@ __device__ __forceinline__ void beam_finish(const BeamParams& p, const BeamShare
     // a warp a beam: maximum and sum of its chunks
     for (int l = warp; l < c.nlive; l += TH / 32) {
         const int beam = s.live(l);
-        const float* qm = ws_ptr<const float>(p.ws, p.maxima) + (rows + beam) * p.cpr;
-        const float* qs = ws_ptr<const float>(p.ws, p.sums) + (rows + beam) * p.cpr;
-        float m = kNegInf, sum = 0.0f, first[3][2];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const bool in = k * 32 + lane < p.cpr;
-            first[k][0] = in ? __ldcg(qm + k * 32 + lane) : kNegInf;
-            first[k][1] = in ? __ldcg(qs + k * 32 + lane) : 0.0f;
-            m = fmaxf(m, first[k][0]);
-        }
-        for (int k = 96 + lane; k < p.cpr; k += 32) m = fmaxf(m, __ldcg(qm + k));
-        m = warp_max(m);
-        const auto part = [&](float km, float ks) { return km > kNegInf ? ks * exp2f((km - m) * p.c2) : ks; };  // of -inf: 0, or NaN
-#pragma unroll
-        for (int k = 0; k < 3; ++k) sum += part(first[k][0], first[k][1]);
-        for (int k = 96 + lane; k < p.cpr; k += 32) sum += part(__ldcg(qm + k), __ldcg(qs + k));
-        sum = warp_sum(sum);
-        if (lane == 0) {
-            s.zmax(beam) = m;
-            s.sum(beam) = make_float2(sum, 0.0f);
-        }
+        const Mass a = row_mass(p, rows + beam);
+        const float m = a.m, sum = a.s;
+        const bool good = sum < kPosInf && m < kPosInf;
+        if (!good && lane == 0) raise_error(p.ws, kErrNonfinite);
+        set_base(p, s, c, g, beam, m, dd{good ? sum : 0.0f, 0.0f});
+    }
+    // the beams' constants: scores are c (z - m) + base
+    for (int i = threadIdx.x; i < c.nover; i += TH) {
+        const float score = start_score(p, g, s.over(i));
+        s.base(s.over(i)) = make_float2(score, 0.0f);
+        atomicMax(&c.best, float_order(score));
     }
     __syncthreads();
     bool precise = false;
     int n;
     for (;;) {
-        // the beams' constants: scores are c (z - m) + base
-        for (int l = threadIdx.x; l < c.nlive; l += TH) {
-            const int beam = s.live(l);
-            const dd sum{s.sum(beam).x, s.sum(beam).y};
-            dd base{kNegInf, 0.0f};
-            if (!(sum.hi < kPosInf) || s.zmax(beam) == kPosInf)
-                raise_error(p.ws, kErrNonfinite);
-            else if (sum.hi > 0.0f)
-                base = dd_sub(dd{start_score(p, g, beam), 0.0f}, dd_log(sum, p.T));
-            s.base(beam) = make_float2(base.hi, base.lo);
-        }
-        for (int i = threadIdx.x; i < c.nover; i += TH) s.base(s.over(i)) = make_float2(start_score(p, g, s.over(i)), 0.0f);
-        __syncthreads();
-        if (warp == 0) {  // the best score, which all others are taken relative to
-            uint64_t best = 0;
-            for (int i = lane; i < c.nlive + c.nover; i += 32) {
-                const float2 b = s.base(i < c.nlive ? s.live(i) : s.over(i - c.nlive));
-                const uint64_t k = key_of(dd{b.x, b.y});
-                best = k > best ? k : best;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const uint64_t k = __shfl_xor_sync(0xffffffffu, best, o);
-                best = k > best ? k : best;
-            }
-            const dd ref = best ? key_value(best) : dd{0.0f, 0.0f};
-            if (lane == 0) c.ref = ref;
-            for (int i = lane; i < c.nlive + c.nover; i += 32) {
-                const int beam = i < c.nlive ? s.live(i) : s.over(i - c.nlive);
-                if (s.base(beam).x > kNegInf) {
-                    const dd b = dd_sub(dd{s.base(beam).x, s.base(beam).y}, ref);
-                    s.base(beam) = make_float2(b.hi, b.lo);
-                }
-            }
-        }
-        __syncthreads();
         float floor;
         n = collect<DT, TH>(p, s, c, g, precise, floor);
-        const bool doubt = rank_and_doubt<TH>(p, s, c, n, floor);
+        const bool doubt = rank_and_doubt<TH>(p, s, c, g, n, floor);
         if (!doubt || precise) break;
         precise = true;
+        fill_exp_table<TH>(p, s);
+        __syncthreads();
         for (int l = 0; l < c.nlive; ++l) {
             const int beam = s.live(l);
-            if (!(s.base(beam).x > kNegInf)) continue;  // the same for all threads
-            const dd sum = precise_sum<DT, TH>(p, c, beam_row<DT>(p, rows + beam), s.zmax(beam));
+            if (!s.unsure(beam) || !(s.base(beam).x > kNegInf)) continue;  // the same for all threads
+            const dd sum = precise_sum<DT, TH>(p, s, c, beam_row<DT>(p, rows + beam).row, s.zmax(beam));
             __syncthreads();
-            if (threadIdx.x == 0) s.sum(beam) = make_float2(sum.hi, sum.lo);
+            set_base(p, s, c, g, beam, s.zmax(beam), sum);
+            __syncthreads();
         }
-        __syncthreads();
     }
     for (int r = threadIdx.x; r < p.M; r += TH) {
         int token = p.pad, beam = 0, over = 1;
@@ -753,7 +824,7 @@ __device__ __forceinline__ void beam_finish(const BeamParams& p, const BeamShare
                 score = start_score(p, g, beam);
             } else {
                 token = (int)(uint32_t)at;
-                score = dd_add(key_value(s.key(s.order(r))), c.ref).hi;
+                score = key_value(s.key(s.order(r))).hi;
                 over = p.eos >= 0 && token == p.eos;
             }
         }
@@ -765,8 +836,131 @@ __device__ __forceinline__ void beam_finish(const BeamParams& p, const BeamShare
     }
 }
 
+// ------------------------------------------------------------------------------------------
+// groups of one: a row's M best tokens go by their logits alone, and are known without the row's sum
+// ------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint64_t token_key(float z, int token) { return (uint64_t)float_order(z + 0.0f) << 32 | (uint32_t)~token; }
+// A place's key where only logits count: the row's sets or chunks, or the sets of the chunks in list1.
+struct RowKey {
+    const float* z_;
+    const int* chunks;
+    __device__ __forceinline__ float z(int i) const { return __ldcg(z_ + (chunks ? chunks[i / kBeamSets] * kBeamSets + i % kBeamSets : i)); }
+    __device__ __forceinline__ uint64_t operator()(int i) const {
+        const float x = z(i);
+        return x > kNegInf ? (uint64_t)float_order(x + 0.0f) << 32 : 0;
+    }
+};
+
+// A key that M to s.cands of the tokens of the sets in list2 are not below.
 template <int DT, int TH>
-__global__ void __launch_bounds__(TH, TH == kBeamWide ? 2 : 8) beam_kernel(const __grid_constant__ BeamParams p) {
+__device__ __noinline__ uint64_t narrow_row(const BeamParams& p, BeamShared s, BeamCounts& c, int g, int n2) {
+    uint64_t lo = 0, hi = ~0ull;
+    while (hi - lo > 1) {
+        const uint64_t mid = lo + (hi - lo) / 2;
+        unsigned mine = 0;
+        scan_sets<DT, TH>(p, s, g, n2, [&](float z, int, int token) { mine += token_key(z, token) >= mid; });
+        const unsigned long long n = block_total(c, mine);
+        if (n > (unsigned)s.cands)
+            lo = mid;
+        else if (n < (unsigned)s.M)
+            hi = mid;
+        else
+            return mid;
+    }
+    return hi;
+}
+
+template <int DT, int TH>
+__device__ __forceinline__ void row_finish(const BeamParams& p, const BeamShared& s, BeamCounts& c, int g) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int n = 0;
+    if (c.nlive) {
+        const bool direct = p.cpr <= beam_keys(s, p.cpr, TH) / kBeamSets;
+        const int n0 = direct ? p.cpr * kBeamSets : p.cpr;
+        const float* sets = ws_ptr<const float>(p.ws, p.sets) + (long long)g * p.cpr * kBeamSets;
+        const RowKey v{direct ? sets : ws_ptr<const float>(p.ws, p.maxima) + (long long)g * p.cpr, nullptr};
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n0; i += TH) s.score(i) = v.z(i);
+        if (warp == 0) {
+            const Mass a = row_mass(p, g);
+            const bool good = a.s < kPosInf && a.m < kPosInf;
+            if (!good && lane == 0) raise_error(p.ws, kErrNonfinite);
+            set_base(p, s, c, g, 0, a.m, dd{good ? a.s : 0.0f, 0.0f});
+        }
+        __syncthreads();
+        if (s.base(0).x > kNegInf) {
+            const float best = s.zmax(0), unit = 1.0f / p.c_hi;
+            float floor = kLowest;
+            bool by_place;
+            const int n1 = choose<TH>(s, c, n0, best, unit, v, direct ? s.list2() : s.list1(), floor, by_place);
+            int n2 = n1;
+            if (!direct) {
+                const float floor1 = floor;
+                const RowKey w{sets, s.list1()};
+                for (int turn = 0; turn < 2; ++turn) {
+                    __syncthreads();
+                    for (int i = threadIdx.x; i < n1 * kBeamSets; i += TH) s.score(i) = w.z(i);
+                    floor = floor1;
+                    n2 = choose<TH>(s, c, n1 * kBeamSets, best, unit, w, s.list2(), floor, by_place);
+                    if (!by_place || turn == 1) break;
+                    // sets are chosen by their places, which follow the chunks'
+                    __syncthreads();
+                    sort_list<TH>(s.list1(), n1);
+                }
+                __syncthreads();
+                for (int i = threadIdx.x; i < n2; i += TH) s.list2()[i] = s.list1()[s.list2()[i] / kBeamSets] * kBeamSets + s.list2()[i] % kBeamSets;
+            }
+            if (threadIdx.x == 0) s.zmin(0) = floor;
+            uint64_t K = 0;
+            for (int turn = 0; turn < 2; ++turn) {
+                __syncthreads();
+                if (threadIdx.x == 0) c.count = 0;
+                __syncthreads();
+                scan_sets<DT, TH>(p, s, g, n2, [&](float z, int, int token) {
+                    const uint64_t key = token_key(z, token);
+                    if (key >= K) {
+                        const int k = atomicAdd(&c.count, 1);
+                        if (k < s.cands) s.key(k) = key;
+                    }
+                });
+                __syncthreads();
+                if (c.count <= s.cands) break;
+                K = narrow_row<DT, TH>(p, s, c, g, n2);
+            }
+            n = min(c.count, s.cands);
+            for (int i = threadIdx.x; i < n; i += TH) {
+                const uint64_t key = s.key(i);
+                int rank = 0;
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) rank += s.key(j) > key;
+                if (rank < p.M) s.order(rank) = i;
+            }
+        }
+        __syncthreads();
+    }
+    for (int r = threadIdx.x; r < p.M; r += TH) {
+        int token = p.pad, over = 1;
+        float score = kNegInf;
+        if (r < n) {
+            const uint64_t key = s.key(s.order(r));
+            token = (int)~(uint32_t)key;
+            const float z = float_of_order((uint32_t)(key >> 32));
+            score = dd_add(dd_mul(two_sum(z, -s.zmax(0)), dd{p.c_hi, p.c_lo}), dd{s.base(0).x, s.base(0).y}).hi;
+            over = p.eos >= 0 && token == p.eos;
+        } else if (r == 0 && c.nover) {
+            score = start_score(p, g, 0);
+        }
+        const long long o = (long long)g * p.M + r;
+        p.tokens[o] = token;
+        p.ancestors[o] = 0;
+        p.out_scores[o] = score;
+        if (p.out_finished) p.out_finished[o] = over;
+    }
+}
+
+template <int DT, int TH, bool ONE>
+__global__ void __launch_bounds__(TH, TH == kBeamWide ? 1 : ONE ? 8 : 5) beam_kernel(const __grid_constant__ BeamParams p) {
     __shared__ BeamCounts c;
     const BeamShared s = beam_shared(p.N, p.M);
     constexpr int kWarps = TH / 32;
@@ -787,7 +981,7 @@ __global__ void __launch_bounds__(TH, TH == kBeamWide ? 2 : 8) beam_kernel(const
             live += __popc(l);
             over += __popc(o);
         }
-        if (lane == 0) c.nlive = live, c.nover = over;
+        if (lane == 0) c.nlive = live, c.nover = over, c.best = 0;
     }
     __syncthreads();
     const int items = c.nlive * p.cpr;
@@ -810,20 +1004,23 @@ __global__ void __launch_bounds__(TH, TH == kBeamWide ? 2 : 8) beam_kernel(const
         __syncthreads();
         if (!c.last) return;
     }
-    beam_finish<DT, TH>(p, s, c, g);
+    if constexpr (ONE)
+        row_finish<DT, TH>(p, s, c, g);
+    else
+        beam_finish<DT, TH>(p, s, c, g);
 }
 
-template <int DT, int TH>
+template <int DT, int TH, bool ONE>
 static cudaError_t launch_beam_as(const BeamParams& p, cudaStream_t st) {
     const size_t shared = beam_shared_bytes(p.N, p.M, p.N * p.cpr, TH);
     if (shared > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(beam_kernel<DT, TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+        const cudaError_t e = cudaFuncSetAttribute(beam_kernel<DT, TH, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return e;
         }
     }
-    beam_kernel<DT, TH><<<(unsigned)p.G * (unsigned)p.blocks, TH, shared, st>>>(p);
+    beam_kernel<DT, TH, ONE><<<(unsigned)p.G * (unsigned)p.blocks, TH, shared, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -833,11 +1030,14 @@ cudaError_t launch_beam(const BeamParams& p0, int dtype, cudaStream_t st) {
     const bool many = p.G >= 2 * sms;
     // few groups: a chunk for each warp, as long as all blocks run at the same time
     const long long chunks = (long long)p.N * p.cpr, want = (chunks + kBeamWide / 32 - 1) / (kBeamWide / 32);
-    const long long fit = many ? 1 : 2ll * sms / p.G;
+    const long long fit = many ? 1 : (long long)sms / p.G;
     p.blocks = (int)(want < fit ? want : fit);
     if (p.blocks < 1) p.blocks = 1;
-    if (dtype == 0) return many ? launch_beam_as<0, kBeamNarrow>(p, st) : launch_beam_as<0, kBeamWide>(p, st);
-    return many ? launch_beam_as<1, kBeamNarrow>(p, st) : launch_beam_as<1, kBeamWide>(p, st);
+    const auto launch = many ? dtype == 0 ? p.N == 1 ? launch_beam_as<0, kBeamNarrow, true> : launch_beam_as<0, kBeamNarrow, false>
+                                          : p.N == 1 ? launch_beam_as<1, kBeamNarrow, true> : launch_beam_as<1, kBeamNarrow, false>
+                             : dtype == 0 ? p.N == 1 ? launch_beam_as<0, kBeamWide, true> : launch_beam_as<0, kBeamWide, false>
+                                          : p.N == 1 ? launch_beam_as<1, kBeamWide, true> : launch_beam_as<1, kBeamWide, false>;
+    return launch(p, st);
 }
 
 }  // namespace smcsd

@@ -11,7 +11,7 @@ namespace smcsd {
 
 constexpr int kBeamMostBeams = 256;  // of a group
 constexpr int kBeamMost = 256;       // selected of a group
-constexpr int kBeamSets = 8;         // sets of 32 16-byte vectors in a chunk of 4 KB
+constexpr int kBeamSets = 16;        // sets of 16 16-byte vectors in a chunk of 4 KB
 constexpr int kBeamMostChunks = 40960;  // of a group: their scores stand in shared memory
 
 struct BeamParams {
