@@ -299,17 +299,9 @@ def kv_pagetable_remap(ancestors, resampled, G, N, table_in, pages_per_seq, num_
     """Returns (table_out, refcount or None)."""
     if stream is not None:
         return _on(stream, kv_pagetable_remap, locals())
-    dev = table_in.device
-    ws = ws or Workspace(OP_PAGETABLE_REMAP, G, 0, 1, dev)
-    table_out = _out(table_out, table_in.shape, torch.int32, dev)
-    if with_refcount and refcount is None:
-        refcount = torch.empty(num_pages, dtype=torch.int32, device=dev)
-    w, n = ws.args
-    rc = load().kv_pagetable_remap(_ptr(ancestors), _ptr(resampled), G, N, _ptr(table_in),
-                                   _ptr(table_out), pages_per_seq, _ptr(refcount), num_pages, w, n,
-                                   _stream())
-    _check(rc, "kv_pagetable_remap")
-    return table_out, refcount
+    ws = ws or Workspace(OP_PAGETABLE_REMAP, G, 0, 1, table_in.device)
+    return (_calls or _native()).kv_pagetable_remap(ancestors, resampled, G, N, table_in, pages_per_seq, num_pages, table_out,
+                                                    refcount, bool(with_refcount), ws.ptr, ws.nbytes)
 
 
 def pacer_block_stop(hidden, w, c, S, b, max_blocks, d, t0, rho, ws=None, lengths=None,
@@ -522,8 +514,8 @@ def _native():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
-                      ("kv_slot_map", "kv_append", "tree_mask", "tree_attention", "logits_process", "beam_select",
-                       "state_reorder", "kv_fork", "kv_free", "kv_compact", "kv_copy_pages", "distill_loss")), _check)
+                      ("kv_slot_map", "kv_append", "tree_mask", "tree_attention", "logits_process", "kv_pagetable_remap",
+                       "beam_select", "state_reorder", "kv_fork", "kv_free", "kv_compact", "kv_copy_pages", "distill_loss")), _check)
         _calls = module
     return _calls
 

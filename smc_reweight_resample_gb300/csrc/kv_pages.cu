@@ -75,12 +75,8 @@ cudaError_t launch_reorder(const ReorderParams& p0, cudaStream_t st) {
 // ------------------------------------------------------------------------------------------
 
 constexpr int kForkThreads = 256;
-
-__global__ void __launch_bounds__(kForkThreads) fork_counts_kernel(const __grid_constant__ ForkParams p) {
-    griddep_launch_dependents();
-    for (long long i = (long long)blockIdx.x * kForkThreads + threadIdx.x; i < p.num_pages; i += (long long)gridDim.x * kForkThreads)
-        p.ref_out[i] = __ldg(p.ref_in + i);
-}
+constexpr int kForkEntries = 4;   // of a thread
+constexpr int kForkMost = 65536;  // entries and pages that one cluster takes
 
 // A page id of a table: whether it is counted. -1 is no page.
 __device__ __forceinline__ bool fork_counts(const ForkParams& p, int id) {
@@ -89,57 +85,116 @@ __device__ __forceinline__ bool fork_counts(const ForkParams& p, int id) {
     return false;
 }
 
-// One thread an entry of the new table. Counts change where an entry does: what a sequence keeps costs no atomic.
-__global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constant__ ForkParams p) {
-    const int P = p.pages_per_seq;
-    const long long n = (long long)p.S * P;
-    bool waited = false;
-    for (long long i = (long long)blockIdx.x * kForkThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kForkThreads) {
-        const int s = (int)(i / P), j = (int)(i - (long long)s * P);
-        int parent = p.parents ? __ldg(p.parents + s) : s;
-        const int length = p.lengths ? __ldg(p.lengths + s) : INT_MAX;
-        bool all = length == INT_MAX;
-        if (parent < -1 || parent >= p.S || length < 0) {
-            raise_error(p.ws, kErrRange);
-            parent = s;
-            all = true;
-        }
-        const int old = __ldg(p.table_in + i);
-        int id = -1;
-        if (parent >= 0 && (all || j < (int)(((long long)length + (1 << p.page_shift) - 1) >> p.page_shift)))
-            id = parent == s ? old : __ldg(p.table_in + (long long)parent * P + j);
-        p.table_out[i] = id;
-        if (id == old) {
-            fork_counts(p, id);
-            continue;
-        }
-        if (!waited) {
-            griddep_wait();  // the counts have been copied
-            waited = true;
-        }
-        if (fork_counts(p, id)) atomicAdd(p.ref_out + id, 1);
-        if (fork_counts(p, old) && atomicSub(p.ref_out + old, 1) <= 0) raise_error(p.ws, kErrRange);  // held, but not counted
+// Sequence s's parent, and how many entries of the parent's row it takes.
+__device__ __forceinline__ void fork_row(const ForkParams& p, int s, int& parent, int& pages) {
+    parent = p.parents ? __ldg(p.parents + s) : s;
+    const int length = p.lengths ? __ldg(p.lengths + s) : INT_MAX;
+    pages = length == INT_MAX ? p.pages_per_seq : (int)(((long long)length + (1 << p.page_shift) - 1) >> p.page_shift);
+    if (parent < -1 || parent >= p.S || length < 0) {
+        raise_error(p.ws, kErrRange);  // kept as it is
+        parent = s;
+        pages = p.pages_per_seq;
     }
-    if (!waited) griddep_wait();
+    if (parent < 0) pages = 0;
+}
+// Counts change where an entry does: what a sequence keeps costs no atomic.
+__device__ __forceinline__ void fork_change(const ForkParams& p, int id, int old) {
+    if (fork_counts(p, id)) atomicAdd(p.ref_out + id, 1);
+    if (fork_counts(p, old) && atomicSub(p.ref_out + old, 1) <= 0) raise_error(p.ws, kErrRange);  // held, but not counted
+}
+
+// Small tables: one cluster copies the counts and writes the new table, meets, and changes the counts.
+constexpr int kForkClusterThreads = 512;
+__global__ void __launch_bounds__(kForkClusterThreads) fork_small_kernel(const __grid_constant__ ForkParams p, FastDiv by_row) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int first = (int)cl.block_rank() * kForkClusterThreads + threadIdx.x, step = (int)cl.num_blocks() * kForkClusterThreads;
+    const int P = p.pages_per_seq, n = p.S * P;
+#pragma unroll 4
+    for (int i = first; i < p.num_pages; i += step) p.ref_out[i] = __ldg(p.ref_in + i);
+    for (int i = first; i < n; i += step) {
+        const int s = (int)fast_div((uint32_t)i, by_row), j = i - s * P;
+        int parent, pages;
+        fork_row(p, s, parent, pages);
+        p.table_out[i] = j < pages ? __ldg(p.table_in + parent * P + j) : -1;
+    }
+    cl.sync();
+    for (int i = first; i < n; i += step) {
+        const int id = p.table_out[i], old = __ldg(p.table_in + i);  // the thread's own entry
+        if (id != old)
+            fork_change(p, id, old);
+        else
+            fork_counts(p, id);
+    }
+}
+
+__global__ void __launch_bounds__(kForkThreads) fork_counts_kernel(const __grid_constant__ ForkParams p) {
+    griddep_launch_dependents();
+    const long long i0 = (long long)blockIdx.x * kForkThreads * kForkEntries + threadIdx.x;
+    int x[kForkEntries];
+#pragma unroll
+    for (int k = 0; k < kForkEntries; ++k)
+        if (i0 + k * kForkThreads < p.num_pages) x[k] = __ldg(p.ref_in + i0 + k * kForkThreads);
+#pragma unroll
+    for (int k = 0; k < kForkEntries; ++k)
+        if (i0 + k * kForkThreads < p.num_pages) p.ref_out[i0 + k * kForkThreads] = x[k];
+}
+
+// A block takes up to 1024 entries of one row, four a thread.
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constant__ ForkParams p, int pieces) {
+    const int P = p.pages_per_seq, s = blockIdx.x / pieces, j0 = (blockIdx.x - s * pieces) * kForkThreads * kForkEntries + threadIdx.x;
+    const long long row = (long long)s * P;
+    int old[kForkEntries], id[kForkEntries], parent, pages;
+#pragma unroll
+    for (int k = 0; k < kForkEntries; ++k) old[k] = j0 + k * kForkThreads < P ? __ldg(p.table_in + row + j0 + k * kForkThreads) : -1;
+    fork_row(p, s, parent, pages);
+#pragma unroll
+    for (int k = 0; k < kForkEntries; ++k) {
+        const int j = j0 + k * kForkThreads;
+        id[k] = j >= pages || j >= P ? -1 : parent == s ? old[k] : __ldg(p.table_in + (long long)parent * P + j);
+    }
+#pragma unroll
+    for (int k = 0; k < kForkEntries; ++k)
+        if (j0 + k * kForkThreads < P) p.table_out[row + j0 + k * kForkThreads] = id[k];
+    griddep_wait();  // the counts have been copied
+#pragma unroll
+    for (int k = 0; k < kForkEntries; ++k) {
+        if (id[k] != old[k])
+            fork_change(p, id[k], old[k]);
+        else
+            fork_counts(p, id[k]);
+    }
 }
 
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t st) {
-    const long long cap = 16ll * device_sm_count();
-    long long b = ((long long)p.num_pages + kForkThreads - 1) / kForkThreads;
-    fork_counts_kernel<<<(unsigned)(b < cap ? b : cap), kForkThreads, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    b = ((long long)p.S * p.pages_per_seq + kForkThreads - 1) / kForkThreads;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(b < cap ? b : cap));
-    cfg.blockDim = dim3(kForkThreads);
     cfg.stream = st;
     cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fork_kernel, p);
+    const long long n = (long long)p.S * p.pages_per_seq;
+    if (n <= kForkMost && p.num_pages <= kForkMost) {
+        // one launch in place of two, as long as a cluster of eight blocks has no more than a few turns to take
+        const long long most = n > p.num_pages ? n : p.num_pages;
+        int C = 1;
+        while (C < 8 && most > C * kForkClusterThreads) C *= 2;
+        cfg.gridDim = dim3(C);
+        cfg.blockDim = dim3(kForkClusterThreads);
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = C;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        return cudaLaunchKernelEx(&cfg, fork_small_kernel, p, make_fastdiv((uint32_t)p.pages_per_seq));
+    }
+    constexpr long long kBlock = kForkThreads * kForkEntries;
+    fork_counts_kernel<<<(unsigned)((p.num_pages + kBlock - 1) / kBlock), kForkThreads, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int pieces = (int)((p.pages_per_seq + kBlock - 1) / kBlock);
+    if ((long long)pieces * p.S > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3((unsigned)pieces * (unsigned)p.S);
+    cfg.blockDim = dim3(kForkThreads);
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, fork_kernel, p, pieces);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -148,6 +203,24 @@ cudaError_t launch_fork(const ForkParams& p, cudaStream_t st) {
 
 constexpr int kCompactThreads = 1024;
 constexpr int kCompactWarps = kCompactThreads / 32;
+constexpr int kCompactMost = 8192;  // table entries that the planning cluster writes
+
+// Table entries and counts of the pages that move, once the moves are known.
+__device__ __forceinline__ void compact_apply(const CompactParams& p, int moves, int used, long long first, long long step) {
+    const int32_t* place = ws_ptr<const int32_t>(p.ws, p.place);
+    for (long long i = first; i < moves; i += step) p.ref_out[__ldcg(p.dst + i)] = __ldg(p.ref_in + __ldcg(p.src + i));
+#pragma unroll 4
+    for (long long i = first; i < p.entries; i += step) {
+        int id = __ldg(p.table_in + i);
+        if (id != -1) {
+            if (id < 0 || id >= p.num_pages || __ldg(p.ref_in + id) <= 0)
+                raise_error(p.ws, kErrRange);  // left as it is
+            else if (id >= used)
+                id = __ldcg(p.dst + __ldcg(place + id));
+        }
+        p.table_out[i] = id;
+    }
+}
 
 // Which page goes where: one cluster. Its warps share out the pages in order, in runs of 32 that a ballot counts. The number
 // of pages in use, U, is the border: a hole's place is the number of free pages before it, that of a page from behind the
@@ -228,31 +301,21 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(const __g
             }
         }
     }
-    cl.sync();  // no block's shared memory is read any more
+    cl.sync();  // the moves are there; no block's shared memory is read any more
+    if (p.small) compact_apply(p, moves, used, rank * kCompactThreads + threadIdx.x, C * kCompactThreads);
 }
 
 constexpr int kApplyThreads = 256;
 
-// Table entries and counts of the pages that move.
 __global__ void __launch_bounds__(kApplyThreads) compact_apply_kernel(const __grid_constant__ CompactParams p) {
-    const int32_t* place = ws_ptr<const int32_t>(p.ws, p.place);
-    const long long first = (long long)blockIdx.x * kApplyThreads + threadIdx.x, step = (long long)gridDim.x * kApplyThreads;
     griddep_wait();
-    const int moves = __ldcg(p.counts), used = __ldcg(p.counts + 1);
-    for (long long i = first; i < moves; i += step) p.ref_out[__ldcg(p.dst + i)] = __ldg(p.ref_in + __ldcg(p.src + i));
-    for (long long i = first; i < p.entries; i += step) {
-        int id = __ldg(p.table_in + i);
-        if (id != -1) {
-            if (id < 0 || id >= p.num_pages || __ldg(p.ref_in + id) <= 0)
-                raise_error(p.ws, kErrRange);  // left as it is
-            else if (id >= used)
-                id = __ldcg(p.dst + __ldcg(place + id));
-        }
-        p.table_out[i] = id;
-    }
+    compact_apply(p, __ldcg(p.counts), __ldcg(p.counts + 1), (long long)blockIdx.x * kApplyThreads + threadIdx.x,
+                  (long long)gridDim.x * kApplyThreads);
 }
 
-cudaError_t launch_compact(const CompactParams& p, cudaStream_t st) {
+cudaError_t launch_compact(const CompactParams& p0, cudaStream_t st) {
+    CompactParams p = p0;
+    p.small = p.entries <= kCompactMost;  // the cluster writes the table too: one launch in place of two
     // as many blocks as leave every warp about 128 pages, at most a portable cluster of 8
     int C = 1;
     while (C < 8 && p.num_pages > C * kCompactWarps * 128) C *= 2;
@@ -267,7 +330,7 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t st) {
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, compact_plan_kernel, p);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.small) return e;
     const long long cap = 16ll * device_sm_count(), most = p.entries > p.num_pages / 2 ? p.entries : p.num_pages / 2;
     long long b = (most + kApplyThreads - 1) / kApplyThreads;
     cfg.gridDim = dim3((unsigned)(b < cap ? b : cap));

@@ -116,6 +116,7 @@ static int fork_or_free(const int32_t* parents, const int32_t* lengths, int S, c
     const int shift = page_shift(page_size);
     if (S <= 0 || pages_per_seq <= 0 || shift < 0 || num_pages <= 0) return SMCSD_ERR_INVALID_ARG;
     if ((long long)pages_per_seq * page_size > 0x7fffffffLL) return SMCSD_ERR_INVALID_ARG;
+    if ((long long)S * ((pages_per_seq + 1023) / 1024) > 0x7fffffffLL) return SMCSD_ERR_INVALID_ARG;  // blocks
     int rc = check_ws(ws, ws_bytes, 256);
     if (rc) return rc;
     const ForkParams p{parents,  lengths, S,           table_in,  table_out, pages_per_seq,

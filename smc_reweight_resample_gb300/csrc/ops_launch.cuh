@@ -108,6 +108,7 @@ struct CompactParams {
     int32_t* counts;  // moves, pages in use
     void* ws;
     size_t place;  // int32 [num_pages]: which move a page from behind is
+    bool small;
 };
 
 inline size_t compact_place() { return kFrontBytes; }

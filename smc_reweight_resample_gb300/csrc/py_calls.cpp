@@ -32,6 +32,7 @@ decltype(&kv_append) f_append;
 decltype(&tree_mask) f_tree_mask;
 decltype(&tree_attention) f_attention;
 decltype(&logits_process) f_logits;
+decltype(&kv_pagetable_remap) f_remap;
 decltype(&beam_select) f_beam;
 decltype(&state_reorder) f_reorder;
 decltype(&kv_fork) f_fork;
@@ -208,12 +209,13 @@ PyObject* tuple(std::initializer_list<at::Tensor> list) {
 
 PyObject* py_bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        Args a(args, n, 13);
+        Args a(args, n, 14);
         f_slot_map = reinterpret_cast<decltype(f_slot_map)>((uintptr_t)a.integer());
         f_append = reinterpret_cast<decltype(f_append)>((uintptr_t)a.integer());
         f_tree_mask = reinterpret_cast<decltype(f_tree_mask)>((uintptr_t)a.integer());
         f_attention = reinterpret_cast<decltype(f_attention)>((uintptr_t)a.integer());
         f_logits = reinterpret_cast<decltype(f_logits)>((uintptr_t)a.integer());
+        f_remap = reinterpret_cast<decltype(f_remap)>((uintptr_t)a.integer());
         f_beam = reinterpret_cast<decltype(f_beam)>((uintptr_t)a.integer());
         f_reorder = reinterpret_cast<decltype(f_reorder)>((uintptr_t)a.integer());
         f_fork = reinterpret_cast<decltype(f_fork)>((uintptr_t)a.integer());
@@ -222,7 +224,7 @@ PyObject* py_bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
         f_copy = reinterpret_cast<decltype(f_copy)>((uintptr_t)a.integer());
         f_distill = reinterpret_cast<decltype(f_distill)>((uintptr_t)a.integer());
         Py_XDECREF(f_error);
-        f_error = Py_NewRef(args[12]);
+        f_error = Py_NewRef(args[13]);
         Py_RETURN_NONE;
     });
 }
@@ -484,6 +486,41 @@ PyObject* py_reorder(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// A contiguous CUDA tensor's address, or null.
+int32_t* words(const at::Tensor* t) {
+    if (!t) return nullptr;
+    if (!t->is_cuda()) value_error("tensor must be on the CUDA device");
+    if (!t->is_contiguous()) value_error("tensor must be contiguous");
+    return static_cast<int32_t*>(t->data_ptr());
+}
+
+// kv_pagetable_remap(ancestors, resampled, G, N, table_in, pages_per_seq, num_pages, table_out, refcount, with_refcount, ws, bytes)
+PyObject* py_remap(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args a(args, n, 12);
+        const at::Tensor& ancestors = a.some();
+        const at::Tensor* resampled = a.tensor();
+        const int G = a.size(), N = a.size();
+        const at::Tensor& table = a.some();
+        const int pages_per_seq = a.size(), num_pages = a.size();
+        const at::Tensor *table_in_out = a.tensor(), *refcount = a.tensor();
+        const bool with_refcount = a.integer() != 0;
+        if (!table.is_cuda()) value_error("tensor must be on the CUDA device");
+        const c10::cuda::CUDAGuard guard(table.device());
+        const at::Tensor table_out = table_in_out ? *table_in_out : at::empty(table.sizes(), table.options().dtype(at::kInt));
+        at::Tensor ref;
+        if (refcount)
+            ref = *refcount;
+        else if (with_refcount)
+            ref = at::empty({num_pages}, table.options().dtype(at::kInt));
+        const Tail t(a, table);
+        check(f_remap(words(&ancestors), words(resampled), G, N, words(&table), words(&table_out), pages_per_seq,
+                      ref.defined() ? words(&ref) : nullptr, num_pages, t.ws, t.bytes, t.stream),
+              "kv_pagetable_remap");
+        return tuple({table_out, ref});
+    });
+}
+
 // kv_fork(table_in, refcount_in, parents, page_size, lengths, table_out, refcount_out, ws, bytes)
 PyObject* py_fork(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
@@ -632,6 +669,7 @@ PyMethodDef methods[] = {
     {"tree_mask", (PyCFunction)(void (*)(void))py_tree_mask, METH_FASTCALL, nullptr},
     {"tree_attention", (PyCFunction)(void (*)(void))py_attention, METH_FASTCALL, nullptr},
     {"logits_process", (PyCFunction)(void (*)(void))py_logits, METH_FASTCALL, nullptr},
+    {"kv_pagetable_remap", (PyCFunction)(void (*)(void))py_remap, METH_FASTCALL, nullptr},
     {"beam_select", (PyCFunction)(void (*)(void))py_beam, METH_FASTCALL, nullptr},
     {"state_reorder", (PyCFunction)(void (*)(void))py_reorder, METH_FASTCALL, nullptr},
     {"kv_fork", (PyCFunction)(void (*)(void))py_fork, METH_FASTCALL, nullptr},
