@@ -4,9 +4,9 @@
 // leave to the rest (0 where the list is taken for everything):
 //   loss = sum_k p_k (log p_k - log q_k) + p_r (log p_r - log q_r),     q_r = sum of q over the tokens that are not listed;
 //   dloss / dz_v = c (P q_v - p_v) for a listed v,  c q_v (P - p_r / q_r) for others,     P = sum p + p_r.
-// A row is read once: a cluster of blocks holds it in shared memory, its listed tokens are taken out of it (their sum is kept apart,
-// so that q_r is a sum and no difference), the blocks' maxima and sums meet in the cluster's shared memories, and each block writes
-// its share of the gradient from what it holds.
+// For the gradient a cluster of blocks holds a row in shared memory: read once, added up, and written from there when the blocks'
+// sums have met in the cluster's shared memories. For the loss alone rows are read to registers. Where there is a rest, the listed
+// tokens are left out of the sum, so that q_r is a sum and no difference.
 #include <cooperative_groups.h>
 
 #include "f32x2.cuh"
@@ -18,6 +18,8 @@ namespace cg = cooperative_groups;
 namespace smcsd {
 
 constexpr int kDistillThreads = 256, kDistillMostThreads = 512;
+constexpr int kDistillStaged = 2560;  // vectors of a block that holds its share, as long as sixteen blocks are enough for a row
+constexpr int kDistillRead = 16384;   // of a block that reads it, where rows are many
 static_assert(kDistillThreads >= kDistillMostTokens, "a thread for each listed token");
 
 __device__ __forceinline__ void copy16_async(uint32_t to, const void* from) {
@@ -95,8 +97,7 @@ struct DistillShared {
     float4 row;                          // the row's mass, the factor of the gradient and the reference that it goes with
     float a[kDistillMostTokens / 32], b[kDistillMostTokens / 32];
     dd d[kDistillMostTokens / 32];
-    int repeats;       // whether a token is listed several times
-};
+    int repeats;};
 
 // Maximum, or sum, over the list's entries, one of each thread of the block's first `warps` warps, which alone call these.
 __device__ __forceinline__ void list_sync(int warps) { asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory"); }
@@ -127,18 +128,6 @@ __device__ __forceinline__ dd list_sum_dd(DistillShared& s, float v, int warps) 
     return a;
 }
 
-// Whether this thread's token stands in the list more than once.
-__device__ __forceinline__ bool list_repeats(int token, const DistillShared& s, int warps, int K) {
-    if (token < 0) token = -2 - (int)threadIdx.x;  // alike with nobody's
-    if (warps == 1) return __popc(__match_any_sync(0xffffffffu, token)) > 1;
-    int n = 0;
-    for (int k = 0; k < K; k += 4) {  // behind K there are -1
-        const int4 t = *reinterpret_cast<const int4*>(s.token + k);
-        n += (t.x == token) + (t.y == token) + (t.z == token) + (t.w == token);
-    }
-    return n > 1;
-}
-
 // This block's share of a row: n of the row's aligned vectors, the first of which begins at the row's element `e0`. It may begin
 // before the row (the row's first vector) and end behind it (its last).
 template <int DT>
@@ -159,6 +148,88 @@ struct Share {
     __device__ int whole_from() const { return e0 < 0 && n > 0 ? 1 : 0; }
     __device__ int whole_to() const { return n > 0 && e0 + n * Geo<DT>::kPerVec > V ? n - 1 : n; }
 };
+
+// Whether this thread's token stands in the list more than once.
+__device__ __forceinline__ bool list_repeats(int token, const DistillShared& s, int warps, int K) {
+    if (token < 0) token = -2 - (int)threadIdx.x;  // alike with nobody's
+    if (warps == 1) return __popc(__match_any_sync(0xffffffffu, token)) > 1;
+    int n = 0;
+    for (int k = 0; k < K; k += 4) {  // behind K there are -1
+        const int4 t = *reinterpret_cast<const int4*>(s.token + k);
+        n += (t.x == token) + (t.y == token) + (t.z == token) + (t.w == token);
+    }
+    return n > 1;
+}
+
+// A thread's entry of the row's list. All threads call this; whether the list has any mass.
+struct Entry {
+    int token;
+    float value;
+    // the teacher's probability and its logarithm; in the token's first place that of all its entries
+    float prob, logp, listed;
+    bool first;
+};
+__device__ __forceinline__ bool list_entry(const DistillParams& p, DistillShared& s, int r, Entry& e) {
+    const int tid = threadIdx.x;
+    e.token = -1;
+    e.value = kNegInf;
+    if (tid < p.K) {
+        e.token = __ldg(p.tokens + (long long)r * p.K + tid);
+        e.value = __ldg(p.values + (long long)r * p.K + tid);
+        if (e.token < 0 || e.token >= p.V) {
+            if (e.token != -1) raise_error(p.ws, kErrRange);
+            e.token = -1;
+            e.value = kNegInf;
+        } else if (!(e.value < kPosInf)) {
+            raise_error(p.ws, kErrNonfinite);
+        }
+    }
+    if (tid < kDistillMostTokens) s.token[tid] = e.token;
+    if (tid == 0) s.repeats = 0;
+    return __syncthreads_or(e.value > kNegInf);
+}
+// The teacher's probabilities, by the warps with entries: p_r and the sum of all are given back to all of their threads.
+__device__ __forceinline__ void list_teacher(const DistillParams& p, DistillShared& s, Entry& e, int lists, float& rest, float& mass) {
+    const int tid = threadIdx.x;
+    if (p.rest) {
+        e.logp = e.value;
+        e.prob = e.value > kNegInf ? expf(e.value) : 0.0f;
+        const dd sum = list_sum_dd(s, e.prob, lists);
+        rest = fmaxf(dd_add(dd{1.0f, 0.0f}, dd_neg(sum)).hi, 0.0f);
+        mass = fmaxf(sum.hi, 1.0f);
+    } else {
+        const float top = list_max(s, e.value, lists);
+        const float x = e.value > kNegInf ? expf(e.value - top) : 0.0f;
+        const dd sum = list_sum_dd(s, x, lists);
+        e.logp = e.value - top - logf(sum.hi);
+        e.prob = x / sum.hi;
+    }
+    s.p[tid] = e.prob;
+    if (list_repeats(e.token, s, lists, p.K)) s.repeats = 1;
+    list_sync(lists);
+    // a token that is listed several times: its first place stands for all of them
+    e.listed = e.prob;
+    if (s.repeats && e.token >= 0) {
+        e.listed = 0.0f;
+        for (int k = p.K - 1; k >= 0; --k)
+            if (s.token[k] == e.token) {
+                e.listed += s.p[k];
+                e.first = k == tid;
+            }
+    }
+}
+// The loss, by the first block's warps with entries, from the row's mass and the rest's.
+__device__ __forceinline__ void list_loss(const DistillParams& p, DistillShared& s, const Entry& e, int lists, float z, float rest, Mass all, Mass R, int r) {
+    const float ls = logf(all.s);
+    float term = 0.0f;
+    if (e.prob > 0.0f) term = e.prob * (e.logp - ((z - all.m) * p.c - ls));
+    if (threadIdx.x == 0 && rest > 0.0f) term += rest * (logf(rest) - (logf(R.s) + (R.m - all.m) * p.c - ls));
+    const float loss = list_sum(s, term, lists);
+    if (threadIdx.x == 0) p.loss[r] = loss;
+}
+__device__ __forceinline__ Mass token_mass(const Entry& e, float z) {
+    return e.first ? Mass{z, z > kNegInf ? 1.0f : z != z ? z : 0.0f} : Mass{kNegInf, 0.0f};
+}
 
 // Elements of a vector one by one: f(e, bits) for those from `lo` to `hi` - 1.
 template <int DT, typename F>
@@ -184,6 +255,10 @@ __device__ __forceinline__ void fetch(const Share<DT>& h, uint4* to) {
     }
 }
 
+__device__ __forceinline__ void st_vec(char* p, const uint4& x) {
+    asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+
 // Writes f(i), a vector, for every vector i of the share to the row `out` of the gradient.
 template <int DT, int TH, typename F>
 __device__ __forceinline__ void write_share(const Share<DT>& h, char* out, F&& f) {
@@ -193,7 +268,7 @@ __device__ __forceinline__ void write_share(const Share<DT>& h, char* out, F&& f
     const bool alike = (reinterpret_cast<uintptr_t>(to) & 15u) == 0;
     const int from = alike ? h.whole_from() : h.n, upto = alike ? h.whole_to() : h.n;
 #pragma unroll 1
-    for (int i = from + threadIdx.x; i < upto; i += TH) *reinterpret_cast<uint4*>(to + 16ll * i) = f(i);
+    for (int i = from + threadIdx.x; i < upto; i += TH) st_vec(to + 16ll * i, f(i));
     if (from == 0 && upto == h.n) return;
     // the first and the last vector, or all of a row that lies otherwise than the logits'
     for (int i = threadIdx.x; i < h.n; i += TH) {
@@ -216,29 +291,16 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 2) distill_ker
     auto started = cl.barrier_arrive();  // the other blocks' shared memory may be written once all have come here
 
     const Share<DT> h(p, r, rank);
-    // the row's list
-    int token = -1;
-    float value = kNegInf;
-    if (tid < p.K) {
-        token = __ldg(p.tokens + (long long)r * p.K + tid);
-        value = __ldg(p.values + (long long)r * p.K + tid);
-        if (token < 0 || token >= p.V) {
-            if (token != -1) raise_error(p.ws, kErrRange);
-            token = -1;
-            value = kNegInf;
-        } else if (!(value < kPosInf)) {
-            raise_error(p.ws, kErrNonfinite);
-        }
-    }
-    if (tid < kDistillMostTokens) s.token[tid] = token;
-    if (tid == 0) s.repeats = 0;
+    Entry e{};
+    const bool some = list_entry(p, s, r, e);
+    const int token = e.token;
+    e.first = token >= 0;
     const float weight = p.weight ? __ldg(p.weight + r) : 1.0f;
-    char* out = p.grad ? static_cast<char*>(p.grad) + (long long)r * p.grad_stride * B : nullptr;
+    char* out = static_cast<char*>(p.grad) + (long long)r * p.grad_stride * B;
 
-    const bool some = __syncthreads_or(value > kNegInf);
     if (!some || (weight == 0.0f && !p.loss)) {
         cl.barrier_wait(std::move(started));
-        if (out) write_share<DT, TH>(h, out, [](int) { return make_uint4(0, 0, 0, 0); });
+        write_share<DT, TH>(h, out, [](int) { return make_uint4(0, 0, 0, 0); });
         if (rank == 0 && tid == 0 && p.loss) p.loss[r] = 0.0f;
         return;
     }
@@ -246,46 +308,17 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 2) distill_ker
     // meanwhile the teacher's probabilities
     const int lists = (p.K + 31) / 32;  // warps with entries
     const bool lister = tid < 32 * lists;
-    float logp = kNegInf, prob = 0.0f, rest = 0.0f, mass = 1.0f, listed = 0.0f;
-    bool first = token >= 0;
-    if (lister) {
-        if (p.rest) {
-            logp = value;
-            prob = value > kNegInf ? expf(value) : 0.0f;
-            const dd sum = list_sum_dd(s, prob, lists);
-            rest = fmaxf(dd_add(dd{1.0f, 0.0f}, dd_neg(sum)).hi, 0.0f);
-            mass = fmaxf(sum.hi, 1.0f);
-        } else {
-            const float top = list_max(s, value, lists);
-            const float e = value > kNegInf ? expf(value - top) : 0.0f;
-            const dd sum = list_sum_dd(s, e, lists);
-            logp = value - top - logf(sum.hi);
-            prob = e / sum.hi;
-        }
-        s.p[tid] = prob;
-        if (list_repeats(token, s, lists, p.K)) s.repeats = 1;
-    }
-    copies_done();
-    __syncthreads();
-    // the listed tokens' logits. Where there is a rest, they are taken out of the share, so that its mass is a sum and no difference
+    float rest = 0.0f, mass = 1.0f;
+    if (lister) list_teacher(p, s, e, lists, rest, mass);
     T* elems = reinterpret_cast<T*>(s_row);
     const int at = token - h.e0;
     const bool mine = token >= 0 && at >= 0 && at < h.n * PV;
     float z = kNegInf;
-    if (mine) z = bits_to_float<DT>((uint32_t)elems[at]);
-    if (lister) {
-        // a token that is listed several times: its first place stands for all of them
-        listed = prob;
-        if (s.repeats && token >= 0) {
-            listed = 0.0f;
-            for (int k = p.K - 1; k >= 0; --k)
-                if (s.token[k] == token) {
-                    listed += s.p[k];
-                    first = k == tid;
-                }
-        }
-    }
-    if (p.rest) {
+    copies_done();
+    // a thread has copied the vectors that it adds up itself, but for a first or last one that does not lie in the row whole
+    if (p.rest || h.whole_from() > 0 || h.whole_to() < h.n) __syncthreads();
+    if (p.rest) {  // the listed tokens are taken out of the share
+        if (mine) z = bits_to_float<DT>((uint32_t)elems[at]);
         if (lister) list_sync(lists);
         if (mine) elems[at] = (T)neg_inf_bits<DT>();
         __syncthreads();
@@ -300,7 +333,7 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 2) distill_ker
         f32x2 sum[Vec<DT>::kPairs];
 #pragma unroll
         for (int k = 0; k < Vec<DT>::kPairs; ++k) sum[k] = pair(0.0f, 0.0f);
-#pragma unroll 2
+#pragma unroll 1
         for (int i = tid; i < h.n; i += TH) {
             const Vec<DT> v(s_row[i]);
 #pragma unroll
@@ -328,12 +361,13 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 2) distill_ker
     a = warp_mass(a, p.c2);
     Mass b{kNegInf, 0.0f};
     if (lister && p.rest) {
-        if (first && mine) b = Mass{z, z > kNegInf ? 1.0f : z != z ? z : 0.0f};
+        if (mine) b = token_mass(e, z);
         b = warp_mass(b, p.c2);
     }
     if ((tid & 31) == 0) s.q[tid >> 5] = make_float4(a.m, a.s, b.m, b.s);
     cl.barrier_wait(std::move(started));
     __syncthreads();
+    if (mine && !p.rest) z = bits_to_float<DT>((uint32_t)elems[at]);
     if (mine) *cl.map_shared_rank(&s.z[tid], 0) = z;
     if (tid < 32) {
         const Masses q = join_lanes(s.q, TH / 32, p.c2);
@@ -358,15 +392,7 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 2) distill_ker
     __syncthreads();
     const float4 row = s.row;
     const Mass all{row.x, row.y};
-    if (rank == 0 && lister && p.loss) {
-        const float ls = logf(all.s);
-        float term = 0.0f;
-        if (prob > 0.0f) term = prob * (logp - ((s.z[tid] - all.m) * p.c - ls));
-        if (tid == 0 && rest > 0.0f) term += rest * (logf(rest) - (logf(s.q[0].y) + (s.q[0].x - all.m) * p.c - ls));
-        const float loss = list_sum(s, term, lists);
-        if (tid == 0) p.loss[r] = loss;
-    }
-    if (!out) return;
+    if (rank == 0 && lister && p.loss) list_loss(p, s, e, lists, s.z[tid], rest, all, Mass{s.q[0].x, s.q[0].y}, r);
     const f32x2 m2 = pair(-row.w, -row.w), scale2 = pair(row.z, row.z);
     write_share<DT, TH>(h, out, [&](int i) {
         Vec<DT> v(s_row[i]);
@@ -375,25 +401,171 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 2) distill_ker
         return v.packed();
     });
     __syncthreads();  // the listed tokens' places have been written as part of the rest
-    if (mine && first) {
+    if (mine && e.first) {
         const float q = exp2f((z - all.m) * p.c2) / all.s;
-        reinterpret_cast<T*>(out)[token] = (T)round_to<DT>(wc * (mass * q - listed));
+        reinterpret_cast<T*>(out)[token] = (T)round_to<DT>(wc * (mass * q - e.listed));
     }
 }
 
-template <int DT, int TH>
-static cudaError_t launch_distill_as(const DistillParams& p, cudaStream_t st) {
-    const size_t shared = 16 * (size_t)p.vecs;
+// ------------------------------------------------------------------------------------------
+// the loss alone
+// ------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint4 ld_once(const char* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+// Vector i of the share where a part of it lies outside the row: -inf there.
+template <int DT>
+__device__ __forceinline__ uint4 ragged_vec(const Share<DT>& h, int i) {
+    constexpr int PV = Geo<DT>::kPerVec;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = DT == 0 ? neg_inf_bits<0>() : neg_inf_bits<1>() * 0x10001u;
+#pragma unroll
+    for (int e = 0; e < PV; ++e) {
+        const int v = h.e0 + i * PV + e;
+        if (v < 0 || v >= h.V) continue;
+        const uint32_t bits = logit_bits<DT>(h.at, (long long)i * PV + e);
+        if (DT == 0)
+            w[e & 3] = bits;
+        else
+            w[(e >> 1) & 3] = e & 1 ? (w[(e >> 1) & 3] & 0xffffu) | bits << 16 : (w[(e >> 1) & 3] & 0xffff0000u) | bits;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Calls f(i, vector i) for this thread's vectors of the share, kEach of them on the way together.
+template <int DT, int kEach, typename F>
+__device__ __forceinline__ void each_vec(const Share<DT>& h, F&& f) {
+    const int from = h.whole_from(), upto = h.whole_to();
+    int i = from + threadIdx.x;
+    const char* at = h.at + 16ll * i;
+    for (; i < upto; i += kEach * kDistillThreads, at += 16 * kEach * kDistillThreads) {
+        uint4 x[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            if (i + k * kDistillThreads < upto) x[k] = ld_once(at + 16 * k * kDistillThreads);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            if (i + k * kDistillThreads < upto) f(i + k * kDistillThreads, x[k]);
+    }
+    // a first and a last vector that do not lie in the row whole
+    if (threadIdx.x == 0 && from > 0) f(0, ragged_vec<DT>(h, 0));
+    if (threadIdx.x == 1 && h.n - 1 >= upto && h.n - 1 >= from) f(h.n - 1, ragged_vec<DT>(h, h.n - 1));
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kDistillThreads, 5) distill_loss_kernel(const __grid_constant__ DistillParams p) {
+    constexpr int PV = Geo<DT>::kPerVec, B = Geo<DT>::kBytes, kEach = 4, kWarps = kDistillThreads / 32;
+    extern __shared__ uint32_t s_listed[];  // where there is a rest: a bit for each element of the share, set if it is listed
+    __shared__ DistillShared s;
+    cg::cluster_group cl = cg::this_cluster();
+    const int C = p.ctas, rank = (int)cl.block_rank(), tid = threadIdx.x;
+    const int r = blockIdx.x / C;
+    auto started = cl.barrier_arrive();
+    const Share<DT> h(p, r, rank);
+    if (p.rest)
+        for (int i = tid; i < (h.n * PV + 31) / 32; i += kDistillThreads) s_listed[i] = 0;
+    Entry e{};
+    const bool some = list_entry(p, s, r, e);
+    if (!some) {
+        cl.barrier_wait(std::move(started));
+        if (rank == 0 && tid == 0) p.loss[r] = 0.0f;
+        return;
+    }
+    e.first = e.token >= 0;
+    float z = kNegInf;  // of all shares: with a rest every block needs the listed tokens' mass, without one the first the loss
+    if (e.token >= 0 && (p.rest || rank == 0))
+        z = logit_at<DT>(static_cast<const char*>(p.logits) + (long long)r * p.row_stride * B, e.token);
+    if (p.rest) {
+        const int at = e.token - h.e0;
+        if (e.token >= 0 && at >= 0 && at < h.n * PV) atomicOr(s_listed + (at >> 5), 1u << (at & 31));
+        __syncthreads();
+    }
+    const auto unlisted = [&](int i, uint4 x) {  // -inf in the listed tokens' places
+        if (p.rest) {
+            const unsigned bits = reinterpret_cast<const unsigned char*>(s_listed)[i * PV >> 3] >> (i * PV & 7);
+            if (bits & ((1u << PV) - 1u)) {
+                const auto hide = [&](uint32_t w, unsigned b) {
+                    if (DT == 0) return b & 1u ? neg_inf_bits<0>() : w;
+                    return (b & 1u ? neg_inf_bits<1>() : w & 0xffffu) | (b & 2u ? neg_inf_bits<1>() << 16 : w & 0xffff0000u);
+                };
+                constexpr int kStep = PV / 4;
+                x = make_uint4(hide(x.x, bits), hide(x.y, bits >> kStep), hide(x.z, bits >> (2 * kStep)), hide(x.w, bits >> (3 * kStep)));
+            }
+        }
+        return x;
+    };
+    const auto top_of = [](const uint4& x) { return word_max<DT>(word_max<DT>(x.x, x.y), word_max<DT>(x.z, x.w)); };
+    // as in the other kernel: relative to the first vector's maximum, or if that says little to the thread's own
+    const f32x2 c2 = pair(p.c2, p.c2);
+    uint32_t top = DT == 0 ? neg_inf_bits<0>() : neg_inf_bits<1>() * 0x10001u;
+    if (tid < h.n) top = top_of(unlisted(tid, tid >= h.whole_from() && tid < h.whole_to() ? ld_once(h.at + 16ll * tid) : ragged_vec<DT>(h, tid)));
+    Mass a{kNegInf, 0.0f};
+#pragma unroll 1
+    for (bool whole = false;; whole = true) {
+        a.m = word_value<DT>(top);
+        const float m0 = a.m > kNegInf ? -a.m : 0.0f;
+        const f32x2 m2 = pair(m0, m0);
+        f32x2 sum[Vec<DT>::kPairs];
+#pragma unroll
+        for (int k = 0; k < Vec<DT>::kPairs; ++k) sum[k] = pair(0.0f, 0.0f);
+        each_vec<DT, kEach>(h, [&](int i, const uint4& x) {
+            const Vec<DT> v(unlisted(i, x));
+#pragma unroll
+            for (int k = 0; k < Vec<DT>::kPairs; ++k) sum[k] = add2(sum[k], exp2_2(mul2(add2(v.x[k], m2), c2)));
+        });
+#pragma unroll
+        for (int k = 1; k < Vec<DT>::kPairs; ++k) sum[0] = add2(sum[0], sum[k]);
+        float lo, hi;
+        halves(sum[0], lo, hi);
+        a.s = lo + hi;
+        if (whole || (a.m > kNegInf && a.s < 1.2676506e30f)) break;  // 2^100
+        each_vec<DT, 1>(h, [&](int i, const uint4& x) { top = word_max<DT>(top, top_of(unlisted(i, x))); });
+    }
+    a = warp_mass(a, p.c2);
+    const int lists = (p.K + 31) / 32;
+    const bool lister = tid < 32 * lists;
+    Mass b{kNegInf, 0.0f};
+    float rest = 0.0f, mass = 1.0f;
+    if (lister) {
+        if (rank == 0) list_teacher(p, s, e, lists, rest, mass);
+        if (p.rest && rank == 0) b = warp_mass(token_mass(e, z), p.c2);
+    }
+    if ((tid & 31) == 0) s.q[tid >> 5] = make_float4(a.m, a.s, b.m, b.s);
+    cl.barrier_wait(std::move(started));
+    __syncthreads();
+    if (tid < 32) {
+        const Masses q = join_lanes(s.q, kWarps, p.c2);
+        if (tid == 0) *cl.map_shared_rank(&s.part[rank], 0) = make_float4(q.a.m, q.a.s, q.b.m, q.b.s);
+    }
+    cl.sync();
+    if (rank == 0 && lister) {
+        const Masses row = join_lanes(s.part, C, p.c2);
+        const Mass R = row.a, all = p.rest ? join(R, row.b, p.c2) : R;
+        if (tid == 0 && !(all.s > 0.0f && all.s < kPosInf && all.m < kPosInf)) raise_error(p.ws, kErrNonfinite);
+        list_loss(p, s, e, lists, z, rest, all, R, r);
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// launches
+// ------------------------------------------------------------------------------------------
+
+template <typename F>
+static cudaError_t launch_rows(F kernel, const DistillParams& p, int threads, size_t shared, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (shared > 40 * 1024) e = cudaFuncSetAttribute(distill_kernel<DT, TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
-    if (e == cudaSuccess && p.ctas > 8) e = cudaFuncSetAttribute(distill_kernel<DT, TH>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (shared > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+    if (e == cudaSuccess && p.ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return e;
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((long long)p.R * p.ctas));
-    cfg.blockDim = dim3(TH);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = shared;
     cfg.stream = st;
     cudaLaunchAttribute at{};
@@ -402,19 +574,29 @@ static cudaError_t launch_distill_as(const DistillParams& p, cudaStream_t st) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, distill_kernel<DT, TH>, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-cudaError_t launch_distill(const DistillParams& p0, int dtype, cudaStream_t st) {
-    DistillParams p = p0;
-    // shares of at most 40 KB, as long as sixteen blocks are enough for that
-    const long long bytes = (long long)p.V * (dtype == 0 ? 4 : 2), vecs = (bytes + 30) / 16;
+template <int DT>
+static cudaError_t launch_distill_as(DistillParams p, cudaStream_t st) {
+    const long long vecs = ((long long)p.V * Geo<DT>::kBytes + 30) / 16;
     p.ctas = 1;
-    while (p.ctas < kDistillMostCtas && vecs > p.ctas * 2560ll) p.ctas *= 2;
+    if (p.grad) {
+        while (p.ctas < kDistillMostCtas && vecs > p.ctas * (long long)kDistillStaged) p.ctas *= 2;
+        p.vecs = (int)((vecs + p.ctas - 1) / p.ctas);
+        const size_t shared = 16 * (size_t)p.vecs;
+        return p.vecs > kDistillStaged ? launch_rows(distill_kernel<DT, kDistillMostThreads>, p, kDistillMostThreads, shared, st)
+                                       : launch_rows(distill_kernel<DT, kDistillThreads>, p, kDistillThreads, shared, st);
+    }
+    while (p.ctas < kDistillMostCtas && vecs > p.ctas * (long long)kDistillRead) p.ctas *= 2;
+    // smaller shares where rows are few, for three turns of the blocks that run at a time
+    while (p.ctas < kDistillMostCtas && vecs > p.ctas * 1024ll && (long long)p.R * p.ctas < 15ll * device_sm_count()) p.ctas *= 2;
     p.vecs = (int)((vecs + p.ctas - 1) / p.ctas);
-    const bool large = p.vecs > 2560;
-    if (dtype == 0) return large ? launch_distill_as<0, kDistillMostThreads>(p, st) : launch_distill_as<0, kDistillThreads>(p, st);
-    return large ? launch_distill_as<1, kDistillMostThreads>(p, st) : launch_distill_as<1, kDistillThreads>(p, st);
+    return launch_rows(distill_loss_kernel<DT>, p, kDistillThreads, p.rest ? (size_t)p.vecs * Geo<DT>::kPerVec / 8 + 4 : 0, st);
+}
+
+cudaError_t launch_distill(const DistillParams& p, int dtype, cudaStream_t st) {
+    return dtype == 0 ? launch_distill_as<0>(p, st) : launch_distill_as<1>(p, st);
 }
 
 }  // namespace smcsd
