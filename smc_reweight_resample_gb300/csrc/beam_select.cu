@@ -15,7 +15,7 @@
 //   - reads these sets again and keeps what is not below the last of them: a little more than M candidates,
 //   - ranks them by counting.
 // Scores are compared as double-floats (FP64 runs at two lanes a clock here). Of one beam this
-// order is exact, whatever its sum; between beams it is as good as the sums (kTol). Where two scores of different beams that decide
+// order is exact, whatever its sum; between beams it is as good as the sums and their logarithms (kTol). Where two scores of different beams that decide
 // anything are nearer than that, the block computes these beams' sums again to 2e-10 and selects anew.
 #include "f32x2.cuh"
 #include "ops_launch.cuh"
@@ -31,7 +31,7 @@ constexpr int kBeamMostCands = 1024;  // candidates that are ranked
 // How far the scores of two beams may be off from one another with hardware exponentials. A sum, relative: the exponential 2^-22; its
 // argument's roundings (of z - m, of c log2 e and of their product: 2.5 * 2^-24 of it, and it is 31 on the average at most, the
 // distribution's entropy over up to 2^31 tokens), times ln 2: 3.2e-6; 8 + 3 + 1 + 5 additions one after another and 8 + 5 of
-// chunks, 2^-24 each; the chunks' scale 2^-22: 6.1e-6. Two of them: 1.2e-5.
+// chunks, 2^-24 each; the chunks' scale 2^-22; the logarithm 4e-8: 6.1e-6. Two of them: 1.2e-5.
 constexpr float kTol = 1.25e-5f;
 
 // A score as an unsigned integer of the same order: the high float first, then the low one (of a normalised double-float). 0 is
@@ -500,6 +500,13 @@ __device__ __forceinline__ dd dd_log(dd v, const Exp2Table& T) {
     return dd_add(dd{y, 0.0f}, dd_add(r, dd{-0.5f * r.hi * r.hi, 0.0f}));
 }
 
+// log of a float to 4e-8: the exponent's part in double-floats, the mantissa's (of 0.75 to 1.5) by the float logarithm.
+__device__ __forceinline__ dd dd_log_fast(float v) {
+    const int k = (__float_as_int(v) - 0x3f400000) >> 23;
+    const float m = __int_as_float(__float_as_int(v) - (k << 23));
+    return dd_add(dd_mul_f(dd{SMCSD_LN2_HI, SMCSD_LN2_LO}, (float)k), dd{logf(m), 0.0f});
+}
+
 // Candidates by beam and token; kEnded stands for the token of a finished beam.
 constexpr int kEnded = -1;
 __device__ __forceinline__ uint64_t place_of(int beam, int token) { return (uint64_t)(uint32_t)beam << 32 | (uint32_t)token; }
@@ -759,9 +766,9 @@ __device__ __forceinline__ Mass row_mass(const BeamParams& p, long long row) {
 }
 
 // A beam's constant from its sum, by whole warps: s_i - log S_i, or none if there is no mass.
-__device__ __forceinline__ void set_base(const BeamParams& p, const BeamShared& s, BeamCounts& c, int g, int beam, float m, dd sum) {
+__device__ __forceinline__ void set_base(const BeamParams& p, const BeamShared& s, BeamCounts& c, int g, int beam, float m, dd sum, bool exact) {
     dd base{kNegInf, 0.0f};
-    if (sum.hi > 0.0f) base = dd_sub(dd{start_score(p, g, beam), 0.0f}, dd_log(sum, p.T));
+    if (sum.hi > 0.0f) base = dd_sub(dd{start_score(p, g, beam), 0.0f}, exact ? dd_log(sum, p.T) : dd_log_fast(sum.hi));
     if ((threadIdx.x & 31) == 0) {
         s.zmax(beam) = m;
         s.base(beam) = make_float2(base.hi, base.lo);
@@ -786,7 +793,7 @@ __device__ __forceinline__ void beam_finish(const BeamParams& p, const BeamShare
         const float m = a.m, sum = a.s;
         const bool good = sum < kPosInf && m < kPosInf;
         if (!good && lane == 0) raise_error(p.ws, kErrNonfinite);
-        set_base(p, s, c, g, beam, m, dd{good ? sum : 0.0f, 0.0f});
+        set_base(p, s, c, g, beam, m, dd{good ? sum : 0.0f, 0.0f}, false);
     }
     // the beams' constants: scores are c (z - m) + base
     for (int i = threadIdx.x; i < c.nover; i += TH) {
@@ -810,7 +817,7 @@ __device__ __forceinline__ void beam_finish(const BeamParams& p, const BeamShare
             if (!s.unsure(beam) || !(s.base(beam).x > kNegInf)) continue;  // the same for all threads
             const dd sum = precise_sum<DT, TH>(p, s, c, beam_row<DT>(p, rows + beam).row, s.zmax(beam));
             __syncthreads();
-            set_base(p, s, c, g, beam, s.zmax(beam), sum);
+            set_base(p, s, c, g, beam, s.zmax(beam), sum, true);
             __syncthreads();
         }
     }
@@ -886,7 +893,7 @@ __device__ __forceinline__ void row_finish(const BeamParams& p, const BeamShared
             const Mass a = row_mass(p, g);
             const bool good = a.s < kPosInf && a.m < kPosInf;
             if (!good && lane == 0) raise_error(p.ws, kErrNonfinite);
-            set_base(p, s, c, g, 0, a.m, dd{good ? a.s : 0.0f, 0.0f});
+            set_base(p, s, c, g, 0, a.m, dd{good ? a.s : 0.0f, 0.0f}, false);
         }
         __syncthreads();
         if (s.base(0).x > kNegInf) {
