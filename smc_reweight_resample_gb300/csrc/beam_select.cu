@@ -350,45 +350,38 @@ __device__ void sort_list(int* list, int n) {
     __syncthreads();
 }
 
-// The level that is looked at first: all sets of the group's live beams where they are few, else all their chunks.
-struct FirstLevel {
-    const float* z_;  // maxima of the group's rows
-    int per, n, log;  // items of a row, of the live rows; log2 of the items of a chunk
-    FastDiv chunks;   // by the chunks of a row
-    __device__ __forceinline__ int beam(const BeamShared& s, int i) const { return s.live((int)fast_div((uint32_t)i >> log, chunks)); }
+// A level: the chunks of the group's live beams; the sets of all of them where they are few; or the sets of the chunks in list1.
+struct Level {
+    const float* maxima;  // of the group's rows
+    int cpr, n, log;      // chunks of a row, items, log2 of the items of a chunk
+    bool listed;
+    FastDiv chunks;       // by the chunks of a row
+    // an item's live beam, by its place among them, and where its maximum stands
+    __device__ __forceinline__ int chunk(const BeamShared& s, int i) const { return listed ? s.list1()[i >> log] : i >> log; }
+    __device__ __forceinline__ int beam(const BeamShared& s, int i) const { return s.live((int)fast_div((uint32_t)chunk(s, i), chunks)); }
     __device__ __forceinline__ float z(const BeamShared& s, int i) const {
-        const int l = (int)fast_div((uint32_t)i >> log, chunks);
-        return __ldcg(z_ + (long long)s.live(l) * per + (i - l * per));
+        const int k = chunk(s, i), l = (int)fast_div((uint32_t)k, chunks);
+        return __ldcg(maxima + (((long long)s.live(l) * cpr + (k - l * cpr)) << log) + (i & ((1 << log) - 1)));
     }
 };
+// The first level (sets at once, where they fit) or the second (the sets of n1 chunks).
 template <int TH>
-__device__ __forceinline__ FirstLevel first_level(const BeamParams& p, const BeamShared& s, int g, int nlive) {
-    FirstLevel v;
-    v.log = nlive * p.cpr <= beam_keys(s, p.N * p.cpr, TH) / kBeamSets ? 4 : 0;
+__device__ __forceinline__ Level level_of(const BeamParams& p, const BeamShared& s, int g, int nlive, bool second, int n1) {
     static_assert(kBeamSets == 16, "shifts by 4");
+    Level v;
+    v.log = second || nlive * p.cpr <= beam_keys(s, p.N * p.cpr, TH) / kBeamSets ? 4 : 0;
+    v.listed = second;
+    v.cpr = p.cpr;
+    v.n = (second ? n1 : nlive * p.cpr) << v.log;
     v.chunks = p.div_cpr;
-    v.per = p.cpr << v.log;
-    v.n = nlive * v.per;
-    v.z_ = ws_ptr<const float>(p.ws, v.log ? p.sets : p.maxima) + (long long)g * p.N * v.per;
+    v.maxima = ws_ptr<const float>(p.ws, v.log ? p.sets : p.maxima) + ((long long)g * p.N * p.cpr << v.log);
     return v;
 }
-// The sets of the chunks in list1.
-struct SecondLevel {
-    const float* z_;
-    int cpr;
-    FastDiv chunks;
-    __device__ __forceinline__ int beam(const BeamShared& s, int i) const { return s.live((int)fast_div((uint32_t)s.list1()[i / kBeamSets], chunks)); }
-    __device__ __forceinline__ float z(const BeamShared& s, int i) const {
-        const int chunk = s.list1()[i / kBeamSets], l = (int)fast_div((uint32_t)chunk, chunks);
-        return __ldcg(z_ + ((long long)s.live(l) * cpr + (chunk - l * cpr)) * kBeamSets + i % kBeamSets);
-    }
-};
 // Keys of a level's items, for what is not done as a rule.
-template <typename L>
 struct LevelKey {
     const BeamParams* p;
     BeamShared s;
-    L level;
+    Level level;
     __device__ __forceinline__ uint64_t operator()(int i) const {
         const int beam = level.beam(s, i);
         return score_key(*p, level.z(s, i), s.zmax(beam), s.base(beam));
@@ -397,8 +390,7 @@ struct LevelKey {
 // An item's score: in float32, off by at most three roundings (of the difference, of the factor, of the sum) of its terms, and for one beam in the order of
 // the logits; or as the high half of its key.
 constexpr float kScoreError = 3e-7f;
-template <typename L>
-__device__ __forceinline__ float level_score(const BeamParams& p, const BeamShared& s, const L& level, int i, float z, bool exact) {
+__device__ __forceinline__ float level_score(const BeamParams& p, const BeamShared& s, const Level& level, int i, float z, bool exact) {
     const int beam = level.beam(s, i);
     if (!exact) return z > kNegInf ? fmaf(p.c_hi, z - s.zmax(beam), s.base(beam).x) : kNegInf;
     const uint64_t key = score_key(p, z, s.zmax(beam), s.base(beam));
@@ -611,29 +603,31 @@ __device__ __noinline__ void narrow_tokens(const BeamParams& p, BeamShared s, Be
 template <int DT, int TH>
 __device__ __forceinline__ int collect(const BeamParams& p, const BeamShared& s, BeamCounts& c, int g, bool exact, float& floor) {
     const int nlive = c.nlive;
-    const FirstLevel v = first_level<TH>(p, s, g, nlive);
-    for (int i = threadIdx.x; i < v.n; i += TH)  // each by the thread that fetched it
-        s.score(i) = level_score(p, s, v, i, exact ? v.z(s, i) : s.score(i), exact);
     floor = kLowest;
-    bool by_place;
-    int n1 = choose<TH>(s, c, v.n, float_of_order(c.best), 1.0f, LevelKey<FirstLevel>{&p, s, v}, v.log ? s.list2() : s.list1(), floor, by_place), n2 = n1;
-    if (!v.log) {
-        const SecondLevel w{ws_ptr<const float>(p.ws, p.sets) + (long long)g * p.N * p.cpr * kBeamSets, p.cpr, p.div_cpr};
+    int n2 = 0;
+    bool second = false;
+    for (int sorted = 0;;) {
+        const Level v = level_of<TH>(p, s, g, nlive, second, n2);
+        const bool there = !second && !exact;  // fetched already, each by the thread that takes it now
+#pragma unroll 2
+        for (int i = threadIdx.x; i < v.n; i += TH) s.score(i) = level_score(p, s, v, i, there ? s.score(i) : v.z(s, i), exact);
         const float floor1 = floor;
-        for (int turn = 0; turn < 2; ++turn) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < n1 * kBeamSets; i += TH) s.score(i) = level_score(p, s, w, i, w.z(s, i), exact);
+        bool by_place;
+        const int got = choose<TH>(s, c, v.n, float_of_order(c.best), 1.0f, LevelKey{&p, s, v}, v.log ? s.list2() : s.list1(), floor, by_place);
+        if (second && by_place && !sorted) {
+            // sets are chosen by their places, which follow the chunks': once more with the chunks in order
+            sort_list<TH>(s.list1(), n2);
             floor = floor1;
-            n2 = choose<TH>(s, c, n1 * kBeamSets, float_of_order(c.best), 1.0f, LevelKey<SecondLevel>{&p, s, w}, s.list2(), floor, by_place);
-            if (!by_place || turn == 1) break;
-            // sets are chosen by their places, which follow the chunks'
-            __syncthreads();
-            sort_list<TH>(s.list1(), n1);
+            sorted = 1;
+            continue;
         }
-        // places in list1 to sets of the group's live beams
-        __syncthreads();
-        if (threadIdx.x == 0) c.chunks = n1;
-        for (int i = threadIdx.x; i < n2; i += TH) s.list2()[i] = s.list1()[s.list2()[i] / kBeamSets] * kBeamSets + s.list2()[i] % kBeamSets;
+        if (second) {  // places in list1 to sets of the group's live beams
+            for (int i = threadIdx.x; i < got; i += TH) s.list2()[i] = s.list1()[s.list2()[i] / kBeamSets] * kBeamSets + s.list2()[i] % kBeamSets;
+            if (threadIdx.x == 0) c.chunks = n2;
+        }
+        n2 = got;
+        if (v.log) break;
+        second = true;
     }
     // the floor as a logit of each live beam, lowered by more than its roundings
     for (int l = threadIdx.x; l < nlive; l += TH) {
@@ -692,11 +686,10 @@ __device__ __noinline__ bool mark_near(const BeamParams& p, BeamShared s, BeamCo
         s.unsure(beam) = s.unsure(of) = 1;
         found = true;
     };
-    const FirstLevel v = first_level<TH>(p, s, g, c.nlive);
-    for (int i = threadIdx.x; i < v.n; i += TH) mark(v.beam(s, i), level_score(p, s, v, i, v.z(s, i), false));
-    if (!v.log) {
-        const SecondLevel w{ws_ptr<const float>(p.ws, p.sets) + (long long)g * p.N * p.cpr * kBeamSets, p.cpr, p.div_cpr};
-        for (int i = threadIdx.x; i < c.chunks * kBeamSets; i += TH) mark(w.beam(s, i), level_score(p, s, w, i, w.z(s, i), false));
+    for (int second = 0; second < 2; ++second) {
+        const Level v = level_of<TH>(p, s, g, c.nlive, second, c.chunks);
+        for (int i = threadIdx.x; i < v.n; i += TH) mark(v.beam(s, i), level_score(p, s, v, i, v.z(s, i), false));
+        if (v.log) break;
     }
     if (c.narrowed)
         for (int l = threadIdx.x; l < c.nlive; l += TH) mark(s.live(l), last);
@@ -782,7 +775,7 @@ __device__ __forceinline__ void beam_finish(const BeamParams& p, const BeamShare
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long rows = (long long)g * p.N;
     {   // the first level's maxima, for which nothing has to be known yet
-        const FirstLevel v = first_level<TH>(p, s, g, c.nlive);
+        const Level v = level_of<TH>(p, s, g, c.nlive, false, 0);
 #pragma unroll 4
         for (int i = threadIdx.x; i < v.n; i += TH) s.score(i) = v.z(s, i);
     }
@@ -848,13 +841,11 @@ __device__ __forceinline__ void beam_finish(const BeamParams& p, const BeamShare
 // ------------------------------------------------------------------------------------------
 
 __device__ __forceinline__ uint64_t token_key(float z, int token) { return (uint64_t)float_order(z + 0.0f) << 32 | (uint32_t)~token; }
-// A place's key where only logits count: the row's sets or chunks, or the sets of the chunks in list1.
+// A place's key where only logits count.
 struct RowKey {
-    const float* z_;
-    const int* chunks;
-    __device__ __forceinline__ float z(int i) const { return __ldcg(z_ + (chunks ? chunks[i / kBeamSets] * kBeamSets + i % kBeamSets : i)); }
+    BeamShared s;
     __device__ __forceinline__ uint64_t operator()(int i) const {
-        const float x = z(i);
+        const float x = s.score(i);
         return x > kNegInf ? (uint64_t)float_order(x + 0.0f) << 32 : 0;
     }
 };
@@ -886,9 +877,9 @@ __device__ __forceinline__ void row_finish(const BeamParams& p, const BeamShared
         const bool direct = p.cpr <= beam_keys(s, p.cpr, TH) / kBeamSets;
         const int n0 = direct ? p.cpr * kBeamSets : p.cpr;
         const float* sets = ws_ptr<const float>(p.ws, p.sets) + (long long)g * p.cpr * kBeamSets;
-        const RowKey v{direct ? sets : ws_ptr<const float>(p.ws, p.maxima) + (long long)g * p.cpr, nullptr};
+        const float* maxima = direct ? sets : ws_ptr<const float>(p.ws, p.maxima) + (long long)g * p.cpr;
 #pragma unroll 4
-        for (int i = threadIdx.x; i < n0; i += TH) s.score(i) = v.z(i);
+        for (int i = threadIdx.x; i < n0; i += TH) s.score(i) = __ldcg(maxima + i);
         if (warp == 0) {
             const Mass a = row_mass(p, g);
             const bool good = a.s < kPosInf && a.m < kPosInf;
@@ -899,24 +890,30 @@ __device__ __forceinline__ void row_finish(const BeamParams& p, const BeamShared
         if (s.base(0).x > kNegInf) {
             const float best = s.zmax(0), unit = 1.0f / p.c_hi;
             float floor = kLowest;
-            bool by_place;
-            const int n1 = choose<TH>(s, c, n0, best, unit, v, direct ? s.list2() : s.list1(), floor, by_place);
-            int n2 = n1;
-            if (!direct) {
-                const float floor1 = floor;
-                const RowKey w{sets, s.list1()};
-                for (int turn = 0; turn < 2; ++turn) {
-                    __syncthreads();
-                    for (int i = threadIdx.x; i < n1 * kBeamSets; i += TH) s.score(i) = w.z(i);
-                    floor = floor1;
-                    n2 = choose<TH>(s, c, n1 * kBeamSets, best, unit, w, s.list2(), floor, by_place);
-                    if (!by_place || turn == 1) break;
-                    // sets are chosen by their places, which follow the chunks'
-                    __syncthreads();
-                    sort_list<TH>(s.list1(), n1);
+            int n2 = 0;
+            bool second = false;
+            for (int sorted = 0;;) {
+                const bool sets_now = direct || second;
+                const int n1 = second ? n2 * kBeamSets : n0;
+                if (second) {
+#pragma unroll 2
+                    for (int i = threadIdx.x; i < n1; i += TH) s.score(i) = __ldcg(sets + s.list1()[i / kBeamSets] * kBeamSets + i % kBeamSets);
                 }
-                __syncthreads();
-                for (int i = threadIdx.x; i < n2; i += TH) s.list2()[i] = s.list1()[s.list2()[i] / kBeamSets] * kBeamSets + s.list2()[i] % kBeamSets;
+                const float floor1 = floor;
+                bool by_place;
+                const int got = choose<TH>(s, c, n1, best, unit, RowKey{s}, sets_now ? s.list2() : s.list1(), floor, by_place);
+                if (second && by_place && !sorted) {
+                    // sets are chosen by their places, which follow the chunks': once more with the chunks in order
+                    sort_list<TH>(s.list1(), n2);
+                    floor = floor1;
+                    sorted = 1;
+                    continue;
+                }
+                if (second)
+                    for (int i = threadIdx.x; i < got; i += TH) s.list2()[i] = s.list1()[s.list2()[i] / kBeamSets] * kBeamSets + s.list2()[i] % kBeamSets;
+                n2 = got;
+                if (sets_now) break;
+                second = true;
             }
             if (threadIdx.x == 0) s.zmin(0) = floor;
             uint64_t K = 0;
@@ -1001,7 +998,7 @@ __global__ void __launch_bounds__(TH, TH == kBeamWide ? 1 : ONE ? 8 : 5) beam_ke
     __syncthreads();
     if (p.blocks > 1) {
         if (threadIdx.x == 0) {
-            unsigned* count = ws_ptr<unsigned>(p.ws, p.count) + g;
+            unsigned* count = ws_ptr<unsigned>(p.ws, kFrontGroup) + g;
             c.last = atom_add_release(count, 1u) == (unsigned)p.blocks - 1u;
             if (c.last) {
                 fence_acquire();
@@ -1034,7 +1031,7 @@ static cudaError_t launch_beam_as(const BeamParams& p, cudaStream_t st) {
 cudaError_t launch_beam(const BeamParams& p0, int dtype, cudaStream_t st) {
     BeamParams p = p0;
     const int sms = device_sm_count();
-    const bool many = p.G >= 2 * sms;
+    const bool many = p.G >= 2 * sms || p.G > kFrontSeqs;  // the front has counters for that many groups
     // few groups: a chunk for each warp, as long as all blocks run at the same time
     const long long chunks = (long long)p.N * p.cpr, want = (chunks + kBeamWide / 32 - 1) / (kBeamWide / 32);
     const long long fit = many ? 1 : (long long)sms / p.G;

@@ -39,7 +39,8 @@ extern "C" int beam_select(const void* logits, long long row_stride, int dtype, 
     if (dtype != SMCSD_F32 && dtype != SMCSD_BF16) return SMCSD_ERR_DTYPE;
     if (!logits || !tokens || !ancestors || !out_scores) return SMCSD_ERR_INVALID_ARG;
     if (G <= 0 || N <= 0 || N > kBeamMostBeams || V <= 0 || V > kMostVocab || M <= 0 || M > kBeamMost) return SMCSD_ERR_INVALID_ARG;
-    if ((long long)G * N > 0x7fffffffLL || (long long)G * M > 0x7fffffffLL || !finite_pos(temperature)) return SMCSD_ERR_INVALID_ARG;
+    if ((long long)G * N > 0x7fffffffLL || (long long)G * M > 0x7fffffffLL || !finite_pos(temperature) || !isfinite(1.5f / temperature))
+        return SMCSD_ERR_INVALID_ARG;
     if (row_stride < V || (uintptr_t)logits % elem_bytes(dtype)) return SMCSD_ERR_INVALID_ARG;
     // outputs that are read while others are written
     if (out_scores == scores || (finished && out_finished == finished)) return SMCSD_ERR_INVALID_ARG;
@@ -67,16 +68,13 @@ extern "C" int beam_select(const void* logits, long long row_stride, int dtype, 
     p.out_scores = out_scores;
     p.out_finished = out_finished;
     p.ws = ws;
-    p.count = L.count;
     p.maxima = L.maxima;
     p.sums = L.sums;
     p.sets = L.sets;
     p.cpr = beam_chunks(V, elem_bytes(dtype));
     p.div_cpr = make_fastdiv((uint32_t)p.cpr);
     p.T = make_exp2_table();
-    cudaStream_t st = (cudaStream_t)stream;
-    if (L.zeroed && cudaMemsetAsync(static_cast<char*>(ws) + L.count, 0, L.zeroed, st) != cudaSuccess) return SMCSD_ERR_CUDA;
-    return from_cuda(launch_beam(p, dtype, st));
+    return from_cuda(launch_beam(p, dtype, (cudaStream_t)stream));
 }
 
 extern "C" int state_reorder(const void* const* src, void* const* dst, const long long* row_bytes, int count,

@@ -28,7 +28,6 @@ struct BeamParams {
     float* out_scores;
     int32_t* out_finished;
     void* ws;
-    size_t count;  // uint32 [G]                     blocks of a group that are done
     size_t maxima; // float [G * N, cpr]             of a chunk
     size_t sums;   // float [G * N, cpr]             relative to it
     size_t sets;   // float [G * N, cpr, kBeamSets]  maximum of a set
@@ -41,19 +40,12 @@ struct BeamParams {
 inline int beam_chunks(int V, int bytes) { return (int)(((long long)V * bytes + 15 + kChunkBytes - 1) / kChunkBytes); }
 
 struct BeamLayout {
-    size_t count, maxima, sums, sets, total, zeroed;
+    size_t maxima, sums, sets, total;
 };
-// Counters of more groups than the front has places for stand behind it (`zeroed` bytes) and are cleared by the call.
 inline BeamLayout beam_layout(int rows, int V) {
     const size_t n = (size_t)rows * (size_t)beam_chunks(V, 4);
     BeamLayout L{};
     size_t o = kFrontBytes;
-    L.count = kFrontGroup;
-    if (rows > kFrontSeqs) {
-        L.count = o;
-        L.zeroed = 4 * (size_t)rows;
-        o = align256(o + L.zeroed);
-    }
     L.maxima = o;
     o = align256(o + 4 * n);
     L.sums = o;

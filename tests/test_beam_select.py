@@ -49,8 +49,8 @@ def test_sizes(smcsd, dtype, G, N, V, M, T):
     assert status == 0
 
 
-def test_more_groups_than_counters(smcsd):
-    # several blocks a group need counters; few groups have many blocks, so both sides of 1024 groups are taken
+def test_few_and_many_groups(smcsd):
+    # several blocks a group, which count themselves, and a block a group
     for G in (1025, 3000):
         assert compare(smcsd, make(G, G, 1, 130, "bf16"), G, 1, 130, 4)[1] == 0
     assert compare(smcsd, make(5, 130, 8, 9001, "bf16"), 130, 8, 9001, 8, scores=np.linspace(-3, 0, 1040).astype(np.float32))[1] == 0
@@ -245,3 +245,22 @@ def test_draft_trees_children(smcsd):
     want = total.flatten().topk(W)
     assert torch.equal(b["ancestors"].long() * V + b["tokens"].long(), want.indices)
     assert (b["scores"].double() - want.values).abs().max() < 1e-5
+
+
+def test_a_group_of_the_largest_size(smcsd):
+    # 64 rows of 1.2 million logits: 37 500 chunks, whose scores fill the shared memory
+    N, V, M = 64, 1_200_000, 48
+    logits, scores = make(3, 1, N, V, "bf16"), torch.linspace(-2, 0, N, device="cuda")
+    ws = smcsd.Workspace(smcsd.OP_BEAM_SELECT, N, 0, V)
+    got = smcsd.beam_select(logits, 1, N, V, M, scores=scores, ws=ws)
+    assert smcsd.check_status(ws) == 0
+    x = torch.stack([torch.log_softmax(logits[i].double(), 0) for i in range(N)]).add_(scores.double()[:, None]).flatten()
+    value = x.topk(M).values
+    assert bool((value[:-1] - value[1:] >= 0).all())
+    at = got["ancestors"].long() * V + got["tokens"].long()
+    assert torch.equal(x[at], value)  # the same candidates in the same order (equal ones are of one row)
+    same = value[:-1] == value[1:]
+    assert bool((at[:-1] < at[1:])[same].all())
+    assert float((got["scores"].double() - value).abs().max()) <= 2e-6 + 2.0 ** -24 * float(value.abs().max())
+    with pytest.raises(smcsd.SMCSDError):
+        smcsd.beam_select(logits[:, :1].contiguous(), 1, 64, 1, 257)

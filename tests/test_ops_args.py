@@ -29,7 +29,7 @@ def test_beam_select(lib):  # noqa: F811
     assert call(n=1 << 24, ws=P(4100)) == -3
     refused(call, -2, dtype=[2, -1])
     refused(call, -1, logits=[None, P(4097)], stride=[99, 0, -100], G=[0, -1, 1 << 30], N=[0, 257, -2], V=[0, -5, END, END - 100], M=[0, 257, -1],
-            T=[0.0, -1.0, float("nan"), float("inf")], tokens=[None], anc=[None], out=[None, FAR], over=[FAR], ws=[None])
+            T=[0.0, -1.0, float("nan"), float("inf"), 1e-45], tokens=[None], anc=[None], out=[None, FAR], over=[FAR], ws=[None])
     assert call(scores=None, finished=None, over=None) == -3
     assert call(V=1 << 30, N=256, stride=1 << 30) == -1  # a group's chunks could not be counted
 
