@@ -492,7 +492,7 @@ int logits_process(const void* logits, void* out, int dtype, int R, int V, int S
  * -inf and 1. A row with nothing but -inf has no candidate; that is not an error here.
  * The order is that of the scores' real values, up to 1e-9 or so: candidates of one beam are ordered by their logits
  * exactly, those of two beams by sums that are computed again, to 2e-10, where hardware exponentials could
- * not tell them apart (a slower path: some 20 us for each such row of 128256). Beams with equal scores and
+ * not tell them apart (a slower path: some 30 us for each such row of 128256). Beams with equal scores and
  * equal rows are exactly equal.
  * N = 1 and scores == NULL gives the M largest log-probabilities of each row: a teacher's top logits, or the children
  * of a draft tree's node.

@@ -1,4 +1,5 @@
-"""GB300-native speculative-decoding verify, SMC-SD reweight / resample and PACER stop rule.
+"""GB300-native speculative-decoding verify, SMC-SD reweight / resample and PACER stop rule, with what stands around them: the paged
+cache, attention of drafts and trees, logits, beam search and a draft's distillation.
 
 The compute path is the CUDA library ``libsmcsd.so`` (C ABI in ``include/smcsd.h``); the
 functions exported here are its ctypes binding (``_binding``), loaded on first use. Build the

@@ -19,6 +19,9 @@ namespace smcsd {
 
 constexpr int kDistillThreads = 256, kDistillMostThreads = 512;
 constexpr int kDistillStaged = 2560;  // vectors of a block that holds its share, as long as sixteen blocks are enough for a row
+// A row of so many vectors is held by one block of 512 threads, so that no blocks have to meet, where there are rows for three turns of
+// them. One block / two, us: 4096 rows of 4000 vectors 96 / 101, of 2625 79.5 / 77; 2000 of 4000 48 / 49; 16 of 4000 7.4 / 6.3.
+constexpr int kDistillAloneFrom = 3584, kDistillAloneTo = 5120;
 constexpr int kDistillRead = 16384;   // of a block that reads it, where rows are many
 static_assert(kDistillThreads >= kDistillMostTokens, "a thread for each listed token");
 
@@ -278,9 +281,11 @@ __device__ __forceinline__ void write_share(const Share<DT>& h, char* out, F&& f
     }
 }
 
-// Shares of 32 KB: six blocks of 256 threads in an SM, each at another point of its row, so that loads, sums and stores overlap.
+// Shares of up to 40 KB: six blocks of 256 threads in an SM, each at another point of its row, so that loads, sums and stores overlap.
+// 2048 rows of 128256 bf16 with 64 tokens each take 200 us, 155 at the copy rate; of that 20 are the sums (issue), 19 the meeting of the
+// clusters of eight, 9 the rest of the structure (measured by leaving each out). DRAM reads and writes each row once.
 template <int DT, int TH>
-__global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 2) distill_kernel(const __grid_constant__ DistillParams p) {
+__global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 3) distill_kernel(const __grid_constant__ DistillParams p) {
     constexpr int PV = Geo<DT>::kPerVec, B = Geo<DT>::kBytes;
     using T = typename Elem<DT>::T;
     extern __shared__ uint4 s_row[];
@@ -408,7 +413,8 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 2) distill_ker
 }
 
 // ------------------------------------------------------------------------------------------
-// the loss alone
+// the loss alone: no share is held, so that shares may be large and a row's meeting comes seldom. 640 rows of 151936 float32 take 75 us,
+// 57 at the copy rate (113 with the kernel above).
 // ------------------------------------------------------------------------------------------
 
 __device__ __forceinline__ uint4 ld_once(const char* p) {
@@ -457,7 +463,7 @@ __device__ __forceinline__ void each_vec(const Share<DT>& h, F&& f) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kDistillThreads, 5) distill_loss_kernel(const __grid_constant__ DistillParams p) {
+__global__ void __launch_bounds__(kDistillThreads, 6) distill_loss_kernel(const __grid_constant__ DistillParams p) {
     constexpr int PV = Geo<DT>::kPerVec, B = Geo<DT>::kBytes, kEach = 4, kWarps = kDistillThreads / 32;
     extern __shared__ uint32_t s_listed[];  // where there is a rest: a bit for each element of the share, set if it is listed
     __shared__ DistillShared s;
@@ -582,7 +588,8 @@ static cudaError_t launch_distill_as(DistillParams p, cudaStream_t st) {
     const long long vecs = ((long long)p.V * Geo<DT>::kBytes + 30) / 16;
     p.ctas = 1;
     if (p.grad) {
-        while (p.ctas < kDistillMostCtas && vecs > p.ctas * (long long)kDistillStaged) p.ctas *= 2;
+        const bool alone = vecs >= kDistillAloneFrom && vecs <= kDistillAloneTo && p.R >= 9 * device_sm_count();
+        while (!alone && p.ctas < kDistillMostCtas && vecs > p.ctas * (long long)kDistillStaged) p.ctas *= 2;
         p.vecs = (int)((vecs + p.ctas - 1) / p.ctas);
         const size_t shared = 16 * (size_t)p.vecs;
         return p.vecs > kDistillStaged ? launch_rows(distill_kernel<DT, kDistillMostThreads>, p, kDistillMostThreads, shared, st)

@@ -91,7 +91,8 @@ struct SeqState {  // per-sequence hand-off between the SD kernels
 // The front of every workspace, at the same place for every operator and shape: what has to be zero when a call begins
 // (and is zero again when it has ended), and the exp table with the scale that it was built for. Everything else that a
 // call writes lies behind it (kFrontBytes), so that one buffer serves calls of any operators and sizes in turn. Operators
-// that keep neither (kv_append, tree_mask, logits_process) have the first 256 bytes alone.
+// that keep neither (kv_append, tree_mask, logits_process, state_reorder, kv_fork, kv_free, kv_copy_pages, distill_loss) have the
+// first 256 bytes alone.
 constexpr int kFrontSeqs = 1024;  // sequences whose counters stand here; those of larger calls are cleared by each call
 constexpr int kFrontArrivals = 1024;
 constexpr size_t kFrontSeq2 = 256;                                  // uint32 [kFrontSeqs]  second pass (SD)
