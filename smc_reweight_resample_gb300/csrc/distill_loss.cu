@@ -100,7 +100,8 @@ struct DistillShared {
     float4 row;                          // the row's mass, the factor of the gradient and the reference that it goes with
     float a[kDistillMostTokens / 32], b[kDistillMostTokens / 32];
     dd d[kDistillMostTokens / 32];
-    int repeats;};
+    int repeats;
+};
 
 // Maximum, or sum, over the list's entries, one of each thread of the block's first `warps` warps, which alone call these.
 __device__ __forceinline__ void list_sync(int warps) { asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory"); }

@@ -75,8 +75,9 @@ cudaError_t launch_reorder(const ReorderParams& p0, cudaStream_t st) {
 // kv_fork, kv_free
 // ------------------------------------------------------------------------------------------
 
-constexpr int kForkThreads = 256;
+constexpr int kForkThreads = 512;  // at most
 constexpr int kForkEntries = 4;   // of a thread
+constexpr int kForkCounts = 8;    // of a thread
 constexpr int kForkMost = 65536;  // entries and pages that one cluster takes
 
 // A page id of a table: whether it is counted. -1 is no page.
@@ -131,33 +132,64 @@ __global__ void __launch_bounds__(kForkClusterThreads) fork_small_kernel(const _
 
 __global__ void __launch_bounds__(kForkThreads) fork_counts_kernel(const __grid_constant__ ForkParams p) {
     griddep_launch_dependents();
-    const long long i0 = (long long)blockIdx.x * kForkThreads * kForkEntries + threadIdx.x;
-    int x[kForkEntries];
+    const long long i0 = (long long)blockIdx.x * kForkThreads * kForkCounts + threadIdx.x;
+    int x[kForkCounts];
 #pragma unroll
-    for (int k = 0; k < kForkEntries; ++k)
+    for (int k = 0; k < kForkCounts; ++k)
         if (i0 + k * kForkThreads < p.num_pages) x[k] = __ldg(p.ref_in + i0 + k * kForkThreads);
 #pragma unroll
-    for (int k = 0; k < kForkEntries; ++k)
+    for (int k = 0; k < kForkCounts; ++k)
         if (i0 + k * kForkThreads < p.num_pages) p.ref_out[i0 + k * kForkThreads] = x[k];
 }
 
-// A block takes up to 1024 entries of one row, four a thread. 10 us for 1024 sequences of 2052 pages, 2.1 million counts copied beside
-// them (34 MB, 5 us at the copy rate): the launches, and counts that change one by one where sequences go.
-__global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constant__ ForkParams p, int pieces) {
-    const int P = p.pages_per_seq, s = blockIdx.x / pieces, j0 = (blockIdx.x - s * pieces) * kForkThreads * kForkEntries + threadIdx.x;
+// A thread's entries of a row, from `j0`: vectors of four, `step` of them apart, or entries as far apart.
+template <bool kWide>
+__device__ __forceinline__ unsigned fork_entry(unsigned j0, int k, unsigned step) {
+    return kWide ? j0 + (k >> 2) * 4 * step + (k & 3) : j0 + k * step;
+}
+template <bool kWide>
+__device__ __forceinline__ void fork_load(int (&x)[kForkEntries], const int* row, unsigned j0, unsigned step, unsigned P) {
+#pragma unroll
+    for (int k = 0; k < kForkEntries; k += kWide ? 4 : 1) {
+        const unsigned j = fork_entry<kWide>(j0, k, step);
+        if (kWide) {
+            const int4 v = j < P ? __ldg(reinterpret_cast<const int4*>(row + j)) : make_int4(-1, -1, -1, -1);
+            x[k] = v.x, x[k + 1] = v.y, x[k + 2] = v.z, x[k + 3] = v.w;
+        } else {
+            x[k] = j < P ? __ldg(row + j) : -1;
+        }
+    }
+}
+
+// A block takes entries of one row, four a thread, a row's blocks as many each. Rows of vectors (their length and both tables' addresses
+// allow it) in blocks of 256 threads: for 1024 sequences of 2052 pages and 2.1 million counts copied beside them 8.0 us where sequences are
+// freed, 195000 entries, and 6.7 where they fork, 176000 (34 MB, 5 us at the copy rate); with 512 threads 0.3 more. Other rows entry by
+// entry: 8.9 and 7.6 with 512 threads, 0.7 more with 256. The counts' copies alone take 2.8, the counts that change one by one 1.4 to 2.5.
+template <bool kWide>
+__global__ void __launch_bounds__(kWide ? kForkThreads / 2 : kForkThreads) fork_kernel(const __grid_constant__ ForkParams p, int pieces) {
+    const int s = blockIdx.x / pieces;
+    const unsigned P = p.pages_per_seq, step = blockDim.x;
+    const unsigned j0 = (blockIdx.x - s * pieces) * step * kForkEntries + (kWide ? 4 : 1) * threadIdx.x;  // may pass 31 bits
     const long long row = (long long)s * P;
     int old[kForkEntries], id[kForkEntries], parent, pages;
-#pragma unroll
-    for (int k = 0; k < kForkEntries; ++k) old[k] = j0 + k * kForkThreads < P ? __ldg(p.table_in + row + j0 + k * kForkThreads) : -1;
+    fork_load<kWide>(old, p.table_in + row, j0, step, P);
     fork_row(p, s, parent, pages);
+    const unsigned upto = (unsigned)pages < P ? pages : P;
+    if (parent != s && upto > 0) fork_load<kWide>(id, p.table_in + (long long)parent * P, j0, step, P);
 #pragma unroll
     for (int k = 0; k < kForkEntries; ++k) {
-        const int j = j0 + k * kForkThreads;
-        id[k] = j >= pages || j >= P ? -1 : parent == s ? old[k] : __ldg(p.table_in + (long long)parent * P + j);
+        if (parent == s) id[k] = old[k];
+        if (fork_entry<kWide>(j0, k, step) >= upto) id[k] = -1;
     }
 #pragma unroll
-    for (int k = 0; k < kForkEntries; ++k)
-        if (j0 + k * kForkThreads < P) p.table_out[row + j0 + k * kForkThreads] = id[k];
+    for (int k = 0; k < kForkEntries; k += kWide ? 4 : 1) {
+        const unsigned j = fork_entry<kWide>(j0, k, step);
+        if (j >= P) continue;
+        if (kWide)
+            *reinterpret_cast<int4*>(p.table_out + row + j) = make_int4(id[k], id[k + 1], id[k + 2], id[k + 3]);
+        else
+            p.table_out[row + j] = id[k];
+    }
     griddep_wait();  // the counts have been copied
 #pragma unroll
     for (int k = 0; k < kForkEntries; ++k) {
@@ -187,17 +219,19 @@ cudaError_t launch_fork(const ForkParams& p, cudaStream_t st) {
         at.val.clusterDim.y = at.val.clusterDim.z = 1;
         return cudaLaunchKernelEx(&cfg, fork_small_kernel, p, make_fastdiv((uint32_t)p.pages_per_seq));
     }
-    constexpr long long kBlock = kForkThreads * kForkEntries;
-    fork_counts_kernel<<<(unsigned)((p.num_pages + kBlock - 1) / kBlock), kForkThreads, 0, st>>>(p);
+    fork_counts_kernel<<<(unsigned)((p.num_pages - 1) / (kForkThreads * kForkCounts) + 1), kForkThreads, 0, st>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int pieces = (int)((p.pages_per_seq + kBlock - 1) / kBlock);
+    const bool wide = p.pages_per_seq % 4 == 0 && ((reinterpret_cast<uintptr_t>(p.table_in) | reinterpret_cast<uintptr_t>(p.table_out)) & 15u) == 0;
+    const int blocks = (p.pages_per_seq - 1) / ((wide ? kForkThreads / 2 : kForkThreads) * kForkEntries) + 1;
+    const int per = (p.pages_per_seq - 1) / blocks + 1, threads = (per + 32 * kForkEntries - 1) / (32 * kForkEntries) * 32;
+    const int pieces = (p.pages_per_seq - 1) / (threads * kForkEntries) + 1;
     if ((long long)pieces * p.S > 0x7fffffffLL) return cudaErrorInvalidValue;
     cfg.gridDim = dim3((unsigned)pieces * (unsigned)p.S);
-    cfg.blockDim = dim3(kForkThreads);
+    cfg.blockDim = dim3(threads);
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
-    return cudaLaunchKernelEx(&cfg, fork_kernel, p, pieces);
+    return cudaLaunchKernelEx(&cfg, wide ? fork_kernel<true> : fork_kernel<false>, p, pieces);
 }
 
 // ------------------------------------------------------------------------------------------

@@ -43,6 +43,22 @@ def test_fork_and_free(smcsd, S, P, num, page):
     assert np.array_equal(host(got[0]), want[0]) and np.array_equal(host(got[1]), want[1])
 
 
+@pytest.mark.parametrize("S,P", [(3, 30_001), (70, 1027), (70, 1028), (33, 2052), (20, 4096), (300, 300), (20_000, 4), (20_000, 5)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_large_tables_of_every_row_and_address(smcsd, S, P, shift):
+    rng = np.random.default_rng(S + P)
+    num, page = 70_001, 16
+    table, ref = random_table(rng, S, P, num)
+    parents = np.where(rng.random(S) < 0.4, np.arange(S), rng.integers(-1, S, S)).astype(np.int32)
+    lengths = rng.integers(0, P * page + 1, S).astype(np.int32)
+    flat = dev(np.concatenate([np.zeros(shift, np.int32), table.ravel()]))[shift:].view(S, P)  # off the vectors' addresses
+    ws = smcsd.Workspace(smcsd.OP_KV_FORK, 1)
+    want = ou.fork(table, ref, parents, lengths, page)
+    got = smcsd.kv_fork(flat, dev(ref), dev(parents), page, lengths=dev(lengths), ws=ws)
+    assert smcsd.check_status(ws) == 0
+    assert np.array_equal(host(got[0]), want[0]) and np.array_equal(host(got[1]), want[1])
+
+
 def test_fork_reads_the_old_table(smcsd):
     # two sequences change places, a third follows one of them
     table = np.array([[0, 1, -1], [2, -1, -1], [3, 4, 5]], np.int32)
