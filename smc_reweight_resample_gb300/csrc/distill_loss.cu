@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 3) distill_ker
         cl.barrier_wait(std::move(started));
         write_share<DT, TH>(h, out, [](int) { return make_uint4(0, 0, 0, 0); });
         if (rank == 0 && tid == 0 && p.loss) p.loss[r] = 0.0f;
+        cl.sync();  // every block stays for the last meeting: where a list changes meanwhile, others may have read another one
         return;
     }
     fetch<DT, TH>(h, s_row);
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(kDistillThreads, 6) distill_loss_kernel(const 
     if (!some) {
         cl.barrier_wait(std::move(started));
         if (rank == 0 && tid == 0) p.loss[r] = 0.0f;
+        cl.sync();  // as in the other kernel
         return;
     }
     e.first = e.token >= 0;

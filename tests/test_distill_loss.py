@@ -270,3 +270,33 @@ def test_a_teachers_list_from_its_logits(smcsd):
         loss, grad, status = compare(smcsd, z, tokens, values, V, 2.0, rest)
         assert status == 0
     assert float(loss.abs().max()) < 1e-4 and float(grad.abs().max()) < 1e-5
+
+
+@pytest.mark.parametrize("V", [24_000, 128_256])
+def test_lists_that_change_meanwhile_harm_nobody(smcsd, V):
+    """A row's blocks may read different lists where another stream writes them: the results are anything, the calls after them right."""
+    R, K = 300, 32
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    logits = torch.randn(R, V, device="cuda", generator=gen, dtype=torch.bfloat16)
+    listed = torch.topk(torch.log_softmax(logits.float(), 1), K, dim=1)
+    tokens, values = listed.indices.int(), listed.values
+    nobody, live = torch.full_like(tokens, -1), tokens.clone()
+    ws = smcsd.Workspace(smcsd.OP_DISTILL_LOSS, R)
+    want = smcsd.distill_loss(logits, tokens, values, V, rest=True, ws=ws)
+    out = [torch.empty_like(x) for x in want]
+    loss_alone = torch.empty_like(want[0])
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for _ in range(20):
+        with torch.cuda.stream(other):
+            for _ in range(10):
+                live.copy_(nobody)
+                live.copy_(tokens)
+        for _ in range(3):
+            smcsd.distill_loss(logits, live, values, V, rest=True, loss=out[0], dlogits=out[1], ws=ws)
+            smcsd.distill_loss(logits, live, values, V, rest=True, loss=loss_alone, grad=False, ws=ws)
+    torch.cuda.synchronize()
+    smcsd.check_status(ws)  # a sum from blocks that read different lists may be reported; this clears it
+    smcsd.distill_loss(logits, live, values, V, rest=True, loss=out[0], dlogits=out[1], ws=ws)
+    assert smcsd.check_status(ws) == 0
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
