@@ -242,18 +242,30 @@ constexpr int kCompactThreads = 1024;
 constexpr int kCompactWarps = kCompactThreads / 32;
 constexpr int kCompactMost = 8192;  // table entries that the planning cluster writes
 
-// Table entries and counts of the pages that move, once the moves are known.
+// Table entries and counts of the pages that move, once the moves are known. Counts that another stream changes meanwhile give other
+// places at each reading: a place that no move can have is reported and not followed, here and below.
 __device__ __forceinline__ void compact_apply(const CompactParams& p, int moves, int used, long long first, long long step) {
     const int32_t* place = ws_ptr<const int32_t>(p.ws, p.place);
-    for (long long i = first; i < moves; i += step) p.ref_out[__ldcg(p.dst + i)] = __ldg(p.ref_in + __ldcg(p.src + i));
+    for (long long i = first; i < moves; i += step) {
+        const int from = __ldcg(p.src + i), to = __ldcg(p.dst + i);
+        if ((unsigned)from < (unsigned)p.num_pages && (unsigned)to < (unsigned)p.num_pages)
+            p.ref_out[to] = __ldg(p.ref_in + from);
+        else
+            raise_error(p.ws, kErrRange);
+    }
 #pragma unroll 4
     for (long long i = first; i < p.entries; i += step) {
         int id = __ldg(p.table_in + i);
         if (id != -1) {
             if (id < 0 || id >= p.num_pages || __ldg(p.ref_in + id) <= 0)
                 raise_error(p.ws, kErrRange);  // left as it is
-            else if (id >= used)
-                id = __ldcg(p.dst + __ldcg(place + id));
+            else if (id >= used) {
+                const int k = __ldcg(place + id);
+                if ((unsigned)k < (unsigned)moves)
+                    id = __ldcg(p.dst + k);
+                else
+                    raise_error(p.ws, kErrRange);
+            }
         }
         p.table_out[i] = id;
     }
@@ -313,11 +325,11 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(const __g
         const int t = *cl.map_shared_rank(&s_before, c);
         if (t >= 0) low = t;
     }
+    const int half = p.num_pages / 2, moves = min(max(used - low, 0), half);
     if (gw == 0 && lane == 0) {
-        p.counts[0] = used - low;
+        p.counts[0] = moves;
         p.counts[1] = used;
     }
-    const int moves = used - low, half = p.num_pages / 2;
     for (int i = moves + rank * kCompactThreads + threadIdx.x; i < half; i += C * kCompactThreads) p.src[i] = p.dst[i] = -1;
     for (int r = r0; r < r1; ++r) {
         const int id = r * 32 + lane;
@@ -330,11 +342,11 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(const __g
         if (id < used) {
             if (ref > 0)
                 p.ref_out[id] = ref;
-            else
+            else if ((unsigned)(id - held) < (unsigned)half)
                 p.dst[id - held] = id;  // its count comes with its page
         } else {
             p.ref_out[id] = 0;
-            if (ref > 0) {
+            if (ref > 0 && (unsigned)(held - low) < (unsigned)half) {
                 p.src[held - low] = id;
                 place[id] = held - low;
             }
