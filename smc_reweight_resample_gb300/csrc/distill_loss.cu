@@ -17,11 +17,12 @@ namespace cg = cooperative_groups;
 
 namespace smcsd {
 
-constexpr int kDistillThreads = 256, kDistillMostThreads = 512;
-constexpr int kDistillStaged = 2560;  // vectors of a block that holds its share, as long as sixteen blocks are enough for a row
-// A row of so many vectors is held by one block of 512 threads, so that no blocks have to meet, where there are rows for three turns of
-// them. One block / two, us: 4096 rows of 4000 vectors 96 / 101, of 2625 79.5 / 77; 2000 of 4000 48 / 49; 16 of 4000 7.4 / 6.3.
-constexpr int kDistillAloneFrom = 3584, kDistillAloneTo = 5120;
+constexpr int kDistillThreads = 256, kDistillMoreThreads = 384, kDistillMostThreads = 512;
+// Vectors of a block that holds its share, as long as sixteen blocks are enough for a row: in blocks of 256 threads, six to an SM; and in
+// blocks of 384, four to an SM, where that makes a row's blocks half as many and there are two for each SM all the same. Us with the
+// larger shares / the smaller: 4096 rows of 43000 bf16 130 / 143, of 90000 276 / 297, of 24000 76.9 / 77.6; 300 of 43000 11.4 / 14.1, of
+// 24000 9.1 / 8.8; 40 of 90000 8.3 / 7.7.
+constexpr int kDistillStaged = 2560, kDistillMore = 3328;
 constexpr int kDistillRead = 16384;   // of a block that reads it, where rows are many
 static_assert(kDistillThreads >= kDistillMostTokens, "a thread for each listed token");
 
@@ -91,7 +92,53 @@ __device__ __forceinline__ Masses join_lanes(const float4* q, int n, float c2) {
     return Masses{Mass{a, __shfl_sync(0xffffffffu, sa, 0)}, Mass{b, __shfl_sync(0xffffffffu, sb, 0)}};
 }
 
+// What the blocks of a cluster tell one another: stores to another block's shared memory that count on its barrier as they land, so
+// that nothing but their landing is waited for (a barrier of the cluster waits for all earlier memory operations too: 19 of 200 us at
+// 2048 x 128256, this 8).
+__device__ __forceinline__ uint32_t shared_address(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t in_block(uint32_t address, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(address), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void tell(uint32_t at, float4 x, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at), "f"(x.x), "f"(x.y),
+                 "f"(x.z), "f"(x.w), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void tell_bits(uint32_t at, uint32_t x, uint32_t bar) {
+    asm volatile("red.async.relaxed.cluster.shared::cluster.mbarrier::complete_tx::bytes.add.u32 [%0], %1, [%2];" ::"r"(at), "r"(x), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void told_init(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool told(uint32_t bar) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar)
+        : "memory");
+    return ok != 0;
+}
+constexpr unsigned long long kToldNs = 2000000000ull;  // longest wait
+__device__ __forceinline__ void wait_told(uint32_t bar, void* ws) {
+    if (told(bar)) return;
+    unsigned long long t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    while (!told(bar)) {
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (t - t0 > kToldNs) {
+            raise_error(ws, kErrTimeout);  // no counters are left behind
+            return;
+        }
+    }
+}
+
 struct DistillShared {
+    alignas(8) unsigned long long bar;  // what the other blocks tell this one
     alignas(16) int token[kDistillMostTokens];
     float p[kDistillMostTokens];
     float z[kDistillMostTokens];    // in the first block: the listed tokens' logits
@@ -286,7 +333,7 @@ __device__ __forceinline__ void write_share(const Share<DT>& h, char* out, F&& f
 // 2048 rows of 128256 bf16 with 64 tokens each take 200 us, 155 at the copy rate; of that 20 are the sums (issue), 19 the meeting of the
 // clusters of eight, 9 the rest of the structure (measured by leaving each out). DRAM reads and writes each row once.
 template <int DT, int TH>
-__global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 3) distill_kernel(const __grid_constant__ DistillParams p) {
+__global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistillMoreThreads ? 4 : 3) distill_kernel(const __grid_constant__ DistillParams p) {
     constexpr int PV = Geo<DT>::kPerVec, B = Geo<DT>::kBytes;
     using T = typename Elem<DT>::T;
     extern __shared__ uint4 s_row[];
@@ -294,7 +341,23 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 3) distill_ker
     cg::cluster_group cl = cg::this_cluster();
     const int C = p.ctas, rank = (int)cl.block_rank(), tid = threadIdx.x;
     const int r = blockIdx.x / C;
-    auto started = cl.barrier_arrive();  // the other blocks' shared memory may be written once all have come here
+    // Each block of a row tells all of them its masses, and the first one the listed tokens' logits (whose bits add up, those of the others
+    // being 0); it leaves when all have told it theirs. How much is told does not depend on the list, of which blocks read different
+    // ones where it changes meanwhile.
+    const uint32_t bar = shared_address(&s.bar);
+    const bool tell_z = p.loss && tid < p.K;
+    if (rank == 0 && tid < kDistillMostTokens) s.z[tid] = 0.0f;
+    if (tid == 0 && C > 1) told_init(bar, 16 * C + (rank == 0 && p.loss ? 4 * p.K * C : 0));
+    auto started = cl.barrier_arrive();  // the other blocks may be told something once all have come here
+    const auto meet = [&](float4 own) {  // by the first warp
+        if (C == 1) {
+            if (tid == 0) s.part[0] = own;
+            __syncwarp();
+            return;
+        }
+        if (tid < C) tell(in_block(shared_address(&s.part[rank]), tid), own, in_block(bar, tid));
+        wait_told(bar, p.ws);
+    };
 
     const Share<DT> h(p, r, rank);
     Entry e{};
@@ -306,9 +369,10 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 3) distill_ker
 
     if (!some || (weight == 0.0f && !p.loss)) {
         cl.barrier_wait(std::move(started));
+        if (tell_z && C > 1) tell_bits(in_block(shared_address(&s.z[tid]), 0), 0, in_block(bar, 0));
+        if (tid < 32) meet(make_float4(kNegInf, 0.0f, kNegInf, 0.0f));
         write_share<DT, TH>(h, out, [](int) { return make_uint4(0, 0, 0, 0); });
         if (rank == 0 && tid == 0 && p.loss) p.loss[r] = 0.0f;
-        cl.sync();  // every block stays for the last meeting: where a list changes meanwhile, others may have read another one
         return;
     }
     fetch<DT, TH>(h, s_row);
@@ -375,12 +439,15 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : 3) distill_ker
     cl.barrier_wait(std::move(started));
     __syncthreads();
     if (mine && !p.rest) z = bits_to_float<DT>((uint32_t)elems[at]);
-    if (mine) *cl.map_shared_rank(&s.z[tid], 0) = z;
+    if (C == 1) {
+        if (mine) s.z[tid] = z;
+    } else if (tell_z) {
+        tell_bits(in_block(shared_address(&s.z[tid]), 0), mine ? __float_as_uint(z) : 0u, in_block(bar, 0));
+    }
     if (tid < 32) {
         const Masses q = join_lanes(s.q, TH / 32, p.c2);
-        if (tid < C) *cl.map_shared_rank(&s.part[rank], tid) = make_float4(q.a.m, q.a.s, q.b.m, q.b.s);
+        meet(make_float4(q.a.m, q.a.s, q.b.m, q.b.s));
     }
-    cl.sync();
 
     // the row's mass, by one warp; without a rest all of it is in R
     const float wc = weight * p.c;
@@ -481,7 +548,7 @@ __global__ void __launch_bounds__(kDistillThreads, 6) distill_loss_kernel(const 
     if (!some) {
         cl.barrier_wait(std::move(started));
         if (rank == 0 && tid == 0) p.loss[r] = 0.0f;
-        cl.sync();  // as in the other kernel
+        cl.sync();  // every block stays for the last meeting, whatever list it has read
         return;
     }
     e.first = e.token >= 0;
@@ -591,12 +658,15 @@ static cudaError_t launch_distill_as(DistillParams p, cudaStream_t st) {
     const long long vecs = ((long long)p.V * Geo<DT>::kBytes + 30) / 16;
     p.ctas = 1;
     if (p.grad) {
-        const bool alone = vecs >= kDistillAloneFrom && vecs <= kDistillAloneTo && p.R >= 9 * device_sm_count();
-        while (!alone && p.ctas < kDistillMostCtas && vecs > p.ctas * (long long)kDistillStaged) p.ctas *= 2;
+        while (p.ctas < kDistillMostCtas && vecs > p.ctas * (long long)kDistillStaged) {
+            if (vecs <= p.ctas * (long long)kDistillMore && (long long)p.R * p.ctas >= 2ll * device_sm_count()) break;
+            p.ctas *= 2;
+        }
         p.vecs = (int)((vecs + p.ctas - 1) / p.ctas);
         const size_t shared = 16 * (size_t)p.vecs;
-        return p.vecs > kDistillStaged ? launch_rows(distill_kernel<DT, kDistillMostThreads>, p, kDistillMostThreads, shared, st)
-                                       : launch_rows(distill_kernel<DT, kDistillThreads>, p, kDistillThreads, shared, st);
+        if (p.vecs <= kDistillStaged) return launch_rows(distill_kernel<DT, kDistillThreads>, p, kDistillThreads, shared, st);
+        if (p.vecs <= kDistillMore) return launch_rows(distill_kernel<DT, kDistillMoreThreads>, p, kDistillMoreThreads, shared, st);
+        return launch_rows(distill_kernel<DT, kDistillMostThreads>, p, kDistillMostThreads, shared, st);
     }
     while (p.ctas < kDistillMostCtas && vecs > p.ctas * (long long)kDistillRead) p.ctas *= 2;
     // smaller shares where rows are few, for three turns of the blocks that run at a time
