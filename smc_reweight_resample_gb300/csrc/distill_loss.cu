@@ -93,8 +93,8 @@ __device__ __forceinline__ Masses join_lanes(const float4* q, int n, float c2) {
 }
 
 // What the blocks of a cluster tell one another: stores to another block's shared memory that count on its barrier as they land, so
-// that nothing but their landing is waited for (a barrier of the cluster waits for all earlier memory operations too: 19 of 200 us at
-// 2048 x 128256, this 8).
+// that nothing but their landing is waited for (a barrier of the cluster waits for all earlier memory operations too: 200 us for 196 at
+// 2048 x 128256, 101 for 94 at 4096 x 32000).
 __device__ __forceinline__ uint32_t shared_address(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ uint32_t in_block(uint32_t address, int rank) {
     uint32_t r;
@@ -140,13 +140,17 @@ __device__ __forceinline__ void wait_told(uint32_t bar, void* ws) {
 struct DistillShared {
     alignas(8) unsigned long long bar;  // what the other blocks tell this one
     alignas(16) int token[kDistillMostTokens];
-    float p[kDistillMostTokens];
+    union {
+        unsigned seen[kDistillMostTokens];  // a table of bits, then
+        float p[kDistillMostTokens];
+    };
     float z[kDistillMostTokens];    // in the first block: the listed tokens' logits
     float4 part[kDistillMostCtas];       // of each block: the rest's mass, the listed tokens' mass
     float4 q[kDistillMostThreads / 32];  // of each warp: the same
     float4 row;                          // the row's mass, the factor of the gradient and the reference that it goes with
     float a[kDistillMostTokens / 32], b[kDistillMostTokens / 32];
     dd d[kDistillMostTokens / 32];
+    float rest, mass;
     int repeats;
 };
 
@@ -200,24 +204,29 @@ struct Share {
     __device__ int whole_to() const { return n > 0 && e0 + n * Geo<DT>::kPerVec > V ? n - 1 : n; }
 };
 
-// Whether this thread's token stands in the list more than once.
-__device__ __forceinline__ bool list_repeats(int token, const DistillShared& s, int warps, int K) {
-    if (token < 0) token = -2 - (int)threadIdx.x;  // alike with nobody's
-    if (warps == 1) return __popc(__match_any_sync(0xffffffffu, token)) > 1;
-    int n = 0;
-    for (int k = 0; k < K; k += 4) {  // behind K there are -1
-        const int4 t = *reinterpret_cast<const int4*>(s.token + k);
-        n += (t.x == token) + (t.y == token) + (t.z == token) + (t.w == token);
+// Whether one of the warp's tokens, of those with `check`, stands in the list more than once. Of more than 32, tokens meet in a table of
+// bits, and one that finds its bit set is looked for in the list by its warp. (Each thread going through the list took 40 us more for 2048 rows
+// with 128 tokens each, 140 with 256.)
+__device__ __forceinline__ bool list_repeats(int token, bool check, DistillShared& s, int warps) {
+    const int lane = threadIdx.x & 31;
+    if (warps == 1) return __any_sync(0xffffffffu, __popc(__match_any_sync(0xffffffffu, check ? token : -1 - lane)) > 1);
+    const unsigned h = (unsigned)token * 0x9e3779b1u >> 19, bit = 1u << (h & 31);
+    unsigned again = __ballot_sync(0xffffffffu, check && (atomicOr(s.seen + (h >> 5), bit) & bit));
+    for (; again; again &= again - 1) {
+        const int t = __shfl_sync(0xffffffffu, token, __ffs(again) - 1);
+        int n = 0;
+        for (int k = 0; k < 32 * warps; k += 32) n += __popc(__ballot_sync(0xffffffffu, s.token[k + lane] == t));
+        if (n > 1) return true;
     }
-    return n > 1;
+    return false;
 }
 
 // A thread's entry of the row's list. All threads call this; whether the list has any mass.
 struct Entry {
     int token;
     float value;
-    // the teacher's probability and its logarithm; in the token's first place that of all its entries
-    float prob, logp, listed;
+    // the logarithm of the teacher's probability; in the token's first place the probability of all its entries
+    float logp, listed;
     bool first;
 };
 __device__ __forceinline__ bool list_entry(const DistillParams& p, DistillShared& s, int r, Entry& e) {
@@ -235,17 +244,18 @@ __device__ __forceinline__ bool list_entry(const DistillParams& p, DistillShared
             raise_error(p.ws, kErrNonfinite);
         }
     }
-    if (tid < kDistillMostTokens) s.token[tid] = e.token;
+    if (tid < kDistillMostTokens) s.token[tid] = e.token, s.seen[tid] = 0;
     if (tid == 0) s.repeats = 0;
     return __syncthreads_or(e.value > kNegInf);
 }
-// The teacher's probabilities, by the warps with entries: p_r and the sum of all are given back to all of their threads.
-__device__ __forceinline__ void list_teacher(const DistillParams& p, DistillShared& s, Entry& e, int lists, float& rest, float& mass) {
+// The teacher's probabilities, by the warps with entries; p_r and the sum of all too.
+__device__ __forceinline__ void list_teacher(const DistillParams& p, DistillShared& s, Entry& e, bool check, int lists) {
     const int tid = threadIdx.x;
+    float rest = 0.0f, mass = 1.0f, prob;
     if (p.rest) {
         e.logp = e.value;
-        e.prob = e.value > kNegInf ? expf(e.value) : 0.0f;
-        const dd sum = list_sum_dd(s, e.prob, lists);
+        prob = e.value > kNegInf ? expf(e.value) : 0.0f;
+        const dd sum = list_sum_dd(s, prob, lists);
         rest = fmaxf(dd_add(dd{1.0f, 0.0f}, dd_neg(sum)).hi, 0.0f);
         mass = fmaxf(sum.hi, 1.0f);
     } else {
@@ -253,27 +263,30 @@ __device__ __forceinline__ void list_teacher(const DistillParams& p, DistillShar
         const float x = e.value > kNegInf ? expf(e.value - top) : 0.0f;
         const dd sum = list_sum_dd(s, x, lists);
         e.logp = e.value - top - logf(sum.hi);
-        e.prob = x / sum.hi;
+        prob = x / sum.hi;
     }
-    s.p[tid] = e.prob;
-    if (list_repeats(e.token, s, lists, p.K)) s.repeats = 1;
+    e.listed = prob;
+    if (list_repeats(e.token, check, s, lists) && (tid & 31) == 0) s.repeats = 1;
     list_sync(lists);
+    s.p[tid] = prob;
+    if (tid == 0) s.rest = rest, s.mass = mass;
+    if (!s.repeats) return;
     // a token that is listed several times: its first place stands for all of them
-    e.listed = e.prob;
-    if (s.repeats && e.token >= 0) {
-        e.listed = 0.0f;
-        for (int k = p.K - 1; k >= 0; --k)
-            if (s.token[k] == e.token) {
-                e.listed += s.p[k];
-                e.first = k == tid;
-            }
-    }
+    list_sync(lists);
+    if (e.token < 0) return;
+    e.listed = 0.0f;
+    for (int k = p.K - 1; k >= 0; --k)
+        if (s.token[k] == e.token) {
+            e.listed += s.p[k];
+            e.first = k == tid;
+        }
 }
 // The loss, by the first block's warps with entries, from the row's mass and the rest's.
-__device__ __forceinline__ void list_loss(const DistillParams& p, DistillShared& s, const Entry& e, int lists, float z, float rest, Mass all, Mass R, int r) {
+__device__ __forceinline__ void list_loss(const DistillParams& p, DistillShared& s, const Entry& e, int lists, float z, Mass all, Mass R, int r) {
     const float ls = logf(all.s);
     float term = 0.0f;
-    if (e.prob > 0.0f) term = e.prob * (e.logp - ((z - all.m) * p.c - ls));
+    const float prob = s.p[threadIdx.x], rest = s.rest;
+    if (prob > 0.0f) term = prob * (e.logp - ((z - all.m) * p.c - ls));
     if (threadIdx.x == 0 && rest > 0.0f) term += rest * (logf(rest) - (logf(R.s) + (R.m - all.m) * p.c - ls));
     const float loss = list_sum(s, term, lists);
     if (threadIdx.x == 0) p.loss[r] = loss;
@@ -330,8 +343,9 @@ __device__ __forceinline__ void write_share(const Share<DT>& h, char* out, F&& f
 }
 
 // Shares of up to 40 KB: six blocks of 256 threads in an SM, each at another point of its row, so that loads, sums and stores overlap.
-// 2048 rows of 128256 bf16 with 64 tokens each take 200 us, 155 at the copy rate; of that 20 are the sums (issue), 19 the meeting of the
-// clusters of eight, 9 the rest of the structure (measured by leaving each out). DRAM reads and writes each row once.
+// 2048 rows of 128256 bf16 with 64 tokens each take 191 us, 155 at the copy rate; of that 20 are the sums (issue; measured by leaving them out),
+// the rest is a row's structure: list, copies, the meeting of eight blocks, writing. DRAM reads and writes each row once. With 256 tokens
+// 221: probabilities of eight warps in every block.
 template <int DT, int TH>
 __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistillMoreThreads ? 4 : 3) distill_kernel(const __grid_constant__ DistillParams p) {
     constexpr int PV = Geo<DT>::kPerVec, B = Geo<DT>::kBytes;
@@ -379,11 +393,10 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistill
     // meanwhile the teacher's probabilities
     const int lists = (p.K + 31) / 32;  // warps with entries
     const bool lister = tid < 32 * lists;
-    float rest = 0.0f, mass = 1.0f;
-    if (lister) list_teacher(p, s, e, lists, rest, mass);
-    T* elems = reinterpret_cast<T*>(s_row);
     const int at = token - h.e0;
     const bool mine = token >= 0 && at >= 0 && at < h.n * PV;
+    if (lister) list_teacher(p, s, e, mine, lists);
+    T* elems = reinterpret_cast<T*>(s_row);
     float z = kNegInf;
     copies_done();
     // a thread has copied the vectors that it adds up itself, but for a first or last one that does not lie in the row whole
@@ -457,7 +470,7 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistill
         if (tid == 0) {
             // the rest relative to its own maximum; one without mass (all -inf) gets no gradient
             float scale = 0.0f;
-            if (R.m > kNegInf) scale = p.rest ? wc * (mass * exp2f((R.m - all.m) * p.c2) / all.s - rest / R.s) : wc / all.s;
+            if (R.m > kNegInf) scale = p.rest ? wc * (s.mass * exp2f((R.m - all.m) * p.c2) / all.s - s.rest / R.s) : wc / all.s;
             s.row = make_float4(all.m, all.s, scale, R.m > kNegInf ? R.m : 0.0f);
             s.q[0].x = R.m, s.q[0].y = R.s;
             if (rank == 0 && !(all.s > 0.0f && all.s < kPosInf && all.m < kPosInf)) raise_error(p.ws, kErrNonfinite);
@@ -466,7 +479,7 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistill
     __syncthreads();
     const float4 row = s.row;
     const Mass all{row.x, row.y};
-    if (rank == 0 && lister && p.loss) list_loss(p, s, e, lists, s.z[tid], rest, all, Mass{s.q[0].x, s.q[0].y}, r);
+    if (rank == 0 && lister && p.loss) list_loss(p, s, e, lists, s.z[tid], all, Mass{s.q[0].x, s.q[0].y}, r);
     const f32x2 m2 = pair(-row.w, -row.w), scale2 = pair(row.z, row.z);
     write_share<DT, TH>(h, out, [&](int i) {
         Vec<DT> v(s_row[i]);
@@ -477,7 +490,7 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistill
     __syncthreads();  // the listed tokens' places have been written as part of the rest
     if (mine && e.first) {
         const float q = exp2f((z - all.m) * p.c2) / all.s;
-        reinterpret_cast<T*>(out)[token] = (T)round_to<DT>(wc * (mass * q - e.listed));
+        reinterpret_cast<T*>(out)[token] = (T)round_to<DT>(wc * (s.mass * q - e.listed));
     }
 }
 
@@ -605,9 +618,8 @@ __global__ void __launch_bounds__(kDistillThreads, 6) distill_loss_kernel(const 
     const int lists = (p.K + 31) / 32;
     const bool lister = tid < 32 * lists;
     Mass b{kNegInf, 0.0f};
-    float rest = 0.0f, mass = 1.0f;
     if (lister) {
-        if (rank == 0) list_teacher(p, s, e, lists, rest, mass);
+        if (rank == 0) list_teacher(p, s, e, e.token >= 0, lists);
         if (p.rest && rank == 0) b = warp_mass(token_mass(e, z), p.c2);
     }
     if ((tid & 31) == 0) s.q[tid >> 5] = make_float4(a.m, a.s, b.m, b.s);
@@ -622,7 +634,7 @@ __global__ void __launch_bounds__(kDistillThreads, 6) distill_loss_kernel(const 
         const Masses row = join_lanes(s.part, C, p.c2);
         const Mass R = row.a, all = p.rest ? join(R, row.b, p.c2) : R;
         if (tid == 0 && !(all.s > 0.0f && all.s < kPosInf && all.m < kPosInf)) raise_error(p.ws, kErrNonfinite);
-        list_loss(p, s, e, lists, z, rest, all, R, r);
+        list_loss(p, s, e, lists, z, all, R, r);
     }
 }
 

@@ -110,6 +110,32 @@ def test_lists_with_gaps_repeats_and_none(smcsd, dtype, rest):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("V,K", [(300, 33), (300, 256), (20_001, 100), (128_256, 64), (128_256, 200), (151_936, 256)])
+def test_long_lists_with_repeats(smcsd, dtype, rest, V, K):
+    R = 6
+    z, tokens, values = make(V + 3 * K, R, V, K, dtype)
+    values -= 3.0                               # so that what is listed more than once leaves a rest
+    tokens[1, K - 1] = tokens[1, 0]             # in the first and the last warp
+    tokens[2, 1::2] = tokens[2, 0::2][: K // 2].clone()
+    tokens[3, 32:] = tokens[3, : K - 32].clone()
+    tokens[4] = tokens[4, 7].clone()
+    tokens[5, ::3] = -1
+    tokens[5, K - 1] = tokens[5, 1]
+    weight = torch.linspace(0.5, 1.5, R, device="cuda")
+    assert compare(smcsd, z, tokens, values, V, 1.0, rest, weight)[2] == 0
+    assert compare(smcsd, z, tokens, values, V, 1.0, rest, weight, grad=False)[2] == 0
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("R,V,dtype", [(310, 21_000, "bf16"), (305, 13_001, "f32"), (80, 90_000, "bf16"), (160, 50_003, "bf16")])
+def test_many_rows_in_large_shares(smcsd, rest, R, V, dtype):
+    z, tokens, values = make(R + V, R, V, 40, dtype)
+    weight = torch.rand(R, device="cuda") * 2 - 0.5
+    assert compare(smcsd, z, tokens, values, V, 1.0, rest, weight)[2] == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rest", [False, True])
 def test_masked_and_far_apart_logits(smcsd, dtype, rest):
     R, V, K = 6, 3001, 8
     z, tokens, values = make(9, R, V, K, dtype)
