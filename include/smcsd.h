@@ -498,7 +498,7 @@ int logits_process(const void* logits, void* out, int dtype, int R, int V, int S
  * of a draft tree's node.
  * logits [G*N rows, row_stride elements apart, V used], aligned to their type; scores float [G*N] (NULL: 0);
  * finished int32 [G*N] (NULL: none); eos_token < 0: none; tokens, ancestors int32, out_scores float,
- * out_finished int32 (NULL to skip) [G*M]; out_scores and out_finished must not be scores and finished. N and
+ * out_finished int32 (NULL to skip) [G*M]; outputs must not overlap scores and finished. N and
  * M are at most 256, and a group's N rows of V logits at most 160 MB. ws: smcsd_workspace_size(SMCSD_OP_BEAM_SELECT, G*N, 0, V).
  * Device-side errors: SMCSD_ERR_NONFINITE (NaN or +inf in logits that are read, or in scores; such a beam has no candidate).
  */
@@ -578,7 +578,8 @@ int kv_copy_pages(void* const* caches, int n_caches, long long page_bytes, int n
  * a loss and a gradient of 0, whatever its logits are (padding). q_v = 0 for a masked token; a loss is +inf where p > 0 meets q = 0.
  * Either output may be NULL, loss for the backward pass alone and dlogits for the forward one; both together read the logits once,
  * as each alone does. logits, dlogits: rows row_stride and dlogits_stride elements apart, V used, of dtype, aligned to
- * it; dlogits may be logits (with one stride), else they must not overlap. top_tokens int32, top_values float [R, K], K at most 256;
+ * it; dlogits may be logits (with one stride), else they must not overlap (rows may lie
+ * between one another's); nor may loss and the other inputs. top_tokens int32, top_values float [R, K], K at most 256;
  * weight, loss float [R]. V times the element size is at most 1638368 bytes. Sums are float32, the gradient is rounded once.
  * Device-side errors: SMCSD_ERR_NONFINITE (NaN or +inf in logits or values, a row of -inf), SMCSD_ERR_RANGE (a token outside
  * [-1, V), taken as none).

@@ -2,6 +2,8 @@
 // and launches.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "ops_launch.cuh"
 #include "smcsd.h"
 #include "smcsd_launch.cuh"
@@ -19,6 +21,35 @@ int check_ws(const void* ws, size_t ws_bytes, size_t need) {
     if (!ws) return SMCSD_ERR_INVALID_ARG;
     if (((uintptr_t)ws & 255u) != 0 || ws_bytes < need) return SMCSD_ERR_WORKSPACE;
     return SMCSD_OK;
+}
+
+// Memory that a call reads or writes, and whether what it writes meets what it reads, which other blocks may not have read yet.
+struct Span {
+    const void* at;
+    unsigned __int128 bytes;
+    Span(const void* p, long long n, long long each) : at(p), bytes((unsigned __int128)n * (unsigned long long)each) {}
+};
+bool meet(const Span& a, const Span& b) {
+    const unsigned __int128 x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+    return a.at && b.at && x < y + b.bytes && y < x + a.bytes;
+}
+bool meet(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+    for (const Span& a : written)
+        for (const Span& b : read)
+            if (meet(a, b)) return true;
+    return false;
+}
+// The same of two matrices' rows of V elements of e bytes, which may lie between one another.
+bool rows_meet(const void* a, long long stride_a, const void* b, long long stride_b, int R, int V, int e) {
+    const auto span = [&](const void* p, long long stride) {
+        Span s(p, R - 1, stride);
+        s.bytes = (s.bytes + (unsigned)V) * (unsigned)e;
+        return s;
+    };
+    if (!meet(span(a, stride_a), span(b, stride_b))) return false;
+    if (stride_a != stride_b || R == 1) return true;
+    const __int128 s = stride_a, d = (((__int128)(uintptr_t)b - (__int128)(uintptr_t)a) / e % s + s) % s;
+    return d < V || s - d < V;
 }
 
 // log2 of a page size of 8 .. 256, or -1
@@ -48,6 +79,10 @@ extern "C" int beam_select(const void* logits, long long row_stride, int dtype, 
     const BeamLayout L = beam_layout(G * N, V);
     int rc = check_ws(ws, ws_bytes, L.total);
     if (rc) return rc;
+    const long long out = (long long)G * M;
+    if (meet({{tokens, out, 4}, {ancestors, out, 4}, {out_scores, out, 4}, {out_finished, out, 4}},
+             {{scores, (long long)G * N, 4}, {finished, (long long)G * N, 4}}))
+        return SMCSD_ERR_INVALID_ARG;
     BeamParams p{};
     p.logits = logits;
     p.row_stride = row_stride;
@@ -117,6 +152,10 @@ static int fork_or_free(const int32_t* parents, const int32_t* lengths, int S, c
     if ((long long)S * ((pages_per_seq + 1023) / 1024) > 0x7fffffffLL) return SMCSD_ERR_INVALID_ARG;  // blocks
     int rc = check_ws(ws, ws_bytes, 256);
     if (rc) return rc;
+    const long long n = (long long)S * pages_per_seq;
+    if (meet({{table_out, n, 4}, {refcount_out, num_pages, 4}},
+             {{table_in, n, 4}, {refcount_in, num_pages, 4}, {parents, S, 4}, {lengths, S, 4}}))
+        return SMCSD_ERR_INVALID_ARG;
     const ForkParams p{parents,  lengths, S,           table_in,  table_out, pages_per_seq,
                        shift,    refcount_in, refcount_out, num_pages, ws};
     return from_cuda(launch_fork(p, (cudaStream_t)stream));
@@ -146,6 +185,10 @@ extern "C" int kv_compact(int S, const int32_t* table_in, int32_t* table_out, in
     if (num_pages > 1 && (!src || !dst || src == dst)) return SMCSD_ERR_INVALID_ARG;
     int rc = check_ws(ws, ws_bytes, compact_bytes(num_pages));
     if (rc) return rc;
+    const long long n = (long long)S * pages_per_seq;
+    if (meet({{table_out, n, 4}, {refcount_out, num_pages, 4}, {src, num_pages / 2, 4}, {dst, num_pages / 2, 4}, {counts, 2, 4}},
+             {{table_in, n, 4}, {refcount_in, num_pages, 4}}))
+        return SMCSD_ERR_INVALID_ARG;
     CompactParams p{};
     p.table_in = table_in;
     p.table_out = table_out;
@@ -198,6 +241,8 @@ extern "C" int distill_loss(const void* logits, long long row_stride, int dtype,
     if (dlogits == logits && dlogits_stride != row_stride) return SMCSD_ERR_INVALID_ARG;
     int rc = check_ws(ws, ws_bytes, 256);
     if (rc) return rc;
+    if (dlogits && dlogits != logits && rows_meet(logits, row_stride, dlogits, dlogits_stride, R, V, b)) return SMCSD_ERR_INVALID_ARG;
+    if (meet({{loss, R, 4}}, {{top_tokens, (long long)R * K, 4}, {top_values, (long long)R * K, 4}, {weight, R, 4}})) return SMCSD_ERR_INVALID_ARG;
     DistillParams p{};
     p.logits = logits;
     p.row_stride = row_stride;

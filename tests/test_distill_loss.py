@@ -298,6 +298,20 @@ def test_a_teachers_list_from_its_logits(smcsd):
     assert float(loss.abs().max()) < 1e-4 and float(grad.abs().max()) < 1e-5
 
 
+def test_gradient_between_the_logits_rows(smcsd):
+    R, V = 5, 1003
+    z, tokens, values = make(11, R, V, 12, "bf16")
+    want = smcsd.distill_loss(z, tokens, values, V)
+    both = torch.zeros(R, 2 * V + 5, device="cuda", dtype=z.dtype)
+    both[:, :V] = z
+    loss, grad = smcsd.distill_loss(both[:, :V], tokens, values, V, dlogits=both[:, V:2 * V])
+    assert torch.equal(loss, want[0]) and torch.equal(grad, want[1]) and torch.equal(both[:, :V], z) and int(both[:, 2 * V:].count_nonzero()) == 0
+    with pytest.raises(smcsd.SMCSDError):
+        smcsd.distill_loss(both[:, :V], tokens, values, V, dlogits=both[:, V - 1:2 * V - 1])
+    with pytest.raises(smcsd.SMCSDError):
+        smcsd.distill_loss(z, tokens, values, V, weight=loss, loss=loss)
+
+
 @pytest.mark.parametrize("V", [24_000, 128_256])
 def test_lists_that_change_meanwhile_harm_nobody(smcsd, V):
     """A row's blocks may read different lists where another stream writes them: the results are anything, the calls after them right."""

@@ -107,6 +107,32 @@ def test_distill_loss(lib):  # noqa: F811
         assert call(dtype=dtype, V=most + 1, stride=most + 1, gstride=most + 1) == -1
 
 
+def test_outputs_that_overlap_inputs(lib):  # noqa: F811
+    """Every call here is refused: what is written would meet what is read."""
+    beam = caller(lib.beam_select, [
+        ("logits", P, FAKE), ("stride", LL, 100), ("dtype", I, 1), ("G", I, 4), ("N", I, 2), ("V", I, 100), ("M", I, 3), ("T", F, 1.0),
+        ("scores", P, FAR), ("finished", P, P(1 << 41)), ("pad", I, 0), ("eos", I, -1), ("tokens", P, FAKE), ("anc", P, FAKE), ("out", P, FAKE),
+        ("over", P, FAKE), ("ws", P, FAKE), ("n", SZ, 1 << 24), ("stream", P, None)])
+    refused(beam, -1, **{out: [P((1 << 40) + 28), P((1 << 40) - 44), P((1 << 41) + 4)] for out in ("tokens", "anc", "out", "over")})
+    for name in ("kv_fork", "kv_free"):
+        fork = caller(getattr(lib, name), ([("parents", P, FAKE)] if name == "kv_fork" else []) + [
+            ("lengths", P, FAKE), ("S", I, 4), ("tin", P, FAR), ("tout", P, P(8192)), ("P", I, 16), ("page", I, 16), ("rin", P, P(1 << 41)),
+            ("rout", P, P(1 << 42)), ("num", I, 100), ("ws", P, FAKE), ("n", SZ, 256), ("stream", P, None)])
+        refused(fork, -1, tout=[P((1 << 40) + 252), P((1 << 40) - 252), P((1 << 41) + 4), P(4096 + 12)], rout=[P((1 << 40) - 396), P((1 << 41) + 396), FAKE])
+    compact = caller(lib.kv_compact, [
+        ("S", I, 4), ("tin", P, FAR), ("tout", P, P(8192)), ("P", I, 16), ("rin", P, P(1 << 41)), ("rout", P, P(1 << 42)), ("num", I, 100),
+        ("src", P, P(1 << 43)), ("dst", P, P(1 << 44)), ("counts", P, P(1 << 45)), ("ws", P, FAKE), ("n", SZ, 1 << 20), ("stream", P, None)])
+    near = [P((1 << 40) + 252), P((1 << 41) + 396)]
+    refused(compact, -1, tout=near, rout=near, src=near, dst=near, counts=near)
+    distill = caller(lib.distill_loss, [
+        ("logits", P, FAR), ("stride", LL, 220), ("dtype", I, 1), ("R", I, 4), ("V", I, 100), ("tokens", P, P(1 << 41)), ("values", P, P(1 << 42)),
+        ("K", I, 5), ("T", F, 1.0), ("rest", I, 0), ("weight", P, P(1 << 43)), ("loss", P, FAKE), ("grad", P, P(1 << 44)), ("gstride", LL, 220),
+        ("ws", P, FAKE), ("n", SZ, 256), ("stream", P, None)])
+    refused(distill, -1, grad=[P((1 << 40) + d) for d in (2, 198, -2, -198, 440 + 198, 242, 1320 + 198, -1320 - 198)],
+            loss=[P((1 << 41) + 76), P((1 << 42) - 12), P((1 << 43) + 4)])
+    assert distill(grad=P((1 << 40) + 200), gstride=440) == -1  # between the logits' rows, but not all of them
+
+
 def test_the_python_calls_refuse_wrong_tensors():
     import torch
 
