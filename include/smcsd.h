@@ -45,8 +45,8 @@
  *     distill_loss for another block of their cluster give up after a few seconds at most and record
  *     SMCSD_ERR_TIMEOUT. The counters that such a call leaves behind are cleared by
  *     smcsd_check_status; calls that use the buffer before that are unspecified. Two kinds of waits have
- *     no limit of their own: the cluster barriers of kv_slot_map, kv_fork, kv_free, kv_compact and
- *     distill_loss (a cluster's blocks run at the same time), and those of tree_attention in bf16
+ *     no limit of their own: the cluster barriers of kv_slot_map, kv_pagetable_remap, kv_fork, kv_free,
+ *     kv_compact and distill_loss (a cluster's blocks run at the same time), and those of tree_attention in bf16
  *     for its SM's tensor memory, as long as another kernel holds some of it. So a bad input cannot fault or hang the GPU; outputs are unspecified
  *     after such an error.
  */

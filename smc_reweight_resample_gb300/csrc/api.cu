@@ -380,10 +380,8 @@ extern "C" int kv_pagetable_remap(const int32_t* ancestors, const int32_t* resam
     int rc = check_ws(ws, ws_bytes, ws_small_bytes());
     if (rc) return rc;
     cudaStream_t st = (cudaStream_t)stream;
-    if (refcount && cudaMemsetAsync(refcount, 0, (size_t)num_pages * sizeof(int32_t), st) != cudaSuccess)
-        return SMCSD_ERR_CUDA;
     RemapParams p{ancestors, resampled, G, N, table_in, table_out, pages_per_seq, refcount, num_pages, ws};
-    return from_cuda(launch_remap(p, st));
+    return from_cuda(refcount ? launch_remap_counted(p, st) : launch_remap(p, st));
 }
 
 extern "C" int pacer_block_stop_pos(const void* hidden, const void* w, const void* pos_emb,

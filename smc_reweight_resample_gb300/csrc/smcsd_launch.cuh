@@ -131,7 +131,8 @@ cudaError_t launch_finish(const StreamParams& p, cudaStream_t st);      // finis
 cudaError_t launch_stream_tma(const StreamParams& p, cudaStream_t st);  // aligned rows
 cudaError_t launch_sd_sample(const SampleParams& p, cudaStream_t st);
 cudaError_t launch_resample(const ResampleParams& p, cudaStream_t st);
-cudaError_t launch_remap(const RemapParams& p, cudaStream_t st);
+cudaError_t launch_remap(const RemapParams& p, cudaStream_t st);          // counts from what refcount holds
+cudaError_t launch_remap_counted(const RemapParams& p, cudaStream_t st);  // from zero
 cudaError_t launch_pacer(const PacerParams& p, cudaStream_t st);
 cudaError_t launch_wait_selftest(void* ws, bool front, unsigned long long limit_ns, cudaStream_t st);
 

@@ -59,6 +59,26 @@ def test_large_tables_of_every_row_and_address(smcsd, S, P, shift):
     assert np.array_equal(host(got[0]), want[0]) and np.array_equal(host(got[1]), want[1])
 
 
+@pytest.mark.parametrize("G,N,P,num", [(1, 1, 1, 1), (1, 4, 33, 200), (3, 5, 100, 1500), (4, 8, 128, 4096), (8, 8, 128, 8192), (8, 8, 129, 8192), (2, 4, 10, 9000)])
+def test_pagetable_remap_of_every_size(smcsd, G, N, P, num):
+    rng = np.random.default_rng(G + P)
+    table = rng.integers(-1, num, (G * N, P)).astype(np.int32)
+    anc = rng.integers(0, N, G * N).astype(np.int32)
+    resampled = rng.integers(0, 2, G).astype(np.int32)
+    ws = smcsd.Workspace(smcsd.OP_PAGETABLE_REMAP, G)
+    for res in (None, resampled):
+        group = np.arange(G * N) // N
+        row = group * N + (anc if res is None else np.where(res[group] != 0, anc, np.arange(G * N) % N))
+        want = table[row]
+        got, count = smcsd.kv_pagetable_remap(dev(anc), None if res is None else dev(res), G, N, dev(table), P, num, ws=ws)
+        assert smcsd.check_status(ws) == 0
+        assert np.array_equal(host(got), want) and np.array_equal(host(count), np.bincount(want[want >= 0].ravel(), minlength=num))
+    table[0, 0] = num
+    anc[-1] = N
+    smcsd.kv_pagetable_remap(dev(anc), None, G, N, dev(table), P, num, ws=ws)
+    assert smcsd.check_status(ws) == smcsd.ERR_RANGE
+
+
 def test_fork_reads_the_old_table(smcsd):
     # two sequences change places, a third follows one of them
     table = np.array([[0, 1, -1], [2, -1, -1], [3, 4, 5]], np.int32)
