@@ -74,7 +74,7 @@ def _calls_command(out: str):
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[x for d in inc for x in ("-I", d)],
             os.path.join(CSRC, "py_calls.cpp"), "-o", out, "-L", os.path.join(root, "lib"), "-ltorch_python",
-            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
 def _calls_key() -> str:
