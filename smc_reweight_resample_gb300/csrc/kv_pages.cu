@@ -18,7 +18,7 @@ constexpr int kReorderUnits = 4;  // units of a thread and turn
 constexpr long long kReorderTurn = kReorderThreads * kReorderUnits;
 
 template <typename U>
-__device__ __forceinline__ void reorder_units(const ReorderParams& p, int t, int block, int blocks) {
+__device__ __forceinline__ void reorder_units(const ReorderParams& p, const int32_t* ancestors, int t, int block, int blocks) {
     const U* src = static_cast<const U*>(p.src[t]);
     U* dst = static_cast<U*>(p.dst[t]);
     const long long w = p.row_units[t], n = w * p.G * p.M;
@@ -30,7 +30,7 @@ __device__ __forceinline__ void reorder_units(const ReorderParams& p, int t, int
             const long long i = i0 + k * kReorderThreads;
             there[k] = i < n;
             if (there[k]) {
-                const int row = (int)(i / w), g = row / p.M, a = __ldg(p.ancestors + row);
+                const int row = (int)(i / w), g = row / p.M, a = __ldg(ancestors + row);
                 there[k] = a >= 0 && a < p.N;
                 if (there[k])
                     x[k] = src[((long long)g * p.N + a) * w + (i - row * w)];
@@ -44,18 +44,21 @@ __device__ __forceinline__ void reorder_units(const ReorderParams& p, int t, int
     }
 }
 
-// All tensors in one launch: each has a run of blocks. 2.9 us for 128 rows of 12 KB in three tensors (1.6 MB either way): the launch, and
+// All tensors in one launch: each has a run of blocks. 2.7 us for 128 rows of 12 KB in three tensors (1.6 MB either way): the launch, and
 // two loads one after the other.
 __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_constant__ ReorderParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int32_t* ancestors = after_wait(p.ancestors);
     int t = 0;
     while (blockIdx.x >= p.first[t + 1]) ++t;
     const int block = (int)(blockIdx.x - p.first[t]), blocks = (int)(p.first[t + 1] - p.first[t]);
     if (p.unit[t] == 4)
-        reorder_units<uint4>(p, t, block, blocks);
+        reorder_units<uint4>(p, ancestors, t, block, blocks);
     else if (p.unit[t] == 2)
-        reorder_units<uint32_t>(p, t, block, blocks);
+        reorder_units<uint32_t>(p, ancestors, t, block, blocks);
     else
-        reorder_units<unsigned char>(p, t, block, blocks);
+        reorder_units<unsigned char>(p, ancestors, t, block, blocks);
 }
 
 cudaError_t launch_reorder(const ReorderParams& p0, cudaStream_t st) {
@@ -67,8 +70,7 @@ cudaError_t launch_reorder(const ReorderParams& p0, cudaStream_t st) {
         if (blocks > cap) blocks = cap;
         p.first[t + 1] = p.first[t] + (unsigned)blocks;
     }
-    reorder_kernel<<<p.first[p.count], kReorderThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_waiting(reorder_kernel, dim3(p.first[p.count]), kReorderThreads, 0, st, p);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -105,10 +107,17 @@ __device__ __forceinline__ void fork_change(const ForkParams& p, int id, int old
     if (fork_counts(p, old) && atomicSub(p.ref_out + old, 1) <= 0) raise_error(p.ws, kErrRange);  // held, but not counted
 }
 
-// Small tables: one cluster copies the counts and writes the new table, meets, and changes the counts. 3 us for 16 sequences of 129
+// Small tables: one cluster copies the counts and writes the new table, meets, and changes the counts. 2.5 to 2.8 us for 16 sequences of 129
 // pages and 2128 counts: latency (two launches took as long, and 2 us more to issue).
 constexpr int kForkClusterThreads = 512;
-__global__ void __launch_bounds__(kForkClusterThreads) fork_small_kernel(const __grid_constant__ ForkParams p, FastDiv by_row) {
+__global__ void __launch_bounds__(kForkClusterThreads) fork_small_kernel(const __grid_constant__ ForkParams p0, const FastDiv by_row) {
+    griddep_wait();
+    griddep_launch_dependents();
+    ForkParams p = p0;
+    p.parents = after_wait(p0.parents);
+    p.lengths = after_wait(p0.lengths);
+    p.table_in = after_wait(p0.table_in);
+    p.ref_in = after_wait(p0.ref_in);
     cg::cluster_group cl = cg::this_cluster();
     const int first = (int)cl.block_rank() * kForkClusterThreads + threadIdx.x, step = (int)cl.num_blocks() * kForkClusterThreads;
     const int P = p.pages_per_seq, n = p.S * P;
@@ -212,12 +221,7 @@ cudaError_t launch_fork(const ForkParams& p, cudaStream_t st) {
         const long long most = n > p.num_pages ? n : p.num_pages;
         int C = 1;
         while (C < 8 && most > C * kForkClusterThreads) C *= 2;
-        cfg.gridDim = dim3(C);
-        cfg.blockDim = dim3(kForkClusterThreads);
-        at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = C;
-        at.val.clusterDim.y = at.val.clusterDim.z = 1;
-        return cudaLaunchKernelEx(&cfg, fork_small_kernel, p, make_fastdiv((uint32_t)p.pages_per_seq));
+        return launch_waiting(fork_small_kernel, dim3(C), kForkClusterThreads, C, st, p, make_fastdiv((uint32_t)p.pages_per_seq));
     }
     fork_counts_kernel<<<(unsigned)((p.num_pages - 1) / (kForkThreads * kForkCounts) + 1), kForkThreads, 0, st>>>(p);
     const cudaError_t e = cudaGetLastError();
@@ -360,6 +364,7 @@ constexpr int kApplyThreads = 256;
 
 __global__ void __launch_bounds__(kApplyThreads) compact_apply_kernel(const __grid_constant__ CompactParams p) {
     griddep_wait();
+    griddep_launch_dependents();
     compact_apply(p, __ldcg(p.counts), __ldcg(p.counts + 1), (long long)blockIdx.x * kApplyThreads + threadIdx.x,
                   (long long)gridDim.x * kApplyThreads);
 }
@@ -402,9 +407,11 @@ constexpr int kCopyLoads = 8;  // 16-byte vectors of a thread and turn: 32 KB a 
 
 // An item is one page of one cache; blocks take them in turn.
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyParams p) {
+    griddep_wait();
+    const int32_t *moved = after_wait(p.src), *moved_to = after_wait(p.dst), *count = after_wait(p.count);
     int n = p.n;
-    if (p.count) {
-        const int c = __ldg(p.count);
+    if (count) {
+        const int c = __ldg(count);
         if (c < 0 || c > n) {
             if (threadIdx.x == 0) raise_error(p.ws, kErrRange);
             return;
@@ -416,7 +423,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
     for (long long it = blockIdx.x; it < items; it += gridDim.x) {
         const long long move = it / pieces, piece = it - move * pieces;
         const int i = (int)(move / p.caches), c = (int)(move - (long long)i * p.caches);
-        const int src = __ldg(p.src + i), dst = __ldg(p.dst + i);
+        const int src = __ldg(moved + i), dst = __ldg(moved_to + i);
         if (src < 0 && dst < 0) continue;
         if (src < 0 || dst < 0 || src >= p.num_pages || dst >= p.num_pages) {
             if (threadIdx.x == 0) raise_error(p.ws, kErrRange);
@@ -438,8 +445,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
 cudaError_t launch_copy_pages(const CopyParams& p, cudaStream_t st) {
     const long long pieces = (p.page_vecs + kCopyThreads * kCopyLoads - 1) / (kCopyThreads * kCopyLoads);
     const long long items = (long long)p.n * p.caches * pieces, cap = 8ll * device_sm_count();
-    copy_pages_kernel<<<(unsigned)(items < cap ? items : cap), kCopyThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_waiting(copy_pages_kernel, dim3((unsigned)(items < cap ? items : cap)), kCopyThreads, 0, st, p);
 }
 
 }  // namespace smcsd

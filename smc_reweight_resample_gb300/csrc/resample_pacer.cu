@@ -54,7 +54,19 @@ __device__ __forceinline__ void remap_entry(const RemapParams& p, long long i, b
     }
 }
 
-__global__ void __launch_bounds__(256) remap_kernel(const __grid_constant__ RemapParams p) {
+// The kernels' arguments once what ran before is done.
+__device__ __forceinline__ RemapParams remap_start(const RemapParams& p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    RemapParams q = p;
+    q.ancestors = after_wait(p.ancestors);
+    q.resampled = after_wait(p.resampled);
+    q.table_in = after_wait(p.table_in);
+    return q;
+}
+
+__global__ void __launch_bounds__(256) remap_kernel(const __grid_constant__ RemapParams p0) {
+    const RemapParams p = remap_start(p0);
     const long long total = (long long)p.G * p.N * p.pages_per_seq;
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
          i += (long long)gridDim.x * blockDim.x)
@@ -64,7 +76,8 @@ __global__ void __launch_bounds__(256) remap_kernel(const __grid_constant__ Rema
 // Small tables whose counts are to be cleared first: one cluster does that, meets, and goes on, in place of a launch before
 // the other kernel.
 constexpr int kRemapThreads = 512;
-__global__ void __launch_bounds__(kRemapThreads) remap_small_kernel(const __grid_constant__ RemapParams p) {
+__global__ void __launch_bounds__(kRemapThreads) remap_small_kernel(const __grid_constant__ RemapParams p0) {
+    const RemapParams p = remap_start(p0);
     cg::cluster_group cl = cg::this_cluster();
     const int first = (int)cl.block_rank() * kRemapThreads + threadIdx.x, step = (int)cl.num_blocks() * kRemapThreads;
     for (int i = first; i < p.num_pages; i += step) p.refcount[i] = 0;
@@ -203,12 +216,11 @@ cudaError_t launch_remap(const RemapParams& p, cudaStream_t st) {
     const long long cap = (long long)device_sm_count() * 8;
     if (blocks > cap) blocks = cap;
     if (blocks < 1) blocks = 1;
-    remap_kernel<<<(int)blocks, 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_waiting(remap_kernel, dim3((unsigned)blocks), 256, 0, st, p);
 }
 
-// One cluster / a clearing launch before: 4 rows of 128 pages, 1024 counts 2.5 / 6.3 us; 32 rows, 4096 counts 2.9 / 3.2 (called 4.8 / 8.3); 64
-// rows, 8192 counts 3.5 / 3.3 (called 5.8 / 7.9); 128 rows, 16384 counts 4.9 / 3.4.
+// One cluster / a clearing launch before: 4 rows of 128 pages, 1024 counts 2.5 / 6.3 us; 32 rows, 4096 counts 2.4 / 3.2 (called 4.3 / 8.3); 64
+// rows, 8192 counts 3.1 / 3.3 (called 4.4 / 7.9); 128 rows, 16384 counts 4.9 / 3.4.
 cudaError_t launch_remap_counted(const RemapParams& p, cudaStream_t st) {
     constexpr int kMost = 8192;  // entries or counts
     const long long total = (long long)p.G * p.N * p.pages_per_seq, most = total > p.num_pages ? total : p.num_pages;
@@ -218,17 +230,7 @@ cudaError_t launch_remap_counted(const RemapParams& p, cudaStream_t st) {
     }
     int C = 1;
     while (C < 8 && most > C * kRemapThreads) C *= 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(C);
-    cfg.blockDim = dim3(kRemapThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = C;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, remap_small_kernel, p);
+    return launch_waiting(remap_small_kernel, dim3(C), kRemapThreads, C, st, p);
 }
 
 cudaError_t launch_pacer(const PacerParams& p, cudaStream_t st) {

@@ -390,6 +390,12 @@ __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A pointer whose loads come after an earlier griddep_wait, those of read-only data too, which a compiler may otherwise move.
+template <typename T>
+__device__ __forceinline__ T* after_wait(T* p) {
+    asm volatile("" : "+l"(p));
+    return p;
+}
 
 // Completion count. Every arrival is a release at device scope (the warp's stores, ordered
 // before lane 0 by the warp barrier, become visible before the count); only the last arriver

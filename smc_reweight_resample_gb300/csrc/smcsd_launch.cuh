@@ -131,6 +131,24 @@ cudaError_t launch_finish(const StreamParams& p, cudaStream_t st);      // finis
 cudaError_t launch_stream_tma(const StreamParams& p, cudaStream_t st);  // aligned rows
 cudaError_t launch_sd_sample(const SampleParams& p, cudaStream_t st);
 cudaError_t launch_resample(const ResampleParams& p, cudaStream_t st);
+// Launches a kernel that begins with griddep_wait, in clusters of `cluster` blocks, so that its launch goes on beside the kernel before it.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_waiting(void (*kernel)(Params...), dim3 grid, int threads, int cluster, cudaStream_t st, const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_remap(const RemapParams& p, cudaStream_t st);          // counts from what refcount holds
 cudaError_t launch_remap_counted(const RemapParams& p, cudaStream_t st);  // from zero
 cudaError_t launch_pacer(const PacerParams& p, cudaStream_t st);

@@ -243,3 +243,94 @@ def test_two_graphs_with_one_workspace(smcsd, name):
     for got in outs:
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------------------------------------
+# kernels whose launch goes on beside the one before them: each call's input is the output of the one before
+# ------------------------------------------------------------------------------------------------
+
+def chain(smcsd, st, wait, between):
+    """Selection, states, tables, forks, freeing, compaction and copies, each from what the one before wrote."""
+    z, states, table, ref, cache = (st[k] for k in ("z", "states", "table", "ref", "cache"))
+    G, N, V, P, num = 3, 4, 700, 40, 900
+    S = G * N
+    ws = st["ws"]
+    states, cache, scores = states.clone(), cache.clone(), torch.zeros(S, device="cuda")
+    for step in range(6):
+        best = smcsd.beam_select(z[step], G, N, V, N, scores=scores, ws=ws["beam"])
+        wait()
+        scores = best["scores"]
+        states, = smcsd.state_reorder([states], best["ancestors"], G, N, ws=ws["state"])
+        wait()
+        table, ref = smcsd.kv_pagetable_remap(best["ancestors"], None, G, N, table, P, num, ws=ws["remap"])
+        wait()
+        states2 = between(states)
+        parents = (best["tokens"] % S).to(torch.int32)
+        wait()
+        table, ref = smcsd.kv_fork(table, ref, parents, 16, ws=ws["fork"])
+        wait()
+        lengths = states2[:, 0].abs().to(torch.int32) % (P * 16)
+        table, ref = smcsd.kv_free(table, ref, lengths, 16, ws=ws["fork"])
+        wait()
+        moved = smcsd.kv_compact(table, ref, ws=ws["compact"])
+        wait()
+        table, ref = moved["table_out"], moved["refcount_out"]
+        smcsd.kv_copy_pages([cache], moved["src"], moved["dst"], count=moved["counts"], ws=ws["fork"])
+        wait()
+        states, = smcsd.state_reorder([states2], best["ancestors"], G, N, ws=ws["state"])
+        wait()
+    return scores, states, table, ref, cache
+
+
+@pytest.mark.parametrize("how", ["stream", "graph", "copies between", "two streams", "graph of two streams"])
+def test_a_chain_without_a_wait_is_the_one_with_waits(smcsd, how):
+    G, N, V, P, num = 3, 4, 700, 40, 900
+    S = G * N
+    rng = np.random.default_rng(5)
+    gen = torch.Generator("cuda").manual_seed(5)
+    z = torch.randn(6, S, V, device="cuda", generator=gen) * 3
+    states = torch.randint(-20_000, 20_000, (S, 333), device="cuda", generator=gen, dtype=torch.int32)
+    table = np.where(rng.random((S, P)) < 0.8, rng.integers(0, num, (S, P)), -1).astype(np.int32)
+    ref = np.bincount(table[table >= 0], minlength=num).astype(np.int32)
+    cache = torch.randn(num, 64, device="cuda", generator=gen)
+    ws = dict(beam=smcsd.Workspace(smcsd.OP_BEAM_SELECT, S, 0, V), state=smcsd.Workspace(smcsd.OP_STATE_REORDER, 1),
+              remap=smcsd.Workspace(smcsd.OP_PAGETABLE_REMAP, G), fork=smcsd.Workspace(smcsd.OP_KV_FORK, 1),
+              compact=smcsd.Workspace(smcsd.OP_KV_COMPACT, 1, 0, num))
+    st = dict(z=z, states=states, table=dev(table), ref=dev(ref), cache=cache, ws=ws)
+    side = torch.cuda.Stream()
+
+    def copied(x):
+        y = torch.zeros_like(x)
+        y.copy_(x)
+        return y
+
+    def aside(x):  # by way of another stream
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            y = torch.empty_like(x)
+            y.copy_(x)
+        here.wait_stream(side)
+        y.record_stream(here)
+        return y
+
+    want = chain(smcsd, st, torch.cuda.synchronize, lambda x: x)
+    torch.cuda.synchronize()
+    between = {"copies between": copied, "two streams": aside, "graph of two streams": aside}.get(how, lambda x: x)
+    if how.startswith("graph"):
+        chain(smcsd, st, lambda: None, lambda x: x)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = chain(smcsd, st, lambda: None, between)
+        for _ in range(5):
+            graph.replay()
+        torch.cuda.synchronize()
+    else:
+        for _ in range(5):
+            got = chain(smcsd, st, lambda: None, between)
+        torch.cuda.synchronize()
+    for w in ws.values():
+        assert smcsd.check_status(w) == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
