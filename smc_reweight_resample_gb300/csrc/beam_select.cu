@@ -68,7 +68,7 @@ struct BeamRow {
 template <int DT>
 __device__ __forceinline__ BeamRow<DT> beam_row(const BeamParams& p, long long r) {
     BeamRow<DT> b;
-    b.row = static_cast<const char*>(p.logits) + r * p.row_stride * Geo<DT>::kBytes;
+    b.row = static_cast<const char*>(after_wait(p.logits)) + r * p.row_stride * Geo<DT>::kBytes;
     const int off = (int)(reinterpret_cast<uintptr_t>(b.row) & 15u);
     b.at = b.row - off;
     b.shift = off / Geo<DT>::kBytes;
@@ -509,7 +509,7 @@ __device__ __forceinline__ dd dd_log_fast(float v) {
 constexpr int kEnded = -1;
 __device__ __forceinline__ uint64_t place_of(int beam, int token) { return (uint64_t)(uint32_t)beam << 32 | (uint32_t)token; }
 __device__ __forceinline__ float start_score(const BeamParams& p, int g, int beam) {
-    return p.scores ? __ldg(p.scores + (long long)g * p.N + beam) : 0.0f;
+    return p.scores ? __ldg(after_wait(p.scores) + (long long)g * p.N + beam) : 0.0f;
 }
 
 // Calls f(logit, beam, token) for every token of the sets in list2 whose logit is not below its beam's zmin. Half a warp takes a set,
@@ -972,6 +972,7 @@ __device__ __forceinline__ void row_finish(const BeamParams& p, const BeamShared
 template <int DT, int TH, bool ONE>
 __global__ void __launch_bounds__(TH, TH == kBeamWide ? 1 : ONE ? 8 : 5) beam_kernel(const __grid_constant__ BeamParams p) {
     __shared__ BeamCounts c;
+    griddep_wait();
     const BeamShared s = beam_shared(p.N, p.M);
     constexpr int kWarps = TH / 32;
     const int g = blockIdx.x / p.blocks, b = blockIdx.x - g * p.blocks;
@@ -983,7 +984,7 @@ __global__ void __launch_bounds__(TH, TH == kBeamWide ? 1 : ONE ? 8 : 5) beam_ke
             const float score = i < p.N ? start_score(p, g, i) : kNegInf;
             if (!(score < kPosInf) && b == 0) raise_error(p.ws, kErrNonfinite);
             const bool some = score > kNegInf && score < kPosInf;
-            const bool ended = some && p.finished && __ldg(p.finished + (long long)g * p.N + i);
+            const bool ended = some && p.finished && __ldg(after_wait(p.finished) + (long long)g * p.N + i);
             const unsigned l = __ballot_sync(0xffffffffu, some && !ended), o = __ballot_sync(0xffffffffu, ended);
             const unsigned before = (1u << lane) - 1u;
             if (some && !ended) s.live(live + __popc(l & before)) = i;
@@ -1031,8 +1032,7 @@ static cudaError_t launch_beam_as(const BeamParams& p, cudaStream_t st) {
             return e;
         }
     }
-    beam_kernel<DT, TH, ONE><<<(unsigned)p.G * (unsigned)p.blocks, TH, shared, st>>>(p);
-    return cudaGetLastError();
+    return launch_waiting(beam_kernel<DT, TH, ONE>, dim3((unsigned)p.G * (unsigned)p.blocks), TH, shared, 0, st, p);
 }
 
 cudaError_t launch_beam(const BeamParams& p0, int dtype, cudaStream_t st) {

@@ -191,7 +191,7 @@ struct Share {
     int n, e0, V;
     __device__ Share(const DistillParams& p, int r, int rank) {
         constexpr int PV = Geo<DT>::kPerVec, B = Geo<DT>::kBytes;
-        const char* row = static_cast<const char*>(p.logits) + (long long)r * p.row_stride * B;
+        const char* row = static_cast<const char*>(after_wait(p.logits)) + (long long)r * p.row_stride * B;
         const int shift = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / B;
         const int first = rank * p.vecs, all = (p.V + shift + PV - 1) / PV - first;
         V = p.V;
@@ -234,8 +234,8 @@ __device__ __forceinline__ bool list_entry(const DistillParams& p, DistillShared
     e.token = -1;
     e.value = kNegInf;
     if (tid < p.K) {
-        e.token = __ldg(p.tokens + (long long)r * p.K + tid);
-        e.value = __ldg(p.values + (long long)r * p.K + tid);
+        e.token = __ldg(after_wait(p.tokens) + (long long)r * p.K + tid);
+        e.value = __ldg(after_wait(p.values) + (long long)r * p.K + tid);
         if (e.token < 0 || e.token >= p.V) {
             if (e.token != -1) raise_error(p.ws, kErrRange);
             e.token = -1;
@@ -373,12 +373,13 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistill
         wait_told(bar, p.ws);
     };
 
+    griddep_wait();
     const Share<DT> h(p, r, rank);
     Entry e{};
     const bool some = list_entry(p, s, r, e);
     const int token = e.token;
     e.first = token >= 0;
-    const float weight = p.weight ? __ldg(p.weight + r) : 1.0f;
+    const float weight = p.weight ? __ldg(after_wait(p.weight) + r) : 1.0f;
     char* out = static_cast<char*>(p.grad) + (long long)r * p.grad_stride * B;
 
     if (!some || (weight == 0.0f && !p.loss)) {
@@ -553,6 +554,7 @@ __global__ void __launch_bounds__(kDistillThreads, 6) distill_loss_kernel(const 
     const int C = p.ctas, rank = (int)cl.block_rank(), tid = threadIdx.x;
     const int r = blockIdx.x / C;
     auto started = cl.barrier_arrive();
+    griddep_wait();
     const Share<DT> h(p, r, rank);
     if (p.rest)
         for (int i = tid; i < (h.n * PV + 31) / 32; i += kDistillThreads) s_listed[i] = 0;
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kDistillThreads, 6) distill_loss_kernel(const 
     e.first = e.token >= 0;
     float z = kNegInf;  // of all shares: with a rest every block needs the listed tokens' mass, without one the first the loss
     if (e.token >= 0 && (p.rest || rank == 0))
-        z = logit_at<DT>(static_cast<const char*>(p.logits) + (long long)r * p.row_stride * B, e.token);
+        z = logit_at<DT>(static_cast<const char*>(after_wait(p.logits)) + (long long)r * p.row_stride * B, e.token);
     if (p.rest) {
         const int at = e.token - h.e0;
         if (e.token >= 0 && at >= 0 && at < h.n * PV) atomicOr(s_listed + (at >> 5), 1u << (at & 31));
@@ -651,18 +653,7 @@ static cudaError_t launch_rows(F kernel, const DistillParams& p, int threads, si
         cudaGetLastError();
         return e;
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((long long)p.R * p.ctas));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = shared;
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = p.ctas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return launch_waiting(kernel, dim3((unsigned)((long long)p.R * p.ctas)), threads, shared, p.ctas, st, p);
 }
 
 template <int DT>

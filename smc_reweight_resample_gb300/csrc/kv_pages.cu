@@ -70,7 +70,7 @@ cudaError_t launch_reorder(const ReorderParams& p0, cudaStream_t st) {
         if (blocks > cap) blocks = cap;
         p.first[t + 1] = p.first[t] + (unsigned)blocks;
     }
-    return launch_waiting(reorder_kernel, dim3(p.first[p.count]), kReorderThreads, 0, st, p);
+    return launch_waiting(reorder_kernel, dim3(p.first[p.count]), kReorderThreads, 0, 0, st, p);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -140,12 +140,14 @@ __global__ void __launch_bounds__(kForkClusterThreads) fork_small_kernel(const _
 }
 
 __global__ void __launch_bounds__(kForkThreads) fork_counts_kernel(const __grid_constant__ ForkParams p) {
-    griddep_launch_dependents();
+    griddep_wait();
+    griddep_launch_dependents();  // the next kernel reads the old table at once
+    const int32_t* ref_in = after_wait(p.ref_in);
     const long long i0 = (long long)blockIdx.x * kForkThreads * kForkCounts + threadIdx.x;
     int x[kForkCounts];
 #pragma unroll
     for (int k = 0; k < kForkCounts; ++k)
-        if (i0 + k * kForkThreads < p.num_pages) x[k] = __ldg(p.ref_in + i0 + k * kForkThreads);
+        if (i0 + k * kForkThreads < p.num_pages) x[k] = __ldg(ref_in + i0 + k * kForkThreads);
 #pragma unroll
     for (int k = 0; k < kForkCounts; ++k)
         if (i0 + k * kForkThreads < p.num_pages) p.ref_out[i0 + k * kForkThreads] = x[k];
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(kWide ? kForkThreads / 2 : kForkThreads) fork_
             p.table_out[row + j] = id[k];
     }
     griddep_wait();  // the counts have been copied
+    griddep_launch_dependents();
 #pragma unroll
     for (int k = 0; k < kForkEntries; ++k) {
         if (id[k] != old[k])
@@ -210,32 +213,22 @@ __global__ void __launch_bounds__(kWide ? kForkThreads / 2 : kForkThreads) fork_
 }
 
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t st) {
-    cudaLaunchConfig_t cfg{};
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
     const long long n = (long long)p.S * p.pages_per_seq;
     if (n <= kForkMost && p.num_pages <= kForkMost) {
         // one launch in place of two, as long as a cluster of eight blocks has no more than a few turns to take
         const long long most = n > p.num_pages ? n : p.num_pages;
         int C = 1;
         while (C < 8 && most > C * kForkClusterThreads) C *= 2;
-        return launch_waiting(fork_small_kernel, dim3(C), kForkClusterThreads, C, st, p, make_fastdiv((uint32_t)p.pages_per_seq));
+        return launch_waiting(fork_small_kernel, dim3(C), kForkClusterThreads, 0, C, st, p, make_fastdiv((uint32_t)p.pages_per_seq));
     }
-    fork_counts_kernel<<<(unsigned)((p.num_pages - 1) / (kForkThreads * kForkCounts) + 1), kForkThreads, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_waiting(fork_counts_kernel, dim3((unsigned)((p.num_pages - 1) / (kForkThreads * kForkCounts) + 1)), kForkThreads, 0, 0, st, p);
     if (e != cudaSuccess) return e;
     const bool wide = p.pages_per_seq % 4 == 0 && ((reinterpret_cast<uintptr_t>(p.table_in) | reinterpret_cast<uintptr_t>(p.table_out)) & 15u) == 0;
     const int blocks = (p.pages_per_seq - 1) / ((wide ? kForkThreads / 2 : kForkThreads) * kForkEntries) + 1;
     const int per = (p.pages_per_seq - 1) / blocks + 1, threads = (per + 32 * kForkEntries - 1) / (32 * kForkEntries) * 32;
     const int pieces = (p.pages_per_seq - 1) / (threads * kForkEntries) + 1;
     if ((long long)pieces * p.S > 0x7fffffffLL) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3((unsigned)pieces * (unsigned)p.S);
-    cfg.blockDim = dim3(threads);
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    return cudaLaunchKernelEx(&cfg, wide ? fork_kernel<true> : fork_kernel<false>, p, pieces);
+    return launch_waiting(wide ? fork_kernel<true> : fork_kernel<false>, dim3((unsigned)pieces * (unsigned)p.S), threads, 0, 0, st, p, pieces);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -280,7 +273,12 @@ __device__ __forceinline__ void compact_apply(const CompactParams& p, int moves,
 // number of pages in use between the border and it, so that the k-th page from behind meets the k-th hole whatever runs first.
 // 5.6 us for 600 pages and 384 table entries, 9.5 with the table for 16384 and 13824: latency (three meetings of the cluster, two
 // passes over a warp's pages).
-__global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(const __grid_constant__ CompactParams p) {
+__global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(const __grid_constant__ CompactParams p0) {
+    griddep_wait();
+    griddep_launch_dependents();
+    CompactParams p = p0;
+    p.ref_in = after_wait(p0.ref_in);
+    p.table_in = after_wait(p0.table_in);
     __shared__ int s_warp[kCompactWarps];
     __shared__ int s_tot, s_before;
     cg::cluster_group cl = cg::this_cluster();
@@ -288,7 +286,6 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(const __g
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gw = rank * kCompactWarps + warp, nw = C * kCompactWarps;
     int32_t* place = ws_ptr<int32_t>(p.ws, p.place);
-    griddep_launch_dependents();
     const int runs = (p.num_pages + 31) / 32, per = (runs + nw - 1) / nw;
     const int r0 = min(runs, gw * per), r1 = min(runs, r0 + per);
     int have = 0;
@@ -362,9 +359,12 @@ __global__ void __launch_bounds__(kCompactThreads) compact_plan_kernel(const __g
 
 constexpr int kApplyThreads = 256;
 
-__global__ void __launch_bounds__(kApplyThreads) compact_apply_kernel(const __grid_constant__ CompactParams p) {
+__global__ void __launch_bounds__(kApplyThreads) compact_apply_kernel(const __grid_constant__ CompactParams p0) {
     griddep_wait();
     griddep_launch_dependents();
+    CompactParams p = p0;
+    p.ref_in = after_wait(p0.ref_in);
+    p.table_in = after_wait(p0.table_in);
     compact_apply(p, __ldcg(p.counts), __ldcg(p.counts + 1), (long long)blockIdx.x * kApplyThreads + threadIdx.x,
                   (long long)gridDim.x * kApplyThreads);
 }
@@ -375,25 +375,11 @@ cudaError_t launch_compact(const CompactParams& p0, cudaStream_t st) {
     // as many blocks as leave every warp about 128 pages, at most a portable cluster of 8
     int C = 1;
     while (C < 8 && p.num_pages > C * kCompactWarps * 128) C *= 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(C);
-    cfg.blockDim = dim3(kCompactThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = C;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, compact_plan_kernel, p);
+    const cudaError_t e = launch_waiting(compact_plan_kernel, dim3(C), kCompactThreads, 0, C, st, p);
     if (e != cudaSuccess || p.small) return e;
     const long long cap = 16ll * device_sm_count(), most = p.entries > p.num_pages / 2 ? p.entries : p.num_pages / 2;
     long long b = (most + kApplyThreads - 1) / kApplyThreads;
-    cfg.gridDim = dim3((unsigned)(b < cap ? b : cap));
-    cfg.blockDim = dim3(kApplyThreads);
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    return cudaLaunchKernelEx(&cfg, compact_apply_kernel, p);
+    return launch_waiting(compact_apply_kernel, dim3((unsigned)(b < cap ? b : cap)), kApplyThreads, 0, 0, st, p);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -445,7 +431,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
 cudaError_t launch_copy_pages(const CopyParams& p, cudaStream_t st) {
     const long long pieces = (p.page_vecs + kCopyThreads * kCopyLoads - 1) / (kCopyThreads * kCopyLoads);
     const long long items = (long long)p.n * p.caches * pieces, cap = 8ll * device_sm_count();
-    return launch_waiting(copy_pages_kernel, dim3((unsigned)(items < cap ? items : cap)), kCopyThreads, 0, st, p);
+    return launch_waiting(copy_pages_kernel, dim3((unsigned)(items < cap ? items : cap)), kCopyThreads, 0, 0, st, p);
 }
 
 }  // namespace smcsd

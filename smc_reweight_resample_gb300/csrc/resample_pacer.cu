@@ -216,7 +216,7 @@ cudaError_t launch_remap(const RemapParams& p, cudaStream_t st) {
     const long long cap = (long long)device_sm_count() * 8;
     if (blocks > cap) blocks = cap;
     if (blocks < 1) blocks = 1;
-    return launch_waiting(remap_kernel, dim3((unsigned)blocks), 256, 0, st, p);
+    return launch_waiting(remap_kernel, dim3((unsigned)blocks), 256, 0, 0, st, p);
 }
 
 // One cluster / a clearing launch before: 4 rows of 128 pages, 1024 counts 2.5 / 6.3 us; 32 rows, 4096 counts 2.4 / 3.2 (called 4.3 / 8.3); 64
@@ -230,7 +230,7 @@ cudaError_t launch_remap_counted(const RemapParams& p, cudaStream_t st) {
     }
     int C = 1;
     while (C < 8 && most > C * kRemapThreads) C *= 2;
-    return launch_waiting(remap_small_kernel, dim3(C), kRemapThreads, C, st, p);
+    return launch_waiting(remap_small_kernel, dim3(C), kRemapThreads, 0, C, st, p);
 }
 
 cudaError_t launch_pacer(const PacerParams& p, cudaStream_t st) {

@@ -131,12 +131,13 @@ cudaError_t launch_finish(const StreamParams& p, cudaStream_t st);      // finis
 cudaError_t launch_stream_tma(const StreamParams& p, cudaStream_t st);  // aligned rows
 cudaError_t launch_sd_sample(const SampleParams& p, cudaStream_t st);
 cudaError_t launch_resample(const ResampleParams& p, cudaStream_t st);
-// Launches a kernel that begins with griddep_wait, in clusters of `cluster` blocks, so that its launch goes on beside the kernel before it.
+// Launches a kernel that waits (griddep_wait) before it touches what earlier kernels may, in clusters of `cluster` blocks, so that its launch goes on beside the kernel before it.
 template <typename... Params, typename... Args>
-inline cudaError_t launch_waiting(void (*kernel)(Params...), dim3 grid, int threads, int cluster, cudaStream_t st, const Args&... args) {
+inline cudaError_t launch_waiting(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, int cluster, cudaStream_t st, const Args&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shared;
     cfg.stream = st;
     cudaLaunchAttribute at[2]{};
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
