@@ -19,7 +19,7 @@
 // anything are nearer than that, the block computes these beams' sums again to 2e-10 and selects anew.
 //
 // A row alone (groups of one) is selected by its logits, without its sum: less code, 64 registers, eight blocks of four warps in an SM.
-// The 64 best of 2048 rows of 128256 bf16 take 127 us, the one best 106; reading alone 93, and 78 at the copy rate: what is left
+// The 64 best of 2048 rows of 128256 bf16 take 124 us, the one best 106; reading alone 93, and 78 at the copy rate: what is left
 // is the selection of the last blocks and the four warps that each block selects with. 8 groups of 16 beams of 128256, 12 of them read,
 // take 20 us: 6 for the reading (25 MB), 1.3 for the blocks' meeting, 1.6 for the sums, 5.6 for the two levels, 0.6 for the sets, 2.2
 // for the order, 2 for the launch: latency. The sums of doubtful beams cost 30 us for a row of 128256.
