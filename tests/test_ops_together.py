@@ -334,3 +334,28 @@ def test_a_chain_without_a_wait_is_the_one_with_waits(smcsd, how):
         assert smcsd.check_status(w) == 0
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_outputs_of_one_allocation_are_tensors_of_their_own(smcsd):
+    import copy
+    import io
+    z = torch.randn(6, 500, device="cuda")
+    want = {k: host(v).copy() for k, v in smcsd.beam_select(z, 2, 3, 500, 5).items()}
+    got = smcsd.beam_select(z, 2, 3, 500, 5)
+    for k, t in got.items():
+        assert t.data_ptr() % 256 == 0 and t.is_contiguous() and t.shape == (10,) and not t.requires_grad and not t._is_view()
+        file = io.BytesIO()
+        torch.save(t, file)
+        file.seek(0)
+        assert np.array_equal(host(torch.load(file)), want[k]) and np.array_equal(host(copy.deepcopy(t)), want[k])
+        assert np.array_equal(host(t[1:4]), want[k][1:4]) and np.array_equal(host(t.view(2, 5) + 0), want[k].reshape(2, 5))
+    tokens = got["tokens"]
+    version = tokens._version
+    got["ancestors"].fill_(-7)
+    del got, t
+    junk = [torch.full((64,), 99, device="cuda", dtype=torch.int32) for _ in range(64)]
+    assert np.array_equal(host(tokens), want["tokens"]) and tokens._version == version and len(junk) == 64
+    scores = torch.zeros(10, device="cuda", requires_grad=True)
+    again = smcsd.beam_select(z, 2, 3, 500, 5)
+    (scores * again["scores"]).sum().backward()
+    assert np.array_equal(host(scores.grad), want["scores"])
