@@ -479,6 +479,9 @@ PyObject* py_reorder(PyObject*, PyObject* const* args, Py_ssize_t n) {
         if (!a.none()) given = tensors_of(args[5], kMostStates, "out"), a.skip();
         if (!given.empty() && given.size() != src.size()) value_error("out must have a tensor for each state");
         std::vector<at::Tensor> dst;
+        int64_t words = 0;
+        for (const at::Tensor* t : src) words += ((int64_t)t->nbytes() / rows * rows_out + 3) / 4;
+        Together made(ancestors, (int)src.size(), words);
         const void* from[kMostStates];
         void* to[kMostStates];
         long long bytes[kMostStates];
@@ -490,7 +493,7 @@ PyObject* py_reorder(PyObject*, PyObject* const* args, Py_ssize_t n) {
             std::vector<int64_t> shape = t.sizes().vec();
             shape[0] = rows_out;
             if (given.empty()) {
-                dst.push_back(fresh(shape, t.scalar_type(), t));
+                dst.push_back(made.take(shape, t.scalar_type()));
             } else {
                 const at::Tensor& o = *given[i];
                 if (o.device() != t.device()) value_error("tensors must be on one device");
