@@ -99,11 +99,26 @@ def _start_calls():
                     return None
         except OSError:
             pass
-    tmp = CALLS + f".tmp{os.getpid()}"
+    folder = os.path.dirname(CALLS_KEY)  # what a build that is stopped leaves behind lies among the objects
+    os.makedirs(folder, exist_ok=True)
+    tmp = os.path.join(folder, f"{os.path.basename(CALLS)}.tmp{os.getpid()}")
     try:
         return subprocess.Popen(_calls_command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp, key
     except OSError as e:
         return e
+
+
+def _remove(path):
+    if os.path.exists(path):
+        os.remove(path)
+
+
+def _drop_calls(started):
+    """Ends the module's compiler and takes its output away."""
+    if isinstance(started, tuple):
+        started[0].kill()
+        started[0].communicate()
+        _remove(started[1])
 
 
 def _finish_calls(started):
@@ -114,12 +129,11 @@ def _finish_calls(started):
     proc, tmp, key = started
     log, _ = proc.communicate()
     if proc.returncode != 0:
+        _remove(tmp)
         sys.stdout.write(log.decode(errors="replace"))
         raise RuntimeError("the compiler failed for py_calls.cpp")
-    if os.path.exists(CALLS_KEY):
-        os.remove(CALLS_KEY)
+    _remove(CALLS_KEY)
     os.replace(tmp, CALLS)
-    os.makedirs(os.path.dirname(CALLS_KEY), exist_ok=True)
     with open(CALLS_KEY, "w") as f:
         f.write(key)
 
@@ -129,8 +143,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str =
     """The library, and the call module beside it, where they are not up to date. The library is there even if the module
     cannot be built, which raises all the same."""
     calls = _start_calls()
-    if force or _stale(out):
-        _build_library(verbose, extra_flags, out, objdir)
+    try:
+        if force or _stale(out):
+            _build_library(verbose, extra_flags, out, objdir)
+    except BaseException:
+        _drop_calls(calls)
+        raise
     _finish_calls(calls)
     return out
 
@@ -156,9 +174,12 @@ def _build_library(verbose, extra_flags, out, objdir):
             failed.append(src)
     if failed:
         raise RuntimeError(f"nvcc failed for {failed}")
-    tmp = out + f".tmp{os.getpid()}"
-    subprocess.check_call([cc, *ARCH, "-shared", "-o", tmp, *objs])
-    os.replace(tmp, out)
+    tmp = os.path.join(objdir, f"{os.path.basename(out)}.tmp{os.getpid()}")
+    try:
+        subprocess.check_call([cc, *ARCH, "-shared", "-o", tmp, *objs])
+        os.replace(tmp, out)
+    finally:
+        _remove(tmp)
 
 
 if __name__ == "__main__":
