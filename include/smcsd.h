@@ -511,8 +511,8 @@ int beam_select(const void* logits, long long row_stride, int dtype, int G, int 
  * Rows of per-sequence states by ancestors: for each of `count` tensors, row g*M+m of dst = row
  * g*N + ancestors[g*M+m] of src (M = N after a resampling or a step of beam search; N = 1: copies for M beams).
  * src, dst and row_bytes are HOST arrays of `count` (at most 64) device pointers and sizes; a source of G*N and a
- * destination of G*M rows of row_bytes each, contiguous, of any type, which must not overlap. An ancestor
- * outside [0, N) is SMCSD_ERR_RANGE (device side) and leaves its rows as they are.
+ * destination of G*M rows of row_bytes each, contiguous, of any type. No destination may overlap a source (its own or another
+ * tensor's), another destination or the ancestors. An ancestor outside [0, N) is SMCSD_ERR_RANGE (device side) and leaves its rows as they are.
  */
 int state_reorder(const void* const* src, void* const* dst, const long long* row_bytes, int count,
                   const int32_t* ancestors, int G, int N, int M, void* ws, size_t ws_bytes, void* stream);

@@ -601,7 +601,7 @@ def beam_select(logits, G, N, V, M, temperature=1.0, scores=None, finished=None,
 
 def state_reorder(states, ancestors, G, N, M=None, out=None, ws=None, stream=None):
     """Rows of each of the tensors `states` [G*N, ...] by ancestors (int32 [G*M], group-local; M=None: N). Returns the list of
-    tensors [G*M, ...] (`out`, if given; not the states themselves)."""
+    tensors [G*M, ...] (`out`, if given: memory of none of the states, in whichever order)."""
     if stream is not None:
         return _on(stream, state_reorder, locals())
     ws = ws or Workspace(OP_STATE_REORDER, 1, device=ancestors.device)

@@ -2,6 +2,7 @@
 // and launches.
 #include <math.h>
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "ops_launch.cuh"
@@ -37,6 +38,21 @@ bool meet(std::initializer_list<Span> written, std::initializer_list<Span> read)
     for (const Span& a : written)
         for (const Span& b : read)
             if (meet(a, b)) return true;
+    return false;
+}
+// The same of many at once, what is written of what is written too; sorts them.
+struct Touched {
+    uintptr_t from, to;
+    bool written;
+};
+bool meet(Touched* t, int n) {
+    std::sort(t, t + n, [](const Touched& a, const Touched& b) { return a.from < b.from; });
+    uintptr_t written = 0, any = 0;  // where what came before ends
+    for (int i = 0; i < n; ++i) {
+        if (t[i].from < (t[i].written ? any : written)) return true;
+        if (t[i].written && t[i].to > written) written = t[i].to;
+        if (t[i].to > any) any = t[i].to;
+    }
     return false;
 }
 // The same of two matrices' rows of V elements of e bytes, which may lie between one another.
@@ -120,18 +136,21 @@ extern "C" int state_reorder(const void* const* src, void* const* dst, const lon
     if (rc) return rc;
     const long long most = (long long)G * (N > M ? N : M);  // rows; a tensor has at most 2^46 bytes
     ReorderParams p{};
+    Touched t[2 * kReorderMost + 1];
     for (int i = 0; i < count; ++i) {
         if (!src[i] || !dst[i] || row_bytes[i] <= 0 || row_bytes[i] > (1ll << 46) / most) return SMCSD_ERR_INVALID_ARG;
-        // a destination row may be written before a source row that shares its memory is read
         const uintptr_t a = (uintptr_t)src[i], b = (uintptr_t)dst[i];
-        const uintptr_t na = (uintptr_t)row_bytes[i] * G * N, nb = (uintptr_t)row_bytes[i] * G * M;
-        if (a < b + nb && b < a + na) return SMCSD_ERR_INVALID_ARG;
+        t[2 * i] = Touched{a, a + (uintptr_t)row_bytes[i] * G * N, false};
+        t[2 * i + 1] = Touched{b, b + (uintptr_t)row_bytes[i] * G * M, true};
         const uintptr_t all = a | b | (uintptr_t)row_bytes[i];
         p.unit[i] = all % 16 == 0 ? 4 : all % 4 == 0 ? 2 : 0;
         p.src[i] = src[i];
         p.dst[i] = dst[i];
         p.row_units[i] = row_bytes[i] >> p.unit[i];
     }
+    // all tensors are moved at one time: a destination may be written before what shares its memory is read, of whichever tensor
+    t[2 * count] = Touched{(uintptr_t)ancestors, (uintptr_t)ancestors + 4 * (uintptr_t)((long long)G * M), false};
+    if (meet(t, 2 * count + 1)) return SMCSD_ERR_INVALID_ARG;
     p.ancestors = ancestors;
     p.count = count;
     p.G = G;

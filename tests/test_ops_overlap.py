@@ -1,0 +1,26 @@
+"""Calls that would write memory that they read, or twice what they write, are refused before anything is enqueued, so they are checked
+through the C ABI without a GPU."""
+import ctypes
+
+from test_serve_args import FAKE, F, I, LL, P, SZ, caller, lib, refused  # noqa: F401
+
+PP, LLP = ctypes.POINTER(P), ctypes.POINTER(LL)
+
+
+def test_state_reorder_with_another_tensors_memory(lib):  # noqa: F811
+    """Three states of 2 * 4 rows of 16, 10 and 3 bytes, and 2 * 4 ancestors of 4 bytes."""
+    a, b, c, anc = 1 << 40, 1 << 41, 1 << 42, 1 << 43
+    x, y, z = 1 << 44, 1 << 45, 1 << 46
+    call = caller(lib.state_reorder, [
+        ("src", PP, (P * 3)(a, b, c)), ("dst", PP, (P * 3)(x, y, z)), ("bytes", LLP, (LL * 3)(16, 10, 3)), ("count", I, 3), ("anc", P, P(anc)),
+        ("G", I, 2), ("N", I, 4), ("M", I, 4), ("ws", P, FAKE), ("n", SZ, 256), ("stream", P, None)])
+    swapped = [(b, a, z), (x, c, b), (c, y, a), (b, c, a)]
+    near = [(b + 79, y, z), (b - 127, y, z), (x, a + 127, z), (x, a - 79, z), (x, y, b + 79), (x, y, a - 23)]
+    twice = [(x, x, z), (x, x + 127, z), (x, y, x - 23), (x, y, y + 79)]
+    ancestors = [(anc, y, z), (x, anc + 31, z), (x, y, anc - 23)]
+    refused(call, -1, dst=[(P * 3)(*d) for d in swapped + near + twice + ancestors])
+    # one tensor more than a pair, and as many as there may be: the last one's memory is the first one's
+    n = 64
+    src, dst = [(1 << 40) + 4096 * i for i in range(n)], [(1 << 41) + 4096 * i for i in range(n)]
+    dst[-1] = src[0] + 64
+    assert call(src=(P * n)(*src), dst=(P * n)(*dst), bytes=(LL * n)(*([16] * n)), count=n) == -1
