@@ -579,7 +579,7 @@ int kv_copy_pages(void* const* caches, int n_caches, long long page_bytes, int n
  * Either output may be NULL, loss for the backward pass alone and dlogits for the forward one; both together read the logits once,
  * as each alone does. logits, dlogits: rows row_stride and dlogits_stride elements apart, V used, of dtype, aligned to
  * it; dlogits may be logits (with one stride), else they must not overlap (rows may lie
- * between one another's); nor may loss and the other inputs. top_tokens int32, top_values float [R, K], K at most 256;
+ * between one another's); nor may either output overlap the lists, weight or the other output, nor loss the logits. top_tokens int32, top_values float [R, K], K at most 256;
  * weight, loss float [R]. V times the element size is at most 1638368 bytes. Sums are float32, the gradient is rounded once.
  * Device-side errors: SMCSD_ERR_NONFINITE (NaN or +inf in logits or values, a row of -inf), SMCSD_ERR_RANGE (a token outside
  * [-1, V), taken as none).

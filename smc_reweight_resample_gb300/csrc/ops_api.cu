@@ -67,6 +67,15 @@ bool rows_meet(const void* a, long long stride_a, const void* b, long long strid
     const __int128 s = stride_a, d = (((__int128)(uintptr_t)b - (__int128)(uintptr_t)a) / e % s + s) % s;
     return d < V || s - d < V;
 }
+// Whether R rows of V elements of e bytes have memory of a span, which may lie between them: rows that begin before its end, and end
+// behind its beginning.
+bool rows_meet(const void* rows, long long stride, int R, int V, int e, const Span& s) {
+    if (!rows || !s.at) return false;
+    const auto floor_div = [](__int128 a, __int128 b) { return a / b - (a % b < 0 ? 1 : 0); };
+    const __int128 step = (__int128)stride * e, from = (__int128)(uintptr_t)s.at - (__int128)(uintptr_t)rows;
+    const __int128 first = floor_div(from - (__int128)V * e, step) + 1, last = floor_div(from + (__int128)s.bytes - 1, step);
+    return (first > 0 ? first : 0) <= (last < R - 1 ? last : R - 1);
+}
 
 // log2 of a page size of 8 .. 256, or -1
 int page_shift(int page_size) {
@@ -261,7 +270,10 @@ extern "C" int distill_loss(const void* logits, long long row_stride, int dtype,
     int rc = check_ws(ws, ws_bytes, 256);
     if (rc) return rc;
     if (dlogits && dlogits != logits && rows_meet(logits, row_stride, dlogits, dlogits_stride, R, V, b)) return SMCSD_ERR_INVALID_ARG;
-    if (meet({{loss, R, 4}}, {{top_tokens, (long long)R * K, 4}, {top_values, (long long)R * K, 4}, {weight, R, 4}})) return SMCSD_ERR_INVALID_ARG;
+    const Span out(loss, R, 4), lists[] = {{top_tokens, (long long)R * K, 4}, {top_values, (long long)R * K, 4}, {weight, R, 4}};
+    if (rows_meet(logits, row_stride, R, V, b, out) || rows_meet(dlogits, dlogits_stride, R, V, b, out)) return SMCSD_ERR_INVALID_ARG;
+    for (const Span& list : lists)
+        if (meet(out, list) || rows_meet(dlogits, dlogits_stride, R, V, b, list)) return SMCSD_ERR_INVALID_ARG;
     DistillParams p{};
     p.logits = logits;
     p.row_stride = row_stride;

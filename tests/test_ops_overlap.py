@@ -24,3 +24,21 @@ def test_state_reorder_with_another_tensors_memory(lib):  # noqa: F811
     src, dst = [(1 << 40) + 4096 * i for i in range(n)], [(1 << 41) + 4096 * i for i in range(n)]
     dst[-1] = src[0] + 64
     assert call(src=(P * n)(*src), dst=(P * n)(*dst), bytes=(LL * n)(*([16] * n)), count=n) == -1
+
+
+def test_distill_loss_with_the_lists_memory(lib):  # noqa: F811
+    """The gradient's rows of 100 bf16, 220 apart, on the lists, the weights or the losses; the losses on the logits."""
+    z, tokens, values, weight, loss, grad = (1 << k for k in range(40, 46))
+    call = caller(lib.distill_loss, [
+        ("logits", P, P(z)), ("stride", LL, 220), ("dtype", I, 1), ("R", I, 4), ("V", I, 100), ("tokens", P, P(tokens)), ("values", P, P(values)),
+        ("K", I, 5), ("T", F, 1.0), ("rest", I, 0), ("weight", P, P(weight)), ("loss", P, P(loss)), ("grad", P, P(grad)), ("gstride", LL, 220),
+        ("ws", P, FAKE), ("n", SZ, 256), ("stream", P, None)])
+    rows = [0, 440, 3 * 440]  # bytes to the first, second and last row of 200 bytes
+    for name, at, size in (("tokens", tokens, 80), ("values", values, 80), ("weight", weight, 16), ("loss", loss, 16)):
+        # a row that ends in the list, or begins in it
+        refused(call, -1, grad=[P(at - r - 198) for r in rows] + [P(at - r + size - 2) for r in rows])
+    refused(call, -1, loss=[P(z + r - 12) for r in rows] + [P(z + r + 196) for r in rows])
+    assert call(grad=P(z), loss=P(z + 440 + 196)) == -1  # in place
+    assert call(dtype=0, grad=P(loss - 3 * 880 - 396)) == -1 and call(dtype=0, loss=P(z + 880 + 396)) == -1
+    for t in (tokens, values, weight):
+        assert call(loss=None, grad=P(t)) == -1
