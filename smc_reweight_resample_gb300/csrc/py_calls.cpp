@@ -522,14 +522,6 @@ PyObject* py_reorder(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// A contiguous CUDA tensor's address, or null.
-int32_t* words(const at::Tensor* t) {
-    if (!t) return nullptr;
-    if (!t->is_cuda()) value_error("tensor must be on the CUDA device");
-    if (!t->is_contiguous()) value_error("tensor must be contiguous");
-    return static_cast<int32_t*>(t->data_ptr());
-}
-
 // kv_pagetable_remap(ancestors, resampled, G, N, table_in, pages_per_seq, num_pages, table_out, refcount, with_refcount, ws, bytes)
 PyObject* py_remap(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
@@ -541,6 +533,18 @@ PyObject* py_remap(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const int pages_per_seq = a.size(), num_pages = a.size();
         const at::Tensor *table_in_out = a.tensor(), *refcount = a.tensor();
         const bool with_refcount = a.integer() != 0;
+        for (const at::Tensor* t : {&ancestors, resampled, &table, table_in_out, refcount})
+            if (t && t->scalar_type() != at::kInt) type_error(std::string("tensor must be Int, not ") + c10::toString(t->scalar_type()));
+        if (G > 0 && N > 0 && pages_per_seq > 0) {  // others are refused by the call
+            const int64_t rows = (int64_t)G * N;
+            at_least(&ancestors, rows, "ancestors");
+            at_least(resampled, G, "resampled");
+            for (const at::Tensor* t : {&table, table_in_out}) {
+                if (t && (__int128)rows * pages_per_seq > t->numel()) value_error("a table is too small");
+                rows_of(t, rows, pages_per_seq, "a table");
+            }
+        }
+        at_least(refcount, num_pages, "refcount");
         if (!table.is_cuda()) value_error("tensor must be on the CUDA device");
         const c10::cuda::CUDAGuard guard(table.device());
         Together made(table, 2, table.numel() + (with_refcount && num_pages > 0 ? num_pages : 0));
@@ -550,9 +554,10 @@ PyObject* py_remap(PyObject*, PyObject* const* args, Py_ssize_t n) {
             ref = *refcount;
         else if (with_refcount)
             ref = made.take({num_pages}, at::kInt);
+        one_device(table, {&ancestors, resampled, &table_out, ref.defined() ? &ref : nullptr});
         const Tail t(a, table);
-        check(f_remap(words(&ancestors), words(resampled), G, N, words(&table), words(&table_out), pages_per_seq,
-                      ref.defined() ? words(&ref) : nullptr, num_pages, t.ws, t.bytes, t.stream),
+        check(f_remap(i32(&ancestors), i32(resampled), G, N, i32(&table), i32(&table_out), pages_per_seq, ref.defined() ? i32(&ref) : nullptr,
+                      num_pages, t.ws, t.bytes, t.stream),
               "kv_pagetable_remap");
         return tuple({table_out, ref});
     });
