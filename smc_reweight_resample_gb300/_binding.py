@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
 import os
 
 import torch
@@ -300,8 +301,45 @@ def kv_pagetable_remap(ancestors, resampled, G, N, table_in, pages_per_seq, num_
     if stream is not None:
         return _on(stream, kv_pagetable_remap, locals())
     ws = ws or Workspace(OP_PAGETABLE_REMAP, G, 0, 1, table_in.device)
-    return (_calls or _native()).kv_pagetable_remap(ancestors, resampled, G, N, table_in, pages_per_seq, num_pages, table_out,
-                                                    refcount, bool(with_refcount), ws.ptr, ws.nbytes)
+    calls = _calls or _native(needed=False) or _Remap
+    return calls.kv_pagetable_remap(ancestors, resampled, G, N, table_in, pages_per_seq, num_pages, table_out, refcount,
+                                    bool(with_refcount), ws.ptr, ws.nbytes)
+
+
+class _Remap:
+    """kv_pagetable_remap where the call module was not built: it belongs to the step, which needs the library alone."""
+
+    @staticmethod
+    def kv_pagetable_remap(ancestors, resampled, G, N, table_in, pages_per_seq, num_pages, table_out, refcount, with_refcount, ws, nbytes):
+        given = [t for t in (ancestors, resampled, table_in, table_out, refcount) if t is not None]
+        for t in given:
+            if t.dtype != torch.int32:
+                raise TypeError(f"tensor must be Int, not {t.dtype}")
+        if min(G, N, pages_per_seq) > 0:  # others are refused by the call
+            for t, n, what in ((ancestors, G * N, "ancestors"), (resampled, G, "resampled"), (table_in, G * N * pages_per_seq, "a table"),
+                               (table_out, G * N * pages_per_seq, "a table")):
+                if t is not None and t.numel() < n:
+                    raise ValueError(f"{what} is too small")
+            for t in (table_in, table_out):
+                # one row behind the other, whichever dimensions make up a row
+                if t is not None and t.dim() > 1 and t.numel() != pages_per_seq and \
+                        pages_per_seq not in [math.prod(t.shape[k:]) for k in range(1, t.dim())]:
+                    raise ValueError("a table has rows of another size")
+        if refcount is not None and refcount.numel() < num_pages:
+            raise ValueError("refcount is too small")
+        dev = table_in.device
+        if dev.type != "cuda":
+            raise ValueError("tensor must be on the CUDA device")
+        if any(t.device != dev for t in given):
+            raise ValueError("tensors must be on one device")
+        with torch.cuda.device(dev):
+            table_out = _out(table_out, table_in.shape, torch.int32, dev)
+            if with_refcount and refcount is None:
+                refcount = torch.empty(num_pages, dtype=torch.int32, device=dev)
+            rc = load().kv_pagetable_remap(_ptr(ancestors), _ptr(resampled), G, N, _ptr(table_in), _ptr(table_out), pages_per_seq,
+                                           _ptr(refcount), num_pages, ctypes.c_void_p(ws), ctypes.c_size_t(nbytes), _stream())
+        _check(rc, "kv_pagetable_remap")
+        return table_out, refcount
 
 
 def pacer_block_stop(hidden, w, c, S, b, max_blocks, d, t0, rho, ws=None, lengths=None,
@@ -501,13 +539,16 @@ class TreeAttentionWorkspace(Workspace):
 _calls = None
 
 
-def _native():
-    """The call module (csrc/py_calls.cpp), loaded and given the library's entry points on first use."""
+def _native(needed=True):
+    """The call module (csrc/py_calls.cpp), loaded and given the library's entry points on first use. None, where it was not built and is
+    not `needed`."""
     global _calls
     if _calls is None:
         lib = load()
         path = os.path.join(_HERE, "_calls.so")
         if not os.path.exists(path):
+            if not needed:
+                return None
             raise RuntimeError(f"call module not built: {path} is missing "
                                "(run smc_reweight_resample_gb300.build.build())")
         spec = importlib.util.spec_from_file_location("smc_reweight_resample_gb300._calls", path)

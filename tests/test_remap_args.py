@@ -42,6 +42,34 @@ def test_wrong_tensors_are_refused():
     refuses(ValueError, "CUDA", table_out=i32(2, 3, 10), refcount=i32(41), table_in=i32(60))
 
 
+@pytest.fixture
+def without_module(monkeypatch, tmp_path):
+    """The binding of an install whose call module could not be built."""
+    monkeypatch.setattr(B, "_calls", None)
+    monkeypatch.setattr(B, "_HERE", str(tmp_path))
+
+
+def test_wrong_tensors_are_refused_without_the_call_module(without_module):
+    assert B._native(needed=False) is None
+    with pytest.raises(RuntimeError, match="not built"):
+        B._native()
+    check_refusals()
+    refuses(ValueError, "CUDA")
+
+
+@pytest.mark.gpu
+def test_the_call_module_is_not_needed(smcsd, without_module):
+    test_tables_of_every_shape_that_fit(smcsd)
+    test_tensors_of_two_devices_are_refused(smcsd)
+    table, resampled = torch.randperm(400, device="cuda").int().view(8, 50), torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    ancestors = torch.randint(0, 4, (8,), device="cuda", dtype=torch.int32)
+    mine = smcsd.kv_pagetable_remap(ancestors, resampled, 2, 4, table, 50, 400, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    moved = torch.arange(2, device="cuda").repeat_interleave(4) * 4 + torch.where(resampled.repeat_interleave(4) != 0, ancestors, torch.arange(8, device="cuda") % 4)
+    assert torch.equal(mine[0], table[moved]) and torch.equal(mine[1].long(), torch.bincount(table[moved].flatten(), minlength=400))
+    assert smcsd._calls is None
+
+
 @pytest.mark.gpu
 def test_tensors_of_two_devices_are_refused(smcsd):
     for name, shape in (("ancestors", (6,)), ("resampled", (2,)), ("table_out", (6, 10)), ("refcount", (40,))):
