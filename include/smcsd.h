@@ -488,8 +488,9 @@ int logits_process(const void* logits, void* out, int dtype, int R, int V, int S
  * best candidate of group g in the order of score (falling), beam, token:
  *   tokens[g*M+m] = v;  ancestors[g*M+m] = i (group-local);  out_scores[g*M+m] = its score;
  *   out_finished[g*M+m] = 1 if the beam was finished or v == eos_token, else 0.
- * Where there are fewer than M candidates (masked tokens of -inf are none), the remaining places get pad_token, 0,
- * -inf and 1. A row with nothing but -inf has no candidate; that is not an error here.
+ * Where there are fewer than M candidates, the remaining places get pad_token, 0, -inf and 1. Masked tokens of -inf
+ * are none, nor are those whose score (or z less the row's largest) lies below float32's range: a token masked with the
+ * type's lowest value is a candidate with T >= 1, and none with T < 1. A row with nothing but -inf has no candidate; that is not an error here.
  * The order is that of the scores' real values, up to 1e-9 or so: candidates of one beam are ordered by their logits
  * exactly, those of two beams by sums that are computed again, to 2e-10, where hardware exponentials could
  * not tell them apart (a slower path: some 30 us for each such row of 128256). Beams with equal scores and

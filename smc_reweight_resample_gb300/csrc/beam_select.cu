@@ -41,7 +41,8 @@ constexpr int kBeamMostCands = 1024;  // candidates that are ranked
 constexpr float kTol = 1.25e-5f;
 
 // A score as an unsigned integer of the same order: the high float first, then the low one (of a normalised double-float). 0 is
-// no score (minus infinity, NaN).
+// no score: minus infinity, and NaN, which double-floats make of what lies below float32's range (tokens masked with the lowest
+// value, by a temperature below 1).
 __device__ __forceinline__ uint32_t float_order(float f) {
     const uint32_t u = __float_as_uint(f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
@@ -953,11 +954,12 @@ __device__ __forceinline__ void row_finish(const BeamParams& p, const BeamShared
         int token = p.pad, over = 1;
         float score = kNegInf;
         if (r < n) {
-            const uint64_t key = s.key(s.order(r));
-            token = (int)~(uint32_t)key;
-            const float z = float_of_order((uint32_t)(key >> 32));
-            score = dd_add(dd_mul(two_sum(z, -s.zmax(0)), dd{p.c_hi, p.c_lo}), dd{s.base(0).x, s.base(0).y}).hi;
-            over = p.eos >= 0 && token == p.eos;
+            const uint64_t key = s.key(s.order(r)), x = score_key(p, float_of_order((uint32_t)(key >> 32)), s.zmax(0), s.base(0));
+            if (x) {  // else its score lies below float32's range, and those of all tokens behind it
+                token = (int)~(uint32_t)key;
+                score = key_value(x).hi;
+                over = p.eos >= 0 && token == p.eos;
+            }
         } else if (r == 0 && c.nover) {
             score = start_score(p, g, 0);
         }
