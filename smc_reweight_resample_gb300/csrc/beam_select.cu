@@ -395,8 +395,13 @@ struct LevelKey {
     }
 };
 // An item's score: in float32, off by at most three roundings (of the difference, of the factor, of the sum) of its terms, and for one beam in the order of
-// the logits; or as the high half of its key.
+// the logits; or as the high half of its key. The terms are the beam's constant b and c (z - m), which is not above 0: no larger than the score
+// where b <= 0, than the score and b together where it is above 0.
 constexpr float kScoreError = 3e-7f;
+// How far a float32 score next to `score` may be off, by that and by the sums.
+__device__ __forceinline__ float doubt_of(const BeamCounts& c, float score) {
+    return kTol + 2.0f * kScoreError * (fabsf(score) + fmaxf(float_of_order(c.best), 0.0f));
+}
 __device__ __forceinline__ float level_score(const BeamParams& p, const BeamShared& s, const Level& level, int i, float z, bool exact) {
     const int beam = level.beam(s, i);
     if (!exact) return z > kNegInf ? fmaf(p.c_hi, z - s.zmax(beam), s.base(beam).x) : kNegInf;
@@ -689,7 +694,7 @@ template <int TH>
 __device__ __noinline__ bool mark_near(const BeamParams& p, BeamShared s, BeamCounts& c, int g, int of, float last) {
     bool found = false;
     const auto mark = [&](int beam, float x) {
-        if (beam == of || !(fabsf(x - last) <= kTol + 2.0f * kScoreError * fabsf(last))) return;
+        if (beam == of || !(fabsf(x - last) <= doubt_of(c, last))) return;
         s.unsure(beam) = s.unsure(of) = 1;
         found = true;
     };
@@ -735,7 +740,7 @@ __device__ __forceinline__ bool rank_and_doubt(const BeamParams& p, const BeamSh
     }
     if (floor > kLowest && n >= p.M) {  // and what was left out
         const float last = key_value(s.key(s.order(p.M - 1))).hi;
-        if (last - floor <= kTol + 2.0f * kScoreError * fabsf(floor)) doubt |= mark_near<TH>(p, s, c, g, (int)(s.at(s.order(p.M - 1)) >> 32), last);
+        if (last - floor <= doubt_of(c, floor)) doubt |= mark_near<TH>(p, s, c, g, (int)(s.at(s.order(p.M - 1)) >> 32), last);
     }
     return __syncthreads_or(doubt);
 }

@@ -74,3 +74,30 @@ def test_scores_next_to_the_end_of_the_range(smcsd, N):
     scores = np.full(N, -3.3e38, np.float32)
     mine = check(smcsd, logits, 1, N, V, M, 1.0, scores)
     assert np.isneginf(mine).any() and np.isfinite(mine).any()
+
+
+def beams_that_cancel(seed, N=64, each=16):
+    """One group: beams with scores of 1e5, as bonuses make them, and a temperature that takes them back. But for one likely token a beam, all
+    candidates' scores lie near zero, 1e-4 and more apart, though z less the row's maximum is rounded in steps of 7.6e-3 / c. One token
+    in 64 is a candidate of any use, so that each stands in a range of its own."""
+    f4 = np.float32
+    rng = np.random.default_rng(seed)
+    T = f4(0.001)
+    c = 1.0 / float(T)
+    step = 2.0 ** -17 * c  # of the scores of tokens next to one another
+    z, scores = np.full((N, 64 * each), -130.0, f4), np.zeros(N, f4)
+    for i in range(N):
+        scores[i], top = f4(1e5 + rng.uniform(-300, 300)), f4(rng.uniform(0.2, 0.24))
+        while abs((float(scores[i]) - c * float(top)) % step - (i + 0.5) * step / N) > 0.2 * step / N:
+            top = np.nextafter(top, f4(4))
+        k = np.floor((float(scores[i]) - c * float(top)) / step) + np.arange(each) - each // 2
+        z[i, 17::64] = -(k * 2.0 ** -17)[rng.permutation(each)]
+        z[i, 5] = top
+    return z, scores, float(T)
+
+
+@pytest.mark.parametrize("seed", [0, 14, 18])
+def test_scores_that_cancel(smcsd, seed):
+    z, scores, T = beams_that_cancel(seed)
+    for M in range(66, 112):
+        check(smcsd, torch.from_numpy(z).cuda(), 1, len(scores), z.shape[1], M, T, scores)
