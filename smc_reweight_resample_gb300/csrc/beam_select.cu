@@ -1033,7 +1033,9 @@ template <int DT, int TH, bool ONE>
 static cudaError_t launch_beam_as(const BeamParams& p, cudaStream_t st) {
     const size_t shared = beam_shared_bytes(p.N, p.M, p.N * p.cpr, TH);
     if (shared > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(beam_kernel<DT, TH, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+        // the most of any call: the limit is the kernel's, and another thread may be about to launch it
+        const int most = (int)beam_shared_bytes(kBeamMostBeams, kBeamMost, kBeamMostChunks, TH);
+        const cudaError_t e = cudaFuncSetAttribute(beam_kernel<DT, TH, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return e;
