@@ -1032,14 +1032,10 @@ __global__ void __launch_bounds__(TH, TH == kBeamWide ? 1 : ONE ? 8 : 5) beam_ke
 template <int DT, int TH, bool ONE>
 static cudaError_t launch_beam_as(const BeamParams& p, cudaStream_t st) {
     const size_t shared = beam_shared_bytes(p.N, p.M, p.N * p.cpr, TH);
-    if (shared > 40 * 1024) {
-        // the most of any call: the limit is the kernel's, and another thread may be about to launch it
-        const int most = (int)beam_shared_bytes(kBeamMostBeams, kBeamMost, kBeamMostChunks, TH);
-        const cudaError_t e = cudaFuncSetAttribute(beam_kernel<DT, TH, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            return e;
-        }
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(beam_kernel<DT, TH, ONE>), shared);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return e;
     }
     return launch_waiting(beam_kernel<DT, TH, ONE>, dim3((unsigned)p.G * (unsigned)p.blocks), TH, shared, 0, st, p);
 }

@@ -646,9 +646,7 @@ __global__ void __launch_bounds__(kDistillThreads, 6) distill_loss_kernel(const 
 
 template <typename F>
 static cudaError_t launch_rows(F kernel, const DistillParams& p, int threads, size_t shared, cudaStream_t st) {
-    cudaError_t e = cudaSuccess;
-    // the most of any call: the limit is the kernel's, and another thread may be about to launch it
-    if (shared > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDistillMostBytes);
+    cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared);
     if (e == cudaSuccess && p.ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) {
         cudaGetLastError();

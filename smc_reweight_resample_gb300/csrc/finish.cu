@@ -252,10 +252,8 @@ static cudaError_t launch_finish_t(const StreamParams& p, cudaStream_t st) {
     const int nw = p.slots < kFinishMaxWarps ? p.slots : kFinishMaxWarps;
     const size_t smem = finish_smem_base(p, MODE);
     auto kern = finish_kernel<DT, MODE, false>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
     return launch_dependent(reinterpret_cast<const void*>(kern), dim3((unsigned)p.R.S),
                             dim3((unsigned)(nw * kWarp)), smem, p, st);
 }
@@ -270,7 +268,7 @@ static cudaError_t launch_finish_cluster_t(const StreamParams& p, cudaStream_t s
                         (finish_stages_table(p) ? (size_t)p.N * p.pages_per_seq * sizeof(int32_t) : 0);
     auto kern = finish_kernel<DT, kModeSMCStep, true>;
     const void* fn = reinterpret_cast<const void*>(kern);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(fn, smem);
     if (e == cudaSuccess && p.N > 8) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();  // (so that no later launch check reports this refusal)

@@ -394,8 +394,8 @@ static cudaError_t launch_sd_sample_t(const SampleParams& p, cudaStream_t st) {
     const size_t smem = (DT == 1 && p.use_table) ? (size_t)kTabSize * sizeof(float2) : 0;
     auto k2 = sd_rows_kernel<DT>;
     auto k3 = sd_residual_kernel<DT>;
-    cudaError_t e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k3, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(reinterpret_cast<const void*>(k2), smem);
+    if (e == cudaSuccess) e = allow_shared(reinterpret_cast<const void*>(k3), smem);
     if (e != cudaSuccess) return e;
     if (p.vec) {
         // aligned rows: one final-token pass over the (target, draft) row pairs as the pipelined

@@ -157,4 +157,8 @@ cudaError_t launch_wait_selftest(void* ws, bool front, unsigned long long limit_
 
 int device_sm_count();
 
+// Lets a kernel take `bytes` of dynamic shared memory on the current device. The limit belongs to the kernel and not to a launch: set to each
+// call's own size it could be lowered by another host thread between one's setting and its launch, so it is only ever raised.
+cudaError_t allow_shared(const void* kernel, size_t bytes);
+
 }  // namespace smcsd

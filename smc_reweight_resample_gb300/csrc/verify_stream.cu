@@ -5,6 +5,9 @@
 // One 640-thread block per SM, 20 warps claiming chunks from the grid-wide dealing as they become
 // free; every logit is read from HBM exactly once. Rows that are drawn from (the (K+1)-th target row of each particle) take
 // the precise path with the block's shared-memory exp table.
+#include <mutex>
+#include <vector>
+
 #include "smcsd_epilogue.cuh"
 
 namespace smcsd {
@@ -69,6 +72,32 @@ int device_sm_count() {
     return n > 0 ? n : 1;
 }
 
+cudaError_t allow_shared(const void* kernel, size_t bytes) {
+    if (bytes <= 40 * 1024) return cudaSuccess;  // with what the kernels have of their own within the 48 KB that need no permission
+    struct Given {
+        int device;
+        const void* kernel;
+        size_t bytes;
+    };
+    static std::mutex lock;
+    static std::vector<Given> given;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const std::lock_guard<std::mutex> guard(lock);
+    for (Given& g : given) {
+        if (g.device != device || g.kernel != kernel) continue;
+        if (bytes <= g.bytes) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess) g.bytes = bytes;
+        return e;
+    }
+    given.reserve(given.size() + 1);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) given.push_back(Given{device, kernel, bytes});
+    return e;
+}
+
 template <int DT, int MODE>
 static cudaError_t launch_stream_t(const StreamParams& p, cudaStream_t st) {
     auto kern = stream_kernel<DT, MODE>;
@@ -78,7 +107,7 @@ static cudaError_t launch_stream_t(const StreamParams& p, cudaStream_t st) {
     int grid = (int)(want < cap ? want : cap);
     if (grid < 1) grid = 1;
     const size_t smem = (MODE != kModeSD && DT == 1 && p.use_table) ? (size_t)kTabSize * sizeof(float2) : 0;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     kern<<<grid, kStreamThreads, smem, st>>>(p);
     return cudaGetLastError();

@@ -71,3 +71,39 @@ def test_distill_loss(smcsd):
         assert smcsd.check_status(ws) == 0
         # uniform: -log q = log V; one listed token. The logarithm and the sum are float32: some units of 2^-24 of a value of 13
         assert abs(float(loss) - float(torch.log(torch.tensor(float(V), dtype=torch.float64)))) < 64 * 2.0 ** -24 * 14
+
+
+@pytest.mark.parametrize("odd", [0, 1])
+def test_smc_step(smcsd, odd):
+    """Groups whose page tables take 0.1 to 32 KB of the finishing kernel's shared memory; temperatures with and without a table of the
+    exponential where rows are not aligned."""
+    lib, keep, calls = smcsd.load(), [], []
+    G, N, K, V, f = 2, 4, 2, 3000 + odd, ctypes.c_float
+    gen = torch.Generator("cuda").manual_seed(1)
+
+    def random(*shape):
+        return torch.randn(*shape, device="cuda", generator=gen)
+    tgt, drf = random(G * N * (K + 1), V).bfloat16(), random(G * N * K, V).bfloat16()
+    tokens = torch.randint(0, V, (G * N * K,), device="cuda", generator=gen, dtype=torch.int32)
+    u, v = torch.rand(G * N, device="cuda", generator=gen), torch.rand(G, device="cuda", generator=gen)
+    for pages, T in ((2000, 1.0), (8, 1e-4), (2040, 1.0), (500, 1e-4)):
+        ws = smcsd.Workspace(smcsd.OP_SMC_STEP, G * N, K, V)
+        table = torch.arange(G * N * pages, device="cuda", dtype=torch.int32)
+        out = [torch.zeros(n, dtype=t, device="cuda") for n, t in ((G * N, torch.int32), (G * N, torch.int32), (G, torch.float32), (G, torch.int32),
+                                                                  (table.numel(), torch.int32), (table.numel(), torch.int32))]
+        logw = torch.zeros(G * N, device="cuda")
+
+        def call(stream, T=T, ws=ws, table=table, out=out, logw=logw, pages=pages):
+            bonus, anc, ess, res, table_out, ref = map(P, out)
+            return lib.smc_step(P(tgt), P(drf), smcsd.BF16, P(tokens), G, N, K, V, f(T), f(1.0), P(u), P(logw), bonus, f(2.0), P(v), anc, ess, res,
+                                P(table), table_out, pages, ref, table.numel(), *ws.args, stream)
+        keep.append((ws, table, out, logw))
+        calls.append(call)
+    torch.cuda.synchronize()
+    assert run_threads(calls, 2000) == []
+    torch.cuda.synchronize()
+    for ws, table, out, logw in keep:
+        anc, res, table_out, ref = out[1], out[3], out[4], out[5]
+        moved = torch.arange(G, device="cuda").repeat_interleave(N) * N + torch.where(res.repeat_interleave(N) != 0, anc, torch.arange(G * N, device="cuda") % N)
+        assert torch.equal(table_out.view(G * N, -1), table.view(G * N, -1)[moved])
+        assert torch.equal(ref.long(), torch.bincount(table_out, minlength=table.numel()))
