@@ -75,6 +75,16 @@ __device__ __forceinline__ Mass join(Mass a, Mass b, float c2) {
     const float m = fmaxf(a.m, b.m);
     return Mass{m, a.s * rescale(a.m, m, c2) + b.s * rescale(b.m, m, c2)};
 }
+// The same mass relative to about its logarithm, where the reference is far below that: a sum of up to 2^113 would make the gradient's
+// factor a subnormal, or 0, for small weights. The factor between the two is good to 2^-23 (c2 (from - to) as a double-float).
+__device__ __forceinline__ Mass centred(Mass a, float c2) {
+    if (!(a.s > 16777216.0f && a.s < kPosInf)) return a;
+    const float m = a.m + log2f(a.s) / c2;
+    const dd d = two_sum(a.m, -m);
+    const float t = f_mul(d.hi, c2), n = rintf(t);
+    if (!(fabsf(t) < 126.0f)) return a;  // logits next to the end of float32's range
+    return Mass{m, a.s * exp2f(n) * exp2f(f_add(f_sub(t, n), f_add(f_fma(d.hi, c2, -t), f_mul(d.lo, c2))))};
+}
 // Two masses each of up to 16 entries, on every lane of the calling warp.
 struct Masses {
     Mass a, b;
@@ -467,7 +477,7 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistill
     const float wc = weight * p.c;
     if (tid < 32) {
         const Masses row = join_lanes(s.part, C, p.c2);
-        const Mass R = row.a, all = p.rest ? join(R, row.b, p.c2) : R;
+        const Mass all = centred(p.rest ? join(row.a, row.b, p.c2) : row.a, p.c2), R = p.rest ? centred(row.a, p.c2) : all;
         if (tid == 0) {
             // the rest relative to its own maximum; one without mass (all -inf) gets no gradient
             float scale = 0.0f;
