@@ -134,17 +134,18 @@ __device__ __forceinline__ bool told(uint32_t bar) {
     return ok != 0;
 }
 constexpr unsigned long long kToldNs = 2000000000ull;  // longest wait
-__device__ __forceinline__ void wait_told(uint32_t bar, void* ws) {
-    if (told(bar)) return;
+__device__ __forceinline__ bool wait_told(uint32_t bar) {
+#ifdef SMCSD_IMPATIENT
+    if (cg::this_cluster().block_rank() & 1) return false;  // a test's build: every second block gives up at once
+#endif
+    if (told(bar)) return true;
     unsigned long long t0, t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
     while (!told(bar)) {
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-        if (t - t0 > kToldNs) {
-            raise_error(ws, kErrTimeout);  // no counters are left behind
-            return;
-        }
+        if (t - t0 > kToldNs) return false;
     }
+    return true;
 }
 
 struct DistillShared {
@@ -161,8 +162,21 @@ struct DistillShared {
     float a[kDistillMostTokens / 32], b[kDistillMostTokens / 32];
     dd d[kDistillMostTokens / 32];
     float rest, mass;
-    int repeats;
+    int repeats, late;
 };
+// A block that has given up waiting (its context may have been off the GPU meanwhile) may still be told something, in shared memory that must
+// not be another block's by then. All its threads stay until the cluster's others have come here too or left, who have told it all
+// by then, and until that has landed.
+__device__ __forceinline__ void stay(const DistillShared& s, uint32_t bar) {
+    if (!s.late) return;
+    cg::this_cluster().sync();  // whoever has left is not waited for
+    unsigned long long t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    do {
+        if (told(bar)) break;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (t - t0 < kToldNs);
+}
 
 // Maximum, or sum, over the list's entries, one of each thread of the block's first `warps` warps, which alone call these.
 __device__ __forceinline__ void list_sync(int warps) { asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory"); }
@@ -255,7 +269,7 @@ __device__ __forceinline__ bool list_entry(const DistillParams& p, DistillShared
         }
     }
     if (tid < kDistillMostTokens) s.token[tid] = e.token, s.seen[tid] = 0;
-    if (tid == 0) s.repeats = 0;
+    if (tid == 0) s.repeats = 0, s.late = 0;
     return __syncthreads_or(e.value > kNegInf);
 }
 // The teacher's probabilities, by the warps with entries; p_r and the sum of all too.
@@ -380,7 +394,10 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistill
             return;
         }
         if (tid < C) tell(in_block(shared_address(&s.part[rank]), tid), own, in_block(bar, tid));
-        wait_told(bar, p.ws);
+        if (!wait_told(bar)) {
+            s.late = 1;
+            raise_error(p.ws, kErrTimeout);  // no counters are left behind
+        }
     };
 
     griddep_wait();
@@ -398,6 +415,8 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistill
         if (tid < 32) meet(make_float4(kNegInf, 0.0f, kNegInf, 0.0f));
         write_share<DT, TH>(h, out, [](int) { return make_uint4(0, 0, 0, 0); });
         if (rank == 0 && tid == 0 && p.loss) p.loss[r] = 0.0f;
+        __syncthreads();
+        stay(s, bar);
         return;
     }
     fetch<DT, TH>(h, s_row);
@@ -503,6 +522,7 @@ __global__ void __launch_bounds__(TH, TH == kDistillThreads ? 6 : TH == kDistill
         const float q = exp2f((z - all.m) * p.c2) / all.s;
         reinterpret_cast<T*>(out)[token] = (T)round_to<DT>(wc * (s.mass * q - e.listed));
     }
+    stay(s, bar);
 }
 
 // ------------------------------------------------------------------------------------------
