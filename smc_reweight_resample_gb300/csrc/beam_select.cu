@@ -472,14 +472,14 @@ __device__ __noinline__ dd precise_sum(const BeamParams& p, BeamShared s, BeamCo
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const dd d = two_sum(z[k], -m);
-            const float th = fmaxf(f_mul(d.hi, c2.hi), -100.0f);  // what is smaller adds nothing, whatever the rest is
+            const float th = fmaxf(f_mul(d.hi, c2.hi), -100.0f);  // what is smaller, a masked token among it, adds nothing, whatever the rest is
             const float tl = f_add(f_add(f_fma(d.hi, c2.hi, -th), f_mul(d.hi, c2.lo)), f_mul(d.lo, c2.hi));
             const float r = f_fma(th, 256.0f, kRound);  // 256 n + j in its last bits
             const int i = __float_as_int(r) - __float_as_int(kRound);
             const float g = f_add(f_fma(f_sub(r, kRound), -0.00390625f, th), th > -100.0f ? tl : 0.0f);
             const float e = f_mul(g, f_fma(g, f_fma(g, 0.0555041087f, 0.240226507f), 0.693147181f));
             const float2 t = table[i & 255];
-            const float u = __int_as_float(((i >> 8) + 127) << 23);
+            const float u = th > -100.0f ? __int_as_float(((i >> 8) + 127) << 23) : 0.0f;
             const dd a = two_sum(acc.hi, f_mul(t.x, u));
             acc.hi = a.hi;
             acc.lo = f_add(acc.lo, f_add(a.lo, f_mul(f_fma(t.x, e, t.y), u)));

@@ -101,3 +101,27 @@ def test_scores_that_cancel(smcsd, seed):
     z, scores, T = beams_that_cancel(seed)
     for M in range(66, 112):
         check(smcsd, torch.from_numpy(z).cuda(), 1, len(scores), z.shape[1], M, T, scores)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1, 2, 700, 9001])
+@pytest.mark.parametrize("G", [3, 310])
+def test_sure_tokens_and_finished_beams_of_one_score(smcsd, dtype, V, G):
+    """Beams with one token left, which has probability 1, keep their score, as finished beams do: equal scores go by the beam."""
+    N, M = 6, 5
+    rng = np.random.default_rng(V)
+    z = np.full((G * N, V), ou.NEG)
+    token = rng.integers(0, V, G * N)
+    z[np.arange(G * N), token] = rng.normal(0, 3, G * N)
+    if V > 2:  # far less likely ones in some rows: 2^-100 and below is nothing beside 1
+        z[::4, :] = np.maximum(z[::4, :], -900.0)
+    scores = np.repeat(rng.normal(-4, 1, G), N).astype(np.float32)
+    finished = (rng.random(G * N) < 0.5).astype(np.int32)
+    logits = torch.from_numpy(z).cuda().to(ou.DTYPES[dtype])
+    ws = smcsd.Workspace(smcsd.OP_BEAM_SELECT, G * N, 0, V)
+    got = smcsd.beam_select(logits, G, N, V, M, scores=dev(scores), finished=dev(finished), pad_token=V, ws=ws)
+    assert smcsd.check_status(ws) == 0
+    assert np.array_equal(host(got["ancestors"]).reshape(G, M), np.tile(np.arange(M), (G, 1)))
+    assert np.array_equal(host(got["scores"]).reshape(G, M), scores.reshape(G, N)[:, :M])
+    assert np.array_equal(host(got["tokens"]).reshape(G, M), np.where(finished, V, token).reshape(G, N)[:, :M])
+    assert np.array_equal(host(got["finished"]).reshape(G, M), finished.reshape(G, N)[:, :M])
