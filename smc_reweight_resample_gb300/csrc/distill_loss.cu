@@ -310,7 +310,11 @@ __device__ __forceinline__ void list_loss(const DistillParams& p, DistillShared&
     const float ls = logf(all.s);
     float term = 0.0f;
     const float prob = s.p[threadIdx.x], rest = s.rest;
-    if (prob > 0.0f) term = prob * (e.logp - ((z - all.m) * p.c - ls));
+    if (prob > 0.0f) {
+        const float away = z - all.m, logq = away * p.c - ls;
+        // a token masked with the lowest value: log q may lie below float32's range though its share of the loss does not
+        term = logq == kNegInf && away > kNegInf ? -(prob * p.c) * away : prob * (e.logp - logq);
+    }
     if (threadIdx.x == 0 && rest > 0.0f) term += rest * (logf(rest) - (logf(R.s) + (R.m - all.m) * p.c - ls));
     const float loss = list_sum(s, term, lists);
     if (threadIdx.x == 0) p.loss[r] = loss;

@@ -30,3 +30,24 @@ def test_small_weights_of_peaked_rows(smcsd, rest, dtype, V, T):
     big = grad[:, first:first + n].double().abs().sum(1) / weight.double().abs()
     assert (big > 0.01).all()
     assert np.isfinite(big.cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [0.25, 0.75, 1.0, 2.0])
+def test_listed_tokens_masked_with_the_lowest_value(smcsd, rest, dtype, T):
+    """The draft masks a token that the teacher gives a hundredth to: its log q may pass float32's range while its part of the loss,
+    -p log q, does not."""
+    R, V, K = 6, 3000, 8
+    gen = torch.Generator("cuda").manual_seed(3)
+    z = torch.randn(R, V, device="cuda", generator=gen).to(dtype)
+    tokens = torch.rand(R, V, device="cuda", generator=gen).topk(K, 1).indices
+    p = torch.full((R, K), 0.13, device="cuda")
+    p[:, 5] = 0.01
+    z[:3, :100] = torch.finfo(dtype).min
+    z[:3] = z[:3].scatter(1, tokens[:3], 0.5).scatter(1, tokens[:3, 5:6], torch.finfo(dtype).min)
+    loss, _, status = compare(smcsd, z, tokens.int(), p.log(), V, T, rest)
+    assert status == 0
+    assert bool(torch.isfinite(loss).all()) and bool((loss[:3] > 1e36).all()) and bool((loss[3:] < 100).all())
+    alone, _, _ = compare(smcsd, z, tokens.int(), p.log(), V, T, rest, grad=False)
+    assert bool(torch.isfinite(alone).all())
