@@ -569,8 +569,9 @@ int kv_copy_pages(void* const* caches, int n_caches, long long page_bytes, int n
  * Distillation from a teacher's top logits: for each of R rows, q = softmax(z / T) of the draft's logits, and the
  * teacher's probabilities p_k of the row's listed tokens top_tokens[r*K+k] (-1: none), from top_values:
  *   rest == 0: p = softmax of the row's values (log-probabilities or logits): the list stands for everything, p_r = 0;
- *   rest == 1: p_k = exp(value), log-probabilities over the whole vocabulary; p_r = max(0, 1 - sum_k p_k) is
+ *   rest == 1: p_k = exp(value), log-probabilities over the whole vocabulary; p_r = 1 - sum_k p_k is
  *              the share of all tokens that are not listed, as one event of probability q_r = 1 - sum of the listed q.
+ *              p_r < 2^-21, which roundings of the values may make of 0, is taken as 0.
  *   loss[r] = sum_k p_k (log p_k - log q_k) + p_r (log p_r - log q_r)             (terms with p = 0 are 0)
  *   dlogits[r, v] = weight[r] * dloss[r] / dz_v
  *                 = weight[r] / T * (P q_v - p_v) for a listed v, weight[r] / T * q_v (P - p_r / q_r) for others,

@@ -280,8 +280,11 @@ __device__ __forceinline__ void list_teacher(const DistillParams& p, DistillShar
         e.logp = e.value;
         prob = e.value > kNegInf ? expf(e.value) : 0.0f;
         const dd sum = list_sum_dd(s, prob, lists);
-        rest = fmaxf(dd_add(dd{1.0f, 0.0f}, dd_neg(sum)).hi, 0.0f);
-        mass = fmaxf(sum.hi, 1.0f);
+        // A list of all that has mass leaves nothing, but for roundings: of the values (half a step of each, 2^-24 of the list's entropy, which is
+        // 5.6 at most) and of their exponentials (2^-23). A rest of that kind would make the loss infinite where q leaves nothing either.
+        rest = dd_add(dd{1.0f, 0.0f}, dd_neg(sum)).hi;
+        if (!(rest >= 4.76837158e-7f)) rest = 0.0f;  // 2^-21
+        mass = rest > 0.0f ? 1.0f : sum.hi;
     } else {
         const float top = list_max(s, e.value, lists);
         const float x = e.value > kNegInf ? expf(e.value - top) : 0.0f;
