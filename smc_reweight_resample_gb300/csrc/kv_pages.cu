@@ -80,7 +80,10 @@ cudaError_t launch_reorder(const ReorderParams& p0, cudaStream_t st) {
 constexpr int kForkThreads = 512;  // at most
 constexpr int kForkEntries = 4;   // of a thread
 constexpr int kForkCounts = 8;    // of a thread
-constexpr int kForkMost = 65536;  // entries and pages that one cluster takes
+// Entries and pages that one cluster takes. Us by it / by two launches, as many pages as entries, forked: 2064 2.6 / 3.0, 4096 2.7 / 3.7,
+// 8192 4.0 / 3.9, 16384 6.4 / 3.9, 49152 15.8 / 4.3; freed: 2064 2.5 / 2.4, 4096 2.6 / 2.6, 8192 3.8 / 2.7, 16384 6.2 / 2.8. Two launches take 2
+// us more to issue where the host is behind.
+constexpr int kForkMost = 8192;
 
 // A page id of a table: whether it is counted. -1 is no page.
 __device__ __forceinline__ bool fork_counts(const ForkParams& p, int id) {
@@ -108,7 +111,7 @@ __device__ __forceinline__ void fork_change(const ForkParams& p, int id, int old
 }
 
 // Small tables: one cluster copies the counts and writes the new table, meets, and changes the counts. 2.5 to 2.8 us for 16 sequences of 129
-// pages and 2128 counts: latency (two launches took as long, and 2 us more to issue).
+// pages and 2128 counts: latency.
 constexpr int kForkClusterThreads = 512;
 __global__ void __launch_bounds__(kForkClusterThreads) fork_small_kernel(const __grid_constant__ ForkParams p0, const FastDiv by_row) {
     griddep_wait();
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kWide ? kForkThreads / 2 : kForkThreads) fork_
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t st) {
     const long long n = (long long)p.S * p.pages_per_seq;
     if (n <= kForkMost && p.num_pages <= kForkMost) {
-        // one launch in place of two, as long as a cluster of eight blocks has no more than a few turns to take
+        // one launch in place of two: two turns of a cluster of eight blocks at most
         const long long most = n > p.num_pages ? n : p.num_pages;
         int C = 1;
         while (C < 8 && most > C * kForkClusterThreads) C *= 2;
