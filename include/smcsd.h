@@ -491,6 +491,8 @@ int logits_process(const void* logits, void* out, int dtype, int R, int V, int S
  * Where there are fewer than M candidates, the remaining places get pad_token, 0, -inf and 1. Masked tokens of -inf
  * are none, nor are those whose score (or z less the row's largest) lies below float32's range: a token masked with the
  * type's lowest value is a candidate with T >= 1, and none with T < 1. A row with nothing but -inf has no candidate; that is not an error here.
+ * out_scores are good to 6e-6 (2e-7 as a rule: the sum's hardware exponentials) and half a step of float32, and carry the error of the
+ * scores that came in: over a search it adds up by the step.
  * The order is that of the scores' real values, up to 1e-9 or so: candidates of one beam are ordered by their logits
  * exactly, those of two beams by sums that are computed again, to 2e-10, where hardware exponentials could
  * not tell them apart (a slower path: some 30 us for each such row of 128256). Beams with equal scores and
@@ -526,7 +528,8 @@ int state_reorder(const void* const* src, void* const* dst, const long long* row
  * so holders other than the table (a prefix cache) keep their share. A partly filled last page is shared too:
  * kv_slot_map copies it when one of its holders writes. parents, lengths int32 [S].
  * Device-side errors: SMCSD_ERR_RANGE for a parent outside [-1, S) or a negative length (the sequence is kept as it is), for page
- * ids outside [-1, num_pages) (copied, not counted), and for a page that is let go though nothing counted it.
+ * ids outside [-1, num_pages) (copied, not counted), and for a page whose count ends below zero, or falls below it on the way (counts
+ * change in any order: where an id is both let go and taken and its count was too small, the error may be reported or not).
  */
 int kv_fork(const int32_t* parents, const int32_t* lengths, int S, const int32_t* table_in,
             int32_t* table_out, int pages_per_seq, int page_size, const int32_t* refcount_in,
@@ -582,7 +585,8 @@ int kv_copy_pages(void* const* caches, int n_caches, long long page_bytes, int n
  * as each alone does. logits, dlogits: rows row_stride and dlogits_stride elements apart, V used, of dtype, aligned to
  * it; dlogits may be logits (with one stride), else they must not overlap (rows may lie
  * between one another's); nor may either output overlap the lists, weight or the other output, nor loss the logits. top_tokens int32, top_values float [R, K], K at most 256;
- * weight, loss float [R]. V times the element size is at most 1638368 bytes. Sums are float32, the gradient is rounded once.
+ * weight, loss float [R]. V times the element size is at most 1638368 bytes. Sums are float32, the gradient is rounded once. (In torch the
+ * call takes no part in autograd: the loss has no graph, and the gradient goes on by logits.backward(dlogits).)
  * Device-side errors: SMCSD_ERR_NONFINITE (NaN or +inf in logits or values, a row of -inf), SMCSD_ERR_RANGE (a token outside
  * [-1, V), taken as none).
  */

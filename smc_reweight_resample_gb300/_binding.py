@@ -691,7 +691,8 @@ def distill_loss(logits, top_tokens, top_values, V, temperature=1.0, rest=False,
     """Loss of the draft's logits [R, >= V] (rows may be strided) against a teacher's top tokens (int32 [R, K], -1: none) with their
     values (float [R, K]), and the gradient weight[r] * dloss[r]/dlogits (pass dlogits=logits for it to take their place). rest: the
     values are log-probabilities over the whole vocabulary, and what they leave goes to all other tokens. Returns (loss float [R] or
-    None, dlogits [R, V] or None)."""
+    None, dlogits [R, V] or None). The loss has no graph, also where the logits require a gradient: logits.backward(dlogits) sends the
+    gradient on (of loss.sum(), or with `weight` of (weight * loss).sum())."""
     if stream is not None:
         return _on(stream, distill_loss, locals())
     ws = ws or Workspace(OP_DISTILL_LOSS, 1, device=logits.device)

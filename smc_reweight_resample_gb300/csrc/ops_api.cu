@@ -115,10 +115,10 @@ extern "C" int beam_select(const void* logits, long long row_stride, int dtype, 
     p.N = N;
     p.V = V;
     p.M = M;
-    p.c = 1.0 / (double)temperature;
-    p.c_hi = (float)p.c;
-    p.c_lo = (float)(p.c - (double)p.c_hi);
-    p.c2 = (float)(p.c * 1.4426950408889634074);
+    const double c = 1.0 / (double)temperature;
+    p.c_hi = (float)c;
+    p.c_lo = (float)(c - (double)p.c_hi);
+    p.c2 = (float)(c * 1.4426950408889634074);
     p.scores = scores;
     p.finished = finished;
     p.pad = pad_token;

@@ -18,8 +18,7 @@ struct BeamParams {
     const void* logits;
     long long row_stride;  // elements
     int G, N, V, M;
-    double c;    // 1 / temperature
-    float c_hi, c_lo, c2;  // c as a double-float; c log2(e)
+    float c_hi, c_lo, c2;  // c = 1 / temperature as a double-float; c log2(e)
     const float* scores;
     const int32_t* finished;
     int pad, eos;
