@@ -6,7 +6,6 @@
 // free; every logit is read from HBM exactly once. Rows that are drawn from (the (K+1)-th target row of each particle) take
 // the precise path with the block's shared-memory exp table.
 #include <mutex>
-#include <vector>
 
 #include "smcsd_epilogue.cuh"
 
@@ -79,23 +78,22 @@ cudaError_t allow_shared(const void* kernel, size_t bytes) {
         const void* kernel;
         size_t bytes;
     };
+    constexpr int kMost = 1024;  // some thirty kernels for each device; nothing here allocates or throws
     static std::mutex lock;
-    static std::vector<Given> given;
+    static Given given[kMost];
+    static int count = 0;
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
     const std::lock_guard<std::mutex> guard(lock);
-    for (Given& g : given) {
-        if (g.device != device || g.kernel != kernel) continue;
-        if (bytes <= g.bytes) return cudaSuccess;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (e == cudaSuccess) g.bytes = bytes;
-        return e;
-    }
-    given.reserve(given.size() + 1);
+    int i = 0;
+    while (i < count && (given[i].device != device || given[i].kernel != kernel)) ++i;
+    if (i < count && bytes <= given[i].bytes) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) given.push_back(Given{device, kernel, bytes});
-    return e;
+    if (e != cudaSuccess || i == kMost) return e;
+    given[i] = Given{device, kernel, bytes};
+    if (i == count) ++count;
+    return cudaSuccess;
 }
 
 template <int DT, int MODE>
