@@ -322,7 +322,7 @@ class _Remap:
                     raise ValueError(f"{what} is too small")
             for t in (table_in, table_out):
                 # one row behind the other, whichever dimensions make up a row
-                if t is not None and t.dim() > 1 and t.numel() != pages_per_seq and \
+                if t is not None and G * N > 1 and t.dim() > 1 and t.numel() != pages_per_seq and \
                         pages_per_seq not in [math.prod(t.shape[k:]) for k in range(1, t.dim())]:
                     raise ValueError("a table has rows of another size")
         if refcount is not None and refcount.numel() < num_pages:

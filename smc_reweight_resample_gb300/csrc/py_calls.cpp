@@ -541,7 +541,7 @@ PyObject* py_remap(PyObject*, PyObject* const* args, Py_ssize_t n) {
             at_least(resampled, G, "resampled");
             for (const at::Tensor* t : {&table, table_in_out}) {
                 if (t && (__int128)rows * pages_per_seq > t->numel()) value_error("a table is too small");
-                rows_of(t, rows, pages_per_seq, "a table");
+                if (rows > 1) rows_of(t, rows, pages_per_seq, "a table");  // of one row the rest is not looked at
             }
         }
         at_least(refcount, num_pages, "refcount");

@@ -96,3 +96,14 @@ def test_tables_of_every_shape_that_fit(smcsd):
     assert ref is None and torch.equal(got[:6], want) and bool((got[6:] == -5).all())
     got, ref = smcsd.kv_pagetable_remap(ancestors, None, 2, 3, table, 10)
     assert ref.numel() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("module", [True, False])
+def test_one_row_of_a_longer_table(smcsd, module, monkeypatch, tmp_path):
+    if not module:
+        monkeypatch.setattr(B, "_calls", None)
+        monkeypatch.setattr(B, "_HERE", str(tmp_path))
+    table, out = torch.arange(20, dtype=torch.int32, device="cuda").view(1, 20), torch.full((1, 20), -7, dtype=torch.int32, device="cuda")
+    got, ref = smcsd.kv_pagetable_remap(i32(1).cuda(), None, 1, 1, table, 12, 20, table_out=out)
+    assert torch.equal(got[0, :12], table[0, :12]) and bool((got[0, 12:] == -7).all()) and ref.tolist() == [1] * 12 + [0] * 8
