@@ -548,7 +548,7 @@ int kv_free(const int32_t* lengths, int S, const int32_t* table_in, int32_t* tab
  * use, the k-th (ascending) page in use from page U on takes the k-th free page below U.
  *   src[k], dst[k], k < counts[0]: the moves, for kv_copy_pages (-1 behind them); counts[1] = U;
  *   table_out, refcount_out: table_in and refcount_in with the pages' new ids; pages from U on are free.
- * src, dst int32 [num_pages / 2] (NULL for one page), counts int32 [2]. Nothing but counts and tables is touched: the caller
+ * src, dst int32 [num_pages / 2] (NULL for one page), counts int32 [2]; no output may overlap another. Nothing but counts and tables is touched: the caller
  * copies the pages of every layer. ws: smcsd_workspace_size(SMCSD_OP_KV_COMPACT, 1, 0, num_pages).
  * Device-side errors: SMCSD_ERR_RANGE (a negative refcount, taken as free; table entries outside [-1, num_pages) or of free pages,
  * left as they are).

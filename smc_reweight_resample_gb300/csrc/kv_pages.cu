@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(kApplyThreads) compact_apply_kernel(const __gr
     CompactParams p = p0;
     p.ref_in = after_wait(p0.ref_in);
     p.table_in = after_wait(p0.table_in);
-    compact_apply(p, __ldcg(p.counts), __ldcg(p.counts + 1), (long long)blockIdx.x * kApplyThreads + threadIdx.x,
+    const int moves = min(max(__ldcg(p.counts), 0), p.num_pages / 2);  // the lists' length, whatever has been written there meanwhile
+    compact_apply(p, moves, __ldcg(p.counts + 1), (long long)blockIdx.x * kApplyThreads + threadIdx.x,
                   (long long)gridDim.x * kApplyThreads);
 }
 

@@ -217,6 +217,10 @@ extern "C" int kv_compact(int S, const int32_t* table_in, int32_t* table_out, in
     if (meet({{table_out, n, 4}, {refcount_out, num_pages, 4}, {src, num_pages / 2, 4}, {dst, num_pages / 2, 4}, {counts, 2, 4}},
              {{table_in, n, 4}, {refcount_in, num_pages, 4}}))
         return SMCSD_ERR_INVALID_ARG;
+    // the moves and their number are read again once the table and the counts are written
+    const auto out = [](const void* at, long long words) { return Touched{(uintptr_t)at, (uintptr_t)at + 4 * (uintptr_t)words, at && words > 0}; };
+    Touched outs[] = {out(table_out, n), out(refcount_out, num_pages), out(src, num_pages / 2), out(dst, num_pages / 2), out(counts, 2)};
+    if (meet(outs, 5)) return SMCSD_ERR_INVALID_ARG;
     CompactParams p{};
     p.table_in = table_in;
     p.table_out = table_out;

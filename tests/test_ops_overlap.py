@@ -42,3 +42,16 @@ def test_distill_loss_with_the_lists_memory(lib):  # noqa: F811
     assert call(dtype=0, grad=P(loss - 3 * 880 - 396)) == -1 and call(dtype=0, loss=P(z + 880 + 396)) == -1
     for t in (tokens, values, weight):
         assert call(loss=None, grad=P(t)) == -1
+
+
+def test_kv_compact_with_outputs_that_share_memory(lib):  # noqa: F811
+    """4 sequences of 16 pages, 100 counts, lists of 50 moves."""
+    at = dict(tout=1 << 42, rout=1 << 43, src=1 << 44, dst=1 << 45, counts=1 << 46)
+    size = dict(tout=256, rout=400, src=200, dst=200, counts=8)
+    call = caller(lib.kv_compact, [
+        ("S", I, 4), ("tin", P, P(1 << 40)), ("tout", P, P(at["tout"])), ("P", I, 16), ("rin", P, P(1 << 41)), ("rout", P, P(at["rout"])), ("num", I, 100),
+        ("src", P, P(at["src"])), ("dst", P, P(at["dst"])), ("counts", P, P(at["counts"])), ("ws", P, FAKE), ("n", SZ, 1 << 20), ("stream", P, None)])
+    for a in at:
+        for b in at:
+            if a != b:
+                refused(call, -1, **{a: [P(at[b]), P(at[b] + size[b] - 4), P(at[b] - size[a] + 4)]})
